@@ -7,13 +7,13 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <mutex>
 #include <new>
 #include <set>
 #include <vector>
 
 #include "../../include/fib_attn.h"
 #include "common.cuh"
+#include "plan.h"
 #include "planner.h"
 
 namespace fibattn {
@@ -53,51 +53,8 @@ size_t noalloc_scratch_bytes();
 
 using namespace fibattn;
 
-namespace {
-// Test hook: every CTA takes a whole SM's shared memory and fills it with `pattern`, so that
-// the kernels launched next on those SMs start from known stale contents.
-__global__ void fill_shared_kernel(uint32_t pattern, int words) {
-  extern __shared__ uint32_t fill_smem[];
-  for (int i = threadIdx.x; i < words; i += blockDim.x) fill_smem[i] = pattern;
-  __syncthreads();
-  // keep the stores: make them observable through a value no thread will ever see
-  if (fill_smem[(threadIdx.x * 7) % words] == pattern + 1u && pattern == 0xffffffffu) fill_smem[0] = 0u;
-}
-}  // namespace
-
-struct fib_attn_plan_s {
-  int base_kind = 0;
-  std::vector<int32_t> custom;
-  std::vector<double> alpha;
-  int W = 0, N_max = 0, D = 0, mode = 0;
-  double rope_base = 10000.0;
-  int device = -1;
-  float2* d_lo = nullptr;
-  float2* d_hi = nullptr;
-  int* d_status = nullptr;
-  unsigned long long wait_ns = 1000000000ULL;  // bound of every device-side wait (1 s)
-  int skip_first_rung_copy = 0;                // test hooks, see fib_attn_plan_set_debug
-  int corrupt_rung_table = 0;
-  BwdStreams side;                             // the bf16 backward's second-half stream
-  std::mutex side_mu;                          // one backward at a time forks onto it
-};
-
-namespace {
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// Frees what a plan holds on the device (each handle may be null).
-void release_device_state(fib_attn_plan_s* p) {
-  cudaFree(p->d_lo);
-  cudaFree(p->d_hi);
-  cudaFree(p->d_status);
-  if (p->side.join) cudaEventDestroy(p->side.join);
-  if (p->side.first_q_done) cudaEventDestroy(p->side.first_q_done);
-  if (p->side.fork) cudaEventDestroy(p->side.fork);
-  if (p->side.stream) cudaStreamDestroy(p->side.stream);
-}
-
-std::vector<int32_t> plan_base(const fib_attn_plan_s* p, int N) {
+namespace fibattn {
+static std::vector<int32_t> plan_base(const fib_attn_plan_s* p, int N) {
   if (p->base_kind == FIB_BASE_FIBONACCI) return fibonacci_base(987);
   if (p->base_kind == FIB_BASE_POW2) return pow2_base(N);
   return p->custom;
@@ -136,6 +93,29 @@ int make_table(const fib_attn_plan_s* p, int layer, int N, const float* alpha_de
   }
   return FIB_OK;
 }
+}  // namespace fibattn
+
+namespace {
+// Test hook: every CTA takes a whole SM's shared memory and fills it with `pattern`, so that
+// the kernels launched next on those SMs start from known stale contents.
+__global__ void fill_shared_kernel(uint32_t pattern, int words) {
+  extern __shared__ uint32_t fill_smem[];
+  for (int i = threadIdx.x; i < words; i += blockDim.x) fill_smem[i] = pattern;
+  __syncthreads();
+  // keep the stores: make them observable through a value no thread will ever see
+  if (fill_smem[(threadIdx.x * 7) % words] == pattern + 1u && pattern == 0xffffffffu) fill_smem[0] = 0u;
+}
+
+// Frees what a plan holds on the device (each handle may be null).
+void release_device_state(fib_attn_plan_s* p) {
+  cudaFree(p->d_lo);
+  cudaFree(p->d_hi);
+  cudaFree(p->d_status);
+  if (p->side.join) cudaEventDestroy(p->side.join);
+  if (p->side.first_q_done) cudaEventDestroy(p->side.first_q_done);
+  if (p->side.fork) cudaEventDestroy(p->side.fork);
+  if (p->side.stream) cudaStreamDestroy(p->side.stream);
+}
 
 // Test hook of the tensor-core forward only (the one kernel family that checks its rung
 // table on the device): the first rung of a host-built table is moved to distance 0, inside
@@ -148,18 +128,6 @@ void corrupt_for_test(const fib_attn_plan_s* p, LayerTable* t) {
   }
 }
 
-int check_device(const fib_attn_plan_s* p) {
-  int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FIB_ERR_CUDA;
-  if (dev != p->device) return FIB_ERR_INVALID_ARG;
-  return FIB_OK;
-}
-
-int check_tensor(const void* ptr) {
-  if (ptr == nullptr || !aligned(ptr, 16)) return FIB_ERR_INVALID_ARG;
-  return FIB_OK;
-}
-
 int check_shape(const fib_attn_plan_s* p, int layer, int B, int H, int N, int dtype) {
   if (p == nullptr) return FIB_ERR_INVALID_ARG;
   if (layer < 0 || layer >= static_cast<int>(p->alpha.size())) return FIB_ERR_INVALID_ARG;
@@ -168,12 +136,6 @@ int check_shape(const fib_attn_plan_s* p, int layer, int B, int H, int N, int dt
   const long long rows = static_cast<long long>(B) * H * N;
   if (rows > (1LL << 40) / kD) return FIB_ERR_INVALID_ARG;
   return FIB_OK;
-}
-
-int cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return FIB_OK;
-  if (e == cudaErrorMemoryAllocation) return FIB_ERR_NOMEM;
-  return FIB_ERR_CUDA;
 }
 
 }  // namespace
@@ -189,6 +151,7 @@ const char* fib_attn_error_string(int code) {
     case FIB_ERR_NOMEM: return "out of memory";
     case FIB_ERR_TIMEOUT: return "device wait timed out";
     case FIB_ERR_DEVICE_ASSERT: return "device-side check failed";
+    case FIB_ERR_NO_PAGES: return "no free cache pages left";
     case FIB_ERR_RANGE: return "value outside the float16 range of the bf16 tensor-core path";
     default: return "unknown status";
   }

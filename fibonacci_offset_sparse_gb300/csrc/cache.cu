@@ -1,0 +1,497 @@
+// The paged key/value cache's own operators (sm_103a): commit (allocate, copy on write, rotate
+// and store accepted tokens), fork (share, reorder, free) and compact (move pages down).
+//
+// Each is two launches: a small one that reads and rewrites the tables and counts, and one
+// that moves rows (commit, compact) or finishes the tables (fork).  The second is a programmatic dependent of
+// the first, so its launch overlaps it, and takes the work list that the first left in the
+// workspace.  All choices are made in an order that no scheduling changes: sequences ascending, free pages
+// ascending; the only atomics are integer sums and minima.
+#include "cache.cuh"
+#include "tc_common.cuh"
+
+namespace fibattn {
+
+namespace {
+
+constexpr int kPlanThreads = 1024;
+
+struct CacheDev {
+  int L, H, P, shift, n_pages, S, max_pages;
+  void* k;
+  void* v;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t* state;
+};
+
+CacheDev device_view(const fib_attn_cache& c) {
+  CacheDev d;
+  d.L = c.n_layers;
+  d.H = c.heads;
+  d.P = c.page_rows;
+  d.shift = log2_of(c.page_rows);
+  d.n_pages = c.n_pages;
+  d.S = c.max_seqs;
+  d.max_pages = c.max_pages;
+  d.k = c.k;
+  d.v = c.v;
+  d.table = c.table;
+  d.lens = c.lens;
+  d.refs = c.refs;
+  d.state = c.state;
+  return d;
+}
+
+__device__ __forceinline__ void wait_for_first() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void let_second_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+// A kernel as a programmatic dependent of the one before it on the stream.
+template <typename... Params, typename... Args>
+cudaError_t launch_second(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// The ids of free pages from the cursor on, ascending, into list[0 .. want); returns how many
+// there are up to `want`.  4096 counts a step; stops as soon as enough are found.
+__device__ int find_free(const CacheDev& c, int want, int32_t* list, int* sums) {
+  int found = 0;
+  const int from = max(0, min(c.state[kStateCursor], c.n_pages));
+  for (int base = from & ~3; base < c.n_pages && found < want; base += 4 * kPlanThreads) {
+    const int id = base + 4 * static_cast<int>(threadIdx.x);
+    int r[4] = {1, 1, 1, 1};
+    if (id + 3 < c.n_pages) {
+      const int4 x = *reinterpret_cast<const int4*>(c.refs + id);
+      r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (id + u < c.n_pages) r[u] = c.refs[id + u];
+    }
+    int n = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (id + u < from) r[u] = 1;
+      n += r[u] == 0;
+    }
+    int total;
+    int at = found + block_scan_1024(n, sums, &total);
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (r[u] == 0) {
+        if (at < want) list[at] = id + u;
+        ++at;
+      }
+    found += total;
+  }
+  __syncthreads();
+  return min(found, want);
+}
+
+// ------------------------------------------------------------------------------- commit --
+// Work list of a commit, in the workspace: one entry a sequence, then the free pages taken.
+struct CommitJob {
+  int len;  // rows before the call
+  int n;    // rows gained (0: nothing to do)
+  int src;  // page whose first len % P rows are copied, or -1
+  int dst;  // ... into this one
+};
+
+struct CommitArgs {
+  CacheDev c;
+  int B, T, n_max;
+  const int32_t* n_new;
+  const int32_t* path;
+  const void* k_new;
+  const void* v_new;
+  const float2* rope_lo;
+  const float2* rope_hi;
+  CommitJob* jobs;
+  int32_t* list;
+};
+
+// One block, a thread a sequence.
+__global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_constant__ CommitArgs a) {
+  __shared__ int s_page[kMaxSeqs], s_first[kMaxSeqs], s_count[kMaxSeqs], s_off[kMaxSeqs];
+  __shared__ int s_sums[33];
+  let_second_start();
+  const CacheDev& c = a.c;
+  const int b = threadIdx.x;
+  int n = 0, len = 0, page = -1, refs = 0;
+  bool bad = false, part = false;
+  if (b < a.B) {
+    n = a.n_new[b];
+    len = c.lens[b];
+    bad = n < 0 || n > a.T || len < 0 || static_cast<long long>(len) + n > static_cast<long long>(c.max_pages) * c.P ||
+          (n > 0 && static_cast<long long>(len) + n > a.n_max);
+    if (bad) n = 0;
+    part = n > 0 && (len & (c.P - 1)) != 0;
+    if (part) {
+      page = c.table[static_cast<size_t>(b) * c.max_pages + (len >> c.shift)];
+      if (page < 0 || page >= c.n_pages)
+        bad = true;
+      else
+        refs = c.refs[page];
+    }
+  }
+  if (a.path != nullptr) {
+    for (long long i = threadIdx.x; i < static_cast<long long>(a.B) * a.T; i += kPlanThreads) {
+      const int seq = static_cast<int>(i / a.T);
+      if (i - static_cast<long long>(seq) * a.T < a.n_new[seq]) {
+        const int node = a.path[i];
+        bad |= node < 0 || node >= a.T;
+      }
+    }
+  }
+  // shared last pages: who else writes into the same one
+  s_page[b] = part && refs > 1 ? page : -1;
+  const bool any_bad = __syncthreads_or(bad);
+  bool copy = false;
+  if (!any_bad && part && refs > 1) {
+    int writers = 0;
+    bool last = true;
+    for (int o = 0; o < a.B; ++o)
+      if (s_page[o] == page) {
+        ++writers;
+        last &= o <= b;
+      }
+    copy = !(writers == refs && last);
+  }
+  const int first = (len + c.P - 1) >> c.shift;
+  const int fresh = n > 0 ? ((len + n + c.P - 1) >> c.shift) - first : 0;
+  int total;
+  const int off = block_scan_1024(any_bad ? 0 : fresh + (copy ? 1 : 0), s_sums, &total);
+  const bool enough = any_bad || find_free(c, total, a.list, s_sums) == total;
+  if (any_bad || !enough) {  // nothing changes
+    if (b < a.B) a.jobs[b] = CommitJob{0, 0, -1, -1};
+    if (b == 0) c.state[kStateStatus] = any_bad ? kStatusDeviceAssert : kStatusNoPages;
+    return;
+  }
+  s_first[b] = first;
+  s_count[b] = fresh;
+  s_off[b] = off + (copy ? 1 : 0);
+  if (b < a.B) {
+    CommitJob j{len, n, -1, -1};
+    if (copy) {
+      j.src = page;
+      j.dst = a.list[off];
+      c.table[static_cast<size_t>(b) * c.max_pages + (len >> c.shift)] = j.dst;
+      c.refs[j.dst] = 1;
+      atomicSub(&c.refs[page], 1);
+    }
+    a.jobs[b] = j;
+    if (n > 0) c.lens[b] = len + n;
+  }
+  if (b == 0 && total > 0) c.state[kStateCursor] = a.list[total - 1] + 1;
+  __syncthreads();
+  for (int s = threadIdx.x >> 5; s < a.B; s += kPlanThreads / 32)
+    for (int i = threadIdx.x & 31; i < s_count[s]; i += 32) {
+      const int id = a.list[s_off[s] + i];
+      c.table[static_cast<size_t>(s) * c.max_pages + s_first[s] + i] = id;
+      c.refs[id] = 1;
+    }
+}
+
+constexpr int kWriteThreads = 128;
+constexpr int kWriteTokens = 64;  // tokens of a sequence a block
+
+// Block (sequence and layer, group of heads, chunk of tokens): copies the shared page's rows, then a quad
+// of threads writes the rows of one token and head (lane layout of common.cuh).
+template <typename DT>
+__global__ void __launch_bounds__(kWriteThreads) commit_write_kernel(const __grid_constant__ CommitArgs a, int heads) {
+  wait_for_first();
+  const CacheDev& c = a.c;
+  const int b = blockIdx.x / c.L, l = blockIdx.x % c.L;
+  const int h0 = blockIdx.y * heads, h1 = min(c.H, h0 + heads);
+  const CommitJob job = a.jobs[b];
+  const int i0 = blockIdx.z * kWriteTokens, i1 = min(job.n, i0 + kWriteTokens);
+  DT* K = static_cast<DT*>(c.k);
+  DT* V = static_cast<DT*>(c.v);
+  const size_t layer = static_cast<size_t>(l) * c.n_pages;
+  if (blockIdx.z == 0 && job.src >= 0) {
+    const int vecs = (job.len & (c.P - 1)) * kD * static_cast<int>(sizeof(DT)) / 16;
+    const size_t from = ((layer + job.src) * c.H + h0) * c.P * kD, to = ((layer + job.dst) * c.H + h0) * c.P * kD;
+    const size_t step = static_cast<size_t>(c.P) * kD;
+    for (int i = threadIdx.x; i < vecs * (h1 - h0); i += kWriteThreads) {
+      const int h = i / vecs, x = i % vecs;
+      const uint4 kx = reinterpret_cast<const uint4*>(K + from + h * step)[x];
+      const uint4 vx = reinterpret_cast<const uint4*>(V + from + h * step)[x];
+      reinterpret_cast<uint4*>(K + to + h * step)[x] = kx;
+      reinterpret_cast<uint4*>(V + to + h * step)[x] = vx;
+    }
+  }
+  const int t = threadIdx.x & 3;
+  for (int item = threadIdx.x >> 2; item < (i1 - i0) * (h1 - h0); item += kWriteThreads / 4) {
+    const int i = i0 + item / (h1 - h0), h = h0 + item % (h1 - h0);
+    const int node = a.path != nullptr ? a.path[static_cast<size_t>(b) * a.T + i] : i;
+    const int pos = job.len + i;
+    const int page = c.table[static_cast<size_t>(b) * c.max_pages + (pos >> c.shift)];
+    const size_t from = (((static_cast<size_t>(l) * a.B + b) * c.H + h) * a.T + node) * kD;
+    const size_t to = (((layer + page) * c.H + h) * c.P + (pos & (c.P - 1))) * kD;
+    float x[16], y[16];
+    load_part(static_cast<const DT*>(a.k_new) + from, t, x);
+    load_part(static_cast<const DT*>(a.v_new) + from, t, y);
+    float2 e[8];
+    rope_row(a.rope_lo, a.rope_hi, pos, t, e);
+    rotate_part(x, e, false);
+    store_part(K + to, t, x);
+    store_part(V + to, t, y);
+  }
+}
+
+// --------------------------------------------------------------------------------- fork --
+struct ForkArgs {
+  CacheDev c;
+  const int32_t* src;
+  int32_t* rows;  // [S, max_pages]: what the sequences' rows become
+  int32_t* lens;  // [S]; -1: the whole call is refused
+};
+
+constexpr int kForkThreads = 256;
+
+__device__ __forceinline__ int pages_of(const CacheDev& c, int len) { return (len + c.P - 1) >> c.shift; }
+
+// A block a sequence: the new row into the workspace, +1 for each page it holds now, -1 for
+// each that it held.  Sums of integers: the order does not matter.
+__global__ void __launch_bounds__(kForkThreads) fork_count_kernel(const __grid_constant__ ForkArgs a) {
+  let_second_start();
+  const CacheDev& c = a.c;
+  const int b = blockIdx.x;
+  bool bad = false;
+  for (int i = threadIdx.x; i < c.S; i += kForkThreads) {
+    const int s = a.src[i], len = c.lens[i];
+    bad |= s < -1 || s >= c.S || len < 0 || len > static_cast<long long>(c.max_pages) * c.P;
+  }
+  if (__syncthreads_or(bad)) {
+    if (threadIdx.x == 0) {
+      a.lens[b] = -1;
+      if (b == 0) c.state[kStateStatus] = kStatusDeviceAssert;
+    }
+    return;
+  }
+  const int s = a.src[b];
+  const int len = s < 0 ? 0 : c.lens[s];
+  if (threadIdx.x == 0) a.lens[b] = len;
+  if (s == b) return;
+  const int now = pages_of(c, len), old = pages_of(c, c.lens[b]);
+  const int32_t* from = c.table + static_cast<size_t>(max(s, 0)) * c.max_pages;
+  const int32_t* mine = c.table + static_cast<size_t>(b) * c.max_pages;
+  for (int j = threadIdx.x; j < now; j += kForkThreads) {
+    const int page = from[j];
+    a.rows[static_cast<size_t>(b) * c.max_pages + j] = page;
+    if (page >= 0 && page < c.n_pages)
+      atomicAdd(&c.refs[page], 1);
+    else
+      c.state[kStateStatus] = kStatusDeviceAssert;
+  }
+  for (int j = threadIdx.x; j < old; j += kForkThreads) {
+    const int page = mine[j];
+    if (page >= 0 && page < c.n_pages)
+      atomicSub(&c.refs[page], 1);
+    else
+      c.state[kStateStatus] = kStatusDeviceAssert;
+  }
+}
+
+// The rows into the table; the lowest page that lost its last holder lowers the cursor.
+__global__ void __launch_bounds__(kForkThreads) fork_write_kernel(const __grid_constant__ ForkArgs a) {
+  wait_for_first();
+  const CacheDev& c = a.c;
+  const int b = blockIdx.x;
+  const int len = a.lens[b];
+  if (len < 0 || a.src[b] == b) return;
+  const int now = pages_of(c, len), old = pages_of(c, c.lens[b]);
+  int lowest = c.n_pages;
+  for (int j = threadIdx.x; j < max(now, old); j += kForkThreads) {
+    int32_t* e = c.table + static_cast<size_t>(b) * c.max_pages + j;
+    if (j < old) {
+      const int page = *e;
+      if (page >= 0 && page < c.n_pages && c.refs[page] == 0) lowest = min(lowest, page);
+    }
+    *e = j < now ? a.rows[static_cast<size_t>(b) * c.max_pages + j] : -1;
+  }
+  if (lowest < c.n_pages) atomicMin(&c.state[kStateCursor], lowest);
+  __syncthreads();  // every thread has read the old length
+  if (threadIdx.x == 0) c.lens[b] = len;
+}
+
+// ------------------------------------------------------------------------------ compact --
+struct CompactArgs {
+  CacheDev c;
+  int32_t* remap;
+  int32_t* moves;  // number of moves
+  int32_t* src;
+  int32_t* dst;
+};
+
+// One block: counts the used pages (n), then lists the free ones below n and the used ones
+// from n on; the i-th of these moves into the i-th of those.
+__global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ CompactArgs a) {
+  __shared__ int s_sums[33];
+  let_second_start();
+  const CacheDev& c = a.c;
+  int mine = 0;
+  for (int id = threadIdx.x; id < c.n_pages; id += kPlanThreads) mine += c.refs[id] > 0;
+  int live;
+  block_scan_1024(mine, s_sums, &live);
+  int holes = 0, moved = 0;
+  for (int base = 0; base < c.n_pages; base += kPlanThreads) {
+    const int id = base + static_cast<int>(threadIdx.x);
+    const bool in = id < c.n_pages;
+    const bool used = in && c.refs[id] > 0;
+    const bool hole = in && !used && id < live, out = used && id >= live;
+    int n_hole, n_out;
+    const int at_hole = holes + block_scan_1024(hole, s_sums, &n_hole);
+    const int at_out = moved + block_scan_1024(out, s_sums, &n_out);
+    if (hole) a.dst[at_hole] = id;
+    __syncthreads();
+    // every hole lies below `live`, so the first `moved + n_out` of them are listed by now
+    if (out) {
+      a.src[at_out] = id;
+      a.remap[id] = a.dst[at_out];
+    } else if (in) {
+      a.remap[id] = used ? id : -1;
+    }
+    holes += n_hole;
+    moved += n_out;
+  }
+  if (threadIdx.x == 0) {
+    *a.moves = moved;
+    c.state[kStateLive] = live;
+    c.state[kStateCursor] = live;
+  }
+}
+
+constexpr int kMoveThreads = 256;
+constexpr int kMoveVecs = 4;  // 16-byte words a thread has in flight
+
+__global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid_constant__ CompactArgs a, int page_vecs) {
+  wait_for_first();
+  const CacheDev& c = a.c;
+  const int moves = *a.moves;
+  if (moves == 0) return;
+  // tables
+  for (int b = blockIdx.x; b < c.S; b += gridDim.x) {
+    const int len = c.lens[b];
+    const int held = len < 0 ? 0 : min(pages_of(c, len), c.max_pages);
+    for (int j = threadIdx.x; j < held; j += kMoveThreads) {
+      int32_t* e = c.table + static_cast<size_t>(b) * c.max_pages + j;
+      const int page = *e;
+      if (page >= 0 && page < c.n_pages) *e = a.remap[page];
+      else c.state[kStateStatus] = kStatusDeviceAssert;
+    }
+  }
+  for (int m = blockIdx.x * kMoveThreads + threadIdx.x; m < moves; m += gridDim.x * kMoveThreads) {
+    const int from = a.src[m];
+    c.refs[a.dst[m]] = c.refs[from];
+    c.refs[from] = 0;
+  }
+  // rows: units of kMoveThreads * kMoveVecs 16-byte words of one page of one layer's K or V
+  const int per = (page_vecs + kMoveThreads * kMoveVecs - 1) / (kMoveThreads * kMoveVecs);
+  const long long units = static_cast<long long>(moves) * c.L * 2 * per;
+  for (long long u = blockIdx.x; u < units; u += gridDim.x) {
+    const int piece = static_cast<int>(u % per);
+    const long long w = u / per;
+    const int m = static_cast<int>(w / (2 * c.L)), s = static_cast<int>(w % (2 * c.L));
+    uint4* pool = static_cast<uint4*>(s & 1 ? c.v : c.k);
+    const size_t layer = static_cast<size_t>(s >> 1) * c.n_pages;
+    const uint4* from = pool + (layer + a.src[m]) * page_vecs;
+    uint4* to = pool + (layer + a.dst[m]) * page_vecs;
+    uint4 x[kMoveVecs];
+#pragma unroll
+    for (int v = 0; v < kMoveVecs; ++v) {
+      const int at = (piece * kMoveVecs + v) * kMoveThreads + threadIdx.x;
+      if (at < page_vecs) x[v] = from[at];
+    }
+#pragma unroll
+    for (int v = 0; v < kMoveVecs; ++v) {
+      const int at = (piece * kMoveVecs + v) * kMoveThreads + threadIdx.x;
+      if (at < page_vecs) to[at] = x[v];
+    }
+  }
+}
+
+size_t round_up(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+// commit: jobs and the pages taken (n_pages at most); fork: rows and lengths; compact: a count
+// and two lists of n_pages.
+size_t cache_workspace_bytes(const fib_attn_cache& c) {
+  const size_t pages = round_up(sizeof(int32_t) * static_cast<size_t>(c.n_pages));
+  const size_t commit = round_up(sizeof(CommitJob) * kMaxSeqs) + pages;
+  const size_t fork = round_up(sizeof(int32_t) * kMaxSeqs) +
+                      round_up(sizeof(int32_t) * static_cast<size_t>(c.max_seqs) * static_cast<size_t>(c.max_pages));
+  const size_t compact = 256 + 2 * pages;
+  size_t m = commit > fork ? commit : fork;
+  return m > compact ? m : compact;
+}
+
+cudaError_t launch_cache_commit(const fib_attn_cache& cache, int B, int T, int n_max, const int32_t* n_new,
+                                const int32_t* path, const void* k_new, const void* v_new, const float2* lo_tab,
+                                const float2* hi_tab, void* ws, cudaStream_t stream) {
+  CommitArgs a;
+  a.c = device_view(cache);
+  a.B = B;
+  a.T = T;
+  a.n_max = n_max;
+  a.n_new = n_new;
+  a.path = path;
+  a.k_new = k_new;
+  a.v_new = v_new;
+  a.rope_lo = lo_tab;
+  a.rope_hi = hi_tab;
+  a.jobs = static_cast<CommitJob*>(ws);
+  a.list = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + round_up(sizeof(CommitJob) * kMaxSeqs));
+  commit_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  // heads a block: so many that a block's 32 quads all have a row of its tokens
+  const int tokens = T < kWriteTokens ? T : kWriteTokens;
+  int heads = kWriteThreads / 4 / tokens;
+  heads = heads < 1 ? 1 : heads > cache.heads ? cache.heads : heads;
+  const dim3 grid(static_cast<unsigned>(B) * cache.n_layers, (cache.heads + heads - 1) / heads,
+                  (T + kWriteTokens - 1) / kWriteTokens);
+  return cache.dtype == FIB_DTYPE_F32
+             ? launch_second(commit_write_kernel<float>, grid, kWriteThreads, stream, a, heads)
+             : launch_second(commit_write_kernel<__nv_bfloat16>, grid, kWriteThreads, stream, a, heads);
+}
+
+cudaError_t launch_cache_fork(const fib_attn_cache& cache, const int32_t* src, void* ws, cudaStream_t stream) {
+  ForkArgs a;
+  a.c = device_view(cache);
+  a.src = src;
+  a.lens = static_cast<int32_t*>(ws);
+  a.rows = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + round_up(sizeof(int32_t) * kMaxSeqs));
+  fork_count_kernel<<<cache.max_seqs, kForkThreads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_second(fork_write_kernel, dim3(static_cast<unsigned>(cache.max_seqs)), kForkThreads, stream, a);
+}
+
+cudaError_t launch_cache_compact(const fib_attn_cache& cache, int32_t* remap, void* ws, cudaStream_t stream) {
+  CompactArgs a;
+  a.c = device_view(cache);
+  a.remap = remap;
+  a.moves = static_cast<int32_t*>(ws);
+  a.src = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + 256);
+  a.dst = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + 256 +
+                                     round_up(sizeof(int32_t) * static_cast<size_t>(cache.n_pages)));
+  compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int row_vecs = kD * (cache.dtype == FIB_DTYPE_F32 ? 4 : 2) / 16;
+  const int page_vecs = cache.heads * cache.page_rows * row_vecs;
+  return launch_second(compact_move_kernel, dim3(152 * 8), kMoveThreads, stream, a, page_vecs);
+}
+
+}  // namespace fibattn

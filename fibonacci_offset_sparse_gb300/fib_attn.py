@@ -16,13 +16,14 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfibattn.so")
 
 FIB_OK, FIB_ERR_INVALID_ARG, FIB_ERR_UNSUPPORTED, FIB_ERR_CUDA, FIB_ERR_NOMEM, \
-    FIB_ERR_TIMEOUT, FIB_ERR_DEVICE_ASSERT, FIB_ERR_RANGE = range(8)
+    FIB_ERR_TIMEOUT, FIB_ERR_DEVICE_ASSERT, FIB_ERR_RANGE, FIB_ERR_NO_PAGES = range(9)
 FIB_DEBUG_SKIP_COPY, FIB_DEBUG_CORRUPT_TABLE = 1, 2
 FIB_BASE_FIBONACCI, FIB_BASE_POW2, FIB_BASE_CUSTOM = 0, 1, 2
 FIB_SCHED_FIXED, FIB_SCHED_LINEAR, FIB_SCHED_COPRIME = 0, 1, 2
 FIB_MODE_MASK, FIB_MODE_INTERP = 0, 1
 FIB_DTYPE_F32, FIB_DTYPE_BF16 = 0, 1
 FIB_HEAD_DIM, FIB_MAX_RUNGS, FIB_MAX_WINDOW, FIB_MAX_LAYERS = 64, 32, 64, 256
+FIB_MAX_DRAFTS, FIB_MAX_SEQS, FIB_MAX_HEADS = 64, 1024, 1024
 
 EXPORTS = [
     "fib_attn_error_string", "fib_attn_base", "fib_attn_schedule", "fib_attn_mask_distances",
@@ -31,7 +32,9 @@ EXPORTS = [
     "fib_attn_fwd_prepare_kv", "fib_attn_fwd_attend", "fib_attn_bwd_workspace_size", "fib_attn_bwd",
     "fib_attn_debug_indices", "fib_attn_last_device_status", "fib_attn_plan_set_debug",
     "fib_attn_bwd_noalloc", "fib_attn_decode", "fib_attn_dense_fwd_workspace_size", "fib_attn_dense_fwd",
-    "fib_attn_debug_fill_shared", "fib_attn_bwd_prepared",
+    "fib_attn_debug_fill_shared", "fib_attn_bwd_prepared", "fib_attn_cache_workspace_size",
+    "fib_attn_cache_commit", "fib_attn_cache_fork", "fib_attn_cache_compact", "fib_attn_tree_decode",
+    "fib_attn_dense_tree_workspace_size", "fib_attn_dense_tree_decode",
 ]
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
@@ -39,6 +42,16 @@ _f32p = ctypes.POINTER(ctypes.c_float)
 _f64p = ctypes.POINTER(ctypes.c_double)
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
+
+
+class CacheStruct(ctypes.Structure):
+    """fib_attn_cache of include/fib_attn.h."""
+    _fields_ = [("dtype", _i), ("n_layers", _i), ("heads", _i), ("page_rows", _i), ("n_pages", _i),
+                ("max_seqs", _i), ("max_pages", _i), ("device", _i), ("k", _vp), ("v", _vp), ("table", _vp),
+                ("lens", _vp), ("refs", _vp), ("state", _vp)]
+
+
+_cachep = ctypes.POINTER(CacheStruct)
 
 _SIGS = {
     "fib_attn_error_string": (ctypes.c_char_p, [_i]),
@@ -70,6 +83,14 @@ _SIGS = {
                                   _vp, _vp, _vp, _vp]),
     "fib_attn_bwd_prepared": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _vp, ctypes.c_size_t, _vp, _vp, _vp, _vp,
                                    _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fib_attn_cache_workspace_size": (ctypes.c_size_t, [_cachep]),
+    "fib_attn_cache_commit": (_i, [_vp, _cachep, _i, _i, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fib_attn_cache_fork": (_i, [_cachep, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fib_attn_cache_compact": (_i, [_cachep, _vp, _vp, ctypes.c_size_t, _vp]),
+    "fib_attn_tree_decode": (_i, [_vp, _i, _cachep, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "fib_attn_dense_tree_workspace_size": (ctypes.c_size_t, [_vp, _cachep, _i, _i, _i]),
+    "fib_attn_dense_tree_decode": (_i, [_vp, _i, _cachep, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                        ctypes.c_size_t, _vp]),
 }
 
 _lib = None
@@ -299,6 +320,187 @@ def fib_attn_decode(plan: Plan, layer: int, pos: int, q, k_cache, v_cache, o=Non
     _check("fib_attn_decode", lib().fib_attn_decode(
         plan.handle, layer, B, H, N, pos, _DT[q.dtype], _ptr(q), _ptr(k_cache), _ptr(v_cache),
         _ptr(o), _ptr(lse), _ptr(alpha_dev), _stream(stream)))
+    return o, lse
+
+
+# ------------------------------------------------------------------------ paged cache, tree decode
+class Cache:
+    """A paged key/value cache (fib_attn_cache): torch tensors and the struct that describes them.
+
+    k, v: pools [n_layers, n_pages, heads, page_rows, 64]; table [max_seqs, max_pages], lens
+    [max_seqs], refs [n_pages] and state [4], int32, are views of one tensor ``meta`` (a copy of
+    it is a snapshot of everything but the rows)."""
+
+    def __init__(self, k, v, meta, max_seqs, max_pages):
+        self.k, self.v, self.meta = k, v, meta
+        self.n_layers, self.n_pages, self.heads, self.page_rows = k.shape[:4]
+        self.max_seqs, self.max_pages, self.dtype, self.device = max_seqs, max_pages, k.dtype, k.device
+        at = _cache_meta(self.n_pages, max_seqs, max_pages)
+        self.state, self.refs = meta[:4], meta[4:4 + self.n_pages]
+        self.lens, self.table = meta[at[0]:at[0] + max_seqs], meta[at[1]:at[2]].view(max_seqs, max_pages)
+        self.struct = CacheStruct(_DT[k.dtype], self.n_layers, self.heads, self.page_rows, self.n_pages, max_seqs,
+                                  max_pages, k.device.index, k.data_ptr(), v.data_ptr(), self.table.data_ptr(),
+                                  self.lens.data_ptr(), self.refs.data_ptr(), self.state.data_ptr())
+
+
+def _cache_meta(n_pages: int, max_seqs: int, max_pages: int):
+    """(first of lens, first of table, end) in a cache's meta tensor; state and refs precede."""
+    lens = 4 + n_pages
+    return lens, lens + max_seqs, lens + max_seqs + max_seqs * max_pages
+
+
+def fib_attn_cache_create(n_layers: int, heads: int, page_rows: int, n_pages: int, max_seqs: int, max_pages: int,
+                          dtype, k=None, v=None, device="cuda") -> Cache:
+    """An empty cache; its memory is allocated by torch, the pools only where not given."""
+    shape = (n_layers, n_pages, heads, page_rows, FIB_HEAD_DIM)
+    device = torch.device(device)
+    if k is not None:
+        device = k.device
+    if device.type != "cuda":
+        raise ValueError("the cache lives on a CUDA device")
+    if device.index is None:
+        device = torch.device("cuda", torch.cuda.current_device())
+    k = torch.zeros(shape, dtype=dtype, device=device) if k is None else k
+    v = torch.zeros(shape, dtype=dtype, device=device) if v is None else v
+    for t in (k, v):
+        if tuple(t.shape) != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+            raise ValueError("k and v must be contiguous [n_layers, n_pages, heads, page_rows, 64] of dtype on one device")
+    at = _cache_meta(n_pages, max_seqs, max_pages)
+    meta = torch.zeros(at[2], dtype=torch.int32, device=device)
+    meta[at[1]:] = -1
+    c = Cache(k, v, meta, max_seqs, max_pages)
+    if lib().fib_attn_cache_workspace_size(ctypes.byref(c.struct)) == 0:
+        raise FibAttnError("fib_attn_cache_create", FIB_ERR_INVALID_ARG)
+    return c
+
+
+def fib_attn_cache_workspace_size(cache: Cache) -> int:
+    return int(lib().fib_attn_cache_workspace_size(ctypes.byref(cache.struct)))
+
+
+def fib_attn_cache_status(cache: Cache) -> int:
+    """The status that the cache's calls recorded (synchronises), cleared."""
+    st = int(cache.state[1].item())
+    cache.state[1] = 0
+    return st
+
+
+def _on(cache: Cache, dtype, *ts):
+    """Contiguous tensors of `dtype` on the cache's device (None passes)."""
+    for t in ts:
+        if t is not None and (t.dtype != dtype or t.device != cache.device or not t.is_contiguous()):
+            raise ValueError(f"expected contiguous {dtype} tensors on {cache.device}")
+
+
+def _scratch(cache: Cache, workspace, need: int, stream):
+    """The caller's workspace, or one of `need` bytes (held for `stream`'s use)."""
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.device)
+        if stream is not None:
+            workspace.record_stream(stream)
+    elif workspace.device != cache.device or not workspace.is_contiguous():
+        raise ValueError(f"the workspace must be contiguous, on {cache.device}")
+    return workspace
+
+
+def fib_attn_cache_commit(plan: Plan, cache: Cache, k_new, v_new, n_new, path=None, workspace=None, stream=None):
+    """Sequence b gains n_new[b] rows, in every layer: k_new, v_new [n_layers, B, heads, T, 64] raw
+    rows; n_new int32 [B]; path int32 [B, T], the nodes taken (None: the first ones)."""
+    _on(cache, cache.dtype, k_new, v_new)
+    _on(cache, torch.int32, n_new, path)
+    if k_new.dim() != 5 or (k_new.shape[0], k_new.shape[2], k_new.shape[4]) != (cache.n_layers, cache.heads, FIB_HEAD_DIM) \
+            or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [n_layers, B, heads, T, 64]")
+    B, T = k_new.shape[1], k_new.shape[3]
+    if tuple(n_new.shape) != (B,) or (path is not None and tuple(path.shape) != (B, T)):
+        raise ValueError("n_new must be [B] and path [B, T]")
+    workspace = _scratch(cache, workspace, fib_attn_cache_workspace_size(cache), stream)
+    _check("fib_attn_cache_commit", lib().fib_attn_cache_commit(
+        plan.handle, ctypes.byref(cache.struct), B, T, _ptr(n_new), _ptr(path), _ptr(k_new), _ptr(v_new),
+        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def fib_attn_cache_fork(cache: Cache, src, workspace=None, stream=None):
+    """Sequence b becomes what sequence src[b] is now (int32 [max_seqs]; -1 ends it)."""
+    _on(cache, torch.int32, src)
+    if tuple(src.shape) != (cache.max_seqs,):
+        raise ValueError("src must be [max_seqs]")
+    workspace = _scratch(cache, workspace, fib_attn_cache_workspace_size(cache), stream)
+    _check("fib_attn_cache_fork", lib().fib_attn_cache_fork(
+        ctypes.byref(cache.struct), _ptr(src), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+
+
+def fib_attn_cache_compact(cache: Cache, remap=None, workspace=None, stream=None):
+    """Moves the pages in use to the lowest ids (their number: cache.state[2]); returns remap int32
+    [n_pages], the new id of each page, -1 for a free one."""
+    if remap is None:
+        remap = torch.empty(cache.n_pages, dtype=torch.int32, device=cache.device)
+        if stream is not None:
+            remap.record_stream(stream)
+    _on(cache, torch.int32, remap)
+    if tuple(remap.shape) != (cache.n_pages,):
+        raise ValueError("remap must be [n_pages]")
+    workspace = _scratch(cache, workspace, fib_attn_cache_workspace_size(cache), stream)
+    _check("fib_attn_cache_compact", lib().fib_attn_cache_compact(
+        ctypes.byref(cache.struct), _ptr(remap), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
+    return remap
+
+
+def _tree_shapes(cache: Cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream):
+    """Checks a tree decode's tensors; returns (B, Hq, T, o, lse) with the outputs allocated."""
+    _on(cache, cache.dtype, q, k_new, v_new, o)
+    _on(cache, torch.int32, parent, n_nodes)
+    _on(cache, torch.float32, lse)
+    if q.dim() != 4 or q.shape[-1] != FIB_HEAD_DIM:
+        raise ValueError("q must be [B, Hq, T, 64]")
+    B, Hq, T = q.shape[:3]
+    if tuple(k_new.shape) != (B, cache.heads, T, FIB_HEAD_DIM) or v_new.shape != k_new.shape:
+        raise ValueError("k_new and v_new must be [B, heads, T, 64]")
+    if (parent is not None and tuple(parent.shape) != (B, T)) or (n_nodes is not None and tuple(n_nodes.shape) != (B,)):
+        raise ValueError("parent must be [B, T] and n_nodes [B]")
+    if (o is not None and o.shape != q.shape) or (lse is not None and tuple(lse.shape) != (B, Hq, T)):
+        raise ValueError("o must have q's shape and lse [B, Hq, T]")
+    made = []
+    if o is None:
+        o = torch.empty_like(q)
+        made.append(o)
+    if lse is None and want_lse:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
+        made.append(lse)
+    if stream is not None:
+        for t in made:
+            t.record_stream(stream)
+    return B, Hq, T, o, lse
+
+
+def fib_attn_tree_decode(plan: Plan, layer: int, cache: Cache, q, k_new, v_new, parent=None, n_nodes=None, o=None,
+                         lse=None, N=None, alpha_dev=None, want_lse: bool = True, stream=None):
+    """A tree of drafted tokens over the cache, the layer's window and rungs: q [B, Hq, T, 64], k_new
+    and v_new [B, heads, T, 64]; parent int32 [B, T] (None: a chain), n_nodes int32 [B] (None: T);
+    N: as in fib_attn_fwd (None: the plan's N_max).  Returns (o, lse)."""
+    B, Hq, T, o, lse = _tree_shapes(cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream)
+    _on(cache, torch.float32, alpha_dev)
+    _check("fib_attn_tree_decode", lib().fib_attn_tree_decode(
+        plan.handle, layer, ctypes.byref(cache.struct), B, Hq, T, plan.N_max if N is None else N, _ptr(q), _ptr(k_new),
+        _ptr(v_new), _ptr(parent), _ptr(n_nodes), _ptr(o), _ptr(lse), _ptr(alpha_dev), _stream(stream)))
+    return o, lse
+
+
+def fib_attn_dense_tree_workspace_size(plan: Plan, cache: Cache, B: int, Hq: int, T: int) -> int:
+    return int(lib().fib_attn_dense_tree_workspace_size(plan.handle, ctypes.byref(cache.struct), B, Hq, T))
+
+
+def fib_attn_dense_tree_decode(plan: Plan, layer: int, cache: Cache, q, k_new, v_new, parent=None, n_nodes=None,
+                               o=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
+    """fib_attn_tree_decode for the dense control: every cached row, the ancestors, the node itself."""
+    B, Hq, T, o, lse = _tree_shapes(cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream)
+    workspace = _scratch(cache, workspace, fib_attn_dense_tree_workspace_size(plan, cache, B, Hq, T), stream)
+    _check("fib_attn_dense_tree_decode", lib().fib_attn_dense_tree_decode(
+        plan.handle, layer, ctypes.byref(cache.struct), B, Hq, T, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(parent),
+        _ptr(n_nodes), _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
+        _stream(stream)))
     return o, lse
 
 

@@ -56,8 +56,9 @@ enum fib_status {
   FIB_ERR_NOMEM = 4,         /* host or device allocation failed                        */
   FIB_ERR_TIMEOUT = 5,       /* a bounded device wait gave up (see last_device_status)  */
   FIB_ERR_DEVICE_ASSERT = 6, /* a device-side check recorded a violated invariant       */
-  FIB_ERR_RANGE = 7          /* an input value does not fit the float16 operands of the
+  FIB_ERR_RANGE = 7,         /* an input value does not fit the float16 operands of the
                                 bf16 tensor-core path (see fib_attn_fwd)                */
+  FIB_ERR_NO_PAGES = 8       /* a commit found fewer free cache pages than it needs     */
 };
 
 /* Test hooks of fib_attn_plan_set_debug (bit flags). */
@@ -72,6 +73,9 @@ enum fib_dtype { FIB_DTYPE_F32 = 0, FIB_DTYPE_BF16 = 1 };
 #define FIB_MAX_RUNGS 32  /* rungs per layer, after dedup */
 #define FIB_MAX_WINDOW 64 /* largest window W */
 #define FIB_MAX_LAYERS 256
+#define FIB_MAX_DRAFTS 64  /* nodes of a tree of drafted tokens */
+#define FIB_MAX_SEQS 1024  /* sequences of a paged cache */
+#define FIB_MAX_HEADS 1024 /* heads of a paged cache and of a decode over it */
 
 /* Human-readable name of a status code (static storage; never NULL).  No counterpart in
  * the paper. */
@@ -211,6 +215,127 @@ int fib_attn_dense_fwd(fib_attn_plan_t p, int B, int H, int N, int dtype, const 
 int fib_attn_decode(fib_attn_plan_t p, int layer, int B, int H, int N, int pos, int dtype,
                     const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
                     const float* alpha_dev, void* stream);
+
+/* ----------------------------------------------------------------- paged cache ----
+ * A key/value cache that sequences share, grow and give back, and decode over it for one new
+ * token or a tree of drafted ones.  The paper has no counterpart of the cache itself; Key
+ * results 2 ("Efficiency") compares the inference latency of the paths that read it.
+ *
+ * The cache is caller-owned device memory that this struct describes.  Row r of sequence b
+ * is row r % page_rows of page table[b][r / page_rows]; rows 0 .. lens[b]-1 are filled.  A
+ * pool row holds, in the type of the inputs, K rotated at its own position ("Implementation":
+ * RoPE is applied before the rows are gathered; rounded once, to that type) or V as given.
+ * refs[p] counts the sequences that hold page p; a page is free iff refs[p] == 0.  Only pages
+ * with refs[p] == 1 are written, so sequences may share pages (fib_attn_cache_fork); a caller
+ * may hold a page itself by adding 1 to its count.  Table entries behind a sequence's pages
+ * are ignored.  To start empty: lens, refs and state 0 (table -1 by custom).
+ * state[0] is a lower bound of the lowest free page (0 always is one; a caller that writes
+ * refs itself lowers it accordingly), state[1] a fib_status that the cache calls record (they
+ * run on the device and cannot return it; the caller reads and clears it), state[2] the number
+ * of pages in use as fib_attn_cache_compact found it, state[3] unused.
+ * Alignment: k, v, refs and state 16 bytes, table and lens 4.  Limits: page_rows one of 16,
+ * 32, 64, 128, 256; n_layers <= FIB_MAX_LAYERS; heads <= FIB_MAX_HEADS; max_seqs <= FIB_MAX_SEQS; max_pages * page_rows <= 2^30;
+ * n_pages * heads * page_rows < 2^31.
+ * Calls that change a cache (commit, fork, compact) are ordered by the caller with one another
+ * and with the decodes that read it (the same stream, or events); so are calls that share a
+ * workspace, in captured graphs too.                                                    */
+typedef struct fib_attn_cache_s {
+  int dtype;      /* fib_dtype of the rows */
+  int n_layers;   /* pools k, v: [n_layers, n_pages, heads, page_rows, 64] */
+  int heads;      /* key/value heads */
+  int page_rows;
+  int n_pages;
+  int max_seqs;   /* table: [max_seqs, max_pages]; lens: [max_seqs]; refs: [n_pages] */
+  int max_pages;
+  int device;     /* CUDA device of the memory below */
+  void* k;
+  void* v;
+  int32_t* table;
+  int32_t* lens;
+  int32_t* refs;
+  int32_t* state; /* [4] */
+} fib_attn_cache;
+
+/* Bytes of device scratch, 256-byte aligned, for fib_attn_cache_commit, _fork and _compact of
+ * this cache (contents on entry ignored); 0 for a struct that breaks the rules above.     */
+size_t fib_attn_cache_workspace_size(const fib_attn_cache* c);
+
+/* Appends accepted tokens to sequences 0 .. B-1, in every layer at once.  Sequence b gains
+ * n_new[b] rows (0 <= n_new[b] <= T; 0: untouched); row lens[b] + i is node path[b][i] of its
+ * T tokens (path NULL: node i, as for a prompt or a chain), at position lens[b] + i: K is
+ * rotated there and rounded to the cache's type, V copied.  k_new, v_new: [n_layers, B,
+ * heads, T, 64] raw rows in the cache's type; n_new: int32 [B]; path: int32 [B, T] or NULL,
+ * both on the device.  Rotation uses the plan's RoPE tables (positions < its N_max).
+ * Pages: in the order of b, a sequence whose partly filled last page is shared (refs > 1)
+ * first takes a free page, copies the filled rows of every layer into it and lets go of the
+ * shared one -- unless every holder of that page gains rows in this call, when the last of
+ * them keeps it -- and then takes what it needs for its new rows; free pages are taken in
+ * ascending order.  Rows of a page behind a sequence's last one are left as they were.
+ * All or nothing: state[1] becomes FIB_ERR_NO_PAGES where too few pages are free, or
+ * FIB_ERR_DEVICE_ASSERT for n_new outside [0, T], a path entry outside [0, T), a length that
+ * would pass max_pages * page_rows or the plan's N_max, or a page id outside the pool, and the
+ * call then changes nothing else.  k_new and v_new must not overlap the cache.
+ * Errors: FIB_ERR_INVALID_ARG (null or misaligned pointers, a struct that breaks the rules, B
+ * outside [1, max_seqs], T outside [1, 2^20], a short workspace, another device current),
+ * FIB_ERR_CUDA.                                                                         */
+int fib_attn_cache_commit(fib_attn_plan_t p, const fib_attn_cache* c, int B, int T,
+                          const int32_t* n_new, const int32_t* path, const void* k_new,
+                          const void* v_new, void* workspace, size_t ws_bytes, void* stream);
+
+/* Sequence b becomes what sequence src[b] is now: it holds the same pages (shared, nothing is
+ * copied) and has its length; src[b] == b keeps, src[b] == -1 ends it (length 0).  src:
+ * int32 [max_seqs] on the device.  One call reorders beams, forks prompts and frees: counts
+ * follow, and a page that no sequence holds any more is free.  Entries of a row behind the new
+ * pages that held old ones become -1.  A src entry outside [-1, max_seqs) or a length outside
+ * [0, max_pages * page_rows] makes state[1] FIB_ERR_DEVICE_ASSERT and changes nothing else; a
+ * page id outside the pool is recorded the same way and not counted.  Errors as commit.   */
+int fib_attn_cache_fork(const fib_attn_cache* c, const int32_t* src, void* workspace,
+                        size_t ws_bytes, void* stream);
+
+/* Moves the pages in use to the lowest ids, so that the pool's tail [state[2], n_pages) is
+ * free: with n pages in use, the i-th used page at or above n (ascending) moves into the i-th
+ * free page below n, in every layer; the others stay.  table and refs follow.  remap: int32
+ * [n_pages] on the device, written: the new id of each page, -1 for one that was free (for
+ * pages that the caller holds itself).  Errors as commit.                                 */
+int fib_attn_cache_compact(const fib_attn_cache* c, int32_t* remap, void* workspace,
+                           size_t ws_bytes, void* stream);
+
+/* Sparse decode of a tree of drafted tokens ("Attended set", "Scaling", "Implementation", as
+ * fib_attn_decode).  Sequence b < B has lens[b] rows in the cache and n_nodes[b] <= T
+ * drafted tokens (NULL: T; 0: none).  parent[b][s] < s is the node that node s follows, or -1
+ * where it follows the cached rows (NULL: a chain, parent s - 1), so node s sits at position
+ * lens[b] + depth(s) and attends what row `position` of fib_attn_fwd attends in the sequence
+ * of the cached rows and its own line of ancestors: the key at distance d is the ancestor d
+ * levels up, or cache row position - d where there is none.  T = 1 is one token.  The drafted
+ * rows are not written to the cache (fib_attn_cache_commit does that with the accepted ones).
+ * q, o: [B, Hq, T, 64]; k_new, v_new: [B, heads, T, 64], raw rows; query head h reads key head
+ * h / (Hq / heads), Hq a multiple of heads; lse: [B, Hq, T] float32 or NULL; parent: int32
+ * [B, T]; n_nodes: int32 [B]; all device, in the cache's type, T <= FIB_MAX_DRAFTS, Hq <=
+ * FIB_MAX_HEADS, B <= max_seqs.  layer: of the plan (distances) and of the cache (rows).  N, 1 <= N <= N_max,
+ * bounds the positions and builds the power-of-two base, as in fib_attn_fwd.  Rows of o and
+ * lse at and behind n_nodes[b] are left as they were.  What a node does not attend (other
+ * branches, rows behind lens[b], padding) is never used in its result, whatever it holds.
+ * A bad n_nodes or parent, a length outside the table, a position >= N or a page id outside
+ * the pool records FIB_ERR_DEVICE_ASSERT in the plan's status word (read with
+ * fib_attn_last_device_status); that sequence's o and lse are then unspecified.
+ * Errors as fib_attn_decode.                                                            */
+int fib_attn_tree_decode(fib_attn_plan_t p, int layer, const fib_attn_cache* c, int B, int Hq,
+                         int T, int N, const void* q, const void* k_new, const void* v_new,
+                         const int32_t* parent, const int32_t* n_nodes, void* o, float* lse,
+                         const float* alpha_dev, void* stream);
+
+/* Dense decode of a tree of drafted tokens, the dense control's ("Controls") form of the call
+ * above: node s attends all lens[b] cached rows, its ancestors and itself.  The plan supplies
+ * only its RoPE tables (positions < N_max) and status word; layer is the cache's.  workspace:
+ * fib_attn_dense_tree_workspace_size(p, c, B, Hq, T) bytes of device scratch, 256-byte
+ * aligned, contents on entry ignored.  Everything else as fib_attn_tree_decode.           */
+size_t fib_attn_dense_tree_workspace_size(fib_attn_plan_t p, const fib_attn_cache* c, int B,
+                                          int Hq, int T);
+int fib_attn_dense_tree_decode(fib_attn_plan_t p, int layer, const fib_attn_cache* c, int B,
+                               int Hq, int T, const void* q, const void* k_new,
+                               const void* v_new, const int32_t* parent,
+                               const int32_t* n_nodes, void* o, float* lse, void* workspace,
+                               size_t ws_bytes, void* stream);
 
 /* --------------------------------------------------------------------- backward ----
  * "Implementation": the interpolated rows make the output differentiable in alpha, and
