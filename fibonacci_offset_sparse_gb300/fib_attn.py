@@ -341,6 +341,7 @@ class Cache:
         self.struct = CacheStruct(_DT[k.dtype], self.n_layers, self.heads, self.page_rows, self.n_pages, max_seqs,
                                   max_pages, k.device.index, k.data_ptr(), v.data_ptr(), self.table.data_ptr(),
                                   self.lens.data_ptr(), self.refs.data_ptr(), self.state.data_ptr())
+        self.pointer, self.index = ctypes.pointer(self.struct), k.device.index
 
 
 def _cache_meta(n_pages: int, max_seqs: int, max_pages: int):
@@ -369,13 +370,13 @@ def fib_attn_cache_create(n_layers: int, heads: int, page_rows: int, n_pages: in
     meta = torch.zeros(at[2], dtype=torch.int32, device=device)
     meta[at[1]:] = -1
     c = Cache(k, v, meta, max_seqs, max_pages)
-    if lib().fib_attn_cache_workspace_size(ctypes.byref(c.struct)) == 0:
+    if lib().fib_attn_cache_workspace_size(c.pointer) == 0:
         raise FibAttnError("fib_attn_cache_create", FIB_ERR_INVALID_ARG)
     return c
 
 
 def fib_attn_cache_workspace_size(cache: Cache) -> int:
-    return int(lib().fib_attn_cache_workspace_size(ctypes.byref(cache.struct)))
+    return int(lib().fib_attn_cache_workspace_size(cache.pointer))
 
 
 def fib_attn_cache_status(cache: Cache) -> int:
@@ -385,50 +386,62 @@ def fib_attn_cache_status(cache: Cache) -> int:
     return st
 
 
-def _on(cache: Cache, dtype, *ts):
-    """Contiguous tensors of `dtype` on the cache's device (None passes)."""
-    for t in ts:
-        if t is not None and (t.dtype != dtype or t.device != cache.device or not t.is_contiguous()):
-            raise ValueError(f"expected contiguous {dtype} tensors on {cache.device}")
+# A decode step makes a few of the calls below a layer, each of a few microseconds on the GPU: their
+# checks read each attribute of a tensor once, and addresses go to ctypes as plain integers.
+def _bad(t, dtype, index) -> bool:
+    """Whether t is not a contiguous `dtype` tensor on CUDA device `index`."""
+    return t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()
 
 
-def _scratch(cache: Cache, workspace, need: int, stream):
-    """The caller's workspace, or one of `need` bytes (held for `stream`'s use)."""
+def _address(t):
+    return None if t is None else t.data_ptr()
+
+
+def _raw_stream(stream, index: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _scratch(cache: Cache, workspace, need, stream):
+    """(address, bytes) of the caller's workspace, or of one of need() bytes (held for `stream`'s use)
+    and the tensor itself."""
     if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=cache.device)
+        workspace = torch.empty(max(need(), 1), dtype=torch.uint8, device=cache.device)
         if stream is not None:
             workspace.record_stream(stream)
-    elif workspace.device != cache.device or not workspace.is_contiguous():
+    elif workspace.get_device() != cache.index or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be contiguous, on {cache.device}")
-    return workspace
+    return workspace.data_ptr(), workspace.nbytes, workspace
 
 
 def fib_attn_cache_commit(plan: Plan, cache: Cache, k_new, v_new, n_new, path=None, workspace=None, stream=None):
     """Sequence b gains n_new[b] rows, in every layer: k_new, v_new [n_layers, B, heads, T, 64] raw
     rows; n_new int32 [B]; path int32 [B, T], the nodes taken (None: the first ones)."""
-    _on(cache, cache.dtype, k_new, v_new)
-    _on(cache, torch.int32, n_new, path)
-    if k_new.dim() != 5 or (k_new.shape[0], k_new.shape[2], k_new.shape[4]) != (cache.n_layers, cache.heads, FIB_HEAD_DIM) \
-            or v_new.shape != k_new.shape:
+    index, shape = cache.index, k_new.shape
+    if len(shape) != 5 or v_new.shape != shape or shape[0] != cache.n_layers or shape[2] != cache.heads or \
+            shape[4] != FIB_HEAD_DIM:
         raise ValueError("k_new and v_new must be [n_layers, B, heads, T, 64]")
-    B, T = k_new.shape[1], k_new.shape[3]
-    if tuple(n_new.shape) != (B,) or (path is not None and tuple(path.shape) != (B, T)):
-        raise ValueError("n_new must be [B] and path [B, T]")
-    workspace = _scratch(cache, workspace, fib_attn_cache_workspace_size(cache), stream)
-    _check("fib_attn_cache_commit", lib().fib_attn_cache_commit(
-        plan.handle, ctypes.byref(cache.struct), B, T, _ptr(n_new), _ptr(path), _ptr(k_new), _ptr(v_new),
-        _ptr(workspace), workspace.numel() * workspace.element_size(), _stream(stream)))
+    B, T = shape[1], shape[3]
+    if _bad(k_new, cache.dtype, index) or _bad(v_new, cache.dtype, index):
+        raise ValueError(f"k_new and v_new must be contiguous {cache.dtype} on {cache.device}")
+    if n_new.shape != (B,) or _bad(n_new, torch.int32, index):
+        raise ValueError(f"n_new must be int32 [B] on {cache.device}")
+    if path is not None and (path.shape != (B, T) or _bad(path, torch.int32, index)):
+        raise ValueError(f"path must be int32 [B, T] on {cache.device}")
+    at, size, workspace = _scratch(cache, workspace, lambda: fib_attn_cache_workspace_size(cache), stream)
+    code = lib().fib_attn_cache_commit(plan.handle, cache.pointer, B, T, n_new.data_ptr(), _address(path),
+                                       k_new.data_ptr(), v_new.data_ptr(), at, size, _raw_stream(stream, index))
+    if code:
+        raise FibAttnError("fib_attn_cache_commit", code)
 
 
 def fib_attn_cache_fork(cache: Cache, src, workspace=None, stream=None):
     """Sequence b becomes what sequence src[b] is now (int32 [max_seqs]; -1 ends it)."""
-    _on(cache, torch.int32, src)
-    if tuple(src.shape) != (cache.max_seqs,):
-        raise ValueError("src must be [max_seqs]")
-    workspace = _scratch(cache, workspace, fib_attn_cache_workspace_size(cache), stream)
-    _check("fib_attn_cache_fork", lib().fib_attn_cache_fork(
-        ctypes.byref(cache.struct), _ptr(src), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+    if src.shape != (cache.max_seqs,) or _bad(src, torch.int32, cache.index):
+        raise ValueError(f"src must be int32 [max_seqs] on {cache.device}")
+    at, size, workspace = _scratch(cache, workspace, lambda: fib_attn_cache_workspace_size(cache), stream)
+    code = lib().fib_attn_cache_fork(cache.pointer, src.data_ptr(), at, size, _raw_stream(stream, cache.index))
+    if code:
+        raise FibAttnError("fib_attn_cache_fork", code)
 
 
 def fib_attn_cache_compact(cache: Cache, remap=None, workspace=None, stream=None):
@@ -438,40 +451,42 @@ def fib_attn_cache_compact(cache: Cache, remap=None, workspace=None, stream=None
         remap = torch.empty(cache.n_pages, dtype=torch.int32, device=cache.device)
         if stream is not None:
             remap.record_stream(stream)
-    _on(cache, torch.int32, remap)
-    if tuple(remap.shape) != (cache.n_pages,):
-        raise ValueError("remap must be [n_pages]")
-    workspace = _scratch(cache, workspace, fib_attn_cache_workspace_size(cache), stream)
-    _check("fib_attn_cache_compact", lib().fib_attn_cache_compact(
-        ctypes.byref(cache.struct), _ptr(remap), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+    elif remap.shape != (cache.n_pages,) or _bad(remap, torch.int32, cache.index):
+        raise ValueError(f"remap must be int32 [n_pages] on {cache.device}")
+    at, size, workspace = _scratch(cache, workspace, lambda: fib_attn_cache_workspace_size(cache), stream)
+    code = lib().fib_attn_cache_compact(cache.pointer, remap.data_ptr(), at, size, _raw_stream(stream, cache.index))
+    if code:
+        raise FibAttnError("fib_attn_cache_compact", code)
     return remap
 
 
-def _tree_shapes(cache: Cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream):
+def _tree_tensors(cache: Cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream):
     """Checks a tree decode's tensors; returns (B, Hq, T, o, lse) with the outputs allocated."""
-    _on(cache, cache.dtype, q, k_new, v_new, o)
-    _on(cache, torch.int32, parent, n_nodes)
-    _on(cache, torch.float32, lse)
-    if q.dim() != 4 or q.shape[-1] != FIB_HEAD_DIM:
+    index, dtype, shape = cache.index, cache.dtype, q.shape
+    if len(shape) != 4 or shape[3] != FIB_HEAD_DIM:
         raise ValueError("q must be [B, Hq, T, 64]")
-    B, Hq, T = q.shape[:3]
-    if tuple(k_new.shape) != (B, cache.heads, T, FIB_HEAD_DIM) or v_new.shape != k_new.shape:
+    B, Hq, T = shape[0], shape[1], shape[2]
+    if k_new.shape != (B, cache.heads, T, FIB_HEAD_DIM) or v_new.shape != k_new.shape:
         raise ValueError("k_new and v_new must be [B, heads, T, 64]")
-    if (parent is not None and tuple(parent.shape) != (B, T)) or (n_nodes is not None and tuple(n_nodes.shape) != (B,)):
-        raise ValueError("parent must be [B, T] and n_nodes [B]")
-    if (o is not None and o.shape != q.shape) or (lse is not None and tuple(lse.shape) != (B, Hq, T)):
-        raise ValueError("o must have q's shape and lse [B, Hq, T]")
-    made = []
+    if _bad(q, dtype, index) or _bad(k_new, dtype, index) or _bad(v_new, dtype, index):
+        raise ValueError(f"q, k_new and v_new must be contiguous {dtype} on {cache.device}")
+    if parent is not None and (parent.shape != (B, T) or _bad(parent, torch.int32, index)):
+        raise ValueError(f"parent must be int32 [B, T] on {cache.device}")
+    if n_nodes is not None and (n_nodes.shape != (B,) or _bad(n_nodes, torch.int32, index)):
+        raise ValueError(f"n_nodes must be int32 [B] on {cache.device}")
     if o is None:
         o = torch.empty_like(q)
-        made.append(o)
-    if lse is None and want_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=q.device)
-        made.append(lse)
-    if stream is not None:
-        for t in made:
-            t.record_stream(stream)
+        if stream is not None:
+            o.record_stream(stream)
+    elif o.shape != shape or _bad(o, dtype, index):
+        raise ValueError(f"o must be like q, on {cache.device}")
+    if lse is not None:
+        if lse.shape != (B, Hq, T) or _bad(lse, torch.float32, index):
+            raise ValueError(f"lse must be float32 [B, Hq, T] on {cache.device}")
+    elif want_lse:
+        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
+        if stream is not None:
+            lse.record_stream(stream)
     return B, Hq, T, o, lse
 
 
@@ -480,27 +495,33 @@ def fib_attn_tree_decode(plan: Plan, layer: int, cache: Cache, q, k_new, v_new, 
     """A tree of drafted tokens over the cache, the layer's window and rungs: q [B, Hq, T, 64], k_new
     and v_new [B, heads, T, 64]; parent int32 [B, T] (None: a chain), n_nodes int32 [B] (None: T);
     N: as in fib_attn_fwd (None: the plan's N_max).  Returns (o, lse)."""
-    B, Hq, T, o, lse = _tree_shapes(cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream)
-    _on(cache, torch.float32, alpha_dev)
-    _check("fib_attn_tree_decode", lib().fib_attn_tree_decode(
-        plan.handle, layer, ctypes.byref(cache.struct), B, Hq, T, plan.N_max if N is None else N, _ptr(q), _ptr(k_new),
-        _ptr(v_new), _ptr(parent), _ptr(n_nodes), _ptr(o), _ptr(lse), _ptr(alpha_dev), _stream(stream)))
+    B, Hq, T, o, lse = _tree_tensors(cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream)
+    if alpha_dev is not None and (alpha_dev.numel() < plan.n_layers or _bad(alpha_dev, torch.float32, cache.index)):
+        raise ValueError(f"alpha_dev must be float32 [n_layers] on {cache.device}")
+    code = lib().fib_attn_tree_decode(
+        plan.handle, layer, cache.pointer, B, Hq, T, plan.N_max if N is None else N, q.data_ptr(), k_new.data_ptr(),
+        v_new.data_ptr(), _address(parent), _address(n_nodes), o.data_ptr(), _address(lse), _address(alpha_dev),
+        _raw_stream(stream, cache.index))
+    if code:
+        raise FibAttnError("fib_attn_tree_decode", code)
     return o, lse
 
 
 def fib_attn_dense_tree_workspace_size(plan: Plan, cache: Cache, B: int, Hq: int, T: int) -> int:
-    return int(lib().fib_attn_dense_tree_workspace_size(plan.handle, ctypes.byref(cache.struct), B, Hq, T))
+    return int(lib().fib_attn_dense_tree_workspace_size(plan.handle, cache.pointer, B, Hq, T))
 
 
 def fib_attn_dense_tree_decode(plan: Plan, layer: int, cache: Cache, q, k_new, v_new, parent=None, n_nodes=None,
                                o=None, lse=None, want_lse: bool = True, workspace=None, stream=None):
     """fib_attn_tree_decode for the dense control: every cached row, the ancestors, the node itself."""
-    B, Hq, T, o, lse = _tree_shapes(cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream)
-    workspace = _scratch(cache, workspace, fib_attn_dense_tree_workspace_size(plan, cache, B, Hq, T), stream)
-    _check("fib_attn_dense_tree_decode", lib().fib_attn_dense_tree_decode(
-        plan.handle, layer, ctypes.byref(cache.struct), B, Hq, T, _ptr(q), _ptr(k_new), _ptr(v_new), _ptr(parent),
-        _ptr(n_nodes), _ptr(o), _ptr(lse), _ptr(workspace), workspace.numel() * workspace.element_size(),
-        _stream(stream)))
+    B, Hq, T, o, lse = _tree_tensors(cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream)
+    at, size, workspace = _scratch(cache, workspace,
+                                   lambda: fib_attn_dense_tree_workspace_size(plan, cache, B, Hq, T), stream)
+    code = lib().fib_attn_dense_tree_decode(
+        plan.handle, layer, cache.pointer, B, Hq, T, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _address(parent),
+        _address(n_nodes), o.data_ptr(), _address(lse), at, size, _raw_stream(stream, cache.index))
+    if code:
+        raise FibAttnError("fib_attn_dense_tree_decode", code)
     return o, lse
 
 
