@@ -1,0 +1,518 @@
+// What the two kernels of the dense tree decode share (tree_dense.cu, tree_dense_tc.cu): the cut of the work,
+// the feeding warp, the drafted keys' part, the rows' output and the join of partials.
+//
+// A kernel's shape P: kUnit cached rows a unit, kRows query rows a block, kTaskCost a task's own cost in
+// units, kLeast units a block at least, kSlots of the ring.
+#pragma once
+#include <cuda.h>
+
+#include "tree.cuh"
+
+namespace fibattn {
+
+constexpr int kDtCons = 128;     // computing threads
+constexpr int kAccStride = 68;   // floats of a row of O in shared memory
+constexpr int kDtPart = kD + 2;  // floats of a partial's row: O, max, sum
+
+struct DenseTreeArgs {
+  TreeArgs a;
+  float* part;  // [blocks][2][ROWS][kDtPart]
+  unsigned long long wait_ns;
+  int blocks;   // blocks of the grid
+};
+
+// ------------------------------------------------------------------------------ schedule --
+// In shared memory: the cost before each sequence, and the sequences' rows and nodes.
+struct Schedule {
+  long long* start;  // [B + 1]
+  int* len;          // [B]
+  int* n;            // [B]; 0 where the sequence has nothing to do
+};
+
+__device__ __forceinline__ Schedule schedule_at(unsigned char* smem, int B) {
+  Schedule s;
+  s.start = reinterpret_cast<long long*>(smem);
+  s.len = reinterpret_cast<int*>(s.start + B + 1);
+  s.n = s.len + B;
+  return s;
+}
+inline size_t schedule_bytes(int B) { return (sizeof(long long) * (B + 1) + 2 * sizeof(int) * B + 127) / 128 * 128; }
+
+template <int UNIT>
+__device__ __forceinline__ int units_of(int len) {
+  return len <= UNIT ? 1 : (len + UNIT - 1) / UNIT;
+}
+
+// Every thread of the block; ends synchronised.
+template <typename P>
+__device__ __forceinline__ void build_schedule(const TreeArgs& a, const Schedule& s) {
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
+    int n, len;
+    if (!sequence_of(a, b, &n, &len)) {
+      atomicExch(a.status, kStatusDeviceAssert);
+      n = len = 0;
+    }
+    s.len[b] = len;
+    s.n[b] = n;
+    s.start[b + 1] = n == 0 ? 0 : static_cast<long long>(units_of<P::kUnit>(len) + P::kTaskCost) * a.H *
+                         ((a.G * n + P::kRows - 1) / P::kRows);
+  }
+  if (threadIdx.x == 0) s.start[0] = 0;
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + static_cast<int>(threadIdx.x);
+      long long x = b < a.B ? s.start[b + 1] : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (static_cast<int>(threadIdx.x) >= d) x += y;
+      }
+      if (b < a.B) s.start[b + 1] = base + x;
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+  }
+  __syncthreads();
+}
+
+// How many of the grid's blocks share the `cost`: fewer where a block would get less than `least` units.
+__device__ __forceinline__ int sharing_blocks(long long cost, int blocks, int least) {
+  const long long want = (cost + least - 1) / least;
+  return want < blocks ? static_cast<int>(want) : blocks;
+}
+// Block c's run begins at cut(c); block_at(x) is the block whose run holds place x.
+__device__ __forceinline__ long long cut(long long cost, int sharing, int c) { return cost * c / sharing; }
+__device__ __forceinline__ int block_at(long long cost, int sharing, long long x) {
+  return static_cast<int>(((x + 1) * sharing - 1) / cost);  // the largest c with cost * c < (x + 1) * sharing
+}
+
+// The task at place u of the cost, and the units of it that lie in [u, end).
+struct Task {
+  int b, h, rb;
+  int len, n;
+  int units;         // of the whole task
+  long long start;   // its place in the cost
+  int first, last;   // units [first, last); none where only a part of the task's own cost is in the run
+};
+template <typename P>
+__device__ __forceinline__ Task task_of(const TreeArgs& a, const Schedule& s, long long u, long long end) {
+  int lo = 0, hi = a.B;  // start[lo] <= u < start[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (s.start[mid] <= u)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  Task t;
+  t.b = lo;
+  t.len = s.len[lo];
+  t.n = s.n[lo];
+  t.units = units_of<P::kUnit>(t.len);
+  const int rbs = (a.G * t.n + P::kRows - 1) / P::kRows, each = t.units + P::kTaskCost;
+  const long long off = u - s.start[lo];
+  const int task = static_cast<int>(off / each);
+  t.start = s.start[lo] + static_cast<long long>(task) * each;
+  t.h = task / rbs;
+  t.rb = task - t.h * rbs;
+  const long long last = min(end - t.start, static_cast<long long>(each)) - P::kTaskCost;
+  t.first = max(0, static_cast<int>(u - t.start) - P::kTaskCost);
+  t.last = max(0, static_cast<int>(last));
+  return t;
+}
+
+// ------------------------------------------------------------------------------ small pieces --
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+// x0, x1 as bf16 pairs hi + lo
+__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  hi = pack_bf2_rn(x0, x1);
+  lo = pack_bf2_rn(x0 - bf_lo(hi), x1 - bf_hi(hi));
+}
+// What a partial of maximum m and sum l counts where the common maximum is `all`.  One without a finite
+// score counts nothing, unless a NaN is in it, which goes on.
+__device__ __forceinline__ float weight_of(float m, float l, float all) {
+  return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - all);
+}
+
+__device__ __forceinline__ void cons_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kDtCons) : "memory"); }
+
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];\n" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// The 16 dims D_t of a row (common.cuh) as they are stored.
+__device__ __forceinline__ void load_raw(const __nv_bfloat16* row, int t, uint4 (&x)[2]) {
+  x[0] = __ldg(reinterpret_cast<const uint4*>(row + 8 * t));
+  x[1] = __ldg(reinterpret_cast<const uint4*>(row + kFreq + 8 * t));
+}
+__device__ __forceinline__ void load_raw(const float* row, int t, uint4 (&x)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(row + (i >> 1) * kFreq + 8 * t) + (i & 1));
+}
+__device__ __forceinline__ void raw_to_float(const uint4 (&x)[2], float (&v)[16], const __nv_bfloat16*) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[8 * i + 2 * j] = bf_lo(w[j]);
+      v[8 * i + 2 * j + 1] = bf_hi(w[j]);
+    }
+  }
+}
+__device__ __forceinline__ void raw_to_float(const uint4 (&x)[4], float (&v)[16], const float*) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[4 * i] = __uint_as_float(x[i].x);
+    v[4 * i + 1] = __uint_as_float(x[i].y);
+    v[4 * i + 2] = __uint_as_float(x[i].z);
+    v[4 * i + 3] = __uint_as_float(x[i].w);
+  }
+}
+
+// ------------------------------------------------------------------------------ feeder --
+// The feeding warp: K and V rows of the units of [u0, u1) into the ring's slots, a page at a time.  A slot
+// is K, then V, kHalf bytes each; float32 rows lie as two halves of 32 dims, a quarter slot apart.
+template <typename DT, typename P>
+__device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sch, long long u0, long long u1, const CUtensorMap* map_k,
+                                     const CUtensorMap* map_v, unsigned char* ring, uint64_t* full_bar, uint64_t* empty_bar,
+                                     volatile int* s_err) {
+  constexpr int UNIT = P::kUnit, kSlots = P::kSlots, kHalf = UNIT * kD * static_cast<int>(sizeof(DT));
+  const TreeArgs& a = da.a;
+  const int lane = threadIdx.x & 31;
+  const int box = min(UNIT, 1 << a.page_shift);  // rows a copy
+  int count = 0, seq = -1, first = 0, page = 0;  // lane x holds the page of entry first + x
+  bool stop = false;
+  for (long long u = u0; u < u1 && !stop;) {
+    const Task k = task_of<P>(a, sch, u, u1);
+    for (int i = k.first; i < k.last; ++i, ++count) {
+      const int slot = count % kSlots;
+      const int rows = min(UNIT, k.len - i * UNIT), boxes = (rows + box - 1) / box;  // none of an empty cache
+      const int entry = (i * UNIT) >> a.page_shift;
+      if (boxes > 0 && (seq != k.b || entry < first || entry + boxes > first + 32)) {
+        seq = k.b;
+        first = entry;
+        page = entry + lane < a.max_pages ? __ldg(a.table + static_cast<size_t>(k.b) * a.max_pages + entry + lane) : 0;
+      }
+      int ok = 1;
+      if (lane == 0) ok = !*s_err && mbar_wait_backoff(&empty_bar[slot], ((count / kSlots) & 1) ^ 1, da.wait_ns);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) {
+        *s_err = 1;
+        stop = true;
+        break;
+      }
+      const uint32_t dst = smem_addr(ring + slot * 2 * kHalf);
+      if (lane == 0) mbar_arrive_tx(&full_bar[slot], boxes * box * 2 * kD * static_cast<int>(sizeof(DT)));
+      for (int x = 0; x < boxes; ++x) {
+        int id = __shfl_sync(0xffffffffu, page, entry + x - first);
+        if (lane == 0) {
+          if (id < 0 || id >= a.n_pages) {
+            atomicExch(a.status, kStatusDeviceAssert);
+            id = 0;
+          }
+          const int y = ((id * a.H + k.h) << a.page_shift) + ((i * UNIT) & ((1 << a.page_shift) - 1));
+          const uint32_t at = dst + x * box * 128;
+          tma_2d(at, map_k, 0, y, &full_bar[slot]);
+          tma_2d(at + kHalf, map_v, 0, y, &full_bar[slot]);
+          if constexpr (sizeof(DT) == 4) {
+            tma_2d(at + kHalf / 2, map_k, 32, y, &full_bar[slot]);
+            tma_2d(at + kHalf + kHalf / 2, map_v, 32, y, &full_bar[slot]);
+          }
+        }
+      }
+    }
+    u = k.start + k.units + P::kTaskCost;
+  }
+  // nothing may be in flight when the block ends
+  if (lane == 0) {
+    for (int c = count - kSlots < 0 ? 0 : count - kSlots; c < count; ++c)
+      mbar_wait(&full_bar[c % kSlots], (c / kSlots) & 1, da.wait_ns);
+    if (*s_err) atomicExch(a.status, kStatusTimeout);
+  }
+}
+
+// ------------------------------------------------------------------------------ a run's pieces --
+// Row r of a task (query head, node): its row of q and o, and the node.
+__device__ __forceinline__ size_t row_of(const TreeArgs& a, const Task& k, int r, int* s) {
+  const int head = r / k.n;
+  *s = r - head * k.n;
+  return (static_cast<size_t>(k.b) * a.Hq + k.h * a.G + head) * a.T + *s;
+}
+// Position of a node; one that N does not hold is reported and clamped, so that the tables are read in bounds.
+__device__ __forceinline__ int position_of(const TreeArgs& a, const Task& k, int depth, bool* ok) {
+  if (k.len + depth < a.N) return k.len + depth;
+  *ok = false;
+  return a.N - 1;
+}
+
+// The task's drafted keys, rotated, into `draft` [n][64]; by the 128 computing threads.
+template <typename DT>
+__device__ __forceinline__ void rotate_drafts(const TreeArgs& a, const Task& k, const WarpTree& tree, float* draft, bool* ok) {
+  const int tid = threadIdx.x, t = tid & 3;
+  const size_t fresh = (static_cast<size_t>(k.b) * a.H + k.h) * a.T * kD;
+  const DT* kn = static_cast<const DT*>(a.kn) + fresh;
+  const DT* vn = static_cast<const DT*>(a.vn) + fresh;
+  for (int x = 0; x < (k.n + kDtCons / 4 - 1) / (kDtCons / 4); ++x) {
+    const int s = x * (kDtCons / 4) + (tid >> 2);
+    const int depth = pick32(tree.depth, s & 63);
+    if (s < k.n) {
+      float y[16];
+      float2 e[8];
+      load_part(kn + static_cast<size_t>(s) * kD, t, y);
+      // the values too, into L1: the rows' loops would wait for each in turn
+      const char* vr = reinterpret_cast<const char*>(vn + static_cast<size_t>(s) * kD) + t * (kD * sizeof(DT) / 4);
+      asm volatile("{ .reg .b32 x; ld.global.nc.b32 x, [%0]; }\n" ::"l"(vr));
+      rope_row(a.rope_lo, a.rope_hi, position_of(a, k, depth, ok), t, e);
+      rotate_part(y, e, false);
+      store_part(draft + s * kD, t, y);
+    }
+  }
+}
+
+// The part of the drafted keys in each row: O (not divided) into acc, maximum and sum into mx and sm.  A quad a
+// row, over the row's ancestors alone.
+template <typename DT>
+__device__ __forceinline__ void attend_drafts(const TreeArgs& a, const Task& k, const WarpTree& tree, const float* draft, int r0, int rows,
+                                              float* acc, float* mx, float* sm, bool* ok) {
+  const int tid = threadIdx.x, t = tid & 3;
+  const DT* vn = static_cast<const DT*>(a.vn) + (static_cast<size_t>(k.b) * a.H + k.h) * a.T * kD;
+  for (int x = 0; x < (rows + kDtCons / 4 - 1) / (kDtCons / 4); ++x) {
+    const int r = x * (kDtCons / 4) + (tid >> 2);
+    const bool in = r < rows;
+    int s = 0;
+    const size_t row = in ? row_of(a, k, r0 + r, &s) : 0;
+    const int depth = pick32(tree.depth, s);
+    uint64_t set = pick64(tree.above, s);
+    if (!in) set = 0;
+    float y[16], o[16], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) y[w] = o[w] = 0.f;
+    if (in) {
+      float2 e[8];
+      load_part(static_cast<const DT*>(a.q) + row * kD, t, y);
+      rope_row(a.rope_lo, a.rope_hi, position_of(a, k, depth, ok), t, e);
+      rotate_part(y, e, false);
+#pragma unroll
+      for (int w = 0; w < 16; ++w) y[w] *= kLog2e / 8.0f;
+    }
+    // the values of the next ancestor are on their way while one is added
+    uint4 next[sizeof(DT)];
+    int key = set != 0 ? __ffsll(static_cast<long long>(set)) - 1 : 0;
+    if (set != 0) load_raw(vn + static_cast<size_t>(key) * kD, t, next);
+    while (__any_sync(0xffffffffu, set != 0)) {
+      const bool on = set != 0;
+      float sc = 0.f, v[16];
+      raw_to_float(next, v, vn);
+      if (on) {
+        float kx[16];
+        const float4* kr = reinterpret_cast<const float4*>(draft + key * kD);
+        *reinterpret_cast<float4*>(kx) = kr[2 * t];
+        *reinterpret_cast<float4*>(kx + 4) = kr[2 * t + 1];
+        *reinterpret_cast<float4*>(kx + 8) = kr[8 + 2 * t];
+        *reinterpret_cast<float4*>(kx + 12) = kr[8 + 2 * t + 1];
+#pragma unroll
+        for (int w = 0; w < 16; ++w) sc = fmaf(y[w], kx[w], sc);
+      }
+      set &= set - 1;
+      if (set != 0) {
+        key = __ffsll(static_cast<long long>(set)) - 1;
+        load_raw(vn + static_cast<size_t>(key) * kD, t, next);
+      }
+      sc = quad_sum(sc);
+      if (on && sc != -INFINITY) {  // weight 0 (a NaN goes on)
+        const float mn = fmaxf(m, sc);
+        const float corr = ex2(m - mn), p = ex2(sc - mn);
+        l = l * corr + p;
+#pragma unroll
+        for (int w = 0; w < 16; ++w) o[w] = fmaf(p, v[w], o[w] * corr);
+        m = mn;
+      }
+    }
+    if (in) {
+      store_part(acc + r * kAccStride, t, o);
+      if (t == 0) {
+        mx[r] = m;
+        sm[r] = l;
+      }
+    }
+  }
+}
+
+// The rows of a piece, O in acc for the common maximum of `parts` (maximum, sum) pairs a row: divided, to o
+// and lse, where the piece is a whole task; as a partial else.
+template <typename DT, int ROWS>
+__device__ __forceinline__ void write_rows(const DenseTreeArgs& da, const Task& k, bool whole, int slot, int r0, int rows,
+                                           const float* acc, const float* mx, const float* sm, int parts) {
+  const TreeArgs& a = da.a;
+  float* part = da.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * ROWS * kDtPart;
+  for (int i = threadIdx.x; i < rows * 16; i += kDtCons) {  // 16 threads a row
+    const int r = i >> 4, d = (i & 15) * 4;
+    float mr = -INFINITY, sum = 0.f;
+    for (int x = 0; x < parts; ++x) mr = fmaxf(mr, mx[x * ROWS + r]);
+    for (int x = 0; x < parts; ++x) sum += sm[x * ROWS + r] * weight_of(mx[x * ROWS + r], sm[x * ROWS + r], mr);
+    const float4 x = *reinterpret_cast<const float4*>(acc + r * kAccStride + d);
+    if (whole) {
+      int s;
+      const size_t row = row_of(a, k, r0 + r, &s);
+      const float inv = 1.f / sum;
+      if constexpr (sizeof(DT) == 4) {
+        *reinterpret_cast<float4*>(static_cast<float*>(a.o) + row * kD + d) = make_float4(x.x * inv, x.y * inv, x.z * inv, x.w * inv);
+      } else {
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * kD + d) =
+            make_uint2(pack_bf2(x.x * inv, x.y * inv), pack_bf2(x.z * inv, x.w * inv));
+      }
+      if (d == 0 && a.lse != nullptr) a.lse[row] = (mr + log2f(sum)) * kLn2;
+    } else {
+      *reinterpret_cast<float2*>(part + r * kDtPart + d) = make_float2(x.x, x.y);
+      *reinterpret_cast<float2*>(part + r * kDtPart + d + 2) = make_float2(x.z, x.w);
+      if (d == 0) *reinterpret_cast<float2*>(part + r * kDtPart + kD) = make_float2(mr, sum);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------------ join --
+// Adds the partials of the tasks whose units more than one block holds.  Block (c, y) serves 8 rows of the task
+// whose first cut is the one in front of block c.  A row has two teams of 16 threads, which take every
+// second partial; the weights come first, so that the loads of O do not wait for one another.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 8;
+
+template <typename DT, typename P>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DenseTreeArgs da) {
+  constexpr int ROWS = P::kRows;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ float4 s_o[kJoinRows][16];
+  const TreeArgs& a = da.a;
+  const Schedule sch = schedule_at(smem, a.B);
+  build_schedule<P>(a, sch);
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  const long long cost = sch.start[a.B];
+  const int sharing = sharing_blocks(cost, da.blocks, P::kLeast);
+  const int c = blockIdx.x;
+  if (c == 0 || c >= sharing) return;
+  const long long u = cut(cost, sharing, c);
+  const Task k = task_of<P>(a, sch, u, cost);
+  // the cut lies behind the task's first unit, and is the first that does
+  const long long t0 = k.start + P::kTaskCost, t1 = t0 + k.units;
+  if (u <= t0 || cut(cost, sharing, c - 1) > t0) return;
+  const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);
+  const int team = threadIdx.x >> 4, d = (threadIdx.x & 15) * 4, share = team & 1, at = team >> 1;
+  const int r = kJoinRows * blockIdx.y + at;
+  if (kJoinRows * static_cast<int>(blockIdx.y) >= rows) return;
+  const int parts = block_at(cost, sharing, t1 - 1) - (c - 1) + 1;  // blocks that hold some of it
+  // partial i lies in block c - 1 + i: in its first place, or its second where the block began before the task
+  const int first_slot = k.start >= cut(cost, sharing, c - 1) ? 1 : 0;
+  auto partial = [&](int i) {
+    const int slot = i == 0 ? first_slot : 0;
+    return da.part + ((static_cast<size_t>(c - 1 + i) * 2 + slot) * ROWS + r) * kDtPart;
+  };
+  float all = -INFINITY, sum = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (r < rows) {
+    for (int i = threadIdx.x & 15; i < parts; i += 16) all = fmaxf(all, partial(i)[kD]);
+  }
+#pragma unroll
+  for (int x = 1; x < 16; x <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, x));
+  if (r < rows) {
+    for (int i = threadIdx.x & 15; i < parts; i += 16) {
+      const float2 ml = *reinterpret_cast<const float2*>(partial(i) + kD);
+      sum += ml.y * weight_of(ml.x, ml.y, all);
+    }
+  }
+#pragma unroll
+  for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+  if (r < rows) {
+#pragma unroll 4
+    for (int i = share; i < parts; i += 2) {
+      const float* p = partial(i);
+      const float2 x = *reinterpret_cast<const float2*>(p + d), y = *reinterpret_cast<const float2*>(p + d + 2);
+      const float2 ml = *reinterpret_cast<const float2*>(p + kD);
+      const float f = weight_of(ml.x, ml.y, all);
+      o.x += x.x * f;
+      o.y += x.y * f;
+      o.z += y.x * f;
+      o.w += y.y * f;
+    }
+  }
+  if (share) s_o[at][d / 4] = o;
+  __syncthreads();
+  if (share || r >= rows) return;
+  const float4 x = s_o[at][d / 4];
+  const float inv = 1.f / sum;
+  o = make_float4((o.x + x.x) * inv, (o.y + x.y) * inv, (o.z + x.z) * inv, (o.w + x.w) * inv);
+  const int head = (r0 + r) / k.n, s = (r0 + r) - head * k.n;
+  const size_t row = (static_cast<size_t>(k.b) * a.Hq + k.h * a.G + head) * a.T + s;
+  if constexpr (sizeof(DT) == 4)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + row * kD + d) = o;
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * kD + d) =
+        make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
+  if (d == 0 && a.lse != nullptr) a.lse[row] = (all + log2f(sum)) * kLn2;
+}
+
+template <typename DT, typename P>
+cudaError_t launch_join(const DenseTreeArgs& da, cudaStream_t stream) {
+  const TreeArgs& a = da.a;
+  cudaLaunchConfig_t cfg = {};
+  const int most = a.G * a.T < P::kRows ? a.G * a.T : P::kRows;
+  cfg.gridDim = dim3(static_cast<unsigned>(da.blocks), (most + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.dynamicSmemBytes = schedule_bytes(a.B);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<DT, P>, da);
+}
+
+// ------------------------------------------------------------------------------ copies --
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// A layer's pool as a matrix of rows of 64 values; a copy takes `box` rows of 128 bytes.
+inline cudaError_t map_of(CUtensorMap* m, const void* pool, long long rows, int es, int box) {
+  static const EncodeTiled encode = [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) != cudaSuccess ||
+        found != cudaDriverEntryPointSuccess)
+      fn = nullptr;
+    return reinterpret_cast<EncodeTiled>(fn);
+  }();
+  if (encode == nullptr) return cudaErrorNotSupported;
+  const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * es};
+  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box)};
+  const cuuint32_t steps[2] = {1, 1};
+  const CUresult r = encode(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+                            const_cast<void*>(pool), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Both pools' maps for units of `unit` rows.
+inline cudaError_t maps_of(const TreeArgs& a, int es, int unit, CUtensorMap* mk, CUtensorMap* mv) {
+  const int box = (1 << a.page_shift) < unit ? 1 << a.page_shift : unit;
+  const long long rows = (static_cast<long long>(a.n_pages) * a.H) << a.page_shift;
+  const cudaError_t e = map_of(mk, a.kc, rows, es, box);
+  return e == cudaSuccess ? map_of(mv, a.vc, rows, es, box) : e;
+}
+
+
+// tree_dense_tc.cu: bf16, more than 8 query rows a key head
+size_t dense_tree_tc_bytes(int rows);
+cudaError_t launch_dense_tree_tc(const DenseTreeArgs& da, cudaStream_t stream);
+
+}  // namespace fibattn

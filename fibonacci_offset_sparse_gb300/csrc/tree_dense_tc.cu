@@ -1,0 +1,505 @@
+// Dense decode of a tree of drafted tokens, bf16 with more than 8 query rows a key head (sm_103a): the
+// work, its cut and its join as in tree_dense.cu, the products on the 5th-generation tensor cores.
+//
+// What bounds it: the read of the cache, as there.  With mma.sync the products alone took as long as the
+// read from some 24 query rows on; here a unit of 128 keys costs its SM about 500 tensor cycles for any
+// number of rows up to 64, a third of the time its 32 KB take from HBM.
+//
+// Per unit of 128 cached rows, with the keys as the 128 rows of the accumulator:
+//   S^T [128 keys x ROWS] = K Q'^T    K from the ring as TMA left it (K-major, 128-byte swizzle), the rotated
+//                                     query split in two bf16 (hi + lo, 16 bits), both added up
+//   P = 2^(S - m)                     a thread a key: its row of S^T from tensor memory to registers, its
+//                                     weights, again hi + lo, to shared memory (16 bytes for 8 query rows)
+//   O^T [64 dims x ROWS] += V^T P^T   V from the ring (its transpose by the descriptor), P as written; O stays
+//                                     in tensor memory over the whole run
+// The maximum m of a row is common to a unit's keys and moves only when a score passes it by more than
+// 8 (weights <= 256 until then): one vote of the four warps a unit; the exact maximum, and O rescaled, are the exception's work.
+//
+// Block: 4 warps of softmax (warp w reads lanes 32w .. of tensor memory), the feeder, and a warp whose one
+// thread issues the products as their operands arrive: S of the next unit runs while a unit's weights are formed.
+#include "tree_dense.cuh"
+
+namespace fibattn {
+
+namespace {
+
+constexpr int kTcThreads = kDtCons + 64;
+constexpr float kNoKey = -1e30f;  // reference of a row that has met no finite score
+
+template <int ROWS>
+struct TcShape {
+  static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 3, kLeast = 1;
+  static constexpr int kSlotBytes = 2 * kUnit * kD * 2, kHalf = kSlotBytes / 2;
+  // two blocks an SM where their rings of two slots and the rest fit twice
+  static constexpr int kResident = ROWS <= 32 ? 2 : 1;
+  static constexpr int kSlots = ROWS <= 32 ? 2 : 4;
+  static constexpr int kColumns = ROWS == 16 ? 64 : ROWS == 32 ? 128 : 256;  // of tensor memory: S twice, O
+  // byte offsets in dynamic shared memory (its base is 1024-byte aligned)
+  static constexpr int kQuery = kSlots * kSlotBytes;    // hi [ROWS][64], lo: K-major, 128-byte swizzle
+  static constexpr int kWeights = kQuery + ROWS * 256;  // hi [ROWS/8][16][8 keys][8 rows], lo; see below for its other uses
+  static constexpr int kAcc = kWeights + ROWS * 512;
+  static constexpr int kRef = kAcc + ROWS * kAccStride * 4;  // [ROWS] the rows' reference
+  static constexpr int kMax = kRef + ROWS * 4;               // [2][ROWS]: of the cached keys, of the drafted ones
+  static constexpr int kSum = kMax + 2 * ROWS * 4;
+  static constexpr int kWarpMax = kSum + 2 * ROWS * 4;       // [4][ROWS]
+  static constexpr int kSchedule = kWarpMax + 4 * ROWS * 4;
+  static size_t bytes(int B) { return kSchedule + schedule_bytes(B); }
+};
+
+// ------------------------------------------------------------------- tensor memory and products --
+__device__ __forceinline__ void tmem_alloc(uint32_t* out, int columns) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_addr(out)), "r"(columns) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+}
+__device__ __forceinline__ void tmem_free(uint32_t at, int columns) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(at), "r"(columns));
+}
+// Shared-memory matrix descriptor: start, leading and stride byte offsets; swizzle 2 = 128 bytes, 0 = none.
+__device__ __forceinline__ uint64_t matrix_at(uint32_t start, uint32_t lead, uint32_t stride, uint32_t swizzle) {
+  return static_cast<uint64_t>((start & 0x3ffffu) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
+         static_cast<uint64_t>(stride >> 4) << 32 | 1ull << 46 | static_cast<uint64_t>(swizzle) << 61;
+}
+// bf16 x bf16 -> float32, M x N; a_mn, b_mn: the operand's rows lie along memory (not its k index).
+constexpr uint32_t product_of(int M, int N, bool a_mn, bool b_mn) {
+  return 1u << 4 | 1u << 7 | 1u << 10 | (a_mn ? 1u << 15 : 0u) | (b_mn ? 1u << 16 : 0u) | static_cast<uint32_t>(N >> 3) << 17 |
+         static_cast<uint32_t>(M >> 4) << 24;
+}
+__device__ __forceinline__ void mma_tc(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b),
+      "r"(desc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// Arrives at the barrier when every product issued so far is done.
+__device__ __forceinline__ void commit_tc(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
+__device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
+
+// 16 columns of a warp's 32 lanes.
+__device__ __forceinline__ void tmem_load16(uint32_t at, float* x) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(at)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_store16(uint32_t at, const float* x) {
+  uint32_t r[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};\n" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
+      "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
+__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
+
+// Whether any of the 128 softmax threads says so; they are synchronised by it.
+__device__ __forceinline__ bool any_of_cons(bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      : "=r"(r)
+      : "r"(static_cast<uint32_t>(x)), "n"(kDtCons)
+      : "memory");
+  return r != 0;
+}
+
+struct TcBars {
+  uint64_t full[4], empty[4];  // slots of the ring
+  uint64_t scores[2];          // S of a unit is in its buffer (units alternate)
+  uint64_t weights;            // P of a unit is in shared memory
+  uint64_t added;              // ... and in O
+  uint64_t query;              // Q' of a piece is in shared memory
+  uint64_t drained;
+};
+
+template <int ROWS>
+__global__ void __launch_bounds__(kTcThreads, TcShape<ROWS>::kResident)
+    dense_tree_tc_kernel(const __grid_constant__ DenseTreeArgs da, const __grid_constant__ CUtensorMap map_k,
+                         const __grid_constant__ CUtensorMap map_v) {
+  using P = TcShape<ROWS>;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ __align__(8) TcBars bars;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_err;
+  const TreeArgs& a = da.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+  if (tid == 0) {
+    s_err = 0;
+    for (int s = 0; s < P::kSlots; ++s) {
+      mbar_init(&bars.full[s], 1);
+      mbar_init(&bars.empty[s], 1);
+    }
+    mbar_init(&bars.scores[0], 1);
+    mbar_init(&bars.scores[1], 1);
+    mbar_init(&bars.weights, 4);
+    mbar_init(&bars.added, 1);
+    mbar_init(&bars.query, 4);
+    mbar_init(&bars.drained, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  const Schedule sch = schedule_at(smem + P::kSchedule, a.B);
+  build_schedule<P>(a, sch);
+  const long long cost = sch.start[a.B];
+  const int sharing = sharing_blocks(cost, da.blocks, P::kLeast);
+  if (static_cast<int>(blockIdx.x) >= sharing) return;
+  const long long u0 = cut(cost, sharing, blockIdx.x), u1 = cut(cost, sharing, blockIdx.x + 1);
+  if (warp == 5) tmem_alloc(&s_tmem, P::kColumns);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * ROWS;
+  const uint32_t base = smem_addr(smem);
+
+  if (warp == 4) {
+    // =================================================================== feeder
+    feed<__nv_bfloat16, P>(da, sch, u0, u1, &map_k, &map_v, smem, bars.full, bars.empty, &s_err);
+  } else if (warp == 5) {
+    // =================================================================== products
+    if (lane == 0) {
+      constexpr uint32_t kScores = product_of(128, ROWS, false, false), kValues = product_of(64, ROWS, true, true);
+      // two cursors over the units of the run: the next S, the next O += V P
+      struct Cursor {
+        long long u;
+        int i, last, count;
+        bool first;  // of its piece
+      } s{u0, 0, 0, 0, false}, o{u0, 0, 0, 0, false};
+      auto next = [&](Cursor& c) {  // moves to a unit; false at the run's end
+        while (c.i == c.last) {
+          if (c.u >= u1) return false;
+          const Task k = task_of<P>(a, sch, c.u, u1);
+          c.u = k.start + k.units + P::kTaskCost;
+          c.i = k.first;
+          c.last = k.last;
+          c.first = true;
+        }
+        return true;
+      };
+      int pieces = 0;
+      bool more_s = next(s), more_o = next(o);
+      unsigned long long since = global_ns();
+      while (more_o && !s_err) {
+        bool did = false;
+        // S of a unit: its keys and its piece's query are there, and its buffer's last user is past it
+        if (more_s && s.count - o.count < 2 && mbar_try(&bars.full[s.count % P::kSlots], (s.count / P::kSlots) & 1) &&
+            (!s.first || mbar_try(&bars.query, pieces & 1))) {
+          if (s.first) ++pieces;
+          fence_after();
+          const uint32_t kt = base + (s.count % P::kSlots) * P::kSlotBytes, d = tmem + (s.count & 1) * ROWS;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              mma_tc(d, matrix_at(kt + 32 * x, 16, 1024, 2), matrix_at(base + P::kQuery + part * ROWS * 128 + 32 * x, 16, 1024, 2), kScores,
+                     part + x > 0);
+          commit_tc(&bars.scores[s.count & 1]);
+          ++s.count;
+          ++s.i;
+          s.first = false;
+          more_s = next(s);
+          did = true;
+        }
+        if (o.count < s.count && mbar_try(&bars.weights, o.count & 1)) {
+          fence_after();
+          const uint32_t vt = base + (o.count % P::kSlots) * P::kSlotBytes + P::kHalf;
+#pragma unroll
+          for (int part = 0; part < 2; ++part)
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              mma_tc(tmem_o, matrix_at(vt + 2048 * x, 16, 1024, 2), matrix_at(base + P::kWeights + part * ROWS * 256 + 256 * x, 128, 2048, 0),
+                     kValues, !o.first || part + x > 0);
+          commit_tc(&bars.empty[o.count % P::kSlots]);
+          commit_tc(&bars.added);
+          ++o.count;
+          ++o.i;
+          o.first = false;
+          more_o = next(o);
+          did = true;
+        }
+        if (did) {
+          since = global_ns();
+        } else if (global_ns() - since > da.wait_ns) {
+          s_err = 1;
+          atomicExch(a.status, kStatusTimeout);
+        }
+      }
+      commit_tc(&bars.drained);  // nothing may be in flight when the block ends
+      mbar_wait(&bars.drained, 0, da.wait_ns);
+    }
+    __syncwarp();
+  } else {
+    // =================================================================== softmax
+    float* s_acc = reinterpret_cast<float*>(smem + P::kAcc);
+    float* s_ref = reinterpret_cast<float*>(smem + P::kRef);
+    float* s_max = reinterpret_cast<float*>(smem + P::kMax);
+    float* s_sum = reinterpret_cast<float*>(smem + P::kSum);
+    float* s_warp = reinterpret_cast<float*>(smem + P::kWarpMax);
+    float* s_draft = reinterpret_cast<float*>(smem + P::kWeights);  // before a piece's weights
+    float* s_part = reinterpret_cast<float*>(smem + P::kWeights);   // after them: [ROWS][128] sums
+    const int t = lane & 3;
+    const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // this warp's lanes of tensor memory
+    int count = 0;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (s_err || mbar_wait(bar, parity, da.wait_ns)) return;
+      s_err = 1;
+      atomicExch(a.status, kStatusTimeout);
+    };
+    for (long long u = u0; u < u1;) {
+      const Task k = task_of<P>(a, sch, u, u1);
+      u = k.start + k.units + P::kTaskCost;
+      if (k.first == k.last) continue;
+      const bool tail = k.last == k.units, whole = tail && k.first == 0;
+      const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);
+      bool ok = true;
+      const WarpTree tree = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(k.b) * a.T, k.n, &ok);
+      // the rotated query: a quad a row, 16 bytes of hi and of lo for 8 dims
+      for (int r = tid >> 2; r < ROWS; r += kDtCons / 4) {
+        int s = 0;
+        const size_t row = r < rows ? row_of(a, k, r0 + r, &s) : 0;
+        const int depth = pick32(tree.depth, s);
+        uint32_t hi[8], lo[8];
+        if (r < rows) {
+          float x[16];
+          float2 e[8];
+          load_part(static_cast<const __nv_bfloat16*>(a.q) + row * kD, t, x);
+          rope_row(a.rope_lo, a.rope_hi, position_of(a, k, depth, &ok), t, e);
+          rotate_part(x, e, false);
+#pragma unroll
+          for (int w = 0; w < 8; ++w) split_bf16(x[2 * w] * (kLog2e / 8.0f), x[2 * w + 1] * (kLog2e / 8.0f), hi[w], lo[w]);
+        } else {
+#pragma unroll
+          for (int w = 0; w < 8; ++w) hi[w] = lo[w] = 0;
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          unsigned char* at = smem + P::kQuery + r * 128 + (((t + 4 * h) ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
+          *reinterpret_cast<uint4*>(at + ROWS * 128) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+        }
+      }
+      if (tid < ROWS) s_ref[tid] = kNoKey;
+      fence_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.query);
+      if (tail) {
+        rotate_drafts<__nv_bfloat16>(a, k, tree, s_draft, &ok);
+        cons_sync();
+        attend_drafts<__nv_bfloat16>(a, k, tree, s_draft, r0, rows, s_acc, s_max + ROWS, s_sum + ROWS, &ok);
+      }
+      cons_sync();
+
+      const int groups = (rows + 7) >> 3;  // of 8 rows: what lies behind them is not formed
+      float l[ROWS];
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r) l[r] = 0.f;
+      for (int i = k.first; i < k.last; ++i, ++count) {
+        const int valid = k.len - i * P::kUnit;  // keys of the unit
+        const bool in = tid < valid;
+        unsigned char* slot = smem + (count % P::kSlots) * P::kSlotBytes;
+        wait(&bars.scores[count & 1], (count >> 1) & 1);
+        fence_after();
+        float s[ROWS];
+#pragma unroll
+        for (int c = 0; c < ROWS / 16; ++c) tmem_load16(tmem + (count & 1) * ROWS + 16 * c + lanes, s + 16 * c);
+        tmem_loaded();
+        bool past = false;
+#pragma unroll
+        for (int c = 0; c < ROWS / 4; ++c) {
+          const float4 ref = *reinterpret_cast<const float4*>(s_ref + 4 * c);
+          const float m[4] = {ref.x, ref.y, ref.z, ref.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if (!in) s[4 * c + e] = -INFINITY;
+            past |= 4 * c + e < rows && !(s[4 * c + e] - m[e] <= 8.f);  // (a NaN too)
+          }
+        }
+        if (any_of_cons(past)) {
+          // A NaN may come of an infinite key, where hi + lo add infinities of opposite signs: the upper
+          // parts' product alone keeps the sign.
+          bool bad = false;
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) bad |= r < rows && isnan(s[r]);
+          if (bad) {
+            wait(&bars.full[count % P::kSlots], (count / P::kSlots) & 1);  // (long over; it orders the copies before these reads)
+            for (int r = 0; r < rows; ++r) {
+              float x = 0.f;
+              for (int d = 0; d < kD; ++d) {
+                const int c = d >> 3;
+                const __nv_bfloat16 kx = *reinterpret_cast<const __nv_bfloat16*>(slot + tid * 128 + ((c ^ (tid & 7)) << 4) + (d & 7) * 2);
+                const __nv_bfloat16 qx =
+                    *reinterpret_cast<const __nv_bfloat16*>(smem + P::kQuery + r * 128 + ((c ^ (r & 7)) << 4) + (d & 7) * 2);
+                x = fmaf(__bfloat162float(kx), __bfloat162float(qx), x);
+              }
+#pragma unroll
+              for (int j = 0; j < ROWS; ++j)
+                if (j == r && isnan(s[j])) s[j] = x;
+            }
+          }
+          __syncwarp();
+#pragma unroll
+          for (int r = 0; r < ROWS; ++r) {
+            float x = s[r];
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+            if (lane == 0) s_warp[warp * ROWS + r] = x;
+          }
+          if (count > 0) wait(&bars.added, (count - 1) & 1);  // O is at rest
+          fence_after();
+          cons_sync();
+          const bool has_o = i > k.first;
+#pragma unroll
+          for (int c = 0; c < ROWS / 16; ++c) {
+            float x[16];
+            if (has_o) {
+              tmem_load16(tmem_o + 16 * c + lanes, x);
+              tmem_loaded();
+            }
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const int r = 16 * c + j;
+              const float m = s_ref[r];
+              const float mn = fmaxf(fmaxf(m, fmaxf(s_warp[r], s_warp[ROWS + r])), fmaxf(s_warp[2 * ROWS + r], s_warp[3 * ROWS + r]));
+              const float corr = ex2(m - mn);
+              l[r] *= corr;
+              if (has_o) x[j] *= corr;
+            }
+            if (has_o) {
+              tmem_store16(tmem_o + 16 * c + lanes, x);
+              tmem_stored();
+            }
+          }
+          cons_sync();
+          if (tid < ROWS)
+            s_ref[tid] = fmaxf(fmaxf(s_ref[tid], fmaxf(s_warp[tid], s_warp[ROWS + tid])), fmaxf(s_warp[2 * ROWS + tid], s_warp[3 * ROWS + tid]));
+          cons_sync();
+        }
+        // weights: of key `tid` for 8 rows each; P of the unit before has to be in O by now
+        if (count > 0) wait(&bars.added, (count - 1) & 1);
+        unsigned char* at = smem + P::kWeights + (tid >> 3) * 128 + (tid & 7) * 16;
+#pragma unroll
+        for (int c = 0; c < ROWS / 8; ++c) {
+          if (c < groups) {
+            const float4 ra = *reinterpret_cast<const float4*>(s_ref + 8 * c), rb = *reinterpret_cast<const float4*>(s_ref + 8 * c + 4);
+            const float m[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int e = 0; e < 8; e += 2) {
+              const float p0 = ex2(s[8 * c + e] - m[e]), p1 = ex2(s[8 * c + e + 1] - m[e + 1]);
+              l[8 * c + e] += p0;
+              l[8 * c + e + 1] += p1;
+              split_bf16(p0, p1, hi[e / 2], lo[e / 2]);
+            }
+            *reinterpret_cast<uint4*>(at + c * 2048) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            *reinterpret_cast<uint4*>(at + ROWS * 256 + c * 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          }
+        }
+        if (!in) {  // a row that was not filled for this sequence: its weight is 0, whatever it holds must be too
+          uint4* v = reinterpret_cast<uint4*>(slot + P::kHalf + tid * 128);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) v[x] = make_uint4(0, 0, 0, 0);
+        }
+        fence_smem();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.weights);
+      }
+      // ---- the run's O, sums and references; with the drafted keys' part, in a fixed order
+      wait(&bars.added, (count - 1) & 1);
+      fence_after();
+      cons_sync();
+#pragma unroll
+      for (int r = 0; r < ROWS; ++r)
+        if (r < rows) s_part[r * kDtCons + tid] = l[r];
+      cons_sync();
+      for (int r = warp; r < rows; r += 4) {
+        const float4 x = *reinterpret_cast<const float4*>(s_part + r * kDtCons + 4 * lane);
+        float sum = (x.x + x.y) + (x.z + x.w);
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) {
+          s_sum[r] = sum;
+          s_max[r] = s_ref[r] == kNoKey ? -INFINITY : s_ref[r];
+        }
+      }
+      cons_sync();
+      const int dim = 16 * warp + lane;  // 16 rows of O^T lie in a warp's first 16 lanes
+#pragma unroll
+      for (int c = 0; c < ROWS / 16; ++c) {
+        if (16 * c >= rows) break;
+        float x[16];
+        tmem_load16(tmem_o + 16 * c + lanes, x);
+        tmem_loaded();
+        if (lane < 16) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int r = 16 * c + j;
+            if (r < rows) {
+              const float all = tail ? fmaxf(s_max[r], s_max[ROWS + r]) : s_max[r];
+              float y = x[j] * weight_of(s_max[r], s_sum[r], all);
+              if (tail) y = fmaf(s_acc[r * kAccStride + dim], weight_of(s_max[ROWS + r], s_sum[ROWS + r], all), y);
+              s_acc[r * kAccStride + dim] = y;
+            }
+          }
+        }
+      }
+      fence_before();
+      cons_sync();
+      if (!ok) atomicExch(a.status, kStatusDeviceAssert);
+      if (!s_err) write_rows<__nv_bfloat16, ROWS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, tail ? 2 : 1);
+      cons_sync();  // everything of the piece is free again
+    }
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 5) tmem_free(tmem, P::kColumns);
+}
+
+template <int ROWS>
+cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
+  using P = TcShape<ROWS>;
+  DenseTreeArgs da = args;
+  da.blocks = 152 * P::kResident;  // 152 SMs
+  CUtensorMap mk, mv;
+  cudaError_t e = maps_of(da.a, 2, P::kUnit, &mk, &mv);
+  if (e != cudaSuccess) return e;
+  const size_t smem = P::bytes(da.a.B);
+  e = cudaFuncSetAttribute(dense_tree_tc_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  dense_tree_tc_kernel<ROWS><<<da.blocks, kTcThreads, smem, stream>>>(da, mk, mv);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  return launch_join<__nv_bfloat16, P>(da, stream);
+}
+
+template <int ROWS>
+size_t part_bytes() {
+  return static_cast<size_t>(152) * TcShape<ROWS>::kResident * 2 * ROWS * kDtPart * sizeof(float);
+}
+
+}  // namespace
+
+size_t dense_tree_tc_bytes(int rows) {
+  return rows <= 16 ? part_bytes<16>() : rows <= 32 ? part_bytes<32>() : rows <= 48 ? part_bytes<48>() : part_bytes<64>();
+}
+
+cudaError_t launch_dense_tree_tc(const DenseTreeArgs& da, cudaStream_t stream) {
+  const int rows = da.a.G * da.a.T;
+  if (rows <= 16) return launch<16>(da, stream);
+  if (rows <= 32) return launch<32>(da, stream);
+  if (rows <= 48) return launch<48>(da, stream);
+  return launch<64>(da, stream);
+}
+
+}  // namespace fibattn
