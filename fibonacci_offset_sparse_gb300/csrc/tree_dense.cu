@@ -33,7 +33,8 @@ namespace fibattn {
 
 namespace {
 
-constexpr int kDtWarps = kDtCons / 32;
+constexpr int kDtWarps = 4;
+constexpr int kDtCons = 32 * kDtWarps;  // computing threads
 constexpr int kDtThreads = kDtCons + 32;
 constexpr int kMmaRows = 8;       // bf16: up to so many query rows here, more in tree_dense_tc.cu
 constexpr int kSlotBytes = 8192;  // K and V of a unit
@@ -533,11 +534,12 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
   using S = DtSmem<DT, NR, TILES>;
   using C = Core<DT, NR>;
   constexpr int UNIT = S::kUnit, ROWS = S::kRows, GROUPS = S::kGroups;
-  constexpr int kSlots = S::kSlots, kRaw = sizeof(DT);  // (16 values of a quad's lane in 16-byte words)
+  constexpr int kSlots = S::kSlots;
   static_assert(kSlots % GROUPS == 0, "a slot belongs to one group");
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) uint64_t full_bar[kSlots], empty_bar[kSlots];
   __shared__ volatile int s_err;
+  __shared__ int s_pos[ROWS];  // positions of a piece's rows
   const TreeArgs& a = da.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -563,7 +565,7 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
   }
 
   // ===================================================================== computing warps
-  const int t = lane & 3, tile = warp % TILES, grp = warp / TILES;
+  const int tile = warp % TILES, grp = warp / TILES;
   float* s_acc = reinterpret_cast<float*>(smem + S::kAcc);
   float* s_max = reinterpret_cast<float*>(smem + S::kMax);
   float* s_sum = reinterpret_cast<float*>(smem + S::kSum);
@@ -584,11 +586,24 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
       int s = 0;
       const size_t row = r < rows ? row_of(a, k, r0 + r, &s) : 0;
       const int depth = pick32(tree.depth, s);
-      C::load_query(a, qs, i, r < rows, row, r < rows ? position_of(a, k, depth, &ok) : 0);
+      const int pos = r < rows ? position_of(a, k, depth, &ok) : 0;
+      s_pos[r] = pos;
+      C::load_query(a, qs, i, r < rows, row, pos);
     }
-    if (tail) rotate_drafts<DT>(a, k, tree, s_draft, &ok);
-    cons_sync();
-    if (tail) attend_drafts<DT>(a, k, tree, s_draft, r0, rows, s_acc, s_max + GROUPS * ROWS, s_sum + GROUPS * ROWS, &ok);
+    if (tail) rotate_drafts<DT, kDtCons>(a, k, tree, s_draft, &ok);
+    cons_sync<kDtCons>();
+    if (tail)
+      attend_drafts<DT, kDtCons>(a, k, tree, s_draft, r0, rows, s_acc, s_max + GROUPS * ROWS, s_sum + GROUPS * ROWS,
+                                 [&](int r, int lane4, float(&y)[16]) {
+                                   int s;
+                                   const size_t row = row_of(a, k, r0 + r, &s);
+                                   float2 e[8];
+                                   load_part(static_cast<const DT*>(a.q) + row * kD, lane4, y);
+                                   rope_row(a.rope_lo, a.rope_hi, s_pos[r], lane4, e);
+                                   rotate_part(y, e, false);
+#pragma unroll
+                                   for (int w = 0; w < 16; ++w) y[w] *= kLog2e / 8.0f;
+                                 });
     // ---- the cached rows: a unit in turn for each group
     C core;
     core.clear();
@@ -612,7 +627,7 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
         s_sum[grp * ROWS + C::kRows * tile + C::own_row(i)] = core.own_sum(i);
       }
     }
-    cons_sync();
+    cons_sync<kDtCons>();
     const int parts = GROUPS + (tail ? 1 : 0);
     float f[C::kOwn], old[C::kOwn];
 #pragma unroll
@@ -635,11 +650,11 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
           if (r < rows) core.add_to(i, s_acc + r * kAccStride, old[i], turn > 0 || tail, f[i]);
         }
       }
-      cons_sync();
+      cons_sync<kDtCons>();
     }
     if (!ok) atomicExch(a.status, kStatusDeviceAssert);
-    if (!s_err) write_rows<DT, ROWS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, parts);
-    cons_sync();  // s_acc, s_max and s_sum are free again
+    if (!s_err) write_rows<DT, ROWS, kDtCons>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, parts);
+    cons_sync<kDtCons>();  // s_acc, s_max and s_sum are free again
   }
 }
 

@@ -10,7 +10,6 @@
 
 namespace fibattn {
 
-constexpr int kDtCons = 128;     // computing threads
 constexpr int kAccStride = 68;   // floats of a row of O in shared memory
 constexpr int kDtPart = kD + 2;  // floats of a partial's row: O, max, sum
 
@@ -139,7 +138,11 @@ __device__ __forceinline__ float weight_of(float m, float l, float all) {
   return m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : ex2(m - all);
 }
 
-__device__ __forceinline__ void cons_sync() { asm volatile("bar.sync 1, %0;\n" ::"n"(kDtCons) : "memory"); }
+// The CONS computing threads of the block.
+template <int CONS>
+__device__ __forceinline__ void cons_sync() {
+  asm volatile("bar.sync 1, %0;\n" ::"n"(CONS) : "memory");
+}
 
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int x, int y, uint64_t* bar) {
   asm volatile(
@@ -254,15 +257,15 @@ __device__ __forceinline__ int position_of(const TreeArgs& a, const Task& k, int
   return a.N - 1;
 }
 
-// The task's drafted keys, rotated, into `draft` [n][64]; by the 128 computing threads.
-template <typename DT>
+// The task's drafted keys, rotated, into `draft` [n][64]; by the CONS computing threads.
+template <typename DT, int CONS>
 __device__ __forceinline__ void rotate_drafts(const TreeArgs& a, const Task& k, const WarpTree& tree, float* draft, bool* ok) {
   const int tid = threadIdx.x, t = tid & 3;
   const size_t fresh = (static_cast<size_t>(k.b) * a.H + k.h) * a.T * kD;
   const DT* kn = static_cast<const DT*>(a.kn) + fresh;
   const DT* vn = static_cast<const DT*>(a.vn) + fresh;
-  for (int x = 0; x < (k.n + kDtCons / 4 - 1) / (kDtCons / 4); ++x) {
-    const int s = x * (kDtCons / 4) + (tid >> 2);
+  for (int x = 0; x < (k.n + CONS / 4 - 1) / (CONS / 4); ++x) {
+    const int s = x * (CONS / 4) + (tid >> 2);
     const int depth = pick32(tree.depth, s & 63);
     if (s < k.n) {
       float y[16];
@@ -279,31 +282,22 @@ __device__ __forceinline__ void rotate_drafts(const TreeArgs& a, const Task& k, 
 }
 
 // The part of the drafted keys in each row: O (not divided) into acc, maximum and sum into mx and sm.  A quad a
-// row, over the row's ancestors alone.
-template <typename DT>
+// row, over the row's ancestors alone.  query(r, t, y): the rotated query of row r times log2(e)/8, dims D_t.
+template <typename DT, int CONS, typename Q>
 __device__ __forceinline__ void attend_drafts(const TreeArgs& a, const Task& k, const WarpTree& tree, const float* draft, int r0, int rows,
-                                              float* acc, float* mx, float* sm, bool* ok) {
+                                              float* acc, float* mx, float* sm, Q&& query) {
   const int tid = threadIdx.x, t = tid & 3;
   const DT* vn = static_cast<const DT*>(a.vn) + (static_cast<size_t>(k.b) * a.H + k.h) * a.T * kD;
-  for (int x = 0; x < (rows + kDtCons / 4 - 1) / (kDtCons / 4); ++x) {
-    const int r = x * (kDtCons / 4) + (tid >> 2);
+  for (int x = 0; x < (rows + CONS / 4 - 1) / (CONS / 4); ++x) {
+    const int r = x * (CONS / 4) + (tid >> 2);
     const bool in = r < rows;
-    int s = 0;
-    const size_t row = in ? row_of(a, k, r0 + r, &s) : 0;
-    const int depth = pick32(tree.depth, s);
+    const int s = in ? (r0 + r) % k.n : 0;
     uint64_t set = pick64(tree.above, s);
     if (!in) set = 0;
     float y[16], o[16], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int w = 0; w < 16; ++w) y[w] = o[w] = 0.f;
-    if (in) {
-      float2 e[8];
-      load_part(static_cast<const DT*>(a.q) + row * kD, t, y);
-      rope_row(a.rope_lo, a.rope_hi, position_of(a, k, depth, ok), t, e);
-      rotate_part(y, e, false);
-#pragma unroll
-      for (int w = 0; w < 16; ++w) y[w] *= kLog2e / 8.0f;
-    }
+    if (in) query(r, t, y);
     // the values of the next ancestor are on their way while one is added
     uint4 next[sizeof(DT)];
     int key = set != 0 ? __ffsll(static_cast<long long>(set)) - 1 : 0;
@@ -349,12 +343,12 @@ __device__ __forceinline__ void attend_drafts(const TreeArgs& a, const Task& k, 
 
 // The rows of a piece, O in acc for the common maximum of `parts` (maximum, sum) pairs a row: divided, to o
 // and lse, where the piece is a whole task; as a partial else.
-template <typename DT, int ROWS>
+template <typename DT, int ROWS, int CONS>
 __device__ __forceinline__ void write_rows(const DenseTreeArgs& da, const Task& k, bool whole, int slot, int r0, int rows,
                                            const float* acc, const float* mx, const float* sm, int parts) {
   const TreeArgs& a = da.a;
   float* part = da.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * ROWS * kDtPart;
-  for (int i = threadIdx.x; i < rows * 16; i += kDtCons) {  // 16 threads a row
+  for (int i = threadIdx.x; i < rows * 16; i += CONS) {  // 16 threads a row
     const int r = i >> 4, d = (i & 15) * 4;
     float mr = -INFINITY, sum = 0.f;
     for (int x = 0; x < parts; ++x) mr = fmaxf(mr, mx[x * ROWS + r]);

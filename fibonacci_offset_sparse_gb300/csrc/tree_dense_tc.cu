@@ -13,23 +13,26 @@
 //   O^T [64 dims x ROWS] += V^T P^T   V from the ring (its transpose by the descriptor), P as written; O stays
 //                                     in tensor memory over the whole run
 // The maximum m of a row is common to a unit's keys and moves only when a score passes it by more than
-// 8 (weights <= 256 until then): one vote of the four warps a unit; the exact maximum, and O rescaled, are the exception's work.
+// 8 (weights <= 256 until then): one vote of four warps a unit; the exact maximum, and O rescaled, are the
+// exception's work.
 //
-// Block: 4 warps of softmax (warp w reads lanes 32w .. of tensor memory), the feeder, and a warp whose one
-// thread issues the products as their operands arrive: S of the next unit runs while a unit's weights are formed.
+// Block: softmax warps (warp w reads lanes 32 (w % 4) .. of tensor memory; four warps share 8 or 16 query
+// rows), the feeder, and a warp whose one thread issues the products as their operands arrive: S of the next
+// unit runs while a unit's weights are formed.
 #include "tree_dense.cuh"
 
 namespace fibattn {
 
 namespace {
 
-constexpr int kTcThreads = kDtCons + 64;
 constexpr float kNoKey = -1e30f;  // reference of a row that has met no finite score
 
 template <int ROWS>
 struct TcShape {
   static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 3, kLeast = 1;
   static constexpr int kSlotBytes = 2 * kUnit * kD * 2, kHalf = kSlotBytes / 2;
+  static constexpr int kGroupRows = ROWS == 16 ? 8 : 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
+  static constexpr int kCons = 128 * kGroups, kThreads = kCons + 64;
   // two blocks an SM where their rings of two slots and the rest fit twice
   static constexpr int kResident = ROWS <= 32 ? 2 : 1;
   static constexpr int kSlots = ROWS <= 32 ? 2 : 4;
@@ -41,7 +44,7 @@ struct TcShape {
   static constexpr int kRef = kAcc + ROWS * kAccStride * 4;  // [ROWS] the rows' reference
   static constexpr int kMax = kRef + ROWS * 4;               // [2][ROWS]: of the cached keys, of the drafted ones
   static constexpr int kSum = kMax + 2 * ROWS * 4;
-  static constexpr int kWarpMax = kSum + 2 * ROWS * 4;       // [4][ROWS]
+  static constexpr int kWarpMax = kSum + 2 * ROWS * 4;       // [4][ROWS]; at the end the two parts' weights [2][ROWS]
   static constexpr int kSchedule = kWarpMax + 4 * ROWS * 4;
   static size_t bytes(int B) { return kSchedule + schedule_bytes(B); }
 };
@@ -78,40 +81,59 @@ __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::be
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
 
-// 16 columns of a warp's 32 lanes.
-__device__ __forceinline__ void tmem_load16(uint32_t at, float* x) {
-  uint32_t r[16];
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
-        "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(at)
-      : "memory");
+// N columns (8 or 16) of a warp's 32 lanes.
+template <int N>
+__device__ __forceinline__ void tmem_load(uint32_t at, float (&x)[N]) {
+  static_assert(N == 8 || N == 16, "shapes used here");
+  uint32_t r[N];
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+  else
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at)
+                 : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = __uint_as_float(r[i]);
+  for (int i = 0; i < N; ++i) x[i] = __uint_as_float(r[i]);
 }
-__device__ __forceinline__ void tmem_store16(uint32_t at, const float* x) {
-  uint32_t r[16];
+template <int N>
+__device__ __forceinline__ void tmem_store(uint32_t at, const float (&x)[N]) {
+  uint32_t r[N];
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(x[i]);
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};\n" ::"r"(r[0]),
-      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]),
-      "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
-      : "memory");
+  for (int i = 0; i < N; ++i) r[i] = __float_as_uint(x[i]);
+  if constexpr (N == 16)
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};\n" ::"r"(r[0]),
+        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]),
+        "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(at)
+        : "memory");
+  else
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};\n" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
+                 "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(at)
+                 : "memory");
+  asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
-__device__ __forceinline__ void tmem_loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory"); }
-__device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory"); }
-
-// Whether any of the 128 softmax threads says so; they are synchronised by it.
-__device__ __forceinline__ bool any_of_cons(bool x) {
+// Whether any of a group's 128 softmax threads says so; they are synchronised by it.
+__device__ __forceinline__ bool any_of_group(int group, bool x) {
   uint32_t r;
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, 2, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+      "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}\n"
       : "=r"(r)
-      : "r"(static_cast<uint32_t>(x)), "n"(kDtCons)
+      : "r"(static_cast<uint32_t>(x)), "r"(2 + group)
       : "memory");
   return r != 0;
+}
+__device__ __forceinline__ void group_sync(int group) { asm volatile("barrier.cta.sync %0, 128;\n" ::"r"(2 + group) : "memory"); }
+__device__ __forceinline__ float warp_max(float x) {
+  float y;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;\n" : "=f"(y) : "f"(x));
+  return y;
 }
 
 struct TcBars {
@@ -124,10 +146,11 @@ struct TcBars {
 };
 
 template <int ROWS>
-__global__ void __launch_bounds__(kTcThreads, TcShape<ROWS>::kResident)
+__global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResident)
     dense_tree_tc_kernel(const __grid_constant__ DenseTreeArgs da, const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v) {
   using P = TcShape<ROWS>;
+  constexpr int CONS = P::kCons, GR = P::kGroupRows, kFeeder = CONS / 32, kIssuer = kFeeder + 1;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(8) TcBars bars;
   __shared__ uint32_t s_tmem;
@@ -143,9 +166,9 @@ __global__ void __launch_bounds__(kTcThreads, TcShape<ROWS>::kResident)
     }
     mbar_init(&bars.scores[0], 1);
     mbar_init(&bars.scores[1], 1);
-    mbar_init(&bars.weights, 4);
+    mbar_init(&bars.weights, 4 * P::kGroups);
     mbar_init(&bars.added, 1);
-    mbar_init(&bars.query, 4);
+    mbar_init(&bars.query, 4 * P::kGroups);
     mbar_init(&bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -155,17 +178,17 @@ __global__ void __launch_bounds__(kTcThreads, TcShape<ROWS>::kResident)
   const int sharing = sharing_blocks(cost, da.blocks, P::kLeast);
   if (static_cast<int>(blockIdx.x) >= sharing) return;
   const long long u0 = cut(cost, sharing, blockIdx.x), u1 = cut(cost, sharing, blockIdx.x + 1);
-  if (warp == 5) tmem_alloc(&s_tmem, P::kColumns);
+  if (warp == kIssuer) tmem_alloc(&s_tmem, P::kColumns);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * ROWS;
   const uint32_t base = smem_addr(smem);
 
-  if (warp == 4) {
+  if (warp == kFeeder) {
     // =================================================================== feeder
     feed<__nv_bfloat16, P>(da, sch, u0, u1, &map_k, &map_v, smem, bars.full, bars.empty, &s_err);
-  } else if (warp == 5) {
+  } else if (warp == kIssuer) {
     // =================================================================== products
     if (lane == 0) {
       constexpr uint32_t kScores = product_of(128, ROWS, false, false), kValues = product_of(64, ROWS, true, true);
@@ -247,8 +270,8 @@ __global__ void __launch_bounds__(kTcThreads, TcShape<ROWS>::kResident)
     float* s_warp = reinterpret_cast<float*>(smem + P::kWarpMax);
     float* s_draft = reinterpret_cast<float*>(smem + P::kWeights);  // before a piece's weights
     float* s_part = reinterpret_cast<float*>(smem + P::kWeights);   // after them: [ROWS][128] sums
-    const int t = lane & 3;
-    const uint32_t lanes = static_cast<uint32_t>(warp) << 21;  // this warp's lanes of tensor memory
+    const int group = warp >> 2, g0 = group * GR, key = tid & 127, wq = warp & 3;  // the thread's query rows and key
+    const uint32_t lanes = static_cast<uint32_t>(wq) << 21;                        // its warp's lanes of tensor memory
     int count = 0;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (s_err || mbar_wait(bar, parity, da.wait_ns)) return;
@@ -261,10 +284,12 @@ __global__ void __launch_bounds__(kTcThreads, TcShape<ROWS>::kResident)
       if (k.first == k.last) continue;
       const bool tail = k.last == k.units, whole = tail && k.first == 0;
       const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);
+      const int mine = min(GR, max(0, rows - g0));  // rows of this group
       bool ok = true;
       const WarpTree tree = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(k.b) * a.T, k.n, &ok);
       // the rotated query: a quad a row, 16 bytes of hi and of lo for 8 dims
-      for (int r = tid >> 2; r < ROWS; r += kDtCons / 4) {
+      for (int r = tid >> 2; r < ROWS; r += CONS / 4) {
+        const int t = lane & 3;
         int s = 0;
         const size_t row = r < rows ? row_of(a, k, r0 + r, &s) : 0;
         const int depth = pick32(tree.depth, s);
@@ -292,120 +317,125 @@ __global__ void __launch_bounds__(kTcThreads, TcShape<ROWS>::kResident)
       fence_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.query);
+      if (tail) rotate_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, &ok);
+      cons_sync<CONS>();
       if (tail) {
-        rotate_drafts<__nv_bfloat16>(a, k, tree, s_draft, &ok);
-        cons_sync();
-        attend_drafts<__nv_bfloat16>(a, k, tree, s_draft, r0, rows, s_acc, s_max + ROWS, s_sum + ROWS, &ok);
-      }
-      cons_sync();
-
-      const int groups = (rows + 7) >> 3;  // of 8 rows: what lies behind them is not formed
-      float l[ROWS];
+        attend_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, r0, rows, s_acc, s_max + ROWS, s_sum + ROWS, [&](int r, int t, float(&y)[16]) {
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r) l[r] = 0.f;
+          for (int h = 0; h < 2; ++h) {
+            const unsigned char* at = smem + P::kQuery + r * 128 + (((t + 4 * h) ^ (r & 7)) << 4);
+            const uint4 hi = *reinterpret_cast<const uint4*>(at), lo = *reinterpret_cast<const uint4*>(at + ROWS * 128);
+            const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, z[4] = {lo.x, lo.y, lo.z, lo.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              y[8 * h + 2 * w] = bf_lo(x[w]) + bf_lo(z[w]);
+              y[8 * h + 2 * w + 1] = bf_hi(x[w]) + bf_hi(z[w]);
+            }
+          }
+        });
+        cons_sync<CONS>();  // the drafted keys' room is the weights' room
+      }
+
+      float l[GR];
+#pragma unroll
+      for (int r = 0; r < GR; ++r) l[r] = 0.f;
       for (int i = k.first; i < k.last; ++i, ++count) {
-        const int valid = k.len - i * P::kUnit;  // keys of the unit
-        const bool in = tid < valid;
+        const bool in = key < k.len - i * P::kUnit;
         unsigned char* slot = smem + (count % P::kSlots) * P::kSlotBytes;
         wait(&bars.scores[count & 1], (count >> 1) & 1);
         fence_after();
-        float s[ROWS];
-#pragma unroll
-        for (int c = 0; c < ROWS / 16; ++c) tmem_load16(tmem + (count & 1) * ROWS + 16 * c + lanes, s + 16 * c);
-        tmem_loaded();
+        float s[GR];
+        tmem_load(tmem + (count & 1) * ROWS + g0 + lanes, s);
         bool past = false;
 #pragma unroll
-        for (int c = 0; c < ROWS / 4; ++c) {
-          const float4 ref = *reinterpret_cast<const float4*>(s_ref + 4 * c);
+        for (int c = 0; c < GR / 4; ++c) {
+          const float4 ref = *reinterpret_cast<const float4*>(s_ref + g0 + 4 * c);
           const float m[4] = {ref.x, ref.y, ref.z, ref.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             if (!in) s[4 * c + e] = -INFINITY;
-            past |= 4 * c + e < rows && !(s[4 * c + e] - m[e] <= 8.f);  // (a NaN too)
+            past |= 4 * c + e < mine && !(s[4 * c + e] - m[e] <= 8.f);  // (a NaN too)
           }
         }
-        if (any_of_cons(past)) {
+        if (any_of_group(group, past)) {
           // A NaN may come of an infinite key, where hi + lo add infinities of opposite signs: the upper
           // parts' product alone keeps the sign.
           bool bad = false;
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) bad |= r < rows && isnan(s[r]);
+          for (int r = 0; r < GR; ++r) bad |= r < mine && isnan(s[r]);
           if (bad) {
             wait(&bars.full[count % P::kSlots], (count / P::kSlots) & 1);  // (long over; it orders the copies before these reads)
-            for (int r = 0; r < rows; ++r) {
+#pragma unroll 1
+            for (int r = 0; r < mine; ++r) {
               float x = 0.f;
+#pragma unroll 1
               for (int d = 0; d < kD; ++d) {
                 const int c = d >> 3;
-                const __nv_bfloat16 kx = *reinterpret_cast<const __nv_bfloat16*>(slot + tid * 128 + ((c ^ (tid & 7)) << 4) + (d & 7) * 2);
+                const __nv_bfloat16 kx = *reinterpret_cast<const __nv_bfloat16*>(slot + key * 128 + ((c ^ (key & 7)) << 4) + (d & 7) * 2);
                 const __nv_bfloat16 qx =
-                    *reinterpret_cast<const __nv_bfloat16*>(smem + P::kQuery + r * 128 + ((c ^ (r & 7)) << 4) + (d & 7) * 2);
+                    *reinterpret_cast<const __nv_bfloat16*>(smem + P::kQuery + (g0 + r) * 128 + ((c ^ (r & 7)) << 4) + (d & 7) * 2);
                 x = fmaf(__bfloat162float(kx), __bfloat162float(qx), x);
               }
 #pragma unroll
-              for (int j = 0; j < ROWS; ++j)
+              for (int j = 0; j < GR; ++j)
                 if (j == r && isnan(s[j])) s[j] = x;
             }
           }
           __syncwarp();
 #pragma unroll
-          for (int r = 0; r < ROWS; ++r) {
-            float x = s[r];
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
-            if (lane == 0) s_warp[warp * ROWS + r] = x;
+          for (int r = 0; r < GR; ++r) {
+            const float x = warp_max(s[r]);
+            if (lane == 0) s_warp[wq * ROWS + g0 + r] = x;
           }
           if (count > 0) wait(&bars.added, (count - 1) & 1);  // O is at rest
           fence_after();
-          cons_sync();
-          const bool has_o = i > k.first;
+          group_sync(group);
+          float corr[GR];
 #pragma unroll
-          for (int c = 0; c < ROWS / 16; ++c) {
-            float x[16];
-            if (has_o) {
-              tmem_load16(tmem_o + 16 * c + lanes, x);
-              tmem_loaded();
-            }
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const int r = 16 * c + j;
-              const float m = s_ref[r];
-              const float mn = fmaxf(fmaxf(m, fmaxf(s_warp[r], s_warp[ROWS + r])), fmaxf(s_warp[2 * ROWS + r], s_warp[3 * ROWS + r]));
-              const float corr = ex2(m - mn);
-              l[r] *= corr;
-              if (has_o) x[j] *= corr;
-            }
-            if (has_o) {
-              tmem_store16(tmem_o + 16 * c + lanes, x);
-              tmem_stored();
-            }
+          for (int r = 0; r < GR; ++r) {
+            const float* w = s_warp + g0 + r;
+            const float m = s_ref[g0 + r];
+            const float mn = fmaxf(m, fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS])));
+            corr[r] = ex2(m - mn);
+            l[r] *= corr[r];
           }
-          cons_sync();
-          if (tid < ROWS)
-            s_ref[tid] = fmaxf(fmaxf(s_ref[tid], fmaxf(s_warp[tid], s_warp[ROWS + tid])), fmaxf(s_warp[2 * ROWS + tid], s_warp[3 * ROWS + tid]));
-          cons_sync();
+          if (i > k.first) {
+            float x[GR];
+            tmem_load(tmem_o + g0 + lanes, x);
+#pragma unroll
+            for (int r = 0; r < GR; ++r) x[r] *= corr[r];
+            tmem_store(tmem_o + g0 + lanes, x);
+          }
+          group_sync(group);
+          if (key < GR) {
+            const float* w = s_warp + g0 + key;
+            s_ref[g0 + key] = fmaxf(s_ref[g0 + key], fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS])));
+          }
+          group_sync(group);
         }
-        // weights: of key `tid` for 8 rows each; P of the unit before has to be in O by now
-        if (count > 0) wait(&bars.added, (count - 1) & 1);
-        unsigned char* at = smem + P::kWeights + (tid >> 3) * 128 + (tid & 7) * 16;
+        // the weights of the thread's key, 8 rows to 16 bytes
+        uint32_t hi[GR / 2], lo[GR / 2];
 #pragma unroll
-        for (int c = 0; c < ROWS / 8; ++c) {
-          if (c < groups) {
-            const float4 ra = *reinterpret_cast<const float4*>(s_ref + 8 * c), rb = *reinterpret_cast<const float4*>(s_ref + 8 * c + 4);
-            const float m[8] = {ra.x, ra.y, ra.z, ra.w, rb.x, rb.y, rb.z, rb.w};
-            uint32_t hi[4], lo[4];
+        for (int c = 0; c < GR / 4; ++c) {
+          const float4 ref = *reinterpret_cast<const float4*>(s_ref + g0 + 4 * c);
+          const float m[4] = {ref.x, ref.y, ref.z, ref.w};
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float p0 = ex2(s[8 * c + e] - m[e]), p1 = ex2(s[8 * c + e + 1] - m[e + 1]);
-              l[8 * c + e] += p0;
-              l[8 * c + e + 1] += p1;
-              split_bf16(p0, p1, hi[e / 2], lo[e / 2]);
-            }
-            *reinterpret_cast<uint4*>(at + c * 2048) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-            *reinterpret_cast<uint4*>(at + ROWS * 256 + c * 2048) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+          for (int e = 0; e < 4; e += 2) {
+            const float p0 = ex2(s[4 * c + e] - m[e]), p1 = ex2(s[4 * c + e + 1] - m[e + 1]);
+            l[4 * c + e] += p0;
+            l[4 * c + e + 1] += p1;
+            split_bf16(p0, p1, hi[2 * c + e / 2], lo[2 * c + e / 2]);
           }
         }
-        if (!in) {  // a row that was not filled for this sequence: its weight is 0, whatever it holds must be too
-          uint4* v = reinterpret_cast<uint4*>(slot + P::kHalf + tid * 128);
+        if (count > 0) wait(&bars.added, (count - 1) & 1);  // P of the unit before is in O
+        unsigned char* at = smem + P::kWeights + (g0 >> 3) * 2048 + (key >> 3) * 128 + (key & 7) * 16;
+#pragma unroll
+        for (int c = 0; c < GR / 8; ++c) {
+          *reinterpret_cast<uint4*>(at + c * 2048) = make_uint4(hi[4 * c], hi[4 * c + 1], hi[4 * c + 2], hi[4 * c + 3]);
+          *reinterpret_cast<uint4*>(at + ROWS * 256 + c * 2048) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
+        }
+        if (group == 0 && !in) {  // a row that was not filled for this sequence: its weight is 0, and so must be what it holds
+          uint4* v = reinterpret_cast<uint4*>(slot + P::kHalf + key * 128);
 #pragma unroll
           for (int x = 0; x < 8; ++x) v[x] = make_uint4(0, 0, 0, 0);
         }
@@ -417,53 +447,47 @@ __global__ void __launch_bounds__(kTcThreads, TcShape<ROWS>::kResident)
       // ---- the run's O, sums and references; with the drafted keys' part, in a fixed order
       wait(&bars.added, (count - 1) & 1);
       fence_after();
-      cons_sync();
+      float o[GR];
+      tmem_load(tmem_o + g0 + lanes, o);
+      cons_sync<CONS>();
 #pragma unroll
-      for (int r = 0; r < ROWS; ++r)
-        if (r < rows) s_part[r * kDtCons + tid] = l[r];
-      cons_sync();
-      for (int r = warp; r < rows; r += 4) {
-        const float4 x = *reinterpret_cast<const float4*>(s_part + r * kDtCons + 4 * lane);
+      for (int r = 0; r < GR; ++r) s_part[(g0 + r) * 128 + key] = l[r];
+      cons_sync<CONS>();
+      for (int r = warp; r < rows; r += CONS / 32) {
+        const float4 x = *reinterpret_cast<const float4*>(s_part + r * 128 + 4 * lane);
         float sum = (x.x + x.y) + (x.z + x.w);
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         if (lane == 0) {
+          const float m = s_ref[r] == kNoKey ? -INFINITY : s_ref[r], all = tail ? fmaxf(m, s_max[ROWS + r]) : m;
           s_sum[r] = sum;
-          s_max[r] = s_ref[r] == kNoKey ? -INFINITY : s_ref[r];
+          s_max[r] = m;
+          s_warp[r] = weight_of(m, sum, all);
+          s_warp[ROWS + r] = tail ? weight_of(s_max[ROWS + r], s_sum[ROWS + r], all) : 0.f;
         }
       }
-      cons_sync();
-      const int dim = 16 * warp + lane;  // 16 rows of O^T lie in a warp's first 16 lanes
+      cons_sync<CONS>();
+      if (lane < 16) {  // 16 rows of O^T lie in a warp's first 16 lanes
+        float* acc = s_acc + g0 * kAccStride + 16 * wq + lane;
 #pragma unroll
-      for (int c = 0; c < ROWS / 16; ++c) {
-        if (16 * c >= rows) break;
-        float x[16];
-        tmem_load16(tmem_o + 16 * c + lanes, x);
-        tmem_loaded();
-        if (lane < 16) {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int r = 16 * c + j;
-            if (r < rows) {
-              const float all = tail ? fmaxf(s_max[r], s_max[ROWS + r]) : s_max[r];
-              float y = x[j] * weight_of(s_max[r], s_sum[r], all);
-              if (tail) y = fmaf(s_acc[r * kAccStride + dim], weight_of(s_max[ROWS + r], s_sum[ROWS + r], all), y);
-              s_acc[r * kAccStride + dim] = y;
-            }
+        for (int r = 0; r < GR; ++r)
+          if (r < mine) {
+            float y = o[r] * s_warp[g0 + r];
+            if (tail) y = fmaf(acc[r * kAccStride], s_warp[ROWS + g0 + r], y);
+            acc[r * kAccStride] = y;
           }
-        }
       }
       fence_before();
-      cons_sync();
+      cons_sync<CONS>();
       if (!ok) atomicExch(a.status, kStatusDeviceAssert);
-      if (!s_err) write_rows<__nv_bfloat16, ROWS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, tail ? 2 : 1);
-      cons_sync();  // everything of the piece is free again
+      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, tail ? 2 : 1);
+      cons_sync<CONS>();  // everything of the piece is free again
     }
   }
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 5) tmem_free(tmem, P::kColumns);
+  if (warp == kIssuer) tmem_free(tmem, P::kColumns);
 }
 
 template <int ROWS>
@@ -477,7 +501,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
   const size_t smem = P::bytes(da.a.B);
   e = cudaFuncSetAttribute(dense_tree_tc_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  dense_tree_tc_kernel<ROWS><<<da.blocks, kTcThreads, smem, stream>>>(da, mk, mv);
+  dense_tree_tc_kernel<ROWS><<<da.blocks, P::kThreads, smem, stream>>>(da, mk, mv);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_join<__nv_bfloat16, P>(da, stream);
