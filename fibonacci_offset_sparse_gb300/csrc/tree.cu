@@ -49,14 +49,6 @@ __device__ __forceinline__ bool load_tree(const TreeArgs& a, int b, TreeSmem* ts
   return !bad;
 }
 
-// Offset (in elements) of cache row x of sequence b, key head h, in the layer's pools; -1 where the
-// page id lies outside the pool.
-__device__ __forceinline__ long long cache_row(const TreeArgs& a, int b, int h, int x) {
-  const int page = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (x >> a.page_shift));
-  if (page < 0 || page >= a.n_pages) return -1;
-  return (((static_cast<long long>(page) * a.H + h) << a.page_shift) + (x & ((1 << a.page_shift) - 1))) * kD;
-}
-
 constexpr int kTreeThreads = 128;
 constexpr int kTreeWarps = kTreeThreads / 32;
 

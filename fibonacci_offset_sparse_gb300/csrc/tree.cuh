@@ -76,4 +76,12 @@ __device__ __forceinline__ bool sequence_of(const TreeArgs& a, int b, int* n, in
          static_cast<long long>(*len) + (*n > 0) <= a.N;
 }
 
+// Offset (in elements) of cache row x of sequence b, key head h, in the layer's pools; -1 where the
+// page id lies outside the pool.
+__device__ __forceinline__ long long cache_row(const TreeArgs& a, int b, int h, int x) {
+  const int page = __ldg(a.table + static_cast<size_t>(b) * a.max_pages + (x >> a.page_shift));
+  if (page < 0 || page >= a.n_pages) return -1;
+  return (((static_cast<long long>(page) * a.H + h) << a.page_shift) + (x & ((1 << a.page_shift) - 1))) * kD;
+}
+
 }  // namespace fibattn

@@ -30,21 +30,21 @@ constexpr float kNoKey = -1e30f;  // reference of a row that has met no finite s
 template <int ROWS>
 struct TcShape {
   static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 3, kLeast = 1;
-  static constexpr int kSlotBytes = 2 * kUnit * kD * 2, kHalf = kSlotBytes / 2;
+  static constexpr int kSlotBytes = kUnit * kD * 2;  // K or V of a unit
   static constexpr int kGroupRows = ROWS == 16 ? 8 : 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
   static constexpr int kCons = 128 * kGroups, kThreads = kCons + 64;
-  // two blocks an SM where their rings of two slots and the rest fit twice
+  // Two blocks an SM where the rest beside their rings is small.  What is on its way from memory is what the
+  // ring holds, so it takes what shared memory is left: K's slot is free once the scores are formed.
   static constexpr int kResident = ROWS <= 32 ? 2 : 1;
-  static constexpr int kSlots = ROWS <= 32 ? 2 : 4;
+  static constexpr int kSlots = ROWS <= 32 ? 5 : 9;
   static constexpr int kColumns = ROWS == 16 ? 64 : ROWS == 32 ? 128 : 256;  // of tensor memory: S twice, O
   // byte offsets in dynamic shared memory (its base is 1024-byte aligned)
   static constexpr int kQuery = kSlots * kSlotBytes;    // hi [ROWS][64], lo: K-major, 128-byte swizzle
   static constexpr int kWeights = kQuery + ROWS * 256;  // hi [ROWS/8][16][8 keys][8 rows], lo; see below for its other uses
-  static constexpr int kAcc = kWeights + ROWS * 512;
-  static constexpr int kRef = kAcc + ROWS * kAccStride * 4;  // [ROWS] the rows' reference
-  static constexpr int kMax = kRef + ROWS * 4;               // [2][ROWS]: of the cached keys, of the drafted ones
+  static constexpr int kRef = kWeights + ROWS * 512;    // [ROWS] the rows' reference
+  static constexpr int kMax = kRef + ROWS * 4;          // [2][ROWS]: of the cached keys, of the drafted ones
   static constexpr int kSum = kMax + 2 * ROWS * 4;
-  static constexpr int kWarpMax = kSum + 2 * ROWS * 4;       // [4][ROWS]; at the end the two parts' weights [2][ROWS]
+  static constexpr int kWarpMax = kSum + 2 * ROWS * 4;  // [4][ROWS]; at the end the two parts' weights [2][ROWS]
   static constexpr int kSchedule = kWarpMax + 4 * ROWS * 4;
   static size_t bytes(int B) { return kSchedule + schedule_bytes(B); }
 };
@@ -136,12 +136,73 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// The units' K and V tiles in turn: the tile 2 count (K) or 2 count + 1 (V), its slot and its round's parity.
+template <int SLOTS>
+struct Tile {
+  int slot;
+  uint32_t parity;
+  __device__ __forceinline__ explicit Tile(int n) : slot(n % SLOTS), parity((n / SLOTS) & 1) {}
+};
+
+// Their feeder: K, then V of each unit of [u0, u1), a page at a time.
+template <typename P>
+__device__ __forceinline__ void feed_tiles(const DenseTreeArgs& da, const Schedule& sch, long long u0, long long u1, const CUtensorMap* map_k,
+                                           const CUtensorMap* map_v, unsigned char* ring, uint64_t* full_bar, uint64_t* empty_bar,
+                                           volatile int* s_err) {
+  const TreeArgs& a = da.a;
+  const int lane = threadIdx.x & 31;
+  const int box = min(P::kUnit, 1 << a.page_shift);  // rows a copy
+  int n = 0, seq = -1, first = 0, page = 0;          // lane x holds the page of entry first + x
+  bool stop = false;
+  for (long long u = u0; u < u1 && !stop;) {
+    const Task k = task_of<P>(a, sch, u, u1);
+    for (int i = k.first; i < k.last && !stop; ++i) {
+      const int rows = min(P::kUnit, k.len - i * P::kUnit), boxes = (rows + box - 1) / box;  // none of an empty cache
+      const int entry = (i * P::kUnit) >> a.page_shift;
+      if (boxes > 0 && (seq != k.b || entry < first || entry + boxes > first + 32)) {
+        seq = k.b;
+        first = entry;
+        page = entry + lane < a.max_pages ? __ldg(a.table + static_cast<size_t>(k.b) * a.max_pages + entry + lane) : 0;
+      }
+      // lane x copies box x: its row in the pools
+      int y = 0;
+      const int id = __shfl_sync(0xffffffffu, page, (entry - first + lane) & 31);
+      if (lane < boxes) {
+        const bool ok = id >= 0 && id < a.n_pages;
+        if (!ok) atomicExch(a.status, kStatusDeviceAssert);
+        y = (((ok ? id : 0) * a.H + k.h) << a.page_shift) + ((i * P::kUnit) & ((1 << a.page_shift) - 1));
+      }
+#pragma unroll
+      for (int v = 0; v < 2; ++v, ++n) {
+        const Tile<P::kSlots> tile(n);
+        if (*s_err || !mbar_wait(&empty_bar[tile.slot], tile.parity ^ 1, da.wait_ns)) stop = true;
+        if (__any_sync(0xffffffffu, stop)) {
+          *s_err = 1;
+          stop = true;
+          break;
+        }
+        if (lane == 0) mbar_arrive_tx(&full_bar[tile.slot], boxes * box * kD * 2);
+        __syncwarp();
+        if (lane < boxes)
+          tma_2d(smem_addr(ring + tile.slot * P::kSlotBytes) + lane * box * 128, v ? map_v : map_k, 0, y, &full_bar[tile.slot]);
+      }
+    }
+    u = k.start + k.units + P::kTaskCost;
+  }
+  // nothing may be in flight when the block ends
+  for (int c = n - P::kSlots < 0 ? 0 : n - P::kSlots; c < n; ++c) {
+    const Tile<P::kSlots> tile(c);
+    mbar_wait(&full_bar[tile.slot], tile.parity, da.wait_ns);
+  }
+  if (*s_err && lane == 0) atomicExch(a.status, kStatusTimeout);
+}
+
 struct TcBars {
-  uint64_t full[4], empty[4];  // slots of the ring
-  uint64_t scores[2];          // S of a unit is in its buffer (units alternate)
-  uint64_t weights;            // P of a unit is in shared memory
-  uint64_t added;              // ... and in O
-  uint64_t query;              // Q' of a piece is in shared memory
+  uint64_t full[10], empty[10];  // slots of the ring
+  uint64_t scores[2];            // S of a unit is in its buffer (units alternate)
+  uint64_t weights;              // P of a unit is in shared memory
+  uint64_t added;                // ... and in O
+  uint64_t query;                // Q' of a piece is in shared memory
   uint64_t drained;
 };
 
@@ -187,7 +248,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
 
   if (warp == kFeeder) {
     // =================================================================== feeder
-    feed<__nv_bfloat16, P>(da, sch, u0, u1, &map_k, &map_v, smem, bars.full, bars.empty, &s_err);
+    feed_tiles<P>(da, sch, u0, u1, &map_k, &map_v, smem, bars.full, bars.empty, &s_err);
   } else if (warp == kIssuer) {
     // =================================================================== products
     if (lane == 0) {
@@ -215,17 +276,18 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       while (more_o && !s_err) {
         bool did = false;
         // S of a unit: its keys and its piece's query are there, and its buffer's last user is past it
-        if (more_s && s.count - o.count < 2 && mbar_try(&bars.full[s.count % P::kSlots], (s.count / P::kSlots) & 1) &&
-            (!s.first || mbar_try(&bars.query, pieces & 1))) {
+        const Tile<P::kSlots> kt(2 * s.count), vt(2 * o.count + 1);
+        if (more_s && s.count - o.count < 2 && mbar_try(&bars.full[kt.slot], kt.parity) && (!s.first || mbar_try(&bars.query, pieces & 1))) {
           if (s.first) ++pieces;
           fence_after();
-          const uint32_t kt = base + (s.count % P::kSlots) * P::kSlotBytes, d = tmem + (s.count & 1) * ROWS;
+          const uint32_t from = base + kt.slot * P::kSlotBytes, d = tmem + (s.count & 1) * ROWS;
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
-              mma_tc(d, matrix_at(kt + 32 * x, 16, 1024, 2), matrix_at(base + P::kQuery + part * ROWS * 128 + 32 * x, 16, 1024, 2), kScores,
+              mma_tc(d, matrix_at(from + 32 * x, 16, 1024, 2), matrix_at(base + P::kQuery + part * ROWS * 128 + 32 * x, 16, 1024, 2), kScores,
                      part + x > 0);
+          commit_tc(&bars.empty[kt.slot]);
           commit_tc(&bars.scores[s.count & 1]);
           ++s.count;
           ++s.i;
@@ -233,16 +295,16 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           more_s = next(s);
           did = true;
         }
-        if (o.count < s.count && mbar_try(&bars.weights, o.count & 1)) {
+        if (o.count < s.count && mbar_try(&bars.weights, o.count & 1) && mbar_try(&bars.full[vt.slot], vt.parity)) {
           fence_after();
-          const uint32_t vt = base + (o.count % P::kSlots) * P::kSlotBytes + P::kHalf;
+          const uint32_t from = base + vt.slot * P::kSlotBytes;
 #pragma unroll
           for (int part = 0; part < 2; ++part)
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-              mma_tc(tmem_o, matrix_at(vt + 2048 * x, 16, 1024, 2), matrix_at(base + P::kWeights + part * ROWS * 256 + 256 * x, 128, 2048, 0),
+              mma_tc(tmem_o, matrix_at(from + 2048 * x, 16, 1024, 2), matrix_at(base + P::kWeights + part * ROWS * 256 + 256 * x, 128, 2048, 0),
                      kValues, !o.first || part + x > 0);
-          commit_tc(&bars.empty[o.count % P::kSlots]);
+          commit_tc(&bars.empty[vt.slot]);
           commit_tc(&bars.added);
           ++o.count;
           ++o.i;
@@ -263,13 +325,13 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
     __syncwarp();
   } else {
     // =================================================================== softmax
-    float* s_acc = reinterpret_cast<float*>(smem + P::kAcc);
     float* s_ref = reinterpret_cast<float*>(smem + P::kRef);
     float* s_max = reinterpret_cast<float*>(smem + P::kMax);
     float* s_sum = reinterpret_cast<float*>(smem + P::kSum);
     float* s_warp = reinterpret_cast<float*>(smem + P::kWarpMax);
     float* s_draft = reinterpret_cast<float*>(smem + P::kWeights);  // before a piece's weights
-    float* s_part = reinterpret_cast<float*>(smem + P::kWeights);   // after them: [ROWS][128] sums
+    float* s_part = reinterpret_cast<float*>(smem + P::kWeights);   // after them: [ROWS][128] sums, then O
+    float* drafts = da.part + static_cast<size_t>(da.blocks) * 2 * ROWS * kDtPart + static_cast<size_t>(blockIdx.x) * ROWS * kAccStride;  // the drafted keys' O
     const int group = warp >> 2, g0 = group * GR, key = tid & 127, wq = warp & 3;  // the thread's query rows and key
     const uint32_t lanes = static_cast<uint32_t>(wq) << 21;                        // its warp's lanes of tensor memory
     int count = 0;
@@ -320,7 +382,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       if (tail) rotate_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, &ok);
       cons_sync<CONS>();
       if (tail) {
-        attend_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, r0, rows, s_acc, s_max + ROWS, s_sum + ROWS, [&](int r, int t, float(&y)[16]) {
+        attend_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, r0, rows, drafts, s_max + ROWS, s_sum + ROWS, [&](int r, int t, float(&y)[16]) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const unsigned char* at = smem + P::kQuery + r * 128 + (((t + 4 * h) ^ (r & 7)) << 4);
@@ -341,7 +403,6 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       for (int r = 0; r < GR; ++r) l[r] = 0.f;
       for (int i = k.first; i < k.last; ++i, ++count) {
         const bool in = key < k.len - i * P::kUnit;
-        unsigned char* slot = smem + (count % P::kSlots) * P::kSlotBytes;
         wait(&bars.scores[count & 1], (count >> 1) & 1);
         fence_after();
         float s[GR];
@@ -364,16 +425,15 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
 #pragma unroll
           for (int r = 0; r < GR; ++r) bad |= r < mine && isnan(s[r]);
           if (bad) {
-            wait(&bars.full[count % P::kSlots], (count / P::kSlots) & 1);  // (long over; it orders the copies before these reads)
+            const long long at = cache_row(a, k.b, k.h, i * P::kUnit + key);  // (the tile's slot may hold another by now)
 #pragma unroll 1
-            for (int r = 0; r < mine; ++r) {
+            for (int r = 0; r < mine && at >= 0; ++r) {
               float x = 0.f;
 #pragma unroll 1
               for (int d = 0; d < kD; ++d) {
-                const int c = d >> 3;
-                const __nv_bfloat16 kx = *reinterpret_cast<const __nv_bfloat16*>(slot + key * 128 + ((c ^ (key & 7)) << 4) + (d & 7) * 2);
+                const __nv_bfloat16 kx = static_cast<const __nv_bfloat16*>(a.kc)[at + d];
                 const __nv_bfloat16 qx =
-                    *reinterpret_cast<const __nv_bfloat16*>(smem + P::kQuery + (g0 + r) * 128 + ((c ^ (r & 7)) << 4) + (d & 7) * 2);
+                    *reinterpret_cast<const __nv_bfloat16*>(smem + P::kQuery + (g0 + r) * 128 + (((d >> 3) ^ (r & 7)) << 4) + (d & 7) * 2);
                 x = fmaf(__bfloat162float(kx), __bfloat162float(qx), x);
               }
 #pragma unroll
@@ -435,7 +495,9 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           *reinterpret_cast<uint4*>(at + ROWS * 256 + c * 2048) = make_uint4(lo[4 * c], lo[4 * c + 1], lo[4 * c + 2], lo[4 * c + 3]);
         }
         if (group == 0 && !in) {  // a row that was not filled for this sequence: its weight is 0, and so must be what it holds
-          uint4* v = reinterpret_cast<uint4*>(slot + P::kHalf + key * 128);
+          const Tile<P::kSlots> vt(2 * count + 1);
+          wait(&bars.full[vt.slot], vt.parity);  // after the copy, which would undo it
+          uint4* v = reinterpret_cast<uint4*>(smem + vt.slot * P::kSlotBytes + key * 128);
 #pragma unroll
           for (int x = 0; x < 8; ++x) v[x] = make_uint4(0, 0, 0, 0);
         }
@@ -468,19 +530,19 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       }
       cons_sync<CONS>();
       if (lane < 16) {  // 16 rows of O^T lie in a warp's first 16 lanes
-        float* acc = s_acc + g0 * kAccStride + 16 * wq + lane;
+        const int at = g0 * kAccStride + 16 * wq + lane;
 #pragma unroll
         for (int r = 0; r < GR; ++r)
           if (r < mine) {
             float y = o[r] * s_warp[g0 + r];
-            if (tail) y = fmaf(acc[r * kAccStride], s_warp[ROWS + g0 + r], y);
-            acc[r * kAccStride] = y;
+            if (tail) y = fmaf(drafts[at + r * kAccStride], s_warp[ROWS + g0 + r], y);
+            s_part[at + r * kAccStride] = y;
           }
       }
       fence_before();
       cons_sync<CONS>();
       if (!ok) atomicExch(a.status, kStatusDeviceAssert);
-      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, tail ? 2 : 1);
+      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_part, s_max, s_sum, tail ? 2 : 1);
       cons_sync<CONS>();  // everything of the piece is free again
     }
   }
@@ -509,7 +571,8 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
 
 template <int ROWS>
 size_t part_bytes() {
-  return static_cast<size_t>(152) * TcShape<ROWS>::kResident * 2 * ROWS * kDtPart * sizeof(float);
+  // two partials a block, and the drafted keys' part of a piece
+  return static_cast<size_t>(152) * TcShape<ROWS>::kResident * ROWS * (2 * kDtPart + kAccStride) * sizeof(float);
 }
 
 }  // namespace
