@@ -524,7 +524,7 @@ struct DtSmem {
   static constexpr int kZero = (kSum + (kGroups + 1) * kRows * 4 + 127) / 128 * 128;
   static constexpr int kQuery = kZero + 128;
   static constexpr int kDraft = kQuery + TILES * C::kQueryBytes;
-  static size_t bytes(int B, int T) { return kDraft + static_cast<size_t>(T) * kD * 4 + schedule_bytes(B); }
+  static size_t bytes(int B, int T) { return kDraft + static_cast<size_t>(T) * kD * 8 + schedule_bytes(B); }
 };
 
 template <typename DT, int NR, int TILES>
@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (tid < 32) reinterpret_cast<float*>(smem + S::kZero)[tid] = 0.f;
-  const Schedule sch = schedule_at(smem + S::kDraft + a.T * kD * 4, a.B);
+  const Schedule sch = schedule_at(smem + S::kDraft + a.T * kD * 8, a.B);
   build_schedule<S>(a, sch);
   const long long cost = sch.start[a.B];
   const int sharing = sharing_blocks(cost, da.blocks, S::kLeast);
@@ -590,10 +590,10 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
       s_pos[r] = pos;
       C::load_query(a, qs, i, r < rows, row, pos);
     }
-    if (tail) rotate_drafts<DT, kDtCons>(a, k, tree, s_draft, &ok);
+    if (tail) stage_drafts<DT, kDtCons>(a, k, tree, s_draft, &ok);
     cons_sync<kDtCons>();
     if (tail)
-      attend_drafts<DT, kDtCons>(a, k, tree, s_draft, r0, rows, s_acc, s_max + GROUPS * ROWS, s_sum + GROUPS * ROWS,
+      attend_drafts<kDtCons>(a, k, tree, s_draft, r0, rows, s_acc, s_max + GROUPS * ROWS, s_sum + GROUPS * ROWS,
                                  [&](int r, int lane4, float(&y)[16]) {
                                    int s;
                                    const size_t row = row_of(a, k, r0 + r, &s);

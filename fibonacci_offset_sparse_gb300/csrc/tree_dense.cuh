@@ -152,36 +152,6 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
-// The 16 dims D_t of a row (common.cuh) as they are stored.
-__device__ __forceinline__ void load_raw(const __nv_bfloat16* row, int t, uint4 (&x)[2]) {
-  x[0] = __ldg(reinterpret_cast<const uint4*>(row + 8 * t));
-  x[1] = __ldg(reinterpret_cast<const uint4*>(row + kFreq + 8 * t));
-}
-__device__ __forceinline__ void load_raw(const float* row, int t, uint4 (&x)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = __ldg(reinterpret_cast<const uint4*>(row + (i >> 1) * kFreq + 8 * t) + (i & 1));
-}
-__device__ __forceinline__ void raw_to_float(const uint4 (&x)[2], float (&v)[16], const __nv_bfloat16*) {
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      v[8 * i + 2 * j] = bf_lo(w[j]);
-      v[8 * i + 2 * j + 1] = bf_hi(w[j]);
-    }
-  }
-}
-__device__ __forceinline__ void raw_to_float(const uint4 (&x)[4], float (&v)[16], const float*) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[4 * i] = __uint_as_float(x[i].x);
-    v[4 * i + 1] = __uint_as_float(x[i].y);
-    v[4 * i + 2] = __uint_as_float(x[i].z);
-    v[4 * i + 3] = __uint_as_float(x[i].w);
-  }
-}
-
 // ------------------------------------------------------------------------------ feeder --
 // The feeding warp: K and V rows of the units of [u0, u1) into the ring's slots, a page at a time.  A slot
 // is K, then V, kHalf bytes each; float32 rows lie as two halves of 32 dims, a quarter slot apart.
@@ -257,9 +227,10 @@ __device__ __forceinline__ int position_of(const TreeArgs& a, const Task& k, int
   return a.N - 1;
 }
 
-// The task's drafted keys, rotated, into `draft` [n][64]; by the CONS computing threads.
+// The task's drafted keys, rotated, and their values into `draft` ([n][64] each, float); by the CONS computing
+// threads.
 template <typename DT, int CONS>
-__device__ __forceinline__ void rotate_drafts(const TreeArgs& a, const Task& k, const WarpTree& tree, float* draft, bool* ok) {
+__device__ __forceinline__ void stage_drafts(const TreeArgs& a, const Task& k, const WarpTree& tree, float* draft, bool* ok) {
   const int tid = threadIdx.x, t = tid & 3;
   const size_t fresh = (static_cast<size_t>(k.b) * a.H + k.h) * a.T * kD;
   const DT* kn = static_cast<const DT*>(a.kn) + fresh;
@@ -268,26 +239,32 @@ __device__ __forceinline__ void rotate_drafts(const TreeArgs& a, const Task& k, 
     const int s = x * (CONS / 4) + (tid >> 2);
     const int depth = pick32(tree.depth, s & 63);
     if (s < k.n) {
-      float y[16];
+      float y[16], v[16];
       float2 e[8];
       load_part(kn + static_cast<size_t>(s) * kD, t, y);
-      // the values too, into L1: the rows' loops would wait for each in turn
-      const char* vr = reinterpret_cast<const char*>(vn + static_cast<size_t>(s) * kD) + t * (kD * sizeof(DT) / 4);
-      asm volatile("{ .reg .b32 x; ld.global.nc.b32 x, [%0]; }\n" ::"l"(vr));
+      load_part(vn + static_cast<size_t>(s) * kD, t, v);
       rope_row(a.rope_lo, a.rope_hi, position_of(a, k, depth, ok), t, e);
       rotate_part(y, e, false);
       store_part(draft + s * kD, t, y);
+      store_part(draft + (k.n + s) * kD, t, v);
     }
   }
 }
 
+__device__ __forceinline__ void read_part(const float* row, int t, float (&x)[16]) {
+  const float4* r = reinterpret_cast<const float4*>(row);
+  *reinterpret_cast<float4*>(x) = r[2 * t];
+  *reinterpret_cast<float4*>(x + 4) = r[2 * t + 1];
+  *reinterpret_cast<float4*>(x + 8) = r[8 + 2 * t];
+  *reinterpret_cast<float4*>(x + 12) = r[8 + 2 * t + 1];
+}
+
 // The part of the drafted keys in each row: O (not divided) into acc, maximum and sum into mx and sm.  A quad a
 // row, over the row's ancestors alone.  query(r, t, y): the rotated query of row r times log2(e)/8, dims D_t.
-template <typename DT, int CONS, typename Q>
+template <int CONS, typename Q>
 __device__ __forceinline__ void attend_drafts(const TreeArgs& a, const Task& k, const WarpTree& tree, const float* draft, int r0, int rows,
                                               float* acc, float* mx, float* sm, Q&& query) {
   const int tid = threadIdx.x, t = tid & 3;
-  const DT* vn = static_cast<const DT*>(a.vn) + (static_cast<size_t>(k.b) * a.H + k.h) * a.T * kD;
   for (int x = 0; x < (rows + CONS / 4 - 1) / (CONS / 4); ++x) {
     const int r = x * (CONS / 4) + (tid >> 2);
     const bool in = r < rows;
@@ -298,28 +275,17 @@ __device__ __forceinline__ void attend_drafts(const TreeArgs& a, const Task& k, 
 #pragma unroll
     for (int w = 0; w < 16; ++w) y[w] = o[w] = 0.f;
     if (in) query(r, t, y);
-    // the values of the next ancestor are on their way while one is added
-    uint4 next[sizeof(DT)];
-    int key = set != 0 ? __ffsll(static_cast<long long>(set)) - 1 : 0;
-    if (set != 0) load_raw(vn + static_cast<size_t>(key) * kD, t, next);
     while (__any_sync(0xffffffffu, set != 0)) {
       const bool on = set != 0;
       float sc = 0.f, v[16];
-      raw_to_float(next, v, vn);
       if (on) {
+        const int key = __ffsll(static_cast<long long>(set)) - 1;
+        set &= set - 1;
         float kx[16];
-        const float4* kr = reinterpret_cast<const float4*>(draft + key * kD);
-        *reinterpret_cast<float4*>(kx) = kr[2 * t];
-        *reinterpret_cast<float4*>(kx + 4) = kr[2 * t + 1];
-        *reinterpret_cast<float4*>(kx + 8) = kr[8 + 2 * t];
-        *reinterpret_cast<float4*>(kx + 12) = kr[8 + 2 * t + 1];
+        read_part(draft + key * kD, t, kx);
+        read_part(draft + (k.n + key) * kD, t, v);
 #pragma unroll
         for (int w = 0; w < 16; ++w) sc = fmaf(y[w], kx[w], sc);
-      }
-      set &= set - 1;
-      if (set != 0) {
-        key = __ffsll(static_cast<long long>(set)) - 1;
-        load_raw(vn + static_cast<size_t>(key) * kD, t, next);
       }
       sc = quad_sum(sc);
       if (on && sc != -INFINITY) {  // weight 0 (a NaN goes on)

@@ -29,7 +29,7 @@ constexpr float kNoKey = -1e30f;  // reference of a row that has met no finite s
 
 template <int ROWS>
 struct TcShape {
-  static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 3, kLeast = 1;
+  static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 6, kLeast = 1;
   static constexpr int kSlotBytes = kUnit * kD * 2;  // K or V of a unit
   static constexpr int kGroupRows = ROWS == 16 ? 8 : 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
   static constexpr int kCons = 128 * kGroups, kThreads = kCons + 64;
@@ -340,12 +340,17 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       s_err = 1;
       atomicExch(a.status, kStatusTimeout);
     };
-    for (long long u = u0; u < u1;) {
-      const Task k = task_of<P>(a, sch, u, u1);
-      u = k.start + k.units + P::kTaskCost;
+    // The task at u, formed anew where it is needed: its fields would hold registers over the loop below.
+    auto task_at = [&](long long u) {
+      asm volatile("" : "+l"(u));
+      return task_of<P>(a, sch, u, u1);
+    };
+    for (long long u = u0, after; u < u1; u = after) {
+      const Task k = task_at(u);
+      after = k.start + k.units + P::kTaskCost;
       if (k.first == k.last) continue;
-      const bool tail = k.last == k.units, whole = tail && k.first == 0;
-      const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);
+      const bool tail = k.last == k.units;
+      const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0), k_first = k.first, k_last = k.last, k_len = k.len;
       const int mine = min(GR, max(0, rows - g0));  // rows of this group
       bool ok = true;
       const WarpTree tree = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(k.b) * a.T, k.n, &ok);
@@ -379,10 +384,10 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       fence_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.query);
-      if (tail) rotate_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, &ok);
+      if (tail) stage_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, &ok);
       cons_sync<CONS>();
       if (tail) {
-        attend_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, r0, rows, drafts, s_max + ROWS, s_sum + ROWS, [&](int r, int t, float(&y)[16]) {
+        attend_drafts<CONS>(a, k, tree, s_draft, r0, rows, drafts, s_max + ROWS, s_sum + ROWS, [&](int r, int t, float(&y)[16]) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const unsigned char* at = smem + P::kQuery + r * 128 + (((t + 4 * h) ^ (r & 7)) << 4);
@@ -401,8 +406,8 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       float l[GR];
 #pragma unroll
       for (int r = 0; r < GR; ++r) l[r] = 0.f;
-      for (int i = k.first; i < k.last; ++i, ++count) {
-        const bool in = key < k.len - i * P::kUnit;
+      for (int i = k_first; i < k_last; ++i, ++count) {
+        const bool in = key < k_len - i * P::kUnit;
         wait(&bars.scores[count & 1], (count >> 1) & 1);
         fence_after();
         float s[GR];
@@ -425,7 +430,8 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
 #pragma unroll
           for (int r = 0; r < GR; ++r) bad |= r < mine && isnan(s[r]);
           if (bad) {
-            const long long at = cache_row(a, k.b, k.h, i * P::kUnit + key);  // (the tile's slot may hold another by now)
+            const Task now = task_at(u);
+            const long long at = cache_row(a, now.b, now.h, i * P::kUnit + key);  // (the tile's slot may hold another by now)
 #pragma unroll 1
             for (int r = 0; r < mine && at >= 0; ++r) {
               float x = 0.f;
@@ -450,21 +456,19 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           if (count > 0) wait(&bars.added, (count - 1) & 1);  // O is at rest
           fence_after();
           group_sync(group);
-          float corr[GR];
 #pragma unroll
-          for (int r = 0; r < GR; ++r) {
-            const float* w = s_warp + g0 + r;
-            const float m = s_ref[g0 + r];
-            const float mn = fmaxf(m, fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS])));
-            corr[r] = ex2(m - mn);
-            l[r] *= corr[r];
-          }
-          if (i > k.first) {
-            float x[GR];
-            tmem_load(tmem_o + g0 + lanes, x);
+          for (int c = 0; c < GR / 8; ++c) {
+            float x[8];
+            tmem_load(tmem_o + g0 + 8 * c + lanes, x);  // (unused at a piece's first unit)
 #pragma unroll
-            for (int r = 0; r < GR; ++r) x[r] *= corr[r];
-            tmem_store(tmem_o + g0 + lanes, x);
+            for (int e = 0; e < 8; ++e) {
+              const float* w = s_warp + g0 + 8 * c + e;
+              const float m = s_ref[g0 + 8 * c + e];
+              const float corr = ex2(m - fmaxf(m, fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS]))));
+              l[8 * c + e] *= corr;
+              x[e] *= corr;
+            }
+            if (i > k_first) tmem_store(tmem_o + g0 + 8 * c + lanes, x);
           }
           group_sync(group);
           if (key < GR) {
@@ -542,7 +546,8 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       fence_before();
       cons_sync<CONS>();
       if (!ok) atomicExch(a.status, kStatusDeviceAssert);
-      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_part, s_max, s_sum, tail ? 2 : 1);
+      const Task done = task_at(u);
+      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, done, tail && done.first == 0, done.start >= u0 ? 1 : 0, r0, rows, s_part, s_max, s_sum, tail ? 2 : 1);
       cons_sync<CONS>();  // everything of the piece is free again
     }
   }
