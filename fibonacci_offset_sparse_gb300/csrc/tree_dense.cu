@@ -554,6 +554,7 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
   if (tid < 32) reinterpret_cast<float*>(smem + S::kZero)[tid] = 0.f;
   const Schedule sch = schedule_at(smem + S::kDraft + a.T * kD * 8, a.B);
   build_schedule<S>(a, sch);
+  if (tid == 0) da.split[blockIdx.x].parts = 0;
   const long long cost = sch.start[a.B];
   const int sharing = sharing_blocks(cost, da.blocks, S::kLeast);
   if (static_cast<int>(blockIdx.x) >= sharing) return;
@@ -576,6 +577,7 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
     const Task k = task_of<S>(a, sch, u, u1);
     u = k.start + k.units + S::kTaskCost;
     if (k.first == k.last) continue;
+    if (tid == 0) note_split<S>(da, k, cost, sharing, u0);
     const bool tail = k.last == k.units, whole = tail && k.first == 0;
     const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);  // row r0 + i is (query head, node)
     bool ok = true;
@@ -679,6 +681,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
   using S = DtSmem<DT, NR, TILES>;
   DenseTreeArgs da = args;
   da.blocks = kGrid<DT, NR, TILES>;
+  da.split = reinterpret_cast<Split*>(da.part + static_cast<size_t>(da.blocks) * 2 * S::kRows * kDtPart);
   const TreeArgs& a = da.a;
   CUtensorMap mk, mv;
   cudaError_t e = maps_of(a, static_cast<int>(sizeof(DT)), S::kUnit, &mk, &mv);
@@ -695,7 +698,8 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
 template <typename DT>
 size_t part_bytes(int rows) {
   return with_shape<DT>(rows, []<int NR, int TILES>() {
-    return static_cast<size_t>(kGrid<DT, NR, TILES>) * 2 * DtSmem<DT, NR, TILES>::kRows * kDtPart * sizeof(float);
+    return static_cast<size_t>(kGrid<DT, NR, TILES>) *
+           (2 * DtSmem<DT, NR, TILES>::kRows * kDtPart * sizeof(float) + sizeof(Split));
   });
 }
 
@@ -717,6 +721,7 @@ cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long w
   da.a = a;
   da.part = static_cast<float*>(ws);
   da.wait_ns = wait_ns;
+  da.split = nullptr;
   da.blocks = 0;
   if (dtype == FIB_DTYPE_BF16 && a.G * a.T > kMmaRows) return launch_dense_tree_tc(da, stream);
   return dtype == FIB_DTYPE_F32 ? launch_rows<float>(da, stream) : launch_rows<__nv_bfloat16>(da, stream);

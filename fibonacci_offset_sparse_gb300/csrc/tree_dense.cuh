@@ -13,9 +13,18 @@ namespace fibattn {
 constexpr int kAccStride = 68;   // floats of a row of O in shared memory
 constexpr int kDtPart = kD + 2;  // floats of a partial's row: O, max, sum
 
+// A task whose units several blocks hold, as the first of them leaves it for the join.
+struct Split {
+  int parts;  // 0: none
+  int slot;   // of the first block's partial; the others' lie in slot 0
+  int b, h, rb, n;
+  int unused[2];
+};
+
 struct DenseTreeArgs {
   TreeArgs a;
-  float* part;  // [blocks][2][ROWS][kDtPart]
+  float* part;   // [blocks][2][ROWS][kDtPart]
+  Split* split;  // [blocks]
   unsigned long long wait_ns;
   int blocks;   // blocks of the grid
 };
@@ -81,7 +90,10 @@ __device__ __forceinline__ int sharing_blocks(long long cost, int blocks, int le
   return want < blocks ? static_cast<int>(want) : blocks;
 }
 // Block c's run begins at cut(c); block_at(x) is the block whose run holds place x.
-__device__ __forceinline__ long long cut(long long cost, int sharing, int c) { return cost * c / sharing; }
+__device__ __forceinline__ long long cut(long long cost, int sharing, int c) {
+  if (cost < 1 << 22) return static_cast<uint32_t>(cost) * static_cast<uint32_t>(c) / static_cast<uint32_t>(sharing);  // (c < 512)
+  return cost * c / sharing;
+}
 __device__ __forceinline__ int block_at(long long cost, int sharing, long long x) {
   return static_cast<int>(((x + 1) * sharing - 1) / cost);  // the largest c with cost * c < (x + 1) * sharing
 }
@@ -111,7 +123,7 @@ __device__ __forceinline__ Task task_of(const TreeArgs& a, const Schedule& s, lo
   t.units = units_of<P::kUnit>(t.len);
   const int rbs = (a.G * t.n + P::kRows - 1) / P::kRows, each = t.units + P::kTaskCost;
   const long long off = u - s.start[lo];
-  const int task = static_cast<int>(off / each);
+  const int task = off < 1LL << 31 ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(each)) : static_cast<int>(off / each);
   t.start = s.start[lo] + static_cast<long long>(task) * each;
   t.h = task / rbs;
   t.rb = task - t.h * rbs;
@@ -340,59 +352,51 @@ __device__ __forceinline__ void write_rows(const DenseTreeArgs& da, const Task& 
 }
 
 // ------------------------------------------------------------------------------ join --
-// Adds the partials of the tasks whose units more than one block holds.  Block (c, y) serves 8 rows of the task
-// whose first cut is the one in front of block c.  A row has two teams of 16 threads, which take every
-// second partial; the weights come first, so that the loads of O do not wait for one another.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 8;
+// Whether this block is the first of several that hold task k's units, and how many those are (one thread,
+// for each piece).
+template <typename P>
+__device__ __forceinline__ void note_split(const DenseTreeArgs& da, const Task& k, long long cost, int sharing, long long u0) {
+  if (k.first > 0 || k.last == k.units) return;
+  const int last = block_at(cost, sharing, k.start + P::kTaskCost + k.units - 1);
+  da.split[blockIdx.x] = Split{last - static_cast<int>(blockIdx.x) + 1, k.start >= u0 ? 1 : 0, k.b, k.h, k.rb, k.n, {0, 0}};
+}
 
-template <typename DT, typename P>
+// Adds the partials of the tasks whose units several blocks hold.  Block (c, y) serves 4 rows of the task that
+// block c is the first of.  16 threads read a row of a partial; a row has four such teams, which take every fourth
+// partial and meet in order.  The weights come first, so that the loads of O do not wait for one another.
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 4;
+constexpr int kJoinTeams = kJoinThreads / 16 / kJoinRows;
+
+template <typename DT, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DenseTreeArgs da) {
-  constexpr int ROWS = P::kRows;
-  extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ float4 s_o[kJoinRows][16];
+  __shared__ float4 s_o[kJoinTeams][kJoinRows][16];
   const TreeArgs& a = da.a;
-  const Schedule sch = schedule_at(smem, a.B);
-  build_schedule<P>(a, sch);
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const long long cost = sch.start[a.B];
-  const int sharing = sharing_blocks(cost, da.blocks, P::kLeast);
-  const int c = blockIdx.x;
-  if (c == 0 || c >= sharing) return;
-  const long long u = cut(cost, sharing, c);
-  const Task k = task_of<P>(a, sch, u, cost);
-  // the cut lies behind the task's first unit, and is the first that does
-  const long long t0 = k.start + P::kTaskCost, t1 = t0 + k.units;
-  if (u <= t0 || cut(cost, sharing, c - 1) > t0) return;
-  const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);
-  const int team = threadIdx.x >> 4, d = (threadIdx.x & 15) * 4, share = team & 1, at = team >> 1;
-  const int r = kJoinRows * blockIdx.y + at;
+  const Split sp = da.split[blockIdx.x];
+  const int r0 = sp.rb * ROWS, rows = sp.parts == 0 ? 0 : min(ROWS, a.G * sp.n - r0);
   if (kJoinRows * static_cast<int>(blockIdx.y) >= rows) return;
-  const int parts = block_at(cost, sharing, t1 - 1) - (c - 1) + 1;  // blocks that hold some of it
-  // partial i lies in block c - 1 + i: in its first place, or its second where the block began before the task
-  const int first_slot = k.start >= cut(cost, sharing, c - 1) ? 1 : 0;
-  auto partial = [&](int i) {
-    const int slot = i == 0 ? first_slot : 0;
-    return da.part + ((static_cast<size_t>(c - 1 + i) * 2 + slot) * ROWS + r) * kDtPart;
-  };
+  const int d = (threadIdx.x & 15) * 4, at = (threadIdx.x >> 4) % kJoinRows, share = (threadIdx.x >> 4) / kJoinRows;
+  const int r = kJoinRows * blockIdx.y + at;
+  const float* first = da.part + ((static_cast<size_t>(blockIdx.x) * 2 + sp.slot) * ROWS + r) * kDtPart;
+  const float* second = da.part + (static_cast<size_t>(blockIdx.x + 1) * 2 * ROWS + r) * kDtPart;
+  auto partial = [&](int i) { return i == 0 ? first : second + static_cast<size_t>(i - 1) * (2 * ROWS * kDtPart); };
   float all = -INFINITY, sum = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (r < rows) {
-    for (int i = threadIdx.x & 15; i < parts; i += 16) all = fmaxf(all, partial(i)[kD]);
-  }
+  if (r < rows)
+    for (int i = threadIdx.x & 15; i < sp.parts; i += 16) all = fmaxf(all, partial(i)[kD]);
 #pragma unroll
   for (int x = 1; x < 16; x <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, x));
-  if (r < rows) {
-    for (int i = threadIdx.x & 15; i < parts; i += 16) {
+  if (r < rows)
+    for (int i = threadIdx.x & 15; i < sp.parts; i += 16) {
       const float2 ml = *reinterpret_cast<const float2*>(partial(i) + kD);
       sum += ml.y * weight_of(ml.x, ml.y, all);
     }
-  }
 #pragma unroll
   for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
   if (r < rows) {
 #pragma unroll 4
-    for (int i = share; i < parts; i += 2) {
+    for (int i = share; i < sp.parts; i += kJoinTeams) {
       const float* p = partial(i);
       const float2 x = *reinterpret_cast<const float2*>(p + d), y = *reinterpret_cast<const float2*>(p + d + 2);
       const float2 ml = *reinterpret_cast<const float2*>(p + kD);
@@ -403,19 +407,22 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
       o.w += y.y * f;
     }
   }
-  if (share) s_o[at][d / 4] = o;
+  s_o[share][at][d / 4] = o;
   __syncthreads();
   if (share || r >= rows) return;
-  const float4 x = s_o[at][d / 4];
+#pragma unroll
+  for (int x = 1; x < kJoinTeams; ++x) {
+    const float4 y = s_o[x][at][d / 4];
+    o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+  }
   const float inv = 1.f / sum;
-  o = make_float4((o.x + x.x) * inv, (o.y + x.y) * inv, (o.z + x.z) * inv, (o.w + x.w) * inv);
-  const int head = (r0 + r) / k.n, s = (r0 + r) - head * k.n;
-  const size_t row = (static_cast<size_t>(k.b) * a.Hq + k.h * a.G + head) * a.T + s;
+  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  const int head = (r0 + r) / sp.n, s = (r0 + r) - head * sp.n;
+  const size_t row = (static_cast<size_t>(sp.b) * a.Hq + sp.h * a.G + head) * a.T + s;
   if constexpr (sizeof(DT) == 4)
     *reinterpret_cast<float4*>(static_cast<float*>(a.o) + row * kD + d) = o;
   else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * kD + d) =
-        make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * kD + d) = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
   if (d == 0 && a.lse != nullptr) a.lse[row] = (all + log2f(sum)) * kLn2;
 }
 
@@ -426,14 +433,13 @@ cudaError_t launch_join(const DenseTreeArgs& da, cudaStream_t stream) {
   const int most = a.G * a.T < P::kRows ? a.G * a.T : P::kRows;
   cfg.gridDim = dim3(static_cast<unsigned>(da.blocks), (most + kJoinRows - 1) / kJoinRows);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = schedule_bytes(a.B);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<DT, P>, da);
+  return cudaLaunchKernelEx(&cfg, join_kernel<DT, P::kRows>, da);
 }
 
 // ------------------------------------------------------------------------------ copies --

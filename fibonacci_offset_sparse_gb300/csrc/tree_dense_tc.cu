@@ -235,6 +235,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
   }
   const Schedule sch = schedule_at(smem + P::kSchedule, a.B);
   build_schedule<P>(a, sch);
+  if (tid == 0) da.split[blockIdx.x].parts = 0;
   const long long cost = sch.start[a.B];
   const int sharing = sharing_blocks(cost, da.blocks, P::kLeast);
   if (static_cast<int>(blockIdx.x) >= sharing) return;
@@ -349,6 +350,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       const Task k = task_at(u);
       after = k.start + k.units + P::kTaskCost;
       if (k.first == k.last) continue;
+      if (tid == 0) note_split<P>(da, k, cost, sharing, u0);
       const bool tail = k.last == k.units;
       const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0), k_first = k.first, k_last = k.last, k_len = k.len;
       const int mine = min(GR, max(0, rows - g0));  // rows of this group
@@ -535,13 +537,19 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       cons_sync<CONS>();
       if (lane < 16) {  // 16 rows of O^T lie in a warp's first 16 lanes
         const int at = g0 * kAccStride + 16 * wq + lane;
+        if (tail) {  // (every load before a store, which it might seem to depend on)
+          float d[GR];
+#pragma unroll
+          for (int r = 0; r < GR; ++r) d[r] = r < mine ? drafts[at + r * kAccStride] : 0.f;
+#pragma unroll
+          for (int r = 0; r < GR; ++r) o[r] = fmaf(o[r], s_warp[g0 + r], d[r] * s_warp[ROWS + g0 + r]);
+        } else {
+#pragma unroll
+          for (int r = 0; r < GR; ++r) o[r] *= s_warp[g0 + r];
+        }
 #pragma unroll
         for (int r = 0; r < GR; ++r)
-          if (r < mine) {
-            float y = o[r] * s_warp[g0 + r];
-            if (tail) y = fmaf(drafts[at + r * kAccStride], s_warp[ROWS + g0 + r], y);
-            s_part[at + r * kAccStride] = y;
-          }
+          if (r < mine) s_part[at + r * kAccStride] = o[r];
       }
       fence_before();
       cons_sync<CONS>();
@@ -562,6 +570,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
   using P = TcShape<ROWS>;
   DenseTreeArgs da = args;
   da.blocks = 152 * P::kResident;  // 152 SMs
+  da.split = reinterpret_cast<Split*>(da.part + static_cast<size_t>(da.blocks) * ROWS * (2 * kDtPart + kAccStride));
   CUtensorMap mk, mv;
   cudaError_t e = maps_of(da.a, 2, P::kUnit, &mk, &mv);
   if (e != cudaSuccess) return e;
@@ -577,7 +586,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
 template <int ROWS>
 size_t part_bytes() {
   // two partials a block, and the drafted keys' part of a piece
-  return static_cast<size_t>(152) * TcShape<ROWS>::kResident * ROWS * (2 * kDtPart + kAccStride) * sizeof(float);
+  return static_cast<size_t>(152) * TcShape<ROWS>::kResident * (ROWS * (2 * kDtPart + kAccStride) * sizeof(float) + sizeof(Split));
 }
 
 }  // namespace
