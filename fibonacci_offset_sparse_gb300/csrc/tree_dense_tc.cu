@@ -29,7 +29,7 @@ constexpr float kNoKey = -1e30f;  // reference of a row that has met no finite s
 
 template <int ROWS>
 struct TcShape {
-  static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 6, kLeast = 1;
+  static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 8, kLeast = 1;
   static constexpr int kSlotBytes = kUnit * kD * 2;  // K or V of a unit
   static constexpr int kGroupRows = ROWS == 16 ? 8 : 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
   static constexpr int kCons = 128 * kGroups, kThreads = kCons + 64;
@@ -119,6 +119,8 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const float (&x)[N]) {
                  : "memory");
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p)); }
+
 // Whether any of a group's 128 softmax threads says so; they are synchronised by it.
 __device__ __forceinline__ bool any_of_group(int group, bool x) {
   uint32_t r;
@@ -232,6 +234,16 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
     mbar_init(&bars.query, 4 * P::kGroups);
     mbar_init(&bars.drained, 1);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
+  // The queries and drafted rows, read once a task behind a full queue of copies: into L2 before it fills.
+  {
+    const long long q_lines = static_cast<long long>(a.B) * a.Hq * a.T, n_lines = static_cast<long long>(a.B) * a.H * a.T;
+    const long long at = static_cast<long long>(blockIdx.x) * P::kThreads + tid, step = static_cast<long long>(gridDim.x) * P::kThreads;
+    for (long long x = at; x < q_lines; x += step) prefetch_l2(static_cast<const __nv_bfloat16*>(a.q) + x * kD);
+    for (long long x = at; x < n_lines; x += step) {
+      prefetch_l2(static_cast<const __nv_bfloat16*>(a.kn) + x * kD);
+      prefetch_l2(static_cast<const __nv_bfloat16*>(a.vn) + x * kD);
+    }
   }
   const Schedule sch = schedule_at(smem + P::kSchedule, a.B);
   build_schedule<P>(a, sch);
@@ -521,31 +533,50 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
 #pragma unroll
       for (int r = 0; r < GR; ++r) s_part[(g0 + r) * 128 + key] = l[r];
       cons_sync<CONS>();
-      for (int r = warp; r < rows; r += CONS / 32) {
-        const float4 x = *reinterpret_cast<const float4*>(s_part + r * 128 + 4 * lane);
-        float sum = (x.x + x.y) + (x.z + x.w);
+      {
+        // warp w sums rows w, w + CONS / 32, ...; then lane j has its j-th row's maximum, sum and parts' weights
+        constexpr int WARPS = CONS / 32, MOST = (ROWS + WARPS - 1) / WARPS;
+        float sum[MOST];
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) {
-          const float m = s_ref[r] == kNoKey ? -INFINITY : s_ref[r], all = tail ? fmaxf(m, s_max[ROWS + r]) : m;
-          s_sum[r] = sum;
-          s_max[r] = m;
-          s_warp[r] = weight_of(m, sum, all);
-          s_warp[ROWS + r] = tail ? weight_of(s_max[ROWS + r], s_sum[ROWS + r], all) : 0.f;
+        for (int j = 0; j < MOST; ++j) {
+          const int r = warp + WARPS * j;
+          const float4 x = r < rows ? *reinterpret_cast<const float4*>(s_part + r * 128 + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+          sum[j] = (x.x + x.y) + (x.z + x.w);
+        }
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+          for (int j = 0; j < MOST; ++j) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
+        float mine_sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < MOST; ++j)
+          if (lane == j) mine_sum = sum[j];
+        const int r = warp + WARPS * lane;
+        if (lane < MOST && r < rows) {
+          const float m = s_ref[r] == kNoKey ? -INFINITY : s_ref[r];
+          const float md = tail ? s_max[ROWS + r] : -INFINITY, ld = tail ? s_sum[ROWS + r] : 0.f, all = fmaxf(m, md);
+          const float w = weight_of(m, mine_sum, all), wd = weight_of(md, ld, all);
+          s_warp[r] = w;
+          s_warp[ROWS + r] = wd;
+          s_max[r] = all;
+          s_sum[r] = mine_sum * w + ld * wd;
         }
       }
       cons_sync<CONS>();
       if (lane < 16) {  // 16 rows of O^T lie in a warp's first 16 lanes
         const int at = g0 * kAccStride + 16 * wq + lane;
-        if (tail) {  // (every load before a store, which it might seem to depend on)
-          float d[GR];
+        float d[GR];  // (every load before a store, which it might seem to depend on)
 #pragma unroll
-          for (int r = 0; r < GR; ++r) d[r] = r < mine ? drafts[at + r * kAccStride] : 0.f;
+        for (int r = 0; r < GR; ++r) d[r] = tail && r < mine ? drafts[at + r * kAccStride] : 0.f;
 #pragma unroll
-          for (int r = 0; r < GR; ++r) o[r] = fmaf(o[r], s_warp[g0 + r], d[r] * s_warp[ROWS + g0 + r]);
-        } else {
+        for (int c = 0; c < GR / 4; ++c) {
+          const float4 w4 = *reinterpret_cast<const float4*>(s_warp + g0 + 4 * c), d4 = *reinterpret_cast<const float4*>(s_warp + ROWS + g0 + 4 * c);
+          const float w[4] = {w4.x, w4.y, w4.z, w4.w}, wd[4] = {d4.x, d4.y, d4.z, d4.w};
 #pragma unroll
-          for (int r = 0; r < GR; ++r) o[r] *= s_warp[g0 + r];
+          for (int e = 0; e < 4; ++e) {
+            o[4 * c + e] *= w[e];
+            if (tail) o[4 * c + e] = fmaf(d[4 * c + e], wd[e], o[4 * c + e]);
+          }
         }
 #pragma unroll
         for (int r = 0; r < GR; ++r)
@@ -555,7 +586,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       cons_sync<CONS>();
       if (!ok) atomicExch(a.status, kStatusDeviceAssert);
       const Task done = task_at(u);
-      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, done, tail && done.first == 0, done.start >= u0 ? 1 : 0, r0, rows, s_part, s_max, s_sum, tail ? 2 : 1);
+      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, done, tail && done.first == 0, done.start >= u0 ? 1 : 0, r0, rows, s_part, s_max, s_sum, 1);
       cons_sync<CONS>();  // everything of the piece is free again
     }
   }
