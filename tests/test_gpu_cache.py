@@ -392,6 +392,67 @@ def test_another_branch_never_reaches_a_node(dtype):
     plan.close()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 3])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_another_branch_never_reaches_a_node_of_a_large_tree(dtype, G, bad):
+    """As above, for as many query rows as the tensor-core kernels take; only v, only k, then both."""
+    r = rng(20)
+    T = 21
+    c, ref, dev, host, _, _ = tree_case(r, dtype, [150, 0], 2, G, T, 32, "chain", None)
+    parent = np.tile([-1] + [max(0, s - 2) for s in range(1, T)], (2, 1))  # 0, then the odd and the even nodes
+    even = list(range(2, T, 2))
+    odd = [0] + list(range(1, T, 2))
+    plan = plan_for(200, W=4)
+    clean = {name: (o.clone(), l.clone()) for name, o, l in both(plan, c, dev, parent=i32(parent))}
+    for what in ("v", "k", "kv"):
+        q, kn, vn = (x.clone() for x in dev)
+        for u in (2, 10, 20):
+            if "k" in what:
+                kn[:, :, u, 3:9] = bad
+            if "v" in what:
+                vn[:, :, u, 7] = bad
+        for name, o, l in both(plan, c, (q, kn, vn), parent=i32(parent)):
+            assert torch.isfinite(o[:, :, odd]).all()
+            # the path may be another one (the error then as against the oracle), the values are not
+            assert (o[:, :, odd].float() - clean[name][0][:, :, odd].float()).abs().max().item() <= 2 * TOL_O + (2 * HALF[dtype] * 4 if dtype == "bf16" else 0)
+            assert (l[:, :, odd] - clean[name][1][:, :, odd]).abs().max().item() <= 2 * TOL_LSE
+            if bad != bad or "v" in what:
+                assert not torch.isfinite(o[:, :, 20]).all()
+    plan.close()
+
+
+@pytest.mark.parametrize("mode,W,alpha", [("mask", 12, 1.1), ("interp", 30, 0.53), ("interp", 2, 0.5)])
+@pytest.mark.parametrize("kind", ["chain", "random", "roots", "last first"])
+@pytest.mark.parametrize("T,G", [(64, 1), (37, 2), (16, 5)])
+def test_unions_of_keys_that_do_and_do_not_fit(mode, W, alpha, kind, T, G):
+    """Trees of every depth over a base of close distances (several rungs read one row), bf16."""
+    r = rng(21, T, W)
+    lens = [500, 0, 30]
+    c, ref, dev, host, parent, live = tree_case(r, "bf16", lens, 2, G, T, 16, "chain" if kind == "last first" else kind, [T, T - 1, T // 2])
+    if kind == "last first":  # depths 0 .. T/2, then all at once back to the roots
+        parent = np.tile([s - 1 if s <= T // 2 else -1 for s in range(T)], (3, 1))
+    base = [1, 2, 3, 5, 20, 21, 22, 23, 24, 25, 40, 60, 61, 100, 150, 151, 152, 153, 300, 301, 400, 477, 499, 500]
+    N = 700
+    m = fa.FIB_MODE_MASK if mode == "mask" else fa.FIB_MODE_INTERP
+    plan = fa.fib_attn_plan_create(fa.FIB_BASE_CUSTOM, [alpha], W, N, m, custom_base=base)
+    o, lse = sevens(dev[0])
+    fa.fib_attn_tree_decode(plan, 0, c, *dev, parent=i32(parent), n_nodes=i32(live), o=o, lse=lse)
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    if mode == "mask":
+        keys = [(x, 0.0) for x in range(W)] + [(d, 0.0) for d in oracle.mask_distances(base, alpha, W, N)]
+    else:
+        keys = [(x, 0.0) for x in range(W)] + [(lo, float(w)) for _, lo, w in oracle.interp_rungs(base, alpha, W, N)]
+    check(o, lse, *co.tree_attend(ref, 0, *host, parent, live, keys), live, "bf16")
+    # a learned alpha on the device gives the same keys (exact in float32 where alpha is)
+    if alpha == 0.5:
+        o2, l2 = sevens(dev[0])
+        fa.fib_attn_tree_decode(plan, 0, c, *dev, parent=i32(parent), n_nodes=i32(live), o=o2, lse=l2,
+                                alpha_dev=torch.tensor([alpha], device="cuda"))
+        assert torch.equal(o, o2) and torch.equal(lse, l2)
+    plan.close()
+
+
 def test_an_infinite_key_that_is_attended():
     """A cached key whose scores are -inf weighs nothing; the other keys count as without it."""
     r = rng(11)
