@@ -23,29 +23,30 @@ namespace fibattn {
 namespace {
 
 constexpr int kTtThreads = 256, kTtWarps = kTtThreads / 32;
-constexpr int kTtRows = 64;                // query rows of a block
-constexpr int kTtPass = 32;                // ... of a pass between barriers
-constexpr int kTtKeys = 192;               // staged rows, a multiple of 16
-constexpr int kTtStride = kTtKeys + 4;     // 4-byte words of a row of S or P: writes of a fragment meet no bank twice
-constexpr int kTtLow = 64;                 // rows of the drafted keys' lower parts
+constexpr int kTtRows = 8 * kTtWarps;   // query rows of a block: 8 a warp
+constexpr int kTtKeys = 176;            // staged rows, a multiple of 16
+constexpr int kTtStride = kTtKeys + 4;  // 4-byte words of a row of S or P: writes of a fragment meet no bank twice
+constexpr int kTtLow = 64;              // rows of the drafted keys' lower parts
 
 // byte offsets in dynamic shared memory (its base is 128-byte aligned)
 constexpr int kTtK = 0;
 constexpr int kTtV = kTtK + kTtKeys * 128;
 constexpr int kTtLo = kTtV + kTtKeys * 128;
-constexpr int kTtQ = kTtLo + kTtLow * 128;                 // fragments: [8 rows][k-step][lane] hi, hi, lo, lo
-constexpr int kTtS = kTtQ + kTtRows / 8 * 2048;            // [kTtPass][kTtStride]: S, then P as hi | lo << 16
-constexpr int kTtOut = kTtS + kTtPass * kTtStride * 4;     // [kTtPass][72] bf16
-constexpr int kTtKey = kTtOut + kTtPass * 144;             // [kTtPass][keys + 1]: weights by key
-size_t tt_bytes(int keys) { return kTtKey + static_cast<size_t>(kTtPass) * (keys + 1) * 4; }
+constexpr int kTtS = kTtLo + kTtLow * 128;              // [row][kTtStride]: S, then P as hi | lo << 16, then O as bf16
+constexpr int kTtKey = kTtS + kTtRows * kTtStride * 4;  // [row][keys + 1]: weights by key
+size_t tt_bytes(int keys) { return kTtKey + static_cast<size_t>(kTtRows) * (keys + 1) * 4; }
 
 struct TtSmem {
-  KeySmem ks;
-  int depth[kMaxDrafts];
-  uint64_t above[kMaxDrafts];
-  int first[kMaxR + 1], at[kMaxR + 2];  // of the window's run (0) and the rungs': first cached row, place among the staged
-  int by_distance[kMaxDrafts];          // first key that reads the row at a distance
-  int lowest, highest;                  // depths of a step's nodes
+  int4 key[kMaxKeys];  // distance, position it needs, weight of the second row, place (below)
+  union {
+    KeySmem ks;        // as built; again for the row-by-row path
+    int from[kTtKeys];  // of a staged cached row: which of the pools' rows it is
+  };
+  unsigned char line[kMaxDrafts][kMaxDrafts];  // [s][d]: the ancestor d levels above node s
+  unsigned char depth[kMaxDrafts];
+  unsigned char by_distance[kMaxDrafts];       // first key that reads the row at a distance
+  int first[kMaxR + 1], at[kMaxR + 2];         // of the window's run (0) and the rungs': first cached row, place among the staged
+  int step;
 };
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
@@ -78,7 +79,7 @@ __device__ __forceinline__ bool not_finite(const uint4& x) { return not_finite(x
 
 __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_constant__ TreeArgs a, int blocks_per_head, int key_stride) {
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ TtSmem ts;
+  __shared__ __align__(16) TtSmem ts;
   const int head = blockIdx.x / blocks_per_head, b = head / a.H, h = head % a.H;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
   build_keys(a.t, a.N, &ts.ks);
@@ -97,90 +98,55 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     if (tid == 0) atomicExch(a.status, kStatusDeviceAssert);
     return;
   }
-  if (warp == 0)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      ts.depth[lane + 32 * i] = tree.depth[i];
-      ts.above[lane + 32 * i] = tree.above[i];
+  if (warp < 2) {  // node `tid`
+    ts.depth[tid] = static_cast<unsigned char>(tree.depth[warp]);
+    if (tid < n) {
+      uint64_t left = tree.above[warp];
+      for (int d = 0; left != 0; ++d) {
+        const int u = 63 - __clzll(static_cast<long long>(left));
+        ts.line[tid][d] = static_cast<unsigned char>(u);
+        left &= ~(1ull << u);
+      }
     }
+  }
   __syncthreads();
   const int W = a.t.W, nr = ts.ks.nr, nv = ts.ks.nv, drafts = (n + 15) & ~15;
-  const __nv_bfloat16* kc = static_cast<const __nv_bfloat16*>(a.kc);
-  const __nv_bfloat16* vc = static_cast<const __nv_bfloat16*>(a.vc);
+  if (tid < nv) ts.key[tid] = make_int4(ts.ks.lo[tid], ts.ks.need[tid], __float_as_int(ts.ks.w[tid]), 0);
+  __syncthreads();
   const uint32_t base = smem_addr(smem);
-  float* s_key = reinterpret_cast<float*>(smem + kTtKey);
   bool bad = false;  // something staged is not finite
 
-  // ---- query fragments of all rows: lane (g, t) of warp w the row 8 w + g
-  if (8 * warp < rows) {
-    const int r = 8 * warp + g;
-    uint4* at = reinterpret_cast<uint4*>(smem + kTtQ) + warp * 128 + lane;
-    if (r < rows) {
-      const int hq = (r0 + r) / n, s = (r0 + r) - hq * n, pos = len + ts.depth[s];
-      const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) +
-                                                            ((static_cast<size_t>(b) * a.Hq + h * a.G + hq) * a.T + s) * kD);
-      uint32_t qh[4][2], ql[4][2];
+  // ---- on their way while the runs are planned: the query's words of row 8 warp + g, and a drafted row's 16 dims
+  const int qr = 8 * warp + g;
+  const int q_head = qr < rows ? (r0 + qr) / n : 0, q_node = qr < rows ? (r0 + qr) - q_head * n : 0;
+  const size_t q_row = (static_cast<size_t>(b) * a.Hq + h * a.G + q_head) * a.T + q_node;
+  const int depth = ts.depth[q_node], pos = len + depth;  // of this lane's row, here and below
+  uint32_t qx[2][2], qy[2][2];
+  {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + q_row * kD) + t;
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
+    for (int k = 0; k < 2; ++k)
 #pragma unroll
-        for (int f = 0; f < 2; ++f) {
-          const int d = 16 * k + 8 * f + 2 * t;
-          const uint32_t x = __ldg(q + d / 2), y = __ldg(q + d / 2 + kFreq / 2);
-          const float2 e0 = rope_factor(a.rope_lo, a.rope_hi, pos, d), e1 = rope_factor(a.rope_lo, a.rope_hi, pos, d + 1);
-          const float sc = kLog2e / 8.0f;
-          const float x0 = bf_lo(x) * sc, x1 = bf_hi(x) * sc, y0 = bf_lo(y) * sc, y1 = bf_hi(y) * sc;
-          split2(x0 * e0.x - y0 * e0.y, x1 * e1.x - y1 * e1.y, qh[k][f], ql[k][f]);
-          split2(x0 * e0.y + y0 * e0.x, x1 * e1.y + y1 * e1.x, qh[k + 2][f], ql[k + 2][f]);
-        }
-#pragma unroll
-      for (int k = 0; k < 4; ++k) at[32 * k] = make_uint4(qh[k][0], qh[k][1], ql[k][0], ql[k][1]);
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) at[32 * k] = make_uint4(0, 0, 0, 0);
-    }
-  }
-  // ---- drafted rows: K rotated, hi in the K tile and lo apart; a quad a row, zeros behind the last
-  for (int u = tid >> 2; u < drafts; u += kTtThreads / 4) {
-    uint32_t hi[8], lo[8];
-    uint4 v[2];
-    if (u < n) {
-      const size_t from = ((static_cast<size_t>(b) * a.H + h) * a.T + u) * kD;
-      float x[16];
-      float2 e[8];
-      load_part(static_cast<const __nv_bfloat16*>(a.kn) + from, t, x);
-      const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.vn) + from);
-      v[0] = __ldg(vr + t);
-      v[1] = __ldg(vr + t + 4);
-      rope_row(a.rope_lo, a.rope_hi, len + ts.depth[u], t, e);
-      rotate_part(x, e, false);
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        split2(x[2 * w], x[2 * w + 1], hi[w], lo[w]);
-        bad |= not_finite(hi[w]);
+      for (int f = 0; f < 2; ++f) {
+        qx[k][f] = __ldg(q + 8 * k + 4 * f);
+        qy[k][f] = __ldg(q + 8 * k + 4 * f + kFreq / 2);
       }
-      bad |= not_finite(v[0]) | not_finite(v[1]);
-    } else {
-      v[0] = v[1] = make_uint4(0, 0, 0, 0);
-#pragma unroll
-      for (int w = 0; w < 8; ++w) hi[w] = lo[w] = 0;
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int at = u * 128 + (((t + 4 * x) ^ (u & 7)) << 4);
-      *reinterpret_cast<uint4*>(smem + kTtK + at) = make_uint4(hi[4 * x], hi[4 * x + 1], hi[4 * x + 2], hi[4 * x + 3]);
-      *reinterpret_cast<uint4*>(smem + kTtLo + at) = make_uint4(lo[4 * x], lo[4 * x + 1], lo[4 * x + 2], lo[4 * x + 3]);
-      *reinterpret_cast<uint4*>(smem + kTtV + at) = v[x];
-    }
   }
-  // ---- the first key that reads the row at distance d: keys are in the order of lo, and read lo and lo + 1
-  if (tid < kMaxDrafts) {
-    int c = 0;
-    while (c < nv && ts.ks.lo[c] + 1 < tid) ++c;
-    ts.by_distance[tid] = c;
+  const int du = tid >> 2;  // 64 quads: every drafted row at once
+  uint4 dk[2], dv[2];
+  dk[0] = dk[1] = dv[0] = dv[1] = make_uint4(0, 0, 0, 0);
+  if (du < n) {
+    const size_t at = ((static_cast<size_t>(b) * a.H + h) * a.T + du) * kD;
+    const uint4* kr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kn) + at);
+    const uint4* vr = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.vn) + at);
+    dk[0] = __ldg(kr + t);
+    dk[1] = __ldg(kr + t + 4);
+    dv[0] = __ldg(vr + t);
+    dv[1] = __ldg(vr + t + 4);
   }
 
-  // The union of the cached rows of `step` query rows from `from` on: its runs' places (thread c < nr + 1 of warp 0 holds
-  // run c); the number of staged rows.  By warp 0.
+  // The union of the cached rows of `step` query rows from `from` on: its runs' places; returns the number of staged
+  // rows.  By warp 0: lane c has run c (0: the window, c: rung c - 1).
   auto plan_runs = [&](int from, int step) {
     int lowest = 64, highest = 0;
     for (int r = from + lane; r < min(from + step, rows); r += 32) {
@@ -191,14 +157,15 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     lowest = __reduce_min_sync(0xffffffffu, lowest);
     highest = __reduce_max_sync(0xffffffffu, highest);
     int total = drafts;
-    for (int c0 = 0; c0 <= nr; c0 += 32) {  // run 0: the window; run c: rung c - 1
+    for (int c0 = 0; c0 <= nr; c0 += 32) {
       const int c = c0 + lane;
       int first = 0, count = 0;
       if (c == 0) {
         first = max(0, len + lowest - (W - 1));
         count = max(0, len - first);
       } else if (c <= nr) {
-        const int lo = ts.ks.lo[W + c - 1], two = ts.ks.w[W + c - 1] > 0.f ? 1 : 0;
+        const int4 k = ts.key[W + c - 1];
+        const int lo = k.x, two = __int_as_float(k.z) > 0.f ? 1 : 0;
         first = max(0, len + lowest - lo - two);
         count = max(0, min(len - 1, len + highest - lo) - first + 1);
       }
@@ -217,19 +184,69 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     if (lane == 0) ts.at[nr + 1] = total;
     return total;
   };
-  // The most rows at a time whose union fits
-  __shared__ int s_step;
-  if (warp == 0) {
+  if (warp == 0) {  // the most rows at a time whose union fits
     int step = kTtRows;
     for (; step >= 8; step >>= 1) {
       bool fits = true;
       for (int from = 0; from < rows && fits; from += step) fits = plan_runs(from, step) <= kTtKeys;
       if (fits) break;
     }
-    if (lane == 0) s_step = step;
+    if (lane == 0) ts.step = step;
+  } else if (warp < 3) {  // the first key that reads the row at distance d: keys are in the order of lo, and read lo and lo + 1
+    const int d = tid - 32;
+    int c = 0, end = nv;
+    while (c < end) {
+      const int mid = (c + end) >> 1;
+      if (ts.key[mid].x + 1 < d)
+        c = mid + 1;
+      else
+        end = mid;
+    }
+    ts.by_distance[d] = static_cast<unsigned char>(c);
+  }
+
+  // ---- query fragments (hi, lo) of the warp's 8 rows, in registers
+  uint32_t qh[4][2], ql[4][2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int f = 0; f < 2; ++f) {
+      const int d = 16 * k + 8 * f + 2 * t;
+      const float2 e0 = rope_factor(a.rope_lo, a.rope_hi, pos, d), e1 = rope_factor(a.rope_lo, a.rope_hi, pos, d + 1);
+      const float sc = kLog2e / 8.0f;
+      const float x0 = bf_lo(qx[k][f]) * sc, x1 = bf_hi(qx[k][f]) * sc, y0 = bf_lo(qy[k][f]) * sc, y1 = bf_hi(qy[k][f]) * sc;
+      split2(x0 * e0.x - y0 * e0.y, x1 * e1.x - y1 * e1.y, qh[k][f], ql[k][f]);
+      split2(x0 * e0.y + y0 * e0.x, x1 * e1.y + y1 * e1.x, qh[k + 2][f], ql[k + 2][f]);
+    }
+  // ---- drafted rows: K rotated, hi in the K tile and lo apart; zeros behind the last
+  if (du < drafts) {
+    uint32_t hi[8], lo[8];
+    float x[16];
+    float2 e[8];
+    const uint32_t w[8] = {dk[0].x, dk[0].y, dk[0].z, dk[0].w, dk[1].x, dk[1].y, dk[1].z, dk[1].w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      x[2 * i] = bf_lo(w[i]);
+      x[2 * i + 1] = bf_hi(w[i]);
+    }
+    rope_row(a.rope_lo, a.rope_hi, du < n ? len + ts.depth[du] : 0, t, e);
+    rotate_part(x, e, false);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      split2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
+      bad |= not_finite(hi[i]);
+    }
+    bad |= not_finite(dv[0]) | not_finite(dv[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int at = du * 128 + (((t + 4 * i) ^ (du & 7)) << 4);
+      *reinterpret_cast<uint4*>(smem + kTtK + at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+      *reinterpret_cast<uint4*>(smem + kTtLo + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+      *reinterpret_cast<uint4*>(smem + kTtV + at) = dv[i];
+    }
   }
   __syncthreads();
-  const int step = s_step;
+  const int step = ts.step;
 
   int from = 0;
   for (; from < rows && step >= 8; from += step) {
@@ -239,172 +256,178 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
       __syncthreads();
     }
     const int total = ts.at[nr + 1], padded = (total + 15) & ~15;
-    // ---- the cached rows, eight 16-byte words of K and of V each
-    for (int i = drafts * 8 + tid; i < padded * 8; i += kTtThreads) {
-      const int x = i >> 3, ch = i & 7;
-      uint4 k = make_uint4(0, 0, 0, 0), v = k;
-      if (x < total) {
-        int c = 0;  // its run
-        while (ts.at[c + 1] <= x) ++c;
-        long long at = cache_row(a, b, h, ts.first[c] + x - ts.at[c]);
-        if (at < 0) {
-          atomicExch(a.status, kStatusDeviceAssert);
-          at = 0;
-        }
-        k = __ldg(reinterpret_cast<const uint4*>(kc + at) + ch);
-        v = __ldg(reinterpret_cast<const uint4*>(vc + at) + ch);
-        bad |= not_finite(k) | not_finite(v);
+    // ---- where the staged rows lie; the keys as the rows below read them: at position p, key c's row lies at place + p
+    // among the staged (its second one in front of that)
+    if (tid >= drafts && tid < total) {
+      int c = 0, end = nr + 1;  // the run: at[c] <= tid < at[c + 1]
+      while (end - c > 1) {
+        const int mid = (c + end) >> 1;
+        if (ts.at[mid] <= tid)
+          c = mid;
+        else
+          end = mid;
       }
-      const int to = x * 128 + ((ch ^ (x & 7)) << 4);
-      *reinterpret_cast<uint4*>(smem + kTtK + to) = k;
-      *reinterpret_cast<uint4*>(smem + kTtV + to) = v;
+      long long at = cache_row(a, b, h, ts.first[c] + tid - ts.at[c]);
+      if (at < 0) {
+        atomicExch(a.status, kStatusDeviceAssert);
+        at = 0;
+      }
+      ts.from[tid] = static_cast<int>(at / kD);
+    }
+    if (tid < nv) {
+      const int run = tid < W ? 0 : tid - W + 1;
+      ts.key[tid].w = ts.at[run] - ts.first[run] - ts.key[tid].x;
+    }
+    __syncthreads();
+    // ---- the cached rows, all on their way at once
+    {
+      constexpr int kMost = kTtKeys * 8 / kTtThreads + 1;
+      uint4 k[kMost], v[kMost];
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {
+        const int i = (drafts + j * (kTtThreads / 8)) * 8 + tid, x = i >> 3, ch = i & 7;
+        k[j] = v[j] = make_uint4(0, 0, 0, 0);
+        if (x < total) {
+          const size_t at = static_cast<size_t>(ts.from[x]) * kD;
+          k[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kc) + at) + ch);
+          v[j] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.vc) + at) + ch);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kMost; ++j) {
+        const int i = (drafts + j * (kTtThreads / 8)) * 8 + tid, x = i >> 3, ch = i & 7;
+        bad |= not_finite(k[j]) | not_finite(v[j]);
+        if (x < padded) {
+          const int to = x * 128 + ((ch ^ (x & 7)) << 4);
+          *reinterpret_cast<uint4*>(smem + kTtK + to) = k[j];
+          *reinterpret_cast<uint4*>(smem + kTtV + to) = v[j];
+        }
+      }
     }
     if (__syncthreads_or(bad)) break;  // the rows from here on one by one
 
-    for (int p0 = from; p0 < min(from + step, rows); p0 += kTtPass) {
-      const int p1 = min(min(p0 + kTtPass, from + step), rows);  // a pass: rows [p0, p1)
-      const int tiles = (p1 - p0 + 7) >> 3, mi = lane >> 3, rl = lane & 7;
-      uint32_t* S = reinterpret_cast<uint32_t*>(smem + kTtS);
-      // ---- scores: an item is 16 keys against 16 query rows
-      for (int item = warp; item < padded / 16 * 2; item += kTtWarps) {
-        const int x0 = (item >> 1) * 16, n0 = (item & 1) * 2;
-        if (n0 >= tiles) continue;
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const uint32_t row = (x0 + (mi & 1) * 8 + rl) * 128;
-        const uint4* qs = reinterpret_cast<const uint4*>(smem + kTtQ) + ((p0 >> 3) + n0) * 128 + lane;
+    // ---- 8 query rows a warp, without a further barrier
+    if (8 * warp >= from && 8 * warp < min(from + step, rows)) {
+      const int mi = lane >> 3, rl = lane & 7;
+      uint32_t* S = reinterpret_cast<uint32_t*>(smem + kTtS) + 8 * warp * kTtStride;
+#pragma unroll 2
+      for (int x0 = 0; x0 < padded; x0 += 16) {
+        float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+        const uint32_t row = base + kTtK + (x0 + (mi & 1) * 8 + rl) * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t ka[4];
           const uint32_t word = ((2 * k + (mi >> 1)) ^ rl) << 4;
-          ldsm4(ka, base + kTtK + row + word);
-          const uint4 q0 = qs[32 * k], q1 = qs[128 + 32 * k];  // (tiles behind the last are not used)
-          mma16(c[0], ka, q0.x, q0.y);
-          mma16(c[1], ka, q1.x, q1.y);
-          mma16(d[0], ka, q0.z, q0.w);
-          mma16(d[1], ka, q1.z, q1.w);
+          ldsm4(ka, row + word);
+          mma16(c, ka, qh[k][0], qh[k][1]);
+          mma16(d, ka, ql[k][0], ql[k][1]);
           if (x0 < drafts) {
-            ldsm4(ka, base + kTtLo + row + word);
-            mma16(d[0], ka, q0.x, q0.y);
-            mma16(d[1], ka, q1.x, q1.y);
+            ldsm4(ka, row + (kTtLo - kTtK) + word);
+            mma16(d, ka, qh[k][0], qh[k][1]);
           }
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            S[(8 * (n0 + j) + 2 * t + (e & 1)) * kTtStride + x0 + g + 8 * (e >> 1)] = __float_as_uint(c[j][e] + d[j][e]);
+        for (int e = 0; e < 4; ++e) S[(2 * t + (e & 1)) * kTtStride + x0 + g + 8 * (e >> 1)] = __float_as_uint(c[e] + d[e]);
       }
-      __syncthreads();
-      // ---- weights: 8 lanes a row
-      {
-        const int pr = tid >> 3, l8 = tid & 7, r = p0 + pr;
-        const bool in = r < p1;
-        const int hq = in ? (r0 + r) / n : 0, s = in ? (r0 + r) - hq * n : 0, depth = ts.depth[s], pos = len + depth;
-        uint32_t* row = S + pr * kTtStride;
-        // where the row at distance dist lies among the staged, read by key c
-        auto place = [&](int c, int dist) {
-          if (dist <= depth) return ancestor_at(ts.above[s], dist);
-          const int run = c < W ? 0 : c - W + 1;
-          return ts.at[run] + pos - dist - ts.first[run];
-        };
-        float sc[kMaxKeys / 8], m = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < kMaxKeys / 8; ++j) {
-          const int c = 8 * j + l8;
-          sc[j] = -INFINITY;
-          if (8 * j >= nv) continue;  // (uniform, as below)
-          if (in && c < nv && pos >= ts.ks.need[c]) {
-            const int lo = ts.ks.lo[c];
-            const float w = ts.ks.w[c];
-            sc[j] = __uint_as_float(row[place(c, lo)]);
-            if (w > 0.f) sc[j] = (1.f - w) * sc[j] + w * __uint_as_float(row[place(c, lo + 1)]);
-          }
-          m = fmaxf(m, sc[j]);
+      __syncwarp();
+      // weights: 4 lanes a row (this lane's: g), keys t, t + 4, ...
+      const bool in = qr < rows;
+      uint32_t* row = S + g * kTtStride;
+      float* key = reinterpret_cast<float*>(smem + kTtKey) + qr * key_stride;
+      const unsigned char* line = ts.line[q_node];
+      float m = -INFINITY;
+      for (int c = t; c < nv; c += 4) {  // scores by key
+        const int4 kk = ts.key[c];
+        float s = -INFINITY;
+        if (in && pos >= kk.y) {
+          const float w = __int_as_float(kk.z);
+          s = __uint_as_float(row[kk.x <= depth ? line[kk.x] : kk.w + pos]);
+          if (w > 0.f) s = (1.f - w) * s + w * __uint_as_float(row[kk.x < depth ? line[kk.x + 1] : kk.w + pos - 1]);
         }
-#pragma unroll
-        for (int x = 1; x < 8; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-        float l = 0.f;
-#pragma unroll
-        for (int j = 0; j < kMaxKeys / 8; ++j) {
-          if (8 * j >= nv) break;
-          sc[j] = exp2f(sc[j] - m);  // (a row has its own key at least; of a row that is none, NaN that nobody reads)
-          l += sc[j];
-        }
-#pragma unroll
-        for (int x = 1; x < 8; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-        const float inv = 1.f / l;
-        __syncwarp();
-        for (int x = l8; x < padded / 4; x += 8) reinterpret_cast<uint4*>(row)[x] = make_uint4(0, 0, 0, 0);
-        __syncwarp();
-        float* key = s_key + pr * key_stride;
-#pragma unroll
-        for (int j = 0; j < kMaxKeys / 8; ++j) {
-          if (8 * j >= nv) break;
-          const int c = 8 * j + l8;
-          if (in && c < nv) {
-            const bool on = pos >= ts.ks.need[c];
-            const float p = on ? sc[j] * inv : 0.f, w = ts.ks.w[c];
-            const int lo = ts.ks.lo[c];
-            key[c] = p;
-            // a cached row of a run is this key's alone
-            if (on && lo > depth) row[place(c, lo)] = split1(p * (1.f - w));
-            if (on && w > 0.f && lo + 1 > depth) row[place(c, lo + 1)] = split1(p * w);
-          }
-        }
-        __syncwarp();
-        // a drafted row may be several keys': their sum in the order of the keys
-        if (in)
-          for (int d = l8; d <= depth; d += 8) {
-            float x = 0.f;
-            for (int c = ts.by_distance[d]; c < nv && ts.ks.lo[c] <= d; ++c) {
-              const float w = ts.ks.w[c];
-              x += key[c] * (ts.ks.lo[c] == d ? 1.f - w : w);
-            }
-            row[ancestor_at(ts.above[s], d)] = split1(x);
-          }
-        if (in && l8 == 0 && a.lse != nullptr)
-          a.lse[(static_cast<size_t>(b) * a.Hq + h * a.G + hq) * a.T + s] = (m + log2f(l)) * kLn2;
+        key[c] = s;
+        m = fmaxf(m, s);
       }
-      __syncthreads();
-      // ---- O^T = V^T P^T: warp w the dims 16 (w % 4) .. and the query rows 16 (w / 4) ..
-      {
-        const int d0 = 16 * (warp & 3), n0 = (warp >> 2) * 2;
-        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        if (n0 < tiles) {
-          for (int x0 = 0; x0 < padded; x0 += 16) {
-            uint32_t va[4];
-            ldsm4_t(va, base + kTtV + (x0 + (mi >> 1) * 8 + rl) * 128 + (((d0 / 8 + (mi & 1)) ^ rl) << 4));
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t* row = S + (8 * (n0 + j) + g) * kTtStride + x0 + 2 * t;
-              const uint2 p = *reinterpret_cast<const uint2*>(row), q = *reinterpret_cast<const uint2*>(row + 8);
-              mma16(c[j], va, __byte_perm(p.x, p.y, 0x5410), __byte_perm(q.x, q.y, 0x5410));
-              mma16(d[j], va, __byte_perm(p.x, p.y, 0x7632), __byte_perm(q.x, q.y, 0x7632));
-            }
-          }
-          __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(smem + kTtOut);
-#pragma unroll
-          for (int j = 0; j < 2; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              out[(8 * (n0 + j) + 2 * t + (e & 1)) * 72 + d0 + g + 8 * (e >> 1)] = __float2bfloat16_rn(c[j][e] + d[j][e]);
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+      __syncwarp();
+      for (int x = t; x < padded / 4; x += 4) reinterpret_cast<uint4*>(row)[x] = make_uint4(0, 0, 0, 0);
+      __syncwarp();
+      float l = 0.f;
+      for (int c = t; c < nv; c += 4) {
+        const int4 kk = ts.key[c];
+        const float p = exp2f(key[c] - m), w = __int_as_float(kk.z);  // (of a row that is none NaN, which nobody reads)
+        key[c] = p;
+        l += p;
+        // a cached row of a run is this key's alone
+        if (in && pos >= kk.y) {
+          if (kk.x > depth) row[kk.w + pos] = split1(p * (1.f - w));
+          if (w > 0.f && kk.x >= depth) row[kk.w + pos - 1] = split1(p * w);
         }
       }
-      __syncthreads();
-      {
-        const int pr = tid >> 3, ch = tid & 7, r = p0 + pr;
-        if (r < p1) {
-          const int hq = (r0 + r) / n, s = (r0 + r) - hq * n;
-          reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + ((static_cast<size_t>(b) * a.Hq + h * a.G + hq) * a.T + s) * kD)[ch] =
-              *reinterpret_cast<const uint4*>(smem + kTtOut + pr * 144 + ch * 16);
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      __syncwarp();
+      // a drafted row may be several keys': their sum in the order of the keys
+      if (in)
+        for (int d = t; d <= depth; d += 4) {
+          float x = 0.f;
+          for (int c = ts.by_distance[d]; c < nv; ++c) {
+            const int4 kk = ts.key[c];
+            if (kk.x > d) break;
+            const float w = __int_as_float(kk.z);
+            x += key[c] * (kk.x == d ? 1.f - w : w);
+          }
+          row[line[d]] = split1(x);
         }
+      const float inv = 1.f / l;
+      if (in && t == 0 && a.lse != nullptr) a.lse[q_row] = (m + log2f(l)) * kLn2;
+      __syncwarp();
+      // O^T = V^T P^T, 16 dims at a time
+      float c[4][4], d[4][4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) c[x][e] = d[x][e] = 0.f;
+#pragma unroll 2
+      for (int x0 = 0; x0 < padded; x0 += 16) {
+        const uint2 p = *reinterpret_cast<const uint2*>(row + x0 + 2 * t), q = *reinterpret_cast<const uint2*>(row + x0 + 2 * t + 8);
+        const uint32_t h0 = __byte_perm(p.x, p.y, 0x5410), h1 = __byte_perm(q.x, q.y, 0x5410);
+        const uint32_t l0 = __byte_perm(p.x, p.y, 0x7632), l1 = __byte_perm(q.x, q.y, 0x7632);
+        const uint32_t vr = base + kTtV + (x0 + (mi >> 1) * 8 + rl) * 128;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          uint32_t va[4];
+          ldsm4_t(va, vr + (((2 * x + (mi & 1)) ^ rl) << 4));
+          mma16(c[x], va, h0, h1);
+          mma16(d[x], va, l0, l1);
+        }
+      }
+      __syncwarp();
+      // rows 2t, 2t + 1 of the fragments; their 1 / l from the lanes that have them
+      __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(S);
+      const float inv0 = __shfl_sync(0xffffffffu, inv, 8 * t), inv1 = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          out[(2 * t + (e & 1)) * 72 + 16 * x + g + 8 * (e >> 1)] = __float2bfloat16_rn((c[x][e] + d[x][e]) * (e & 1 ? inv1 : inv0));
+      __syncwarp();
+      if (in) {
+        uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + q_row * kD);
+        to[t] = *reinterpret_cast<const uint4*>(out + g * 72 + 8 * t);
+        to[t + 4] = *reinterpret_cast<const uint4*>(out + g * 72 + 8 * t + 32);
       }
     }
   }
+  if (from >= rows) return;
   // ---- what is left, row by row
+  __syncthreads();
+  build_keys(a.t, a.N, &ts.ks);
+  const WarpTree again = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(b) * a.T, n, &ok);
+  __syncthreads();
   for (int r = from + warp; r < rows; r += kTtWarps) {
-    const int hq = (r0 + r) / n, s = (r0 + r) - hq * n, depth = ts.depth[s];
-    attend_row<__nv_bfloat16, 1>(a, &ts.ks, b, h, (static_cast<size_t>(b) * a.Hq + h * a.G + hq) * a.T + s, depth, len + depth, ts.above[s], 0,
+    const int hq = (r0 + r) / n, s = (r0 + r) - hq * n, d = pick32(again.depth, s);
+    attend_row<__nv_bfloat16, 1>(a, &ts.ks, b, h, (static_cast<size_t>(b) * a.Hq + h * a.G + hq) * a.T + s, d, len + d, pick64(again.above, s), 0,
                                  nullptr);
   }
 }
