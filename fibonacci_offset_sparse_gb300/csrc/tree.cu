@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(32 * kTreeWarps) tree_kernel(const __grid_cons
   const int r = (blockIdx.x % blocks_per_head) * (kTreeWarps / PER) + (PER == 1 ? warp : 0);
   if (r >= n * a.G) return;  // (of the whole block where four warps share a row)
   const int g = r / n, s = r - g * n;
-  const WarpTree tree = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(b) * a.T, n, &ok);
+  const WarpTree tree = warp_tree(a, b, n, &ok);
   const int depth = pick32(tree.depth, s), pos = len + depth;
   const uint64_t above = pick64(tree.above, s);
   if (pos >= a.N) ok = false;

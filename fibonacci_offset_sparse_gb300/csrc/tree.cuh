@@ -26,7 +26,7 @@ __device__ __forceinline__ int pick32(const int (&x)[2], int s) {
 // rounds a node knows those up to 2^i levels above it.  *ok turns false (in every lane) where a
 // parent is out of its range; the nodes are then taken as roots, so that nothing is read out
 // of bounds.
-__device__ __forceinline__ WarpTree warp_tree(const int32_t* parent, int n, bool* ok) {
+__device__ __forceinline__ WarpTree warp_tree(const TreeArgs& a, int b, int n, bool* ok) {
   const int lane = threadIdx.x & 31;
   WarpTree t;
   int up[2];
@@ -34,15 +34,19 @@ __device__ __forceinline__ WarpTree warp_tree(const int32_t* parent, int n, bool
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
     const int s = lane + 32 * i;
-    up[i] = -1;
-    if (s < n) {
-      up[i] = parent == nullptr ? s - 1 : parent[s];
-      if (up[i] < -1 || up[i] >= s) {
-        bad = true;
-        up[i] = -1;
-      }
-    }
+    up[i] = s - 1;  // (the row of parents is read whole, so that the load does not wait for n)
+    if (a.parent != nullptr && s < a.T) up[i] = a.parent[static_cast<size_t>(b) * a.T + s];
     t.above[i] = 1ull << s;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int s = lane + 32 * i;
+    if (s >= n) {
+      up[i] = -1;
+    } else if (up[i] < -1 || up[i] >= s) {
+      bad = true;
+      up[i] = -1;
+    }
   }
   if (__any_sync(0xffffffffu, bad)) {
     *ok = false;

@@ -581,7 +581,7 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
     const bool tail = k.last == k.units, whole = tail && k.first == 0;
     const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);  // row r0 + i is (query head, node)
     bool ok = true;
-    const WarpTree tree = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(k.b) * a.T, k.n, &ok);
+    const WarpTree tree = warp_tree(a, k.b, k.n, &ok);
     uint4* qs = reinterpret_cast<uint4*>(smem + S::kQuery + tile * C::kQueryBytes);
     for (int i = grp; i < C::kLoads; i += GROUPS) {
       const int r = C::kRows * tile + C::load_row(i);

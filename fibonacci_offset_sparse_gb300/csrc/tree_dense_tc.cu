@@ -367,7 +367,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0), k_first = k.first, k_last = k.last, k_len = k.len;
       const int mine = min(GR, max(0, rows - g0));  // rows of this group
       bool ok = true;
-      const WarpTree tree = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(k.b) * a.T, k.n, &ok);
+      const WarpTree tree = warp_tree(a, k.b, k.n, &ok);
       // the rotated query: a quad a row, 16 bytes of hi and of lo for 8 dims
       for (int r = tid >> 2; r < ROWS; r += CONS / 4) {
         const int t = lane & 3;

@@ -26,6 +26,7 @@ constexpr int kTtThreads = 256, kTtWarps = kTtThreads / 32;
 constexpr int kTtRows = 8 * kTtWarps;   // query rows of a block: 8 a warp
 constexpr int kTtKeys = 176;            // staged rows, a multiple of 16
 constexpr int kTtStride = kTtKeys + 4;  // 4-byte words of a row of S or P: writes of a fragment meet no bank twice
+constexpr int kTtLeast = 32;            // query rows at a time, at least: fewer leave most warps idle
 constexpr int kTtLow = 64;              // rows of the drafted keys' lower parts
 
 // byte offsets in dynamic shared memory (its base is 128-byte aligned)
@@ -91,7 +92,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
   }
   const int r0 = (blockIdx.x % blocks_per_head) * kTtRows, rows = min(kTtRows, n * a.G - r0);
   if (rows <= 0) return;
-  const WarpTree tree = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(b) * a.T, n, &ok);
+  const WarpTree tree = warp_tree(a, b, n, &ok);
   const int deepest = __reduce_max_sync(0xffffffffu, max(lane < n ? tree.depth[0] : 0, lane + 32 < n ? tree.depth[1] : 0));
   if (static_cast<long long>(len) + deepest >= a.N) ok = false;
   if (!ok) {  // (the same in all warps)
@@ -186,7 +187,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
   };
   if (warp == 0) {  // the most rows at a time whose union fits
     int step = kTtRows;
-    for (; step >= 8; step >>= 1) {
+    for (; step >= kTtLeast; step >>= 1) {
       bool fits = true;
       for (int from = 0; from < rows && fits; from += step) fits = plan_runs(from, step) <= kTtKeys;
       if (fits) break;
@@ -249,7 +250,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
   const int step = ts.step;
 
   int from = 0;
-  for (; from < rows && step >= 8; from += step) {
+  for (; from < rows && step >= kTtLeast; from += step) {
     if (step < rows) {  // (else the plan of the only step stands)
       __syncthreads();
       if (warp == 0) plan_runs(from, step);
@@ -312,22 +313,27 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
       uint32_t* S = reinterpret_cast<uint32_t*>(smem + kTtS) + 8 * warp * kTtStride;
 #pragma unroll 2
       for (int x0 = 0; x0 < padded; x0 += 16) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f}, d[4] = {0.f, 0.f, 0.f, 0.f};
+        float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
         const uint32_t row = base + kTtK + (x0 + (mi & 1) * 8 + rl) * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t ka[4];
           const uint32_t word = ((2 * k + (mi >> 1)) ^ rl) << 4;
           ldsm4(ka, row + word);
-          mma16(c, ka, qh[k][0], qh[k][1]);
-          mma16(d, ka, ql[k][0], ql[k][1]);
-          if (x0 < drafts) {
-            ldsm4(ka, row + (kTtLo - kTtK) + word);
-            mma16(d, ka, qh[k][0], qh[k][1]);
+          mma16(c[k & 1], ka, qh[k][0], qh[k][1]);
+          mma16(d[k & 1], ka, ql[k][0], ql[k][1]);
+        }
+        if (x0 < drafts) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            uint32_t ka[4];
+            ldsm4(ka, row + (kTtLo - kTtK) + (((2 * k + (mi >> 1)) ^ rl) << 4));
+            mma16(d[k & 1], ka, qh[k][0], qh[k][1]);
           }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) S[(2 * t + (e & 1)) * kTtStride + x0 + g + 8 * (e >> 1)] = __float_as_uint(c[e] + d[e]);
+        for (int e = 0; e < 4; ++e)
+          S[(2 * t + (e & 1)) * kTtStride + x0 + g + 8 * (e >> 1)] = __float_as_uint((c[0][e] + c[1][e]) + (d[0][e] + d[1][e]));
       }
       __syncwarp();
       // weights: 4 lanes a row (this lane's: g), keys t, t + 4, ...
@@ -336,16 +342,22 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
       float* key = reinterpret_cast<float*>(smem + kTtKey) + qr * key_stride;
       const unsigned char* line = ts.line[q_node];
       float m = -INFINITY;
-      for (int c = t; c < nv; c += 4) {  // scores by key
-        const int4 kk = ts.key[c];
-        float s = -INFINITY;
-        if (in && pos >= kk.y) {
-          const float w = __int_as_float(kk.z);
-          s = __uint_as_float(row[kk.x <= depth ? line[kk.x] : kk.w + pos]);
-          if (w > 0.f) s = (1.f - w) * s + w * __uint_as_float(row[kk.x < depth ? line[kk.x + 1] : kk.w + pos - 1]);
+      for (int c0 = t; c0 < nv; c0 += 16) {  // scores by key, four at a time: every read before a write
+        float x[4], y[4], w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int4 kk = ts.key[min(c0 + 4 * j, nv - 1)];
+          const bool on = in && c0 + 4 * j < nv && pos >= kk.y;
+          w[j] = on ? __int_as_float(kk.z) : 0.f;
+          x[j] = on ? __uint_as_float(row[kk.x <= depth ? line[kk.x] : kk.w + pos]) : -INFINITY;
+          y[j] = w[j] > 0.f ? __uint_as_float(row[kk.x < depth ? line[kk.x + 1] : kk.w + pos - 1]) : 0.f;
         }
-        key[c] = s;
-        m = fmaxf(m, s);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (w[j] > 0.f) x[j] = (1.f - w[j]) * x[j] + w[j] * y[j];
+          if (c0 + 4 * j < nv) key[c0 + 4 * j] = x[j];
+          m = fmaxf(m, x[j]);
+        }
       }
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
@@ -353,15 +365,25 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
       for (int x = t; x < padded / 4; x += 4) reinterpret_cast<uint4*>(row)[x] = make_uint4(0, 0, 0, 0);
       __syncwarp();
       float l = 0.f;
-      for (int c = t; c < nv; c += 4) {
-        const int4 kk = ts.key[c];
-        const float p = exp2f(key[c] - m), w = __int_as_float(kk.z);  // (of a row that is none NaN, which nobody reads)
-        key[c] = p;
-        l += p;
-        // a cached row of a run is this key's alone
-        if (in && pos >= kk.y) {
-          if (kk.x > depth) row[kk.w + pos] = split1(p * (1.f - w));
-          if (w > 0.f && kk.x >= depth) row[kk.w + pos - 1] = split1(p * w);
+      for (int c0 = t; c0 < nv; c0 += 16) {
+        float p[4];
+        int4 kk[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          kk[j] = ts.key[min(c0 + 4 * j, nv - 1)];
+          p[j] = c0 + 4 * j < nv ? exp2f(key[c0 + 4 * j] - m) : 0.f;  // (of a row that is none NaN, which nobody reads)
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float w = __int_as_float(kk[j].z);
+          l += p[j];
+          if (c0 + 4 * j >= nv) continue;
+          key[c0 + 4 * j] = p[j];
+          // a cached row of a run is this key's alone
+          if (in && pos >= kk[j].y) {
+            if (kk[j].x > depth) row[kk[j].w + pos] = split1(p[j] * (1.f - w));
+            if (w > 0.f && kk[j].x >= depth) row[kk[j].w + pos - 1] = split1(p[j] * w);
+          }
         }
       }
       l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -423,7 +445,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
   // ---- what is left, row by row
   __syncthreads();
   build_keys(a.t, a.N, &ts.ks);
-  const WarpTree again = warp_tree(a.parent == nullptr ? nullptr : a.parent + static_cast<size_t>(b) * a.T, n, &ok);
+  const WarpTree again = warp_tree(a, b, n, &ok);
   __syncthreads();
   for (int r = from + warp; r < rows; r += kTtWarps) {
     const int hq = (r0 + r) / n, s = (r0 + r) - hq * n, d = pick32(again.depth, s);
