@@ -188,30 +188,29 @@ __device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sc
         first = entry;
         page = entry + lane < a.max_pages ? __ldg(a.table + static_cast<size_t>(k.b) * a.max_pages + entry + lane) : 0;
       }
-      int ok = 1;
-      if (lane == 0) ok = !*s_err && mbar_wait_backoff(&empty_bar[slot], ((count / kSlots) & 1) ^ 1, da.wait_ns);
-      if (!__shfl_sync(0xffffffffu, ok, 0)) {
+      // lane x copies box x: its row in the pools
+      int y = 0;
+      const int id = __shfl_sync(0xffffffffu, page, (entry - first + lane) & 31);
+      if (lane < boxes) {
+        const bool ok = id >= 0 && id < a.n_pages;
+        if (!ok) atomicExch(a.status, kStatusDeviceAssert);
+        y = (((ok ? id : 0) * a.H + k.h) << a.page_shift) + ((i * UNIT) & ((1 << a.page_shift) - 1));
+      }
+      if (*s_err || !mbar_wait(&empty_bar[slot], ((count / kSlots) & 1) ^ 1, da.wait_ns)) stop = true;
+      if (__any_sync(0xffffffffu, stop)) {
         *s_err = 1;
         stop = true;
         break;
       }
-      const uint32_t dst = smem_addr(ring + slot * 2 * kHalf);
       if (lane == 0) mbar_arrive_tx(&full_bar[slot], boxes * box * 2 * kD * static_cast<int>(sizeof(DT)));
-      for (int x = 0; x < boxes; ++x) {
-        int id = __shfl_sync(0xffffffffu, page, entry + x - first);
-        if (lane == 0) {
-          if (id < 0 || id >= a.n_pages) {
-            atomicExch(a.status, kStatusDeviceAssert);
-            id = 0;
-          }
-          const int y = ((id * a.H + k.h) << a.page_shift) + ((i * UNIT) & ((1 << a.page_shift) - 1));
-          const uint32_t at = dst + x * box * 128;
-          tma_2d(at, map_k, 0, y, &full_bar[slot]);
-          tma_2d(at + kHalf, map_v, 0, y, &full_bar[slot]);
-          if constexpr (sizeof(DT) == 4) {
-            tma_2d(at + kHalf / 2, map_k, 32, y, &full_bar[slot]);
-            tma_2d(at + kHalf + kHalf / 2, map_v, 32, y, &full_bar[slot]);
-          }
+      __syncwarp();
+      if (lane < boxes) {
+        const uint32_t at = smem_addr(ring + slot * 2 * kHalf) + lane * box * 128;
+        tma_2d(at, map_k, 0, y, &full_bar[slot]);
+        tma_2d(at + kHalf, map_v, 0, y, &full_bar[slot]);
+        if constexpr (sizeof(DT) == 4) {
+          tma_2d(at + kHalf / 2, map_k, 32, y, &full_bar[slot]);
+          tma_2d(at + kHalf + kHalf / 2, map_v, 32, y, &full_bar[slot]);
         }
       }
     }
