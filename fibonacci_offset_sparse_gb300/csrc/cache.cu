@@ -61,28 +61,35 @@ cudaError_t launch_second(void (*kernel)(Params...), dim3 grid, int threads, cud
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The ids of free pages from the cursor on, ascending, into list[0 .. want); returns how many
-// there are up to `want`.  4096 counts a step; stops as soon as enough are found.
-__device__ int find_free(const CacheDev& c, int want, int32_t* list, int* sums) {
+// The counts of four pages from `id` (a multiple of 4) on; 0 behind the last page.
+__device__ __forceinline__ void load_counts(const CacheDev& c, int id, int (&r)[4]) {
+  r[0] = r[1] = r[2] = r[3] = 0;
+  if (id + 3 < c.n_pages) {
+    const int4 x = *reinterpret_cast<const int4*>(c.refs + id);
+    r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (id + u < c.n_pages) r[u] = c.refs[id + u];
+  }
+}
+// ... 1 (in use) for those outside [from, n_pages).
+__device__ __forceinline__ void load_refs(const CacheDev& c, int id, int from, int (&r)[4]) {
+  load_counts(c, id, r);
+#pragma unroll
+  for (int u = 0; u < 4; ++u)
+    if (id + u < from || id + u >= c.n_pages) r[u] = 1;
+}
+
+// The ids of free pages from `from` on, ascending, into list[0 .. want); returns how many there
+// are up to `want`.  4096 counts a step (r: those of the first, loaded by the caller ahead of its other reads);
+// stops as soon as enough are found.
+__device__ int find_free(const CacheDev& c, int from, int (&r)[4], int want, int32_t* list, int* sums) {
   int found = 0;
-  const int from = max(0, min(c.state[kStateCursor], c.n_pages));
   for (int base = from & ~3; base < c.n_pages && found < want; base += 4 * kPlanThreads) {
     const int id = base + 4 * static_cast<int>(threadIdx.x);
-    int r[4] = {1, 1, 1, 1};
-    if (id + 3 < c.n_pages) {
-      const int4 x = *reinterpret_cast<const int4*>(c.refs + id);
-      r[0] = x.x; r[1] = x.y; r[2] = x.z; r[3] = x.w;
-    } else {
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        if (id + u < c.n_pages) r[u] = c.refs[id + u];
-    }
-    int n = 0;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (id + u < from) r[u] = 1;
-      n += r[u] == 0;
-    }
+    if (base > from) load_refs(c, id, from, r);
+    const int n = (r[0] == 0) + (r[1] == 0) + (r[2] == 0) + (r[3] == 0);
     int total;
     int at = found + block_scan_1024(n, sums, &total);
 #pragma unroll
@@ -126,6 +133,10 @@ __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_
   let_second_start();
   const CacheDev& c = a.c;
   const int b = threadIdx.x;
+  // the first step of the search for free pages, on its way while the sequences are read
+  const int cursor = max(0, min(c.state[kStateCursor], c.n_pages));
+  int counts[4];
+  load_refs(c, (cursor & ~3) + 4 * static_cast<int>(threadIdx.x), cursor, counts);
   int n = 0, len = 0, page = -1, refs = 0;
   bool bad = false, part = false;
   if (b < a.B) {
@@ -170,7 +181,7 @@ __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_
   const int fresh = n > 0 ? ((len + n + c.P - 1) >> c.shift) - first : 0;
   int total;
   const int off = block_scan_1024(any_bad ? 0 : fresh + (copy ? 1 : 0), s_sums, &total);
-  const bool enough = any_bad || find_free(c, total, a.list, s_sums) == total;
+  const bool enough = any_bad || find_free(c, cursor, counts, total, a.list, s_sums) == total;
   if (any_bad || !enough) {  // nothing changes
     if (b < a.B) a.jobs[b] = CommitJob{0, 0, -1, -1};
     if (b == 0) c.state[kStateStatus] = any_bad ? kStatusDeviceAssert : kStatusNoPages;
@@ -256,69 +267,112 @@ struct ForkArgs {
   int32_t* lens;  // [S]; -1: the whole call is refused
 };
 
-constexpr int kForkThreads = 256;
-
 __device__ __forceinline__ int pages_of(const CacheDev& c, int len) { return (len + c.P - 1) >> c.shift; }
 
-// A block a sequence: the new row into the workspace, +1 for each page it holds now, -1 for
-// each that it held.  Sums of integers: the order does not matter.
-__global__ void __launch_bounds__(kForkThreads) fork_count_kernel(const __grid_constant__ ForkArgs a) {
-  let_second_start();
+// Whether the call is refused (the same in every block).
+__device__ __forceinline__ bool fork_refused(const ForkArgs& a) {
   const CacheDev& c = a.c;
-  const int b = blockIdx.x;
   bool bad = false;
-  for (int i = threadIdx.x; i < c.S; i += kForkThreads) {
+  for (int i = threadIdx.x; i < c.S; i += blockDim.x) {
     const int s = a.src[i], len = c.lens[i];
     bad |= s < -1 || s >= c.S || len < 0 || len > static_cast<long long>(c.max_pages) * c.P;
   }
-  if (__syncthreads_or(bad)) {
-    if (threadIdx.x == 0) {
-      a.lens[b] = -1;
-      if (b == 0) c.state[kStateStatus] = kStatusDeviceAssert;
-    }
-    return;
-  }
+  return __syncthreads_or(bad);
+}
+
+// Sequence b, by `threads` threads of number t: the new row into the workspace, +1 for each page it holds now, -1
+// for each that it held.  Sums of integers: the order does not matter.
+__device__ __forceinline__ void fork_count(const ForkArgs& a, int b, int t, int threads) {
+  const CacheDev& c = a.c;
   const int s = a.src[b];
   const int len = s < 0 ? 0 : c.lens[s];
-  if (threadIdx.x == 0) a.lens[b] = len;
+  if (t == 0) a.lens[b] = len;
   if (s == b) return;
   const int now = pages_of(c, len), old = pages_of(c, c.lens[b]);
   const int32_t* from = c.table + static_cast<size_t>(max(s, 0)) * c.max_pages;
   const int32_t* mine = c.table + static_cast<size_t>(b) * c.max_pages;
-  for (int j = threadIdx.x; j < now; j += kForkThreads) {
-    const int page = from[j];
-    a.rows[static_cast<size_t>(b) * c.max_pages + j] = page;
-    if (page >= 0 && page < c.n_pages)
-      atomicAdd(&c.refs[page], 1);
-    else
-      c.state[kStateStatus] = kStatusDeviceAssert;
-  }
-  for (int j = threadIdx.x; j < old; j += kForkThreads) {
-    const int page = mine[j];
-    if (page >= 0 && page < c.n_pages)
-      atomicSub(&c.refs[page], 1);
-    else
-      c.state[kStateStatus] = kStatusDeviceAssert;
+  for (int j = t; j < max(now, old); j += threads) {
+    const int in = j < now ? from[j] : 0, out = j < old ? mine[j] : 0;
+    if (j < now) {
+      a.rows[static_cast<size_t>(b) * c.max_pages + j] = in;
+      if (in >= 0 && in < c.n_pages)
+        atomicAdd(&c.refs[in], 1);
+      else
+        c.state[kStateStatus] = kStatusDeviceAssert;
+    }
+    if (j < old) {
+      if (out >= 0 && out < c.n_pages)
+        atomicSub(&c.refs[out], 1);
+      else
+        c.state[kStateStatus] = kStatusDeviceAssert;
+    }
   }
 }
 
-// The rows into the table; the lowest page that lost its last holder lowers the cursor.
-__global__ void __launch_bounds__(kForkThreads) fork_write_kernel(const __grid_constant__ ForkArgs a) {
-  wait_for_first();
+// Then its row into the table; returns the lowest of its old pages that has lost its last holder.  Its length is
+// the caller's to write, when all its threads are past this.
+__device__ __forceinline__ int fork_write(const ForkArgs& a, int b, int t, int threads) {
   const CacheDev& c = a.c;
-  const int b = blockIdx.x;
-  const int len = a.lens[b];
-  if (len < 0 || a.src[b] == b) return;
-  const int now = pages_of(c, len), old = pages_of(c, c.lens[b]);
   int lowest = c.n_pages;
-  for (int j = threadIdx.x; j < max(now, old); j += kForkThreads) {
+  if (a.src[b] == b) return lowest;
+  const int now = pages_of(c, __ldcg(a.lens + b)), old = pages_of(c, c.lens[b]);
+  for (int j = t; j < max(now, old); j += threads) {
     int32_t* e = c.table + static_cast<size_t>(b) * c.max_pages + j;
     if (j < old) {
       const int page = *e;
-      if (page >= 0 && page < c.n_pages && c.refs[page] == 0) lowest = min(lowest, page);
+      if (page >= 0 && page < c.n_pages && __ldcg(c.refs + page) == 0) lowest = min(lowest, page);
     }
-    *e = j < now ? a.rows[static_cast<size_t>(b) * c.max_pages + j] : -1;
+    *e = j < now ? __ldcg(a.rows + static_cast<size_t>(b) * c.max_pages + j) : -1;
   }
+  return lowest;
+}
+
+// Small tables: both halves in one launch, by one cluster of blocks; a warp a sequence.
+constexpr int kForkCluster = 8;
+constexpr int kForkWarps = 16;
+
+__global__ void __launch_bounds__(32 * kForkWarps) fork_cluster_kernel(const __grid_constant__ ForkArgs a) {
+  const CacheDev& c = a.c;
+  if (fork_refused(a)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) c.state[kStateStatus] = kStatusDeviceAssert;
+    return;  // (every block of the cluster)
+  }
+  const int first = blockIdx.x * kForkWarps + (threadIdx.x >> 5), step = gridDim.x * kForkWarps, lane = threadIdx.x & 31;
+  for (int b = first; b < c.S; b += step) fork_count(a, b, lane, 32);
+  __threadfence();
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  int lowest = c.n_pages;
+  for (int b = first; b < c.S; b += step) {
+    lowest = min(lowest, fork_write(a, b, lane, 32));
+    __syncwarp();  // every lane has read the old length
+    if (lane == 0) c.lens[b] = __ldcg(a.lens + b);
+  }
+  lowest = __reduce_min_sync(0xffffffffu, lowest);
+  if (lane == 0 && lowest < c.n_pages) atomicMin(&c.state[kStateCursor], lowest);
+}
+
+// Large ones: a block a sequence, the second half in a launch of its own.
+constexpr int kForkThreads = 256;
+
+__global__ void __launch_bounds__(kForkThreads) fork_count_kernel(const __grid_constant__ ForkArgs a) {
+  let_second_start();
+  const int b = blockIdx.x;
+  if (fork_refused(a)) {
+    if (threadIdx.x == 0) {
+      a.lens[b] = -1;
+      if (b == 0) a.c.state[kStateStatus] = kStatusDeviceAssert;
+    }
+    return;
+  }
+  fork_count(a, b, threadIdx.x, kForkThreads);
+}
+
+__global__ void __launch_bounds__(kForkThreads) fork_write_kernel(const __grid_constant__ ForkArgs a) {
+  wait_for_first();
+  const CacheDev& c = a.c;
+  const int b = blockIdx.x, len = a.lens[b];
+  if (len < 0) return;
+  const int lowest = fork_write(a, b, threadIdx.x, kForkThreads);
   if (lowest < c.n_pages) atomicMin(&c.state[kStateCursor], lowest);
   __syncthreads();  // every thread has read the old length
   if (threadIdx.x == 0) c.lens[b] = len;
@@ -334,35 +388,58 @@ struct CompactArgs {
 };
 
 // One block: counts the used pages (n), then lists the free ones below n and the used ones
-// from n on; the i-th of these moves into the i-th of those.
+// from n on; the i-th of these moves into the i-th of those.  4096 counts a step; those of the first step, all
+// of a pool of up to 4096 pages, are read once.
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid_constant__ CompactArgs a) {
   __shared__ int s_sums[33];
   let_second_start();
   const CacheDev& c = a.c;
-  int mine = 0;
-  for (int id = threadIdx.x; id < c.n_pages; id += kPlanThreads) mine += c.refs[id] > 0;
+  constexpr int kStep = 4 * kPlanThreads;
+  const int t4 = 4 * static_cast<int>(threadIdx.x);
+  int head[4];
+  load_counts(c, t4, head);
+  int mine = (head[0] > 0) + (head[1] > 0) + (head[2] > 0) + (head[3] > 0);
+  for (int base = kStep; base < c.n_pages; base += kStep) {
+    int r[4];
+    load_counts(c, base + t4, r);
+    mine += (r[0] > 0) + (r[1] > 0) + (r[2] > 0) + (r[3] > 0);
+  }
   int live;
   block_scan_1024(mine, s_sums, &live);
   int holes = 0, moved = 0;
-  for (int base = 0; base < c.n_pages; base += kPlanThreads) {
-    const int id = base + static_cast<int>(threadIdx.x);
-    const bool in = id < c.n_pages;
-    const bool used = in && c.refs[id] > 0;
-    const bool hole = in && !used && id < live, out = used && id >= live;
-    int n_hole, n_out;
-    const int at_hole = holes + block_scan_1024(hole, s_sums, &n_hole);
-    const int at_out = moved + block_scan_1024(out, s_sums, &n_out);
-    if (hole) a.dst[at_hole] = id;
-    __syncthreads();
-    // every hole lies below `live`, so the first `moved + n_out` of them are listed by now
-    if (out) {
-      a.src[at_out] = id;
-      a.remap[id] = a.dst[at_out];
-    } else if (in) {
-      a.remap[id] = used ? id : -1;
+  for (int base = 0; base < c.n_pages; base += kStep) {
+    int r[4] = {head[0], head[1], head[2], head[3]};
+    if (base > 0) load_counts(c, base + t4, r);
+    // holes in the lower half of the sum, movers in the upper (4096 of each at most)
+    int both = 0;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int id = base + t4 + u;
+      if (id < c.n_pages) both += r[u] > 0 ? (id >= live ? 1 << 16 : 0) : (id < live ? 1 : 0);
     }
-    holes += n_hole;
-    moved += n_out;
+    int total;
+    const int at = block_scan_1024(both, s_sums, &total);
+    int at_hole = holes + (at & 0xffff), at_out = moved + (at >> 16);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int id = base + t4 + u;
+      if (id < live && id < c.n_pages && r[u] <= 0) a.dst[at_hole++] = id;
+    }
+    __syncthreads();
+    // every hole lies below `live`, so as many as the movers so far are listed by now
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int id = base + t4 + u;
+      if (id >= c.n_pages) break;
+      int to = r[u] > 0 ? id : -1;
+      if (r[u] > 0 && id >= live) {
+        to = a.dst[at_out];
+        a.src[at_out++] = id;
+      }
+      a.remap[id] = to;
+    }
+    holes += total & 0xffff;
+    moved += total >> 16;
   }
   if (threadIdx.x == 0) {
     *a.moves = moved;
@@ -372,7 +449,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveVecs = 4;  // 16-byte words a thread has in flight
+constexpr int kMoveVecs = 8;  // 16-byte words a thread has in flight
 
 __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid_constant__ CompactArgs a, int page_vecs) {
   wait_for_first();
@@ -472,6 +549,24 @@ cudaError_t launch_cache_fork(const fib_attn_cache& cache, const int32_t* src, v
   a.src = src;
   a.lens = static_cast<int32_t*>(ws);
   a.rows = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + round_up(sizeof(int32_t) * kMaxSeqs));
+  // One launch while the table is small.  32 x 64 entries: 12.3 us a call among others, 15.9 us in two (7.3 and 5.8 us in
+  // a graph, where launches cost little); 256 x 512: 51 us by one cluster, 7.6 us in two.
+  if (static_cast<long long>(cache.max_seqs) * cache.max_pages <= 1 << 13) {
+    const int blocks = (cache.max_seqs + kForkWarps - 1) / kForkWarps;
+    int size = 1;
+    while (size < blocks && size < kForkCluster) size *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(size));
+    cfg.blockDim = dim3(32 * kForkWarps);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fork_cluster_kernel, a);
+  }
   fork_count_kernel<<<cache.max_seqs, kForkThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
