@@ -24,24 +24,34 @@ namespace {
 
 constexpr int kTtThreads = 256, kTtWarps = kTtThreads / 32;
 constexpr int kTtRows = 8 * kTtWarps;   // query rows of a block: 8 a warp
-constexpr int kTtKeys = 176;            // staged rows, a multiple of 16
-constexpr int kTtStride = kTtKeys + 4;  // 4-byte words of a row of S or P: writes of a fragment meet no bank twice
-constexpr int kTtLeast = 32;            // query rows at a time, at least: fewer leave most warps idle
-constexpr int kTtLow = 64;              // rows of the drafted keys' lower parts
+constexpr int kTtMost = 304;            // staged rows a block may have
 
-// byte offsets in dynamic shared memory (its base is 128-byte aligned)
-constexpr int kTtK = 0;
-constexpr int kTtV = kTtK + kTtKeys * 128;
-constexpr int kTtLo = kTtV + kTtKeys * 128;
-constexpr int kTtS = kTtLo + kTtLow * 128;              // [row][kTtStride]: S, then P as hi | lo << 16, then O as bf16
-constexpr int kTtKey = kTtS + kTtRows * kTtStride * 4;  // [row][keys + 1]: weights by key
-size_t tt_bytes(int keys) { return kTtKey + static_cast<size_t>(kTtRows) * (keys + 1) * 4; }
+// Sizes of a call and byte offsets in dynamic shared memory (its base is 128-byte aligned).  So many staged rows that
+// two blocks share an SM: the fewer query rows, the less room their scores take.
+struct TtShape {
+  int keys;    // staged rows, a multiple of 16
+  int stride;  // 4-byte words of a row of S or P, 4 modulo 16: writes of a fragment meet no bank twice
+  int v, lo, s, key, key_stride, bytes;
+};
+TtShape shape_of(int rows, int T, int keys) {
+  TtShape p;
+  const int r8 = rows < kTtRows ? (rows + 7) / 8 * 8 : kTtRows;
+  p.keys = r8 <= 16 ? 304 : r8 <= 32 ? 240 : 176;
+  p.stride = p.keys + 4;
+  p.v = p.keys * 128;                         // K [keys][64], then V, 16-byte words swizzled by row
+  p.lo = 2 * p.v;                             // the drafted keys' lower parts
+  p.s = p.lo + (T + 15) / 16 * 16 * 128;      // [row][stride]: S, then P as hi | lo << 16, then O as bf16
+  p.key = p.s + r8 * p.stride * 4;            // [row][key_stride]: weights by key
+  p.key_stride = keys + 1;
+  p.bytes = p.key + r8 * p.key_stride * 4;
+  return p;
+}
 
 struct TtSmem {
   int4 key[kMaxKeys];  // distance, position it needs, weight of the second row, place (below)
   union {
     KeySmem ks;        // as built; again for the row-by-row path
-    int from[kTtKeys];  // of a staged cached row: which of the pools' rows it is
+    int from[kTtMost];  // of a staged cached row: which of the pools' rows it is
   };
   unsigned char line[kMaxDrafts][kMaxDrafts];  // [s][d]: the ancestor d levels above node s
   unsigned char depth[kMaxDrafts];
@@ -78,7 +88,8 @@ __device__ __forceinline__ uint32_t split1(float x) {
 __device__ __forceinline__ bool not_finite(uint32_t x) { return (~x & 0x7f80u) == 0 || (~x & 0x7f800000u) == 0; }
 __device__ __forceinline__ bool not_finite(const uint4& x) { return not_finite(x.x) | not_finite(x.y) | not_finite(x.z) | not_finite(x.w); }
 
-__global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_constant__ TreeArgs a, int blocks_per_head, int key_stride) {
+__global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_constant__ TreeArgs a, int blocks_per_head,
+                                                                     const __grid_constant__ TtShape shape) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ __align__(16) TtSmem ts;
   const int head = blockIdx.x / blocks_per_head, b = head / a.H, h = head % a.H;
@@ -185,14 +196,14 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     if (lane == 0) ts.at[nr + 1] = total;
     return total;
   };
-  if (warp == 0) {  // the most rows at a time whose union fits
+  if (warp == 0) {  // the most rows at a time whose union fits, in two steps at most (more leave most warps idle too long)
     int step = kTtRows;
-    for (; step >= kTtLeast; step >>= 1) {
+    for (; step >= 8 && 2 * step >= rows; step >>= 1) {
       bool fits = true;
-      for (int from = 0; from < rows && fits; from += step) fits = plan_runs(from, step) <= kTtKeys;
+      for (int from = 0; from < rows && fits; from += step) fits = plan_runs(from, step) <= shape.keys;
       if (fits) break;
     }
-    if (lane == 0) ts.step = step;
+    if (lane == 0) ts.step = step >= 8 && 2 * step >= rows ? step : 0;
   } else if (warp < 3) {  // the first key that reads the row at distance d: keys are in the order of lo, and read lo and lo + 1
     const int d = tid - 32;
     int c = 0, end = nv;
@@ -241,16 +252,16 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int at = du * 128 + (((t + 4 * i) ^ (du & 7)) << 4);
-      *reinterpret_cast<uint4*>(smem + kTtK + at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-      *reinterpret_cast<uint4*>(smem + kTtLo + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-      *reinterpret_cast<uint4*>(smem + kTtV + at) = dv[i];
+      *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
+      *reinterpret_cast<uint4*>(smem + shape.lo + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+      *reinterpret_cast<uint4*>(smem + shape.v + at) = dv[i];
     }
   }
   __syncthreads();
   const int step = ts.step;
 
   int from = 0;
-  for (; from < rows && step >= kTtLeast; from += step) {
+  for (; from < rows && step > 0; from += step) {
     if (step < rows) {  // (else the plan of the only step stands)
       __syncthreads();
       if (warp == 0) plan_runs(from, step);
@@ -259,34 +270,33 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     const int total = ts.at[nr + 1], padded = (total + 15) & ~15;
     // ---- where the staged rows lie; the keys as the rows below read them: at position p, key c's row lies at place + p
     // among the staged (its second one in front of that)
-    if (tid >= drafts && tid < total) {
-      int c = 0, end = nr + 1;  // the run: at[c] <= tid < at[c + 1]
+    for (int x = drafts + tid; x < total; x += kTtThreads) {
+      int c = 0, end = nr + 1;  // the run: at[c] <= x < at[c + 1]
       while (end - c > 1) {
         const int mid = (c + end) >> 1;
-        if (ts.at[mid] <= tid)
+        if (ts.at[mid] <= x)
           c = mid;
         else
           end = mid;
       }
-      long long at = cache_row(a, b, h, ts.first[c] + tid - ts.at[c]);
+      long long at = cache_row(a, b, h, ts.first[c] + x - ts.at[c]);
       if (at < 0) {
         atomicExch(a.status, kStatusDeviceAssert);
         at = 0;
       }
-      ts.from[tid] = static_cast<int>(at / kD);
+      ts.from[x] = static_cast<int>(at / kD);
     }
     if (tid < nv) {
       const int run = tid < W ? 0 : tid - W + 1;
       ts.key[tid].w = ts.at[run] - ts.first[run] - ts.key[tid].x;
     }
     __syncthreads();
-    // ---- the cached rows, all on their way at once
-    {
-      constexpr int kMost = kTtKeys * 8 / kTtThreads + 1;
-      uint4 k[kMost], v[kMost];
+    // ---- the cached rows, 192 on their way at once
+    for (int x0 = drafts; x0 < padded; x0 += 6 * (kTtThreads / 8)) {
+      uint4 k[6], v[6];
 #pragma unroll
-      for (int j = 0; j < kMost; ++j) {
-        const int i = (drafts + j * (kTtThreads / 8)) * 8 + tid, x = i >> 3, ch = i & 7;
+      for (int j = 0; j < 6; ++j) {
+        const int x = x0 + j * (kTtThreads / 8) + (tid >> 3), ch = tid & 7;
         k[j] = v[j] = make_uint4(0, 0, 0, 0);
         if (x < total) {
           const size_t at = static_cast<size_t>(ts.from[x]) * kD;
@@ -295,13 +305,13 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
         }
       }
 #pragma unroll
-      for (int j = 0; j < kMost; ++j) {
-        const int i = (drafts + j * (kTtThreads / 8)) * 8 + tid, x = i >> 3, ch = i & 7;
+      for (int j = 0; j < 6; ++j) {
+        const int x = x0 + j * (kTtThreads / 8) + (tid >> 3), ch = tid & 7;
         bad |= not_finite(k[j]) | not_finite(v[j]);
         if (x < padded) {
           const int to = x * 128 + ((ch ^ (x & 7)) << 4);
-          *reinterpret_cast<uint4*>(smem + kTtK + to) = k[j];
-          *reinterpret_cast<uint4*>(smem + kTtV + to) = v[j];
+          *reinterpret_cast<uint4*>(smem + to) = k[j];
+          *reinterpret_cast<uint4*>(smem + shape.v + to) = v[j];
         }
       }
     }
@@ -309,12 +319,12 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
 
     // ---- 8 query rows a warp, without a further barrier
     if (8 * warp >= from && 8 * warp < min(from + step, rows)) {
-      const int mi = lane >> 3, rl = lane & 7;
-      uint32_t* S = reinterpret_cast<uint32_t*>(smem + kTtS) + 8 * warp * kTtStride;
+      const int mi = lane >> 3, rl = lane & 7, stride = shape.stride;
+      uint32_t* S = reinterpret_cast<uint32_t*>(smem + shape.s) + 8 * warp * stride;
 #pragma unroll 2
       for (int x0 = 0; x0 < padded; x0 += 16) {
         float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-        const uint32_t row = base + kTtK + (x0 + (mi & 1) * 8 + rl) * 128;
+        const uint32_t row = base + (x0 + (mi & 1) * 8 + rl) * 128;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           uint32_t ka[4];
@@ -327,19 +337,19 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t ka[4];
-            ldsm4(ka, row + (kTtLo - kTtK) + (((2 * k + (mi >> 1)) ^ rl) << 4));
+            ldsm4(ka, row + shape.lo + (((2 * k + (mi >> 1)) ^ rl) << 4));
             mma16(d[k & 1], ka, qh[k][0], qh[k][1]);
           }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          S[(2 * t + (e & 1)) * kTtStride + x0 + g + 8 * (e >> 1)] = __float_as_uint((c[0][e] + c[1][e]) + (d[0][e] + d[1][e]));
+          S[(2 * t + (e & 1)) * stride + x0 + g + 8 * (e >> 1)] = __float_as_uint((c[0][e] + c[1][e]) + (d[0][e] + d[1][e]));
       }
       __syncwarp();
       // weights: 4 lanes a row (this lane's: g), keys t, t + 4, ...
       const bool in = qr < rows;
-      uint32_t* row = S + g * kTtStride;
-      float* key = reinterpret_cast<float*>(smem + kTtKey) + qr * key_stride;
+      uint32_t* row = S + g * stride;
+      float* key = reinterpret_cast<float*>(smem + shape.key) + qr * shape.key_stride;
       const unsigned char* line = ts.line[q_node];
       float m = -INFINITY;
       for (int c0 = t; c0 < nv; c0 += 16) {  // scores by key, four at a time: every read before a write
@@ -415,7 +425,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
         const uint2 p = *reinterpret_cast<const uint2*>(row + x0 + 2 * t), q = *reinterpret_cast<const uint2*>(row + x0 + 2 * t + 8);
         const uint32_t h0 = __byte_perm(p.x, p.y, 0x5410), h1 = __byte_perm(q.x, q.y, 0x5410);
         const uint32_t l0 = __byte_perm(p.x, p.y, 0x7632), l1 = __byte_perm(q.x, q.y, 0x7632);
-        const uint32_t vr = base + kTtV + (x0 + (mi >> 1) * 8 + rl) * 128;
+        const uint32_t vr = base + shape.v + (x0 + (mi >> 1) * 8 + rl) * 128;
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           uint32_t va[4];
@@ -456,17 +466,25 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
 
 }  // namespace
 
-// From 16 query rows a key head on (measured, 512 heads of a batch: 8 rows 00 us here and 00 row by row, 16 rows 00 and 00).
-bool tree_tc_serves(const TreeArgs& a) { return a.G * a.T >= 16; }
+// A block takes some 11 us whatever its rows, and 304 run at a time; row by row takes 4.5 us and 2.6 ns a row of the
+// whole batch.  Measured (us here, row by row): 512 blocks of 64 rows 32 and 87, of 16 rows 21.5 and 26, of 12 rows 21.7 and
+// 20.4; 128 blocks of 64 rows 12.7 and 25, of 16 rows 10.3 and 8.7; 32 blocks of 64 rows 12.3 and 8.2.
+// A chain's union grows with its length: it fits for 12 nodes of the Fibonacci base's distances, more are served row by
+// row.  (Deep trees that are given by their parents are found on the device only; they take 1.3 times the time then.)
+bool tree_tc_serves(const TreeArgs& a) {
+  if (a.parent == nullptr && a.T > 12) return false;
+  const long long heads = static_cast<long long>(a.B) * a.H, blocks = heads * ((a.G * a.T + kTtRows - 1) / kTtRows);
+  return heads * a.G * a.T > 4200 * ((blocks + 303) / 304) - 1700;
+}
 
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream) {
-  const int per = (a.G * a.T + kTtRows - 1) / kTtRows, keys = a.t.W + a.t.n;
-  const size_t smem = tt_bytes(keys);
-  const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(tt_bytes(kMaxKeys)));
+  const int per = (a.G * a.T + kTtRows - 1) / kTtRows;
+  const TtShape shape = shape_of(a.G * a.T, a.T, a.t.W + a.t.n);
+  const cudaError_t e = cudaFuncSetAttribute(tree_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
   if (e != cudaSuccess) return e;
   const long long blocks = static_cast<long long>(a.B) * a.H * per;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  tree_tc_kernel<<<static_cast<unsigned>(blocks), kTtThreads, smem, stream>>>(a, per, keys + 1);
+  tree_tc_kernel<<<static_cast<unsigned>(blocks), kTtThreads, shape.bytes, stream>>>(a, per, shape);
   return cudaGetLastError();
 }
 

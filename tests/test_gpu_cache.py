@@ -292,6 +292,11 @@ CASES = [  # B's lengths, H, G, T, P, tree, live nodes
     ([129, 300], 1, 1, 64, 128, "random", None),
     ([40, 1000], 2, 4, 64, 256, "roots", [64, 1]),
     ([2048, 63, 65], 1, 5, 7, 16, None, None),
+    ([300, 17, 64], 20, 1, 64, 32, "random", [64, 50, 64]),     # enough rows for the sparse decode's tensor-core kernel
+    ([90, 0, 1033, 5], 32, 3, 9, 16, "random", [9, 9, 8, 0]),
+    ([5, 0, 77, 200, 16, 31, 64, 9], 32, 1, 12, 16, None, None),
+    ([700, 129, 0], 2, 1, 24, 64, "random", [24, 17, 24]),      # each number of row tiles of the dense decode's
+    ([128, 257], 1, 3, 16, 128, "random", [16, 11]),
 ]
 
 
@@ -399,7 +404,7 @@ def test_another_branch_never_reaches_a_node_of_a_large_tree(dtype, G, bad):
     """As above, for as many query rows as the tensor-core kernels take; only v, only k, then both."""
     r = rng(20)
     T = 21
-    c, ref, dev, host, _, _ = tree_case(r, dtype, [150, 0], 2, G, T, 32, "chain", None)
+    c, ref, dev, host, _, _ = tree_case(r, dtype, [150, 0], 64, G, T, 32, "chain", None)
     parent = np.tile([-1] + [max(0, s - 2) for s in range(1, T)], (2, 1))  # 0, then the odd and the even nodes
     even = list(range(2, T, 2))
     odd = [0] + list(range(1, T, 2))
@@ -429,7 +434,7 @@ def test_unions_of_keys_that_do_and_do_not_fit(mode, W, alpha, kind, T, G):
     """Trees of every depth over a base of close distances (several rungs read one row), bf16."""
     r = rng(21, T, W)
     lens = [500, 0, 30]
-    c, ref, dev, host, parent, live = tree_case(r, "bf16", lens, 2, G, T, 16, "chain" if kind == "last first" else kind, [T, T - 1, T // 2])
+    c, ref, dev, host, parent, live = tree_case(r, "bf16", lens, 16, G, T, 16, "chain" if kind == "last first" else kind, [T, T - 1, T // 2])
     if kind == "last first":  # depths 0 .. T/2, then all at once back to the roots
         parent = np.tile([s - 1 if s <= T // 2 else -1 for s in range(T)], (3, 1))
     base = [1, 2, 3, 5, 20, 21, 22, 23, 24, 25, 40, 60, 61, 100, 150, 151, 152, 153, 300, 301, 400, 477, 499, 500]
@@ -744,7 +749,7 @@ def test_two_plans_on_two_streams_at_once():
 @pytest.mark.parametrize("pattern", [0x7fc00000, 0x7c007c00, 0xffffffff])
 def test_stale_shared_memory_does_not_reach_the_outputs(pattern):
     r = rng(19)
-    for case in (3, 5, 6):
+    for case in (3, 5, 6, 9):
         c, ref, dev, host, parent, live = tree_case(r, "bf16", *CASES[case])
         plan = plan_for(2300, W=8)
         nodes = i32(live)
