@@ -165,6 +165,9 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
 }
 
 // ------------------------------------------------------------------------------ feeder --
+// For what is in flight when a block gives up: its wait is not the caller's, which may be too short for a copy.
+constexpr unsigned long long kDrainNs = 2000000000ull;
+
 // The feeding warp: K and V rows of the units of [u0, u1) into the ring's slots, a page at a time.  A slot
 // is K, then V, kHalf bytes each; float32 rows lie as two halves of 32 dims, a quarter slot apart.
 template <typename DT, typename P>
@@ -219,7 +222,7 @@ __device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sc
   // nothing may be in flight when the block ends
   if (lane == 0) {
     for (int c = count - kSlots < 0 ? 0 : count - kSlots; c < count; ++c)
-      mbar_wait(&full_bar[c % kSlots], (c / kSlots) & 1, da.wait_ns);
+      mbar_wait(&full_bar[c % kSlots], (c / kSlots) & 1, kDrainNs);
     if (*s_err) atomicExch(a.status, kStatusTimeout);
   }
 }

@@ -25,7 +25,7 @@ namespace fibattn {
 
 namespace {
 
-constexpr float kNoKey = -1e30f;  // reference of a row that has met no finite score
+constexpr float kNoKey = 1e30f;  // a row's reference, negated, before it has met a finite score
 
 template <int ROWS>
 struct TcShape {
@@ -41,7 +41,7 @@ struct TcShape {
   // byte offsets in dynamic shared memory (its base is 1024-byte aligned)
   static constexpr int kQuery = kSlots * kSlotBytes;    // hi [ROWS][64], lo: K-major, 128-byte swizzle
   static constexpr int kWeights = kQuery + ROWS * 256;  // hi [ROWS/8][16][8 keys][8 rows], lo; see below for its other uses
-  static constexpr int kRef = kWeights + ROWS * 512;    // [ROWS] the rows' reference
+  static constexpr int kRef = kWeights + ROWS * 512;    // [ROWS] the rows' references, negated
   static constexpr int kMax = kRef + ROWS * 4;          // [2][ROWS]: of the cached keys, of the drafted ones
   static constexpr int kSum = kMax + 2 * ROWS * 4;
   static constexpr int kWarpMax = kSum + 2 * ROWS * 4;  // [4][ROWS]; at the end the two parts' weights [2][ROWS]
@@ -138,6 +138,19 @@ __device__ __forceinline__ float warp_max(float x) {
   return y;
 }
 
+// x0 += y0, x1 += y1
+__device__ __forceinline__ void add2(float& x0, float& x1, float y0, float y1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(x0), "+f"(x1)
+      : "f"(y0), "f"(y1));
+}
+// The largest of three; NaN where one is.
+__device__ __forceinline__ float max_nan(float x, float y, float z) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 // The units' K and V tiles in turn: the tile 2 count (K) or 2 count + 1 (V), its slot and its round's parity.
 template <int SLOTS>
 struct Tile {
@@ -194,7 +207,7 @@ __device__ __forceinline__ void feed_tiles(const DenseTreeArgs& da, const Schedu
   // nothing may be in flight when the block ends
   for (int c = n - P::kSlots < 0 ? 0 : n - P::kSlots; c < n; ++c) {
     const Tile<P::kSlots> tile(c);
-    mbar_wait(&full_bar[tile.slot], tile.parity, da.wait_ns);
+    mbar_wait(&full_bar[tile.slot], tile.parity, kDrainNs);
   }
   if (*s_err && lane == 0) atomicExch(a.status, kStatusTimeout);
 }
@@ -333,7 +346,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
         }
       }
       commit_tc(&bars.drained);  // nothing may be in flight when the block ends
-      mbar_wait(&bars.drained, 0, da.wait_ns);
+      mbar_wait(&bars.drained, 0, kDrainNs);
     }
     __syncwarp();
   } else {
@@ -394,7 +407,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           *reinterpret_cast<uint4*>(at + ROWS * 128) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
         }
       }
-      if (tid < ROWS) s_ref[tid] = kNoKey;
+      if (tid < ROWS) s_ref[tid] = tid < rows ? kNoKey : 0.f;  // (a row that is none has scores of 0)
       fence_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.query);
@@ -421,89 +434,95 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
 #pragma unroll
       for (int r = 0; r < GR; ++r) l[r] = 0.f;
       for (int i = k_first; i < k_last; ++i, ++count) {
-        const bool in = key < k_len - i * P::kUnit;
+        const bool all = k_len - i * P::kUnit >= P::kUnit, in = key < k_len - i * P::kUnit;
         wait(&bars.scores[count & 1], (count >> 1) & 1);
         fence_after();
-        float s[GR];
-        tmem_load(tmem + (count & 1) * ROWS + g0 + lanes, s);
-        bool past = false;
+        float x[GR];  // the scores, then over their references
+        auto load = [&] {
+          tmem_load(tmem + (count & 1) * ROWS + g0 + lanes, x);
+          if (!all) {
 #pragma unroll
-        for (int c = 0; c < GR / 4; ++c) {
-          const float4 ref = *reinterpret_cast<const float4*>(s_ref + g0 + 4 * c);
-          const float m[4] = {ref.x, ref.y, ref.z, ref.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            if (!in) s[4 * c + e] = -INFINITY;
-            past |= 4 * c + e < mine && !(s[4 * c + e] - m[e] <= 8.f);  // (a NaN too)
+            for (int r = 0; r < GR; ++r) x[r] = in ? x[r] : -INFINITY;
           }
-        }
-        if (any_of_group(group, past)) {
+        };
+        auto refer = [&] {
+#pragma unroll
+          for (int c = 0; c < GR / 4; ++c) {
+            const float4 ref = *reinterpret_cast<const float4*>(s_ref + g0 + 4 * c);
+            add2(x[4 * c], x[4 * c + 1], ref.x, ref.y);
+            add2(x[4 * c + 2], x[4 * c + 3], ref.z, ref.w);
+          }
+        };
+        load();
+        refer();
+        float most = x[0];
+#pragma unroll
+        for (int r = 1; r + 1 < GR; r += 2) most = max_nan(most, x[r], x[r + 1]);
+        if (any_of_group(group, !(max_nan(most, x[GR - 1], x[GR - 1]) <= 8.f))) {  // (a NaN too)
           // A NaN may come of an infinite key, where hi + lo add infinities of opposite signs: the upper
           // parts' product alone keeps the sign.
+          load();  // (its buffer is not written before this unit's weights are there)
           bool bad = false;
 #pragma unroll
-          for (int r = 0; r < GR; ++r) bad |= r < mine && isnan(s[r]);
+          for (int r = 0; r < GR; ++r) bad |= r < mine && isnan(x[r]);
           if (bad) {
             const Task now = task_at(u);
             const long long at = cache_row(a, now.b, now.h, i * P::kUnit + key);  // (the tile's slot may hold another by now)
 #pragma unroll 1
             for (int r = 0; r < mine && at >= 0; ++r) {
-              float x = 0.f;
+              float y = 0.f;
 #pragma unroll 1
               for (int d = 0; d < kD; ++d) {
                 const __nv_bfloat16 kx = static_cast<const __nv_bfloat16*>(a.kc)[at + d];
                 const __nv_bfloat16 qx =
                     *reinterpret_cast<const __nv_bfloat16*>(smem + P::kQuery + (g0 + r) * 128 + (((d >> 3) ^ (r & 7)) << 4) + (d & 7) * 2);
-                x = fmaf(__bfloat162float(kx), __bfloat162float(qx), x);
+                y = fmaf(__bfloat162float(kx), __bfloat162float(qx), y);
               }
 #pragma unroll
               for (int j = 0; j < GR; ++j)
-                if (j == r && isnan(s[j])) s[j] = x;
+                if (j == r && isnan(x[j])) x[j] = y;
             }
           }
           __syncwarp();
 #pragma unroll
           for (int r = 0; r < GR; ++r) {
-            const float x = warp_max(s[r]);
-            if (lane == 0) s_warp[wq * ROWS + g0 + r] = x;
+            const float y = warp_max(x[r]);
+            if (lane == 0) s_warp[wq * ROWS + g0 + r] = y;
           }
           if (count > 0) wait(&bars.added, (count - 1) & 1);  // O is at rest
           fence_after();
           group_sync(group);
 #pragma unroll
           for (int c = 0; c < GR / 8; ++c) {
-            float x[8];
-            tmem_load(tmem_o + g0 + 8 * c + lanes, x);  // (unused at a piece's first unit)
+            float y[8];
+            tmem_load(tmem_o + g0 + 8 * c + lanes, y);  // (unused at a piece's first unit)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
               const float* w = s_warp + g0 + 8 * c + e;
-              const float m = s_ref[g0 + 8 * c + e];
+              const float m = -s_ref[g0 + 8 * c + e];
               const float corr = ex2(m - fmaxf(m, fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS]))));
               l[8 * c + e] *= corr;
-              x[e] *= corr;
+              y[e] *= corr;
             }
-            if (i > k_first) tmem_store(tmem_o + g0 + 8 * c + lanes, x);
+            if (i > k_first) tmem_store(tmem_o + g0 + 8 * c + lanes, y);
           }
           group_sync(group);
           if (key < GR) {
             const float* w = s_warp + g0 + key;
-            s_ref[g0 + key] = fmaxf(s_ref[g0 + key], fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS])));
+            s_ref[g0 + key] = -fmaxf(-s_ref[g0 + key], fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS])));
           }
           group_sync(group);
+          refer();
         }
         // the weights of the thread's key, 8 rows to 16 bytes
         uint32_t hi[GR / 2], lo[GR / 2];
 #pragma unroll
-        for (int c = 0; c < GR / 4; ++c) {
-          const float4 ref = *reinterpret_cast<const float4*>(s_ref + g0 + 4 * c);
-          const float m[4] = {ref.x, ref.y, ref.z, ref.w};
-#pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            const float p0 = ex2(s[4 * c + e] - m[e]), p1 = ex2(s[4 * c + e + 1] - m[e + 1]);
-            l[4 * c + e] += p0;
-            l[4 * c + e + 1] += p1;
-            split_bf16(p0, p1, hi[2 * c + e / 2], lo[2 * c + e / 2]);
-          }
+        for (int c = 0; c < GR / 2; ++c) {
+          float p0 = ex2(x[2 * c]), p1 = ex2(x[2 * c + 1]);
+          add2(l[2 * c], l[2 * c + 1], p0, p1);
+          hi[c] = pack_bf2_rn(p0, p1);
+          add2(p0, p1, -bf_lo(hi[c]), -bf_hi(hi[c]));
+          lo[c] = pack_bf2_rn(p0, p1);
         }
         if (count > 0) wait(&bars.added, (count - 1) & 1);  // P of the unit before is in O
         unsigned char* at = smem + P::kWeights + (g0 >> 3) * 2048 + (key >> 3) * 128 + (key & 7) * 16;
@@ -553,7 +572,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           if (lane == j) mine_sum = sum[j];
         const int r = warp + WARPS * lane;
         if (lane < MOST && r < rows) {
-          const float m = s_ref[r] == kNoKey ? -INFINITY : s_ref[r];
+          const float m = s_ref[r] == kNoKey ? -INFINITY : -s_ref[r];
           const float md = tail ? s_max[ROWS + r] : -INFINITY, ld = tail ? s_sum[ROWS + r] : 0.f, all = fmaxf(m, md);
           const float w = weight_of(m, mine_sum, all), wd = weight_of(md, ld, all);
           s_warp[r] = w;
