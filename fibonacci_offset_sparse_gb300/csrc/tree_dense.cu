@@ -15,7 +15,7 @@
 //
 // Block: 4 warps that compute and one that feeds them.  The feeder copies K and V rows of a unit by
 // TMA (128-byte swizzle) into a slot of a ring, a page at a time.  The computing warps are TILES row
-// tiles times 4 / TILES groups; the groups take the units in turn, and each warp keeps an online
+// tiles (2 where float32 has more than 16 query rows) times 4 / TILES groups; the groups take the units in turn, and each warp keeps an online
 // softmax (running maximum and sum, O in registers) over its units; the groups merge at the end of the run.
 //   bf16: mma.sync m16n8k16 with the keys (then the dimensions of V) as the 16 rows of a tile and 8
 //   query rows as its columns, so that a single query pays for 8 rows and not for 16, and a warp that
@@ -33,9 +33,6 @@ namespace fibattn {
 
 namespace {
 
-constexpr int kDtWarps = 4;
-constexpr int kDtCons = 32 * kDtWarps;  // computing threads
-constexpr int kDtThreads = kDtCons + 32;
 // bf16: up to so many query rows here, more in tree_dense_tc.cu.  16 x 65536 cached rows: 8 rows 168 us here and 183 us
 // there, 16 rows 283 and 184; 4096 rows, one query 11.9 and 16.1.
 constexpr int kMmaRows = 8;
@@ -82,7 +79,7 @@ __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) 
 // warps share them (registers are left for O and the scores).  unit: one unit's keys; rows of it from `valid` on
 // were not filled for this sequence and count as absent, whatever lies there (`zero`: 128 bytes of 0,
 // read in their place).  each(f): f(row, dim, pair of values) over O, dims d and d + step.
-template <typename DT, int NR>
+template <typename DT>
 struct Core;
 
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
@@ -91,20 +88,20 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// bf16, 8 NR query rows.  Lane (g, t): of the scores keys g and g + 8 of each 16, rows 8n + 2t and + 1;
+// bf16, 8 query rows.  Lane (g, t): of the scores keys g and g + 8 of each 16, rows 2t and 2t + 1;
 // of O dims g and g + 8 of each 16, the same rows.
-template <int NR>
-struct Core<__nv_bfloat16, NR> {
-  static constexpr int kRows = 8 * NR, kOwn = 2 * NR, UNIT = kUnitRows<__nv_bfloat16>;
-  static constexpr int kQueryBytes = NR * 4 * 512;  // [8 rows][k-step of 16 dims][lane]: hi, hi, lo, lo
-  float o[NR][4][4];                                // [8 rows][16 dims][fragment]
-  float m[NR][2], l[NR][2];
+template <>
+struct Core<__nv_bfloat16> {
+  static constexpr int kRows = 8, UNIT = kUnitRows<__nv_bfloat16>;
+  static constexpr int kQueryBytes = 4 * 512;  // [k-step of 16 dims][lane]: hi, hi, lo, lo
+  float o[4][4];  // [16 dims][fragment]
+  float m[2], l[2];
 
-  // rows of the query that this lane loads: row 8n + g
-  static constexpr int kLoads = NR;
-  __device__ __forceinline__ static int load_row(int i) { return 8 * i + ((threadIdx.x & 31) >> 2); }
-  __device__ __forceinline__ static void load_query(const TreeArgs& a, uint4* qs, int i, bool in, size_t row, int pos) {
-    uint4* at = qs + i * 128 + (threadIdx.x & 31);
+  // the row of the query that this lane loads
+  static constexpr int kLoads = 1;
+  __device__ __forceinline__ static int load_row(int) { return (threadIdx.x & 31) >> 2; }
+  __device__ __forceinline__ static void load_query(const TreeArgs& a, uint4* qs, int, bool in, size_t row, int pos) {
+    uint4* at = qs + (threadIdx.x & 31);
     if (!in) {
 #pragma unroll
       for (int s = 0; s < 4; ++s) at[32 * s] = make_uint4(0, 0, 0, 0);
@@ -129,65 +126,51 @@ struct Core<__nv_bfloat16, NR> {
     for (int s = 0; s < 4; ++s) at[32 * s] = make_uint4(qh[s][0], qh[s][1], ql[s][0], ql[s][1]);
   }
   __device__ __forceinline__ void clear() {
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
 #pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-      for (int x = 0; x < 4; ++x) o[n][x][0] = o[n][x][1] = o[n][x][2] = o[n][x][3] = 0.f;
-    }
+    for (int x = 0; x < 4; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
   }
-  __device__ __forceinline__ static void scores(uint32_t kt, const uint4* qs, float (&s)[2][NR][4]) {
+  __device__ __forceinline__ static void scores(uint32_t kt, const uint4* qs, float (&s)[2][4]) {
     const int mi = (threadIdx.x & 31) >> 3, rl = threadIdx.x & 7;
     const uint32_t row = kt + ((mi & 1) * 8 + rl) * 128;
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-      for (int n = 0; n < NR; ++n) s[x][n][0] = s[x][n][1] = s[x][n][2] = s[x][n][3] = 0.f;
+    for (int x = 0; x < 2; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t a[2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) ldsm_x4(a[x], row + x * 2048 + (((2 * k + (mi >> 1)) ^ rl) << 4));
-      uint4 q[NR];
+      const uint4 q = qs[k * 32 + (threadIdx.x & 31)];
 #pragma unroll
-      for (int n = 0; n < NR; ++n) q[n] = qs[n * 128 + k * 32 + (threadIdx.x & 31)];
-      // all upper parts, then all lower ones: two products on one sum stay 2 NR apart
+      for (int x = 0; x < 2; ++x) mma_bf16(s[x], a[x], q.x, q.y);
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) mma_bf16(s[x][n], a[x], q[n].x, q[n].y);
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int x = 0; x < 2; ++x) mma_bf16(s[x][n], a[x], q[n].z, q[n].w);
+      for (int x = 0; x < 2; ++x) mma_bf16(s[x], a[x], q.z, q.w);
     }
   }
   // Where a score came out NaN, the upper parts' product alone: an infinite key keeps its sign there, where
   // hi + lo may add two infinities of opposite signs.
-  __device__ __forceinline__ static void mend(uint32_t kt, const uint4* qs, float (&s)[2][NR][4]) {
+  __device__ __forceinline__ static void mend(uint32_t kt, const uint4* qs, float (&s)[2][4]) {
     const int mi = (threadIdx.x & 31) >> 3, rl = threadIdx.x & 7;
     const uint32_t row = kt + ((mi & 1) * 8 + rl) * 128;
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float c[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int x = 0; x < 2; ++x) {
+      float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k) {
-          uint32_t a[4];
-          ldsm_x4(a, row + x * 2048 + (((2 * k + (mi >> 1)) ^ rl) << 4));
-          const uint4 q = qs[n * 128 + k * 32 + (threadIdx.x & 31)];
-          mma_bf16(c, a, q.x, q.y);
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (isnan(s[x][n][e])) s[x][n][e] = c[e];
+      for (int k = 0; k < 4; ++k) {
+        uint32_t a[4];
+        ldsm_x4(a, row + x * 2048 + (((2 * k + (mi >> 1)) ^ rl) << 4));
+        const uint4 q = qs[k * 32 + (threadIdx.x & 31)];
+        mma_bf16(c, a, q.x, q.y);
       }
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (isnan(s[x][e])) s[x][e] = c[e];
+    }
   }
   __device__ __forceinline__ void unit(uint32_t slot, const uint4* qs, uint32_t zero, int valid) {
     const int lane = threadIdx.x & 31, g = lane >> 2, mi = lane >> 3, rl = lane & 7;
-    float s[2][NR][4], sum[NR][2];
+    float s[2][4], sum[2];
     for (bool again = false;;) {  // a second time only where an infinite key made a NaN of hi + lo
       scores(slot, qs, s);
       if (again) mend(slot, qs, s);
@@ -195,110 +178,83 @@ struct Core<__nv_bfloat16, NR> {
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (16 * x + g + 8 * (e >> 1) >= valid) s[x][n][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e)
+            if (16 * x + g + 8 * (e >> 1) >= valid) s[x][e] = -INFINITY;
       }
       // the reference moves only when a score passes it by more than 8 (weights <= 256 until then), so
       // that the lanes of a row need not agree on a maximum for each unit
-      bool past = false;
-      float mx[NR][2];
+      float mx[2];
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
+      for (int e = 0; e < 2; ++e) mx[e] = fmaxf(fmaxf(s[0][e], s[0][2 + e]), fmaxf(s[1][e], s[1][2 + e]));
+      if (__any_sync(0xffffffffu, mx[0] > m[0] + 8.f || mx[1] > m[1] + 8.f)) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[n][e] = fmaxf(fmaxf(s[0][n][e], s[0][n][2 + e]), fmaxf(s[1][n][e], s[1][n][2 + e]));
-          past |= mx[n][e] > m[n][e] + 8.f;
+          float x = mx[e];
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          x = fmaxf(x, m[e]);
+          const float corr = m[e] == -INFINITY ? 1.f : ex2(m[e] - x);  // (nothing but zeros or a NaN yet)
+          m[e] = x;
+          l[e] *= corr;
+#pragma unroll
+          for (int d = 0; d < 4; ++d) {
+            o[d][e] *= corr;
+            o[d][2 + e] *= corr;
+          }
         }
-      if (__any_sync(0xffffffffu, past)) {
+      }
 #pragma unroll
-        for (int n = 0; n < NR; ++n)
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[e] == -INFINITY ? 0.f : m[e];  // no key yet: every weight is 0
+        sum[e] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float x = mx[n][e];
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            x = fmaxf(x, m[n][e]);
-            const float corr = m[n][e] == -INFINITY ? 1.f : ex2(m[n][e] - x);  // (nothing but zeros or a NaN yet)
-            m[n][e] = x;
-            l[n][e] *= corr;
+        for (int x = 0; x < 2; ++x)
 #pragma unroll
-            for (int d = 0; d < 4; ++d) {
-              o[n][d][e] *= corr;
-              o[n][d][2 + e] *= corr;
-            }
+          for (int h = 0; h < 2; ++h) {
+            s[x][2 * h + e] = ex2(s[x][2 * h + e] - ref);
+            sum[e] += s[x][2 * h + e];
           }
       }
-      bool bad = false;
-#pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float ref = m[n][e] == -INFINITY ? 0.f : m[n][e];  // no key yet: every weight is 0
-          sum[n][e] = 0.f;
-#pragma unroll
-          for (int x = 0; x < 2; ++x)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              s[x][n][2 * h + e] = ex2(s[x][n][2 * h + e] - ref);
-              sum[n][e] += s[x][n][2 * h + e];
-            }
-          bad |= isnan(sum[n][e]);
-        }
-      if (again || !__any_sync(0xffffffffu, bad)) break;
+      if (again || !__any_sync(0xffffffffu, isnan(sum[0]) || isnan(sum[1]))) break;
       again = true;
     }
-#pragma unroll
-    for (int n = 0; n < NR; ++n) {
-      l[n][0] += sum[n][0];
-      l[n][1] += sum[n][1];
-    }
+    l[0] += sum[0];
+    l[1] += sum[1];
     // O += V^T P: the weights turned from (key, row) to (row, key) 8 x 8 at a time
     const uint32_t vt = slot + kHalf;
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-      uint32_t ph[NR][2], pl[NR][2];
+      uint32_t ph[2], pl[2];
 #pragma unroll
-      for (int n = 0; n < NR; ++n)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t hi, lo;
-          split_bf16(s[x][n][2 * h], s[x][n][2 * h + 1], hi, lo);
-          ph[n][h] = transpose8x8(hi);
-          pl[n][h] = transpose8x8(lo);
-        }
+      for (int h = 0; h < 2; ++h) {
+        uint32_t hi, lo;
+        split_bf16(s[x][2 * h], s[x][2 * h + 1], hi, lo);
+        ph[h] = transpose8x8(hi);
+        pl[h] = transpose8x8(lo);
+      }
       const int key = 16 * x + (mi >> 1) * 8 + rl;
       const uint32_t row = key < valid ? vt + key * 128 : zero;
       uint32_t a[4][4];
 #pragma unroll
       for (int d = 0; d < 4; ++d) ldsm_x4_t(a[d], row + (((2 * d + (mi & 1)) ^ rl) << 4));
 #pragma unroll
-      for (int d = 0; d < 4; ++d)
+      for (int d = 0; d < 4; ++d) mma_bf16(o[d], a[d], ph[0], ph[1]);
 #pragma unroll
-        for (int n = 0; n < NR; ++n) mma_bf16(o[n][d], a[d], ph[n][0], ph[n][1]);
-#pragma unroll
-      for (int d = 0; d < 4; ++d)
-#pragma unroll
-        for (int n = 0; n < NR; ++n) mma_bf16(o[n][d], a[d], pl[n][0], pl[n][1]);
+      for (int d = 0; d < 4; ++d) mma_bf16(o[d], a[d], pl[0], pl[1]);
     }
   }
-  // the rows' sums over the lanes; the rows of own value i
+  // the rows' sums over the lanes
   __device__ __forceinline__ void finish() {
 #pragma unroll
-    for (int n = 0; n < NR; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 4);
-        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 8);
-        l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], 16);
-      }
+    for (int e = 0; e < 2; ++e) {
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 4);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 8);
+      l[e] += __shfl_xor_sync(0xffffffffu, l[e], 16);
+    }
   }
   __device__ __forceinline__ static bool leader() { return (threadIdx.x & 31) < 4; }
-  __device__ __forceinline__ static int own_row(int i) { return 8 * (i >> 1) + 2 * (threadIdx.x & 3) + (i & 1); }
-  __device__ __forceinline__ float own_max(int i) const { return m[i >> 1][i & 1]; }
-  __device__ __forceinline__ float own_sum(int i) const { return l[i >> 1][i & 1]; }
+  __device__ __forceinline__ static int own_row(int i) { return 2 * (threadIdx.x & 3) + i; }  // the row of m[i], l[i]
   // O of own value i into row `acc`: f times O, and `old` times what is there where `keep`; the loads of a
   // row first, so that they do not wait for one another's stores
   __device__ __forceinline__ void add_to(int i, float* acc, float old, bool keep, float f) const {
@@ -308,7 +264,7 @@ struct Core<__nv_bfloat16, NR> {
     for (int d = 0; d < 8; ++d) x[d] = keep ? acc[8 * d + g] : 0.f;
 #pragma unroll
     for (int d = 0; d < 8; ++d) {
-      const float y = o[i >> 1][d >> 1][2 * (d & 1) + (i & 1)] * f;
+      const float y = o[d >> 1][2 * (d & 1) + i] * f;
       acc[8 * d + g] = keep ? fmaf(x[d], old, y) : y;
     }
   }
@@ -316,9 +272,9 @@ struct Core<__nv_bfloat16, NR> {
 
 // float32, 16 query rows.  Lane (g, t): rows g and g + 8; of the scores keys 2t and 2t + 1 of each 8, of
 // O dims 2t and 2t + 1 of each 8.
-template <int NR>
-struct Core<float, NR> {
-  static constexpr int kRows = 16, kOwn = 2, UNIT = kUnitRows<float>, NT = UNIT / 8;
+template <>
+struct Core<float> {
+  static constexpr int kRows = 16, UNIT = kUnitRows<float>, NT = UNIT / 8;
   static constexpr int kQueryBytes = 8 * 2 * 512;  // [k-step of 8 dims][hi, lo][lane]
   float o[8][4], m[2], l[2];
 
@@ -491,8 +447,6 @@ struct Core<float, NR> {
   }
   __device__ __forceinline__ static bool leader() { return (threadIdx.x & 3) == 0; }
   __device__ __forceinline__ static int own_row(int i) { return 8 * i + ((threadIdx.x & 31) >> 2); }
-  __device__ __forceinline__ float own_max(int i) const { return m[i]; }
-  __device__ __forceinline__ float own_sum(int i) const { return l[i]; }
   __device__ __forceinline__ void add_to(int i, float* acc, float old, bool keep, float f) const {
     const int t = threadIdx.x & 3;
     float2 x[8];
@@ -508,17 +462,21 @@ struct Core<float, NR> {
 };
 
 // ------------------------------------------------------------------------------ the kernel --
-template <typename DT, int NR, int TILES>
+// Blocks an SM holds, by registers (an SM's four parts hold 512 a lane each: four warps of 128, three of 168) and shared
+// memory.  float32, 8 x 65536 rows: three blocks of 4 groups and 4 slots 205 us, two of 4 groups and 8 slots 286, two of
+// 7 groups and 7 slots 254 (a unit's feeding takes a feeder longer than its computing takes the groups).  With 32 query
+// rows two blocks take 333 us and three 317, but 64 rows, whose drafts leave room for two, 671 and 786; one task of 64 rows
+// on four tiles instead of two tasks 923.
+template <typename DT, int TILES>
 struct DtSmem {
-  using C = Core<DT, NR>;
-  static constexpr int kUnit = C::UNIT, kTaskCost = 12, kLeast = kDtWarps;
-  static constexpr int kRows = C::kRows * TILES, kGroups = kDtWarps / TILES;
-  // Blocks an SM holds, by registers (its four parts hold 512 a lane each: four warps of 128, three of
-  // 168) and shared memory.
-  static constexpr int kResident = sizeof(DT) == 2 && kRows <= 16 ? 3 : 2;
+  using C = Core<DT>;
+  static constexpr bool kHalves = sizeof(DT) == 2;
+  static constexpr int kUnit = C::UNIT, kTaskCost = 12, kLeast = 4;
+  static constexpr int kGroups = TILES == 1 ? 4 : 2, kCons = 32 * TILES * kGroups, kThreads = kCons + 32;
+  static constexpr int kRows = C::kRows * TILES;
+  static constexpr int kResident = TILES == 1 ? 3 : 2;
   // of the ring; a multiple of the groups, so that a slot is always the same group's
-  static constexpr int kSlots = TILES == 1 ? 8 : 4;
-  static constexpr int kRegs = kResident == 3 ? 128 : 168;
+  static constexpr int kSlots = kHalves ? 8 : 4;
   // byte offsets in dynamic shared memory (its base is 1024-byte aligned)
   static constexpr int kAcc = kSlots * kSlotBytes;
   static constexpr int kMax = kAcc + kRows * kAccStride * 4;
@@ -529,13 +487,13 @@ struct DtSmem {
   static size_t bytes(int B, int T) { return kDraft + static_cast<size_t>(T) * kD * 8 + schedule_bytes(B); }
 };
 
-template <typename DT, int NR, int TILES>
-__global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>::kRegs))
+template <typename DT, int TILES>
+__global__ void __launch_bounds__(DtSmem<DT, TILES>::kThreads, DtSmem<DT, TILES>::kResident)
     dense_tree_kernel(const __grid_constant__ DenseTreeArgs da, const __grid_constant__ CUtensorMap map_k,
                       const __grid_constant__ CUtensorMap map_v) {
-  using S = DtSmem<DT, NR, TILES>;
-  using C = Core<DT, NR>;
-  constexpr int UNIT = S::kUnit, ROWS = S::kRows, GROUPS = S::kGroups;
+  using S = DtSmem<DT, TILES>;
+  using C = Core<DT>;
+  constexpr int UNIT = S::kUnit, ROWS = S::kRows, GROUPS = S::kGroups, CONS = S::kCons;
   constexpr int kSlots = S::kSlots;
   static_assert(kSlots % GROUPS == 0, "a slot belongs to one group");
   extern __shared__ __align__(1024) unsigned char smem[];
@@ -562,7 +520,7 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
   if (static_cast<int>(blockIdx.x) >= sharing) return;
   const long long u0 = cut(cost, sharing, blockIdx.x), u1 = cut(cost, sharing, blockIdx.x + 1);
 
-  if (warp == kDtWarps) {
+  if (warp == CONS / 32) {
     feed<DT, S>(da, sch, u0, u1, &map_k, &map_v, smem, full_bar, empty_bar, &s_err);
     return;
   }
@@ -594,10 +552,10 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
       s_pos[r] = pos;
       C::load_query(a, qs, i, r < rows, row, pos);
     }
-    if (tail) stage_drafts<DT, kDtCons>(a, k, tree, s_draft, &ok);
-    cons_sync<kDtCons>();
+    if (tail) stage_drafts<DT, CONS>(a, k, tree, s_draft, &ok);
+    cons_sync<CONS>();
     if (tail)
-      attend_drafts<kDtCons>(a, k, tree, s_draft, r0, rows, s_acc, s_max + GROUPS * ROWS, s_sum + GROUPS * ROWS,
+      attend_drafts<CONS>(a, k, tree, s_draft, r0, rows, s_acc, s_max + GROUPS * ROWS, s_sum + GROUPS * ROWS,
                                  [&](int r, int lane4, float(&y)[16]) {
                                    int s;
                                    const size_t row = row_of(a, k, r0 + r, &s);
@@ -626,16 +584,16 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
     core.finish();
     if (C::leader()) {
 #pragma unroll
-      for (int i = 0; i < C::kOwn; ++i) {
-        s_max[grp * ROWS + C::kRows * tile + C::own_row(i)] = core.own_max(i);
-        s_sum[grp * ROWS + C::kRows * tile + C::own_row(i)] = core.own_sum(i);
+      for (int i = 0; i < 2; ++i) {
+        s_max[grp * ROWS + C::kRows * tile + C::own_row(i)] = core.m[i];
+        s_sum[grp * ROWS + C::kRows * tile + C::own_row(i)] = core.l[i];
       }
     }
-    cons_sync<kDtCons>();
+    cons_sync<CONS>();
     const int parts = GROUPS + (tail ? 1 : 0);
-    float f[C::kOwn], old[C::kOwn];
+    float f[2], old[2];
 #pragma unroll
-    for (int i = 0; i < C::kOwn; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int r = C::kRows * tile + C::own_row(i);
       float all = -INFINITY;
 #pragma unroll
@@ -643,79 +601,58 @@ __global__ void __launch_bounds__(kDtThreads) __maxnreg__((DtSmem<DT, NR, TILES>
       const bool drafts = tail && r < rows;
       const float md = drafts ? s_max[GROUPS * ROWS + r] : -INFINITY;
       all = fmaxf(all, md);
-      f[i] = weight_of(core.own_max(i), core.own_sum(i), all);
+      f[i] = weight_of(core.m[i], core.l[i], all);
       old[i] = grp > 0 ? 1.f : drafts ? weight_of(md, s_sum[GROUPS * ROWS + r], all) : 0.f;
     }
     for (int turn = 0; turn < GROUPS; ++turn) {
       if (grp == turn) {
 #pragma unroll
-        for (int i = 0; i < C::kOwn; ++i) {
+        for (int i = 0; i < 2; ++i) {
           const int r = C::kRows * tile + C::own_row(i);
           if (r < rows) core.add_to(i, s_acc + r * kAccStride, old[i], turn > 0 || tail, f[i]);
         }
       }
-      cons_sync<kDtCons>();
+      cons_sync<CONS>();
     }
     if (!ok) atomicExch(a.status, kStatusDeviceAssert);
-    if (!s_err) write_rows<DT, ROWS, kDtCons>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, parts);
-    cons_sync<kDtCons>();  // s_acc, s_max and s_sum are free again
+    if (!s_err) write_rows<DT, ROWS, CONS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, parts);
+    cons_sync<CONS>();  // s_acc, s_max and s_sum are free again
   }
 }
 
-// Calls f.template operator()<NR, TILES>() with the shape for `rows` query rows of a key head: as few
-// rows as hold them all, 64 at most.
-template <typename DT, typename F>
-auto with_shape(int rows, F&& f) {
-  if constexpr (sizeof(DT) == 4) {
-    if (rows <= 16) return f.template operator()<2, 1>();
-    if (rows <= 32) return f.template operator()<2, 2>();
-    return f.template operator()<2, 4>();
-  } else {
-    return f.template operator()<1, 1>();
-  }
-}
+template <typename DT, int TILES>
+constexpr int kGrid = 152 * DtSmem<DT, TILES>::kResident;  // 152 SMs
 
-template <typename DT, int NR, int TILES>
-constexpr int kGrid = 152 * DtSmem<DT, NR, TILES>::kResident;  // 152 SMs
-
-template <typename DT, int NR, int TILES>
+template <typename DT, int TILES>
 cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
-  using S = DtSmem<DT, NR, TILES>;
+  using S = DtSmem<DT, TILES>;
   DenseTreeArgs da = args;
-  da.blocks = kGrid<DT, NR, TILES>;
+  da.blocks = kGrid<DT, TILES>;
   da.split = reinterpret_cast<Split*>(da.part + static_cast<size_t>(da.blocks) * 2 * S::kRows * kDtPart);
   const TreeArgs& a = da.a;
   CUtensorMap mk, mv;
   cudaError_t e = maps_of(a, static_cast<int>(sizeof(DT)), S::kUnit, &mk, &mv);
   if (e != cudaSuccess) return e;
   const size_t smem = S::bytes(a.B, a.T);
-  e = cudaFuncSetAttribute(dense_tree_kernel<DT, NR, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  e = cudaFuncSetAttribute(dense_tree_kernel<DT, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  dense_tree_kernel<DT, NR, TILES><<<da.blocks, kDtThreads, smem, stream>>>(da, mk, mv);
+  dense_tree_kernel<DT, TILES><<<da.blocks, S::kThreads, smem, stream>>>(da, mk, mv);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_join<DT, S>(da, stream);
 }
 
-template <typename DT>
-size_t part_bytes(int rows) {
-  return with_shape<DT>(rows, []<int NR, int TILES>() {
-    return static_cast<size_t>(kGrid<DT, NR, TILES>) *
-           (2 * DtSmem<DT, NR, TILES>::kRows * kDtPart * sizeof(float) + sizeof(Split));
-  });
-}
-
-template <typename DT>
-cudaError_t launch_rows(const DenseTreeArgs& da, cudaStream_t stream) {
-  return with_shape<DT>(da.a.G * da.a.T, [&]<int NR, int TILES>() { return launch<DT, NR, TILES>(da, stream); });
+template <typename DT, int TILES>
+size_t part_bytes() {
+  return static_cast<size_t>(kGrid<DT, TILES>) * (2 * DtSmem<DT, TILES>::kRows * kDtPart * sizeof(float) + sizeof(Split));
 }
 
 }  // namespace
 
 size_t dense_tree_workspace_bytes(int B, int Hq, int H, int T, int dtype) {
   const int rows = Hq / H * T;
-  if (dtype == FIB_DTYPE_BF16 && rows > kMmaRows) return dense_tree_tc_bytes(rows);
-  return dtype == FIB_DTYPE_F32 ? part_bytes<float>(rows) : part_bytes<__nv_bfloat16>(rows);
+  if (dtype == FIB_DTYPE_F32) return rows <= 16 ? part_bytes<float, 1>() : part_bytes<float, 2>();
+  return rows <= kMmaRows ? part_bytes<__nv_bfloat16, 1>() : dense_tree_tc_bytes(rows);
 }
 
 cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long wait_ns, void* ws, cudaStream_t stream) {
@@ -725,8 +662,9 @@ cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long w
   da.wait_ns = wait_ns;
   da.split = nullptr;
   da.blocks = 0;
-  if (dtype == FIB_DTYPE_BF16 && a.G * a.T > kMmaRows) return launch_dense_tree_tc(da, stream);
-  return dtype == FIB_DTYPE_F32 ? launch_rows<float>(da, stream) : launch_rows<__nv_bfloat16>(da, stream);
+  const int rows = a.G * a.T;
+  if (dtype == FIB_DTYPE_F32) return rows <= 16 ? launch<float, 1>(da, stream) : launch<float, 2>(da, stream);
+  return rows <= kMmaRows ? launch<__nv_bfloat16, 1>(da, stream) : launch_dense_tree_tc(da, stream);
 }
 
 }  // namespace fibattn

@@ -164,6 +164,14 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];\n" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+      : "memory");
+}
+
 // ------------------------------------------------------------------------------ feeder --
 // For what is in flight when a block gives up: its wait is not the caller's, which may be too short for a copy.
 constexpr unsigned long long kDrainNs = 2000000000ull;
@@ -174,6 +182,7 @@ template <typename DT, typename P>
 __device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sch, long long u0, long long u1, const CUtensorMap* map_k,
                                      const CUtensorMap* map_v, unsigned char* ring, uint64_t* full_bar, uint64_t* empty_bar,
                                      volatile int* s_err) {
+  static_assert(sizeof(DT) == 2 || P::kUnit <= 16, "a unit's float32 rows are one copy: they lie in one page");
   constexpr int UNIT = P::kUnit, kSlots = P::kSlots, kHalf = UNIT * kD * static_cast<int>(sizeof(DT));
   const TreeArgs& a = da.a;
   const int lane = threadIdx.x & 31;
@@ -209,11 +218,12 @@ __device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sc
       __syncwarp();
       if (lane < boxes) {
         const uint32_t at = smem_addr(ring + slot * 2 * kHalf) + lane * box * 128;
-        tma_2d(at, map_k, 0, y, &full_bar[slot]);
-        tma_2d(at + kHalf, map_v, 0, y, &full_bar[slot]);
         if constexpr (sizeof(DT) == 4) {
-          tma_2d(at + kHalf / 2, map_k, 32, y, &full_bar[slot]);
-          tma_2d(at + kHalf + kHalf / 2, map_v, 32, y, &full_bar[slot]);
+          tma_3d(at, map_k, 0, y, 0, &full_bar[slot]);
+          tma_3d(at + kHalf, map_v, 0, y, 0, &full_bar[slot]);
+        } else {
+          tma_2d(at, map_k, 0, y, &full_bar[slot]);
+          tma_2d(at + kHalf, map_v, 0, y, &full_bar[slot]);
         }
       }
     }
@@ -449,7 +459,7 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// A layer's pool as a matrix of rows of 64 values; a copy takes `box` rows of 128 bytes.
+// A layer's pool as rows of 64 values (float32: as two halves of 32); a copy takes `box` rows, 128 bytes at a time.
 inline cudaError_t map_of(CUtensorMap* m, const void* pool, long long rows, int es, int box) {
   static const EncodeTiled encode = [] {
     void* fn = nullptr;
@@ -460,11 +470,11 @@ inline cudaError_t map_of(CUtensorMap* m, const void* pool, long long rows, int 
     return reinterpret_cast<EncodeTiled>(fn);
   }();
   if (encode == nullptr) return cudaErrorNotSupported;
-  const cuuint64_t dims[2] = {kD, static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(kD) * es};
-  const cuuint32_t boxes[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box)};
-  const cuuint32_t steps[2] = {1, 1};
-  const CUresult r = encode(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+  const cuuint64_t n = static_cast<cuuint64_t>(rows), row_bytes = static_cast<cuuint64_t>(kD) * es;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(128 / es), n, row_bytes / 128}, strides[2] = {row_bytes, 128};
+  const cuuint32_t boxes[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box), static_cast<cuuint32_t>(row_bytes / 128)};
+  const cuuint32_t steps[3] = {1, 1, 1};
+  const CUresult r = encode(m, es == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, es == 2 ? 2 : 3,
                             const_cast<void*>(pool), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
