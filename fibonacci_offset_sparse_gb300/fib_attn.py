@@ -401,13 +401,23 @@ def _raw_stream(stream, index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
+def _empty(cache: Cache, shape, dtype, stream, kept=True):
+    """A new tensor that a call on `stream` (None: the current one) writes: memory of that stream, which nothing
+    enqueued elsewhere still uses; where it is kept, the current stream's as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=cache.device)
+    here = torch.cuda.current_stream(cache.device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=cache.device)
+    if kept:
+        t.record_stream(here)
+    return t
+
+
 def _scratch(cache: Cache, workspace, need, stream):
-    """(address, bytes) of the caller's workspace, or of one of need() bytes (held for `stream`'s use)
-    and the tensor itself."""
+    """(address, bytes) of the caller's workspace, or of one of need() bytes, and the tensor itself."""
     if workspace is None:
-        workspace = torch.empty(max(need(), 1), dtype=torch.uint8, device=cache.device)
-        if stream is not None:
-            workspace.record_stream(stream)
+        workspace = _empty(cache, max(need(), 1), torch.uint8, stream, kept=False)
     elif workspace.get_device() != cache.index or not workspace.is_contiguous():
         raise ValueError(f"the workspace must be contiguous, on {cache.device}")
     return workspace.data_ptr(), workspace.nbytes, workspace
@@ -448,9 +458,7 @@ def fib_attn_cache_compact(cache: Cache, remap=None, workspace=None, stream=None
     """Moves the pages in use to the lowest ids (their number: cache.state[2]); returns remap int32
     [n_pages], the new id of each page, -1 for a free one."""
     if remap is None:
-        remap = torch.empty(cache.n_pages, dtype=torch.int32, device=cache.device)
-        if stream is not None:
-            remap.record_stream(stream)
+        remap = _empty(cache, cache.n_pages, torch.int32, stream)
     elif remap.shape != (cache.n_pages,) or _bad(remap, torch.int32, cache.index):
         raise ValueError(f"remap must be int32 [n_pages] on {cache.device}")
     at, size, workspace = _scratch(cache, workspace, lambda: fib_attn_cache_workspace_size(cache), stream)
@@ -475,18 +483,14 @@ def _tree_tensors(cache: Cache, q, k_new, v_new, parent, n_nodes, o, lse, want_l
     if n_nodes is not None and (n_nodes.shape != (B,) or _bad(n_nodes, torch.int32, index)):
         raise ValueError(f"n_nodes must be int32 [B] on {cache.device}")
     if o is None:
-        o = torch.empty_like(q)
-        if stream is not None:
-            o.record_stream(stream)
+        o = _empty(cache, shape, dtype, stream)
     elif o.shape != shape or _bad(o, dtype, index):
         raise ValueError(f"o must be like q, on {cache.device}")
     if lse is not None:
         if lse.shape != (B, Hq, T) or _bad(lse, torch.float32, index):
             raise ValueError(f"lse must be float32 [B, Hq, T] on {cache.device}")
     elif want_lse:
-        lse = torch.empty((B, Hq, T), dtype=torch.float32, device=cache.device)
-        if stream is not None:
-            lse.record_stream(stream)
+        lse = _empty(cache, (B, Hq, T), torch.float32, stream)
     return B, Hq, T, o, lse
 
 

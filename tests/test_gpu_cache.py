@@ -484,6 +484,121 @@ def test_an_infinite_key_that_is_attended():
     plan.close()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("T,H", [(1, 1), (8, 2), (9, 1), (24, 2), (40, 1), (64, 2), (64, 32)])
+def test_infinite_cached_keys(dtype, sign, T, H):
+    """A cached key whose dimension 0 is infinite scores +inf or -inf by the sign of the rotated query's dimension 0.
+    A node all of whose such scores are -inf is as without these keys; one that meets +inf has no softmax."""
+    r = rng(20, T, H)
+    lens, W = [300, 150], 12
+    c, ref, dev, host, parent, live = tree_case(r, dtype, lens, H, 1, T, 32, "roots", None, poison=False)
+    bad = [[0, 140, 299, 297], [149, 31]]  # the last ones lie in the window of a tree of roots
+    for b, rows in enumerate(bad):
+        for x in rows:
+            page = ref.table[b][x // 32]
+            c.k[:, page, :, x % 32] = 0
+            c.k[:, page, :, x % 32, 0] = sign * float("inf")
+    N = 400
+    plan = plan_for(N, W=W)
+    qf = host[0].copy()
+    up = np.stack([[[qf[b, h, s, 0] * np.cos(lens[b]) - qf[b, h, s, 32] * np.sin(lens[b]) for s in range(T)] for h in range(H)]
+                   for b in range(2)]) * sign > 0  # scores +inf
+    keys = {"sparse": keys_of(W, "mask", "fib", 1.0, N), "dense": None}
+    for name, o, l in both(plan, c, dev, parent=i32(parent), N=N):
+        meets = np.ones((2, H, T), bool)
+        want_o, want_l = np.zeros((2, H, T, 64)), np.zeros((2, H, T))
+        for b in range(2):
+            seen = range(lens[b]) if keys[name] is None else sorted({lens[b] - d for d, _ in keys[name] if 0 < d <= lens[b]})
+            meets[b] = any(x in bad[b] for x in seen)
+            seen = [x for x in seen if x not in bad[b]]
+            kr, vr = ref.rows(0, b)
+            for h in range(H):
+                for s in range(T):
+                    qr = co.turn(qf[b, h, s], lens[b])
+                    ks = np.concatenate([kr[seen, h], co.turn(host[1][b, h, s], lens[b])[None]])
+                    vs = np.concatenate([vr[seen, h], host[2][b, h, s][None]])
+                    x = ks @ qr / 8
+                    p = np.exp(x - x.max())
+                    want_o[b, h, s], want_l[b, h, s] = p @ vs / p.sum(), x.max() + np.log(p.sum())
+        none = up & meets
+        o, l = o.double().cpu().numpy(), l.double().cpu().numpy()
+        assert np.isnan(o[none]).all(), name
+        assert not np.isfinite(l[none]).any(), name
+        tol = TOL_O + (HALF[dtype] * np.abs(want_o) if dtype == "bf16" else 0)
+        assert np.all((np.abs(o - want_o) <= tol)[~none]), name
+        assert np.all((np.abs(l - want_l) <= TOL_LSE)[~none]), name
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    plan.close()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H", [(1, 2), (8, 1), (16, 2), (24, 1), (40, 2), (64, 1)])
+def test_the_most_sequences(dtype, T, H):
+    """As many sequences as a cache may have, most of them short or empty."""
+    r = rng(21, T)
+    B = 1024
+    lens = [int(x) for x in r.integers(0, 20, B)]
+    for b in r.integers(0, B, 5):
+        lens[b] = 200
+    nodes = [int(x) for x in r.integers(0, T + 1, B)]
+    c, ref, dev, host, parent, live = tree_case(r, dtype, lens, H, 1, T, 16, "random", nodes, poison=False)
+    plan = plan_for(300, W=8)
+    some = sorted({int(x) for x in r.integers(0, B, 40)} | {0, B - 1} | {b for b in range(B) if lens[b] == 200})
+    few = [n if b in some else 0 for b, n in enumerate(live)]
+    o, lse = sevens(dev[0])
+    o2, lse2 = sevens(dev[0])
+    fa.fib_attn_tree_decode(plan, 1, c, *dev, parent=i32(parent), n_nodes=i32(live), o=o, lse=lse)
+    fa.fib_attn_dense_tree_decode(plan, 1, c, *dev, parent=i32(parent), n_nodes=i32(live), o=o2, lse=lse2)
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    for x, l, keys in ((o, lse, keys_of(8, "mask", "fib", 1.0, 300)), (o2, lse2, None)):
+        ro, rl = co.tree_attend(ref, 1, *host, parent, few, keys)
+        check(x[some], l[some], ro[some], rl[some], [live[b] for b in some], dtype)
+        assert all(bool((x[b, :, n:] == 7).all()) and not bool((l[b, :, :n] == 7).any()) for b, n in enumerate(live))
+    plan.close()
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 16), ("bf16", 32), ("bf16", 64), ("f32", 5), ("f32", 30)])
+def test_a_wait_that_gives_up_is_reported(dtype, T):
+    """The shortest wait a plan takes, 1 us, is about as long as a read of the cache: the call ends, its result is right
+    or said not to be, and that of the next call with the usual wait is right."""
+    r = rng(22, T)
+    c, ref, dev, host, parent, live = tree_case(r, dtype, [60000], 4, 1, T, 64, "random", None, poison=False)
+    plan = plan_for(60100)
+    fa.fib_attn_plan_set_debug(plan, False, 1000)
+    want = co.tree_attend(ref, 0, *host, parent, live)
+    for usual in (False, True):
+        if usual:
+            fa.fib_attn_plan_set_debug(plan, False, 10 ** 9)
+        o, lse = fa.fib_attn_dense_tree_decode(plan, 0, c, *dev, parent=i32(parent))
+        status = fa.fib_attn_last_device_status(plan)
+        assert status == fa.FIB_OK or (status == fa.FIB_ERR_TIMEOUT and not usual)
+        if status == fa.FIB_OK:
+            check(o, lse, *want, live, dtype)
+    plan.close()
+
+
+def test_outputs_and_workspaces_of_a_call_on_another_stream():
+    """What a call allocates for a stream that it is given is that stream's memory: work that the current stream
+    still has to do on freed memory of its own does not meet it."""
+    r = rng(23)
+    c, ref, dev, host, parent, live = tree_case(r, "bf16", [3000, 2000], 4, 1, 16, 64, "random", None, poison=False)
+    plan, side = plan_for(3100), torch.cuda.Stream()
+    par = i32(parent)
+    want = [x.clone() for x in fa.fib_attn_dense_tree_decode(plan, 0, c, *dev, parent=par)]
+    big = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    size = fa.fib_attn_dense_tree_workspace_size(plan, c, 2, 4, 16)
+    for _ in range(5):
+        big.add_(1)  # the current stream is busy for a while
+        for shape, dt in ((size, torch.uint8), (dev[0].shape, torch.bfloat16), (dev[0].shape[:3], torch.float32)):
+            torch.empty(shape, dtype=dt, device="cuda").fill_(99)  # still to be written when it is freed
+        got = fa.fib_attn_dense_tree_decode(plan, 0, c, *dev, parent=par, stream=side)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    plan.close()
+
+
 @pytest.mark.parametrize("what", ["nodes", "negative", "parent", "self", "len", "position", "page id"])
 def test_a_bad_sequence_is_reported_and_the_others_are_right(what):
     r = rng(12)
