@@ -128,7 +128,7 @@ struct CommitArgs {
 
 // One block, a thread a sequence.
 __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_constant__ CommitArgs a) {
-  __shared__ int s_page[kMaxSeqs], s_first[kMaxSeqs], s_count[kMaxSeqs], s_off[kMaxSeqs];
+  __shared__ int s_page[kMaxSeqs], s_len[kMaxSeqs], s_first[kMaxSeqs], s_count[kMaxSeqs], s_off[kMaxSeqs];
   __shared__ int s_sums[33];
   let_second_start();
   const CacheDev& c = a.c;
@@ -163,19 +163,21 @@ __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_
       }
     }
   }
-  // shared last pages: who else writes into the same one
+  // shared last pages: who else writes into the same one.  The longest keeps it (the last of those), where all
+  // holders write: what the others copy from it lies in front of its new rows.
   s_page[b] = part && refs > 1 ? page : -1;
+  s_len[b] = len;
   const bool any_bad = __syncthreads_or(bad);
   bool copy = false;
   if (!any_bad && part && refs > 1) {
     int writers = 0;
-    bool last = true;
+    bool keeps = true;
     for (int o = 0; o < a.B; ++o)
       if (s_page[o] == page) {
         ++writers;
-        last &= o <= b;
+        keeps &= s_len[o] < len || (s_len[o] == len && o <= b);
       }
-    copy = !(writers == refs && last);
+    copy = !(writers == refs && keeps);
   }
   const int first = (len + c.P - 1) >> c.shift;
   const int fresh = n > 0 ? ((len + n + c.P - 1) >> c.shift) - first : 0;

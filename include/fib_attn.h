@@ -227,7 +227,8 @@ int fib_attn_decode(fib_attn_plan_t p, int layer, int B, int H, int N, int pos, 
  * RoPE is applied before the rows are gathered; rounded once, to that type) or V as given.
  * refs[p] counts the sequences that hold page p; a page is free iff refs[p] == 0.  Only pages
  * with refs[p] == 1 are written, so sequences may share pages (fib_attn_cache_fork); a caller
- * may hold a page itself by adding 1 to its count.  Table entries behind a sequence's pages
+ * may hold a page itself by adding 1 to its count, and one that shortens a sequence gives the
+ * pages behind it back itself (counts, and state[0]).  Table entries behind a sequence's pages
  * are ignored.  To start empty: lens, refs and state 0 (table -1 by custom).
  * state[0] is a lower bound of the lowest free page (0 always is one; a caller that writes
  * refs itself lowers it accordingly), state[1] a fib_status that the cache calls record (they
@@ -268,8 +269,8 @@ size_t fib_attn_cache_workspace_size(const fib_attn_cache* c);
  * both on the device.  Rotation uses the plan's RoPE tables (positions < its N_max).
  * Pages: in the order of b, a sequence whose partly filled last page is shared (refs > 1)
  * first takes a free page, copies the filled rows of every layer into it and lets go of the
- * shared one -- unless every holder of that page gains rows in this call, when the last of
- * them keeps it -- and then takes what it needs for its new rows; free pages are taken in
+ * shared one -- unless every holder of that page gains rows in this call, when the longest of
+ * them (the last of those) keeps it -- and then takes what it needs for its new rows; free pages are taken in
  * ascending order.  Rows of a page behind a sequence's last one are left as they were.
  * All or nothing: state[1] becomes FIB_ERR_NO_PAGES where too few pages are free, or
  * FIB_ERR_DEVICE_ASSERT for n_new outside [0, T], a path entry outside [0, T), a length that

@@ -39,16 +39,18 @@ class PagedCache:
         copies = []
         for page, seqs in holders.items():
             if self.refs[page] > 1:
-                copies += seqs[:-1] if len(seqs) == self.refs[page] else seqs
+                keeper = max(seqs, key=lambda b: (self.lens[b], b)) if len(seqs) == self.refs[page] else None
+                copies += [b for b in seqs if b != keeper]
         fresh = [self.pages(self.lens[b] + n) - self.pages(self.lens[b]) if n else 0 for b, n in enumerate(n_new)]
         free = [p for p, c in enumerate(self.refs) if c == 0]
         if len(copies) + sum(fresh) > len(free):
             return False
+        before = self.k.copy(), self.v.copy()
         for b, n in enumerate(n_new):
             j, rows = divmod(self.lens[b], P)
             if b in copies:
                 old, new = self.table[b][j], free.pop(0)
-                self.k[:, new, :, :rows], self.v[:, new, :, :rows] = self.k[:, old, :, :rows], self.v[:, old, :, :rows]
+                self.k[:, new, :, :rows], self.v[:, new, :, :rows] = before[0][:, old, :, :rows], before[1][:, old, :, :rows]
                 self.refs[old] -= 1
                 self.refs[new] = 1
                 self.table[b][j] = new

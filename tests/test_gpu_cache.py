@@ -141,6 +141,28 @@ def test_commit_copies_a_shared_last_page(writers, held):
     plan.close()
 
 
+@pytest.mark.parametrize("lens", [[18, 40, 25], [40, 18, 40], [47, 33, 34], [33, 34, 47]])
+def test_commit_of_sequences_that_were_shortened(lens):
+    """Holders of one page of different lengths all gain rows: the copies are of the page as it was."""
+    r = rng(24, *lens)
+    c, ref = make_cache(r, "f32", 2, 2, 16, [48, 48, 48], 6, share=[(1, 0, 3), (2, 0, 3)])
+    for b, n in enumerate(lens):  # as a caller does that takes back rejected rows
+        for j in range(ref.pages(n), ref.pages(48)):
+            ref.refs[ref.table[b][j]] -= 1
+            ref.table[b][j] = -1
+        ref.lens[b] = n
+    c.table.copy_(i32(ref.table))
+    c.lens.copy_(i32(ref.lens))
+    c.refs.copy_(i32(ref.refs))
+    c.state[0] = 0
+    kn, kf = draw(r, (2, 3, 2, 9, 64), "f32")
+    vn, vf = draw(r, (2, 3, 2, 9, 64), "f32")
+    fa.fib_attn_cache_commit(plan_for(), c, kn, vn, i32([9, 7, 9]))
+    assert ref.commit(kf, vf, [9, 7, 9])
+    same_tables(c, ref)
+    close_rows(c, ref, "f32")
+
+
 def test_commit_takes_the_lowest_free_pages_and_moves_its_bound():
     r = rng(3)
     P = 16
