@@ -14,8 +14,9 @@
 // A weight 0 times an infinity or NaN is NaN, so rows of which some value is not finite take the block to the
 // row-by-row path, as do trees so deep that the union does not fit even for 8 rows at a time.
 //
-// What bounds it: the latency of a block's steps (lengths and tree; pages; rows; three phases between barriers), two
-// blocks an SM; the tensor work is a quarter of that.
+// What bounds it: the latency of a block's steps (lengths and tree; tables; pages; rows; products, weights, products), two
+// blocks an SM by shared memory and registers: 64 sequences of 8 heads and 64 nodes are 512 blocks and take two rounds, 31
+// us for a floor of 4.4 (issue slots 37% busy, tensor pipes 18%).
 #include "tree.cuh"
 
 namespace fibattn {
@@ -54,7 +55,6 @@ struct TtSmem {
     int from[kTtMost];  // of a staged cached row: which of the pools' rows it is
   };
   unsigned char line[kMaxDrafts][kMaxDrafts];  // [s][d]: the ancestor d levels above node s
-  unsigned char depth[kMaxDrafts];
   unsigned char by_distance[kMaxDrafts];       // first key that reads the row at a distance
   int first[kMaxR + 1], at[kMaxR + 2];         // of the window's run (0) and the rungs': first cached row, place among the staged
   int step;
@@ -110,21 +110,8 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     if (tid == 0) atomicExch(a.status, kStatusDeviceAssert);
     return;
   }
-  if (warp < 2) {  // node `tid`
-    ts.depth[tid] = static_cast<unsigned char>(tree.depth[warp]);
-    if (tid < n) {
-      uint64_t left = tree.above[warp];
-      for (int d = 0; left != 0; ++d) {
-        const int u = 63 - __clzll(static_cast<long long>(left));
-        ts.line[tid][d] = static_cast<unsigned char>(u);
-        left &= ~(1ull << u);
-      }
-    }
-  }
   __syncthreads();
   const int W = a.t.W, nr = ts.ks.nr, nv = ts.ks.nv, drafts = (n + 15) & ~15;
-  if (tid < nv) ts.key[tid] = make_int4(ts.ks.lo[tid], ts.ks.need[tid], __float_as_int(ts.ks.w[tid]), 0);
-  __syncthreads();
   const uint32_t base = smem_addr(smem);
   bool bad = false;  // something staged is not finite
 
@@ -132,7 +119,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
   const int qr = 8 * warp + g;
   const int q_head = qr < rows ? (r0 + qr) / n : 0, q_node = qr < rows ? (r0 + qr) - q_head * n : 0;
   const size_t q_row = (static_cast<size_t>(b) * a.Hq + h * a.G + q_head) * a.T + q_node;
-  const int depth = ts.depth[q_node], pos = len + depth;  // of this lane's row, here and below
+  const int depth = pick32(tree.depth, q_node), pos = len + depth;  // of this lane's row, here and below
   uint32_t qx[2][2], qy[2][2];
   {
     const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + q_row * kD) + t;
@@ -145,6 +132,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
       }
   }
   const int du = tid >> 2;  // 64 quads: every drafted row at once
+  const int d_pos = len + pick32(tree.depth, du);
   uint4 dk[2], dv[2];
   dk[0] = dk[1] = dv[0] = dv[1] = make_uint4(0, 0, 0, 0);
   if (du < n) {
@@ -158,13 +146,15 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
   }
 
   // The union of the cached rows of `step` query rows from `from` on: its runs' places; returns the number of staged
-  // rows.  By warp 0: lane c has run c (0: the window, c: rung c - 1).
-  auto plan_runs = [&](int from, int step) {
+  // rows.  By one warp: lane c has run c (0: the window, c: rung c - 1).  key(c): distance and weight of key c.
+  auto plan_runs = [&](int from, int step, auto&& key) {
     int lowest = 64, highest = 0;
-    for (int r = from + lane; r < min(from + step, rows); r += 32) {
-      const int d = ts.depth[(r0 + r) % n];
-      lowest = min(lowest, d);
-      highest = max(highest, d);
+    for (int x = from; x < min(from + step, rows); x += 32) {
+      const int r = min(x + lane, rows - 1), d = pick32(tree.depth, (r0 + r) % n);
+      if (x + lane < min(from + step, rows)) {
+        lowest = min(lowest, d);
+        highest = max(highest, d);
+      }
     }
     lowest = __reduce_min_sync(0xffffffffu, lowest);
     highest = __reduce_max_sync(0xffffffffu, highest);
@@ -176,8 +166,8 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
         first = max(0, len + lowest - (W - 1));
         count = max(0, len - first);
       } else if (c <= nr) {
-        const int4 k = ts.key[W + c - 1];
-        const int lo = k.x, two = __int_as_float(k.z) > 0.f ? 1 : 0;
+        float w;
+        const int lo = key(W + c - 1, w), two = w > 0.f ? 1 : 0;
         first = max(0, len + lowest - lo - two);
         count = max(0, min(len - 1, len + highest - lo) - first + 1);
       }
@@ -196,25 +186,40 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     if (lane == 0) ts.at[nr + 1] = total;
     return total;
   };
-  if (warp == 0) {  // the most rows at a time whose union fits, in two steps at most (more leave most warps idle too long)
+  // the tables, a warp or two each: nodes, runs, distances, keys
+  if (warp < 2) {  // node `tid`
+    if (tid < n) {
+      uint64_t left = tree.above[warp];
+      for (int d = 0; left != 0; ++d) {
+        const int u = 63 - __clzll(static_cast<long long>(left));
+        ts.line[tid][d] = static_cast<unsigned char>(u);
+        left &= ~(1ull << u);
+      }
+    }
+  } else if (warp == 2) {  // the most rows at a time whose union fits, in two steps at most (more leave most warps idle too long)
     int step = kTtRows;
     for (; step >= 8 && 2 * step >= rows; step >>= 1) {
       bool fits = true;
-      for (int from = 0; from < rows && fits; from += step) fits = plan_runs(from, step) <= shape.keys;
+      for (int from = 0; from < rows && fits; from += step) fits = plan_runs(from, step, [&](int c, float& w) {
+          w = ts.ks.w[c];
+          return ts.ks.lo[c];
+        }) <= shape.keys;
       if (fits) break;
     }
     if (lane == 0) ts.step = step >= 8 && 2 * step >= rows ? step : 0;
-  } else if (warp < 3) {  // the first key that reads the row at distance d: keys are in the order of lo, and read lo and lo + 1
-    const int d = tid - 32;
+  } else if (warp < 5) {  // the first key that reads the row at distance d: keys are in the order of lo, and read lo and lo + 1
+    const int d = tid - 96;
     int c = 0, end = nv;
     while (c < end) {
       const int mid = (c + end) >> 1;
-      if (ts.key[mid].x + 1 < d)
+      if (ts.ks.lo[mid] + 1 < d)
         c = mid + 1;
       else
         end = mid;
     }
     ts.by_distance[d] = static_cast<unsigned char>(c);
+  } else {
+    for (int c = tid - 160; c < nv; c += kTtThreads - 160) ts.key[c] = make_int4(ts.ks.lo[c], ts.ks.need[c], __float_as_int(ts.ks.w[c]), 0);
   }
 
   // ---- query fragments (hi, lo) of the warp's 8 rows, in registers
@@ -241,7 +246,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
       x[2 * i] = bf_lo(w[i]);
       x[2 * i + 1] = bf_hi(w[i]);
     }
-    rope_row(a.rope_lo, a.rope_hi, du < n ? len + ts.depth[du] : 0, t, e);
+    rope_row(a.rope_lo, a.rope_hi, du < n ? d_pos : 0, t, e);
     rotate_part(x, e, false);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -264,7 +269,11 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
   for (; from < rows && step > 0; from += step) {
     if (step < rows) {  // (else the plan of the only step stands)
       __syncthreads();
-      if (warp == 0) plan_runs(from, step);
+      if (warp == 0)
+        plan_runs(from, step, [&](int c, float& w) {
+          w = __int_as_float(ts.key[c].z);
+          return ts.key[c].x;
+        });
       __syncthreads();
     }
     const int total = ts.at[nr + 1], padded = (total + 15) & ~15;
@@ -466,9 +475,9 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
 
 }  // namespace
 
-// A block takes some 11 us whatever its rows, and 304 run at a time; row by row takes 4.5 us and 2.6 ns a row of the
-// whole batch.  Measured (us here, row by row): 512 blocks of 64 rows 32 and 87, of 16 rows 21.5 and 26, of 12 rows 21.7 and
-// 20.4; 128 blocks of 64 rows 12.7 and 25, of 16 rows 10.3 and 8.7; 32 blocks of 64 rows 12.3 and 8.2.
+// A block takes some 10 us whatever its rows, and 304 run at a time; row by row takes 4.5 us and 2.6 ns a row of the
+// whole batch.  Measured (us here, row by row): 512 blocks of 64 rows 31 and 87, of 16 rows 20 and 26, of 12 rows 21 and
+// 20; 128 blocks of 64 rows 12.7 and 25, of 16 rows 10.3 and 8.7; 32 blocks of 64 rows 12.3 and 8.2.
 // A chain's union grows with its length: it fits for 12 nodes of the Fibonacci base's distances, more are served row by
 // row.  (Deep trees that are given by their parents are found on the device only; they take 1.3 times the time then.)
 bool tree_tc_serves(const TreeArgs& a) {
