@@ -77,6 +77,12 @@ __device__ __forceinline__ void mma_tc(uint32_t d, uint64_t a, uint64_t b, uint3
 __device__ __forceinline__ void commit_tc(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n" ::"r"(smem_addr(bar)) : "memory");
 }
+// One lane of the warp, which the compiler can tell is one: the products' operands then need no loop over lanes.
+__device__ __forceinline__ bool one_lane() {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;\n" ::: "memory"); }
 __device__ __forceinline__ void fence_smem() { asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory"); }
@@ -277,7 +283,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
     feed_tiles<P>(da, sch, u0, u1, &map_k, &map_v, smem, bars.full, bars.empty, &s_err);
   } else if (warp == kIssuer) {
     // =================================================================== products
-    if (lane == 0) {
+    if (one_lane()) {
       constexpr uint32_t kScores = product_of(128, ROWS, false, false), kValues = product_of(64, ROWS, true, true);
       // two cursors over the units of the run: the next S, the next O += V P
       struct Cursor {
