@@ -237,6 +237,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
   __shared__ __align__(8) TcBars bars;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_err;
+  __shared__ volatile long long s_run[2], s_place;  // the block's run; where in it the softmax warps are
   const TreeArgs& a = da.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -271,6 +272,10 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
   const int sharing = sharing_blocks(cost, da.blocks, P::kLeast);
   if (static_cast<int>(blockIdx.x) >= sharing) return;
   const long long u0 = cut(cost, sharing, blockIdx.x), u1 = cut(cost, sharing, blockIdx.x + 1);
+  if (tid == 0) {
+    s_run[0] = u0;
+    s_run[1] = u1;
+  }
   if (warp == kIssuer) tmem_alloc(&s_tmem, P::kColumns);
   fence_before();
   __syncthreads();
@@ -363,7 +368,6 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
     float* s_warp = reinterpret_cast<float*>(smem + P::kWarpMax);
     float* s_draft = reinterpret_cast<float*>(smem + P::kWeights);  // before a piece's weights
     float* s_part = reinterpret_cast<float*>(smem + P::kWeights);   // after them: [ROWS][128] sums, then O
-    float* drafts = da.part + static_cast<size_t>(da.blocks) * 2 * ROWS * kDtPart + static_cast<size_t>(blockIdx.x) * ROWS * kAccStride;  // the drafted keys' O
     const int group = warp >> 2, g0 = group * GR, key = tid & 127, wq = warp & 3;  // the thread's query rows and key
     const uint32_t lanes = static_cast<uint32_t>(wq) << 21;                        // its warp's lanes of tensor memory
     int count = 0;
@@ -372,19 +376,30 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       s_err = 1;
       atomicExch(a.status, kStatusTimeout);
     };
-    // The task at u, formed anew where it is needed: its fields would hold registers over the loop below.
-    auto task_at = [&](long long u) {
-      asm volatile("" : "+l"(u));
-      return task_of<P>(a, sch, u, u1);
+    // Of a piece, formed anew from shared memory where they are needed: held over the units' loop they would cost it
+    // spills, and what shared memory leaves of L1 does not hold those (64 rows: 297 us with them, @@ without).
+    auto task_here = [&] { return task_of<P>(a, sch, s_place, s_run[1]); };
+    auto drafts_here = [&] {  // the drafted keys' O
+      uint32_t block;
+      asm volatile("mov.u32 %0, %%ctaid.x;\n" : "=r"(block));
+      return da.part + static_cast<size_t>(da.blocks) * 2 * ROWS * kDtPart + static_cast<size_t>(block) * ROWS * kAccStride;
     };
-    for (long long u = u0, after; u < u1; u = after) {
-      const Task k = task_at(u);
-      after = k.start + k.units + P::kTaskCost;
-      if (k.first == k.last) continue;
-      if (tid == 0) note_split<P>(da, k, cost, sharing, u0);
+    for (long long u = s_run[0]; u < s_run[1];) {
+      const Task k = task_of<P>(a, sch, u, s_run[1]);
+      if (k.first == k.last) {
+        u = k.start + k.units + P::kTaskCost;
+        continue;
+      }
+      if (tid == 0) s_place = u;
+      if (tid == 0) {
+        const long long all = *static_cast<volatile long long*>(sch.start + a.B);
+        note_split<P>(da, k, all, sharing_blocks(all, da.blocks, P::kLeast), s_run[0]);
+      }
+      const int k_first = k.first, k_last = k.last, k_len = k.len;
+      const int mine = min(GR, max(0, a.G * k.n - k.rb * ROWS - g0));  // rows of this group
+      {
       const bool tail = k.last == k.units;
-      const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0), k_first = k.first, k_last = k.last, k_len = k.len;
-      const int mine = min(GR, max(0, rows - g0));  // rows of this group
+      const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);
       bool ok = true;
       const WarpTree tree = warp_tree(a, k.b, k.n, &ok);
       // the rotated query: a quad a row, 16 bytes of hi and of lo for 8 dims
@@ -420,7 +435,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       if (tail) stage_drafts<__nv_bfloat16, CONS>(a, k, tree, s_draft, &ok);
       cons_sync<CONS>();
       if (tail) {
-        attend_drafts<CONS>(a, k, tree, s_draft, r0, rows, drafts, s_max + ROWS, s_sum + ROWS, [&](int r, int t, float(&y)[16]) {
+        attend_drafts<CONS>(a, k, tree, s_draft, r0, rows, drafts_here(), s_max + ROWS, s_sum + ROWS, [&](int r, int t, float(&y)[16]) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const unsigned char* at = smem + P::kQuery + r * 128 + (((t + 4 * h) ^ (r & 7)) << 4);
@@ -434,6 +449,8 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           }
         });
         cons_sync<CONS>();  // the drafted keys' room is the weights' room
+      }
+      if (!ok) atomicExch(a.status, kStatusDeviceAssert);
       }
 
       float l[GR];
@@ -472,7 +489,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
 #pragma unroll
           for (int r = 0; r < GR; ++r) bad |= r < mine && isnan(x[r]);
           if (bad) {
-            const Task now = task_at(u);
+            const Task now = task_here();
             const long long at = cache_row(a, now.b, now.h, i * P::kUnit + key);  // (the tile's slot may hold another by now)
 #pragma unroll 1
             for (int r = 0; r < mine && at >= 0; ++r) {
@@ -550,6 +567,9 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
         if (lane == 0) mbar_arrive(&bars.weights);
       }
       // ---- the run's O, sums and references; with the drafted keys' part, in a fixed order
+      const Task done = task_here();
+      const bool tail = done.last == done.units;
+      const int r0 = done.rb * ROWS, rows = min(ROWS, a.G * done.n - r0);
       wait(&bars.added, (count - 1) & 1);
       fence_after();
       float o[GR];
@@ -590,6 +610,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       cons_sync<CONS>();
       if (lane < 16) {  // 16 rows of O^T lie in a warp's first 16 lanes
         const int at = g0 * kAccStride + 16 * wq + lane;
+        const float* drafts = drafts_here();
         float d[GR];  // (every load before a store, which it might seem to depend on)
 #pragma unroll
         for (int r = 0; r < GR; ++r) d[r] = tail && r < mine ? drafts[at + r * kAccStride] : 0.f;
@@ -609,9 +630,8 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       }
       fence_before();
       cons_sync<CONS>();
-      if (!ok) atomicExch(a.status, kStatusDeviceAssert);
-      const Task done = task_at(u);
-      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, done, tail && done.first == 0, done.start >= u0 ? 1 : 0, r0, rows, s_part, s_max, s_sum, 1);
+      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, done, tail && done.first == 0, done.start >= s_run[0] ? 1 : 0, r0, rows, s_part, s_max, s_sum, 1);
+      u = done.start + done.units + P::kTaskCost;
       cons_sync<CONS>();  // everything of the piece is free again
     }
   }
