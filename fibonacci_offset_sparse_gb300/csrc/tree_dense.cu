@@ -3,7 +3,9 @@
 // O_s = sum_j p_sj v_j, p = softmax(q'_s . k'_j / 8).
 //
 // What bounds it: every cached row is read once for all nodes and query heads of its key head, so up to some
-// 64 rows of queries a key the read of the cache from HBM is the floor.
+// 64 rows of queries a key the read of the cache from HBM is the floor.  16 sequences x 8 heads x 65536 rows, one
+// query: 168 us, 6.6 TB/s (98% of a measured copy).  float32, 8 x 8 x 65536: 205 us, 5.4 TB/s, what three blocks' rings
+// hold in flight.  A call of one sequence is 9 us of launches, lengths, query, first copies and join.
 //
 // Work: a unit is kUnit consecutive cached rows of one task; a task is a (sequence, key head, block of
 // ROWS query rows) and costs its units and kTaskCost more, what a block spends before and after
@@ -33,8 +35,8 @@ namespace fibattn {
 
 namespace {
 
-// bf16: up to so many query rows here, more in tree_dense_tc.cu.  16 x 65536 cached rows: 8 rows 168 us here and 183 us
-// there, 16 rows 283 and 184; 4096 rows, one query 11.9 and 16.1.
+// bf16: up to so many query rows here, more in tree_dense_tc.cu.  8 rows over 16 x 65536 cached ones take 169 us here and 168
+// there, over 32 x 1024 17.2 and 21.9; one query over 4096 11.9 and 16.1; 16 rows over 16 x 65536 283 here and 172 there.
 constexpr int kMmaRows = 8;
 constexpr int kSlotBytes = 8192;  // K and V of a unit
 constexpr int kHalf = kSlotBytes / 2;

@@ -2,8 +2,9 @@
 // work, its cut and its join as in tree_dense.cu, the products on the 5th-generation tensor cores.
 //
 // What bounds it: the read of the cache, as there.  With mma.sync the products alone took as long as the
-// read from some 24 query rows on; here a unit of 128 keys costs its SM about 500 tensor cycles for any
-// number of rows up to 64, a third of the time its 32 KB take from HBM.
+// read from some 24 query rows on; here the tensor pipes are busy for a fifth of the time.  16 sequences x 8 heads x
+// 65536 rows: 16 query rows 172 us, 24 rows 176 (6.3 TB/s, 93% of a measured copy), 32 rows 178; 48 rows 208 and 64 rows
+// 240, where one block an SM is bound by the steps of its softmax warps.
 //
 // Per unit of 128 cached rows, with the keys as the 128 rows of the accumulator:
 //   S^T [128 keys x ROWS] = K Q'^T    K from the ring as TMA left it (K-major, 128-byte swizzle), the rotated
