@@ -451,7 +451,9 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const __grid
 }
 
 constexpr int kMoveThreads = 256;
-constexpr int kMoveVecs = 8;  // 16-byte words a thread has in flight
+// 16-byte words a thread has in flight.  Half of 1024 pages of 16 layers, 1.07 GB read and written: 4 182 us, 8 171, 16 168
+// (6.4 TB/s).
+constexpr int kMoveVecs = 16;
 
 __global__ void __launch_bounds__(kMoveThreads) compact_move_kernel(const __grid_constant__ CompactArgs a, int page_vecs) {
   wait_for_first();

@@ -17,7 +17,7 @@
 // 8 (weights <= 256 until then): one vote of four warps a unit; the exact maximum, and O rescaled, are the
 // exception's work.
 //
-// Block: softmax warps (warp w reads lanes 32 (w % 4) .. of tensor memory; four warps share 8 or 16 query
+// Block: softmax warps (warp w reads lanes 32 (w % 4) .. of tensor memory; four warps share 16 query
 // rows), the feeder, and a warp whose one thread issues the products as their operands arrive: S of the next
 // unit runs while a unit's weights are formed.
 #include "tree_dense.cuh"
@@ -33,10 +33,11 @@ struct TcShape {
   // Task cost: 256 tasks of 64 rows over 4096 cached ones take 66 us at 12, 77 at 8 and 68 at 16; 16 x 65536 177, 182, 178.
   static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 12, kLeast = 1;
   static constexpr int kSlotBytes = kUnit * kD * 2;  // K or V of a unit
-  static constexpr int kGroupRows = ROWS == 16 ? 8 : 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
+  static constexpr int kGroupRows = 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
   static constexpr int kCons = 128 * kGroups, kThreads = kCons + 64;
-  // Two blocks an SM where the rest beside their rings is small.  What is on its way from memory is what the
-  // ring holds, so it takes what shared memory is left: K's slot is free once the scores are formed.
+  // Two blocks an SM where the rest beside their rings is small: 16 x 65536 rows, 16 query rows 172 us (one block of 9
+  // slots 179), 32 rows 178 (185); 32 x 2048, 16 rows 27 (35).  What is on its way from memory is what the ring holds, so
+  // it takes what shared memory is left: K's slot is free once the scores are formed.
   static constexpr int kResident = ROWS <= 32 ? 2 : 1;
   static constexpr int kSlots = ROWS <= 32 ? 5 : 9;
   static constexpr int kColumns = ROWS == 16 ? 64 : ROWS == 32 ? 128 : 256;  // of tensor memory: S twice, O
