@@ -359,6 +359,8 @@ def fib_attn_cache_create(n_layers: int, heads: int, page_rows: int, n_pages: in
         device = k.device
     if device.type != "cuda":
         raise ValueError("the cache lives on a CUDA device")
+    if dtype not in _DT:
+        raise ValueError("the cache holds float32 or bfloat16")
     if device.index is None:
         device = torch.device("cuda", torch.cuda.current_device())
     k = torch.zeros(shape, dtype=dtype, device=device) if k is None else k

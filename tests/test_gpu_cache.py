@@ -695,6 +695,8 @@ def test_refusals_of_the_binding_and_the_library():
         fa.fib_attn_cache_compact(c, remap=i32([0]))
     with pytest.raises(fa.FibAttnError):
         fa.fib_attn_cache_create(1, 1, 24, 4, 1, 1, torch.float32)
+    with pytest.raises(ValueError):
+        fa.fib_attn_cache_create(1, 1, 16, 4, 1, 1, torch.float16)
     plan.close()
 
 
