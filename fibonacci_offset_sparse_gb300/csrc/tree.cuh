@@ -5,6 +5,12 @@
 
 namespace fibattn {
 
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // The nodes of one sequence's tree over the lanes of a warp: lane x holds nodes x and x + 32.
 // above[i]: bit u is set where node u is the node itself or one of its ancestors; since a parent has
 // a smaller number than its child, ancestors lie nearer the higher their bit.

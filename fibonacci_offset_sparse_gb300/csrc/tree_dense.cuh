@@ -134,11 +134,6 @@ __device__ __forceinline__ Task task_of(const TreeArgs& a, const Schedule& s, lo
 }
 
 // ------------------------------------------------------------------------------ small pieces --
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 // x0, x1 as bf16 pairs hi + lo
 __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf2_rn(x0, x1);

@@ -365,11 +365,15 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
         float x[4], y[4], w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
+          // (no branches: both rows' places are looked up for every key, in bounds where it is none)
           const int4 kk = ts.key[min(c0 + 4 * j, nv - 1)];
           const bool on = in && c0 + 4 * j < nv && pos >= kk.y;
+          const int above0 = line[min(kk.x, kMaxDrafts - 1)], above1 = line[min(kk.x + 1, kMaxDrafts - 1)];
+          const int at0 = kk.x <= depth ? above0 : kk.w + pos, at1 = kk.x < depth ? above1 : kk.w + pos - 1;
           w[j] = on ? __int_as_float(kk.z) : 0.f;
-          x[j] = on ? __uint_as_float(row[kk.x <= depth ? line[kk.x] : kk.w + pos]) : -INFINITY;
-          y[j] = w[j] > 0.f ? __uint_as_float(row[kk.x < depth ? line[kk.x + 1] : kk.w + pos - 1]) : 0.f;
+          x[j] = __uint_as_float(row[on ? at0 : 0]);
+          y[j] = __uint_as_float(row[w[j] > 0.f ? at1 : 0]);
+          if (!on) x[j] = -INFINITY;
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           kk[j] = ts.key[min(c0 + 4 * j, nv - 1)];
-          p[j] = c0 + 4 * j < nv ? exp2f(key[c0 + 4 * j] - m) : 0.f;  // (of a row that is none NaN, which nobody reads)
+          p[j] = c0 + 4 * j < nv ? ex2(key[min(c0 + 4 * j, nv - 1)] - m) : 0.f;  // (of a row that is none NaN, which nobody reads)
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -412,11 +416,15 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
       if (in)
         for (int d = t; d <= depth; d += 4) {
           float x = 0.f;
-          for (int c = ts.by_distance[d]; c < nv; ++c) {
-            const int4 kk = ts.key[c];
-            if (kk.x > d) break;
-            const float w = __int_as_float(kk.z);
-            x += key[c] * (kk.x == d ? 1.f - w : w);
+          for (int c = ts.by_distance[d], more = 1; more; c += 3) {  // seldom more than two: three at a time
+#pragma unroll
+            for (int j = 0; j < 3; ++j) {
+              const int at = min(c + j, nv - 1);
+              const int4 kk = ts.key[at];
+              const float w = __int_as_float(kk.z), p = key[at] * (kk.x == d ? 1.f - w : w);
+              more = c + j < nv && kk.x <= d;
+              if (more) x += p;
+            }
           }
           row[line[d]] = split1(x);
         }
