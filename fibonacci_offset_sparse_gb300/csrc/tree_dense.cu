@@ -516,7 +516,7 @@ __global__ void __launch_bounds__(DtSmem<DT, TILES>::kThreads, DtSmem<DT, TILES>
   if (tid < 32) reinterpret_cast<float*>(smem + S::kZero)[tid] = 0.f;
   const Schedule sch = schedule_at(smem + S::kDraft + a.T * kD * 8, a.B);
   build_schedule<S>(a, sch);
-  if (tid == 0) da.split[blockIdx.x].parts = 0;
+  if (tid == 0) clear_splits(da);
   const long long cost = sch.start[a.B];
   const int sharing = sharing_blocks(cost, da.blocks, S::kLeast);
   if (static_cast<int>(blockIdx.x) >= sharing) return;
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(DtSmem<DT, TILES>::kThreads, DtSmem<DT, TILES>
     const Task k = task_of<S>(a, sch, u, u1);
     u = k.start + k.units + S::kTaskCost;
     if (k.first == k.last) continue;
-    if (tid == 0) note_split<S>(da, k, cost, sharing, u0);
+    if (tid == 0) note_split<S>(da, k, cost, sharing);
     const bool tail = k.last == k.units, whole = tail && k.first == 0;
     const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);  // row r0 + i is (query head, node)
     bool ok = true;
@@ -646,7 +646,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
 
 template <typename DT, int TILES>
 size_t part_bytes() {
-  return static_cast<size_t>(kGrid<DT, TILES>) * (2 * DtSmem<DT, TILES>::kRows * kDtPart * sizeof(float) + sizeof(Split));
+  return static_cast<size_t>(kGrid<DT, TILES>) * (2 * DtSmem<DT, TILES>::kRows * kDtPart * sizeof(float) + 2 * sizeof(Split));
 }
 
 }  // namespace

@@ -13,18 +13,20 @@ namespace fibattn {
 constexpr int kAccStride = 68;   // floats of a row of O in shared memory
 constexpr int kDtPart = kD + 2;  // floats of a partial's row: O, max, sum
 
-// A task whose units several blocks hold, as the first of them leaves it for the join.
+// A task whose units several blocks hold, as each of them leaves it for the join: [0] the one that its run begins
+// with, [1] the one that it is the first block of.
 struct Split {
   int parts;  // 0: none
+  int first;  // block; the others follow it
   int slot;   // of the first block's partial; the others' lie in slot 0
   int b, h, rb, n;
-  int unused[2];
+  int unused;
 };
 
 struct DenseTreeArgs {
   TreeArgs a;
   float* part;   // [blocks][2][ROWS][kDtPart]
-  Split* split;  // [blocks]
+  Split* split;  // [blocks][2]
   unsigned long long wait_ns;
   int blocks;   // blocks of the grid
 };
@@ -359,86 +361,131 @@ __device__ __forceinline__ void write_rows(const DenseTreeArgs& da, const Task& 
 }
 
 // ------------------------------------------------------------------------------ join --
-// Whether this block is the first of several that hold task k's units, and how many those are (one thread,
-// for each piece).
+// Notes task k where other blocks hold units of it too (one thread, for each piece).
 template <typename P>
-__device__ __forceinline__ void note_split(const DenseTreeArgs& da, const Task& k, long long cost, int sharing, long long u0) {
-  if (k.first > 0 || k.last == k.units) return;
-  const int last = block_at(cost, sharing, k.start + P::kTaskCost + k.units - 1);
-  da.split[blockIdx.x] = Split{last - static_cast<int>(blockIdx.x) + 1, k.start >= u0 ? 1 : 0, k.b, k.h, k.rb, k.n, {0, 0}};
+__device__ __forceinline__ void note_split(const DenseTreeArgs& da, const Task& k, long long cost, int sharing) {
+  if (k.first == 0 && k.last == k.units) return;
+  const long long begin = k.start + P::kTaskCost;
+  const int first = block_at(cost, sharing, begin), last = block_at(cost, sharing, begin + k.units - 1);
+  da.split[2 * blockIdx.x + (k.first == 0 ? 1 : 0)] =
+      Split{last - first + 1, first, k.start >= cut(cost, sharing, first) ? 1 : 0, k.b, k.h, k.rb, k.n, 0};
 }
+__device__ __forceinline__ void clear_splits(const DenseTreeArgs& da) { da.split[2 * blockIdx.x].parts = da.split[2 * blockIdx.x + 1].parts = 0; }
 
-// Adds the partials of the tasks whose units several blocks hold.  Block (c, y) serves 4 rows of the task that
-// block c is the first of.  16 threads read a row of a partial; a row has four such teams, which take every fourth
-// partial and meet in order.  The weights come first, so that the loads of O do not wait for one another.
+// Adds the partials of the tasks whose units several blocks hold.  As many blocks as hold a task share its rows here, so
+// that the work is spread however few the tasks are.  16 threads read a row of a partial.  Up to 16 partials: such a team
+// a row, the weights in its lanes.  More: a row at a time, its weights in shared memory, 16 teams that take
+// every 16th partial and meet in order.  One sequence and head, 60000 rows: a call of
+// one query 16 us, 8 queries 19; 39 and 48 where a block in order joined four rows of a task.
 constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 4;
-constexpr int kJoinTeams = kJoinThreads / 16 / kJoinRows;
+constexpr int kJoinTeams = kJoinThreads / 16;
+constexpr int kMostBlocks = 512;  // of a grid
+
+__device__ __forceinline__ void add_row(float4& o, const float* p, float f) {
+  const float2 x = *reinterpret_cast<const float2*>(p), y = *reinterpret_cast<const float2*>(p + 2);
+  o.x += x.x * f;
+  o.y += x.y * f;
+  o.z += y.x * f;
+  o.w += y.y * f;
+}
 
 template <typename DT, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ DenseTreeArgs da) {
-  __shared__ float4 s_o[kJoinTeams][kJoinRows][16];
+  __shared__ float s_w[kMostBlocks], s_red[2][kJoinThreads / 32];
+  __shared__ float4 s_o[kJoinTeams][16];
   const TreeArgs& a = da.a;
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
-  const Split sp = da.split[blockIdx.x];
-  const int r0 = sp.rb * ROWS, rows = sp.parts == 0 ? 0 : min(ROWS, a.G * sp.n - r0);
-  if (kJoinRows * static_cast<int>(blockIdx.y) >= rows) return;
-  const int d = (threadIdx.x & 15) * 4, at = (threadIdx.x >> 4) % kJoinRows, share = (threadIdx.x >> 4) / kJoinRows;
-  const int r = kJoinRows * blockIdx.y + at;
-  const float* first = da.part + ((static_cast<size_t>(blockIdx.x) * 2 + sp.slot) * ROWS + r) * kDtPart;
-  const float* second = da.part + (static_cast<size_t>(blockIdx.x + 1) * 2 * ROWS + r) * kDtPart;
-  auto partial = [&](int i) { return i == 0 ? first : second + static_cast<size_t>(i - 1) * (2 * ROWS * kDtPart); };
-  float all = -INFINITY, sum = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (r < rows)
-    for (int i = threadIdx.x & 15; i < sp.parts; i += 16) all = fmaxf(all, partial(i)[kD]);
+  const int tid = threadIdx.x, team = tid >> 4, lane = tid & 15, d = 4 * lane;
+  const Split sp = da.split[2 * blockIdx.x + blockIdx.y];
+  if (sp.parts == 0) return;
+  const int q0 = sp.rb * ROWS, rows = min(ROWS, a.G * sp.n - q0), each = (rows + sp.parts - 1) / sp.parts;
+  const int begin = (static_cast<int>(blockIdx.x) - sp.first) * each, end = min(rows, begin + each);
+  const float* one = da.part + (static_cast<size_t>(sp.first) * 2 + sp.slot) * ROWS * kDtPart;
+  const float* more = da.part + static_cast<size_t>(sp.first) * 2 * ROWS * kDtPart;
+  auto partial = [&](int i, int r) { return (i == 0 ? one : more + static_cast<size_t>(i) * (2 * ROWS * kDtPart)) + r * kDtPart; };
+  auto write = [&](int r, float4 o, float all, float sum) {
+    const float inv = 1.f / sum;
+    o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    const int head = (q0 + r) / sp.n, s = (q0 + r) - head * sp.n;
+    const size_t row = (static_cast<size_t>(sp.b) * a.Hq + sp.h * a.G + head) * a.T + s;
+    if constexpr (sizeof(DT) == 4)
+      *reinterpret_cast<float4*>(static_cast<float*>(a.o) + row * kD + d) = o;
+    else
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * kD + d) = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
+    if (d == 0 && a.lse != nullptr) a.lse[row] = (all + log2f(sum)) * kLn2;
+  };
+  if (sp.parts <= 16) {
+    for (int r0 = begin; r0 < end; r0 += kJoinTeams) {  // (the same trips in every warp: its two teams meet in the shuffles)
+      const int r = r0 + team;
+      const bool in = r < end;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (in && lane < sp.parts) ml = *reinterpret_cast<const float2*>(partial(lane, r) + kD);
+      float all = ml.x;
 #pragma unroll
-  for (int x = 1; x < 16; x <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, x));
-  if (r < rows)
-    for (int i = threadIdx.x & 15; i < sp.parts; i += 16) {
-      const float2 ml = *reinterpret_cast<const float2*>(partial(i) + kD);
-      sum += ml.y * weight_of(ml.x, ml.y, all);
-    }
+      for (int x = 1; x < 16; x <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, x));
+      const float w = weight_of(ml.x, ml.y, all);
+      float sum = ml.y * w;
 #pragma unroll
-  for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
-  if (r < rows) {
+      for (int x = 1; x < 16; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = share; i < sp.parts; i += kJoinTeams) {
-      const float* p = partial(i);
-      const float2 x = *reinterpret_cast<const float2*>(p + d), y = *reinterpret_cast<const float2*>(p + d + 2);
-      const float2 ml = *reinterpret_cast<const float2*>(p + kD);
-      const float f = weight_of(ml.x, ml.y, all);
-      o.x += x.x * f;
-      o.y += x.y * f;
-      o.z += y.x * f;
-      o.w += y.y * f;
+      for (int i = 0; i < sp.parts; ++i) {
+        const float f = __shfl_sync(0xffffffffu, w, i, 16);
+        if (in) add_row(o, partial(i, r) + d, f);
+      }
+      if (in) write(r, o, all, sum);
     }
+    return;
   }
-  s_o[share][at][d / 4] = o;
-  __syncthreads();
-  if (share || r >= rows) return;
+  for (int r = begin; r < end; ++r) {
+    float2 ml[kMostBlocks / kJoinThreads];
+    float all = -INFINITY, sum = 0.f;
 #pragma unroll
-  for (int x = 1; x < kJoinTeams; ++x) {
-    const float4 y = s_o[x][at][d / 4];
-    o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+    for (int u = 0; u < kMostBlocks / kJoinThreads; ++u) {
+      const int i = tid + u * kJoinThreads;
+      ml[u] = i < sp.parts ? *reinterpret_cast<const float2*>(partial(i, r) + kD) : make_float2(-INFINITY, 0.f);
+      all = fmaxf(all, ml[u].x);
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, x));
+    if ((tid & 31) == 0) s_red[0][tid >> 5] = all;
+    __syncthreads();
+#pragma unroll
+    for (int x = 0; x < kJoinThreads / 32; ++x) all = fmaxf(all, s_red[0][x]);
+#pragma unroll
+    for (int u = 0; u < kMostBlocks / kJoinThreads; ++u) {
+      const float w = weight_of(ml[u].x, ml[u].y, all);
+      s_w[tid + u * kJoinThreads] = w;
+      sum += ml[u].y * w;
+    }
+#pragma unroll
+    for (int x = 1; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+    if ((tid & 31) == 0) s_red[1][tid >> 5] = sum;
+    __syncthreads();
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+    for (int i = team; i < sp.parts; i += kJoinTeams) add_row(o, partial(i, r) + d, s_w[i]);
+    s_o[team][lane] = o;
+    __syncthreads();
+    if (team == 0) {
+      sum = s_red[1][0];
+#pragma unroll
+      for (int x = 1; x < kJoinThreads / 32; ++x) sum += s_red[1][x];
+#pragma unroll
+      for (int x = 1; x < kJoinTeams; ++x) {
+        const float4 y = s_o[x][lane];
+        o = make_float4(o.x + y.x, o.y + y.y, o.z + y.z, o.w + y.w);
+      }
+      write(r, o, all, sum);
+    }
+    __syncthreads();  // the shared memory is the next row's
   }
-  const float inv = 1.f / sum;
-  o = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  const int head = (r0 + r) / sp.n, s = (r0 + r) - head * sp.n;
-  const size_t row = (static_cast<size_t>(sp.b) * a.Hq + sp.h * a.G + head) * a.T + s;
-  if constexpr (sizeof(DT) == 4)
-    *reinterpret_cast<float4*>(static_cast<float*>(a.o) + row * kD + d) = o;
-  else
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.o) + row * kD + d) = make_uint2(pack_bf2(o.x, o.y), pack_bf2(o.z, o.w));
-  if (d == 0 && a.lse != nullptr) a.lse[row] = (all + log2f(sum)) * kLn2;
 }
 
 template <typename DT, typename P>
 cudaError_t launch_join(const DenseTreeArgs& da, cudaStream_t stream) {
-  const TreeArgs& a = da.a;
   cudaLaunchConfig_t cfg = {};
-  const int most = a.G * a.T < P::kRows ? a.G * a.T : P::kRows;
-  cfg.gridDim = dim3(static_cast<unsigned>(da.blocks), (most + kJoinRows - 1) / kJoinRows);
+  cfg.gridDim = dim3(static_cast<unsigned>(da.blocks), 2);
   cfg.blockDim = dim3(kJoinThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];

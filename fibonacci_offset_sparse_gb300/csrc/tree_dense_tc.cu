@@ -31,7 +31,7 @@ constexpr float kNoKey = 1e30f;  // a row's reference, negated, before it has me
 template <int ROWS>
 struct TcShape {
   // Task cost: 256 tasks of 64 rows over 4096 cached ones take 66 us at 12, 77 at 8 and 68 at 16; 16 x 65536 177, 182, 178.
-  static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 12, kLeast = 1;
+  static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 12, kLeast = 3;
   static constexpr int kSlotBytes = kUnit * kD * 2;  // K or V of a unit
   static constexpr int kGroupRows = 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
   static constexpr int kCons = 128 * kGroups, kThreads = kCons + 64;
@@ -270,7 +270,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
   }
   const Schedule sch = schedule_at(smem + P::kSchedule, a.B);
   build_schedule<P>(a, sch);
-  if (tid == 0) da.split[blockIdx.x].parts = 0;
+  if (tid == 0) clear_splits(da);
   const long long cost = sch.start[a.B];
   const int sharing = sharing_blocks(cost, da.blocks, P::kLeast);
   if (static_cast<int>(blockIdx.x) >= sharing) return;
@@ -396,7 +396,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       if (tid == 0) s_place = u;
       if (tid == 0) {
         const long long all = *static_cast<volatile long long*>(sch.start + a.B);
-        note_split<P>(da, k, all, sharing_blocks(all, da.blocks, P::kLeast), s_run[0]);
+        note_split<P>(da, k, all, sharing_blocks(all, da.blocks, P::kLeast));
       }
       const int k_first = k.first, k_last = k.last, k_len = k.len;
       const int mine = min(GR, max(0, a.G * k.n - k.rb * ROWS - g0));  // rows of this group
@@ -665,7 +665,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
 template <int ROWS>
 size_t part_bytes() {
   // two partials a block, and the drafted keys' part of a piece
-  return static_cast<size_t>(152) * TcShape<ROWS>::kResident * (ROWS * (2 * kDtPart + kAccStride) * sizeof(float) + sizeof(Split));
+  return static_cast<size_t>(152) * TcShape<ROWS>::kResident * (ROWS * (2 * kDtPart + kAccStride) * sizeof(float) + 2 * sizeof(Split));
 }
 
 }  // namespace
