@@ -13,7 +13,7 @@
 // long axis), whatever the lengths are: lengths live on the device, so every block computes the
 // cut from them.  A block that holds a whole task writes its outputs; else it leaves a
 // partial (max, sum, unnormalised O) in the workspace and join_kernel adds the partials of a
-// task in the order of the blocks.
+// task in a fixed order.
 //
 // Block: 4 warps that compute and one that feeds them.  The feeder copies K and V rows of a unit by
 // TMA (128-byte swizzle) into a slot of a ring, a page at a time.  The computing warps are TILES row

@@ -3,8 +3,8 @@
 //
 // What bounds it: the read of the cache, as there.  With mma.sync the products alone took as long as the
 // read from some 24 query rows on; here the tensor pipes are busy for a fifth of the time.  16 sequences x 8 heads x
-// 65536 rows: 16 query rows 172 us, 24 rows 176 (6.3 TB/s, 93% of a measured copy), 32 rows 178; 48 rows 208 and 64 rows
-// 240, where one block an SM is bound by the steps of its softmax warps.
+// 65536 rows: 16 query rows 172 us, 24 rows 174 (6.4 TB/s, 94% of a measured copy), 32 rows 175; 48 rows 205 and 64 rows
+// 238, where one block an SM is bound by the steps of its softmax warps.
 //
 // Per unit of 128 cached rows, with the keys as the 128 rows of the accumulator:
 //   S^T [128 keys x ROWS] = K Q'^T    K from the ring as TMA left it (K-major, 128-byte swizzle), the rotated
@@ -31,6 +31,7 @@ constexpr float kNoKey = 1e30f;  // a row's reference, negated, before it has me
 template <int ROWS>
 struct TcShape {
   // Task cost: 256 tasks of 64 rows over 4096 cached ones take 66 us at 12, 77 at 8 and 68 at 16; 16 x 65536 177, 182, 178.
+  // Units a block: one sequence and head of 30000 rows takes 23 us at 3, 39 at 1 and 22 at 6; 8 heads of 4096 17, 21 and 19.
   static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 12, kLeast = 3;
   static constexpr int kSlotBytes = kUnit * kD * 2;  // K or V of a unit
   static constexpr int kGroupRows = 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
