@@ -8,7 +8,7 @@
 // ascending; the only atomics are integer sums and minima.
 //
 // What bounds them: the rows' bytes where there are many, else the plan's chain of reads (counts and lengths, tables, a
-// scan, a list).  Commit of 64 sequences x 16 layers, 134 MB: 24 us, 4 of them the plan; of one token for 32 sequences
+// scan, a list).  Commit of 64 sequences x 16 layers, 134 MB: 21 us, 4 of them the plan; of one token for 32 sequences
 // 6.5.  Fork of 32 x 64 and of 256 x 512 table entries 8 us.  Compaction of 1.07 GB 168 us (6.4 TB/s, 94% of a
 // measured copy), of 20 MB 7.
 #include "cache.cuh"
@@ -131,10 +131,15 @@ struct CommitArgs {
   int32_t* list;
 };
 
-// One block, a thread a sequence.
+// One block, a thread a sequence.  What it waits for is a chain of reads, so those that depend on nothing come first, and
+// the pages taken stay in shared memory unless they are many.
+constexpr int kShortList = 4096;
+
 __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_constant__ CommitArgs a) {
-  __shared__ int s_page[kMaxSeqs], s_len[kMaxSeqs], s_first[kMaxSeqs], s_count[kMaxSeqs], s_off[kMaxSeqs];
+  __shared__ __align__(16) int s_page[kMaxSeqs], s_len[kMaxSeqs];
+  __shared__ int s_first[kMaxSeqs], s_count[kMaxSeqs], s_off[kMaxSeqs];
   __shared__ int s_sums[33];
+  __shared__ int32_t s_list[kShortList];
   let_second_start();
   const CacheDev& c = a.c;
   const int b = threadIdx.x;
@@ -142,14 +147,22 @@ __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_
   const int cursor = max(0, min(c.state[kStateCursor], c.n_pages));
   int counts[4];
   load_refs(c, (cursor & ~3) + 4 * static_cast<int>(threadIdx.x), cursor, counts);
+  // ... and the first 1024 entries of the paths, with the numbers that say which of them count
+  const long long nodes = a.path == nullptr ? 0 : static_cast<long long>(a.B) * a.T;
+  int node = 0, seq = 0, gains = 0;
+  if (threadIdx.x < nodes) {
+    seq = static_cast<int>(threadIdx.x) / a.T;
+    node = a.path[threadIdx.x];
+    gains = a.n_new[seq];
+  }
   int n = 0, len = 0, page = -1, refs = 0;
-  bool bad = false, part = false;
+  bool bad = static_cast<int>(threadIdx.x) - seq * a.T < gains && (node < 0 || node >= a.T), part = false;
   if (b < a.B) {
     n = a.n_new[b];
     len = c.lens[b];
-    bad = n < 0 || n > a.T || len < 0 || static_cast<long long>(len) + n > static_cast<long long>(c.max_pages) * c.P ||
+    bad |= n < 0 || n > a.T || len < 0 || static_cast<long long>(len) + n > static_cast<long long>(c.max_pages) * c.P ||
           (n > 0 && static_cast<long long>(len) + n > a.n_max);
-    if (bad) n = 0;
+    if (bad) n = 0;  // (nothing changes then)
     part = n > 0 && (len & (c.P - 1)) != 0;
     if (part) {
       page = c.table[static_cast<size_t>(b) * c.max_pages + (len >> c.shift)];
@@ -159,14 +172,10 @@ __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_
         refs = c.refs[page];
     }
   }
-  if (a.path != nullptr) {
-    for (long long i = threadIdx.x; i < static_cast<long long>(a.B) * a.T; i += kPlanThreads) {
-      const int seq = static_cast<int>(i / a.T);
-      if (i - static_cast<long long>(seq) * a.T < a.n_new[seq]) {
-        const int node = a.path[i];
-        bad |= node < 0 || node >= a.T;
-      }
-    }
+  for (long long i = threadIdx.x + kPlanThreads; i < nodes; i += kPlanThreads) {
+    seq = static_cast<int>(i / a.T);
+    node = a.path[i];
+    bad |= i - static_cast<long long>(seq) * a.T < a.n_new[seq] && (node < 0 || node >= a.T);
   }
   // shared last pages: who else writes into the same one.  The longest keeps it (the last of those), where all
   // holders write: what the others copy from it lies in front of its new rows.
@@ -177,18 +186,24 @@ __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_
   if (!any_bad && part && refs > 1) {
     int writers = 0;
     bool keeps = true;
-    for (int o = 0; o < a.B; ++o)
-      if (s_page[o] == page) {
-        ++writers;
-        keeps &= s_len[o] < len || (s_len[o] == len && o <= b);
+    for (int o = 0; o < a.B; o += 4) {
+      const int4 p = *reinterpret_cast<const int4*>(s_page + o), l = *reinterpret_cast<const int4*>(s_len + o);
+      const int ps[4] = {p.x, p.y, p.z, p.w}, ls[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool same = ps[u] == page;  // (-1 behind the last sequence)
+        writers += same;
+        keeps &= !same | (ls[u] < len) | ((ls[u] == len) & (o + u <= b));
       }
+    }
     copy = !(writers == refs && keeps);
   }
   const int first = (len + c.P - 1) >> c.shift;
   const int fresh = n > 0 ? ((len + n + c.P - 1) >> c.shift) - first : 0;
   int total;
   const int off = block_scan_1024(any_bad ? 0 : fresh + (copy ? 1 : 0), s_sums, &total);
-  const bool enough = any_bad || find_free(c, cursor, counts, total, a.list, s_sums) == total;
+  int32_t* list = total <= kShortList ? s_list : a.list;
+  const bool enough = any_bad || find_free(c, cursor, counts, total, list, s_sums) == total;
   if (any_bad || !enough) {  // nothing changes
     if (b < a.B) a.jobs[b] = CommitJob{0, 0, -1, -1};
     if (b == 0) c.state[kStateStatus] = any_bad ? kStatusDeviceAssert : kStatusNoPages;
@@ -201,7 +216,7 @@ __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_
     CommitJob j{len, n, -1, -1};
     if (copy) {
       j.src = page;
-      j.dst = a.list[off];
+      j.dst = list[off];
       c.table[static_cast<size_t>(b) * c.max_pages + (len >> c.shift)] = j.dst;
       c.refs[j.dst] = 1;
       atomicSub(&c.refs[page], 1);
@@ -209,11 +224,11 @@ __global__ void __launch_bounds__(kPlanThreads) commit_plan_kernel(const __grid_
     a.jobs[b] = j;
     if (n > 0) c.lens[b] = len + n;
   }
-  if (b == 0 && total > 0) c.state[kStateCursor] = a.list[total - 1] + 1;
+  if (b == 0 && total > 0) c.state[kStateCursor] = list[total - 1] + 1;
   __syncthreads();
   for (int s = threadIdx.x >> 5; s < a.B; s += kPlanThreads / 32)
     for (int i = threadIdx.x & 31; i < s_count[s]; i += 32) {
-      const int id = a.list[s_off[s] + i];
+      const int id = list[s_off[s] + i];
       c.table[static_cast<size_t>(s) * c.max_pages + s_first[s] + i] = id;
       c.refs[id] = 1;
     }
