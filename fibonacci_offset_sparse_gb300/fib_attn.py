@@ -395,10 +395,6 @@ def _bad(t, dtype, index) -> bool:
     return t.dtype is not dtype or t.get_device() != index or not t.is_contiguous()
 
 
-def _address(t):
-    return None if t is None else t.data_ptr()
-
-
 def _raw_stream(stream, index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
@@ -440,7 +436,7 @@ def fib_attn_cache_commit(plan: Plan, cache: Cache, k_new, v_new, n_new, path=No
     if path is not None and (path.shape != (B, T) or _bad(path, torch.int32, index)):
         raise ValueError(f"path must be int32 [B, T] on {cache.device}")
     at, size, workspace = _scratch(cache, workspace, lambda: fib_attn_cache_workspace_size(cache), stream)
-    code = lib().fib_attn_cache_commit(plan.handle, cache.pointer, B, T, n_new.data_ptr(), _address(path),
+    code = lib().fib_attn_cache_commit(plan.handle, cache.pointer, B, T, n_new.data_ptr(), None if path is None else path.data_ptr(),
                                        k_new.data_ptr(), v_new.data_ptr(), at, size, _raw_stream(stream, index))
     if code:
         raise FibAttnError("fib_attn_cache_commit", code)
@@ -471,25 +467,32 @@ def fib_attn_cache_compact(cache: Cache, remap=None, workspace=None, stream=None
 
 
 def _tree_tensors(cache: Cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream):
-    """Checks a tree decode's tensors; returns (B, Hq, T, o, lse) with the outputs allocated."""
-    index, dtype, shape = cache.index, cache.dtype, q.shape
+    """Checks a tree decode's tensors; returns (B, Hq, T, o, lse) with the outputs allocated.  (Written out: each call of a
+    helper costs as much as what it would check.)"""
+    index, dtype = cache.index, cache.dtype
+    shape = q.shape
     if len(shape) != 4 or shape[3] != FIB_HEAD_DIM:
         raise ValueError("q must be [B, Hq, T, 64]")
-    B, Hq, T = shape[0], shape[1], shape[2]
-    if k_new.shape != (B, cache.heads, T, FIB_HEAD_DIM) or v_new.shape != k_new.shape:
+    B, Hq, T, _ = shape
+    drafts = (B, cache.heads, T, FIB_HEAD_DIM)
+    if k_new.shape != drafts or v_new.shape != drafts:
         raise ValueError("k_new and v_new must be [B, heads, T, 64]")
-    if _bad(q, dtype, index) or _bad(k_new, dtype, index) or _bad(v_new, dtype, index):
+    if q.dtype is not dtype or k_new.dtype is not dtype or v_new.dtype is not dtype or q.get_device() != index or \
+            k_new.get_device() != index or v_new.get_device() != index or \
+            not (q.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous()):
         raise ValueError(f"q, k_new and v_new must be contiguous {dtype} on {cache.device}")
-    if parent is not None and (parent.shape != (B, T) or _bad(parent, torch.int32, index)):
+    if parent is not None and (parent.shape != (B, T) or parent.dtype is not torch.int32 or parent.get_device() != index or
+                               not parent.is_contiguous()):
         raise ValueError(f"parent must be int32 [B, T] on {cache.device}")
-    if n_nodes is not None and (n_nodes.shape != (B,) or _bad(n_nodes, torch.int32, index)):
+    if n_nodes is not None and (n_nodes.shape != (B,) or n_nodes.dtype is not torch.int32 or n_nodes.get_device() != index or
+                                not n_nodes.is_contiguous()):
         raise ValueError(f"n_nodes must be int32 [B] on {cache.device}")
     if o is None:
         o = _empty(cache, shape, dtype, stream)
-    elif o.shape != shape or _bad(o, dtype, index):
+    elif o.shape != shape or o.dtype is not dtype or o.get_device() != index or not o.is_contiguous():
         raise ValueError(f"o must be like q, on {cache.device}")
     if lse is not None:
-        if lse.shape != (B, Hq, T) or _bad(lse, torch.float32, index):
+        if lse.shape != (B, Hq, T) or lse.dtype is not torch.float32 or lse.get_device() != index or not lse.is_contiguous():
             raise ValueError(f"lse must be float32 [B, Hq, T] on {cache.device}")
     elif want_lse:
         lse = _empty(cache, (B, Hq, T), torch.float32, stream)
@@ -506,7 +509,8 @@ def fib_attn_tree_decode(plan: Plan, layer: int, cache: Cache, q, k_new, v_new, 
         raise ValueError(f"alpha_dev must be float32 [n_layers] on {cache.device}")
     code = lib().fib_attn_tree_decode(
         plan.handle, layer, cache.pointer, B, Hq, T, plan.N_max if N is None else N, q.data_ptr(), k_new.data_ptr(),
-        v_new.data_ptr(), _address(parent), _address(n_nodes), o.data_ptr(), _address(lse), _address(alpha_dev),
+        v_new.data_ptr(), None if parent is None else parent.data_ptr(), None if n_nodes is None else n_nodes.data_ptr(),
+        o.data_ptr(), None if lse is None else lse.data_ptr(), None if alpha_dev is None else alpha_dev.data_ptr(),
         _raw_stream(stream, cache.index))
     if code:
         raise FibAttnError("fib_attn_tree_decode", code)
@@ -524,8 +528,9 @@ def fib_attn_dense_tree_decode(plan: Plan, layer: int, cache: Cache, q, k_new, v
     at, size, workspace = _scratch(cache, workspace,
                                    lambda: fib_attn_dense_tree_workspace_size(plan, cache, B, Hq, T), stream)
     code = lib().fib_attn_dense_tree_decode(
-        plan.handle, layer, cache.pointer, B, Hq, T, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), _address(parent),
-        _address(n_nodes), o.data_ptr(), _address(lse), at, size, _raw_stream(stream, cache.index))
+        plan.handle, layer, cache.pointer, B, Hq, T, q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(),
+        None if parent is None else parent.data_ptr(), None if n_nodes is None else n_nodes.data_ptr(), o.data_ptr(),
+        None if lse is None else lse.data_ptr(), at, size, _raw_stream(stream, cache.index))
     if code:
         raise FibAttnError("fib_attn_dense_tree_decode", code)
     return o, lse
