@@ -253,7 +253,10 @@ int fib_attn_plan_create(fib_attn_plan_t* out, int base_kind, const int32_t* cus
       delete p;
       return st;
     }
+    p->tables.push_back(t);
   }
+  const float any = 0.f;  // (its address only says that there is a device alpha)
+  if (mode == FIB_MODE_INTERP) p->dev_status = make_table(p, 0, N_max, &any, &p->dev_table);
   if (cudaGetDevice(&p->device) != cudaSuccess) {
     delete p;
     return FIB_ERR_CUDA;

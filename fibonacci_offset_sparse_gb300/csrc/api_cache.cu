@@ -34,8 +34,15 @@ int check_workspace(const void* ws, size_t bytes, size_t need) {
   return ws == nullptr || !aligned(ws, 256) || bytes < need ? FIB_ERR_INVALID_ARG : FIB_OK;
 }
 
-// make_table allocates on the host; nothing may escape a C entry point.
+// The layer's key table: at N_max, where most calls are, the plan's own.  make_table allocates on the host; nothing may
+// escape a C entry point.
 int table_of(const fib_attn_plan_s* p, int layer, int N, const float* alpha_dev, LayerTable* t) noexcept {
+  if (N == p->N_max) {
+    *t = alpha_dev == nullptr ? p->tables[layer] : p->dev_table;
+    t->layer = layer;
+    t->alpha_dev = alpha_dev;
+    return alpha_dev == nullptr ? FIB_OK : p->dev_status;
+  }
   try {
     return make_table(p, layer, N, alpha_dev, t);
   } catch (...) {

@@ -22,6 +22,10 @@ struct fib_attn_plan_s {
   unsigned long long wait_ns = 1000000000ULL;  // bound of every device-side wait (1 s)
   int skip_first_rung_copy = 0;                // test hooks, see fib_attn_plan_set_debug
   int corrupt_rung_table = 0;
+  // At N_max: every layer's table, and the one that a device alpha completes (INTERP; its status).
+  std::vector<fibattn::LayerTable> tables;
+  fibattn::LayerTable dev_table = {};
+  int dev_status = FIB_ERR_UNSUPPORTED;
   fibattn::BwdStreams side;                             // the bf16 backward's second-half stream
   std::mutex side_mu;                          // one backward at a time forks onto it
 };
