@@ -606,19 +606,22 @@ __global__ void __launch_bounds__(DtSmem<DT, TILES>::kThreads, DtSmem<DT, TILES>
       f[i] = weight_of(core.m[i], core.l[i], all);
       old[i] = grp > 0 ? 1.f : drafts ? weight_of(md, s_sum[GROUPS * ROWS + r], all) : 0.f;
     }
-    for (int turn = 0; turn < GROUPS; ++turn) {
-      if (grp == turn) {
+    // even groups into one sum, odd ones into another, which takes the query's room (and the drafts'): two turns of four groups
+    float* s_odd = reinterpret_cast<float*>(smem + S::kQuery);
+    static_assert(TILES * C::kQueryBytes + kD * 8 >= ROWS * kAccStride * 4, "room for the odd groups' sum");
+    for (int turn = 0; turn < GROUPS / 2; ++turn) {
+      if (grp / 2 == turn) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int r = C::kRows * tile + C::own_row(i);
-          if (r < rows) core.add_to(i, s_acc + r * kAccStride, old[i], turn > 0 || tail, f[i]);
+          if (r < rows) core.add_to(i, (grp & 1 ? s_odd : s_acc) + r * kAccStride, old[i], turn > 0 || (grp == 0 && tail), f[i]);
         }
       }
       cons_sync<CONS>();
     }
     if (!ok) atomicExch(a.status, kStatusDeviceAssert);
-    if (!s_err) write_rows<DT, ROWS, CONS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_max, s_sum, parts);
-    cons_sync<CONS>();  // s_acc, s_max and s_sum are free again
+    if (!s_err) write_rows<DT, ROWS, CONS>(da, k, whole, k.start >= u0 ? 1 : 0, r0, rows, s_acc, s_odd, s_max, s_sum, parts);
+    cons_sync<CONS>();  // all of it is free again
   }
 }
 

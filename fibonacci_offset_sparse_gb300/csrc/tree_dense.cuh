@@ -328,11 +328,11 @@ __device__ __forceinline__ void attend_drafts(const TreeArgs& a, const Task& k, 
   }
 }
 
-// The rows of a piece, O in acc for the common maximum of `parts` (maximum, sum) pairs a row: divided, to o
+// The rows of a piece, O in acc (and the rest of it in `more`, where that is given) for the common maximum of `parts` (maximum, sum) pairs a row: divided, to o
 // and lse, where the piece is a whole task; as a partial else.
 template <typename DT, int ROWS, int CONS>
 __device__ __forceinline__ void write_rows(const DenseTreeArgs& da, const Task& k, bool whole, int slot, int r0, int rows,
-                                           const float* acc, const float* mx, const float* sm, int parts) {
+                                           const float* acc, const float* more, const float* mx, const float* sm, int parts) {
   const TreeArgs& a = da.a;
   float* part = da.part + (static_cast<size_t>(blockIdx.x) * 2 + slot) * ROWS * kDtPart;
   for (int i = threadIdx.x; i < rows * 16; i += CONS) {  // 16 threads a row
@@ -340,7 +340,11 @@ __device__ __forceinline__ void write_rows(const DenseTreeArgs& da, const Task& 
     float mr = -INFINITY, sum = 0.f;
     for (int x = 0; x < parts; ++x) mr = fmaxf(mr, mx[x * ROWS + r]);
     for (int x = 0; x < parts; ++x) sum += sm[x * ROWS + r] * weight_of(mx[x * ROWS + r], sm[x * ROWS + r], mr);
-    const float4 x = *reinterpret_cast<const float4*>(acc + r * kAccStride + d);
+    float4 x = *reinterpret_cast<const float4*>(acc + r * kAccStride + d);
+    if (more != nullptr) {
+      const float4 y = *reinterpret_cast<const float4*>(more + r * kAccStride + d);
+      x = make_float4(x.x + y.x, x.y + y.y, x.z + y.z, x.w + y.w);
+    }
     if (whole) {
       int s;
       const size_t row = row_of(a, k, r0 + r, &s);

@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       }
       fence_before();
       cons_sync<CONS>();
-      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, done, tail && done.first == 0, done.start >= s_run[0] ? 1 : 0, r0, rows, s_part, s_max, s_sum, 1);
+      if (!s_err) write_rows<__nv_bfloat16, ROWS, CONS>(da, done, tail && done.first == 0, done.start >= s_run[0] ? 1 : 0, r0, rows, s_part, nullptr, s_max, s_sum, 1);
       u = done.start + done.units + P::kTaskCost;
       cons_sync<CONS>();  // everything of the piece is free again
     }
