@@ -35,8 +35,8 @@ namespace fibattn {
 
 namespace {
 
-// bf16: up to so many query rows here, more in tree_dense_tc.cu.  8 rows over 16 x 65536 cached ones take 169 us here and 168
-// there, over 32 x 1024 17.2 and 21.9; one query over 4096 11.9 and 16.1; 16 rows over 16 x 65536 283 here and 172 there.
+// bf16: up to so many query rows here, more in tree_dense_tc.cu.  8 rows over 16 x 65536 cached ones take 170 us here and
+// there, over 32 x 1024 17 and 21; one query over 4096 9.8 and 14.3; 16 rows over 16 x 65536 283 here (two tiles of 8) and 173 there.
 constexpr int kMmaRows = 8;
 constexpr int kSlotBytes = 8192;  // K and V of a unit
 constexpr int kHalf = kSlotBytes / 2;

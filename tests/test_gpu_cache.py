@@ -600,6 +600,26 @@ def test_a_wait_that_gives_up_is_reported(dtype, T):
     plan.close()
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("case", [2, 6, 7, 9, 12])
+def test_without_lse_and_with_outputs_allocated(dtype, case):
+    """want_lse=False gives the same o; so do outputs and workspace that the call allocates."""
+    c, ref, dev, host, parent, live = tree_case(rng(25, case), dtype, *CASES[case])
+    plan = plan_for(2300, W=8)
+    kw = dict(parent=i32(parent), n_nodes=i32(live))
+    for fn in (fa.fib_attn_tree_decode, fa.fib_attn_dense_tree_decode):
+        o, lse = sevens(dev[0])
+        fn(plan, 1, c, *dev, o=o, lse=lse, **kw)
+        o2, none = fn(plan, 1, c, *dev, want_lse=False, **kw)
+        o3, l3 = fn(plan, 1, c, *dev, **kw)
+        assert none is None
+        for b, n in enumerate(live):
+            assert torch.equal(o[b, :, :n], o2[b, :, :n]) and torch.equal(o[b, :, :n], o3[b, :, :n])
+            assert torch.equal(lse[b, :, :n], l3[b, :, :n])
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    plan.close()
+
+
 def test_outputs_and_workspaces_of_a_call_on_another_stream():
     """What a call allocates for a stream that it is given is that stream's memory: work that the current stream
     still has to do on freed memory of its own does not meet it."""
