@@ -483,15 +483,16 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
 
 }  // namespace
 
-// A block takes some 10 us whatever its rows, and 304 run at a time; row by row takes 4.5 us and 2.6 ns a row of the
-// whole batch.  Measured (us here, row by row): 512 blocks of 64 rows 31 and 87, of 16 rows 20 and 26, of 12 rows 21 and
-// 20; 128 blocks of 64 rows 12.7 and 25, of 16 rows 10.3 and 8.7; 32 blocks of 64 rows 12.3 and 8.2.
+// A round of 304 blocks takes some 8 us at least, whatever their rows; row by row takes 4.5 us and 2.5 ns a row of the whole
+// batch.  Measured (us here, row by row): 512 blocks of 64 rows 31 and 87, of 16 rows 19 and 26, of 12 rows 19.4 and 20.5, of 8
+// rows 16.5 and 14.2; 256 blocks of 16 rows 10.6 and 14.5; 128 blocks of 32 rows 9.6 and 14.8, of 16 rows 9.0 and 8.6; 64
+// blocks of 64 rows 11.6 and 14.1; 32 blocks of 64 rows 11.5 and 8.4.
 // A chain's union grows with its length: it fits for 12 nodes of the Fibonacci base's distances, more are served row by
 // row.  (Deep trees that are given by their parents are found on the device only; they take 1.3 times the time then.)
 bool tree_tc_serves(const TreeArgs& a) {
   if (a.parent == nullptr && a.T > 12) return false;
   const long long heads = static_cast<long long>(a.B) * a.H, blocks = heads * ((a.G * a.T + kTtRows - 1) / kTtRows);
-  return heads * a.G * a.T > 4200 * ((blocks + 303) / 304) - 1700;
+  return heads * a.G * a.T > 2800 * ((blocks + 303) / 304) - 400;
 }
 
 cudaError_t launch_tree_tc(const TreeArgs& a, cudaStream_t stream) {
