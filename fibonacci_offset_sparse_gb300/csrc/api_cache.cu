@@ -175,7 +175,7 @@ int fib_attn_dense_tree_decode(fib_attn_plan_t p, int layer, const fib_attn_cach
   if (st == FIB_OK) st = check_cache_device(c);
   if (st != FIB_OK) return st;
   a.t = LayerTable{};
-  return cuda_status(launch_dense_tree(a, c->dtype, p->wait_ns, workspace, static_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_dense_tree(a, c->dtype, p->wait_ns, p->skip_first_rung_copy, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

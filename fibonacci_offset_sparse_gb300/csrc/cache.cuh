@@ -43,7 +43,7 @@ struct TreeArgs {
 };
 cudaError_t launch_tree(const TreeArgs& a, int dtype, cudaStream_t stream);
 size_t dense_tree_workspace_bytes(int B, int Hq, int H, int T, int dtype);
-cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long wait_ns, void* ws, cudaStream_t stream);
+cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long wait_ns, int skip_copy, void* ws, cudaStream_t stream);
 
 inline int log2_of(int x) {
   int s = 0;

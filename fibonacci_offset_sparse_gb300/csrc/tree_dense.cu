@@ -574,11 +574,12 @@ __global__ void __launch_bounds__(DtSmem<DT, TILES>::kThreads, DtSmem<DT, TILES>
     for (int i = k.first; i < k.last; ++i, ++count) {
       if (count % GROUPS != grp) continue;
       const int slot = count % kSlots;
-      if (!s_err && !mbar_wait(&full_bar[slot], (count / kSlots) & 1, da.wait_ns)) {
+      if (!warp_wait(&full_bar[slot], (count / kSlots) & 1, da.wait_ns, &s_err)) {
         s_err = 1;
-        atomicExch(a.status, kStatusTimeout);
+        if (lane == 0) atomicExch(a.status, kStatusTimeout);
+        continue;  // (the slot is not released: its rows may still be on their way)
       }
-      if (!s_err) core.unit(ring + slot * kSlotBytes, qs, zero, k.len - i * UNIT);
+      core.unit(ring + slot * kSlotBytes, qs, zero, k.len - i * UNIT);
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty_bar[slot]);
     }
@@ -660,8 +661,9 @@ size_t dense_tree_workspace_bytes(int B, int Hq, int H, int T, int dtype) {
   return rows <= kMmaRows ? part_bytes<__nv_bfloat16, 1>() : dense_tree_tc_bytes(rows);
 }
 
-cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long wait_ns, void* ws, cudaStream_t stream) {
+cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long wait_ns, int skip_copy, void* ws, cudaStream_t stream) {
   DenseTreeArgs da;
+  da.skip_copy = skip_copy;
   da.a = a;
   da.part = static_cast<float*>(ws);
   da.wait_ns = wait_ns;

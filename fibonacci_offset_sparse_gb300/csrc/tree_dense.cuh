@@ -29,6 +29,7 @@ struct DenseTreeArgs {
   Split* split;  // [blocks][2]
   unsigned long long wait_ns;
   int blocks;   // blocks of the grid
+  int skip_copy;  // test hook: the first unit's K of every task is never copied
 };
 
 // ------------------------------------------------------------------------------ schedule --
@@ -173,8 +174,17 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
 // For what is in flight when a block gives up: its wait is not the caller's, which may be too short for a copy.
 constexpr unsigned long long kDrainNs = 2000000000ull;
 
+// A whole warp's wait, with one answer for all its lanes: false where one of them gave up (limit_ns) or the block already
+// had (s_err).  What follows, warp-wide instructions among it, is every lane's or none's.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, volatile int* s_err) {
+  const bool there = !*s_err && mbar_wait(bar, parity, limit_ns);
+  return __all_sync(0xffffffffu, there);
+}
+
 // The feeding warp: K and V rows of the units of [u0, u1) into the ring's slots, a page at a time.  A slot
-// is K, then V, kHalf bytes each; float32 rows lie as two halves of 32 dims, a quarter slot apart.
+// is K, then V, kHalf bytes each; float32 rows lie as two halves of 32 dims, a quarter slot apart.  A slot is filled again only
+// when every warp that reads it has seen its rows land and is done with them: one that gives up does not release it, and the
+// feeder then gives up too, so that no copy is ever under way into a slot of which another has not landed.
 template <typename DT, typename P>
 __device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sch, long long u0, long long u1, const CUtensorMap* map_k,
                                      const CUtensorMap* map_v, unsigned char* ring, uint64_t* full_bar, uint64_t* empty_bar,
@@ -186,6 +196,7 @@ __device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sc
   const int box = min(UNIT, 1 << a.page_shift);  // rows a copy
   int count = 0, seq = -1, first = 0, page = 0;  // lane x holds the page of entry first + x
   bool stop = false;
+  uint32_t left_out = 0;  // slots that the test hook never fills
   for (long long u = u0; u < u1 && !stop;) {
     const Task k = task_of<P>(a, sch, u, u1);
     for (int i = k.first; i < k.last; ++i, ++count) {
@@ -205,11 +216,14 @@ __device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sc
         if (!ok) atomicExch(a.status, kStatusDeviceAssert);
         y = (((ok ? id : 0) * a.H + k.h) << a.page_shift) + ((i * UNIT) & ((1 << a.page_shift) - 1));
       }
-      if (*s_err || !mbar_wait(&empty_bar[slot], ((count / kSlots) & 1) ^ 1, da.wait_ns)) stop = true;
-      if (__any_sync(0xffffffffu, stop)) {
+      if (!warp_wait(&empty_bar[slot], ((count / kSlots) & 1) ^ 1, da.wait_ns, s_err)) {
         *s_err = 1;
         stop = true;
         break;
+      }
+      if (da.skip_copy && i == 0) {
+        left_out |= 1u << slot;
+        continue;
       }
       if (lane == 0) mbar_arrive_tx(&full_bar[slot], boxes * box * 2 * kD * static_cast<int>(sizeof(DT)));
       __syncwarp();
@@ -229,7 +243,7 @@ __device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sc
   // nothing may be in flight when the block ends
   if (lane == 0) {
     for (int c = count - kSlots < 0 ? 0 : count - kSlots; c < count; ++c)
-      mbar_wait(&full_bar[c % kSlots], (c / kSlots) & 1, kDrainNs);
+      if (!(left_out >> (c % kSlots) & 1)) mbar_wait(&full_bar[c % kSlots], (c / kSlots) & 1, kDrainNs);
     if (*s_err) atomicExch(a.status, kStatusTimeout);
   }
 }

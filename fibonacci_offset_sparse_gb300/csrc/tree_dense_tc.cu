@@ -179,6 +179,7 @@ __device__ __forceinline__ void feed_tiles(const DenseTreeArgs& da, const Schedu
   const int box = min(P::kUnit, 1 << a.page_shift);  // rows a copy
   int n = 0, seq = -1, first = 0, page = 0;          // lane x holds the page of entry first + x
   bool stop = false;
+  uint32_t left_out = 0;  // slots that the test hook never fills
   for (long long u = u0; u < u1 && !stop;) {
     const Task k = task_of<P>(a, sch, u, u1);
     for (int i = k.first; i < k.last && !stop; ++i) {
@@ -200,11 +201,14 @@ __device__ __forceinline__ void feed_tiles(const DenseTreeArgs& da, const Schedu
 #pragma unroll
       for (int v = 0; v < 2; ++v, ++n) {
         const Tile<P::kSlots> tile(n);
-        if (*s_err || !mbar_wait(&empty_bar[tile.slot], tile.parity ^ 1, da.wait_ns)) stop = true;
-        if (__any_sync(0xffffffffu, stop)) {
+        if (!warp_wait(&empty_bar[tile.slot], tile.parity ^ 1, da.wait_ns, s_err)) {
           *s_err = 1;
           stop = true;
           break;
+        }
+        if (da.skip_copy && i == 0 && v == 0) {
+          left_out |= 1u << tile.slot;
+          continue;
         }
         if (lane == 0) mbar_arrive_tx(&full_bar[tile.slot], boxes * box * kD * 2);
         __syncwarp();
@@ -217,8 +221,9 @@ __device__ __forceinline__ void feed_tiles(const DenseTreeArgs& da, const Schedu
   // nothing may be in flight when the block ends
   for (int c = n - P::kSlots < 0 ? 0 : n - P::kSlots; c < n; ++c) {
     const Tile<P::kSlots> tile(c);
-    mbar_wait(&full_bar[tile.slot], tile.parity, kDrainNs);
+    if (!(left_out >> tile.slot & 1)) mbar_wait(&full_bar[tile.slot], tile.parity, kDrainNs);
   }
+  __syncwarp();
   if (*s_err && lane == 0) atomicExch(a.status, kStatusTimeout);
 }
 
@@ -375,10 +380,16 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
     const int group = warp >> 2, g0 = group * GR, key = tid & 127, wq = warp & 3;  // the thread's query rows and key
     const uint32_t lanes = static_cast<uint32_t>(wq) << 21;                        // its warp's lanes of tensor memory
     int count = 0;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
+    // After a wait that gave up, nothing is waited for any more; what follows works on whatever lies there, in bounds, and is
+    // not written.  A warp waits as a whole (its tensor memory instructions are warp-wide), but for a lone thread's wait.
+    auto wait_alone = [&](uint64_t* bar, uint32_t parity) {
       if (s_err || mbar_wait(bar, parity, da.wait_ns)) return;
       s_err = 1;
       atomicExch(a.status, kStatusTimeout);
+    };
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      wait_alone(bar, parity);
+      __syncwarp();
     };
     // Of a piece, formed anew from shared memory where they are needed: held over the units' loop they would cost it
     // spills, and what shared memory leaves of L1 does not hold those (16 x 65536 rows, 64 query rows: 297 us with them, 264 without).
@@ -560,7 +571,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
         }
         if (group == 0 && !in) {  // a row that was not filled for this sequence: its weight is 0, and so must be what it holds
           const Tile<P::kSlots> vt(2 * count + 1);
-          wait(&bars.full[vt.slot], vt.parity);  // after the copy, which would undo it
+          wait_alone(&bars.full[vt.slot], vt.parity);  // after the copy, which would undo it
           uint4* v = reinterpret_cast<uint4*>(smem + vt.slot * P::kSlotBytes + key * 128);
 #pragma unroll
           for (int x = 0; x < 8; ++x) v[x] = make_uint4(0, 0, 0, 0);

@@ -427,9 +427,10 @@ int fib_attn_debug_indices(fib_attn_plan_t p, int layer, int N, int i_begin, int
  * stage rows with the bulk-copy engine wait on mbarriers; every such wait gives up after
  * wait_ns nanoseconds (default 1e9; accepted range [1e3, 6e10]), records FIB_ERR_TIMEOUT in
  * the status word, lets the copies already in flight land and returns without writing
- * output.  debug_flags: FIB_DEBUG_SKIP_COPY makes the bf16 tensor-core forward never
- * complete one of its staged copies (the values of the window block), which drives that
- * timeout path; FIB_DEBUG_CORRUPT_TABLE moves the first rung of the bf16 tensor-core
+ * output (of fib_attn_dense_tree_decode o and lse are unspecified then).  debug_flags:
+ * FIB_DEBUG_SKIP_COPY makes the bf16 tensor-core forward never complete one of its staged
+ * copies (the values of the window block) and fib_attn_dense_tree_decode never begin one (the
+ * first keys of each sequence and head), which drives that timeout path; FIB_DEBUG_CORRUPT_TABLE moves the first rung of the bf16 tensor-core
  * forward's host-built rung table to distance 0 (a row inside the window, so every address
  * stays inside the sequence), which its device-side table check rejects with
  * FIB_ERR_DEVICE_ASSERT before any rung row is read.  Host-only; takes effect on the next
@@ -446,9 +447,9 @@ int fib_attn_debug_fill_shared(uint32_t pattern, void* stream);
 /* Synchronises the plan's device, then returns and clears the device status word (no
  * counterpart in the paper): FIB_OK, FIB_ERR_TIMEOUT (a bounded wait gave up),
  * FIB_ERR_DEVICE_ASSERT (the tensor-core forward's check of its rung table: every rung
- * beyond the window and inside the sequence, in ascending order) or FIB_ERR_RANGE (a value
- * outside the float16 range, see fib_attn_fwd).  Where several calls recorded a code, the
- * last one written is returned.                                                        */
+ * beyond the window and inside the sequence, in ascending order; a tree decode's checks of
+ * what it reads on the device) or FIB_ERR_RANGE (a value outside the float16 range, see
+ * fib_attn_fwd).  Where several calls recorded a code, the last one written is returned.   */
 int fib_attn_last_device_status(fib_attn_plan_t p);
 
 #ifdef __cplusplus
