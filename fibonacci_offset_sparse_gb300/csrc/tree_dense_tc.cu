@@ -12,7 +12,7 @@
 //   P = 2^(S - m)                     a thread a key: its row of S^T from tensor memory to registers, its
 //                                     weights, again hi + lo, to shared memory (16 bytes for 8 query rows)
 //   O^T [64 dims x ROWS] += V^T P^T   V from the ring (its transpose by the descriptor), P as written; O stays
-//                                     in tensor memory over the whole run
+//                                     in tensor memory for 16 units, then the softmax warps add it to the run's sum there
 // The maximum m of a row is common to a unit's keys and moves only when a score passes it by more than
 // 8 (weights <= 256 until then): one vote of four warps a unit; the exact maximum, and O rescaled, are the
 // exception's work.
@@ -26,6 +26,10 @@ namespace fibattn {
 
 namespace {
 
+// Units whose products the tensor pipes add to one another.  They round toward zero at each product (16 a unit), 3.6e-8 of the sum in
+// the mean and all to one side: over 131072 rows 5.6e-4 of O were lost where a run was one chain, a tenth of a step of bf16,
+// and 1e-5 are at 16 units.
+constexpr int kChain = 16;
 constexpr float kNoKey = 1e30f;  // a row's reference, negated, before it has met a finite score
 
 template <int ROWS>
@@ -41,7 +45,8 @@ struct TcShape {
   // it takes what shared memory is left: K's slot is free once the scores are formed.
   static constexpr int kResident = ROWS <= 32 ? 2 : 1;
   static constexpr int kSlots = ROWS <= 32 ? 5 : 9;
-  static constexpr int kColumns = ROWS == 16 ? 64 : ROWS == 32 ? 128 : 256;  // of tensor memory: S twice, O
+  static constexpr int kColumns = ROWS == 16 ? 64 : ROWS == 32 ? 128 : 256;  // of tensor memory: S twice, O, the sum of earlier O
+  static_assert(4 * ROWS <= kColumns, "columns");
   // byte offsets in dynamic shared memory (its base is 1024-byte aligned)
   static constexpr int kQuery = kSlots * kSlotBytes;    // hi [ROWS][64], lo: K-major, 128-byte swizzle
   static constexpr int kWeights = kQuery + ROWS * 256;  // hi [ROWS/8][16][8 keys][8 rows], lo; see below for its other uses
@@ -289,7 +294,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * ROWS;
+  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * ROWS, tmem_sum = tmem + 3 * ROWS;
   const uint32_t base = smem_addr(smem);
 
   if (warp == kFeeder) {
@@ -302,15 +307,15 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       // two cursors over the units of the run: the next S, the next O += V P
       struct Cursor {
         long long u;
-        int i, last, count;
+        int i, begin, last, count;
         bool first;  // of its piece
-      } s{u0, 0, 0, 0, false}, o{u0, 0, 0, 0, false};
+      } s{u0, 0, 0, 0, 0, false}, o{u0, 0, 0, 0, 0, false};
       auto next = [&](Cursor& c) {  // moves to a unit; false at the run's end
         while (c.i == c.last) {
           if (c.u >= u1) return false;
           const Task k = task_of<P>(a, sch, c.u, u1);
           c.u = k.start + k.units + P::kTaskCost;
-          c.i = k.first;
+          c.i = c.begin = k.first;
           c.last = k.last;
           c.first = true;
         }
@@ -344,12 +349,13 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
         if (o.count < s.count && mbar_try(&bars.weights, o.count & 1) && mbar_try(&bars.full[vt.slot], vt.parity)) {
           fence_after();
           const uint32_t from = base + vt.slot * P::kSlotBytes;
+          const bool add = (o.i - o.begin) % kChain != 0;
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+          for (int part = 1; part >= 0; --part)
 #pragma unroll
             for (int x = 0; x < 8; ++x)
               mma_tc(tmem_o, matrix_at(from + 2048 * x, 16, 1024, 2), matrix_at(base + P::kWeights + part * ROWS * 256 + 256 * x, 128, 2048, 0),
-                     kValues, !o.first || part + x > 0);
+                     kValues, add || part == 0 || x > 0);
           commit_tc(&bars.empty[vt.slot]);
           commit_tc(&bars.added);
           ++o.count;
@@ -530,19 +536,26 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           if (count > 0) wait(&bars.added, (count - 1) & 1);  // O is at rest
           fence_after();
           group_sync(group);
+          // O, then the sum of earlier O.  By the same instructions 24 query rows take 178 us, with a copy for each 189; 64
+          // rows, whose registers are shorter, 267 and 259.
 #pragma unroll
           for (int c = 0; c < GR / 8; ++c) {
-            float y[8];
-            tmem_load(tmem_o + g0 + 8 * c + lanes, y);  // (unused at a piece's first unit)
+#pragma unroll(ROWS == 64 ? 2 : 1)
+            for (int part = 0; part < 2; ++part) {
+              if (part == 1 && i <= k_first + kChain) break;
+              const uint32_t from = tmem_o + part * ROWS + g0 + 8 * c + lanes;
+              float y[8];
+              tmem_load(from, y);  // (unused at a piece's first unit)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float* w = s_warp + g0 + 8 * c + e;
-              const float m = -s_ref[g0 + 8 * c + e];
-              const float corr = ex2(m - fmaxf(m, fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS]))));
-              l[8 * c + e] *= corr;
-              y[e] *= corr;
+              for (int e = 0; e < 8; ++e) {
+                const float* w = s_warp + g0 + 8 * c + e;
+                const float m = -s_ref[g0 + 8 * c + e];
+                const float corr = ex2(m - fmaxf(m, fmaxf(fmaxf(w[0], w[ROWS]), fmaxf(w[2 * ROWS], w[3 * ROWS]))));
+                if (part == 0) l[8 * c + e] *= corr;
+                y[e] *= corr;
+              }
+              if (part == 1 || i > k_first) tmem_store(from, y);
             }
-            if (i > k_first) tmem_store(tmem_o + g0 + 8 * c + lanes, y);
           }
           group_sync(group);
           if (key < GR) {
@@ -563,6 +576,20 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           lo[c] = pack_bf2_rn(p0, p1);
         }
         if (count > 0) wait(&bars.added, (count - 1) & 1);  // P of the unit before is in O
+        if (i > k_first && (i - k_first) % kChain == 0) {   // O to the sum; the next product starts anew
+          fence_after();
+#pragma unroll
+          for (int c = 0; c < GR / 8; ++c) {
+            float y[8], z[8];
+            tmem_load(tmem_o + g0 + 8 * c + lanes, y);
+            if (i > k_first + kChain) {
+              tmem_load(tmem_sum + g0 + 8 * c + lanes, z);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) y[e] += z[e];
+            }
+            tmem_store(tmem_sum + g0 + 8 * c + lanes, y);
+          }
+        }
         unsigned char* at = smem + P::kWeights + (g0 >> 3) * 2048 + (key >> 3) * 128 + (key & 7) * 16;
 #pragma unroll
         for (int c = 0; c < GR / 8; ++c) {
@@ -589,6 +616,12 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       fence_after();
       float o[GR];
       tmem_load(tmem_o + g0 + lanes, o);
+      if (k_last > k_first + kChain) {
+        float z[GR];
+        tmem_load(tmem_sum + g0 + lanes, z);
+#pragma unroll
+        for (int r = 0; r < GR; ++r) o[r] += z[r];
+      }
       cons_sync<CONS>();
 #pragma unroll
       for (int r = 0; r < GR; ++r) s_part[(g0 + r) * 128 + key] = l[r];

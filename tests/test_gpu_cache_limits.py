@@ -43,3 +43,74 @@ def test_a_copy_that_never_comes_is_reported(dtype, T, lens):
         assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
         check(o, lse, *want, live, dtype)
     plan.close()
+
+
+# ----------------------------------------------------------------------------- long contexts
+def long_case(dtype, B, H, T, n, fill, seed):
+    """B sequences of n rows in pages of 64, one after the other in the pools, and T drafts each that follow the cached
+    rows alone.  fill(shape, generator): the values."""
+    dt = {"f32": torch.float32, "bf16": torch.bfloat16}[dtype]
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    pages = -(-n // 64)
+    k = torch.empty((1, B * pages, H, 64, 64), device="cuda", dtype=dt).normal_(generator=g)
+    v = fill((B, pages, H, 64, 64), g).to(dt).view(1, B * pages, H, 64, 64)
+    c = fa.fib_attn_cache_create(1, H, 64, B * pages, B, pages, dt, k=k, v=v)
+    c.table.copy_(torch.arange(B * pages, dtype=torch.int32).view(B, pages))
+    c.lens.fill_(n)
+    c.refs.fill_(1)
+    q, kn = (torch.empty((B, H, T, 64), device="cuda").normal_(generator=g).to(dt) for _ in range(2))
+    vn = fill((B, T, H, 1, 64), g).to(dt).view(B, T, H, 64).transpose(1, 2).contiguous()
+    return c, q, kn, vn, i32(np.full((B, T), -1))
+
+
+def exact_long(c, q, kn, vn, n, rows):
+    """The outputs of the drafts `rows` (a slice) in 64 bits, on the GPU."""
+    B, H, T, _ = q.shape
+    turned = [torch.from_numpy(co.turn(x.double().cpu().numpy(), np.full((B, H, T), n))).cuda()[:, :, rows] for x in (q, kn)]
+    out = torch.empty_like(turned[0])
+    k, v = (x.view(B, -1, H, 64, 64) for x in (c.k, c.v))
+    for b in range(B):
+        for h in range(H):
+            x, own = turned[0][b, h], turned[1][b, h]
+            s = torch.cat([x @ k[b, :, h].reshape(-1, 64)[:n].double().T, (x * own).sum(1, keepdim=True)], 1) / 8
+            p = torch.softmax(s, 1)
+            out[b, h] = p[:, :-1] @ v[b, :, h].reshape(-1, 64)[:n].double() + p[:, -1:] * vn[b, h, rows].double()
+    return out
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 64])
+def test_equal_values_over_a_long_context(T):
+    """Every value is 1, so every output is: what is left is how the sums are held.  A block's warps add one unit of 16 rows
+    after the other to O and to the sum of the weights, some 900 at most here, each rounded to nearest: an error of at most 2^-24
+    of a sum that grows to its end, 2^-24 / 3 in the mean square, sqrt(900) of them 6e-7 for each of the two sums; ten of
+    the two, 8.5e-6, are allowed.  Sums that round toward zero at every product err by some 2^-25 a product, all to one side."""
+    c, q, kn, vn, par = long_case("f32", 8, 8, T, 65536, lambda s, g: torch.ones(s, device="cuda"), 31)
+    plan = plan_for(65600)
+    o, _ = fa.fib_attn_dense_tree_decode(plan, 0, c, q, kn, vn, parent=par)
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    off = (o.double() - 1).abs().max().item()
+    assert off <= 8.5e-6
+    plan.close()
+
+
+@pytest.mark.parametrize("T", [8, 16, 32, 64])
+def test_mean_error_over_a_long_context(T):
+    """bf16, values around a mean of their own for each sequence, head and dimension in [1, 2).  An output is rounded to a
+    multiple of 2^-7, 2^-7 / sqrt(12) / 1.4 = 1.6e-3 of it in the mean square and as often up as down: over the 16 * 8 * 64
+    means 1.8e-5, of which six are allowed.  The tensor pipes' own sums, which round toward zero, may add 256 products of at
+    most 2^-24 each on average, 1.5e-5."""
+    B, H, n = 16, 8, 131072
+
+    def fill(shape, g):
+        mean = 1 + torch.rand((B, 1, H, 1, 64), generator=torch.Generator(device="cuda").manual_seed(7), device="cuda")
+        return torch.empty(shape, device="cuda").normal_(generator=g).mul_(0.1).add_(mean)
+
+    c, q, kn, vn, par = long_case("bf16", B, H, T, n, fill, 32)
+    plan = plan_for(n + 100)
+    o, _ = fa.fib_attn_dense_tree_decode(plan, 0, c, q, kn, vn, parent=par)
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    rows = slice(0, T, T // 8)
+    want = exact_long(c, q, kn, vn, n, rows)
+    off = ((o[:, :, rows].double() - want) / want).mean().item()
+    assert abs(off) <= 1.1e-4 + 1.5e-5
+    plan.close()
