@@ -28,7 +28,10 @@
 //   16 query rows a tile, whose weights are in place for the second product as the first leaves them.
 // The tensor pipes round each sum toward zero (measured: 3.6e-8 of it a product in the mean, all to one side), so that a chain of
 // products over a whole run would lose 1e-4 of O over 8 x 65536 rows.  Here each unit's products have a sum of their own, the
-// smaller ones first, and O is added up from those in float32, rounded to nearest.
+// smaller ones first, and O is added up from those in float32, rounded to nearest.  float32: the query and the weights are split to
+// nearest and a score is two chains of four products, for the same reason: over 8 x 8191 rows O is 4.4e-7 off the 64-bit result
+// (a float32 evaluation 2.3e-7), 9.9e-7 with all operands cut off and one chain, in 236 and 230 us over 8 x 65536 rows.  K and V are
+// cut: to split them to nearest would take 3.7e-7 and, with 32 query rows, 389 us instead of 377.
 // The drafted keys (at most 64, each seen by its own descendants only) are added by the block that holds a
 // task's last unit, on CUDA cores in float32: a quad a query row, over the row's ancestors
 // alone, so that another branch's values, NaN included, never meet a product.
@@ -76,6 +79,13 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], const uint32_t (&a)[4], 
 // its upper 10 bits).  An infinity or NaN stays in hi; its rest is NaN, as is the product's sum then.
 __device__ __forceinline__ void split_tf32(float x, uint32_t& hi, uint32_t& lo) {
   hi = __float_as_uint(x) & 0xffffe000u;
+  lo = __float_as_uint(x - __uint_as_float(hi));
+}
+
+// The same with the upper part rounded to nearest, so that the rest has either sign: products of two rests are left out, and
+// would else all err to one side.  For |x| < 2^127 (an infinity or NaN stays as above).
+__device__ __forceinline__ void split_tf32_near(float x, uint32_t& hi, uint32_t& lo) {
+  hi = (__float_as_uint(x) + (isfinite(x) ? 0x1000u : 0u)) & 0xffffe000u;
   lo = __float_as_uint(x - __uint_as_float(hi));
 }
 
@@ -308,8 +318,8 @@ struct Core<float> {
           x = __ldg(q + d) * (kLog2e / 8.0f);
           y = __ldg(q + d + kFreq) * (kLog2e / 8.0f);
         }
-        split_tf32(x * e.x - y * e.y, at[256 * s + 2 * f], at[256 * s + 128 + 2 * f]);
-        split_tf32(x * e.y + y * e.x, at[256 * (s + 4) + 2 * f], at[256 * (s + 4) + 128 + 2 * f]);
+        split_tf32_near(x * e.x - y * e.y, at[256 * s + 2 * f], at[256 * s + 128 + 2 * f]);
+        split_tf32_near(x * e.y + y * e.x, at[256 * (s + 4) + 2 * f], at[256 * (s + 4) + 128 + 2 * f]);
       }
   }
   __device__ __forceinline__ void clear() {
@@ -321,11 +331,11 @@ struct Core<float> {
   __device__ __forceinline__ static void scores(uint32_t kt, const uint4* qs, float (&s)[NT][4]) {
     const int mi = (threadIdx.x & 31) >> 3, rl = threadIdx.x & 7;
     const uint32_t row = kt + rl * 128;  // dims 0..31, then 32..63 a half tile further
-    float c[2][NT][4];                   // the small products apart: three chains a tile instead of one
+    float c[3][NT][4];                   // half of the large products and the small ones apart: four short chains a tile
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = c[0][n][e] = c[1][n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[n][e] = c[0][n][e] = c[1][n][e] = c[2][n][e] = 0.f;
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       uint32_t h[2][4], lo[2][4];
@@ -343,7 +353,7 @@ struct Core<float> {
           uint32_t h0, l0, h1, l1;
           split_tf32(__uint_as_float(b[2 * k]), h0, l0);
           split_tf32(__uint_as_float(b[2 * k + 1]), h1, l1);
-          mma_tf32(s[n], h[k], h0, h1);
+          mma_tf32(p < 2 ? c[2][n] : s[n], h[k], h0, h1);
           mma_tf32(c[0][n], lo[k], h0, h1);
           mma_tf32(c[1][n], h[k], l0, l1);
         }
@@ -352,7 +362,7 @@ struct Core<float> {
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] += c[0][n][e] + c[1][n][e];
+      for (int e = 0; e < 4; ++e) s[n][e] = (s[n][e] + c[2][n][e]) + (c[0][n][e] + c[1][n][e]);
   }
   __device__ __forceinline__ static void mend(uint32_t kt, const uint4* qs, float (&s)[NT][4]) {  // as above
     const int mi = (threadIdx.x & 31) >> 3, rl = threadIdx.x & 7;
@@ -431,10 +441,10 @@ struct Core<float> {
     uint32_t hi[NT][4], lo[NT][4], row[NT][2], half[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-      split_tf32(s[n][0], hi[n][0], lo[n][0]);
-      split_tf32(s[n][2], hi[n][1], lo[n][1]);
-      split_tf32(s[n][1], hi[n][2], lo[n][2]);
-      split_tf32(s[n][3], hi[n][3], lo[n][3]);
+      split_tf32_near(s[n][0], hi[n][0], lo[n][0]);
+      split_tf32_near(s[n][2], hi[n][1], lo[n][1]);
+      split_tf32_near(s[n][1], hi[n][2], lo[n][2]);
+      split_tf32_near(s[n][3], hi[n][3], lo[n][3]);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int k = 8 * n + 2 * t + x;

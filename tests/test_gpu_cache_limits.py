@@ -114,3 +114,19 @@ def test_mean_error_over_a_long_context(T):
     off = ((o[:, :, rows].double() - want) / want).mean().item()
     assert abs(off) <= 1.1e-4 + 1.5e-5
     plan.close()
+
+
+@pytest.mark.parametrize("T", [1, 20])
+def test_mean_error_in_float32(T):
+    """float32, values around 1.  What errs to one side: the two last products of a unit's sum, cut off half a step of the
+    sum on average, 2^-24 each at most, and the lower part of a value, cut off half of its last step, 2^-24; 1.8e-7 in all.  The
+    rest (the weights' parts, sums rounded to nearest) errs to either side and leaves nothing in the mean over the outputs."""
+    B, H, n = 4, 8, 8000
+    c, q, kn, vn, par = long_case("f32", B, H, T, n, lambda s, g: torch.empty(s, device="cuda").normal_(generator=g).add_(1), 33)
+    plan = plan_for(n + 100)
+    o, _ = fa.fib_attn_dense_tree_decode(plan, 0, c, q, kn, vn, parent=par)
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    want = exact_long(c, q, kn, vn, n, slice(0, T))
+    off = ((o.double() - want) / want).mean().item()
+    assert abs(off) <= 1.8e-7
+    plan.close()
