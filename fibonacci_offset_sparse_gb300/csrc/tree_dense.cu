@@ -669,11 +669,11 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
   da.blocks = kGrid<DT, TILES>;
   da.split = reinterpret_cast<Split*>(da.part + static_cast<size_t>(da.blocks) * 2 * S::kRows * kDtPart);
   const TreeArgs& a = da.a;
-  CUtensorMap mk, mv;
-  cudaError_t e = maps_of(a, static_cast<int>(sizeof(DT)), S::kUnit, &mk, &mv);
-  if (e != cudaSuccess) return e;
   const size_t smem = S::bytes(a.B, a.T);
-  e = cudaFuncSetAttribute(dense_tree_kernel<DT, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(dense_tree_kernel<DT, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  e = maps_of(a, static_cast<int>(sizeof(DT)), S::kUnit, &mk, &mv);
   if (e != cudaSuccess) return e;
   dense_tree_kernel<DT, TILES><<<da.blocks, S::kThreads, smem, stream>>>(da, mk, mv);
   e = cudaGetLastError();

@@ -540,7 +540,8 @@ inline cudaError_t map_of(CUtensorMap* m, const void* pool, long long rows, int 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// Both pools' maps for units of `unit` rows.
+// Both pools' maps for units of `unit` rows.  After a call of the runtime that needs the device's context: encode is the driver's, and
+// a host thread has no context of its own accord until then.
 inline cudaError_t maps_of(const TreeArgs& a, int es, int unit, CUtensorMap* mk, CUtensorMap* mv) {
   const int box = (1 << a.page_shift) < unit ? 1 << a.page_shift : unit;
   const long long rows = (static_cast<long long>(a.n_pages) * a.H) << a.page_shift;

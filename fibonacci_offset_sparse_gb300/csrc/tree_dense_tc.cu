@@ -695,11 +695,11 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
   DenseTreeArgs da = args;
   da.blocks = 152 * P::kResident;  // 152 SMs
   da.split = reinterpret_cast<Split*>(da.part + static_cast<size_t>(da.blocks) * ROWS * (2 * kDtPart + kAccStride));
-  CUtensorMap mk, mv;
-  cudaError_t e = maps_of(da.a, 2, P::kUnit, &mk, &mv);
-  if (e != cudaSuccess) return e;
   const size_t smem = P::bytes(da.a.B);
-  e = cudaFuncSetAttribute(dense_tree_tc_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = cudaFuncSetAttribute(dense_tree_tc_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  e = maps_of(da.a, 2, P::kUnit, &mk, &mv);
   if (e != cudaSuccess) return e;
   dense_tree_tc_kernel<ROWS><<<da.blocks, P::kThreads, smem, stream>>>(da, mk, mv);
   e = cudaGetLastError();

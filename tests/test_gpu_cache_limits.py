@@ -1,6 +1,7 @@
 """The paged cache and the tree decodes at their limits: waits that run out, several host threads, one workspace for every
 size, long contexts, large tables (needs a GPU).  Tolerances as in test_gpu_cache.py, unless a test derives its own."""
 import os
+import threading
 
 import numpy as np
 import pytest
@@ -129,4 +130,54 @@ def test_mean_error_in_float32(T):
     want = exact_long(c, q, kn, vn, n, slice(0, T))
     off = ((o.double() - want) / want).mean().item()
     assert abs(off) <= 1.8e-7
+    plan.close()
+
+
+# ------------------------------------------------------------------------------- host threads
+def in_thread(fn):
+    """fn() in a host thread that has made no CUDA call yet."""
+    got = []
+
+    def run():
+        try:
+            got.append(fn())
+        except Exception as e:
+            got.append(e)
+
+    t = threading.Thread(target=run)
+    t.start()
+    t.join()
+    assert not isinstance(got[0], Exception), got[0]
+    return got[0]
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 16), ("bf16", 32), ("bf16", 48), ("bf16", 64), ("f32", 5), ("f32", 30)])
+@pytest.mark.parametrize("op", ["dense", "sparse", "commit", "fork", "compact"])
+def test_a_first_call_of_a_host_thread(op, dtype, T):
+    """Everything that the call needs is there beforehand, so that it is the thread's first use of CUDA."""
+    r = rng(35, T)
+    c, ref, dev, host, parent, live = tree_case(r, dtype, [70, 3], 1, 1, T, 16, "random", None, poison=False)
+    plan, par, side = plan_for(200), i32(parent), torch.cuda.Stream()
+    o, lse = torch.empty_like(dev[0]), torch.empty(dev[0].shape[:3], device="cuda")
+    kn, vn = (x[None].expand(2, -1, -1, -1, -1).contiguous() for x in dev[1:])
+    n_new, src, remap = i32([1, 0]), i32([1, 0]), i32(np.zeros(c.n_pages))
+    need = max(fa.fib_attn_cache_workspace_size(c), fa.fib_attn_dense_tree_workspace_size(plan, c, 2, 1, T))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    call = {
+        "dense": lambda: fa.fib_attn_dense_tree_decode(plan, 0, c, *dev, parent=par, o=o, lse=lse, workspace=ws, stream=side),
+        "sparse": lambda: fa.fib_attn_tree_decode(plan, 0, c, *dev, parent=par, o=o, lse=lse, stream=side),
+        "commit": lambda: fa.fib_attn_cache_commit(plan, c, kn, vn, n_new, workspace=ws, stream=side),
+        "fork": lambda: fa.fib_attn_cache_fork(c, src, workspace=ws, stream=side),
+        "compact": lambda: fa.fib_attn_cache_compact(c, remap=remap, workspace=ws, stream=side)}[op]
+    torch.cuda.synchronize()
+    in_thread(call)
+    torch.cuda.synchronize()
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK and fa.fib_attn_cache_status(c) == fa.FIB_OK
+    if op == "dense":
+        want = fa.fib_attn_dense_tree_decode(plan, 0, c, *dev, parent=par)
+    if op == "sparse":
+        want = fa.fib_attn_tree_decode(plan, 0, c, *dev, parent=par)
+    if op in ("dense", "sparse"):
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+    assert c.lens.tolist() == {"commit": [71, 3], "fork": [3, 70]}.get(op, [70, 3])
     plan.close()
