@@ -520,6 +520,7 @@ struct DtSmem {
   static constexpr int kQuery = kZero + 128;
   static constexpr int kDraft = kQuery + TILES * C::kQueryBytes;
   static size_t bytes(int B, int T) { return kDraft + static_cast<size_t>(T) * kD * 8 + schedule_bytes(B); }
+  static size_t most_bytes() { return bytes(kMaxSeqs, TILES == 1 ? kRows : kMaxDrafts); }
 };
 
 template <typename DT, int TILES>
@@ -670,7 +671,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
   da.split = reinterpret_cast<Split*>(da.part + static_cast<size_t>(da.blocks) * 2 * S::kRows * kDtPart);
   const TreeArgs& a = da.a;
   const size_t smem = S::bytes(a.B, a.T);
-  cudaError_t e = cudaFuncSetAttribute(dense_tree_kernel<DT, TILES>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_shared(dense_tree_kernel<DT, TILES>, S::most_bytes());
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
   e = maps_of(a, static_cast<int>(sizeof(DT)), S::kUnit, &mk, &mv);

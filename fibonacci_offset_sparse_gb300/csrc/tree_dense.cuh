@@ -514,6 +514,13 @@ cudaError_t launch_join(const DenseTreeArgs& da, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, join_kernel<DT, P::kRows>, da);
 }
 
+// The most dynamic shared memory that a kernel's launches ask for.  The same for every call: the limit is the kernel's, not a
+// launch's, and host threads set it and launch at the same time.
+template <typename Kernel>
+cudaError_t allow_shared(Kernel kernel, size_t most) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
+}
+
 // ------------------------------------------------------------------------------ copies --
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,

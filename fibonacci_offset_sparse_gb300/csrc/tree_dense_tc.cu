@@ -696,7 +696,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
   da.blocks = 152 * P::kResident;  // 152 SMs
   da.split = reinterpret_cast<Split*>(da.part + static_cast<size_t>(da.blocks) * ROWS * (2 * kDtPart + kAccStride));
   const size_t smem = P::bytes(da.a.B);
-  cudaError_t e = cudaFuncSetAttribute(dense_tree_tc_kernel<ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  cudaError_t e = allow_shared(dense_tree_tc_kernel<ROWS>, P::bytes(kMaxSeqs));
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
   e = maps_of(da.a, 2, P::kUnit, &mk, &mv);

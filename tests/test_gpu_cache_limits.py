@@ -181,3 +181,40 @@ def test_a_first_call_of_a_host_thread(op, dtype, T):
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
     assert c.lens.tolist() == {"commit": [71, 3], "fork": [3, 70]}.get(op, [70, 3])
     plan.close()
+
+
+@pytest.mark.parametrize("dtype,T,most", [("bf16", 1, 8), ("bf16", 16, 16), ("bf16", 33, 48), ("f32", 1, 16), ("f32", 17, 64)])
+def test_calls_of_different_sizes_from_several_host_threads(dtype, T, most):
+    """One sequence with few drafts in some threads, a thousand with many in others; the same kernel, nothing else shared.  The
+    library is called directly, so that the calls lie close together."""
+    jobs = []
+    for i, (B, t) in enumerate(((1, T), (1000, most)) * 3):
+        r = rng(34, i, t)
+        c, ref, dev, host, parent, live = tree_case(r, dtype, [30] + [0] * (B - 1), 1, 1, t, 16, "random", None, poison=False)
+        plan, par = plan_for(200), i32(parent)
+        ws = torch.empty(fa.fib_attn_dense_tree_workspace_size(plan, c, B, 1, t), dtype=torch.uint8, device="cuda")
+        want = fa.fib_attn_dense_tree_decode(plan, 0, c, *dev, parent=par)
+        got = tuple(torch.empty_like(x) for x in want)
+        side = torch.cuda.Stream()
+        args = (plan.handle, 0, c.pointer, B, 1, t, *(x.data_ptr() for x in dev), par.data_ptr(), None, got[0].data_ptr(),
+                got[1].data_ptr(), ws.data_ptr(), ws.nbytes, side.cuda_stream)
+        jobs.append(dict(args=args, got=got, want=want, side=side, plan=plan, codes=set(), keep=(c, dev, par, ws)))
+    torch.cuda.synchronize()
+    ready, fn = threading.Barrier(len(jobs)), fa.lib().fib_attn_dense_tree_decode
+
+    def calls(j):
+        j["side"].synchronize()  # (the thread's first call)
+        ready.wait()
+        for _ in range(3000):
+            j["codes"].add(fn(*j["args"]))
+
+    threads = [threading.Thread(target=calls, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for j in jobs:
+        assert j["codes"] == {fa.FIB_OK}
+        assert all(torch.equal(x, y) for x, y in zip(j["got"], j["want"]))
+        j["plan"].close()
