@@ -158,7 +158,7 @@ size_t fib_attn_dense_tree_workspace_size(fib_attn_plan_t p, const fib_attn_cach
   if (p == nullptr || check_cache(c) != FIB_OK || B < 1 || B > c->max_seqs || T < 1 || T > FIB_MAX_DRAFTS || Hq < 1 ||
       Hq > FIB_MAX_HEADS || Hq % c->heads != 0)
     return 0;
-  return dense_tree_workspace_bytes(B, Hq, c->heads, T, c->dtype);
+  return dense_tree_workspace_bytes(Hq, c->heads, T, c->dtype);
 }
 
 int fib_attn_dense_tree_decode(fib_attn_plan_t p, int layer, const fib_attn_cache* c, int B, int Hq, int T,
@@ -168,7 +168,7 @@ int fib_attn_dense_tree_decode(fib_attn_plan_t p, int layer, const fib_attn_cach
   TreeArgs a;
   int st = tree_args(p, layer, c, B, Hq, T, p == nullptr ? 0 : p->N_max, q, k_new, v_new, parent, n_nodes, o, lse, &a);
   if (st != FIB_OK) return st;
-  if (check_workspace(workspace, ws_bytes, dense_tree_workspace_bytes(B, Hq, c->heads, T, c->dtype)))
+  if (check_workspace(workspace, ws_bytes, dense_tree_workspace_bytes(Hq, c->heads, T, c->dtype)))
     return FIB_ERR_INVALID_ARG;
   if (workspace == q || workspace == o || workspace == k_new || workspace == v_new) return FIB_ERR_INVALID_ARG;
   st = check_device(p);

@@ -42,7 +42,7 @@ struct TreeArgs {
   int* status;
 };
 cudaError_t launch_tree(const TreeArgs& a, int dtype, cudaStream_t stream);
-size_t dense_tree_workspace_bytes(int B, int Hq, int H, int T, int dtype);
+size_t dense_tree_workspace_bytes(int Hq, int H, int T, int dtype);
 cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long wait_ns, int skip_copy, void* ws, cudaStream_t stream);
 
 inline int log2_of(int x) {

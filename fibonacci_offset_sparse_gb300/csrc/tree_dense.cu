@@ -35,6 +35,8 @@
 // The drafted keys (at most 64, each seen by its own descendants only) are added by the block that holds a
 // task's last unit, on CUDA cores in float32: a quad a query row, over the row's ancestors
 // alone, so that another branch's values, NaN included, never meet a product.
+#include <algorithm>
+
 #include "tree_dense.cuh"
 
 namespace fibattn {
@@ -689,10 +691,13 @@ size_t part_bytes() {
 
 }  // namespace
 
-size_t dense_tree_workspace_bytes(int B, int Hq, int H, int T, int dtype) {
+// The most that the kernels of so many query rows or fewer need, so that what serves a call serves every smaller one: a kernel for more
+// rows may have half the blocks.
+size_t dense_tree_workspace_bytes(int Hq, int H, int T, int dtype) {
   const int rows = Hq / H * T;
-  if (dtype == FIB_DTYPE_F32) return rows <= 16 ? part_bytes<float, 1>() : part_bytes<float, 2>();
-  return rows <= kMmaRows ? part_bytes<__nv_bfloat16, 1>() : dense_tree_tc_bytes(rows);
+  if (dtype == FIB_DTYPE_F32) return rows <= 16 ? part_bytes<float, 1>() : std::max(part_bytes<float, 1>(), part_bytes<float, 2>());
+  const size_t few = part_bytes<__nv_bfloat16, 1>();
+  return rows <= kMmaRows ? few : std::max(few, dense_tree_tc_bytes(rows));
 }
 
 cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long wait_ns, int skip_copy, void* ws, cudaStream_t stream) {

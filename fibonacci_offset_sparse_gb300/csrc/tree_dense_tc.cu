@@ -20,6 +20,8 @@
 // Block: softmax warps (warp w reads lanes 32 (w % 4) .. of tensor memory; four warps share 16 query
 // rows), the feeder, and a warp whose one thread issues the products as their operands arrive: S of the next
 // unit runs while a unit's weights are formed.
+#include <algorithm>
+
 #include "tree_dense.cuh"
 
 namespace fibattn {
@@ -715,8 +717,13 @@ size_t part_bytes() {
 
 }  // namespace
 
+// (the most of any number of rows up to this)
 size_t dense_tree_tc_bytes(int rows) {
-  return rows <= 16 ? part_bytes<16>() : rows <= 32 ? part_bytes<32>() : rows <= 48 ? part_bytes<48>() : part_bytes<64>();
+  size_t most = part_bytes<16>();
+  if (rows > 16) most = std::max(most, part_bytes<32>());
+  if (rows > 32) most = std::max(most, part_bytes<48>());
+  if (rows > 48) most = std::max(most, part_bytes<64>());
+  return most;
 }
 
 cudaError_t launch_dense_tree_tc(const DenseTreeArgs& da, cudaStream_t stream) {

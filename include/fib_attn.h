@@ -329,7 +329,8 @@ int fib_attn_tree_decode(fib_attn_plan_t p, int layer, const fib_attn_cache* c, 
  * above: node s attends all lens[b] cached rows, its ancestors and itself.  The plan supplies
  * only its RoPE tables (positions < N_max) and status word; layer is the cache's.  workspace:
  * fib_attn_dense_tree_workspace_size(p, c, B, Hq, T) bytes of device scratch, 256-byte
- * aligned, contents on entry ignored.  An infinite value (V) in an attended row makes that
+ * aligned, contents on entry ignored; the size grows with Hq / heads * T and with nothing
+ * else, so that the largest call's serves every smaller one.  An infinite value (V) in an attended row makes that
  * dimension of o infinite or NaN.  Everything else as fib_attn_tree_decode.               */
 size_t fib_attn_dense_tree_workspace_size(fib_attn_plan_t p, const fib_attn_cache* c, int B,
                                           int Hq, int T);

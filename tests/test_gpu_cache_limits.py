@@ -218,3 +218,25 @@ def test_calls_of_different_sizes_from_several_host_threads(dtype, T, most):
         assert j["codes"] == {fa.FIB_OK}
         assert all(torch.equal(x, y) for x, y in zip(j["got"], j["want"]))
         j["plan"].close()
+
+
+# ------------------------------------------------------------------------------- workspaces
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G", [1, 2])
+def test_one_workspace_for_every_number_of_drafts(dtype, G):
+    """Sized for the largest tree, it serves every smaller one."""
+    r = rng(36, G)
+    c, ref, dev, host, parent, live = tree_case(r, dtype, [2000, 0, 333], 2, G, 64, 32, "random", None, poison=False)
+    plan = plan_for(2100)
+    sizes = [fa.fib_attn_dense_tree_workspace_size(plan, c, 3, 2 * G, T) for T in range(1, 65)]
+    assert sizes == sorted(sizes)
+    assert sizes[-1] == fa.fib_attn_dense_tree_workspace_size(plan, c, 1, 2 * G, 64)
+    assert sizes[-1] <= fa.fib_attn_dense_tree_workspace_size(plan, c, 3, 8 * G, 64)
+    ws = torch.empty(sizes[-1], dtype=torch.uint8, device="cuda")
+    for T in (1, 8, 9, 16, 17, 24, 32, 33, 48, 49, 64):
+        q, kn, vn = (x[:, :, :T].contiguous() for x in dev)
+        o, lse = fa.fib_attn_dense_tree_decode(plan, 0, c, q, kn, vn, parent=i32(parent[:, :T]), workspace=ws)
+        want = co.tree_attend(ref, 0, *(x[:, :, :T] for x in host), parent[:, :T], [T] * 3)
+        check(o, lse, *want, [T] * 3, dtype)
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    plan.close()
