@@ -21,6 +21,7 @@
 // rows), the feeder, and a warp whose one thread issues the products as their operands arrive: S of the next
 // unit runs while a unit's weights are formed.
 #include <algorithm>
+#include <cfloat>
 
 #include "tree_dense.cuh"
 
@@ -32,7 +33,7 @@ namespace {
 // the mean and all to one side: over 131072 rows 5.6e-4 of O were lost where a run was one chain, a tenth of a step of bf16,
 // and 1e-5 are at 16 units.
 constexpr int kChain = 16;
-constexpr float kNoKey = 1e30f;  // a row's reference, negated, before it has met a finite score
+constexpr float kNoKey = FLT_MAX;  // a row's reference, negated, before it has met a finite score: below every score
 
 template <int ROWS>
 struct TcShape {

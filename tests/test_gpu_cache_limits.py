@@ -10,7 +10,7 @@ import torch
 from fibonacci_offset_sparse_gb300 import fib_attn as fa
 from oracle import cache_oracle as co
 
-from .test_gpu_cache import check, i32, plan_for, rng, tree_case
+from .test_gpu_cache import HALF, TOL_O, check, i32, plan_for, rng, tree_case
 
 pytestmark = pytest.mark.gpu
 
@@ -239,4 +239,32 @@ def test_one_workspace_for_every_number_of_drafts(dtype, G):
         want = co.tree_attend(ref, 0, *(x[:, :, :T] for x in host), parent[:, :T], [T] * 3)
         check(o, lse, *want, [T] * 3, dtype)
     assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    plan.close()
+
+
+# --------------------------------------------------------------------------- far below zero
+@pytest.mark.parametrize("nearest", ["cached", "drafted"])
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 16), ("bf16", 32), ("bf16", 48), ("bf16", 64), ("f32", 5), ("f32", 30)])
+def test_scores_far_below_zero(dtype, T, nearest):
+    """Every score is below -1e30, as of keys that a caller has put out of the way.  Those of one size differ by nothing and
+    those of different ones by 1e30 and more, so that the nearest share the weight, whatever a score's rounding is."""
+    r = rng(37, T)
+    c, ref, dev, host, parent, live = tree_case(r, dtype, [500, 40, 300], 1, 1, T, 32, "roots", None, poison=False)
+    for x in (c.k, dev[0], dev[1]):
+        x.zero_()
+    for x in (ref.k, host[0], host[1]):
+        x[...] = 0
+    size = 2.0 ** (53 + r.integers(1, 4, ref.k.shape[:4]))
+    ref.k[..., 31] = size
+    c.k[..., 31] = torch.from_numpy(size).to(c.k)
+    host[0][..., 31], host[1][..., 31] = -2.0 ** 53, 2.0 ** (53 if nearest == "drafted" else 57)  # (dimension 31 turns by 1.3e-4 a row)
+    for t, h in zip(dev[:2], host[:2]):
+        t.copy_(torch.from_numpy(h))
+    plan = plan_for(600)
+    o, lse = fa.fib_attn_dense_tree_decode(plan, 0, c, *dev, parent=i32(parent))
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    ro, rl = co.tree_attend(ref, 0, *host, parent, live)
+    assert rl.max() < -1e30
+    assert np.all(np.abs(o.double().cpu().numpy() - ro) <= TOL_O + (HALF[dtype] * np.abs(ro) if dtype == "bf16" else 0))
+    assert np.all(np.abs(lse.double().cpu().numpy() / rl - 1) <= 2.0 ** -15)  # (a bf16 query is held in 16 bits)
     plan.close()
