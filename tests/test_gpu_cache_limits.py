@@ -10,7 +10,8 @@ import torch
 from fibonacci_offset_sparse_gb300 import fib_attn as fa
 from oracle import cache_oracle as co
 
-from .test_gpu_cache import HALF, TOL_O, check, i32, plan_for, rng, tree_case
+from .test_gpu_cache import (HALF, TOL_LSE, TOL_O, check, close_rows, draw, i32, keys_of, make_cache, plan_for, rng, same_tables,
+                             sevens, snapshot, tree_case, unchanged)
 
 pytestmark = pytest.mark.gpu
 
@@ -64,19 +65,20 @@ def long_case(dtype, B, H, T, n, fill, seed):
     return c, q, kn, vn, i32(np.full((B, T), -1))
 
 
-def exact_long(c, q, kn, vn, n, rows):
-    """The outputs of the drafts `rows` (a slice) in 64 bits, on the GPU."""
+def exact_long(c, q, kn, vn, n, rows, lse=False):
+    """The outputs (and lse) of the drafts `rows` (a slice) in 64 bits, on the GPU."""
     B, H, T, _ = q.shape
     turned = [torch.from_numpy(co.turn(x.double().cpu().numpy(), np.full((B, H, T), n))).cuda()[:, :, rows] for x in (q, kn)]
     out = torch.empty_like(turned[0])
+    log = torch.empty_like(out[..., 0])
     k, v = (x.view(B, -1, H, 64, 64) for x in (c.k, c.v))
     for b in range(B):
         for h in range(H):
             x, own = turned[0][b, h], turned[1][b, h]
             s = torch.cat([x @ k[b, :, h].reshape(-1, 64)[:n].double().T, (x * own).sum(1, keepdim=True)], 1) / 8
-            p = torch.softmax(s, 1)
+            p, log[b, h] = torch.softmax(s, 1), torch.logsumexp(s, 1)
             out[b, h] = p[:, :-1] @ v[b, :, h].reshape(-1, 64)[:n].double() + p[:, -1:] * vn[b, h, rows].double()
-    return out
+    return (out, log) if lse else out
 
 
 @pytest.mark.parametrize("T", [1, 16, 17, 64])
@@ -267,4 +269,169 @@ def test_scores_far_below_zero(dtype, T, nearest):
     assert rl.max() < -1e30
     assert np.all(np.abs(o.double().cpu().numpy() - ro) <= TOL_O + (HALF[dtype] * np.abs(ro) if dtype == "bf16" else 0))
     assert np.all(np.abs(lse.double().cpu().numpy() / rl - 1) <= 2.0 ** -15)  # (a bf16 query is held in 16 bits)
+    plan.close()
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 8), ("bf16", 16), ("bf16", 32), ("bf16", 48), ("bf16", 64), ("f32", 3), ("f32", 40)])
+def test_dense_decode_of_a_long_context(dtype, T):
+    """Every output and lse over 300000 rows; the same rows in pages in another order give the same bits."""
+    B, H, n = 2, 1, 300000
+    c, q, kn, vn, par = long_case(dtype, B, H, T, n, lambda s, g: torch.empty(s, device="cuda").normal_(generator=g), 38)
+    plan = plan_for(n + 100)
+    o, lse = fa.fib_attn_dense_tree_decode(plan, 0, c, q, kn, vn, parent=par)
+    want, want_l = exact_long(c, q, kn, vn, n, slice(0, T), lse=True)
+    order = torch.from_numpy(rng(38).permutation(c.n_pages)).cuda()  # the same rows in other pages
+    moved = torch.empty_like(order)
+    moved[order] = torch.arange(c.n_pages, device="cuda")
+    for x in (c.k, c.v):
+        x.copy_(x[:, order])
+    c.table.copy_(moved[c.table.long()].int())
+    o2, lse2 = fa.fib_attn_dense_tree_decode(plan, 0, c, q, kn, vn, parent=par)
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert ((o.double() - want).abs() <= TOL_O + (HALF[dtype] * want.abs() if dtype == "bf16" else 0)).all()
+    assert ((lse.double() - want_l).abs() <= TOL_LSE).all()
+    plan.close()
+
+
+# ------------------------------------------------------------------------------ large tables
+@pytest.mark.parametrize("S,P,most", [(300, 16, 1000), (1024, 16, 200), (9, 16, 20000)])
+def test_fork_of_a_large_table(S, P, most):
+    """More than 8192 table entries: the two launches."""
+    r = rng(39, S)
+    lens = [int(x) for x in r.integers(0, most, S)]
+    max_pages = -(-most // P)
+    assert S * max_pages > 8192
+    c, ref = make_cache(r, "f32", 1, 1, P, lens, max_pages, spare=300)
+    for _ in range(3):
+        src = [int(x) for x in np.where(r.random(S) < 0.3, np.arange(S), r.integers(-1, S, S))]
+        fa.fib_attn_cache_fork(c, i32(src))
+        ref.fork(src)
+        same_tables(c, ref)
+        cursor = c.state[0].item()
+        assert (c.refs[:cursor] > 0).all()
+    assert fa.fib_attn_cache_status(c) == fa.FIB_OK
+    for bad in ([S] + [-1] * (S - 1), [-1] * (S - 1) + [-2]):
+        before = snapshot(c)
+        fa.fib_attn_cache_fork(c, i32(bad))
+        unchanged(c, before, fa.FIB_ERR_DEVICE_ASSERT)
+    fa.fib_attn_cache_fork(c, i32([-1] * S))
+    assert not c.refs.any() and not c.lens.any() and (c.table == -1).all()
+
+
+def test_fork_of_a_large_table_in_a_graph():
+    r = rng(40)
+    S, P, most = 200, 16, 1000
+    lens = [int(x) for x in r.integers(0, most, S)]
+    c, ref = make_cache(r, "f32", 1, 1, P, lens, -(-most // P))
+    src = i32(np.arange(S))
+    ws = torch.empty(fa.fib_attn_cache_workspace_size(c), dtype=torch.uint8, device="cuda")
+    fa.fib_attn_cache_fork(c, src, workspace=ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        fa.fib_attn_cache_fork(c, src, workspace=ws)
+    for _ in range(3):
+        new = r.integers(-1, S, S)
+        src.copy_(i32(new))
+        g.replay()
+        torch.cuda.synchronize()
+        ref.fork([int(x) for x in new])
+        same_tables(c, ref)
+
+
+def test_a_commit_that_takes_thousands_of_pages():
+    """More pages than the plan keeps in shared memory, from between pages that are in use."""
+    r = rng(41)
+    P, T, lens, n_new = 16, 34000, [5, 0, 33], [33000, 34000, 1]
+    c, ref = make_cache(r, "f32", 1, 1, P, lens, 2200, spare=9000)
+    held = r.random(c.n_pages) < 0.4  # by the caller
+    c.refs += i32(held)
+    ref.refs = [a + int(b) for a, b in zip(ref.refs, held)]
+    (kn, kf), (vn, vf) = draw(r, (1, 3, 1, T, 64), "f32"), draw(r, (1, 3, 1, T, 64), "f32")
+    plan = plan_for(40000)
+    fa.fib_attn_cache_commit(plan, c, kn, vn, i32(n_new))
+    assert ref.commit(kf, vf, n_new)
+    same_tables(c, ref)
+    close_rows(c, ref, "f32")
+    assert fa.fib_attn_cache_status(c) == fa.FIB_OK
+    # and one page too many
+    free = int((c.refs == 0).sum())
+    c.refs[torch.nonzero(c.refs == 0)[:free - 4300].flatten()] = 1
+    c.state[0] = 0
+    before = snapshot(c)
+    fa.fib_attn_cache_commit(plan, c, kn, vn, i32([34000, 0, 34000]))
+    unchanged(c, before, fa.FIB_ERR_DEVICE_ASSERT)  # (33005 + 34000 rows pass the table)
+    c.lens[0] = c.lens[1] = 0
+    before = snapshot(c)
+    fa.fib_attn_cache_commit(plan, c, kn, vn, i32([34000, 34000, 34000]))
+    unchanged(c, before, fa.FIB_ERR_NO_PAGES)
+    plan.close()
+
+
+@pytest.mark.parametrize("where", [None, 1023, 1024, 1030, 2047, 2399])
+def test_paths_of_more_than_a_thousand_entries(where):
+    r = rng(42)
+    B, T, P = 12, 200, 16
+    c, ref = make_cache(r, "bf16", 1, 2, P, [7] * B, 20, spare=200)
+    (kn, kf), (vn, vf) = draw(r, (1, B, 2, T, 64), "bf16"), draw(r, (1, B, 2, T, 64), "bf16")
+    path = np.stack([r.permutation(T) for _ in range(B)])
+    n_new = [T, 3, T, 0, T, T, 150, T, T, T, 199, T]
+    path[3], path[1, 3:], path[10, 199:] = -5, T, 1 << 30  # not taken, so of no matter
+    plan = plan_for()
+    if where is not None:
+        b, i = divmod(where, T)
+        assert i < n_new[b]
+        path[b, i] = T if where % 2 else -1
+        before = snapshot(c)
+        fa.fib_attn_cache_commit(plan, c, kn, vn, i32(n_new), path=i32(path))
+        unchanged(c, before, fa.FIB_ERR_DEVICE_ASSERT)
+    else:
+        fa.fib_attn_cache_commit(plan, c, kn, vn, i32(n_new), path=i32(path))
+        assert ref.commit(kf, vf, n_new, path)
+        same_tables(c, ref)
+        close_rows(c, ref, "bf16")
+    plan.close()
+
+
+# --------------------------------------------------------------- a learned alpha on the device
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("base,alpha,W,N", [("fib", 1.2713, 12, None), ("fib", 0.53, 1, 2000), ("pow2", 0.8125, 9, None)])
+@pytest.mark.parametrize("lens,H,G,T", [([1500, 0, 3], 2, 1, 1), ([700, 129], 3, 2, 9), ([33, 1900, 0, 64], 8, 2, 20)])
+def test_sparse_decode_row_by_row_with_a_device_alpha(dtype, base, alpha, W, N, lens, H, G, T):
+    """Learned alpha: the key table is built on the device, of one row's four warps and of a warp a row."""
+    r = rng(43, T)
+    c, ref, dev, host, parent, live = tree_case(r, dtype, lens, H, G, T, 16, "random", None)
+    plan = fa.fib_attn_plan_create(fa.FIB_BASE_FIBONACCI if base == "fib" else fa.FIB_BASE_POW2, [1.0, 0.7], W, 2048, fa.FIB_MODE_INTERP)
+    learned = torch.tensor([9.0, alpha], device="cuda", dtype=torch.float32)
+    o, lse = sevens(dev[0])
+    fa.fib_attn_tree_decode(plan, 1, c, *dev, parent=i32(parent), o=o, lse=lse, N=N, alpha_dev=learned)
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    keys = keys_of(W, "interp", base, float(learned[1]), N or 2048)
+    check(o, lse, *co.tree_attend(ref, 1, *host, parent, live, keys), live, dtype)
+    plan.close()
+
+
+# ------------------------------------------------------------------------------ bad sequences
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,H,G", [(6, 2, 2), (24, 1, 1), (64, 20, 1)])
+@pytest.mark.parametrize("what", ["nodes", "parent", "len", "page id"])
+def test_outputs_beside_a_bad_sequence(dtype, T, H, G, what):
+    """The sequence after a refused one, its outputs and all, in each kernel."""
+    r = rng(44, T)
+    c, ref, dev, host, parent, live = tree_case(r, dtype, [20, 700, 45], H, G, T, 16, "random", None)
+    plan = plan_for(900)
+    nodes, par = [T] * 3, parent.copy()
+    if what == "nodes":
+        nodes[0] = T + 1
+    elif what == "parent":
+        par[0, 3] = 3
+    elif what == "len":
+        c.lens[0] = 16 * c.max_pages + 1
+    else:
+        c.table[0, 0] = c.n_pages
+    for fn, keys in ((fa.fib_attn_tree_decode, keys_of(8, "mask", "fib", 1.0, 900)), (fa.fib_attn_dense_tree_decode, None)):
+        o, lse = fn(plan, 0, c, *dev, parent=i32(par), n_nodes=i32(nodes))
+        assert fa.fib_attn_last_device_status(plan) == fa.FIB_ERR_DEVICE_ASSERT
+        ro, rl = co.tree_attend(ref, 0, *host, parent, [0, T, T], keys)
+        check(o[1:], lse[1:], ro[1:], rl[1:], [T, T], dtype)
     plan.close()
