@@ -20,10 +20,9 @@
 // tiles (2 where float32 has more than 16 query rows) times 4 / TILES groups; the groups take the units in turn, and each warp keeps an online
 // softmax (running maximum and sum, O in registers) over its units; the groups merge at the end of the run.
 //   bf16: mma.sync m16n8k16 with the keys (then the dimensions of V) as the 16 rows of a tile and 8
-//   query rows as its columns, so that a single query pays for 8 rows and not for 16, and a warp that
-//   holds 32 reads each K and V row once for all of them.  K and V enter as they are stored; the rotated
-//   query and the softmax weights are split in two bf16 (x = hi + lo, 16 bits of significand), each
-//   product twice, so that neither is rounded to 8 bits.
+//   query rows as its columns, so that a single query pays for 8 rows and not for 16.  K and V enter as
+//   they are stored; the rotated query is split in three bf16 (24 bits of significand: lse is float32; with two, 16 bits,
+//   lse was 1.3e-6 off where it is 3e-7 now) and the softmax weights in two (O is rounded to 8 bits).
 //   float32: mma.sync m16n8k8 on tf32 with both operands split (hi, lo): hi*hi + hi*lo + lo*hi, 21 bits;
 //   16 query rows a tile, whose weights are in place for the second product as the first leaves them.
 // The tensor pipes round each sum toward zero (measured: 3.6e-8 of it a product in the mean, all to one side), so that a chain of
@@ -110,7 +109,7 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 template <>
 struct Core<__nv_bfloat16> {
   static constexpr int kRows = 8, UNIT = kUnitRows<__nv_bfloat16>;
-  static constexpr int kQueryBytes = 4 * 512;  // [k-step of 16 dims][lane]: hi, hi, lo, lo
+  static constexpr int kQueryBytes = 4 * 768;  // [k-step of 16 dims][lane]: hi, hi, mid, mid; then lo, lo
   float o[4][4];  // [16 dims][fragment]
   float m[2], l[2];
 
@@ -119,12 +118,16 @@ struct Core<__nv_bfloat16> {
   __device__ __forceinline__ static int load_row(int) { return (threadIdx.x & 31) >> 2; }
   __device__ __forceinline__ static void load_query(const TreeArgs& a, uint4* qs, int, bool in, size_t row, int pos) {
     uint4* at = qs + (threadIdx.x & 31);
+    uint2* low = reinterpret_cast<uint2*>(qs + 128) + (threadIdx.x & 31);
     if (!in) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) at[32 * s] = make_uint4(0, 0, 0, 0);
+      for (int s = 0; s < 4; ++s) {
+        at[32 * s] = make_uint4(0, 0, 0, 0);
+        low[32 * s] = make_uint2(0, 0);
+      }
       return;
     }
-    uint32_t qh[4][2], ql[4][2];
+    uint32_t qh[4][2], qm[4][2], ql[4][2];
     const int t = threadIdx.x & 3;
     const uint32_t* q = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + row * kD);
 #pragma unroll
@@ -136,11 +139,14 @@ struct Core<__nv_bfloat16> {
         const float2 e0 = rope_factor(a.rope_lo, a.rope_hi, pos, d), e1 = rope_factor(a.rope_lo, a.rope_hi, pos, d + 1);
         const float sc = kLog2e / 8.0f;
         const float x0 = bf_lo(x) * sc, x1 = bf_hi(x) * sc, y0 = bf_lo(y) * sc, y1 = bf_hi(y) * sc;
-        split_bf16(x0 * e0.x - y0 * e0.y, x1 * e1.x - y1 * e1.y, qh[s][f], ql[s][f]);
-        split_bf16(x0 * e0.y + y0 * e0.x, x1 * e1.y + y1 * e1.x, qh[s + 2][f], ql[s + 2][f]);
+        split_bf16(x0 * e0.x - y0 * e0.y, x1 * e1.x - y1 * e1.y, qh[s][f], qm[s][f], ql[s][f]);
+        split_bf16(x0 * e0.y + y0 * e0.x, x1 * e1.y + y1 * e1.x, qh[s + 2][f], qm[s + 2][f], ql[s + 2][f]);
       }
 #pragma unroll
-    for (int s = 0; s < 4; ++s) at[32 * s] = make_uint4(qh[s][0], qh[s][1], ql[s][0], ql[s][1]);
+    for (int s = 0; s < 4; ++s) {
+      at[32 * s] = make_uint4(qh[s][0], qh[s][1], qm[s][0], qm[s][1]);
+      low[32 * s] = make_uint2(ql[s][0], ql[s][1]);
+    }
   }
   __device__ __forceinline__ void clear() {
     m[0] = m[1] = -INFINITY;
@@ -151,22 +157,33 @@ struct Core<__nv_bfloat16> {
   __device__ __forceinline__ static void scores(uint32_t kt, const uint4* qs, float (&s)[2][4]) {
     const int mi = (threadIdx.x & 31) >> 3, rl = threadIdx.x & 7;
     const uint32_t row = kt + ((mi & 1) * 8 + rl) * 128;
+    const uint2* low = reinterpret_cast<const uint2*>(qs + 128);
+    float c[2][4];  // the small products apart
 #pragma unroll
-    for (int x = 0; x < 2; ++x) s[x][0] = s[x][1] = s[x][2] = s[x][3] = 0.f;
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[x][e] = c[x][e] = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       uint32_t a[2][4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) ldsm_x4(a[x], row + x * 2048 + (((2 * k + (mi >> 1)) ^ rl) << 4));
       const uint4 q = qs[k * 32 + (threadIdx.x & 31)];
+      const uint2 l = low[k * 32 + (threadIdx.x & 31)];
 #pragma unroll
       for (int x = 0; x < 2; ++x) mma_bf16(s[x], a[x], q.x, q.y);
 #pragma unroll
-      for (int x = 0; x < 2; ++x) mma_bf16(s[x], a[x], q.z, q.w);
+      for (int x = 0; x < 2; ++x) mma_bf16(c[x], a[x], l.x, l.y);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) mma_bf16(c[x], a[x], q.z, q.w);
     }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[x][e] += c[x][e];
   }
   // Where a score came out NaN, the upper parts' product alone: an infinite key keeps its sign there, where
-  // hi + lo may add two infinities of opposite signs.
+  // the parts' sum may add two infinities of opposite signs.
   __device__ __forceinline__ static void mend(uint32_t kt, const uint4* qs, float (&s)[2][4]) {
     const int mi = (threadIdx.x & 31) >> 3, rl = threadIdx.x & 7;
     const uint32_t row = kt + ((mi & 1) * 8 + rl) * 128;
@@ -188,7 +205,7 @@ struct Core<__nv_bfloat16> {
   __device__ __forceinline__ void unit(uint32_t slot, const uint4* qs, uint32_t zero, int valid) {
     const int lane = threadIdx.x & 31, g = lane >> 2, mi = lane >> 3, rl = lane & 7;
     float s[2][4], sum[2];
-    for (bool again = false;;) {  // a second time only where an infinite key made a NaN of hi + lo
+    for (bool again = false;;) {  // a second time only where an infinite key made a NaN of the parts' sum
       scores(slot, qs, s);
       if (again) mend(slot, qs, s);
       if (valid < UNIT) {

@@ -142,6 +142,13 @@ __device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uin
   hi = pack_bf2_rn(x0, x1);
   lo = pack_bf2_rn(x0 - bf_lo(hi), x1 - bf_hi(hi));
 }
+// ... as hi + mid + lo: all 24 bits
+__device__ __forceinline__ void split_bf16(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf2_rn(x0, x1);
+  x0 -= bf_lo(hi);
+  x1 -= bf_hi(hi);
+  split_bf16(x0, x1, mid, lo);
+}
 // What a partial of maximum m and sum l counts where the common maximum is `all`.  One without a finite
 // score counts nothing, unless a NaN is in it, which goes on.
 __device__ __forceinline__ float weight_of(float m, float l, float all) {

@@ -8,7 +8,7 @@
 //
 // Per unit of 128 cached rows, with the keys as the 128 rows of the accumulator:
 //   S^T [128 keys x ROWS] = K Q'^T    K from the ring as TMA left it (K-major, 128-byte swizzle), the rotated
-//                                     query split in two bf16 (hi + lo, 16 bits), both added up
+//                                     query split in three bf16 (24 bits), all added up
 //   P = 2^(S - m)                     a thread a key: its row of S^T from tensor memory to registers, its
 //                                     weights, again hi + lo, to shared memory (16 bytes for 8 query rows)
 //   O^T [64 dims x ROWS] += V^T P^T   V from the ring (its transpose by the descriptor), P as written; O stays
@@ -51,8 +51,8 @@ struct TcShape {
   static constexpr int kColumns = ROWS == 16 ? 64 : ROWS == 32 ? 128 : 256;  // of tensor memory: S twice, O, the sum of earlier O
   static_assert(4 * ROWS <= kColumns, "columns");
   // byte offsets in dynamic shared memory (its base is 1024-byte aligned)
-  static constexpr int kQuery = kSlots * kSlotBytes;    // hi [ROWS][64], lo: K-major, 128-byte swizzle
-  static constexpr int kWeights = kQuery + ROWS * 256;  // hi [ROWS/8][16][8 keys][8 rows], lo; see below for its other uses
+  static constexpr int kQuery = kSlots * kSlotBytes;    // hi [ROWS][64], mid, lo: K-major, 128-byte swizzle
+  static constexpr int kWeights = kQuery + ROWS * 384;  // hi [ROWS/8][16][8 keys][8 rows], lo; see below for its other uses
   static constexpr int kRef = kWeights + ROWS * 512;    // [ROWS] the rows' references, negated
   static constexpr int kMax = kRef + ROWS * 4;          // [2][ROWS]: of the cached keys, of the drafted ones
   static constexpr int kSum = kMax + 2 * ROWS * 4;
@@ -336,11 +336,11 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           fence_after();
           const uint32_t from = base + kt.slot * P::kSlotBytes, d = tmem + (s.count & 1) * ROWS;
 #pragma unroll
-          for (int part = 0; part < 2; ++part)
+          for (int part = 2; part >= 0; --part)
 #pragma unroll
             for (int x = 0; x < 4; ++x)
               mma_tc(d, matrix_at(from + 32 * x, 16, 1024, 2), matrix_at(base + P::kQuery + part * ROWS * 128 + 32 * x, 16, 1024, 2), kScores,
-                     part + x > 0);
+                     part < 2 || x > 0);
           commit_tc(&bars.empty[kt.slot]);
           commit_tc(&bars.scores[s.count & 1]);
           ++s.count;
@@ -426,13 +426,13 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       const int r0 = k.rb * ROWS, rows = min(ROWS, a.G * k.n - r0);
       bool ok = true;
       const WarpTree tree = warp_tree(a, k.b, k.n, &ok);
-      // the rotated query: a quad a row, 16 bytes of hi and of lo for 8 dims
+      // the rotated query: a quad a row, 16 bytes of each part for 8 dims
       for (int r = tid >> 2; r < ROWS; r += CONS / 4) {
         const int t = lane & 3;
         int s = 0;
         const size_t row = r < rows ? row_of(a, k, r0 + r, &s) : 0;
         const int depth = pick32(tree.depth, s);
-        uint32_t hi[8], lo[8];
+        uint32_t hi[8], mid[8], lo[8];
         if (r < rows) {
           float x[16];
           float2 e[8];
@@ -440,16 +440,17 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
           rope_row(a.rope_lo, a.rope_hi, position_of(a, k, depth, &ok), t, e);
           rotate_part(x, e, false);
 #pragma unroll
-          for (int w = 0; w < 8; ++w) split_bf16(x[2 * w] * (kLog2e / 8.0f), x[2 * w + 1] * (kLog2e / 8.0f), hi[w], lo[w]);
+          for (int w = 0; w < 8; ++w) split_bf16(x[2 * w] * (kLog2e / 8.0f), x[2 * w + 1] * (kLog2e / 8.0f), hi[w], mid[w], lo[w]);
         } else {
 #pragma unroll
-          for (int w = 0; w < 8; ++w) hi[w] = lo[w] = 0;
+          for (int w = 0; w < 8; ++w) hi[w] = mid[w] = lo[w] = 0;
         }
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           unsigned char* at = smem + P::kQuery + r * 128 + (((t + 4 * h) ^ (r & 7)) << 4);
           *reinterpret_cast<uint4*>(at) = make_uint4(hi[4 * h], hi[4 * h + 1], hi[4 * h + 2], hi[4 * h + 3]);
-          *reinterpret_cast<uint4*>(at + ROWS * 128) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
+          *reinterpret_cast<uint4*>(at + ROWS * 128) = make_uint4(mid[4 * h], mid[4 * h + 1], mid[4 * h + 2], mid[4 * h + 3]);
+          *reinterpret_cast<uint4*>(at + ROWS * 256) = make_uint4(lo[4 * h], lo[4 * h + 1], lo[4 * h + 2], lo[4 * h + 3]);
         }
       }
       if (tid < ROWS) s_ref[tid] = tid < rows ? kNoKey : 0.f;  // (a row that is none has scores of 0)
@@ -463,12 +464,17 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const unsigned char* at = smem + P::kQuery + r * 128 + (((t + 4 * h) ^ (r & 7)) << 4);
-            const uint4 hi = *reinterpret_cast<const uint4*>(at), lo = *reinterpret_cast<const uint4*>(at + ROWS * 128);
-            const uint32_t x[4] = {hi.x, hi.y, hi.z, hi.w}, z[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              y[8 * h + 2 * w] = bf_lo(x[w]) + bf_lo(z[w]);
-              y[8 * h + 2 * w + 1] = bf_hi(x[w]) + bf_hi(z[w]);
+            for (int w = 0; w < 8; ++w) y[8 * h + w] = 0.f;
+#pragma unroll
+            for (int part = 2; part >= 0; --part) {
+              const uint4 q = *reinterpret_cast<const uint4*>(at + part * ROWS * 128);
+              const uint32_t x[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                y[8 * h + 2 * w] += bf_lo(x[w]);
+                y[8 * h + 2 * w + 1] += bf_hi(x[w]);
+              }
             }
           }
         });
@@ -506,7 +512,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
 #pragma unroll
         for (int r = 1; r + 1 < GR; r += 2) most = max_nan(most, x[r], x[r + 1]);
         if (any_of_group(group, !(max_nan(most, x[GR - 1], x[GR - 1]) <= 8.f))) {  // (a NaN too)
-          // A NaN may come of an infinite key, where hi + lo add infinities of opposite signs: the upper
+          // A NaN may come of an infinite key, where the parts' sum adds infinities of opposite signs: the upper
           // parts' product alone keeps the sign.
           load();  // (its buffer is not written before this unit's weights are there)
           bool bad = false;

@@ -435,3 +435,23 @@ def test_outputs_beside_a_bad_sequence(dtype, T, H, G, what):
         ro, rl = co.tree_attend(ref, 0, *host, parent, [0, T, T], keys)
         check(o[1:], lse[1:], ro[1:], rl[1:], [T, T], dtype)
     plan.close()
+
+
+# ---------------------------------------------------------------------------- lse in 32 bits
+@pytest.mark.parametrize("op", ["dense"])
+@pytest.mark.parametrize("T,H,G", [(1, 24, 1), (5, 8, 1), (16, 4, 1), (11, 3, 2), (47, 2, 1), (64, 2, 1), (64, 8, 1), (24, 32, 2)])
+def test_lse_of_bf16_is_that_of_float32(op, T, H, G):
+    """Short contexts, whose lse is little more than a score.  bf16 inputs, everything between them and lse in float32: of a score of
+    size 1 the sums of the tensor pipes, cut off at four products or so of up to 2^-23 each, leave some 2.5e-7 in the mean square, 2^x
+    and log2 2e-7, rotation and the rest 1e-7: 3.4e-7.  A query that is held in 16 bits leaves 1.3e-6."""
+    r = rng(45, T, H)
+    lens = [0, 1, 2, 3, 5, 9, 17, 40]
+    c, ref, dev, host, parent, live = tree_case(r, "bf16", lens, H, G, T, 16, "random", None, poison=False)
+    plan = plan_for(200)
+    fn, keys = (fa.fib_attn_dense_tree_decode, None) if op == "dense" else (fa.fib_attn_tree_decode, keys_of(8, "mask", "fib", 1.0, 200))
+    _, lse = fn(plan, 0, c, *dev, parent=i32(parent))
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    _, want = co.tree_attend(ref, 0, *host, parent, live, keys)
+    off = np.sqrt(np.mean((lse.double().cpu().numpy() - want) ** 2))
+    assert off <= 5e-7
+    plan.close()
