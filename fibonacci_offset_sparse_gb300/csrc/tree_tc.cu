@@ -9,14 +9,17 @@
 // scores (and blends an interpolated key's two: scores are linear in the key), and its weights go
 // into a matrix of mostly zeros for O = P V.
 //
-//   mma.sync m16n8k16, keys (then dims) as the 16 rows, 8 query rows as the columns, as in tree_dense.cu; the query,
-//   the weights and the drafted keys (rotated here) are split in two bf16, hi + lo.
+//   mma.sync m16n8k16, keys (then dims) as the 16 rows, 8 query rows as the columns, as in tree_dense.cu; the query
+//   and the drafted keys, rotated here, are split in three bf16 (24 bits: lse is float32; 16 bits left 1.9e-6 in it), the
+//   weights in two (O is rounded to 8 bits).
 // A weight 0 times an infinity or NaN is NaN, so rows of which some value is not finite take the block to the
 // row-by-row path, as do trees so deep that the union does not fit even for 8 rows at a time.
 //
 // What bounds it: the latency of a block's steps (lengths and tree; tables; pages; rows; products, weights, products), two
 // blocks an SM by shared memory and registers: 64 sequences of 8 heads and 64 nodes are 512 blocks and take two rounds, 31
 // us for a floor of 4.4 (issue slots 37% busy, tensor pipes 18%).
+#include <algorithm>
+
 #include "tree.cuh"
 
 namespace fibattn {
@@ -40,11 +43,11 @@ TtShape shape_of(int rows, int T, int keys) {
   p.keys = r8 <= 16 ? 304 : r8 <= 32 ? 240 : 176;
   p.stride = p.keys + 4;
   p.v = p.keys * 128;                         // K [keys][64], then V, 16-byte words swizzled by row
-  p.lo = 2 * p.v;                             // the drafted keys' lower parts
+  p.lo = 2 * p.v;                             // the drafted keys' middle parts
   p.s = p.lo + (T + 15) / 16 * 16 * 128;      // [row][stride]: S, then P as hi | lo << 16, then O as bf16
-  p.key = p.s + r8 * p.stride * 4;            // [row][key_stride]: weights by key
+  p.key = p.s + r8 * p.stride * 4;            // the drafted keys' lowest parts, then [row][key_stride]: weights by key
   p.key_stride = keys + 1;
-  p.bytes = p.key + r8 * p.key_stride * 4;
+  p.bytes = p.key + std::max(r8 * p.key_stride * 4, (T + 15) / 16 * 16 * 128);
   return p;
 }
 
@@ -78,6 +81,11 @@ __device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uin
 __device__ __forceinline__ void split2(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   hi = pack_bf2_rn(x0, x1);
   lo = pack_bf2_rn(x0 - bf_lo(hi), x1 - bf_hi(hi));
+}
+// ... as hi + mid + lo
+__device__ __forceinline__ void split3(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf2_rn(x0, x1);
+  split2(x0 - bf_lo(hi), x1 - bf_hi(hi), mid, lo);
 }
 // x as hi | lo << 16
 __device__ __forceinline__ uint32_t split1(float x) {
@@ -222,8 +230,8 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     for (int c = tid - 160; c < nv; c += kTtThreads - 160) ts.key[c] = make_int4(ts.ks.lo[c], ts.ks.need[c], __float_as_int(ts.ks.w[c]), 0);
   }
 
-  // ---- query fragments (hi, lo) of the warp's 8 rows, in registers
-  uint32_t qh[4][2], ql[4][2];
+  // ---- query fragments (hi, mid, lo) of the warp's 8 rows, in registers
+  uint32_t qh[4][2], qm[4][2], ql[4][2];
 #pragma unroll
   for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -232,15 +240,15 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
       const float2 e0 = rope_factor(a.rope_lo, a.rope_hi, pos, d), e1 = rope_factor(a.rope_lo, a.rope_hi, pos, d + 1);
       const float sc = kLog2e / 8.0f;
       const float x0 = bf_lo(qx[k][f]) * sc, x1 = bf_hi(qx[k][f]) * sc, y0 = bf_lo(qy[k][f]) * sc, y1 = bf_hi(qy[k][f]) * sc;
-      split2(x0 * e0.x - y0 * e0.y, x1 * e1.x - y1 * e1.y, qh[k][f], ql[k][f]);
-      split2(x0 * e0.y + y0 * e0.x, x1 * e1.y + y1 * e1.x, qh[k + 2][f], ql[k + 2][f]);
+      split3(x0 * e0.x - y0 * e0.y, x1 * e1.x - y1 * e1.y, qh[k][f], qm[k][f], ql[k][f]);
+      split3(x0 * e0.y + y0 * e0.x, x1 * e1.y + y1 * e1.x, qh[k + 2][f], qm[k + 2][f], ql[k + 2][f]);
     }
-  // ---- drafted rows: K rotated, hi in the K tile and lo apart; zeros behind the last
-  if (du < drafts) {
-    uint32_t hi[8], lo[8];
+  // ---- drafted rows: K rotated, hi in the K tile, mid and lo apart; zeros behind the last
+  auto stage_draft = [&](const uint4 (&kr)[2], bool again) {  // (again: lo alone, whose room the weights have taken)
+    uint32_t hi[8], mid[8], lo[8];
     float x[16];
     float2 e[8];
-    const uint32_t w[8] = {dk[0].x, dk[0].y, dk[0].z, dk[0].w, dk[1].x, dk[1].y, dk[1].z, dk[1].w};
+    const uint32_t w[8] = {kr[0].x, kr[0].y, kr[0].z, kr[0].w, kr[1].x, kr[1].y, kr[1].z, kr[1].w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       x[2 * i] = bf_lo(w[i]);
@@ -250,17 +258,23 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     rotate_part(x, e, false);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      split2(x[2 * i], x[2 * i + 1], hi[i], lo[i]);
+      split3(x[2 * i], x[2 * i + 1], hi[i], mid[i], lo[i]);
       bad |= not_finite(hi[i]);
     }
-    bad |= not_finite(dv[0]) | not_finite(dv[1]);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int at = du * 128 + (((t + 4 * i) ^ (du & 7)) << 4);
+      *reinterpret_cast<uint4*>(smem + shape.key + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+      if (again) continue;
       *reinterpret_cast<uint4*>(smem + at) = make_uint4(hi[4 * i], hi[4 * i + 1], hi[4 * i + 2], hi[4 * i + 3]);
-      *reinterpret_cast<uint4*>(smem + shape.lo + at) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
-      *reinterpret_cast<uint4*>(smem + shape.v + at) = dv[i];
+      *reinterpret_cast<uint4*>(smem + shape.lo + at) = make_uint4(mid[4 * i], mid[4 * i + 1], mid[4 * i + 2], mid[4 * i + 3]);
     }
+  };
+  if (du < drafts) {
+    stage_draft(dk, false);
+    bad |= not_finite(dv[0]) | not_finite(dv[1]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) *reinterpret_cast<uint4*>(smem + shape.v + du * 128 + (((t + 4 * i) ^ (du & 7)) << 4)) = dv[i];
   }
   __syncthreads();
   const int step = ts.step;
@@ -274,6 +288,16 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
           w = __int_as_float(ts.key[c].z);
           return ts.key[c].x;
         });
+      if (from > 0 && du < drafts) {
+        uint4 kr[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+        if (du < n) {
+          const size_t at = ((static_cast<size_t>(b) * a.H + h) * a.T + du) * kD;
+          const uint4* row = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kn) + at);
+          kr[0] = __ldg(row + t);
+          kr[1] = __ldg(row + t + 4);
+        }
+        stage_draft(kr, true);
+      }
       __syncthreads();
     }
     const int total = ts.at[nr + 1], padded = (total + 15) & ~15;
@@ -326,10 +350,11 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
     }
     if (__syncthreads_or(bad)) break;  // the rows from here on one by one
 
-    // ---- 8 query rows a warp, without a further barrier
-    if (8 * warp >= from && 8 * warp < min(from + step, rows)) {
-      const int mi = lane >> 3, rl = lane & 7, stride = shape.stride;
-      uint32_t* S = reinterpret_cast<uint32_t*>(smem + shape.s) + 8 * warp * stride;
+    // ---- 8 query rows a warp
+    const bool takes = 8 * warp >= from && 8 * warp < min(from + step, rows);
+    const int mi = lane >> 3, rl = lane & 7, stride = shape.stride;
+    uint32_t* S = reinterpret_cast<uint32_t*>(smem + shape.s) + 8 * warp * stride;
+    if (takes) {
 #pragma unroll 2
       for (int x0 = 0; x0 < padded; x0 += 16) {
         float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}}, d[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
@@ -341,12 +366,17 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
           ldsm4(ka, row + word);
           mma16(c[k & 1], ka, qh[k][0], qh[k][1]);
           mma16(d[k & 1], ka, ql[k][0], ql[k][1]);
+          mma16(d[k & 1], ka, qm[k][0], qm[k][1]);
         }
         if (x0 < drafts) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             uint32_t ka[4];
-            ldsm4(ka, row + shape.lo + (((2 * k + (mi >> 1)) ^ rl) << 4));
+            const uint32_t word = ((2 * k + (mi >> 1)) ^ rl) << 4;
+            ldsm4(ka, row + shape.key + word);
+            mma16(d[k & 1], ka, qh[k][0], qh[k][1]);
+            ldsm4(ka, row + shape.lo + word);
+            mma16(d[k & 1], ka, qm[k][0], qm[k][1]);
             mma16(d[k & 1], ka, qh[k][0], qh[k][1]);
           }
         }
@@ -354,7 +384,9 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
         for (int e = 0; e < 4; ++e)
           S[(2 * t + (e & 1)) * stride + x0 + g + 8 * (e >> 1)] = __float_as_uint((c[0][e] + c[1][e]) + (d[0][e] + d[1][e]));
       }
-      __syncwarp();
+    }
+    __syncthreads();  // the drafted keys' lowest parts are read; from here on a warp keeps to its own rows
+    if (takes) {
       // weights: 4 lanes a row (this lane's: g), keys t, t + 4, ...
       const bool in = qr < rows;
       uint32_t* row = S + g * stride;

@@ -438,7 +438,7 @@ def test_outputs_beside_a_bad_sequence(dtype, T, H, G, what):
 
 
 # ---------------------------------------------------------------------------- lse in 32 bits
-@pytest.mark.parametrize("op", ["dense"])
+@pytest.mark.parametrize("op", ["dense", "sparse"])
 @pytest.mark.parametrize("T,H,G", [(1, 24, 1), (5, 8, 1), (16, 4, 1), (11, 3, 2), (47, 2, 1), (64, 2, 1), (64, 8, 1), (24, 32, 2)])
 def test_lse_of_bf16_is_that_of_float32(op, T, H, G):
     """Short contexts, whose lse is little more than a score.  bf16 inputs, everything between them and lse in float32: of a score of
@@ -454,4 +454,24 @@ def test_lse_of_bf16_is_that_of_float32(op, T, H, G):
     _, want = co.tree_attend(ref, 0, *host, parent, live, keys)
     off = np.sqrt(np.mean((lse.double().cpu().numpy() - want) ** 2))
     assert off <= 5e-7
+    plan.close()
+
+
+def test_lse_of_bf16_where_the_union_takes_two_steps():
+    """The same for the sparse decode of a tree so deep that its rows are served in two steps: queries four times as large, cached
+    keys of 0, so that the drafted keys make lse; four times the errors above."""
+    r = rng(46)
+    c, ref, dev, host, parent, live = tree_case(r, "bf16", [1500], 40, 1, 64, 64, "random", None, poison=False)
+    parent = np.arange(64)[None] - 4
+    parent[parent < 0] = -1
+    c.k.zero_()
+    ref.k[...] = 0
+    dev[0].mul_(4)
+    host[0][...] *= 4
+    plan = plan_for(2000)
+    _, lse = fa.fib_attn_tree_decode(plan, 0, c, *dev, parent=i32(parent))
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    _, want = co.tree_attend(ref, 0, *host, parent, live, keys_of(8, "mask", "fib", 1.0, 2000))
+    off = np.sqrt(np.mean((lse.double().cpu().numpy() - want) ** 2, axis=(0, 1)))
+    assert off[:32].max() <= 2e-6 and off[32:].max() <= 2e-6
     plan.close()
