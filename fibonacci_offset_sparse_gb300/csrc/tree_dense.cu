@@ -536,7 +536,8 @@ struct DtSmem {
   static constexpr int kMax = kAcc + kRows * kAccStride * 4;
   static constexpr int kSum = kMax + (kGroups + 1) * kRows * 4;
   static constexpr int kZero = (kSum + (kGroups + 1) * kRows * 4 + 127) / 128 * 128;
-  static constexpr int kQuery = kZero + 128;
+  static constexpr int kFixed = kZero + 128;  // barriers, flag, positions: statically they would be padded to the base's 1024 bytes
+  static constexpr int kQuery = kFixed + (2 * 8 * kSlots + 16 + 4 * kRows + 127) / 128 * 128;
   static constexpr int kDraft = kQuery + TILES * C::kQueryBytes;
   static size_t bytes(int B, int T) { return kDraft + static_cast<size_t>(T) * kD * 8 + schedule_bytes(B); }
   static size_t most_bytes() { return bytes(kMaxSeqs, TILES == 1 ? kRows : kMaxDrafts); }
@@ -552,9 +553,10 @@ __global__ void __launch_bounds__(DtSmem<DT, TILES>::kThreads, DtSmem<DT, TILES>
   constexpr int kSlots = S::kSlots;
   static_assert(kSlots % GROUPS == 0, "a slot belongs to one group");
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) uint64_t full_bar[kSlots], empty_bar[kSlots];
-  __shared__ volatile int s_err;
-  __shared__ int s_pos[ROWS];  // positions of a piece's rows
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + S::kFixed);
+  uint64_t* empty_bar = full_bar + kSlots;
+  volatile int& s_err = *reinterpret_cast<volatile int*>(empty_bar + kSlots);
+  int* s_pos = reinterpret_cast<int*>(smem + S::kFixed + 16 * kSlots + 16);  // positions of a piece's rows
   const TreeArgs& a = da.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
