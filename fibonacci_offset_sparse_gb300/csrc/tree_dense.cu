@@ -154,6 +154,10 @@ struct Core<__nv_bfloat16> {
 #pragma unroll
     for (int x = 0; x < 4; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
   }
+  // Bits that are there only when every product with V is, and so every load of K and V by any lane.
+  __device__ __forceinline__ uint32_t touched() const {
+    return __float_as_uint(o[0][0]) | __float_as_uint(o[1][0]) | __float_as_uint(o[2][0]) | __float_as_uint(o[3][0]);
+  }
   __device__ __forceinline__ static void scores(uint32_t kt, const uint4* qs, float (&s)[2][4]) {
     const int mi = (threadIdx.x & 31) >> 3, rl = threadIdx.x & 7;
     const uint32_t row = kt + ((mi & 1) * 8 + rl) * 128;
@@ -346,6 +350,12 @@ struct Core<float> {
     l[0] = l[1] = 0.f;
 #pragma unroll
     for (int n = 0; n < 8; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  }
+  __device__ __forceinline__ uint32_t touched() const {  // as above
+    uint32_t x = 0;
+#pragma unroll
+    for (int n = 0; n < 8; ++n) x |= __float_as_uint(o[n][0]);
+    return x;
   }
   __device__ __forceinline__ static void scores(uint32_t kt, const uint4* qs, float (&s)[NT][4]) {
     const int mi = (threadIdx.x & 31) >> 3, rl = threadIdx.x & 7;
@@ -636,7 +646,9 @@ __global__ void __launch_bounds__(DtSmem<DT, TILES>::kThreads, DtSmem<DT, TILES>
       }
       core.unit(ring + slot * kSlotBytes, qs, zero, k.len - i * UNIT);
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty_bar[slot]);
+      // The slot is released when its values have come, not when their loads were sent: the address waits for the products.  Loads
+      // that other blocks' traffic held up in the SM would else be overtaken by the release, and the next copy by them.
+      if (lane == 0) mbar_arrive_at(smem_addr(&empty_bar[slot]) + (core.touched() & da.zero));
     }
     // ---- merge the groups (and the drafted keys' part) in a fixed order
     core.finish();
@@ -726,6 +738,7 @@ cudaError_t launch_dense_tree(const TreeArgs& a, int dtype, unsigned long long w
   da.part = static_cast<float*>(ws);
   da.wait_ns = wait_ns;
   da.split = nullptr;
+  da.zero = 0;
   da.blocks = 0;
   const int rows = a.G * a.T;
   if (dtype == FIB_DTYPE_F32) return rows <= 16 ? launch<float, 1>(da, stream) : launch<float, 2>(da, stream);

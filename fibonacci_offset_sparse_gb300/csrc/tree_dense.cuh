@@ -30,6 +30,7 @@ struct DenseTreeArgs {
   unsigned long long wait_ns;
   int blocks;   // blocks of the grid
   int skip_copy;  // test hook: the first unit's K of every task is never copied
+  uint32_t zero;  // 0, which the compiler does not know
 };
 
 // ------------------------------------------------------------------------------ schedule --
@@ -186,6 +187,10 @@ constexpr unsigned long long kDrainNs = 2000000000ull;
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, unsigned long long limit_ns, volatile int* s_err) {
   const bool there = !*s_err && mbar_wait(bar, parity, limit_ns);
   return __all_sync(0xffffffffu, there);
+}
+
+__device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(bar) : "memory");
 }
 
 // The feeding warp: K and V rows of the units of [u0, u1) into the ring's slots, a page at a time.  A slot

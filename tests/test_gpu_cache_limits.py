@@ -475,3 +475,23 @@ def test_lse_of_bf16_where_the_union_takes_two_steps():
     off = np.sqrt(np.mean((lse.double().cpu().numpy() - want) ** 2, axis=(0, 1)))
     assert off[:32].max() <= 2e-6 and off[32:].max() <= 2e-6
     plan.close()
+
+
+# ------------------------------------------------------------------- traffic of other blocks
+@pytest.mark.parametrize("dtype,T,H", [("f32", 64, 20), ("f32", 16, 30), ("f32", 1, 64), ("bf16", 1, 64), ("bf16", 8, 64), ("bf16", 16, 40),
+                                       ("bf16", 64, 20)])
+def test_the_same_bits_beside_blocks_that_report_at_once(dtype, T, H):
+    """The blocks of a refused tree all write the status word, which holds up the loads of the blocks beside them: the other
+    sequences' outputs are the same bits as without, every time."""
+    r = rng(47, T)
+    c, ref, dev, host, parent, live = tree_case(r, dtype, [20, 700, 45, 900], H, 1, T, 16, "random", None)
+    plan, good, bad = plan_for(1000), i32(parent), i32(parent)
+    bad[0, T // 2] = T // 2
+    for fn in (fa.fib_attn_dense_tree_decode, fa.fib_attn_tree_decode):
+        want = [x.clone() for x in fn(plan, 0, c, *dev, parent=good)]
+        assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+        for _ in range(100):
+            got = fn(plan, 0, c, *dev, parent=bad)
+            assert all(torch.equal(x[1:], y[1:]) for x, y in zip(got, want))
+        assert fa.fib_attn_last_device_status(plan) == fa.FIB_ERR_DEVICE_ASSERT
+    plan.close()
