@@ -534,7 +534,7 @@ struct Core<float> {
 template <typename DT, int TILES>
 struct DtSmem {
   using C = Core<DT>;
-  static constexpr bool kHalves = sizeof(DT) == 2;
+  static constexpr bool kHalves = sizeof(DT) == 2, kPacked = false;
   static constexpr int kUnit = C::UNIT, kTaskCost = 12, kLeast = 4;
   static constexpr int kGroups = TILES == 1 ? 4 : 2, kCons = 32 * TILES * kGroups, kThreads = kCons + 32;
   static constexpr int kRows = C::kRows * TILES;
@@ -549,7 +549,7 @@ struct DtSmem {
   static constexpr int kFixed = kZero + 128;  // barriers, flag, positions: statically they would be padded to the base's 1024 bytes
   static constexpr int kQuery = kFixed + (2 * 8 * kSlots + 16 + 4 * kRows + 127) / 128 * 128;
   static constexpr int kDraft = kQuery + TILES * C::kQueryBytes;
-  static size_t bytes(int B, int T) { return kDraft + static_cast<size_t>(T) * kD * 8 + schedule_bytes(B); }
+  static size_t bytes(int B, int T) { return kDraft + static_cast<size_t>(T) * kD * 8 + Schedule<kPacked>::bytes(B); }
   static size_t most_bytes() { return bytes(kMaxSeqs, TILES == 1 ? kRows : kMaxDrafts); }
 };
 
@@ -579,10 +579,10 @@ __global__ void __launch_bounds__(DtSmem<DT, TILES>::kThreads, DtSmem<DT, TILES>
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   if (tid < 32) reinterpret_cast<float*>(smem + S::kZero)[tid] = 0.f;
-  const Schedule sch = schedule_at(smem + S::kDraft + a.T * kD * 8, a.B);
+  const Schedule<S::kPacked> sch(smem + S::kDraft + a.T * kD * 8, a.B);
   build_schedule<S>(a, sch);
   if (tid == 0) clear_splits(da);
-  const long long cost = sch.start[a.B];
+  const long long cost = sch.end(a.B);
   const int sharing = sharing_blocks(cost, da.blocks, S::kLeast);
   if (static_cast<int>(blockIdx.x) >= sharing) return;
   const long long u0 = cut(cost, sharing, blockIdx.x), u1 = cut(cost, sharing, blockIdx.x + 1);

@@ -34,21 +34,52 @@ struct DenseTreeArgs {
 };
 
 // ------------------------------------------------------------------------------ schedule --
-// In shared memory: the cost before each sequence, and the sequences' rows and nodes.
+// In shared memory: the cost before each sequence, and the sequences' rows and nodes (which where n is 0 are never looked up).
+template <bool PACKED>
 struct Schedule {
-  long long* start;  // [B + 1]
-  int* len;          // [B]
-  int* n;            // [B]; 0 where the sequence has nothing to do
-};
+  long long* at;  // [B + 1]
+  int* rows;      // [B]
+  int* nodes;     // [B]
 
-__device__ __forceinline__ Schedule schedule_at(unsigned char* smem, int B) {
-  Schedule s;
-  s.start = reinterpret_cast<long long*>(smem);
-  s.len = reinterpret_cast<int*>(s.start + B + 1);
-  s.n = s.len + B;
-  return s;
-}
-inline size_t schedule_bytes(int B) { return (sizeof(long long) * (B + 1) + 2 * sizeof(int) * B + 127) / 128 * 128; }
+  __device__ __forceinline__ Schedule(unsigned char* smem, int B)
+      : at(reinterpret_cast<long long*>(smem)), rows(reinterpret_cast<int*>(at + B + 1)), nodes(rows + B) {}
+  static size_t bytes(int B) { return (sizeof(long long) * (B + 1) + 2 * sizeof(int) * B + 127) / 128 * 128; }
+  __device__ __forceinline__ long long start(int b) const { return at[b]; }
+  __device__ __forceinline__ int len(int b) const { return rows[b]; }
+  __device__ __forceinline__ int n(int b) const { return nodes[b]; }
+  __device__ __forceinline__ void set(int b, long long start, int len, int n) const {
+    at[b] = start;
+    rows[b] = len;
+    nodes[b] = n;
+  }
+  __device__ __forceinline__ void move(int b, long long start) const { at[b] = start; }
+  __device__ __forceinline__ void end(int B, long long cost) const { at[B] = cost; }
+  __device__ __forceinline__ long long end(int B) const { return *static_cast<volatile long long*>(at + B); }
+};
+// The same in half the room, for batches so long that it decides how many blocks share an SM; a little slower to look up.  Of
+// a word the upper 38 bits are the cost (at most 2^16 units and kTaskCost for 1024 query heads of 64 nodes in tasks of 32 rows, or
+// 1024 heads of one, for 1024 sequences), 20 the rows (below 2^20, as positions are), 6 the nodes less 1.
+template <>
+struct Schedule<true> {
+  unsigned long long* word;  // [B + 1]
+
+  __device__ __forceinline__ Schedule(unsigned char* smem, int) : word(reinterpret_cast<unsigned long long*>(smem)) {}
+  static size_t bytes(int B) { return sizeof(unsigned long long) * (B + 1); }
+  __device__ __forceinline__ long long start(int b) const { return static_cast<long long>(word[b] >> 26); }
+  __device__ __forceinline__ int len(int b) const { return static_cast<int>(word[b] >> 6) & 0xfffff; }
+  __device__ __forceinline__ int n(int b) const { return (static_cast<int>(word[b]) & 63) + 1; }
+  __device__ __forceinline__ void set(int b, long long start, int len, int n) const {
+    word[b] = static_cast<unsigned long long>(start) << 26 | static_cast<unsigned long long>(len & 0xfffff) << 6 | ((n - 1) & 63);
+  }
+  __device__ __forceinline__ void move(int b, long long start) const {
+    word[b] = static_cast<unsigned long long>(start) << 26 | (word[b] & 0x3ffffff);
+  }
+  __device__ __forceinline__ void end(int B, long long cost) const { word[B] = static_cast<unsigned long long>(cost) << 26; }
+  __device__ __forceinline__ long long end(int B) const {
+    return static_cast<long long>(*static_cast<volatile unsigned long long*>(word + B) >> 26);
+  }
+};
+static_assert(kMaxDrafts == 64 && kMaxSeqs == 1024 && FIB_MAX_HEADS == 1024, "bits of a word");
 
 template <int UNIT>
 __device__ __forceinline__ int units_of(int len) {
@@ -57,33 +88,32 @@ __device__ __forceinline__ int units_of(int len) {
 
 // Every thread of the block; ends synchronised.
 template <typename P>
-__device__ __forceinline__ void build_schedule(const TreeArgs& a, const Schedule& s) {
+__device__ __forceinline__ void build_schedule(const TreeArgs& a, const Schedule<P::kPacked>& s) {
   for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
     int n, len;
     if (!sequence_of(a, b, &n, &len)) {
       atomicExch(a.status, kStatusDeviceAssert);
       n = len = 0;
     }
-    s.len[b] = len;
-    s.n[b] = n;
-    s.start[b + 1] = n == 0 ? 0 : static_cast<long long>(units_of<P::kUnit>(len) + P::kTaskCost) * a.H *
-                         ((a.G * n + P::kRows - 1) / P::kRows);
+    // the sequence's own cost first
+    s.set(b, n == 0 ? 0 : static_cast<long long>(units_of<P::kUnit>(len) + P::kTaskCost) * a.H * ((a.G * n + P::kRows - 1) / P::kRows), len, n);
   }
-  if (threadIdx.x == 0) s.start[0] = 0;
   __syncthreads();
   if (threadIdx.x < 32) {
     long long base = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const int b = b0 + static_cast<int>(threadIdx.x);
-      long long x = b < a.B ? s.start[b + 1] : 0;
+      const long long own = b < a.B ? s.start(b) : 0;
+      long long x = own;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
         const long long y = __shfl_up_sync(0xffffffffu, x, d);
         if (static_cast<int>(threadIdx.x) >= d) x += y;
       }
-      if (b < a.B) s.start[b + 1] = base + x;
+      if (b < a.B) s.move(b, base + x - own);
       base += __shfl_sync(0xffffffffu, x, 31);
     }
+    if (threadIdx.x == 0) s.end(a.B, base);
   }
   __syncthreads();
 }
@@ -111,24 +141,24 @@ struct Task {
   int first, last;   // units [first, last); none where only a part of the task's own cost is in the run
 };
 template <typename P>
-__device__ __forceinline__ Task task_of(const TreeArgs& a, const Schedule& s, long long u, long long end) {
-  int lo = 0, hi = a.B;  // start[lo] <= u < start[hi]
+__device__ __forceinline__ Task task_of(const TreeArgs& a, const Schedule<P::kPacked>& s, long long u, long long end) {
+  int lo = 0, hi = a.B;  // start(lo) <= u < start(hi)
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
-    if (s.start[mid] <= u)
+    if (s.start(mid) <= u)
       lo = mid;
     else
       hi = mid;
   }
   Task t;
   t.b = lo;
-  t.len = s.len[lo];
-  t.n = s.n[lo];
+  t.len = s.len(lo);
+  t.n = s.n(lo);
   t.units = units_of<P::kUnit>(t.len);
   const int rbs = (a.G * t.n + P::kRows - 1) / P::kRows, each = t.units + P::kTaskCost;
-  const long long off = u - s.start[lo];
+  const long long off = u - s.start(lo);
   const int task = off < 1LL << 31 ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(each)) : static_cast<int>(off / each);
-  t.start = s.start[lo] + static_cast<long long>(task) * each;
+  t.start = s.start(lo) + static_cast<long long>(task) * each;
   t.h = task / rbs;
   t.rb = task - t.h * rbs;
   const long long last = min(end - t.start, static_cast<long long>(each)) - P::kTaskCost;
@@ -198,7 +228,7 @@ __device__ __forceinline__ void mbar_arrive_at(uint32_t bar) {
 // when every warp that reads it has seen its rows land and is done with them: one that gives up does not release it, and the
 // feeder then gives up too, so that no copy is ever under way into a slot of which another has not landed.
 template <typename DT, typename P>
-__device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule& sch, long long u0, long long u1, const CUtensorMap* map_k,
+__device__ __forceinline__ void feed(const DenseTreeArgs& da, const Schedule<P::kPacked>& sch, long long u0, long long u1, const CUtensorMap* map_k,
                                      const CUtensorMap* map_v, unsigned char* ring, uint64_t* full_bar, uint64_t* empty_bar,
                                      volatile int* s_err) {
   static_assert(sizeof(DT) == 2 || P::kUnit <= 16, "a unit's float32 rows are one copy: they lie in one page");

@@ -35,7 +35,20 @@ namespace {
 constexpr int kChain = 16;
 constexpr float kNoKey = FLT_MAX;  // a row's reference, negated, before it has met a finite score: below every score
 
-template <int ROWS>
+// Barriers and what the warps tell one another.
+struct TcFixed {
+  uint64_t full[10], empty[10];  // slots of the ring
+  uint64_t scores[2];            // S of a unit is in its buffer (units alternate)
+  uint64_t weights;              // P of a unit is in shared memory
+  uint64_t added;                // ... and in O
+  uint64_t query;                // Q' of a piece is in shared memory
+  uint64_t drained;
+  long long run[2], place;       // the block's run; where in it the softmax warps are
+  uint32_t tmem;
+  int err;
+};
+
+template <int ROWS, bool PACKED>
 struct TcShape {
   // Task cost: 256 tasks of 64 rows over 4096 cached ones take 66 us at 12, 77 at 8 and 68 at 16; 16 x 65536 177, 182, 178.
   // Units a block: one sequence and head of 30000 rows takes 23 us at 3, 39 at 1 and 22 at 6; 8 heads of 4096 17, 21 and 19.
@@ -57,8 +70,11 @@ struct TcShape {
   static constexpr int kMax = kRef + ROWS * 4;          // [2][ROWS]: of the cached keys, of the drafted ones
   static constexpr int kSum = kMax + 2 * ROWS * 4;
   static constexpr int kWarpMax = kSum + 2 * ROWS * 4;  // [4][ROWS]; at the end the two parts' weights [2][ROWS]
-  static constexpr int kSchedule = kWarpMax + 4 * ROWS * 4;
-  static size_t bytes(int B) { return kSchedule + schedule_bytes(B); }
+  // Where two blocks share an SM the barriers are dynamic memory too: static memory is padded to the dynamic base's 1024 bytes.
+  static constexpr int kFixed = kWarpMax + 4 * ROWS * 4;
+  static constexpr int kSchedule = kFixed + (kResident == 2 ? sizeof(TcFixed) : 0);
+  static constexpr bool kPacked = PACKED;
+  static size_t bytes(int B) { return kSchedule + Schedule<PACKED>::bytes(B); }
 };
 
 // ------------------------------------------------------------------- tensor memory and products --
@@ -179,7 +195,7 @@ struct Tile {
 
 // Their feeder: K, then V of each unit of [u0, u1), a page at a time.
 template <typename P>
-__device__ __forceinline__ void feed_tiles(const DenseTreeArgs& da, const Schedule& sch, long long u0, long long u1, const CUtensorMap* map_k,
+__device__ __forceinline__ void feed_tiles(const DenseTreeArgs& da, const Schedule<P::kPacked>& sch, long long u0, long long u1, const CUtensorMap* map_k,
                                            const CUtensorMap* map_v, unsigned char* ring, uint64_t* full_bar, uint64_t* empty_bar,
                                            volatile int* s_err) {
   const TreeArgs& a = da.a;
@@ -235,26 +251,27 @@ __device__ __forceinline__ void feed_tiles(const DenseTreeArgs& da, const Schedu
   if (*s_err && lane == 0) atomicExch(a.status, kStatusTimeout);
 }
 
-struct TcBars {
-  uint64_t full[10], empty[10];  // slots of the ring
-  uint64_t scores[2];            // S of a unit is in its buffer (units alternate)
-  uint64_t weights;              // P of a unit is in shared memory
-  uint64_t added;                // ... and in O
-  uint64_t query;                // Q' of a piece is in shared memory
-  uint64_t drained;
-};
+template <typename P>
+__device__ __forceinline__ TcFixed* fixed_at(unsigned char* smem) {
+  if constexpr (P::kResident == 2) {
+    return reinterpret_cast<TcFixed*>(smem + P::kFixed);
+  } else {
+    __shared__ __align__(8) TcFixed fixed;
+    return &fixed;
+  }
+}
 
-template <int ROWS>
-__global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResident)
+template <int ROWS, bool PACKED>
+__global__ void __launch_bounds__(TcShape<ROWS, PACKED>::kThreads, TcShape<ROWS, PACKED>::kResident)
     dense_tree_tc_kernel(const __grid_constant__ DenseTreeArgs da, const __grid_constant__ CUtensorMap map_k,
                          const __grid_constant__ CUtensorMap map_v) {
-  using P = TcShape<ROWS>;
+  using P = TcShape<ROWS, PACKED>;
   constexpr int CONS = P::kCons, GR = P::kGroupRows, kFeeder = CONS / 32, kIssuer = kFeeder + 1;
   extern __shared__ __align__(1024) unsigned char smem[];
-  __shared__ __align__(8) TcBars bars;
-  __shared__ uint32_t s_tmem;
-  __shared__ volatile int s_err;
-  __shared__ volatile long long s_run[2], s_place;  // the block's run; where in it the softmax warps are
+  TcFixed& bars = *fixed_at<P>(smem);
+  volatile int& s_err = bars.err;
+  volatile long long(&s_run)[2] = bars.run;
+  volatile long long& s_place = bars.place;
   const TreeArgs& a = da.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
@@ -282,10 +299,10 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       prefetch_l2(static_cast<const __nv_bfloat16*>(a.vn) + x * kD);
     }
   }
-  const Schedule sch = schedule_at(smem + P::kSchedule, a.B);
+  const Schedule<PACKED> sch(smem + P::kSchedule, a.B);
   build_schedule<P>(a, sch);
   if (tid == 0) clear_splits(da);
-  const long long cost = sch.start[a.B];
+  const long long cost = sch.end(a.B);
   const int sharing = sharing_blocks(cost, da.blocks, P::kLeast);
   if (static_cast<int>(blockIdx.x) >= sharing) return;
   const long long u0 = cut(cost, sharing, blockIdx.x), u1 = cut(cost, sharing, blockIdx.x + 1);
@@ -293,11 +310,11 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
     s_run[0] = u0;
     s_run[1] = u1;
   }
-  if (warp == kIssuer) tmem_alloc(&s_tmem, P::kColumns);
+  if (warp == kIssuer) tmem_alloc(&bars.tmem, P::kColumns);
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = s_tmem, tmem_o = tmem + 2 * ROWS, tmem_sum = tmem + 3 * ROWS;
+  const uint32_t tmem = bars.tmem, tmem_o = tmem + 2 * ROWS, tmem_sum = tmem + 3 * ROWS;
   const uint32_t base = smem_addr(smem);
 
   if (warp == kFeeder) {
@@ -416,7 +433,7 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
       }
       if (tid == 0) s_place = u;
       if (tid == 0) {
-        const long long all = *static_cast<volatile long long*>(sch.start + a.B);
+        const long long all = sch.end(a.B);
         note_split<P>(da, k, all, sharing_blocks(all, da.blocks, P::kLeast));
       }
       const int k_first = k.first, k_last = k.last, k_len = k.len;
@@ -698,19 +715,19 @@ __global__ void __launch_bounds__(TcShape<ROWS>::kThreads, TcShape<ROWS>::kResid
   if (warp == kIssuer) tmem_free(tmem, P::kColumns);
 }
 
-template <int ROWS>
+template <int ROWS, bool PACKED = false>
 cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
-  using P = TcShape<ROWS>;
+  using P = TcShape<ROWS, PACKED>;
   DenseTreeArgs da = args;
   da.blocks = 152 * P::kResident;  // 152 SMs
   da.split = reinterpret_cast<Split*>(da.part + static_cast<size_t>(da.blocks) * ROWS * (2 * kDtPart + kAccStride));
   const size_t smem = P::bytes(da.a.B);
-  cudaError_t e = allow_shared(dense_tree_tc_kernel<ROWS>, P::bytes(kMaxSeqs));
+  cudaError_t e = allow_shared(dense_tree_tc_kernel<ROWS, PACKED>, P::bytes(kMaxSeqs));
   if (e != cudaSuccess) return e;
   CUtensorMap mk, mv;
   e = maps_of(da.a, 2, P::kUnit, &mk, &mv);
   if (e != cudaSuccess) return e;
-  dense_tree_tc_kernel<ROWS><<<da.blocks, P::kThreads, smem, stream>>>(da, mk, mv);
+  dense_tree_tc_kernel<ROWS, PACKED><<<da.blocks, P::kThreads, smem, stream>>>(da, mk, mv);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_join<__nv_bfloat16, P>(da, stream);
@@ -719,7 +736,7 @@ cudaError_t launch(const DenseTreeArgs& args, cudaStream_t stream) {
 template <int ROWS>
 size_t part_bytes() {
   // two partials a block, and the drafted keys' part of a piece
-  return static_cast<size_t>(152) * TcShape<ROWS>::kResident * (ROWS * (2 * kDtPart + kAccStride) * sizeof(float) + 2 * sizeof(Split));
+  return static_cast<size_t>(152) * TcShape<ROWS, false>::kResident * (ROWS * (2 * kDtPart + kAccStride) * sizeof(float) + 2 * sizeof(Split));
 }
 
 }  // namespace
@@ -736,7 +753,9 @@ size_t dense_tree_tc_bytes(int rows) {
 cudaError_t launch_dense_tree_tc(const DenseTreeArgs& da, cudaStream_t stream) {
   const int rows = da.a.G * da.a.T;
   if (rows <= 16) return launch<16>(da, stream);
-  if (rows <= 32) return launch<32>(da, stream);
+  // 32 rows: a packed schedule where the other would leave room for one block an SM.  200 sequences of 1024 rows take 136 us
+  // without and 141 with it, 256 244 and 172, 400 378 and 263.
+  if (rows <= 32) return 2 * (TcShape<32, false>::bytes(da.a.B) + 1024) > 228 * 1024 ? launch<32, true>(da, stream) : launch<32>(da, stream);
   if (rows <= 48) return launch<48>(da, stream);
   return launch<64>(da, stream);
 }
