@@ -313,6 +313,7 @@ __global__ void __launch_bounds__(kBThreadsT, 3) bwd_q_kernel(BtcArgs a) {
     }
   };
   auto release_stage = [&](int n) {
+    __threadfence_block();
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty_bar[n % kBSlots]);
   };
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(kBThreadsT, 3) bwd_kv_kernel(BtcArgs a) {
     }
   };
   auto release_stage = [&](int n) {
+    __threadfence_block();
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty_bar[n % kBSlots]);
   };

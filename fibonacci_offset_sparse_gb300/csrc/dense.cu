@@ -252,6 +252,7 @@ __global__ void __launch_bounds__(kDnThreads, 3) dense_fwd_kernel(const __grid_c
         mma16816(O[nd + 1], pa0, pa1, pa2, pa3, b[2], b[3]);
       }
     }
+    __threadfence_block();
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty_bar[slot]);
     if (++slot == kDnSlots) {

@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kTcThreads, MODE == 0 ? FIB_TC_MIN_CTAS : FIB_
     }
   };
   auto release_stage = [&](int n) {
+    __threadfence_block();
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty_bar[n % kSlots]);
   };
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(kTcThreads, MODE == 0 ? FIB_TC_MIN_CTAS : FIB_
       }
       rung_pv(st + SR * kRowBytes, p, O);
     }
+    __threadfence_block();
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty_bar[slot]);
     if (r + 1 < nrt) meta(r + 1);  // uniform

@@ -63,6 +63,9 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
       "l"(src), "r"(bytes), "r"(smem_addr(bar))
       : "memory");
 }
+// Where it releases a slot that the next copy overwrites, a __threadfence_block() by the whole warp stands in front of it (or its
+// address waits for what was read): the slot's last loads could else still be under way, held up in the SM by other blocks'
+// traffic (all of a block's threads that write the status word, say), when the copy lands.
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];\n" ::"r"(smem_addr(bar)) : "memory");
 }
