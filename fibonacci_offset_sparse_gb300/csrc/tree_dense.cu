@@ -3,9 +3,9 @@
 // O_s = sum_j p_sj v_j, p = softmax(q'_s . k'_j / 8).
 //
 // What bounds it: every cached row is read once for all nodes and query heads of its key head, so up to some
-// 64 rows of queries a key the read of the cache from HBM is the floor.  16 sequences x 8 heads x 65536 rows, one
-// query: 168 us, 6.6 TB/s (98% of a measured copy).  float32, 8 x 8 x 65536: 205 us, 5.4 TB/s, what three blocks' rings
-// hold in flight.  A call of one sequence is 9 us of launches, lengths, query, first copies and join.
+// 64 rows of queries a key the read of the cache from HBM is the floor.  16 sequences of 4096, 8192 .. 65536 rows, 8 heads (1.14
+// GB), one query: 175 us, 6.5 TB/s (96% of a measured copy).  float32, 8 sequences of 8192 .. 65536 rows (1.21 GB): 233 us, 5.2
+// TB/s, what three blocks' rings hold in flight.  A call of one sequence is 9 us of launches, lengths, query, first copies and join.
 //
 // Work: a unit is kUnit consecutive cached rows of one task; a task is a (sequence, key head, block of
 // ROWS query rows) and costs its units and kTaskCost more, what a block spends before and after
@@ -26,11 +26,11 @@
 //   float32: mma.sync m16n8k8 on tf32 with both operands split (hi, lo): hi*hi + hi*lo + lo*hi, 21 bits;
 //   16 query rows a tile, whose weights are in place for the second product as the first leaves them.
 // The tensor pipes round each sum toward zero (measured: 3.6e-8 of it a product in the mean, all to one side), so that a chain of
-// products over a whole run would lose 1e-4 of O over 8 x 65536 rows.  Here each unit's products have a sum of their own, the
+// products over a whole run would lose 1e-4 of O over 8 x 8 heads of 65536 rows.  Here each unit's products have a sum of their own, the
 // smaller ones first, and O is added up from those in float32, rounded to nearest.  float32: the query and the weights are split to
-// nearest and a score is two chains of four products, for the same reason: over 8 x 8191 rows O is 4.4e-7 off the 64-bit result
-// (a float32 evaluation 2.3e-7), 9.9e-7 with all operands cut off and one chain, in 236 and 230 us over 8 x 65536 rows.  K and V are
-// cut: to split them to nearest would take 3.7e-7 and, with 32 query rows, 389 us instead of 377.
+// nearest and a score is two chains of four products, for the same reason: over 8191 rows O is 4.4e-7 off the 64-bit result (a
+// float32 evaluation 2.3e-7), 9.9e-7 with all operands cut off and one chain, in 236 and 230 us for the 8 sequences above.  K and V
+// are cut: to split them to nearest would leave 3.7e-7 and take, with 32 query rows, 389 us instead of 377.
 // The drafted keys (at most 64, each seen by its own descendants only) are added by the block that holds a
 // task's last unit, on CUDA cores in float32: a quad a query row, over the row's ancestors
 // alone, so that another branch's values, NaN included, never meet a product.
@@ -42,8 +42,9 @@ namespace fibattn {
 
 namespace {
 
-// bf16: up to so many query rows here, more in tree_dense_tc.cu.  8 rows over 16 x 65536 cached ones take 170 us here and
-// there, over 32 x 1024 17 and 21; one query over 4096 9.8 and 14.3; 16 rows over 16 x 65536 283 here (two tiles of 8) and 173 there.
+// bf16: up to so many query rows here, more in tree_dense_tc.cu.  8 rows over the 16 sequences above take 174 us here and
+// 176 there, over 32 sequences of up to 1024 rows 17 and 23; one query over 4096 9.9 and 15.2; 16 rows over the 16 sequences took 283
+// here (two tiles of 8) where they took 173 there.
 constexpr int kMmaRows = 8;
 constexpr int kSlotBytes = 8192;  // K and V of a unit
 constexpr int kHalf = kSlotBytes / 2;
@@ -527,10 +528,10 @@ struct Core<float> {
 
 // ------------------------------------------------------------------------------ the kernel --
 // Blocks an SM holds, by registers (an SM's four parts hold 512 a lane each: four warps of 128, three of 168) and shared
-// memory.  float32, 8 x 65536 rows: three blocks of 4 groups and 4 slots 205 us, two of 4 groups and 8 slots 286, two of
-// 7 groups and 7 slots 254 (a unit's feeding takes a feeder longer than its computing takes the groups).  With 32 query
-// rows two blocks take 333 us and three 317, but 64 rows, whose drafts leave room for two, 671 and 786; one task of 64 rows
-// on four tiles instead of two tasks 923.
+// memory.  float32, when the 8 sequences above took 205 us: three blocks of 4 groups and 4 slots 205 us, two of 4 groups and 8
+// slots 286, two of 7 groups and 7 slots 254 (a unit's feeding takes a feeder longer than its computing takes the groups).  With 32
+// query rows two blocks took 333 us and three 317, but 64 rows, whose drafts leave room for two, 671 and 786; one task of 64 rows
+// on four tiles instead of two tasks 923.  As it is: 233 us, 376 with 32 rows, 735 with 64.
 template <typename DT, int TILES>
 struct DtSmem {
   using C = Core<DT>;
@@ -546,7 +547,7 @@ struct DtSmem {
   static constexpr int kMax = kAcc + kRows * kAccStride * 4;
   static constexpr int kSum = kMax + (kGroups + 1) * kRows * 4;
   static constexpr int kZero = (kSum + (kGroups + 1) * kRows * 4 + 127) / 128 * 128;
-  static constexpr int kFixed = kZero + 128;  // barriers, flag, positions: statically they would be padded to the base's 1024 bytes
+  static constexpr int kFixed = kZero + 128;  // barriers, flag, positions: statically they are padded to the base's 1024 bytes
   static constexpr int kQuery = kFixed + (2 * 8 * kSlots + 16 + 4 * kRows + 127) / 128 * 128;
   static constexpr int kDraft = kQuery + TILES * C::kQueryBytes;
   static size_t bytes(int B, int T) { return kDraft + static_cast<size_t>(T) * kD * 8 + Schedule<kPacked>::bytes(B); }

@@ -436,7 +436,7 @@ __device__ __forceinline__ void clear_splits(const DenseTreeArgs& da) { da.split
 // that the work is spread however few the tasks are.  16 threads read a row of a partial.  Up to 16 partials: such a team
 // a row, the weights in its lanes.  More: a row at a time, its weights in shared memory, 16 teams that take
 // every 16th partial and meet in order.  One sequence and head, 60000 rows: a call of
-// one query 16 us, 8 queries 19; 39 and 48 where a block in order joined four rows of a task.
+// one query 15 us, 8 queries 18; 39 and 48 where a block in order joined four rows of a task.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinTeams = kJoinThreads / 16;
 constexpr int kMostBlocks = 512;  // of a grid

@@ -2,9 +2,9 @@
 // work, its cut and its join as in tree_dense.cu, the products on the 5th-generation tensor cores.
 //
 // What bounds it: the read of the cache, as there.  With mma.sync the products alone took as long as the
-// read from some 24 query rows on; here the tensor pipes are busy for a fifth of the time.  16 sequences x 8 heads x
-// 65536 rows: 16 query rows 172 us, 24 rows 174 (6.4 TB/s, 94% of a measured copy), 32 rows 175; 48 rows 205 and 64 rows
-// 238, where one block an SM is bound by the steps of its softmax warps.
+// read from some 24 query rows on; here the tensor pipes are busy for a fifth of the time.  16 sequences of 4096, 8192 .. 65536
+// rows, 8 heads (1.14 GB): 16 query rows 177 us (6.4 TB/s, 95% of a measured copy), 24 and 32 rows 182; 48 rows 225 and 64 rows
+// 263, where one block an SM is bound by the steps of its softmax warps.  Every 64 rows read the cache once: 128 take 506, 256 997.
 //
 // Per unit of 128 cached rows, with the keys as the 128 rows of the accumulator:
 //   S^T [128 keys x ROWS] = K Q'^T    K from the ring as TMA left it (K-major, 128-byte swizzle), the rotated
@@ -50,15 +50,16 @@ struct TcFixed {
 
 template <int ROWS, bool PACKED>
 struct TcShape {
-  // Task cost: 256 tasks of 64 rows over 4096 cached ones take 66 us at 12, 77 at 8 and 68 at 16; 16 x 65536 177, 182, 178.
-  // Units a block: one sequence and head of 30000 rows takes 23 us at 3, 39 at 1 and 22 at 6; 8 heads of 4096 17, 21 and 19.
+  // Task cost: 256 tasks of 64 rows over 4096 cached ones take 99 us at 12, 96 at 8 and 100 at 16; the 16 sequences above with 24
+  // query rows 181, 180 and 183.  Units a block: one sequence and head of 30000 rows takes 15.8 us at 3, 17.4 at 1 and 17.0 at 6; 8
+  // heads of 4096 17.1, 16.2 and 18.0.
   static constexpr int kUnit = 128, kRows = ROWS, kTaskCost = 12, kLeast = 3;
   static constexpr int kSlotBytes = kUnit * kD * 2;  // K or V of a unit
   static constexpr int kGroupRows = 16, kGroups = ROWS / kGroupRows;  // query rows of four softmax warps
   static constexpr int kCons = 128 * kGroups, kThreads = kCons + 64;
-  // Two blocks an SM where the rest beside their rings is small: 16 x 65536 rows, 16 query rows 172 us (one block of 9
-  // slots 179), 32 rows 178 (185); 32 x 2048, 16 rows 27 (35).  What is on its way from memory is what the ring holds, so
-  // it takes what shared memory is left: K's slot is free once the scores are formed.
+  // Two blocks an SM where the rest beside their rings is small: when the 16 sequences took 172 us with 16 query rows, one block
+  // of 9 slots took 179; with 32 rows 178 and 185; 32 sequences of up to 2048, 16 rows, 27 and 35.  What is on its way from memory
+  // is what the ring holds, so it takes what shared memory is left: K's slot is free once the scores are formed.
   static constexpr int kResident = ROWS <= 32 ? 2 : 1;
   static constexpr int kSlots = ROWS <= 32 ? 5 : 9;
   static constexpr int kColumns = ROWS == 16 ? 64 : ROWS == 32 ? 128 : 256;  // of tensor memory: S twice, O, the sum of earlier O
@@ -418,7 +419,8 @@ __global__ void __launch_bounds__(TcShape<ROWS, PACKED>::kThreads, TcShape<ROWS,
       __syncwarp();
     };
     // Of a piece, formed anew from shared memory where they are needed: held over the units' loop they would cost it
-    // spills, and what shared memory leaves of L1 does not hold those (16 x 65536 rows, 64 query rows: 297 us with them, 264 without).
+    // spills, and what shared memory leaves of L1 does not hold those (64 query rows over the 16 sequences: 297 us with them, 264
+    // without, at the time).
     auto task_here = [&] { return task_of<P>(a, sch, s_place, s_run[1]); };
     auto drafts_here = [&] {  // the drafted keys' O
       uint32_t block;

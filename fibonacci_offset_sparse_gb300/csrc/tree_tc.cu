@@ -16,8 +16,8 @@
 // row-by-row path, as do trees so deep that the union does not fit even for 8 rows at a time.
 //
 // What bounds it: the latency of a block's steps (lengths and tree; tables; pages; rows; products, weights, products), two
-// blocks an SM by shared memory and registers: 64 sequences of 8 heads and 64 nodes are 512 blocks and take two rounds, 31
-// us for a floor of 4.4 (issue slots 37% busy, tensor pipes 18%).
+// blocks an SM by shared memory and registers: 64 sequences of 8 heads and 64 nodes are 512 blocks and take two rounds, 33.6
+// us for a floor of 4.4 (issue slots 38% busy, tensor pipes 24%); 30.5 with query and drafts in two parts.
 #include <algorithm>
 
 #include "tree.cuh"
@@ -516,9 +516,9 @@ __global__ void __launch_bounds__(kTtThreads, 2) tree_tc_kernel(const __grid_con
 }  // namespace
 
 // A round of 304 blocks takes some 8 us at least, whatever their rows; row by row takes 4.5 us and 2.5 ns a row of the whole
-// batch.  Measured (us here, row by row): 512 blocks of 64 rows 31 and 87, of 16 rows 19 and 26, of 12 rows 19.4 and 20.5, of 8
-// rows 16.5 and 14.2; 256 blocks of 16 rows 10.6 and 14.5; 128 blocks of 32 rows 9.6 and 14.8, of 16 rows 9.0 and 8.6; 64
-// blocks of 64 rows 11.6 and 14.1; 32 blocks of 64 rows 11.5 and 8.4.
+// batch (interpolated; 2.1 where the keys are rows).  Measured on such keys (us here, row by row): 512 blocks of 64 rows 31 and 72, of
+// 16 rows 17.7 and 21.0, of 12 rows 17.5 and 16.2, of 8 rows 16.6 and 11.7; 256 blocks of 16 rows 9.9 and 12.1; 128 blocks of 32 rows
+// 9.0 and 12.1, of 16 rows 8.4 and 7.0; 64 blocks of 64 rows 11.6 and 12.3; 32 blocks of 64 rows 11.4 and 7.1.
 // A chain's union grows with its length: it fits for 12 nodes of the Fibonacci base's distances, more are served row by
 // row.  (Deep trees that are given by their parents are found on the device only; they take 1.3 times the time then.)
 bool tree_tc_serves(const TreeArgs& a) {
