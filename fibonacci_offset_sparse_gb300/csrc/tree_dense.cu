@@ -22,7 +22,7 @@
 //   bf16: mma.sync m16n8k16 with the keys (then the dimensions of V) as the 16 rows of a tile and 8
 //   query rows as its columns, so that a single query pays for 8 rows and not for 16.  K and V enter as
 //   they are stored; the rotated query is split in three bf16 (24 bits of significand: lse is float32; with two, 16 bits,
-//   lse was 1.3e-6 off where it is 3e-7 now) and the softmax weights in two (O is rounded to 8 bits).
+//   lse was 1.3e-6 off where it is 1.6e-7) and the softmax weights in two (O is rounded to 8 bits).
 //   float32: mma.sync m16n8k8 on tf32 with both operands split (hi, lo): hi*hi + hi*lo + lo*hi, 21 bits;
 //   16 query rows a tile, whose weights are in place for the second product as the first leaves them.
 // The tensor pipes round each sum toward zero (measured: 3.6e-8 of it a product in the mean, all to one side), so that a chain of

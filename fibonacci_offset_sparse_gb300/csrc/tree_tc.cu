@@ -10,7 +10,7 @@
 // into a matrix of mostly zeros for O = P V.
 //
 //   mma.sync m16n8k16, keys (then dims) as the 16 rows, 8 query rows as the columns, as in tree_dense.cu; the query
-//   and the drafted keys, rotated here, are split in three bf16 (24 bits: lse is float32; 16 bits left 1.9e-6 in it), the
+//   and the drafted keys, rotated here, are split in three bf16 (24 bits: lse is float32, 1.3e-7 off; 16 bits left 1.9e-6), the
 //   weights in two (O is rounded to 8 bits).
 // A weight 0 times an infinity or NaN is NaN, so rows of which some value is not finite take the block to the
 // row-by-row path, as do trees so deep that the union does not fit even for 8 rows at a time.
