@@ -50,3 +50,27 @@ def fib_attention(plan, layer: int, q, k, v, alpha=None):
     """O of layer ``layer`` for q, k, v [B, H, N, 64] (contiguous CUDA, float32 or bfloat16);
     ``alpha``: device float32 [n_layers] (INTERP: used and differentiated) or None."""
     return _FibAttention.apply(q, k, v, alpha, plan, layer)
+
+
+class _Rotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, pos, start, rope):
+        ctx.rope = rope
+        ctx.save_for_backward(pos, start)
+        return fa.fib_attn_rotary(rope, q, k, pos=pos, start=start)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        pos, start = ctx.saved_tensors
+        # the map is linear, and its transpose the same kernel; gradients come in any strides
+        grads = [g if g.stride(-1) == 1 else g.contiguous() for g, need in zip((dq, dk), ctx.needs_input_grad) if need]
+        out = iter(fa.fib_attn_rotary(ctx.rope, *grads, pos=pos, start=start, transpose=True) if grads else ())
+        return (*(next(out) if need else None for need in ctx.needs_input_grad[:2]), None, None, None)
+
+
+def rotary(rope, q, k=None, pos=None, start=None):
+    """(q, k) rotated by their positions (fib_attn_rotary): q [B, Hq, N, 64], k [B, Hk, N, 64] or None, in any strides, as views
+    of a projection are; pos int32 [B, N], or start int32 [B] + n, or n.  For plans that do not rotate
+    (fib_attn_plan_set_rotation).  A backward that is captured into a graph needs leaves of which no eager graph lives, as
+    any of torch does: x.detach().requires_grad_() is one."""
+    return _Rotary.apply(q, k, pos, start, rope)

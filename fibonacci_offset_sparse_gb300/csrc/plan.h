@@ -15,6 +15,7 @@ struct fib_attn_plan_s {
   std::vector<double> alpha;
   int W = 0, N_max = 0, D = 0, mode = 0;
   double rope_base = 10000.0;
+  bool rotates = true;  // else the tables below hold the identity
   int device = -1;
   float2* d_lo = nullptr;
   float2* d_hi = nullptr;

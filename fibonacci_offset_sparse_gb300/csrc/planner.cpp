@@ -16,6 +16,8 @@
 
 namespace fibattn {
 
+constexpr double kPi = 3.14159265358979323846;
+
 std::vector<int32_t> fibonacci_base(int32_t limit) {
   // 1, 2, 3, 5, ...: the Fibonacci sequence with its repeated leading 1 dropped.
   std::vector<int32_t> out;
@@ -98,6 +100,10 @@ std::vector<Rung> interp_rungs(const int32_t* base, int n_base, double alpha, in
 void rope_tables(int n_max, double rope_base, std::vector<float>* lo, std::vector<float>* hi) {
   double theta[kHalf];
   for (int m = 0; m < kHalf; ++m) theta[m] = std::pow(rope_base, -2.0 * m / kHeadDim);
+  rope_tables(n_max, theta, lo, hi);
+}
+
+void rope_tables(int n_max, const double* theta, std::vector<float>* lo, std::vector<float>* hi) {
   lo->assign(static_cast<size_t>(kRopeSplit) * kHalf * 2, 0.f);
   for (int p = 0; p < kRopeSplit; ++p)
     for (int m = 0; m < kHalf; ++m) {
@@ -114,6 +120,29 @@ void rope_tables(int n_max, double rope_base, std::vector<float>* lo, std::vecto
       (*hi)[(static_cast<size_t>(p) * kHalf + m) * 2 + 0] = static_cast<float>(std::cos(a));
       (*hi)[(static_cast<size_t>(p) * kHalf + m) * 2 + 1] = static_cast<float>(std::sin(a));
     }
+}
+
+bool rope_frequencies(const fib_attn_rope_spec& r, double* theta) {
+  if (r.layout != FIB_ROPE_HALF && r.layout != FIB_ROPE_INTERLEAVED) return false;
+  if (r.rot_dim < 2 || r.rot_dim > kHeadDim || r.rot_dim % 2 != 0) return false;
+  if (!std::isfinite(r.base) || r.base <= 1.0 || !std::isfinite(r.amplitude) || r.amplitude <= 0.0) return false;
+  if (r.scaling < FIB_ROPE_PLAIN || r.scaling > FIB_ROPE_YARN) return false;
+  if (r.scaling != FIB_ROPE_PLAIN && (!std::isfinite(r.factor) || r.factor < 1.0)) return false;
+  if (r.scaling == FIB_ROPE_YARN &&
+      (r.n_train < 1 || !std::isfinite(r.slow) || !std::isfinite(r.fast) || r.slow < 0.0 || r.fast <= r.slow))
+    return false;
+  double base = r.base;
+  if (r.scaling == FIB_ROPE_NTK && r.rot_dim > 2) base *= std::pow(r.factor, static_cast<double>(r.rot_dim) / (r.rot_dim - 2));
+  for (int m = 0; m < r.rot_dim / 2; ++m) {
+    theta[m] = std::pow(base, -2.0 * m / r.rot_dim);
+    if (r.scaling == FIB_ROPE_LINEAR) theta[m] /= r.factor;
+    if (r.scaling == FIB_ROPE_YARN) {
+      const double turns = r.n_train * theta[m] / (2.0 * kPi);
+      const double keep = std::min(1.0, std::max(0.0, (turns - r.slow) / (r.fast - r.slow)));
+      theta[m] *= keep + (1.0 - keep) / r.factor;
+    }
+  }
+  return true;
 }
 
 }  // namespace fibattn

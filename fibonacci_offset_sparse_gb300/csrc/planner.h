@@ -4,6 +4,8 @@
 #include <cstdint>
 #include <vector>
 
+#include "../../include/fib_attn.h"
+
 namespace fibattn {
 
 constexpr int kHeadDim = 64;
@@ -37,5 +39,10 @@ std::vector<Rung> interp_rungs(const int32_t* base, int n_base, double alpha, in
 //   hi[ph * 32 + m] = e^{i ph * kRopeSplit theta_m}, ph <= n_max / kRopeSplit
 // with theta_m = rope_base^(-2m/64), all angles and cos/sin evaluated in binary64.
 void rope_tables(int n_max, double rope_base, std::vector<float>* lo, std::vector<float>* hi);
+// The same for 32 frequencies of the caller's.
+void rope_tables(int n_max, const double* theta, std::vector<float>* lo, std::vector<float>* hi);
+
+// The rot_dim / 2 frequencies of a rotation; false where its description breaks the rules.
+bool rope_frequencies(const fib_attn_rope_spec& r, double* theta);
 
 }  // namespace fibattn

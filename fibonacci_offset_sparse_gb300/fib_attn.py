@@ -8,6 +8,7 @@ no CPU fallback, and a missing or unloadable library raises immediately.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -22,6 +23,8 @@ FIB_BASE_FIBONACCI, FIB_BASE_POW2, FIB_BASE_CUSTOM = 0, 1, 2
 FIB_SCHED_FIXED, FIB_SCHED_LINEAR, FIB_SCHED_COPRIME = 0, 1, 2
 FIB_MODE_MASK, FIB_MODE_INTERP = 0, 1
 FIB_DTYPE_F32, FIB_DTYPE_BF16 = 0, 1
+FIB_ROPE_HALF, FIB_ROPE_INTERLEAVED = 0, 1
+FIB_ROPE_PLAIN, FIB_ROPE_LINEAR, FIB_ROPE_NTK, FIB_ROPE_YARN = 0, 1, 2, 3
 FIB_HEAD_DIM, FIB_MAX_RUNGS, FIB_MAX_WINDOW, FIB_MAX_LAYERS = 64, 32, 64, 256
 FIB_MAX_DRAFTS, FIB_MAX_SEQS, FIB_MAX_HEADS = 64, 1024, 1024
 
@@ -34,7 +37,8 @@ EXPORTS = [
     "fib_attn_bwd_noalloc", "fib_attn_decode", "fib_attn_dense_fwd_workspace_size", "fib_attn_dense_fwd",
     "fib_attn_debug_fill_shared", "fib_attn_bwd_prepared", "fib_attn_cache_workspace_size",
     "fib_attn_cache_commit", "fib_attn_cache_fork", "fib_attn_cache_compact", "fib_attn_tree_decode",
-    "fib_attn_dense_tree_workspace_size", "fib_attn_dense_tree_decode",
+    "fib_attn_dense_tree_workspace_size", "fib_attn_dense_tree_decode", "fib_attn_plan_set_rotation",
+    "fib_attn_rope_frequencies", "fib_attn_rope_create", "fib_attn_rope_destroy", "fib_attn_rotary", "fib_attn_rope_status",
 ]
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
@@ -51,7 +55,15 @@ class CacheStruct(ctypes.Structure):
                 ("lens", _vp), ("refs", _vp), ("state", _vp)]
 
 
+class RopeSpec(ctypes.Structure):
+    """fib_attn_rope_spec of include/fib_attn.h."""
+    _fields_ = [("layout", _i), ("rot_dim", _i), ("scaling", _i), ("n_train", _i), ("base", ctypes.c_double),
+                ("factor", ctypes.c_double), ("slow", ctypes.c_double), ("fast", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
 _cachep = ctypes.POINTER(CacheStruct)
+_ropep = ctypes.POINTER(RopeSpec)
+_strides, _stridesp = ctypes.c_int64 * 3, ctypes.POINTER(ctypes.c_int64)
 
 _SIGS = {
     "fib_attn_error_string": (ctypes.c_char_p, [_i]),
@@ -91,6 +103,13 @@ _SIGS = {
     "fib_attn_dense_tree_workspace_size": (ctypes.c_size_t, [_vp, _cachep, _i, _i, _i]),
     "fib_attn_dense_tree_decode": (_i, [_vp, _i, _cachep, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                         ctypes.c_size_t, _vp]),
+    "fib_attn_plan_set_rotation": (_i, [_vp, _i]),
+    "fib_attn_rope_frequencies": (_i, [_ropep, _f64p]),
+    "fib_attn_rope_create": (_i, [ctypes.POINTER(_vp), _ropep, _i]),
+    "fib_attn_rope_destroy": (_i, [_vp]),
+    "fib_attn_rotary": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _stridesp, _vp, _stridesp, _vp, _stridesp, _vp, _stridesp, _vp,
+                             _vp, _i, _vp]),
+    "fib_attn_rope_status": (_i, [_vp]),
 }
 
 _lib = None
@@ -195,6 +214,11 @@ def fib_attn_plan_create(base_kind: int, alpha, W: int, N_max: int, mode: int,
         ctypes.byref(h), base_kind, _arr(ctypes.c_int32, cb) if cb else None, len(cb),
         _arr(ctypes.c_double, alpha), len(alpha), W, N_max, D, mode, float(rope_base)))
     return Plan(h, len(alpha), W, N_max, mode, torch.cuda.current_device())
+
+
+def fib_attn_plan_set_rotation(plan: Plan, rotate: bool):
+    """Whether the plan's calls rotate queries and keys, or take them as they come (synchronises)."""
+    _check("fib_attn_plan_set_rotation", lib().fib_attn_plan_set_rotation(plan.handle, 1 if rotate else 0))
 
 
 def fib_attn_plan_distances(plan: Plan, layer: int, N: int) -> list[int]:
@@ -323,6 +347,100 @@ def fib_attn_decode(plan: Plan, layer: int, pos: int, q, k_cache, v_cache, o=Non
     return o, lse
 
 
+# ------------------------------------------------------------------------------ rotary positions
+class Rope:
+    """Owns a fib_attn_rope_t (destroyed with the object)."""
+
+    def __init__(self, handle, spec, N_max, device):
+        self.handle, self.spec, self.N_max, self.device = handle, spec, N_max, device
+
+    def close(self):
+        if self.handle:
+            lib().fib_attn_rope_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _rope_spec(rot_dim, layout, base, scaling, factor, n_train, slow, fast, amplitude):
+    if amplitude is None:
+        amplitude = 0.1 * math.log(factor) + 1.0 if scaling == FIB_ROPE_YARN and factor > 0 else 1.0
+    return RopeSpec(layout, rot_dim, scaling, n_train, base, factor, slow, fast, amplitude)
+
+
+def fib_attn_rope_frequencies(rot_dim: int = 64, layout: int = FIB_ROPE_HALF, base: float = 10000.0, scaling: int = FIB_ROPE_PLAIN,
+                              factor: float = 1.0, n_train: int = 1024, slow: float = 1.0, fast: float = 32.0) -> list[float]:
+    """The frequencies of the rot_dim / 2 pairs (host only)."""
+    spec = _rope_spec(rot_dim, layout, base, scaling, factor, n_train, slow, fast, 1.0)
+    out = (ctypes.c_double * 32)()
+    _check("fib_attn_rope_frequencies", lib().fib_attn_rope_frequencies(ctypes.byref(spec), out))
+    return list(out[:rot_dim // 2])
+
+
+def fib_attn_rope_create(N_max: int, rot_dim: int = 64, layout: int = FIB_ROPE_HALF, base: float = 10000.0, scaling: int = FIB_ROPE_PLAIN,
+                         factor: float = 1.0, n_train: int = 1024, slow: float = 1.0, fast: float = 32.0, amplitude=None) -> Rope:
+    """Rotary positions < N_max on the current device.  amplitude None: 0.1 ln(factor) + 1 with FIB_ROPE_YARN, 1 else."""
+    spec = _rope_spec(rot_dim, layout, base, scaling, factor, n_train, slow, fast, amplitude)
+    h = _vp()
+    _check("fib_attn_rope_create", lib().fib_attn_rope_create(ctypes.byref(h), ctypes.byref(spec), N_max))
+    return Rope(h, spec, N_max, torch.cuda.current_device())
+
+
+def fib_attn_rope_status(rope: Rope) -> int:
+    """The status that calls with the handle recorded on the device (synchronises), cleared."""
+    return int(lib().fib_attn_rope_status(rope.handle))
+
+
+def _rotary_tensor(x, name, dtype, index, B, N):
+    if x.dim() != 4 or x.shape[3] != FIB_HEAD_DIM or x.shape[0] != B or x.shape[2] != N or x.dtype is not dtype or \
+            x.get_device() != index or x.stride(3) != 1:
+        raise ValueError(f"{name} must be [B, heads, N, 64] {dtype} on cuda:{index}, its last dim contiguous")
+    return x.data_ptr(), _strides(*x.stride()[:3])
+
+
+def fib_attn_rotary(rope: Rope, q, k=None, pos=None, start=None, transpose: bool = False, q_out=None, k_out=None, stream=None):
+    """q [B, Hq, N, 64] and, where given, k [B, Hk, N, 64] (any strides, the last dim contiguous) rotated by pos int32 [B, N], or
+    start int32 [B] + n, or n; transpose: the transposed map (gradients).  Returns (q_out, k_out), contiguous where they are
+    allocated; an output may be its own input."""
+    if q.dim() != 4:
+        raise ValueError("q must be [B, heads, N, 64]")
+    B, Hq, N, _ = q.shape
+    index, dtype = q.get_device(), q.dtype
+    if dtype not in _DT or index != rope.device:
+        raise ValueError(f"q must be float32 or bfloat16 on cuda:{rope.device}")
+    if k is None and k_out is not None:
+        raise ValueError("k_out without k")
+    if pos is not None and (pos.shape != (B, N) or _bad(pos, torch.int32, index)):
+        raise ValueError(f"pos must be int32 [B, N] on cuda:{index}")
+    if start is not None and (start.shape != (B,) or _bad(start, torch.int32, index)):
+        raise ValueError(f"start must be int32 [B] on cuda:{index}")
+    at, ats = _rotary_tensor(q, "q", dtype, index, B, N)
+    if q_out is None:
+        q_out = _empty_on(q.device, q.shape, dtype, stream)
+    to, tos = _rotary_tensor(q_out, "q_out", dtype, index, B, N)
+    if q_out.shape[1] != Hq:
+        raise ValueError("q_out must have q's heads")
+    Hk, kat, kats, kto, ktos = 0, None, None, None, None
+    if k is not None:
+        Hk = k.shape[1]
+        kat, kats = _rotary_tensor(k, "k", dtype, index, B, N)
+        if k_out is None:
+            k_out = _empty_on(k.device, k.shape, dtype, stream)
+        kto, ktos = _rotary_tensor(k_out, "k_out", dtype, index, B, N)
+        if k_out.shape[1] != Hk:
+            raise ValueError("k_out must have k's heads")
+    code = lib().fib_attn_rotary(rope.handle, _DT[dtype], B, N, Hq, Hk, at, ats, to, tos, kat, kats, kto, ktos,
+                                 None if pos is None else pos.data_ptr(), None if start is None else start.data_ptr(),
+                                 1 if transpose else 0, _raw_stream(stream, index))
+    if code:
+        raise FibAttnError("fib_attn_rotary", code)
+    return q_out, k_out
+
+
 # ------------------------------------------------------------------------ paged cache, tree decode
 class Cache:
     """A paged key/value cache (fib_attn_cache): torch tensors and the struct that describes them.
@@ -399,17 +517,21 @@ def _raw_stream(stream, index: int) -> int:
     return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _empty(cache: Cache, shape, dtype, stream, kept=True):
+def _empty_on(device, shape, dtype, stream, kept=True):
     """A new tensor that a call on `stream` (None: the current one) writes: memory of that stream, which nothing
     enqueued elsewhere still uses; where it is kept, the current stream's as well."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=cache.device)
-    here = torch.cuda.current_stream(cache.device)
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream(device)
     with torch.cuda.stream(stream):
-        t = torch.empty(shape, dtype=dtype, device=cache.device)
+        t = torch.empty(shape, dtype=dtype, device=device)
     if kept:
         t.record_stream(here)
     return t
+
+
+def _empty(cache: Cache, shape, dtype, stream, kept=True):
+    return _empty_on(cache.device, shape, dtype, stream, kept)
 
 
 def _scratch(cache: Cache, workspace, need, stream):

@@ -69,6 +69,9 @@ enum fib_schedule_kind { FIB_SCHED_FIXED = 0, FIB_SCHED_LINEAR = 1, FIB_SCHED_CO
 enum fib_mode { FIB_MODE_MASK = 0, FIB_MODE_INTERP = 1 };
 enum fib_dtype { FIB_DTYPE_F32 = 0, FIB_DTYPE_BF16 = 1 };
 
+enum fib_rope_layout { FIB_ROPE_HALF = 0, FIB_ROPE_INTERLEAVED = 1 };
+enum fib_rope_scaling { FIB_ROPE_PLAIN = 0, FIB_ROPE_LINEAR = 1, FIB_ROPE_NTK = 2, FIB_ROPE_YARN = 3 };
+
 #define FIB_HEAD_DIM 64   /* the only head dimension built */
 #define FIB_MAX_RUNGS 32  /* rungs per layer, after dedup */
 #define FIB_MAX_WINDOW 64 /* largest window W */
@@ -126,6 +129,16 @@ int fib_attn_interp_rungs(const int32_t* base, int n_base, double alpha, int W, 
 int fib_attn_plan_create(fib_attn_plan_t* out, int base_kind, const int32_t* custom_base,
                          int n_custom, const double* alpha, int n_layers, int W, int N_max,
                          int D, int mode, double rope_base);
+
+/* Whether the plan's calls rotate queries and keys (rotate != 0, as after creation) or take
+ * them as they come (0): rotated by the caller (fib_attn_rotary: other layouts, part of the
+ * head, scaled frequencies, positions of the caller's own) or not at all.  Then a cached row is K as given,
+ * and "rotated at its own position" means nothing in every call of this plan.  A query or key
+ * that is infinite or NaN makes both dims of its pair (m, m + 32) NaN all the same.
+ * Synchronises the device, then writes the plan's tables: not during a stream capture, and a
+ * captured call follows the setting of its replay.  Errors: FIB_ERR_INVALID_ARG (null plan, another device
+ * current), FIB_ERR_NOMEM, FIB_ERR_CUDA.                                                */
+int fib_attn_plan_set_rotation(fib_attn_plan_t p, int rotate);
 
 /* Frees the plan and its device tables (synchronises the device first).  NULL is OK.
  * No counterpart in the paper.                                                        */
@@ -215,6 +228,72 @@ int fib_attn_dense_fwd(fib_attn_plan_t p, int B, int H, int N, int dtype, const 
 int fib_attn_decode(fib_attn_plan_t p, int layer, int B, int H, int N, int pos, int dtype,
                     const void* q, const void* k_cache, const void* v_cache, void* o, float* lse,
                     const float* alpha_dev, void* stream);
+
+/* -------------------------------------------------------------- rotary positions ----
+ * The rotation by itself, for what the plans' own ("Implementation": RoPE before the gather; the
+ * pages use "vanilla RoPE, no scaling") does not cover: other layouts, part of the head,
+ * frequencies scaled for long contexts, positions that are not row numbers (packed documents,
+ * a cache whose rows lost neighbours).  Its results go to calls of a plan that does not rotate
+ * (fib_attn_plan_set_rotation).
+ *
+ * The first rot_dim dims of a head are rotate pairs: HALF (m, m + rot_dim/2), INTERLEAVED
+ * (2m, 2m + 1), m < rot_dim/2; the others are copied.  The pair (a, b) at position p becomes
+ * amplitude * (a cos - b sin, a sin + b cos) of the angle p * theta_m, with
+ *   PLAIN   theta_m = base^(-2m/rot_dim);
+ *   LINEAR  that divided by factor;
+ *   NTK     (base * factor^(rot_dim/(rot_dim-2)))^(-2m/rot_dim) (rot_dim 2: as PLAIN);
+ *   YARN    theta_m (g + (1-g)/factor), g = clamp((n_train theta_m / 2pi - slow) / (fast - slow),
+ *           0, 1) of PLAIN's theta_m: pairs of few turns in n_train positions are stretched,
+ *           those of many kept.  (An amplitude of 0.1 ln(factor) + 1 goes with it.)
+ * Rules: rot_dim even, 2 .. 64; base > 1; amplitude > 0; factor >= 1 (but PLAIN); n_train >= 1,
+ * 0 <= slow < fast (YARN); all finite.                                                  */
+typedef struct fib_attn_rope_spec_s {
+  int layout;
+  int rot_dim;
+  int scaling;
+  int n_train;
+  double base;
+  double factor;
+  double slow;
+  double fast;
+  double amplitude;
+} fib_attn_rope_spec;
+typedef struct fib_attn_rope_s* fib_attn_rope_t;
+
+/* theta_out: the rot_dim/2 frequencies.  Host only.  FIB_ERR_INVALID_ARG on a null pointer
+ * or a spec that breaks the rules.                                                      */
+int fib_attn_rope_frequencies(const fib_attn_rope_spec* spec, double* theta_out);
+
+/* Tables for positions < N_max (1 <= N_max <= 1<<20), built in binary64 and stored as float32
+ * on the current device, which must be current in every call with the handle.  Errors:
+ * FIB_ERR_INVALID_ARG, FIB_ERR_NOMEM, FIB_ERR_CUDA.                                     */
+int fib_attn_rope_create(fib_attn_rope_t* out, const fib_attn_rope_spec* spec, int N_max);
+
+/* Frees it (synchronises the device first).  NULL is OK.                                */
+int fib_attn_rope_destroy(fib_attn_rope_t r);
+
+/* q_out = q and k_out = k rotated by their positions, in one launch.  q: [B, Hq, N, 64], k:
+ * [B, Hk, N, 64], any strides: q_strides = {b, h, n}, in elements, the last dim contiguous (so a
+ * fused projection's view and [B, N, H, 64] are read in place; strides of inputs may be 0), outputs the same with rows
+ * that do not overlap.  Hk = 0: no keys (the k arguments are ignored).  Position of row n of
+ * sequence b: pos[b][n] (int32 [B, N] contiguous), else start[b] + n (int32 [B]; a cache's lens,
+ * say), else n; at most one of them is given.  transpose != 0: the transposed map (angles
+ * negated, the same amplitude), which takes the outputs' gradient to the inputs'.
+ * q_out may be q itself with the same strides (k_out k), and else must not overlap what the
+ * call reads.  Values are rotated in float32 and rounded once.  A position outside [0, N_max)
+ * records FIB_ERR_DEVICE_ASSERT in the handle's status word and leaves its rows unwritten.
+ * 1 <= B, N; B * N < 2^31; 1 <= Hq <= FIB_MAX_HEADS; 0 <= Hk <= FIB_MAX_HEADS.  Pointers and
+ * strides aligned to 16 bytes, and HALF with rot_dim a multiple of 16, take the wide path;
+ * else elements are moved one by one (pointers aligned to the type).  Errors: FIB_ERR_INVALID_ARG,
+ * FIB_ERR_CUDA.                                                                         */
+int fib_attn_rotary(fib_attn_rope_t r, int dtype, int B, int N, int Hq, int Hk, const void* q,
+                    const int64_t* q_strides, void* q_out, const int64_t* q_out_strides,
+                    const void* k, const int64_t* k_strides, void* k_out,
+                    const int64_t* k_out_strides, const int32_t* pos, const int32_t* start,
+                    int transpose, void* stream);
+
+/* Synchronises the device, then returns and clears the handle's status word.            */
+int fib_attn_rope_status(fib_attn_rope_t r);
 
 /* ----------------------------------------------------------------- paged cache ----
  * A key/value cache that sequences share, grow and give back, and decode over it for one new
