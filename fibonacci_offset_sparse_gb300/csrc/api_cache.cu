@@ -138,6 +138,27 @@ int fib_attn_cache_compact(const fib_attn_cache* c, int32_t* remap, void* worksp
   return cuda_status(launch_cache_compact(*c, remap, workspace, static_cast<cudaStream_t>(stream)));
 }
 
+size_t fib_attn_cache_evict_workspace_size(const fib_attn_cache* c, int rows) {
+  if (check_cache(c) != FIB_OK || rows < 1 || rows > (1 << 30)) return 0;
+  return cache_evict_workspace_bytes(*c, rows);
+}
+
+int fib_attn_cache_evict(fib_attn_plan_t p, const fib_attn_cache* c, int B, int rows, const int32_t* keep, int sink, int recent,
+                         float* weights, int32_t* dropped, void* workspace, size_t ws_bytes, void* stream) {
+  int st = check_cache(c);
+  if (st != FIB_OK) return st;
+  if (p == nullptr || B < 1 || B > c->max_seqs || rows < 1 || rows > (1 << 30)) return FIB_ERR_INVALID_ARG;
+  if (sink < 0 || recent < 0 || sink > (1 << 29) || recent > (1 << 29)) return FIB_ERR_INVALID_ARG;
+  if (check_ints(keep) || weights == nullptr || !aligned(weights, 4) || !aligned(dropped, 4)) return FIB_ERR_INVALID_ARG;
+  if (dropped != nullptr && (dropped == keep || dropped == c->lens || dropped == c->table || dropped == c->refs)) return FIB_ERR_INVALID_ARG;
+  if (check_workspace(workspace, ws_bytes, cache_evict_workspace_bytes(*c, rows)) || workspace == weights) return FIB_ERR_INVALID_ARG;
+  st = check_device(p);
+  if (st == FIB_OK) st = check_cache_device(c);
+  if (st != FIB_OK) return st;
+  return cuda_status(launch_cache_evict(*c, B, rows, keep, sink, recent, p->N_max, weights, dropped, p->d_lo, p->d_hi, p->rotates,
+                                        workspace, static_cast<cudaStream_t>(stream)));
+}
+
 int fib_attn_tree_decode(fib_attn_plan_t p, int layer, const fib_attn_cache* c, int B, int Hq, int T, int N,
                          const void* q, const void* k_new, const void* v_new, const int32_t* parent,
                          const int32_t* n_nodes, void* o, float* lse, const float* alpha_dev, void* stream) {

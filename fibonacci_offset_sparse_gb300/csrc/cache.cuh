@@ -20,6 +20,11 @@ cudaError_t launch_cache_commit(const fib_attn_cache& c, int B, int T, int n_max
 cudaError_t launch_cache_fork(const fib_attn_cache& c, const int32_t* src, void* ws, cudaStream_t stream);
 cudaError_t launch_cache_compact(const fib_attn_cache& c, int32_t* remap, void* ws, cudaStream_t stream);
 
+size_t cache_evict_workspace_bytes(const fib_attn_cache& c, int rows);
+cudaError_t launch_cache_evict(const fib_attn_cache& c, int B, int rows, const int32_t* keep, int sink, int recent, int n_max,
+                               float* weights, int32_t* dropped, const float2* lo_tab, const float2* hi_tab, bool turns, void* ws,
+                               cudaStream_t stream);
+
 // What the decodes share.  kc, vc: the layer's pools.
 struct TreeArgs {
   LayerTable t;  // sparse only

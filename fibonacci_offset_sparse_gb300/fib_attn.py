@@ -8,6 +8,7 @@ no CPU fallback, and a missing or unloadable library raises immediately.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
@@ -39,6 +40,7 @@ EXPORTS = [
     "fib_attn_cache_commit", "fib_attn_cache_fork", "fib_attn_cache_compact", "fib_attn_tree_decode",
     "fib_attn_dense_tree_workspace_size", "fib_attn_dense_tree_decode", "fib_attn_plan_set_rotation",
     "fib_attn_rope_frequencies", "fib_attn_rope_create", "fib_attn_rope_destroy", "fib_attn_rotary", "fib_attn_rope_status",
+    "fib_attn_cache_evict_workspace_size", "fib_attn_cache_evict",
 ]
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
@@ -63,7 +65,7 @@ class RopeSpec(ctypes.Structure):
 
 _cachep = ctypes.POINTER(CacheStruct)
 _ropep = ctypes.POINTER(RopeSpec)
-_strides, _stridesp = ctypes.c_int64 * 3, ctypes.POINTER(ctypes.c_int64)
+_i64p = ctypes.POINTER(ctypes.c_int64)
 
 _SIGS = {
     "fib_attn_error_string": (ctypes.c_char_p, [_i]),
@@ -107,9 +109,11 @@ _SIGS = {
     "fib_attn_rope_frequencies": (_i, [_ropep, _f64p]),
     "fib_attn_rope_create": (_i, [ctypes.POINTER(_vp), _ropep, _i]),
     "fib_attn_rope_destroy": (_i, [_vp]),
-    "fib_attn_rotary": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _stridesp, _vp, _stridesp, _vp, _stridesp, _vp, _stridesp, _vp,
+    "fib_attn_rotary": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _i64p, _vp, _i64p, _vp, _i64p, _vp, _i64p, _vp,
                              _vp, _i, _vp]),
     "fib_attn_rope_status": (_i, [_vp]),
+    "fib_attn_cache_evict_workspace_size": (ctypes.c_size_t, [_cachep, _i]),
+    "fib_attn_cache_evict": (_i, [_vp, _cachep, _i, _i, _vp, _i, _i, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
 }
 
 _lib = None
@@ -395,47 +399,50 @@ def fib_attn_rope_status(rope: Rope) -> int:
     return int(lib().fib_attn_rope_status(rope.handle))
 
 
-def _rotary_tensor(x, name, dtype, index, B, N):
-    if x.dim() != 4 or x.shape[3] != FIB_HEAD_DIM or x.shape[0] != B or x.shape[2] != N or x.dtype is not dtype or \
-            x.get_device() != index or x.stride(3) != 1:
+@functools.lru_cache(maxsize=256)
+def _stride_array(strides):
+    return (ctypes.c_int64 * 3)(*strides[:3])
+
+
+def _rotary_tensor(x, name, dtype, index, shape):
+    """(heads, address, strides) of [B, heads, N, 64] with shape's B and N."""
+    own, strides = x.shape, x.stride()
+    if len(own) != 4 or own[0] != shape[0] or own[2] != shape[2] or own[3] != FIB_HEAD_DIM or strides[3] != 1 or x.dtype is not dtype or \
+            x.get_device() != index:
         raise ValueError(f"{name} must be [B, heads, N, 64] {dtype} on cuda:{index}, its last dim contiguous")
-    return x.data_ptr(), _strides(*x.stride()[:3])
+    return own[1], x.data_ptr(), _stride_array(strides)
 
 
 def fib_attn_rotary(rope: Rope, q, k=None, pos=None, start=None, transpose: bool = False, q_out=None, k_out=None, stream=None):
     """q [B, Hq, N, 64] and, where given, k [B, Hk, N, 64] (any strides, the last dim contiguous) rotated by pos int32 [B, N], or
     start int32 [B] + n, or n; transpose: the transposed map (gradients).  Returns (q_out, k_out), contiguous where they are
     allocated; an output may be its own input."""
-    if q.dim() != 4:
-        raise ValueError("q must be [B, heads, N, 64]")
-    B, Hq, N, _ = q.shape
-    index, dtype = q.get_device(), q.dtype
-    if dtype not in _DT or index != rope.device:
-        raise ValueError(f"q must be float32 or bfloat16 on cuda:{rope.device}")
-    if k is None and k_out is not None:
-        raise ValueError("k_out without k")
-    if pos is not None and (pos.shape != (B, N) or _bad(pos, torch.int32, index)):
+    shape, dtype, index = q.shape, q.dtype, rope.device
+    if len(shape) != 4 or dtype not in _DT:
+        raise ValueError("q must be [B, heads, N, 64], float32 or bfloat16")
+    Hq, at, ats = _rotary_tensor(q, "q", dtype, index, shape)
+    if pos is not None and (pos.shape != (shape[0], shape[2]) or _bad(pos, torch.int32, index)):
         raise ValueError(f"pos must be int32 [B, N] on cuda:{index}")
-    if start is not None and (start.shape != (B,) or _bad(start, torch.int32, index)):
+    if start is not None and (start.shape != (shape[0],) or _bad(start, torch.int32, index)):
         raise ValueError(f"start must be int32 [B] on cuda:{index}")
-    at, ats = _rotary_tensor(q, "q", dtype, index, B, N)
     if q_out is None:
-        q_out = _empty_on(q.device, q.shape, dtype, stream)
-    to, tos = _rotary_tensor(q_out, "q_out", dtype, index, B, N)
-    if q_out.shape[1] != Hq:
+        q_out = _empty_on(q.device, shape, dtype, stream)
+    heads, to, tos = _rotary_tensor(q_out, "q_out", dtype, index, shape)
+    if heads != Hq:
         raise ValueError("q_out must have q's heads")
     Hk, kat, kats, kto, ktos = 0, None, None, None, None
     if k is not None:
-        Hk = k.shape[1]
-        kat, kats = _rotary_tensor(k, "k", dtype, index, B, N)
+        Hk, kat, kats = _rotary_tensor(k, "k", dtype, index, shape)
         if k_out is None:
             k_out = _empty_on(k.device, k.shape, dtype, stream)
-        kto, ktos = _rotary_tensor(k_out, "k_out", dtype, index, B, N)
-        if k_out.shape[1] != Hk:
+        heads, kto, ktos = _rotary_tensor(k_out, "k_out", dtype, index, shape)
+        if heads != Hk:
             raise ValueError("k_out must have k's heads")
-    code = lib().fib_attn_rotary(rope.handle, _DT[dtype], B, N, Hq, Hk, at, ats, to, tos, kat, kats, kto, ktos,
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    code = lib().fib_attn_rotary(rope.handle, _DT[dtype], shape[0], shape[2], Hq, Hk, at, ats, to, tos, kat, kats, kto, ktos,
                                  None if pos is None else pos.data_ptr(), None if start is None else start.data_ptr(),
-                                 1 if transpose else 0, _raw_stream(stream, index))
+                                 transpose, _raw_stream(stream, index))
     if code:
         raise FibAttnError("fib_attn_rotary", code)
     return q_out, k_out
@@ -586,6 +593,32 @@ def fib_attn_cache_compact(cache: Cache, remap=None, workspace=None, stream=None
     if code:
         raise FibAttnError("fib_attn_cache_compact", code)
     return remap
+
+
+def _weights_rows(cache: Cache, weights) -> int:
+    shape = weights.shape
+    if len(shape) != 4 or shape[:3] != (cache.n_layers, cache.max_seqs, cache.heads) or _bad(weights, torch.float32, cache.index):
+        raise ValueError(f"weights must be float32 [n_layers, max_seqs, heads, rows] on {cache.device}")
+    return shape[3]
+
+
+def fib_attn_cache_evict_workspace_size(cache: Cache, rows: int) -> int:
+    return int(lib().fib_attn_cache_evict_workspace_size(cache.pointer, rows))
+
+
+def fib_attn_cache_evict(plan: Plan, cache: Cache, weights, keep, sink: int, recent: int, dropped=None, workspace=None, stream=None):
+    """Sequence b with more than keep[b] rows (int32 [B]) is left with its first `sink`, its last `recent` and the heaviest between,
+    by weights float32 [n_layers, max_seqs, heads, rows]; dropped int32 [B] gains what went."""
+    rows, index = _weights_rows(cache, weights), cache.index
+    if len(keep.shape) != 1 or _bad(keep, torch.int32, index):
+        raise ValueError(f"keep must be int32 [B] on {cache.device}")
+    if dropped is not None and (dropped.shape != keep.shape or _bad(dropped, torch.int32, index)):
+        raise ValueError(f"dropped must be int32 [B] on {cache.device}")
+    at, size, workspace = _scratch(cache, workspace, lambda: fib_attn_cache_evict_workspace_size(cache, rows), stream)
+    code = lib().fib_attn_cache_evict(plan.handle, cache.pointer, keep.shape[0], rows, keep.data_ptr(), sink, recent, weights.data_ptr(),
+                                      None if dropped is None else dropped.data_ptr(), at, size, _raw_stream(stream, index))
+    if code:
+        raise FibAttnError("fib_attn_cache_evict", code)
 
 
 def _tree_tensors(cache: Cache, q, k_new, v_new, parent, n_nodes, o, lse, want_lse, stream):

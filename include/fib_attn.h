@@ -316,7 +316,7 @@ int fib_attn_rope_status(fib_attn_rope_t r);
  * Alignment: k, v, refs and state 16 bytes, table and lens 4.  Limits: page_rows one of 16,
  * 32, 64, 128, 256; n_layers <= FIB_MAX_LAYERS; heads <= FIB_MAX_HEADS; max_seqs <= FIB_MAX_SEQS; max_pages * page_rows <= 2^30;
  * n_pages * heads * page_rows < 2^31.
- * Calls that change a cache (commit, fork, compact) are ordered by the caller with one another
+ * Calls that change a cache (commit, fork, compact, evict) are ordered by the caller with one another
  * and with the decodes that read it (the same stream, or events); so are calls that share a
  * workspace, in captured graphs too.                                                    */
 typedef struct fib_attn_cache_s {
@@ -379,6 +379,32 @@ int fib_attn_cache_fork(const fib_attn_cache* c, const int32_t* src, void* works
  * pages that the caller holds itself).  Errors as commit.                                 */
 int fib_attn_cache_compact(const fib_attn_cache* c, int32_t* remap, void* workspace,
                            size_t ws_bytes, void* stream);
+
+/* Eviction by accumulated attention weight: a cache in bounded memory, as a control to the
+ * static sparse pattern (the paper has no counterpart).  Sequence b < B with more than keep[b] rows is left
+ * with keep[b], for every layer and key head by itself: its first `sink`, its last `recent` and,
+ * of those between, the keep[b] - sink - recent of the largest weights[layer][b][head][row]
+ * (of equal ones the first; a NaN is below every number).  They move down in order, their
+ * weights with them; K is turned from the old row to the new one (by a plan that rotates, so that a
+ * row still holds K rotated at its own position; rounded once to the cache's type), or moved as it is
+ * (by one that does not: positions are then the caller's, lens[b] + dropped[b] that of the next token).
+ * weights: float32 [n_layers, max_seqs, heads, rows] on the device (fib_attn_cache_weigh adds
+ * them up); entries behind keep[b] stay as they were.  keep: int32 [B]; dropped: int32 [B] or
+ * NULL, gains the number of rows that went; both on the device.
+ * Pages: in the order of b, then of rows, a page behind the sink that is shared (refs > 1) and still
+ * needed is replaced by a free one, free ones in ascending order; pages behind the new last row
+ * are let go of (their table entries become -1).  Pages that lie in the sink stay shared.  Rows behind a
+ * sequence's last one are left as they were.
+ * All or nothing: state[1] becomes FIB_ERR_NO_PAGES where too few pages are free, or
+ * FIB_ERR_DEVICE_ASSERT for keep[b] < 0, a length outside the table, a page id outside the pool or, of a
+ * sequence that would shrink, sink + recent > keep[b] or more rows than `rows` or the plan's
+ * N_max, and the call then changes nothing else.  It changes the cache, as a commit does.
+ * workspace: fib_attn_cache_evict_workspace_size(c, rows) bytes, 256-byte aligned, contents on
+ * entry ignored.  Errors as commit.                                                     */
+size_t fib_attn_cache_evict_workspace_size(const fib_attn_cache* c, int rows);
+int fib_attn_cache_evict(fib_attn_plan_t p, const fib_attn_cache* c, int B, int rows,
+                         const int32_t* keep, int sink, int recent, float* weights,
+                         int32_t* dropped, void* workspace, size_t ws_bytes, void* stream);
 
 /* Sparse decode of a tree of drafted tokens ("Attended set", "Scaling", "Implementation", as
  * fib_attn_decode).  Sequence b < B has lens[b] rows in the cache and n_nodes[b] <= T

@@ -95,6 +95,42 @@ class PagedCache:
                 row[j] = remap[row[j]]
         return remap, n
 
+    def evict(self, weights, keep, sink: int, recent: int, dropped, turns: bool = True) -> bool:
+        """Keeps of each longer sequence the first rows, the last and the heaviest between; weights [layers, seqs, heads, rows] and
+        dropped are changed in place.  False (and nothing done) where the pages do not suffice."""
+        P, long = self.P, [b for b in range(len(keep)) if self.lens[b] > keep[b]]
+        held = list(self.refs)
+        written = {b: [j for j in range(sink // P, self.pages(keep[b])) if held[self.table[b][j]] > 1] for b in long}
+        free = [p for p, c in enumerate(self.refs) if c == 0]
+        if sum(len(w) for w in written.values()) > len(free):
+            return False
+        k0, v0, w0 = self.k.copy(), self.v.copy(), weights.copy()
+        for b in long:
+            n, m, old = self.lens[b], keep[b], list(self.table[b])
+            for j in written[b]:
+                self.table[b][j] = free.pop(0)
+                self.refs[self.table[b][j]] = 1
+                self.refs[old[j]] -= 1
+            for j in range(self.pages(m), self.pages(n)):
+                self.refs[old[j]] -= 1
+                self.table[b][j] = -1
+            for layer in range(self.k.shape[0]):
+                for h in range(self.k.shape[2]):
+                    w = w0[layer, b, h].astype(np.float64)
+                    mid = sorted(range(sink, n - recent), key=lambda r: (math.isnan(w[r]), 0.0 if math.isnan(w[r]) else -w[r], r))
+                    stays = sorted([*range(sink), *mid[:m - sink - recent], *range(n - recent, n)])
+                    for j, r in enumerate(stays):
+                        weights[layer, b, h, j] = w0[layer, b, h, r]
+                        if j // P < sink // P:
+                            continue
+                        at, was = self.table[b][j // P], old[r // P]
+                        x = k0[layer, was, h, r % P]
+                        self.k[layer, at, h, j % P] = turn(x, j - r) if turns and j != r else x
+                        self.v[layer, at, h, j % P] = v0[layer, was, h, r % P]
+            self.lens[b] = m
+            dropped[b] += n - m
+        return True
+
     def rows(self, layer: int, b: int):
         """K and V of sequence b as [len, heads, D]."""
         p = np.arange(self.lens[b])

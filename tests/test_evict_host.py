@@ -1,0 +1,46 @@
+"""Eviction and weighing, what needs no GPU: argument checks, and the oracle's eviction on a case written out."""
+import ctypes
+
+import numpy as np
+import pytest
+
+from fibonacci_offset_sparse_gb300 import fib_attn as fa
+from oracle import cache_oracle as co
+from tests.test_cache_host import BAD, lib, struct  # noqa: F401
+
+
+@pytest.mark.parametrize("kw", BAD, ids=[str(x) for x in BAD])
+def test_struct_rules(lib, kw):  # noqa: F811
+    p = ctypes.byref(struct(**kw))
+    assert lib.fib_attn_cache_evict_workspace_size(p, 100) == 0
+    assert lib.fib_attn_cache_evict(1 << 12, p, 1, 100, 16, 0, 0, 32, None, 256, 1 << 40, None) == fa.FIB_ERR_INVALID_ARG
+
+
+def test_evict_arguments(lib):  # noqa: F811
+    s = struct()
+    p = ctypes.byref(s)
+    need = lib.fib_attn_cache_evict_workspace_size(p, 100)
+    assert need > 0 and lib.fib_attn_cache_evict_workspace_size(p, 0) == 0 and lib.fib_attn_cache_evict_workspace_size(None, 1) == 0
+    assert lib.fib_attn_cache_evict(None, p, 1, 100, 16, 0, 0, 32, None, 256, need, None) == fa.FIB_ERR_INVALID_ARG
+    plan = 1 << 12  # never looked into: each call is refused for another argument
+    good = dict(B=1, rows=100, keep=16, sink=0, recent=0, weights=32, dropped=None, ws=256, size=need)
+    for kw in (dict(B=0), dict(B=4), dict(rows=0), dict(rows=(1 << 30) + 1), dict(keep=None), dict(keep=18), dict(sink=-1), dict(recent=-1),
+               dict(recent=(1 << 29) + 1), dict(weights=None), dict(weights=34), dict(dropped=17), dict(dropped=16), dict(dropped=s.lens),
+               dict(dropped=s.refs), dict(ws=None), dict(ws=272), dict(size=need - 1), dict(weights=256)):
+        x = {**good, **kw}
+        assert lib.fib_attn_cache_evict(plan, p, x["B"], x["rows"], x["keep"], x["sink"], x["recent"], x["weights"], x["dropped"], x["ws"],
+                                        x["size"], None) == fa.FIB_ERR_INVALID_ARG, kw
+
+
+def test_oracle_evicts_as_written():
+    """Two sequences of two pages of 4 rows that share the first page; one layer, one head of two dims."""
+    k = np.arange(5 * 4 * 2, dtype=np.float64).reshape(1, 5, 1, 4, 2)
+    c = co.PagedCache(k.copy(), k.copy() + 100, [[0, 1], [0, 2]], [7, 6], [2, 1, 1, 0, 0])
+    w = np.array([[[[9, 1, 5, 5, 2, 7, 0, 3]], [[0, 0, 0, 0, 0, 0, 0, 0]]]], np.float32)
+    dropped = [0, 0]
+    assert c.evict(w, [4, 6], 1, 1, dropped, turns=False)
+    # rows 0 (first), 6 (last), 5 (weight 7) and 2 (5, the first of two) stay, in the first free page, as the old one is shared
+    assert c.table == [[3, -1], [0, 2]] and c.lens == [4, 6] and c.refs == [1, 0, 1, 1, 0] and dropped == [3, 0]
+    assert np.array_equal(c.k[0, 3, 0], [k[0, 0, 0, 0], k[0, 0, 0, 2], k[0, 1, 0, 1], k[0, 1, 0, 2]])
+    assert np.array_equal(c.v[0, 3, 0], c.k[0, 3, 0] + 100)
+    assert w[0, 0, 0].tolist() == [9, 5, 7, 0, 2, 7, 0, 3]

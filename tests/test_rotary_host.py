@@ -74,7 +74,7 @@ def test_create_and_null_arguments(lib):
     for a in (0.0, -1.0, math.nan, math.inf):
         assert lib.fib_attn_rope_create(ctypes.byref(h), ctypes.byref(fa.RopeSpec(0, 64, 0, 0, 10000.0, 1.0, 0.0, 0.0, a)), 16) == fa.FIB_ERR_INVALID_ARG
     assert not h.value
-    s = fa._strides(64, 64, 64)
+    s = (ctypes.c_int64 * 3)(64, 64, 64)
     assert lib.fib_attn_rotary(None, 0, 1, 1, 1, 0, 64, s, 1 << 20, s, None, None, None, None, None, None, 0, None) == fa.FIB_ERR_INVALID_ARG
     assert lib.fib_attn_rope_status(None) == fa.FIB_ERR_INVALID_ARG
     assert lib.fib_attn_rope_destroy(None) == fa.FIB_OK
