@@ -1,0 +1,392 @@
+// The attention weight that new tokens give to each row of the paged cache, added up (sm_103a):
+//   weights[r] = (r < first ? weights[r] : 0) + sum over query rows m with r <= p_m of exp(q'_m . K_r / 8 - lse_m).
+// A row's sum needs no other row once lse is known, so a row belongs to one warp (or one thread, weigh_tc.cu): no partials, no atomics,
+// one order of sums.  Two launches: the queries rotated, scaled and split once; then one pass over K.
+//
+// What bounds it: the read of K.  Here, for up to 8 query rows a key head (and float32 of any number): keys as the 16 rows of
+// mma.sync's tile, queries as its 8 columns, a warp 64 (float32: 32) rows at a time, 8 KB of loads on their way a warp straight to its
+// registers, in which a lane's 16-byte words are the tile's fragments (the order of the dims is the same for both).
+// Precision: scores are float32.  The query is split in three bf16 (24 bits; cached bf16 rows enter as stored), float32 query and
+// rows each in two tf32 to nearest (22 bits); the small parts are added up first, as the pipes round toward zero.
+#include "weigh.cuh"
+
+namespace fibattn {
+
+namespace {
+
+// ------------------------------------------------------------------------------------- queries --
+constexpr int kPrepThreads = 128;
+
+__device__ __forceinline__ float tf32_of(float x) {
+  uint32_t y;
+  asm("cvt.rna.tf32.f32 %0, %1;\n" : "=r"(y) : "f"(x));
+  return __uint_as_float(y);
+}
+
+// A quad a query row (of mpad, those behind the last one as 0): block (layer and sequence, 32 rows, head).
+template <typename DT>
+__global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_constant__ WeighArgs a) {
+  let_second_start();
+  const int t = threadIdx.x & 3, l = blockIdx.x / a.B, b = blockIdx.x % a.B;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.next = 0;
+  bool ok;
+  const WeighSeq s = weigh_seq(a, b, &ok);
+  if (!ok && threadIdx.x == 0) atomicExch(a.status, kStatusDeviceAssert);
+  if (s.n == 0) return;
+  const int used = s.n * a.G;
+  for (int h = blockIdx.z; h < a.c.H; h += gridDim.z) {
+    const size_t task = (static_cast<size_t>(l) * a.B + b) * a.c.H + h;
+    for (int m = blockIdx.y * (kPrepThreads / 4) + (threadIdx.x >> 2); m < a.mpad; m += gridDim.y * (kPrepThreads / 4)) {
+      if (m >= (used + 63) / 64 * 64) break;  // (no tile reaches behind these)
+      const int i = m / a.G, g = m - i * a.G;
+      int node = i;
+      bool live = m < used;
+      if (live && a.path != nullptr) {
+        node = a.path[static_cast<size_t>(b) * a.T + i];
+        if (node < 0 || node >= a.T) {
+          live = false;
+          atomicExch(a.status, kStatusDeviceAssert);
+        }
+      }
+      float x[16];
+      float ref = INFINITY;
+      if (live) {
+        const size_t row = ((static_cast<size_t>(l) * a.B + b) * a.Hq + h * a.G + g) * a.T + node;
+        float2 e[8];
+        load_part(static_cast<const DT*>(a.q) + row * kD, t, x);
+        rope_row(a.rope_lo, a.rope_hi, s.len - s.n + i, t, e);
+        rotate_part(x, e, false);
+        ref = a.lse[row] * kLog2e;
+#pragma unroll
+        for (int u = 0; u < 16; ++u) x[u] *= kLog2e / 8.0f;
+      } else {
+#pragma unroll
+        for (int u = 0; u < 16; ++u) x[u] = 0.f;
+      }
+      if (t == 0) a.lse2[task * a.mpad + m] = ref;
+      const int r = m & 7;
+      if constexpr (sizeof(DT) == 2) {
+        unsigned char* at = a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes + r * 128;
+#pragma unroll
+        for (int part = 0; part < 3; ++part) {
+          uint32_t w[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            w[u] = pack_bf2_rn(x[2 * u], x[2 * u + 1]);
+            x[2 * u] -= bf_lo(w[u]);
+            x[2 * u + 1] -= bf_hi(w[u]);
+          }
+          *reinterpret_cast<uint4*>(at + part * kPartBytes + ((t ^ r) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(at + part * kPartBytes + (((t + 4) ^ r) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      } else {
+        float* at = reinterpret_cast<float*>(a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes32) + r * kD;
+        float hi[16], lo[16];
+#pragma unroll
+        for (int u = 0; u < 16; ++u) {
+          hi[u] = tf32_of(x[u]);
+          lo[u] = tf32_of(x[u] - hi[u]);
+        }
+        store_part(at, t, hi);
+        store_part(at + 8 * kD, t, lo);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------------------- rows --
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+
+__device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// A lane's fragments.  Lane (g, t) = (lane / 4, lane % 4).
+template <typename DT>
+struct Frag;
+template <>
+struct Frag<__nv_bfloat16> {
+  static constexpr int kTiles = 4, kWords = 2;  // 16-byte words of a row that a lane holds: dims 8t .., 32+8t ..
+  static constexpr int kGroup = kGroupBytes;
+  uint4 q[3][2];
+  __device__ __forceinline__ static int word(int t, int k) { return t + 4 * k; }
+  __device__ __forceinline__ void load(const unsigned char* group, int g, int t) {
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) q[p][k] = *reinterpret_cast<const uint4*>(group + p * kPartBytes + g * 128 + ((word(t, k) ^ g) << 4));
+  }
+  // Scores of 16 rows (x0: row g, x1: row g + 8) and 8 queries; upper: of the queries' upper part alone.
+  __device__ __forceinline__ void scores(const uint4 (&x0)[2], const uint4 (&x1)[2], float (&c)[4], bool upper) const {
+    c[0] = c[1] = c[2] = c[3] = 0.f;
+#pragma unroll
+    for (int p = 2; p >= 0; --p) {
+      if (upper && p > 0) continue;
+      mma_bf16(c, x0[0].x, x1[0].x, x0[1].x, x1[1].x, q[p][0].x, q[p][1].x);
+      mma_bf16(c, x0[0].y, x1[0].y, x0[1].y, x1[1].y, q[p][0].y, q[p][1].y);
+      mma_bf16(c, x0[0].z, x1[0].z, x0[1].z, x1[1].z, q[p][0].z, q[p][1].z);
+      mma_bf16(c, x0[0].w, x1[0].w, x0[1].w, x1[1].w, q[p][0].w, q[p][1].w);
+    }
+  }
+};
+template <>
+struct Frag<float> {
+  static constexpr int kTiles = 2, kWords = 4;  // dims 16k + 4t .., k = 0 .. 3
+  static constexpr int kGroup = kGroupBytes32;
+  uint4 q[2][4];
+  __device__ __forceinline__ static int word(int t, int k) { return t + 4 * k; }
+  __device__ __forceinline__ void load(const unsigned char* group, int g, int t) {
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q[p][k] = reinterpret_cast<const uint4*>(group)[(p * 8 + g) * 16 + word(t, k)];
+  }
+  __device__ __forceinline__ void scores(const uint4 (&x0)[4], const uint4 (&x1)[4], float (&c)[4], bool upper) const {
+    c[0] = c[1] = c[2] = c[3] = 0.f;
+    float d[4] = {0.f, 0.f, 0.f, 0.f};  // the large products
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t u0[4] = {x0[k].x, x0[k].y, x0[k].z, x0[k].w}, u1[4] = {x1[k].x, x1[k].y, x1[k].z, x1[k].w};
+      const uint32_t qh[4] = {q[0][k].x, q[0][k].y, q[0][k].z, q[0][k].w}, ql[4] = {q[1][k].x, q[1][k].y, q[1][k].z, q[1][k].w};
+      uint32_t h0[4], h1[4], l0[4], l1[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float f0 = __uint_as_float(u0[e]), f1 = __uint_as_float(u1[e]), g0 = tf32_of(f0), g1 = tf32_of(f1);
+        h0[e] = __float_as_uint(g0);
+        h1[e] = __float_as_uint(g1);
+        l0[e] = __float_as_uint(tf32_of(f0 - g0));
+        l1[e] = __float_as_uint(tf32_of(f1 - g1));
+      }
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        if (!upper) {
+          mma_tf32(c, l0[e], l1[e], l0[e + 1], l1[e + 1], qh[e], qh[e + 1]);
+          mma_tf32(c, h0[e], h1[e], h0[e + 1], h1[e + 1], ql[e], ql[e + 1]);
+        }
+        mma_tf32(d, h0[e], h1[e], h0[e + 1], h1[e + 1], qh[e], qh[e + 1]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] += d[e];
+  }
+};
+
+// The schedule: units before each sequence's (of all layers and heads), one run of them a warp.
+template <typename DT, bool ONE>  // ONE: 8 query rows at most, whose fragments stay in registers
+__global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constant__ WeighArgs a) {
+  using F = Frag<DT>;
+  constexpr int TILES = F::kTiles, UNIT = 16 * TILES, VALUES = TILES / 2;  // a lane's rows at the end
+  __shared__ long long s_start[kMaxSeqs + 1];
+  const CacheDev& c = a.c;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  for (int b = threadIdx.x; b < a.B; b += kThreads) {
+    bool ok;
+    const WeighSeq s = weigh_seq(a, b, &ok);
+    s_start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + UNIT - 1) / UNIT) * c.L * c.H;
+  }
+  __syncthreads();
+  if (threadIdx.x < 32) {
+    long long base = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const int b = b0 + lane;
+      const long long own = b < a.B ? s_start[b] : 0;
+      long long x = own;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, x, d);
+        if (lane >= d) x += y;
+      }
+      if (b < a.B) s_start[b] = base + x - own;
+      base += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s_start[a.B] = base;
+  }
+  __syncthreads();
+  wait_for_first();
+  const long long total = s_start[a.B], warps = static_cast<long long>(gridDim.x) * kWarps, w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
+  const long long each = total / warps, rest = total % warps;
+  long long u = w * each + min(w, rest);
+  const long long u1 = u + each + (w < rest ? 1 : 0);
+  while (u < u1) {
+    // the task of unit u, and its units in this run
+    int lo = 0, hi = a.B;  // s_start[lo] <= u < s_start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_start[mid] <= u)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    const int b = lo;
+    bool ok;
+    const WeighSeq s = weigh_seq(a, b, &ok);
+    const int units = (s.len + UNIT - 1) / UNIT;
+    const long long off = u - s_start[b];
+    const int lh = static_cast<int>(off / units), l = lh / c.H, h = lh % c.H;
+    const int i0 = static_cast<int>(off - static_cast<long long>(lh) * units), i1 = static_cast<int>(min(static_cast<long long>(units), i0 + (u1 - u)));
+    u += i1 - i0;
+    const size_t task = (static_cast<size_t>(l) * a.B + b) * c.H + h;
+    const unsigned char* parts = a.parts + task * (a.mpad / 8) * F::kGroup;
+    const float* lse2 = a.lse2 + task * a.mpad;
+    const int used = s.n * a.G, groups = (used + 7) / 8, before = s.len - s.n;  // query row m sees rows up to before + m / G
+    const DT* pool = static_cast<const DT*>(c.k) + ((static_cast<size_t>(l) * c.n_pages * c.H + h) << c.shift) * kD;
+    const size_t page_elems = (static_cast<size_t>(c.H) << c.shift) * kD;
+    const int32_t* table = c.table + static_cast<size_t>(b) * c.max_pages;
+    float* out = a.weights + ((static_cast<size_t>(l) * c.S + b) * c.H + h) * a.rows;
+    F q;
+    float ref[2];
+    int sees[2];  // the last row that the lane's two queries see
+    auto take = [&](int group) {
+      q.load(parts + static_cast<size_t>(group) * F::kGroup, g, t);
+      const float2 r = *reinterpret_cast<const float2*>(lse2 + group * 8 + 2 * t);
+      ref[0] = r.x;
+      ref[1] = r.y;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int m = group * 8 + 2 * t + e;
+        sees[e] = m < used ? before + m / a.G : -1;
+      }
+    };
+    if (ONE) take(0);
+    for (int i = i0; i < i1; ++i) {
+      const int r0 = i * UNIT;
+      uint4 x[TILES][2][F::kWords];
+      bool in[TILES];
+#pragma unroll
+      for (int k = 0; k < TILES; ++k) {
+        const int r = r0 + 16 * k;
+        in[k] = r < s.len;
+        const int page = in[k] ? table[r >> c.shift] : 0;
+        if (in[k] && (page < 0 || page >= c.n_pages)) {
+          in[k] = false;
+          if (lane == 0) atomicExch(a.status, kStatusDeviceAssert);
+        }
+        const uint4* p = reinterpret_cast<const uint4*>(pool + page * page_elems + static_cast<size_t>((r & (c.P - 1)) + g) * kD);
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int z = 0; z < F::kWords; ++z) x[k][e][z] = in[k] ? __ldg(p + e * 8 * (kD * sizeof(DT) / 16) + F::word(t, z)) : make_uint4(0, 0, 0, 0);
+      }
+      float old[VALUES];
+#pragma unroll
+      for (int v = 0; v < VALUES; ++v) {
+        const int r = r0 + 32 * v + 8 * t + g;
+        old[v] = r < s.first && r < s.len ? out[r] : 0.f;
+      }
+      float sum[2 * TILES];
+#pragma unroll
+      for (int v = 0; v < 2 * TILES; ++v) sum[v] = 0.f;
+      for (int group = ONE ? 0 : max(0, r0 - before) * a.G / 8; group < groups; ++group) {
+        if (!ONE) take(group);
+        // whether some query of the group is none, or does not see every row of the unit
+        const bool all = group * 8 + 8 <= used && before + group * 8 / a.G >= r0 + UNIT - 1;
+        float part[2 * TILES];
+        // A NaN may come of an infinite key, where the parts' products are infinities of opposite signs: the upper
+        // part's alone keep the sign, and a second round takes them.
+#pragma unroll 1
+        for (int round = 0; round < 2; ++round) {
+          bool bad = false;
+#pragma unroll
+          for (int k = 0; k < TILES; ++k) {
+            float y[4];
+            q.scores(x[k][0], x[k][1], y, false);
+            if (round == 1) {
+              float z[4];
+              q.scores(x[k][0], x[k][1], z, true);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] = isnan(y[e]) ? z[e] : y[e];
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float y0 = exp2_approx(y[2 * e] - ref[0]), y1 = exp2_approx(y[2 * e + 1] - ref[1]);
+              if (!all) {
+                const int r = r0 + 16 * k + 8 * e + g;
+                y0 = r <= sees[0] ? y0 : 0.f;
+                y1 = r <= sees[1] ? y1 : 0.f;
+              }
+              part[2 * k + e] = y0 + y1;
+              bad |= isnan(y0 + y1);
+            }
+          }
+          if (!__any_sync(0xffffffffu, bad)) break;
+        }
+#pragma unroll
+        for (int v = 0; v < 2 * TILES; ++v) sum[v] += part[v];
+      }
+      // a quad has the sums of 8 rows a value over its lanes' columns; then lane t writes those of value t (and t + 4)
+#pragma unroll
+      for (int v = 0; v < 2 * TILES; ++v) sum[v] = quad_sum(sum[v]);
+#pragma unroll
+      for (int v = 0; v < VALUES; ++v) {
+        const int r = r0 + 32 * v + 8 * t + g;
+        const float y = t == 0 ? sum[4 * v] : t == 1 ? sum[4 * v + 1] : t == 2 ? sum[4 * v + 2] : sum[4 * v + 3];
+        bool there = false;  // of the tile that row r lies in
+#pragma unroll
+        for (int k = 0; k < TILES; ++k) there |= in[k] && k == 2 * v + (t >> 1);
+        if (there && r < s.len) out[r] = old[v] + y;
+      }
+    }
+  }
+}
+
+template <typename DT>
+cudaError_t launch(const WeighArgs& a, cudaStream_t stream) {
+  const int z = a.c.H < 64 ? a.c.H : 64;
+  int y = (a.mpad + kPrepThreads / 4 - 1) / (kPrepThreads / 4);
+  if (y > 1024) y = 1024;
+  weigh_prep_kernel<DT><<<dim3(static_cast<unsigned>(a.c.L) * a.B, y, z), kPrepThreads, 0, stream>>>(a);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const dim3 grid(152 * 2);  // 152 SMs
+  return a.G * a.T <= 8 ? launch_second(weigh_kernel<DT, true>, grid, kThreads, stream, a)
+                        : launch_second(weigh_kernel<DT, false>, grid, kThreads, stream, a);
+}
+
+int padded(int rows) { return rows <= 8 ? 8 : (rows + 63) / 64 * 64; }
+
+}  // namespace
+
+size_t weigh_workspace_bytes(const fib_attn_cache& c, int B, int Hq, int T) {
+  const size_t tasks = static_cast<size_t>(c.n_layers) * B * c.heads, mpad = padded(Hq / c.heads * T);
+  return 256 + round_up(tasks * mpad * sizeof(float)) + tasks * (mpad / 8) * (c.dtype == FIB_DTYPE_F32 ? kGroupBytes32 : kGroupBytes);
+}
+
+cudaError_t launch_cache_weigh(const fib_attn_cache& cache, int B, int Hq, int T, int rows, int n_max, const int32_t* n_new, const int32_t* path,
+                               const int32_t* first, const void* q, const float* lse, float* weights, const float2* lo_tab,
+                               const float2* hi_tab, int* status, unsigned long long wait_ns, void* ws, cudaStream_t stream) {
+  WeighArgs a;
+  a.c = device_view(cache);
+  a.B = B;
+  a.Hq = Hq;
+  a.G = Hq / cache.heads;
+  a.T = T;
+  a.rows = rows;
+  a.n_max = n_max;
+  a.mpad = padded(a.G * T);
+  a.n_new = n_new;
+  a.path = path;
+  a.first = first;
+  a.q = q;
+  a.lse = lse;
+  a.weights = weights;
+  a.rope_lo = lo_tab;
+  a.rope_hi = hi_tab;
+  a.status = status;
+  unsigned char* at = static_cast<unsigned char*>(ws);
+  a.next = reinterpret_cast<unsigned long long*>(at);
+  at += 256;
+  a.lse2 = reinterpret_cast<float*>(at);
+  at += round_up(static_cast<size_t>(cache.n_layers) * B * cache.heads * a.mpad * sizeof(float));
+  a.parts = at;
+  a.wait_ns = wait_ns;
+  return cache.dtype == FIB_DTYPE_F32 ? launch<float>(a, stream) : launch<__nv_bfloat16>(a, stream);
+}
+
+}  // namespace fibattn

@@ -40,7 +40,7 @@ EXPORTS = [
     "fib_attn_cache_commit", "fib_attn_cache_fork", "fib_attn_cache_compact", "fib_attn_tree_decode",
     "fib_attn_dense_tree_workspace_size", "fib_attn_dense_tree_decode", "fib_attn_plan_set_rotation",
     "fib_attn_rope_frequencies", "fib_attn_rope_create", "fib_attn_rope_destroy", "fib_attn_rotary", "fib_attn_rope_status",
-    "fib_attn_cache_evict_workspace_size", "fib_attn_cache_evict",
+    "fib_attn_cache_evict_workspace_size", "fib_attn_cache_evict", "fib_attn_cache_weigh_workspace_size", "fib_attn_cache_weigh",
 ]
 
 _i32p = ctypes.POINTER(ctypes.c_int32)
@@ -112,6 +112,8 @@ _SIGS = {
     "fib_attn_rotary": (_i, [_vp, _i, _i, _i, _i, _i, _vp, _i64p, _vp, _i64p, _vp, _i64p, _vp, _i64p, _vp,
                              _vp, _i, _vp]),
     "fib_attn_rope_status": (_i, [_vp]),
+    "fib_attn_cache_weigh_workspace_size": (ctypes.c_size_t, [_cachep, _i, _i, _i]),
+    "fib_attn_cache_weigh": (_i, [_vp, _cachep, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
     "fib_attn_cache_evict_workspace_size": (ctypes.c_size_t, [_cachep, _i]),
     "fib_attn_cache_evict": (_i, [_vp, _cachep, _i, _i, _vp, _i, _i, _vp, _vp, _vp, ctypes.c_size_t, _vp]),
 }
@@ -600,6 +602,34 @@ def _weights_rows(cache: Cache, weights) -> int:
     if len(shape) != 4 or shape[:3] != (cache.n_layers, cache.max_seqs, cache.heads) or _bad(weights, torch.float32, cache.index):
         raise ValueError(f"weights must be float32 [n_layers, max_seqs, heads, rows] on {cache.device}")
     return shape[3]
+
+
+def fib_attn_cache_weigh_workspace_size(cache: Cache, B: int, Hq: int, T: int) -> int:
+    return int(lib().fib_attn_cache_weigh_workspace_size(cache.pointer, B, Hq, T))
+
+
+def fib_attn_cache_weigh(plan: Plan, cache: Cache, q, lse, n_new, weights, path=None, first=None, workspace=None, stream=None):
+    """Adds to weights float32 [n_layers, max_seqs, heads, rows] what the last n_new[b] rows' tokens (just committed) give to each
+    row: q [n_layers, B, Hq, T, 64] raw and lse float32 [n_layers, B, Hq, T] of their nodes, path as in the commit; weights of rows
+    from first int32 [B] on (None: the new ones) begin with this call."""
+    index, shape, rows = cache.index, q.shape, _weights_rows(cache, weights)
+    if len(shape) != 5 or shape[0] != cache.n_layers or shape[4] != FIB_HEAD_DIM or _bad(q, cache.dtype, index):
+        raise ValueError(f"q must be contiguous [n_layers, B, Hq, T, 64] {cache.dtype} on {cache.device}")
+    _, B, Hq, T, _ = shape
+    if lse.shape != shape[:4] or _bad(lse, torch.float32, index):
+        raise ValueError(f"lse must be float32 [n_layers, B, Hq, T] on {cache.device}")
+    if n_new.shape != (B,) or _bad(n_new, torch.int32, index):
+        raise ValueError(f"n_new must be int32 [B] on {cache.device}")
+    if path is not None and (path.shape != (B, T) or _bad(path, torch.int32, index)):
+        raise ValueError(f"path must be int32 [B, T] on {cache.device}")
+    if first is not None and (first.shape != (B,) or _bad(first, torch.int32, index)):
+        raise ValueError(f"first must be int32 [B] on {cache.device}")
+    at, size, workspace = _scratch(cache, workspace, lambda: fib_attn_cache_weigh_workspace_size(cache, B, Hq, T), stream)
+    code = lib().fib_attn_cache_weigh(plan.handle, cache.pointer, B, Hq, T, rows, n_new.data_ptr(), None if path is None else path.data_ptr(),
+                                      None if first is None else first.data_ptr(), q.data_ptr(), lse.data_ptr(), weights.data_ptr(), at, size,
+                                      _raw_stream(stream, index))
+    if code:
+        raise FibAttnError("fib_attn_cache_weigh", code)
 
 
 def fib_attn_cache_evict_workspace_size(cache: Cache, rows: int) -> int:

@@ -380,6 +380,35 @@ int fib_attn_cache_fork(const fib_attn_cache* c, const int32_t* src, void* works
 int fib_attn_cache_compact(const fib_attn_cache* c, int32_t* remap, void* workspace,
                            size_t ws_bytes, void* stream);
 
+/* The attention weight that new tokens give to each cached row, added up (dense attention, as
+ * fib_attn_dense_tree_decode and fib_attn_dense_fwd): what eviction goes by.  Called behind the commit of those tokens,
+ * with its B, T, n_new and path: sequence b's last n_new[b] rows are its new tokens, row
+ * lens[b] - n_new[b] + i that of node path[b][i] (path NULL: node i), whose query and lse lie at
+ * that node.  For every layer, key head h and row r < lens[b],
+ *   weights[layer][b][h][r] = (r < first[b] ? weights[layer][b][h][r] : 0)
+ *     + sum of exp(score - lse) over the new tokens at position r or behind and the query heads of h,
+ * with score = RoPE(q) . K_r / 8, K_r as the cache holds it (a new row rounded to its type, where a decode
+ * had it as drafted), and the tokens' positions those of their rows.  first: int32 [B], or NULL: lens[b] -
+ * n_new[b] (rows that were there are added to, the new ones begin; a zero begins them all, as behind
+ * a prompt of which only the last tokens weigh).  A call of n_new[b] = 0 leaves the sequence's weights.
+ * q: [n_layers, B, Hq, T, 64] raw, in the cache's type and finite; Hq a multiple of the cache's
+ * heads; lse: float32 [n_layers, B, Hq, T]; weights: float32 [n_layers, max_seqs, heads, rows]; n_new: int32
+ * [B]; path: int32 [B, T] or NULL; all on the device.  Rows at and behind lens[b], and what lies in queries that no
+ * row is the node of, are never used; entries of weights behind lens[b] stay as they were.  Sums are float32, in
+ * an order that depends on nothing but the sizes.  fib_attn_cache_fork moves no weights: row src[b] of
+ * them goes on as row b.
+ * n_new[b] outside [0, T], a length below it or above the table, `rows` or the plan's N_max records
+ * FIB_ERR_DEVICE_ASSERT in the plan's status word and leaves the sequence's weights; so does a page id
+ * outside the pool, for its rows; a path entry outside [0, T) too, and the sequence's weights are
+ * then unspecified.  A wait that runs out (fib_attn_plan_set_debug) records FIB_ERR_TIMEOUT; weights are then unspecified.
+ * workspace: fib_attn_cache_weigh_workspace_size(c, B, Hq, T) bytes, 256-byte aligned,
+ * contents on entry ignored.  Errors as commit.                                         */
+size_t fib_attn_cache_weigh_workspace_size(const fib_attn_cache* c, int B, int Hq, int T);
+int fib_attn_cache_weigh(fib_attn_plan_t p, const fib_attn_cache* c, int B, int Hq, int T, int rows,
+                         const int32_t* n_new, const int32_t* path, const int32_t* first,
+                         const void* q, const float* lse, float* weights, void* workspace,
+                         size_t ws_bytes, void* stream);
+
 /* Eviction by accumulated attention weight: a cache in bounded memory, as a control to the
  * static sparse pattern (the paper has no counterpart).  Sequence b < B with more than keep[b] rows is left
  * with keep[b], for every layer and key head by itself: its first `sink`, its last `recent` and,

@@ -95,6 +95,29 @@ class PagedCache:
                 row[j] = remap[row[j]]
         return remap, n
 
+    def weigh(self, weights, q, lse, n_new, path=None, first=None, turns: bool = True):
+        """Adds to weights [layers, seqs, heads, rows] what the last n_new[b] rows' tokens give to each row; q [layers, B, Hq, T, D] raw,
+        lse [layers, B, Hq, T]."""
+        H = self.k.shape[2]
+        G = q.shape[2] // H
+        for b, n in enumerate(n_new):
+            if n == 0:
+                continue
+            length = self.lens[b]
+            begin = length - n if first is None else first[b]
+            for layer in range(q.shape[0]):
+                K, _ = self.rows(layer, b)
+                for h in range(H):
+                    got = np.zeros(length)
+                    for i in range(n):
+                        node, p = i if path is None else path[b][i], length - n + i
+                        for g in range(h * G, (h + 1) * G):
+                            x = q[layer, b, g, node]
+                            s = K[:p + 1, h] @ (turn(x, p) if turns else x) / math.sqrt(len(x))
+                            got[:p + 1] += np.exp(s - lse[layer, b, g, node])
+                    old = np.where(np.arange(length) < begin, weights[layer, b, h, :length], 0.0)
+                    weights[layer, b, h, :length] = old + got
+
     def evict(self, weights, keep, sink: int, recent: int, dropped, turns: bool = True) -> bool:
         """Keeps of each longer sequence the first rows, the last and the heaviest between; weights [layers, seqs, heads, rows] and
         dropped are changed in place.  False (and nothing done) where the pages do not suffice."""

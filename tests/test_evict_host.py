@@ -44,3 +44,32 @@ def test_oracle_evicts_as_written():
     assert np.array_equal(c.k[0, 3, 0], [k[0, 0, 0, 0], k[0, 0, 0, 2], k[0, 1, 0, 1], k[0, 1, 0, 2]])
     assert np.array_equal(c.v[0, 3, 0], c.k[0, 3, 0] + 100)
     assert w[0, 0, 0].tolist() == [9, 5, 7, 0, 2, 7, 0, 3]
+
+
+def test_weigh_arguments(lib):  # noqa: F811
+    s = struct()
+    p = ctypes.byref(s)
+    need = lib.fib_attn_cache_weigh_workspace_size(p, 2, 8, 3)
+    assert need > 0 and lib.fib_attn_cache_weigh_workspace_size(None, 2, 8, 3) == 0
+    assert lib.fib_attn_cache_weigh(None, p, 2, 8, 3, 100, 16, None, None, 16, 16, 32, 256, need, None) == fa.FIB_ERR_INVALID_ARG
+    good = dict(B=2, Hq=8, T=3, rows=100, n=16, path=None, first=None, q=512, lse=16, w=32, ws=256, size=need)
+    for kw in (dict(B=0), dict(B=4), dict(Hq=0), dict(Hq=6), dict(Hq=1028), dict(T=0), dict(T=(1 << 20) + 1), dict(rows=0), dict(n=None), dict(n=18),
+               dict(path=18), dict(first=17), dict(q=None), dict(q=520), dict(lse=None), dict(lse=18), dict(w=None), dict(w=33), dict(w=16),
+               dict(ws=None), dict(ws=264), dict(size=need - 1), dict(q=256), dict(lse=256), dict(w=256)):
+        x = {**good, **kw}
+        assert lib.fib_attn_cache_weigh(1 << 12, p, x["B"], x["Hq"], x["T"], x["rows"], x["n"], x["path"], x["first"], x["q"], x["lse"], x["w"],
+                                        x["ws"], x["size"], None) == fa.FIB_ERR_INVALID_ARG, kw
+    with_bad = ctypes.byref(struct(heads=0))
+    assert lib.fib_attn_cache_weigh_workspace_size(with_bad, 2, 8, 3) == 0
+    assert lib.fib_attn_cache_weigh(1 << 12, with_bad, 2, 8, 3, 100, 16, None, None, 512, 16, 32, 256, need, None) == fa.FIB_ERR_INVALID_ARG
+
+
+def test_oracle_weighs_as_written():
+    """One layer, one head of two dims at rest (no rotation); three rows, of which the last two are new."""
+    k = np.array([[2.0, 0.0], [0.0, 2.0], [1.0, 1.0], [9.0, 9.0]]).reshape(1, 1, 1, 4, 2)
+    c = co.PagedCache(k, k, [[0]], [3], [1])
+    w = np.array([[[[10.0, 20.0, 30.0, 40.0]]]])
+    q = np.array([[1.0, 0.0], [0.0, 1.0]]).reshape(1, 1, 1, 2, 2)
+    c.weigh(w, q, np.zeros((1, 1, 1, 2)), [2], turns=False)
+    e = np.exp(np.array([2.0, 0.0, 1.0]) / np.sqrt(2)), np.exp(np.array([0.0, 2.0, 1.0]) / np.sqrt(2))
+    assert np.allclose(w[0, 0, 0], [10 + e[0][0] + e[1][0], e[0][1] + e[1][1], e[1][2], 40.0], rtol=1e-14)
