@@ -13,7 +13,7 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfibattn.so")
 
 SOURCES = ["planner.cpp", "api.cu", "fwd.cu", "fwd_tc.cu", "bwd.cu", "bwd_tc.cu", "decode.cu", "dense.cu",
-           "cache.cu", "evict.cu", "weigh.cu", "tree.cu", "tree_tc.cu", "tree_dense.cu", "tree_dense_tc.cu", "api_cache.cu", "rotary.cu", "api_rope.cu"]
+           "cache.cu", "evict.cu", "weigh.cu", "weigh_tc.cu", "tree.cu", "tree_tc.cu", "tree_dense.cu", "tree_dense_tc.cu", "api_cache.cu", "rotary.cu", "api_rope.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++20", "-lineinfo", "-Xcompiler", "-fPIC,-O2",
               "--expt-relaxed-constexpr", "-I" + os.path.join(ROOT, "include")]

@@ -159,7 +159,7 @@ int fib_attn_cache_weigh(fib_attn_plan_t p, const fib_attn_cache* c, int B, int 
   if (st == FIB_OK) st = check_cache_device(c);
   if (st != FIB_OK) return st;
   return cuda_status(launch_cache_weigh(*c, B, Hq, T, rows, p->N_max, n_new, path, first, q, lse, weights, p->d_lo, p->d_hi, p->d_status,
-                                        p->wait_ns, workspace, static_cast<cudaStream_t>(stream)));
+                                        p->wait_ns, p->skip_first_rung_copy, workspace, static_cast<cudaStream_t>(stream)));
 }
 
 size_t fib_attn_cache_evict_workspace_size(const fib_attn_cache* c, int rows) {

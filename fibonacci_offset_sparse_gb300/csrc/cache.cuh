@@ -23,7 +23,8 @@ cudaError_t launch_cache_compact(const fib_attn_cache& c, int32_t* remap, void* 
 size_t weigh_workspace_bytes(const fib_attn_cache& c, int B, int Hq, int T);
 cudaError_t launch_cache_weigh(const fib_attn_cache& c, int B, int Hq, int T, int rows, int n_max, const int32_t* n_new, const int32_t* path,
                                const int32_t* first, const void* q, const float* lse, float* weights, const float2* lo_tab,
-                               const float2* hi_tab, int* status, unsigned long long wait_ns, void* ws, cudaStream_t stream);
+                               const float2* hi_tab, int* status, unsigned long long wait_ns, int skip_copy, void* ws,
+                               cudaStream_t stream);
 size_t cache_evict_workspace_bytes(const fib_attn_cache& c, int rows);
 cudaError_t launch_cache_evict(const fib_attn_cache& c, int B, int rows, const int32_t* keep, int sink, int recent, int n_max,
                                float* weights, int32_t* dropped, const float2* lo_tab, const float2* hi_tab, bool turns, void* ws,

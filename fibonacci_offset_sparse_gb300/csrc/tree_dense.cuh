@@ -568,8 +568,8 @@ using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, 
                                  const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// A layer's pool as rows of 64 values (float32: as two halves of 32); a copy takes `box` rows, 128 bytes at a time.
-inline cudaError_t map_of(CUtensorMap* m, const void* pool, long long rows, int es, int box) {
+// The driver's function that describes such a copy; null where it has none.
+inline EncodeTiled encode_tiled() {
   static const EncodeTiled encode = [] {
     void* fn = nullptr;
     cudaDriverEntryPointQueryResult found;
@@ -578,6 +578,12 @@ inline cudaError_t map_of(CUtensorMap* m, const void* pool, long long rows, int 
       fn = nullptr;
     return reinterpret_cast<EncodeTiled>(fn);
   }();
+  return encode;
+}
+
+// A layer's pool as rows of 64 values (float32: as two halves of 32); a copy takes `box` rows, 128 bytes at a time.
+inline cudaError_t map_of(CUtensorMap* m, const void* pool, long long rows, int es, int box) {
+  const EncodeTiled encode = encode_tiled();
   if (encode == nullptr) return cudaErrorNotSupported;
   const cuuint64_t n = static_cast<cuuint64_t>(rows), row_bytes = static_cast<cuuint64_t>(kD) * es;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(128 / es), n, row_bytes / 128}, strides[2] = {row_bytes, 128};

@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float y0 = exp2_approx(y[2 * e] - ref[0]), y1 = exp2_approx(y[2 * e + 1] - ref[1]);
+              float y0 = ex2(y[2 * e] - ref[0]), y1 = ex2(y[2 * e + 1] - ref[1]);
               if (!all) {
                 const int r = r0 + 16 * k + 8 * e + g;
                 y0 = r <= sees[0] ? y0 : 0.f;
@@ -345,8 +345,11 @@ cudaError_t launch(const WeighArgs& a, cudaStream_t stream) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 grid(152 * 2);  // 152 SMs
-  return a.G * a.T <= 8 ? launch_second(weigh_kernel<DT, true>, grid, kThreads, stream, a)
-                        : launch_second(weigh_kernel<DT, false>, grid, kThreads, stream, a);
+  if (a.G * a.T <= 8) return launch_second(weigh_kernel<DT, true>, grid, kThreads, stream, a);
+  if constexpr (sizeof(DT) == 2)
+    return launch_weigh_tc(a, stream);
+  else
+    return launch_second(weigh_kernel<DT, false>, grid, kThreads, stream, a);
 }
 
 int padded(int rows) { return rows <= 8 ? 8 : (rows + 63) / 64 * 64; }
@@ -360,7 +363,8 @@ size_t weigh_workspace_bytes(const fib_attn_cache& c, int B, int Hq, int T) {
 
 cudaError_t launch_cache_weigh(const fib_attn_cache& cache, int B, int Hq, int T, int rows, int n_max, const int32_t* n_new, const int32_t* path,
                                const int32_t* first, const void* q, const float* lse, float* weights, const float2* lo_tab,
-                               const float2* hi_tab, int* status, unsigned long long wait_ns, void* ws, cudaStream_t stream) {
+                               const float2* hi_tab, int* status, unsigned long long wait_ns, int skip_copy, void* ws,
+                               cudaStream_t stream) {
   WeighArgs a;
   a.c = device_view(cache);
   a.B = B;
@@ -386,6 +390,7 @@ cudaError_t launch_cache_weigh(const fib_attn_cache& cache, int B, int Hq, int T
   at += round_up(static_cast<size_t>(cache.n_layers) * B * cache.heads * a.mpad * sizeof(float));
   a.parts = at;
   a.wait_ns = wait_ns;
+  a.skip_copy = skip_copy;
   return cache.dtype == FIB_DTYPE_F32 ? launch<float>(a, stream) : launch<__nv_bfloat16>(a, stream);
 }
 

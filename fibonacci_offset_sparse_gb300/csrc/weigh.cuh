@@ -1,6 +1,7 @@
 // The accumulated attention weight of cached rows: what its kernels share (weigh.cu, weigh_tc.cu).
 #pragma once
 #include "cache_dev.cuh"
+#include "tree.cuh"
 
 namespace fibattn {
 
@@ -24,17 +25,12 @@ struct WeighArgs {
   float* lse2;
   unsigned long long* next;  // weigh_tc.cu: the next task to be taken
   unsigned long long wait_ns;
+  int skip_copy;  // test hook: the first rows of every task of weigh_tc.cu are never copied
 };
 
 constexpr int kPartBytes = 8 * kD * 2;        // 8 rows of one bf16 part
 constexpr int kGroupBytes = 3 * kPartBytes;   // 8 query rows, bf16
 constexpr int kGroupBytes32 = 2 * 8 * kD * 4;  // ... float32
-
-__device__ __forceinline__ float exp2_approx(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;\n" : "=f"(y) : "f"(x));
-  return y;
-}
 
 // Sequence b of a call: rows, new ones (0: nothing to do), the first row whose weight begins with this call.
 struct WeighSeq {

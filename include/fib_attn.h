@@ -562,10 +562,10 @@ int fib_attn_debug_indices(fib_attn_plan_t p, int layer, int N, int i_begin, int
  * stage rows with the bulk-copy engine wait on mbarriers; every such wait gives up after
  * wait_ns nanoseconds (default 1e9; accepted range [1e3, 6e10]), records FIB_ERR_TIMEOUT in
  * the status word, lets the copies already in flight land and returns without writing
- * output (of fib_attn_dense_tree_decode o and lse are unspecified then).  debug_flags:
+ * output (of fib_attn_dense_tree_decode o and lse, of fib_attn_cache_weigh the weights are unspecified then).  debug_flags:
  * FIB_DEBUG_SKIP_COPY makes the bf16 tensor-core forward never complete one of its staged
- * copies (the values of the window block) and fib_attn_dense_tree_decode never begin one (the
- * first keys of each sequence and head), which drives that timeout path; FIB_DEBUG_CORRUPT_TABLE moves the first rung of the bf16 tensor-core
+ * copies (the values of the window block) and fib_attn_dense_tree_decode and fib_attn_cache_weigh (bf16, more
+ * than 8 query rows a key head) never begin one (the first keys of each sequence and head), which drives that timeout path; FIB_DEBUG_CORRUPT_TABLE moves the first rung of the bf16 tensor-core
  * forward's host-built rung table to distance 0 (a row inside the window, so every address
  * stays inside the sequence), which its device-side table check rejects with
  * FIB_ERR_DEVICE_ASSERT before any rung row is read.  Host-only; takes effect on the next

@@ -265,3 +265,15 @@ def test_commit_decode_weigh_evict_as_they_are_used(dtype, T):
         fa.fib_attn_cache_evict(plan, c, w, keep, 4, T, dropped=dropped)
     assert fa.fib_attn_cache_status(c) == fa.FIB_OK and fa.fib_attn_last_device_status(plan) == fa.FIB_OK
     assert (c.lens <= keep).all() and [int(x) + int(y) for x, y in zip(c.lens, dropped)] == [4 * T, 4 * (T - 1 if T > 1 else 1)]
+
+
+def test_a_wait_that_runs_out():
+    """A copy that never comes: the call ends, reports, and the next one is right."""
+    r = rng(209)
+    c, ref, q, qf, lse, w, _ = setup(r, "bf16", 2, 2, 1, 20, 16, [600, 100], [20, 20])
+    plan = plan_for(1000)
+    fa.fib_attn_plan_set_debug(plan, True, 2_000_000)
+    fa.fib_attn_cache_weigh(plan, c, q, torch.from_numpy(lse).cuda(), i32([20, 20]), torch.from_numpy(w).cuda())
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_ERR_TIMEOUT
+    fa.fib_attn_plan_set_debug(plan, False, 1_000_000_000)
+    run(c, ref, plan, q, qf, lse, w, [20, 20])
