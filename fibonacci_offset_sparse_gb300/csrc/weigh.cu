@@ -49,21 +49,21 @@ __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_c
         }
       }
       float x[16];
-      float ref = INFINITY;
+      float ref = -INFINITY;
       if (live) {
         const size_t row = ((static_cast<size_t>(l) * a.B + b) * a.Hq + h * a.G + g) * a.T + node;
         float2 e[8];
         load_part(static_cast<const DT*>(a.q) + row * kD, t, x);
         rope_row(a.rope_lo, a.rope_hi, s.len - s.n + i, t, e);
         rotate_part(x, e, false);
-        ref = a.lse[row] * kLog2e;
+        ref = -a.lse[row] * kLog2e;
 #pragma unroll
         for (int u = 0; u < 16; ++u) x[u] *= kLog2e / 8.0f;
       } else {
 #pragma unroll
         for (int u = 0; u < 16; ++u) x[u] = 0.f;
       }
-      if (t == 0) a.lse2[task * a.mpad + m] = ref;
+      if (t == 0) a.refs[task * a.mpad + m] = ref;
       const int r = m & 7;
       if constexpr (sizeof(DT) == 2) {
         unsigned char* at = a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes + r * 128;
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     u += i1 - i0;
     const size_t task = (static_cast<size_t>(l) * a.B + b) * c.H + h;
     const unsigned char* parts = a.parts + task * (a.mpad / 8) * F::kGroup;
-    const float* lse2 = a.lse2 + task * a.mpad;
+    const float* refs = a.refs + task * a.mpad;
     const int used = s.n * a.G, groups = (used + 7) / 8, before = s.len - s.n;  // query row m sees rows up to before + m / G
     const DT* pool = static_cast<const DT*>(c.k) + ((static_cast<size_t>(l) * c.n_pages * c.H + h) << c.shift) * kD;
     const size_t page_elems = (static_cast<size_t>(c.H) << c.shift) * kD;
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     int sees[2];  // the last row that the lane's two queries see
     auto take = [&](int group) {
       q.load(parts + static_cast<size_t>(group) * F::kGroup, g, t);
-      const float2 r = *reinterpret_cast<const float2*>(lse2 + group * 8 + 2 * t);
+      const float2 r = *reinterpret_cast<const float2*>(refs + group * 8 + 2 * t);
       ref[0] = r.x;
       ref[1] = r.y;
 #pragma unroll
@@ -305,7 +305,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float y0 = ex2(y[2 * e] - ref[0]), y1 = ex2(y[2 * e + 1] - ref[1]);
+              float y0 = ex2(y[2 * e] + ref[0]), y1 = ex2(y[2 * e + 1] + ref[1]);
               if (!all) {
                 const int r = r0 + 16 * k + 8 * e + g;
                 y0 = r <= sees[0] ? y0 : 0.f;
@@ -386,7 +386,7 @@ cudaError_t launch_cache_weigh(const fib_attn_cache& cache, int B, int Hq, int T
   unsigned char* at = static_cast<unsigned char*>(ws);
   a.next = reinterpret_cast<unsigned long long*>(at);
   at += 256;
-  a.lse2 = reinterpret_cast<float*>(at);
+  a.refs = reinterpret_cast<float*>(at);
   at += round_up(static_cast<size_t>(cache.n_layers) * B * cache.heads * a.mpad * sizeof(float));
   a.parts = at;
   a.wait_ns = wait_ns;

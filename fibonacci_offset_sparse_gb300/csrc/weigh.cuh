@@ -20,9 +20,9 @@ struct WeighArgs {
   int* status;
   // Workspace.  parts: for each layer, sequence and key head, and 8 query rows after one another, the rotated rows times
   // log2(e)/8, split: bf16 hi, mid, lo, each [8][64] with its 16-byte words swizzled as the tensor pipes' 128-byte pattern, word w of
-  // row r at w ^ r; float32 hi, lo (tf32), each [8][64].  lse2: lse * log2(e), +inf where there is no row.
+  // row r at w ^ r; float32 hi, lo (tf32), each [8][64].  refs: -lse * log2(e), -inf where there is no row.
   unsigned char* parts;
-  float* lse2;
+  float* refs;
   unsigned long long* next;  // weigh_tc.cu: the next task to be taken
   unsigned long long wait_ns;
   int skip_copy;  // test hook: the first rows of every task of weigh_tc.cu are never copied

@@ -23,7 +23,7 @@ namespace {
 constexpr int kTile = 128, kTiles = 4, kGroupRows = kTile * kTiles;  // rows of a task
 constexpr int kCols = 128;                                            // query rows of a product
 constexpr int kTileBytes = kTile * kD * 2, kSlots = 6;
-constexpr int kQueryBytes = kCols / 8 * kGroupBytes, kQuerySlot = kQueryBytes + kCols * 4 + 512;  // and lse; a multiple of 1024
+constexpr int kQueryBytes = kCols / 8 * kGroupBytes, kQuerySlot = kQueryBytes + kCols * 4 + 512;  // and their references; a multiple of 1024
 constexpr int kBuffers = 4;                                           // of tensor memory, kCols columns each
 constexpr int kSumWarps = 8, kFeeder = 8, kIssuer = 9, kThreads = 320;
 constexpr int kQueries = kSlots * kTileBytes, kSchedule = kQueries + 2 * kQuerySlot;
@@ -54,9 +54,18 @@ __device__ __forceinline__ int chunks(const TcTask& k) { return (k.used + kCols 
 // Columns of chunk c's product.
 __device__ __forceinline__ int columns(const TcTask& k, int c) { return min(kCols, (k.used - c * kCols + 15) / 16 * 16); }
 
+// The sequences, in shared memory: the tasks before each, and what it is.
+struct TcSchedule {
+  long long* start;  // [B + 1]
+  WeighSeq* seq;     // [B]
+  __device__ __forceinline__ TcSchedule(unsigned char* at, int B) : start(reinterpret_cast<long long*>(at)), seq(reinterpret_cast<WeighSeq*>(start + B + 1)) {}
+  static size_t bytes(int B) { return sizeof(long long) * (B + 1) + sizeof(WeighSeq) * B; }
+};
+
 // Task `id` of the call, if there is one (tiles > 0): sequences in order, of each the first rows of all layers and heads before the next.
-__device__ __forceinline__ TcTask task_at(const WeighArgs& a, const long long* start, unsigned long long id) {
+__device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& sch, unsigned long long id) {
   TcTask k = {};
+  const long long* start = sch.start;
   if (id >= static_cast<unsigned long long>(start[a.B])) return k;
   const long long u = static_cast<long long>(id);
   int lo = 0, hi = a.B;
@@ -67,8 +76,7 @@ __device__ __forceinline__ TcTask task_at(const WeighArgs& a, const long long* s
     else
       hi = mid;
   }
-  bool ok;
-  const WeighSeq s = weigh_seq(a, lo, &ok);
+  const WeighSeq s = sch.seq[lo];
   const int per = a.c.L * a.c.H;
   const long long off = u - start[lo];
   const int j = static_cast<int>(off / per), lh = static_cast<int>(off - static_cast<long long>(j) * per);
@@ -134,7 +142,7 @@ __device__ __noinline__ float add_infinite(const WeighArgs& a, const TcTask& k, 
       const float x = __bfloat162float(*reinterpret_cast<const __nv_bfloat16*>(q + (((d >> 3) ^ (m & 7)) << 4) + (d & 7) * 2));
       s += x * (negative >> d & 1 ? -INFINITY : INFINITY);
     }
-    sum += ex2(s - a.lse2[task * a.mpad + m]);
+    sum += ex2(s + a.refs[task * a.mpad + m]);
   }
   return sum;
 }
@@ -143,7 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(16) TcBars bars;
   volatile int& s_err = bars.err;
-  long long* start = reinterpret_cast<long long*>(smem + kSchedule);  // [B + 1] tasks before each sequence's
+  const TcSchedule sch(smem + kSchedule, a.B);
+  long long* start = sch.start;
   const CacheDev& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -168,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   for (int b = tid; b < a.B; b += kThreads) {
     bool ok;
     const WeighSeq s = weigh_seq(a, b, &ok);
+    sch.seq[b] = s;
     start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + kGroupRows - 1) / kGroupRows) * c.L * c.H;
   }
   __syncthreads();
@@ -197,18 +207,18 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   if (warp == kFeeder) {
     // =================================================================== feeder
     const int box = min(kTile, c.P);  // rows a copy
-    auto fetch = [&] {                // a task's number
-      unsigned long long id = 0;
-      if (lane == 0) id = atomicAdd(a.next, 1ull);
-      return __shfl_sync(0xffffffffu, id, 0);
-    };
+    // A task's number, in lane 0, and not waited for before it is used.  Taken early where tasks are short; where they are long
+    // late, as one that waits for its block waits for nothing else.
+    auto fetch = [&] { return lane == 0 ? atomicAdd(a.next, 1ull) : 0ull; };
+    auto known = [&](unsigned long long id) { return task_at(a, sch, __shfl_sync(0xffffffffu, id, 0)); };
     auto page_of = [&](const TcTask& k) {  // of the lane-th page of the task's rows
       const int at = (k.r0 >> c.shift) + lane;
       return k.tiles > 0 && at < c.max_pages ? __ldg(c.table + static_cast<size_t>(k.b) * c.max_pages + at) : -1;
     };
-    TcTask now = task_at(a, start, fetch());
-    int page = page_of(now);
-    unsigned long long after = fetch();
+    unsigned long long id = fetch();
+    TcTask now = known(id), next = {};
+    int page = page_of(now), next_page = 0;
+    bool taken = false;  // id is the number of the task after the next that is known
     int tc = 0, kc = 0, qc = 0;
     uint32_t left_out = 0;  // slots that the test hook never fills
     bool stop = false;
@@ -221,12 +231,22 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       __syncwarp();
       ++tc;
       if (now.tiles == 0) break;
-      // the task after this one, its pages on their way while this one's copies wait for their slots
-      const TcTask next = task_at(a, start, after);
-      const int next_page = page_of(next);
-      if (next.tiles > 0) after = fetch();
       const size_t task = (static_cast<size_t>(now.l) * a.B + now.b) * c.H + now.h;
       const int c0 = first_chunk(a, now, now.r0), c1 = chunks(now);
+      const bool is_short = c1 - c0 == 1;
+      auto look_ahead = [&] {
+        if (!taken) id = fetch();
+        next = known(id);
+        next_page = page_of(next);
+        taken = false;
+      };
+      if (is_short) {  // the next one's pages, and the number of the one behind it, come while this one's copies wait for their slots
+        look_ahead();
+        if (next.tiles > 0) {
+          id = fetch();
+          taken = true;
+        }
+      }
       for (int ch = c0; ch < c1 && !stop; ++ch, ++qc) {
         const int slot = qc & 1, n = columns(now, ch);
         if (!warp_wait(&bars.q_empty[slot], ((qc >> 1) & 1) ^ 1, a.wait_ns, &s_err)) {
@@ -238,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           const size_t m = task * a.mpad + static_cast<size_t>(ch) * kCols;
           mbar_arrive_tx(&bars.q_full[slot], n / 8 * kGroupBytes + n * 4);
           bulk_g2s(to, a.parts + m / 8 * kGroupBytes, n / 8 * kGroupBytes, &bars.q_full[slot]);
-          bulk_g2s(to + kQueryBytes, a.lse2 + m, n * 4, &bars.q_full[slot]);
+          bulk_g2s(to + kQueryBytes, a.refs + m, n * 4, &bars.q_full[slot]);
         }
         __syncwarp();
         if (ch != c0) continue;
@@ -266,6 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           __syncwarp();
         }
       }
+      if (!is_short && !stop) look_ahead();
       now = next;
       page = next_page;
     }
@@ -355,10 +376,12 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       float* out = a.weights + ((static_cast<size_t>(k.l) * c.S + k.b) * c.H + k.h) * a.rows;
       const int row = k.r0 + set * kTile + wq * 32 + lane;  // the thread's rows: this one, and two tiles on
       float sum[2] = {0.f, 0.f}, old[2];
+      bool there[2];  // (read here, so that nothing is waited for at the end)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = row + 2 * i * kTile;
         old[i] = r < k.first && r < k.len ? out[r] : 0.f;
+        there[i] = r < k.len && row_at(a, k, r) >= 0;
       }
       const int c0 = first_chunk(a, k, k.r0), c1 = chunks(k);
       for (int ch = c0; ch < c1 && go; ++ch, ++qc) {
@@ -380,36 +403,42 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           const bool all = m0 + n <= k.used && k.before + m0 / a.G >= k.r0 + (t + 1) * kTile - 1;
           const int lo = max(0, r - k.before) * a.G - m0, hi = k.used - m0;  // the columns that see row r
           float s[4] = {0.f, 0.f, 0.f, 0.f};
-          auto use = [&](const uint32_t (&x)[16], int col) {
+          auto use = [&]<bool ALL>(const uint32_t (&x)[16], int col) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const float4 l4 = *reinterpret_cast<const float4*>(ref + col + e);
+              const float4 r4 = *reinterpret_cast<const float4*>(ref + col + e);
               float y[4] = {__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])};
-              add2(y[0], y[1], -l4.x, -l4.y);
-              add2(y[2], y[3], -l4.z, -l4.w);
+              add2(y[0], y[1], r4.x, r4.y);
+              add2(y[2], y[3], r4.z, r4.w);
 #pragma unroll
               for (int f = 0; f < 4; ++f) {
                 y[f] = ex2(y[f]);
-                if (!all) y[f] = col + e + f >= lo && col + e + f < hi ? y[f] : 0.f;
+                if (!ALL) y[f] = col + e + f >= lo && col + e + f < hi ? y[f] : 0.f;
               }
               add2(s[0], s[1], y[0], y[1]);
               add2(s[2], s[3], y[2], y[3]);
             }
           };
           const uint32_t from = tmem + buf * kCols + lanes;
-          uint32_t x[16], y[16];
-          ld16(from, x);
-          wait16(x);
-          for (int col = 0; col < n; col += 32) {
-            const bool second = col + 16 < n;
-            if (second) ld16(from + col + 16, y);
-            use(x, col);
-            if (!second) break;
-            wait16(y);
-            if (col + 32 < n) ld16(from + col + 32, x);
-            use(y, col + 16);
+          auto add = [&]<bool ALL>() {
+            uint32_t x[16], y[16];
+            ld16(from, x);
             wait16(x);
-          }
+            for (int col = 0; col < n; col += 32) {
+              const bool second = col + 16 < n;
+              if (second) ld16(from + col + 16, y);
+              use.template operator()<ALL>(x, col);
+              if (!second) break;
+              wait16(y);
+              if (col + 32 < n) ld16(from + col + 32, x);
+              use.template operator()<ALL>(y, col + 16);
+              wait16(x);
+            }
+          };
+          if (all)
+            add.template operator()<true>();
+          else
+            add.template operator()<false>();
           fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.s_empty[buf]);
@@ -425,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = row + 2 * i * kTile;
-        if (r < k.len && row_at(a, k, r) >= 0) out[r] = old[i] + sum[i];
+        if (there[i]) out[r] = old[i] + sum[i];
       }
     }
   }
@@ -451,7 +480,7 @@ cudaError_t map_layers(CUtensorMap* m, const CacheDev& c, int box) {
 }  // namespace
 
 cudaError_t launch_weigh_tc(const WeighArgs& a, cudaStream_t stream) {
-  cudaError_t e = allow_shared(weigh_tc_kernel, kSchedule + sizeof(long long) * (kMaxSeqs + 1));
+  cudaError_t e = allow_shared(weigh_tc_kernel, kSchedule + TcSchedule::bytes(kMaxSeqs));
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   e = map_layers(&map, a.c, a.c.P < kTile ? a.c.P : kTile);
@@ -459,7 +488,7 @@ cudaError_t launch_weigh_tc(const WeighArgs& a, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(152);  // one block an SM
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSchedule + sizeof(long long) * (a.B + 1);
+  cfg.dynamicSmemBytes = kSchedule + TcSchedule::bytes(a.B);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
