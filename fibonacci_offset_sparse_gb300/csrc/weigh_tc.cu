@@ -4,14 +4,13 @@
 // A tile is 128 rows of K, as TMA leaves them (K-major, 128-byte swizzle), times up to 128 query rows of the split query, all three parts
 // added up into one accumulator of tensor memory: S [128 rows x queries].  There a thread has a row, so its sum is a loop over its columns:
 //   one load from tensor memory, one add (a pair at a time), one exp2, one add; no shuffle.
-// A task is up to four tiles of a sequence, layer and head, which stay in shared memory while its queries pass by 128 at a time
+// A task is up to four tiles of a sequence, layer and head, which stay in shared memory while its queries pass by 64 at a time
 // (of those that see the tile); blocks take tasks as they come, so that those of prompts, which cost from 4 products to hundreds, fill all
 // SMs.  A row's sum is one thread's, in the order of the queries, whichever block it is.
 //
-// What bounds it: few query rows the read of K, many the products (three parts) and exp2.  128 columns, as products of 64 take
-// as long to read their operands from shared memory as those of 128.
+// What bounds it: few query rows the read of K, many the products (three parts) and exp2.
 //
-// Block: 8 warps that sum (four to the even tiles, four to the odd ones), the feeder, and a warp whose one lane issues the products.
+// Block: 16 warps that sum (four a tile of the task), the feeder, and a warp whose one lane issues the products.
 #include "tcgen05.cuh"
 #include "tree_dense.cuh"
 #include "weigh.cuh"
@@ -21,12 +20,18 @@ namespace fibattn {
 namespace {
 
 constexpr int kTile = 128, kTiles = 4, kGroupRows = kTile * kTiles;  // rows of a task
-constexpr int kCols = 128;                                            // query rows of a product
+constexpr int kCols = 64;                                             // query rows of a product
 constexpr int kTileBytes = kTile * kD * 2, kSlots = 6;
-constexpr int kQueryBytes = kCols / 8 * kGroupBytes, kQuerySlot = kQueryBytes + kCols * 4 + 512;  // and their references; a multiple of 1024
-constexpr int kBuffers = 4;                                           // of tensor memory, kCols columns each
-constexpr int kSumWarps = 8, kFeeder = 8, kIssuer = 9, kThreads = 320;
-constexpr int kQueries = kSlots * kTileBytes, kSchedule = kQueries + 2 * kQuerySlot;
+// Slots of queries: one is free again when its products are done and its references read, so it is for some 2.5 us, of which
+// the products of 128 columns took 1.6: with two slots of 128 columns prompts of 2048 took 61 us, a window of 32 tokens 85.
+constexpr int kQuerySlots = 4;
+constexpr int kQueryBytes = kCols / 8 * kGroupBytes, kQuerySlot = kQueryBytes + 1024;  // and their references; a multiple of 1024
+// Buffers of tensor memory, kCols columns each: two a tile of the task, so that a barrier is waited for by the four warps of one tile
+// alone, one round after the other.  (Its parity cannot tell a warp that is a round ahead from one that is not.)
+constexpr int kBuffers = 2 * kTiles;
+constexpr int kShort = 4;                                             // chunks of a task that is short
+constexpr int kSumWarps = 4 * kTiles, kFeeder = kSumWarps, kIssuer = kSumWarps + 1, kThreads = 32 * (kSumWarps + 2);
+constexpr int kQueries = kSlots * kTileBytes, kSchedule = kQueries + kQuerySlots * kQuerySlot;
 static_assert(kQuerySlot % 1024 == 0 && kBuffers * kCols == 512, "layout");
 
 struct TcTask {
@@ -39,7 +44,7 @@ struct TcTask {
 
 struct TcBars {
   uint64_t k_full[kSlots], k_empty[kSlots];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full[kQuerySlots], q_empty[kQuerySlots];
   uint64_t s_full[kBuffers], s_empty[kBuffers];
   uint64_t t_full[2], t_empty[2];
   uint64_t drained;
@@ -79,7 +84,8 @@ __device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& 
   const WeighSeq s = sch.seq[lo];
   const int per = a.c.L * a.c.H;
   const long long off = u - start[lo];
-  const int j = static_cast<int>(off / per), lh = static_cast<int>(off - static_cast<long long>(j) * per);
+  const int j = off < 1LL << 31 ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(per)) : static_cast<int>(off / per);
+  const int lh = static_cast<int>(off - static_cast<long long>(j) * per);
   k.b = lo;
   k.l = lh / a.c.H;
   k.h = lh - k.l * a.c.H;
@@ -161,9 +167,11 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       mbar_init(&bars.k_full[s], 1);
       mbar_init(&bars.k_empty[s], 1);
     }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < kQuerySlots; ++s) {
       mbar_init(&bars.q_full[s], 1);
       mbar_init(&bars.q_empty[s], 1 + kSumWarps);
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.t_full[s], 1);
       mbar_init(&bars.t_empty[s], 1 + kSumWarps);
     }
@@ -233,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       if (now.tiles == 0) break;
       const size_t task = (static_cast<size_t>(now.l) * a.B + now.b) * c.H + now.h;
       const int c0 = first_chunk(a, now, now.r0), c1 = chunks(now);
-      const bool is_short = c1 - c0 == 1;
+      const bool is_short = c1 - c0 <= kShort;
       auto look_ahead = [&] {
         if (!taken) id = fetch();
         next = known(id);
@@ -248,8 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         }
       }
       for (int ch = c0; ch < c1 && !stop; ++ch, ++qc) {
-        const int slot = qc & 1, n = columns(now, ch);
-        if (!warp_wait(&bars.q_empty[slot], ((qc >> 1) & 1) ^ 1, a.wait_ns, &s_err)) {
+        const int slot = qc % kQuerySlots, n = columns(now, ch);
+        if (!warp_wait(&bars.q_empty[slot], ((qc / kQuerySlots) & 1) ^ 1, a.wait_ns, &s_err)) {
           stop = true;
           break;
         }
@@ -298,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     if (lane == 0) {
       for (int x = max(0, kc - kSlots); x < kc; ++x)
         if (!(left_out >> (x % kSlots) & 1)) mbar_wait(&bars.k_full[x % kSlots], (x / kSlots) & 1, kDrainNs);
-      for (int x = max(0, qc - 2); x < qc; ++x) mbar_wait(&bars.q_full[x & 1], (x >> 1) & 1, kDrainNs);
+      for (int x = max(0, qc - kQuerySlots); x < qc; ++x) mbar_wait(&bars.q_full[x % kQuerySlots], (x / kQuerySlots) & 1, kDrainNs);
     }
     __syncwarp();
   } else if (warp == kIssuer) {
@@ -311,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         atomicExch(a.status, kStatusTimeout);
         return false;
       };
-      int tc = 0, kc = 0, qc = 0, item = 0;
+      int tc = 0, kc = 0, qc = 0, done[kTiles] = {};  // done: products for each tile of the tasks
       bool go = true;
       while (go && wait(&bars.t_full[tc & 1], (tc >> 1) & 1)) {
         const TcTask k = bars.task[tc & 1];
@@ -322,31 +330,35 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         const int c0 = first_chunk(a, k, k.r0), c1 = chunks(k);
         int seen = 0;  // tiles whose copy has been waited for
         for (int ch = c0; ch < c1 && go; ++ch, ++qc) {
-          go = wait(&bars.q_full[qc & 1], (qc >> 1) & 1);
+          go = wait(&bars.q_full[qc % kQuerySlots], (qc / kQuerySlots) & 1);
           if (!go) break;
-          const uint32_t q = base + kQueries + (qc & 1) * kQuerySlot, desc = product_of(kTile, columns(k, ch), false, false);
-          for (int t = 0; t < k.tiles; ++t) {
-            if (first_chunk(a, k, k.r0 + t * kTile) > ch) break;  // (nor do later tiles' rows have one that sees them)
-            const int ks = (kc + t) % kSlots, buf = item % kBuffers;
+          // descriptors' addresses count 16 bytes: 32 bytes on a k step, a part's 1024 on a part
+          const uint64_t q = matrix_at(base + kQueries + qc % kQuerySlots * kQuerySlot, 16, kGroupBytes, 2);
+          const uint32_t desc = product_of(kTile, columns(k, ch), false, false);
+#pragma unroll
+          for (int t = 0; t < kTiles; ++t) {
+            // (nor do later tiles' rows have a query that sees them)
+            if (!go || t >= k.tiles || first_chunk(a, k, k.r0 + t * kTile) > ch) break;
+            const int ks = (kc + t) % kSlots, buf = 2 * t + (done[t] & 1);
             if (t >= seen) {
               go = wait(&bars.k_full[ks], ((kc + t) / kSlots) & 1);
               if (!go) break;
               seen = t + 1;
             }
-            go = wait(&bars.s_empty[buf], ((item / kBuffers) & 1) ^ 1);
+            go = wait(&bars.s_empty[buf], ((done[t] >> 1) & 1) ^ 1);
             if (!go) break;
             fence_after();
-            const uint32_t from = base + ks * kTileBytes, d = tmem + buf * kCols;
+            const uint64_t rows = matrix_at(base + ks * kTileBytes, 16, 1024, 2);
+            const uint32_t d = tmem + buf * kCols;
 #pragma unroll
             for (int part = 2; part >= 0; --part)
 #pragma unroll
-              for (int x = 0; x < 4; ++x)
-                mma_tc(d, matrix_at(from + 32 * x, 16, 1024, 2), matrix_at(q + part * kPartBytes + 32 * x, 16, kGroupBytes, 2), desc, part < 2 || x > 0);
+              for (int x = 0; x < 4; ++x) mma_tc(d, rows + 2 * x, q + part * (kPartBytes / 16) + 2 * x, desc, part < 2 || x > 0);
             commit_tc(&bars.s_full[buf]);
             if (ch == c1 - 1) commit_tc(&bars.k_empty[ks]);
-            ++item;
+            ++done[t];
           }
-          if (go) commit_tc(&bars.q_empty[qc & 1]);
+          if (go) commit_tc(&bars.q_empty[qc % kQuerySlots]);
         }
         kc += k.tiles;
       }
@@ -356,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     __syncwarp();
   } else {
     // =================================================================== sums
-    const int set = warp >> 2, wq = warp & 3;
+    const int mine = warp >> 2, wq = warp & 3;  // the warp's tile of a task, and its 32 rows of that
     const uint32_t lanes = static_cast<uint32_t>(wq) << 21;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (warp_wait(bar, parity, a.wait_ns, &s_err)) return true;
@@ -364,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       if (lane == 0) atomicExch(a.status, kStatusTimeout);
       return false;
     };
-    int tc = 0, qc = 0, item = 0;
+    int tc = 0, qc = 0, done = 0;
     bool go = true;
     while (go && wait(&bars.t_full[tc & 1], (tc >> 1) & 1)) {
       const TcTask k = bars.task[tc & 1];
@@ -374,33 +386,24 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       ++tc;
       if (k.tiles == 0) break;
       float* out = a.weights + ((static_cast<size_t>(k.l) * c.S + k.b) * c.H + k.h) * a.rows;
-      const int row = k.r0 + set * kTile + wq * 32 + lane;  // the thread's rows: this one, and two tiles on
-      float sum[2] = {0.f, 0.f}, old[2];
-      bool there[2];  // (read here, so that nothing is waited for at the end)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = row + 2 * i * kTile;
-        old[i] = r < k.first && r < k.len ? out[r] : 0.f;
-        there[i] = r < k.len && row_at(a, k, r) >= 0;
-      }
+      const int r = k.r0 + mine * kTile + wq * 32 + lane;  // the thread's row
+      float sum = 0.f;
+      const float old = r < k.first && r < k.len ? out[r] : 0.f;
+      const int page = r < k.len ? __ldg(c.table + static_cast<size_t>(k.b) * c.max_pages + (r >> c.shift)) : -1;  // (looked at in the end)
       const int c0 = first_chunk(a, k, k.r0), c1 = chunks(k);
       for (int ch = c0; ch < c1 && go; ++ch, ++qc) {
         const int n = columns(k, ch), m0 = ch * kCols;
-        const float* ref = reinterpret_cast<const float*>(smem + kQueries + (qc & 1) * kQuerySlot + kQueryBytes);
-        go = wait(&bars.q_full[qc & 1], (qc >> 1) & 1);
+        const float* ref = reinterpret_cast<const float*>(smem + kQueries + qc % kQuerySlots * kQuerySlot + kQueryBytes);
+        go = wait(&bars.q_full[qc % kQuerySlots], (qc / kQuerySlots) & 1);
         if (!go) break;
-#pragma unroll
-        for (int t = 0; t < kTiles; ++t) {
-          if (t >= k.tiles || first_chunk(a, k, k.r0 + t * kTile) > ch) break;
-          const int at = item++;
-          if ((t & 1) != set) continue;
-          const int buf = at % kBuffers;
-          go = go && wait(&bars.s_full[buf], (at / kBuffers) & 1);
+        if (mine < k.tiles && first_chunk(a, k, k.r0 + mine * kTile) <= ch) {  // some of these queries see rows of the tile
+          const int buf = 2 * mine + (done & 1);
+          go = wait(&bars.s_full[buf], (done >> 1) & 1);
+          ++done;
           if (!go) break;
           fence_after();
-          const int r = row + (t - set) * kTile;
           // whether every column is a query row that sees all rows of the tile
-          const bool all = m0 + n <= k.used && k.before + m0 / a.G >= k.r0 + (t + 1) * kTile - 1;
+          const bool all = m0 + n <= k.used && k.before + m0 / a.G >= k.r0 + (mine + 1) * kTile - 1;
           const int lo = max(0, r - k.before) * a.G - m0, hi = k.used - m0;  // the columns that see row r
           float s[4] = {0.f, 0.f, 0.f, 0.f};
           auto use = [&]<bool ALL>(const uint32_t (&x)[16], int col) {
@@ -444,18 +447,14 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           if (lane == 0) mbar_arrive(&bars.s_empty[buf]);
           float part = (s[0] + s[1]) + (s[2] + s[3]);
           if (isnan(part) && r < k.len) part = add_infinite(a, k, r, max(m0, m0 + lo), min(m0 + n, k.used));
-          sum[t >> 1] += part;
+          sum += part;
         }
         __threadfence_block();  // the references have been read
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.q_empty[qc & 1]);
+        if (lane == 0) mbar_arrive(&bars.q_empty[qc % kQuerySlots]);
       }
       if (!go) break;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = row + 2 * i * kTile;
-        if (there[i]) out[r] = old[i] + sum[i];
-      }
+      if (page >= 0 && page < c.n_pages) out[r] = old + sum;
     }
   }
   fence_before();
