@@ -5,12 +5,18 @@
 // added up into one accumulator of tensor memory: S [128 rows x queries].  There a thread has a row, so its sum is a loop over its columns:
 //   one load from tensor memory, one add (a pair at a time), one exp2, one add; no shuffle.
 // A task is up to four tiles of a sequence, layer and head, which stay in shared memory while its queries pass by 64 at a time
-// (of those that see the tile); blocks take tasks as they come, so that those of prompts, which cost from 4 products to hundreds, fill all
-// SMs.  A row's sum is one thread's, in the order of the queries, whichever block it is.
+// (of those that see the tile), or, where there are 64 at most, eight tiles that pass by the queries.  Blocks take tasks as they
+// come, so that those of prompts, which cost from 4 products to hundreds, fill all SMs.  A row's sum is one thread's, in the order of the
+// queries, whichever block it is.
 //
 // What bounds it: few query rows the read of K, many the products (three parts) and exp2.
 //
-// Block: 16 warps that sum (four a tile of the task), the feeder, and a warp whose one lane issues the products.
+// Block: 16 warps that sum (four a tile), and one warp each for the tasks, the queries, the copies of each of the four tiles and the
+// products of each.  A warp's step (a wait, a few addresses, a copy) takes 500 to 1000 cycles and the twelve products of a tile 900,
+// whatever their columns, as much as a tile may take: with one warp for tasks, queries and copies and one for products a window of 32
+// tokens took 85 us, whatever else was changed, with warps of their own for the copies 73.
+#include <climits>
+
 #include "tcgen05.cuh"
 #include "tree_dense.cuh"
 #include "weigh.cuh"
@@ -19,18 +25,18 @@ namespace fibattn {
 
 namespace {
 
-constexpr int kTile = 128, kTiles = 4, kGroupRows = kTile * kTiles;  // rows of a task
+constexpr int kTile = 128, kTiles = 4, kGroupRows = kTile * kTiles;  // rows of a round
+constexpr int kRounds = 2;                                            // of a task with no more than kCols query rows; else 1
 constexpr int kCols = 64;                                             // query rows of a product
-constexpr int kTileBytes = kTile * kD * 2, kSlots = 6;
-// Slots of queries: one is free again when its products are done and its references read, so it is for some 2.5 us, of which
-// the products of 128 columns took 1.6: with two slots of 128 columns prompts of 2048 took 61 us, a window of 32 tokens 85.
-constexpr int kQuerySlots = 4;
+constexpr int kTileBytes = kTile * kD * 2, kSlots = 2 * kTiles;       // two a tile of the round
+// Slots of queries: one is free again when its products are done and its references read, some 2.5 us after its copy began.
+constexpr int kQuerySlots = 3;
 constexpr int kQueryBytes = kCols / 8 * kGroupBytes, kQuerySlot = kQueryBytes + 1024;  // and their references; a multiple of 1024
-// Buffers of tensor memory, kCols columns each: two a tile of the task, so that a barrier is waited for by the four warps of one tile
+// Buffers of tensor memory, kCols columns each: two a tile of the round, so that a barrier is waited for by the four warps of one tile
 // alone, one round after the other.  (Its parity cannot tell a warp that is a round ahead from one that is not.)
 constexpr int kBuffers = 2 * kTiles;
-constexpr int kShort = 4;                                             // chunks of a task that is short
-constexpr int kSumWarps = 4 * kTiles, kFeeder = kSumWarps, kIssuer = kSumWarps + 1, kThreads = 32 * (kSumWarps + 2);
+constexpr int kSumWarps = 4 * kTiles, kIssuer = kSumWarps, kFeedK = kIssuer + kTiles, kTasks = kFeedK + kTiles, kFeedQ = kTasks + 1;
+constexpr int kThreads = 32 * (kFeedQ + 1);
 constexpr int kQueries = kSlots * kTileBytes, kSchedule = kQueries + kQuerySlots * kQuerySlot;
 static_assert(kQuerySlot % 1024 == 0 && kBuffers * kCols == 512, "layout");
 
@@ -38,8 +44,7 @@ struct TcTask {
   int b, l, h;
   int len, before, used;  // rows; query row m sees rows up to before + m / G; query rows
   int first;
-  int r0, tiles;          // tiles 0: there is none any more
-  int pad;
+  int r0, rounds;         // rounds 0: there is none any more
 };
 
 struct TcBars {
@@ -53,6 +58,8 @@ struct TcBars {
   int err;
 };
 
+// Rows of a task of a sequence with `used` query rows.
+__device__ __forceinline__ int task_rows(int used) { return used <= kCols ? kRounds * kGroupRows : kGroupRows; }
 // The chunk of queries from which on some of them see row r, of a task.
 __device__ __forceinline__ int first_chunk(const WeighArgs& a, const TcTask& k, int r) { return max(0, r - k.before) * a.G / kCols; }
 __device__ __forceinline__ int chunks(const TcTask& k) { return (k.used + kCols - 1) / kCols; }
@@ -67,7 +74,7 @@ struct TcSchedule {
   static size_t bytes(int B) { return sizeof(long long) * (B + 1) + sizeof(WeighSeq) * B; }
 };
 
-// Task `id` of the call, if there is one (tiles > 0): sequences in order, of each the first rows of all layers and heads before the next.
+// Task `id` of the call, if there is one (rounds > 0): sequences in order, of each the first rows of all layers and heads before the next.
 __device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& sch, unsigned long long id) {
   TcTask k = {};
   const long long* start = sch.start;
@@ -93,8 +100,9 @@ __device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& 
   k.before = s.len - s.n;
   k.used = s.n * a.G;
   k.first = s.first;
-  k.r0 = j * kGroupRows;
-  k.tiles = min(kTiles, (s.len - k.r0 + kTile - 1) / kTile);
+  const int rows = task_rows(k.used);
+  k.r0 = j * rows;
+  k.rounds = (min(rows, s.len - k.r0) + kGroupRows - 1) / kGroupRows;
   return k;
 }
 
@@ -169,24 +177,25 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     }
     for (int s = 0; s < kQuerySlots; ++s) {
       mbar_init(&bars.q_full[s], 1);
-      mbar_init(&bars.q_empty[s], 1 + kSumWarps);
+      mbar_init(&bars.q_empty[s], kTiles + kSumWarps);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.t_full[s], 1);
-      mbar_init(&bars.t_empty[s], 1 + kSumWarps);
+      mbar_init(&bars.t_empty[s], 1 + 2 * kTiles + kSumWarps);
     }
     for (int s = 0; s < kBuffers; ++s) {
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.s_empty[s], 4);
     }
-    mbar_init(&bars.drained, 1);
+    mbar_init(&bars.drained, kTiles);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
   for (int b = tid; b < a.B; b += kThreads) {
     bool ok;
     const WeighSeq s = weigh_seq(a, b, &ok);
+    const int rows = task_rows(s.n * a.G);
     sch.seq[b] = s;
-    start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + kGroupRows - 1) / kGroupRows) * c.L * c.H;
+    start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + rows - 1) / rows) * c.L * c.H;
   }
   __syncthreads();
   if (warp == 0) {
@@ -209,208 +218,206 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   fence_before();
   __syncthreads();
   fence_after();
-  const uint32_t tmem = bars.tmem, base = smem_addr(smem);
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), base = smem_addr(smem);
   wait_for_first();
 
-  if (warp == kFeeder) {
-    // =================================================================== feeder
-    const int box = min(kTile, c.P);  // rows a copy
-    // A task's number, in lane 0, and not waited for before it is used.  Taken early where tasks are short; where they are long
-    // late, as one that waits for its block waits for nothing else.
-    auto fetch = [&] { return lane == 0 ? atomicAdd(a.next, 1ull) : 0ull; };
-    auto known = [&](unsigned long long id) { return task_at(a, sch, __shfl_sync(0xffffffffu, id, 0)); };
-    auto page_of = [&](const TcTask& k) {  // of the lane-th page of the task's rows
-      const int at = (k.r0 >> c.shift) + lane;
-      return k.tiles > 0 && at < c.max_pages ? __ldg(c.table + static_cast<size_t>(k.b) * c.max_pages + at) : -1;
-    };
-    unsigned long long id = fetch();
-    TcTask now = known(id), next = {};
-    int page = page_of(now), next_page = 0;
-    bool taken = false;  // id is the number of the task after the next that is known
-    int tc = 0, kc = 0, qc = 0;
-    uint32_t left_out = 0;  // slots that the test hook never fills
-    bool stop = false;
-    while (!stop) {
-      if (!warp_wait(&bars.t_empty[tc & 1], ((tc >> 1) & 1) ^ 1, a.wait_ns, &s_err)) break;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (warp_wait(bar, parity, a.wait_ns, &s_err)) return true;
+    s_err = 1;
+    if (lane == 0) atomicExch(a.status, kStatusTimeout);
+    return false;
+  };
+  // Task number tc of the block, and that this warp has read it (a warp that is done with it only later says so itself).
+  auto read = [&](int tc, TcTask* k) {
+    if (!wait(&bars.t_full[tc & 1], (tc >> 1) & 1)) return false;
+    *k = bars.task[tc & 1];
+    return k->rounds > 0;
+  };
+  auto release = [&](int tc) {
+    __threadfence_block();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars.t_empty[tc & 1]);
+  };
+
+  if (warp == kTasks) {
+    // =================================================================== tasks
+    for (int tc = 0; wait(&bars.t_empty[tc & 1], ((tc >> 1) & 1) ^ 1); ++tc) {
+      unsigned long long id = lane == 0 ? atomicAdd(a.next, 1ull) : 0;
+      const TcTask k = task_at(a, sch, __shfl_sync(0xffffffffu, id, 0));
       if (lane == 0) {
-        bars.task[tc & 1] = now;
+        bars.task[tc & 1] = k;
         mbar_arrive(&bars.t_full[tc & 1]);
       }
       __syncwarp();
-      ++tc;
-      if (now.tiles == 0) break;
-      const size_t task = (static_cast<size_t>(now.l) * a.B + now.b) * c.H + now.h;
-      const int c0 = first_chunk(a, now, now.r0), c1 = chunks(now);
-      const bool is_short = c1 - c0 <= kShort;
-      auto look_ahead = [&] {
-        if (!taken) id = fetch();
-        next = known(id);
-        next_page = page_of(next);
-        taken = false;
-      };
-      if (is_short) {  // the next one's pages, and the number of the one behind it, come while this one's copies wait for their slots
-        look_ahead();
-        if (next.tiles > 0) {
-          id = fetch();
-          taken = true;
-        }
-      }
-      for (int ch = c0; ch < c1 && !stop; ++ch, ++qc) {
-        const int slot = qc % kQuerySlots, n = columns(now, ch);
-        if (!warp_wait(&bars.q_empty[slot], ((qc / kQuerySlots) & 1) ^ 1, a.wait_ns, &s_err)) {
-          stop = true;
-          break;
-        }
+      if (k.rounds == 0) break;
+      // A long task is taken alone, till the last of its queries is under way: one that waits for its block waits for nothing else.
+      if (k.used > kCols && !wait(&bars.t_empty[tc & 1], (tc >> 1) & 1)) break;
+    }
+  } else if (warp == kFeedQ) {
+    // =================================================================== copies of queries
+    int n = 0;
+    bool go = true;
+    TcTask k;
+    for (int tc = 0; go && read(tc, &k); ++tc) {
+      const size_t m = ((static_cast<size_t>(k.l) * a.B + k.b) * c.H + k.h) * a.mpad;
+      const int c1 = chunks(k);
+      for (int ch = first_chunk(a, k, k.r0); ch < c1; ++ch, ++n) {
+        const int slot = n % kQuerySlots, cols = columns(k, ch);
+        go = wait(&bars.q_empty[slot], ((n / kQuerySlots) & 1) ^ 1);
+        if (!go) break;
         if (lane == 0) {
           unsigned char* to = smem + kQueries + slot * kQuerySlot;
-          const size_t m = task * a.mpad + static_cast<size_t>(ch) * kCols;
-          mbar_arrive_tx(&bars.q_full[slot], n / 8 * kGroupBytes + n * 4);
-          bulk_g2s(to, a.parts + m / 8 * kGroupBytes, n / 8 * kGroupBytes, &bars.q_full[slot]);
-          bulk_g2s(to + kQueryBytes, a.refs + m, n * 4, &bars.q_full[slot]);
+          const size_t at = m + static_cast<size_t>(ch) * kCols;
+          mbar_arrive_tx(&bars.q_full[slot], cols / 8 * kGroupBytes + cols * 4);
+          bulk_g2s(to, a.parts + at / 8 * kGroupBytes, cols / 8 * kGroupBytes, &bars.q_full[slot]);
+          bulk_g2s(to + kQueryBytes, a.refs + at, cols * 4, &bars.q_full[slot]);
         }
         __syncwarp();
-        if (ch != c0) continue;
-        for (int t = 0; t < now.tiles; ++t, ++kc) {
-          const int ks = kc % kSlots, rows = min(kTile, now.len - now.r0 - t * kTile), boxes = (rows + box - 1) / box;
-          if (!warp_wait(&bars.k_empty[ks], ((kc / kSlots) & 1) ^ 1, a.wait_ns, &s_err)) {
-            stop = true;
-            break;
-          }
-          // lane x copies box x: page (tile's first row + x box) / P of the task
-          const int first = t * kTile + lane * box, id = __shfl_sync(0xffffffffu, page, (first >> c.shift) & 31);
-          if (a.skip_copy && t == 0) {
-            left_out |= 1u << ks;
-            continue;
-          }
-          left_out &= ~(1u << ks);
-          if (lane == 0) mbar_arrive_tx(&bars.k_full[ks], boxes * box * kD * 2);
-          __syncwarp();
-          if (lane < boxes) {
-            const bool ok = id >= 0 && id < c.n_pages;
-            if (!ok) atomicExch(a.status, kStatusDeviceAssert);
-            tma_3d(base + ks * kTileBytes + lane * box * 128, &map_k, 0, (((ok ? id : 0) * c.H + now.h) << c.shift) + (first & (c.P - 1)), now.l,
-                   &bars.k_full[ks]);
-          }
-          __syncwarp();
-        }
       }
-      if (!is_short && !stop) look_ahead();
-      now = next;
-      page = next_page;
-    }
-    if (s_err || stop) {
-      s_err = 1;
-      if (lane == 0) atomicExch(a.status, kStatusTimeout);
+      release(tc);
     }
     // nothing may be in flight when the block ends
-    if (lane == 0) {
-      for (int x = max(0, kc - kSlots); x < kc; ++x)
-        if (!(left_out >> (x % kSlots) & 1)) mbar_wait(&bars.k_full[x % kSlots], (x / kSlots) & 1, kDrainNs);
-      for (int x = max(0, qc - kQuerySlots); x < qc; ++x) mbar_wait(&bars.q_full[x % kQuerySlots], (x / kQuerySlots) & 1, kDrainNs);
-    }
+    if (lane == 0)
+      for (int x = max(0, n - kQuerySlots); x < n; ++x) mbar_wait(&bars.q_full[x % kQuerySlots], (x / kQuerySlots) & 1, kDrainNs);
     __syncwarp();
-  } else if (warp == kIssuer) {
-    // =================================================================== products
-    if (one_lane()) {
-      auto wait = [&](uint64_t* bar, uint32_t parity) {
-        if (s_err) return false;
-        if (mbar_wait(bar, parity, a.wait_ns)) return true;
-        s_err = 1;
-        atomicExch(a.status, kStatusTimeout);
-        return false;
-      };
-      int tc = 0, kc = 0, qc = 0, done[kTiles] = {};  // done: products for each tile of the tasks
-      bool go = true;
-      while (go && wait(&bars.t_full[tc & 1], (tc >> 1) & 1)) {
-        const TcTask k = bars.task[tc & 1];
-        __threadfence_block();
-        mbar_arrive(&bars.t_empty[tc & 1]);
-        ++tc;
-        if (k.tiles == 0) break;
-        const int c0 = first_chunk(a, k, k.r0), c1 = chunks(k);
-        int seen = 0;  // tiles whose copy has been waited for
-        for (int ch = c0; ch < c1 && go; ++ch, ++qc) {
-          go = wait(&bars.q_full[qc % kQuerySlots], (qc / kQuerySlots) & 1);
-          if (!go) break;
-          // descriptors' addresses count 16 bytes: 32 bytes on a k step, a part's 1024 on a part
-          const uint64_t q = matrix_at(base + kQueries + qc % kQuerySlots * kQuerySlot, 16, kGroupBytes, 2);
-          const uint32_t desc = product_of(kTile, columns(k, ch), false, false);
+  } else if (warp >= kFeedK && warp < kFeedK + kTiles) {
+    // =================================================================== copies of rows: tile t of each round
+    const int t = warp - kFeedK, box = min(kTile, c.P);  // rows a copy
+    int n = 0;
+    bool go = true, left_out[2] = {false, false};        // slots that the test hook does not fill
+    TcTask k;
+    for (int tc = 0; go && read(tc, &k); ++tc) {
+      release(tc);
+      for (int x = 0; x < k.rounds; ++x) {
+        const int r0 = k.r0 + x * kGroupRows + t * kTile;
+        if (r0 >= k.len) break;
+        const int boxes = (min(kTile, k.len - r0) + box - 1) / box, s = n & 1, slot = 2 * t + s;
+        // lane i copies box i
+        const int r = r0 + lane * box;
+        int id = lane < boxes ? __ldg(c.table + static_cast<size_t>(k.b) * c.max_pages + (r >> c.shift)) : 0;
+        if (id < 0 || id >= c.n_pages) {
+          atomicExch(a.status, kStatusDeviceAssert);
+          id = 0;
+        }
+        go = wait(&bars.k_empty[slot], ((n >> 1) & 1) ^ 1);
+        if (!go) break;
+        ++n;
+        left_out[s] = a.skip_copy && x == 0 && t == 0;
+        if (left_out[s]) continue;
+        if (lane == 0) mbar_arrive_tx(&bars.k_full[slot], boxes * box * kD * 2);
+        __syncwarp();
+        if (lane < boxes)
+          tma_3d(base + slot * kTileBytes + lane * box * 128, &map_k, 0, ((id * c.H + k.h) << c.shift) + (r & (c.P - 1)), k.l, &bars.k_full[slot]);
+        __syncwarp();
+      }
+    }
+    if (lane == 0)
+      for (int x = max(0, n - 2); x < n; ++x)
+        if (!left_out[x & 1]) mbar_wait(&bars.k_full[2 * t + (x & 1)], (x >> 1) & 1, kDrainNs);
+    __syncwarp();
+  } else if (warp >= kIssuer && warp < kIssuer + kTiles) {
+    // =================================================================== products of tile t of each round
+    // The warp goes as one and its values are the same in all lanes (shuffled, so that the compiler can tell); one lane issues.
+    auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
+    // Descriptors count 16 bytes: 32 bytes on a k step, a part's 1024 on a part.
+    constexpr uint32_t kLead = 16 / 16 << 16, kRowsHigh = 1024 / 16 | 1u << 14 | 2u << 29, kQueryHigh = kGroupBytes / 16 | 1u << 14 | 2u << 29;
+    auto at = [](uint32_t high, uint32_t low) { return static_cast<uint64_t>(high) << 32 | low; };
+    const int t = same(warp - kIssuer);
+    const uint32_t rows0 = (base + 2 * t * kTileBytes) >> 4 | kLead, query0 = (base + kQueries) >> 4 | kLead, out0 = tmem + 2 * t * kCols;
+    int qs = 0, q_round = 0, filled = 0, done = 0;  // tiles copied, products made
+    bool go = true;
+    TcTask k;
+    for (int tc = 0; go && read(tc, &k); ++tc) {
+      const int c0 = same(first_chunk(a, k, k.r0)), c1 = same(chunks(k)), last = same(columns(k, chunks(k) - 1));
+      int from[kRounds];  // the first chunk that sees rows of the tile
 #pragma unroll
-          for (int t = 0; t < kTiles; ++t) {
-            // (nor do later tiles' rows have a query that sees them)
-            if (!go || t >= k.tiles || first_chunk(a, k, k.r0 + t * kTile) > ch) break;
-            const int ks = (kc + t) % kSlots, buf = 2 * t + (done[t] & 1);
-            if (t >= seen) {
-              go = wait(&bars.k_full[ks], ((kc + t) / kSlots) & 1);
-              if (!go) break;
-              seen = t + 1;
-            }
-            go = wait(&bars.s_empty[buf], ((done[t] >> 1) & 1) ^ 1);
-            if (!go) break;
-            fence_after();
-            const uint64_t rows = matrix_at(base + ks * kTileBytes, 16, 1024, 2);
-            const uint32_t d = tmem + buf * kCols;
+      for (int x = 0; x < kRounds; ++x) {
+        const int r = k.r0 + x * kGroupRows + t * kTile;
+        from[x] = same(x < k.rounds && r < k.len ? first_chunk(a, k, r) : INT_MAX);
+      }
+      release(tc);
+      for (int ch = c0; ch < c1 && go; ++ch) {
+        go = wait(&bars.q_full[qs], q_round & 1);
+        if (!go) break;
+        const uint32_t query = query0 + qs * (kQuerySlot / 16), desc = product_of(kTile, ch == c1 - 1 ? last : kCols, false, false);
+#pragma unroll
+        for (int x = 0; x < kRounds; ++x) {
+          if (from[x] > ch) break;
+          // the tile is there from the first chunk that sees it to the last
+          const int slot = filled & 1, buf = done & 1;
+          if (ch == max(from[x], c0)) go = wait(&bars.k_full[2 * t + slot], (filled >> 1) & 1);
+          if (go) go = wait(&bars.s_empty[2 * t + buf], ((done >> 1) & 1) ^ 1);
+          if (!go) break;
+          fence_after();
+          const uint32_t rows = rows0 + slot * (kTileBytes / 16), d = out0 + buf * kCols;
+          if (one_lane()) {
 #pragma unroll
             for (int part = 2; part >= 0; --part)
 #pragma unroll
-              for (int x = 0; x < 4; ++x) mma_tc(d, rows + 2 * x, q + part * (kPartBytes / 16) + 2 * x, desc, part < 2 || x > 0);
-            commit_tc(&bars.s_full[buf]);
-            if (ch == c1 - 1) commit_tc(&bars.k_empty[ks]);
-            ++done[t];
+              for (int y = 0; y < 4; ++y)
+                mma_tc(d, at(kRowsHigh, rows + 2 * y), at(kQueryHigh, query + part * (kPartBytes / 16) + 2 * y), desc, part < 2 || y > 0);
+            commit_tc(&bars.s_full[2 * t + buf]);
+            if (ch == c1 - 1) commit_tc(&bars.k_empty[2 * t + slot]);
           }
-          if (go) commit_tc(&bars.q_empty[qc % kQuerySlots]);
+          ++done;
+          if (ch == c1 - 1) ++filled;
         }
-        kc += k.tiles;
+        if (go && one_lane()) commit_tc(&bars.q_empty[qs]);
+        if (++qs == kQuerySlots) {
+          qs = 0;
+          ++q_round;
+        }
       }
-      commit_tc(&bars.drained);  // nothing may be in flight when the block ends
+    }
+    if (one_lane()) {  // nothing may be in flight when the block ends
+      commit_tc(&bars.drained);
       mbar_wait(&bars.drained, 0, kDrainNs);
     }
     __syncwarp();
   } else {
     // =================================================================== sums
-    const int mine = warp >> 2, wq = warp & 3;  // the warp's tile of a task, and its 32 rows of that
+    const int mine = warp >> 2, wq = warp & 3;  // the warp's tile of a round, and its 32 rows of that
     const uint32_t lanes = static_cast<uint32_t>(wq) << 21;
-    auto wait = [&](uint64_t* bar, uint32_t parity) {
-      if (warp_wait(bar, parity, a.wait_ns, &s_err)) return true;
-      s_err = 1;
-      if (lane == 0) atomicExch(a.status, kStatusTimeout);
-      return false;
-    };
-    int tc = 0, qc = 0, done = 0;
+    int n = 0, done = 0;
     bool go = true;
-    while (go && wait(&bars.t_full[tc & 1], (tc >> 1) & 1)) {
-      const TcTask k = bars.task[tc & 1];
-      __threadfence_block();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.t_empty[tc & 1]);
-      ++tc;
-      if (k.tiles == 0) break;
+    TcTask k;
+    for (int tc = 0; go && read(tc, &k); ++tc) {
+      release(tc);
       float* out = a.weights + ((static_cast<size_t>(k.l) * c.S + k.b) * c.H + k.h) * a.rows;
-      const int r = k.r0 + mine * kTile + wq * 32 + lane;  // the thread's row
-      float sum = 0.f;
-      const float old = r < k.first && r < k.len ? out[r] : 0.f;
-      const int page = r < k.len ? __ldg(c.table + static_cast<size_t>(k.b) * c.max_pages + (r >> c.shift)) : -1;  // (looked at in the end)
-      const int c0 = first_chunk(a, k, k.r0), c1 = chunks(k);
-      for (int ch = c0; ch < c1 && go; ++ch, ++qc) {
-        const int n = columns(k, ch), m0 = ch * kCols;
-        const float* ref = reinterpret_cast<const float*>(smem + kQueries + qc % kQuerySlots * kQuerySlot + kQueryBytes);
-        go = wait(&bars.q_full[qc % kQuerySlots], (qc / kQuerySlots) & 1);
+      const int32_t* table = c.table + static_cast<size_t>(k.b) * c.max_pages;
+      float sum[kRounds], old[kRounds];
+      int page[kRounds];  // (looked at in the end)
+#pragma unroll
+      for (int x = 0; x < kRounds; ++x) {
+        const int r = k.r0 + x * kGroupRows + mine * kTile + wq * 32 + lane;  // the thread's row
+        sum[x] = 0.f;
+        old[x] = x < k.rounds && r < k.first && r < k.len ? out[r] : 0.f;
+        page[x] = x < k.rounds && r < k.len ? __ldg(table + (r >> c.shift)) : -1;
+      }
+      const int c1 = chunks(k);
+      for (int ch = first_chunk(a, k, k.r0); ch < c1 && go; ++ch, ++n) {
+        const int cols = columns(k, ch), m0 = ch * kCols, sees = k.before + m0 / a.G;  // the last row that the first column sees
+        const float* ref = reinterpret_cast<const float*>(smem + kQueries + n % kQuerySlots * kQuerySlot + kQueryBytes);
+        go = wait(&bars.q_full[n % kQuerySlots], (n / kQuerySlots) & 1);
         if (!go) break;
-        if (mine < k.tiles && first_chunk(a, k, k.r0 + mine * kTile) <= ch) {  // some of these queries see rows of the tile
+#pragma unroll
+        for (int x = 0; x < kRounds; ++x) {
+          const int first = k.r0 + x * kGroupRows + mine * kTile, r = first + wq * 32 + lane;
+          if (x >= k.rounds || first >= k.len || first_chunk(a, k, first) > ch) break;  // none of these queries sees the tile
           const int buf = 2 * mine + (done & 1);
           go = wait(&bars.s_full[buf], (done >> 1) & 1);
-          ++done;
           if (!go) break;
+          ++done;
           fence_after();
           // whether every column is a query row that sees all rows of the tile
-          const bool all = m0 + n <= k.used && k.before + m0 / a.G >= k.r0 + (mine + 1) * kTile - 1;
+          const bool all = m0 + cols <= k.used && sees >= first + kTile - 1;
           const int lo = max(0, r - k.before) * a.G - m0, hi = k.used - m0;  // the columns that see row r
           float s[4] = {0.f, 0.f, 0.f, 0.f};
-          auto use = [&]<bool ALL>(const uint32_t (&x)[16], int col) {
+          auto use = [&]<bool ALL>(const uint32_t (&z)[16], int col) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
               const float4 r4 = *reinterpret_cast<const float4*>(ref + col + e);
-              float y[4] = {__uint_as_float(x[e]), __uint_as_float(x[e + 1]), __uint_as_float(x[e + 2]), __uint_as_float(x[e + 3])};
+              float y[4] = {__uint_as_float(z[e]), __uint_as_float(z[e + 1]), __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3])};
               add2(y[0], y[1], r4.x, r4.y);
               add2(y[2], y[3], r4.z, r4.w);
 #pragma unroll
@@ -424,18 +431,18 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           };
           const uint32_t from = tmem + buf * kCols + lanes;
           auto add = [&]<bool ALL>() {
-            uint32_t x[16], y[16];
-            ld16(from, x);
-            wait16(x);
-            for (int col = 0; col < n; col += 32) {
-              const bool second = col + 16 < n;
-              if (second) ld16(from + col + 16, y);
-              use.template operator()<ALL>(x, col);
+            uint32_t y[16], z[16];
+            ld16(from, y);
+            wait16(y);
+            for (int col = 0; col < cols; col += 32) {
+              const bool second = col + 16 < cols;
+              if (second) ld16(from + col + 16, z);
+              use.template operator()<ALL>(y, col);
               if (!second) break;
+              wait16(z);
+              if (col + 32 < cols) ld16(from + col + 32, y);
+              use.template operator()<ALL>(z, col + 16);
               wait16(y);
-              if (col + 32 < n) ld16(from + col + 32, x);
-              use.template operator()<ALL>(y, col + 16);
-              wait16(x);
             }
           };
           if (all)
@@ -446,15 +453,19 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.s_empty[buf]);
           float part = (s[0] + s[1]) + (s[2] + s[3]);
-          if (isnan(part) && r < k.len) part = add_infinite(a, k, r, max(m0, m0 + lo), min(m0 + n, k.used));
-          sum += part;
+          if (isnan(part) && r < k.len) part = add_infinite(a, k, r, max(m0, m0 + lo), min(m0 + cols, k.used));
+          sum[x] += part;
         }
         __threadfence_block();  // the references have been read
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.q_empty[qc % kQuerySlots]);
+        if (lane == 0) mbar_arrive(&bars.q_empty[n % kQuerySlots]);
       }
       if (!go) break;
-      if (page >= 0 && page < c.n_pages) out[r] = old + sum;
+#pragma unroll
+      for (int x = 0; x < kRounds; ++x) {
+        const int r = k.r0 + x * kGroupRows + mine * kTile + wq * 32 + lane;
+        if (page[x] >= 0 && page[x] < c.n_pages) out[r] = old[x] + sum[x];
+      }
     }
   }
   fence_before();
