@@ -261,6 +261,11 @@ int fib_attn_plan_create(fib_attn_plan_t* out, int base_kind, const int32_t* cus
     delete p;
     return FIB_ERR_CUDA;
   }
+  for (int m = 0; m < kFreq; ++m) {
+    const double turn = std::pow(rope_base, -2.0 * m / kD) / (2.0 * 3.14159265358979323846);
+    p->turn[m].x = static_cast<float>(turn);
+    p->turn[m].y = static_cast<float>(turn - static_cast<double>(p->turn[m].x));
+  }
   std::vector<float> lo, hi;
   rope_tables(N_max, rope_base, &lo, &hi);
   cudaError_t e = cudaMalloc(&p->d_lo, lo.size() * sizeof(float));

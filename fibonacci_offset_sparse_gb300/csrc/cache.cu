@@ -480,8 +480,8 @@ cudaError_t launch_cache_commit(const fib_attn_cache& cache, int B, int T, int n
   const dim3 grid(static_cast<unsigned>(B) * cache.n_layers, (cache.heads + heads - 1) / heads,
                   (T + kWriteTokens - 1) / kWriteTokens);
   return cache.dtype == FIB_DTYPE_F32
-             ? launch_second(commit_write_kernel<float>, grid, kWriteThreads, stream, a, heads)
-             : launch_second(commit_write_kernel<__nv_bfloat16>, grid, kWriteThreads, stream, a, heads);
+             ? launch_second(commit_write_kernel<float>, grid, kWriteThreads, 0, stream, a, heads)
+             : launch_second(commit_write_kernel<__nv_bfloat16>, grid, kWriteThreads, 0, stream, a, heads);
 }
 
 cudaError_t launch_cache_fork(const fib_attn_cache& cache, const int32_t* src, void* ws, cudaStream_t stream) {
@@ -511,7 +511,7 @@ cudaError_t launch_cache_fork(const fib_attn_cache& cache, const int32_t* src, v
   fork_count_kernel<<<cache.max_seqs, kForkThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_second(fork_write_kernel, dim3(static_cast<unsigned>(cache.max_seqs)), kForkThreads, stream, a);
+  return launch_second(fork_write_kernel, dim3(static_cast<unsigned>(cache.max_seqs)), kForkThreads, 0, stream, a);
 }
 
 cudaError_t launch_cache_compact(const fib_attn_cache& cache, int32_t* remap, void* ws, cudaStream_t stream) {
@@ -527,7 +527,7 @@ cudaError_t launch_cache_compact(const fib_attn_cache& cache, int32_t* remap, vo
   if (e != cudaSuccess) return e;
   const int row_vecs = kD * (cache.dtype == FIB_DTYPE_F32 ? 4 : 2) / 16;
   const int page_vecs = cache.heads * cache.page_rows * row_vecs;
-  return launch_second(compact_move_kernel, dim3(152 * 8), kMoveThreads, stream, a, page_vecs);
+  return launch_second(compact_move_kernel, dim3(152 * 8), kMoveThreads, 0, stream, a, page_vecs);
 }
 
 }  // namespace fibattn

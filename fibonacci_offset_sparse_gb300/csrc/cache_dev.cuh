@@ -39,12 +39,13 @@ inline CacheDev device_view(const fib_attn_cache& c) {
 __device__ __forceinline__ void wait_for_first() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void let_second_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
-// A kernel as a programmatic dependent of the one before it on the stream.
+// A kernel, with `shared` bytes of dynamic shared memory, as a programmatic dependent of the one before it on the stream.
 template <typename... Params, typename... Args>
-inline cudaError_t launch_second(void (*kernel)(Params...), dim3 grid, int threads, cudaStream_t stream, Args... args) {
+inline cudaError_t launch_second(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t stream, Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = shared;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -2,13 +2,12 @@
 //
 // Of a sequence's rows the first, the last and, of those between, the heaviest stay, for each layer and key head by itself; they move
 // down in order, K turned from its old place to the new one (e^{-i (old - new) theta} a pair; a plan that does not rotate moves
-// it as it is).  Three launches in a chain, each a programmatic dependent of the one before:
-//   plan    one block: what each sequence keeps, the free pages that take the place of shared ones, tables, counts, lengths;
-//   select  a block a sequence, layer and head: the weight of the last row that stays, by three passes over the weights' bits (11, 11,
-//           10), then the list of rows that stay, in order; the weights move here;
-//   move    a block for K and one for V: a row never moves up, so the rows that a step writes were all read in it or before, and one
-//           barrier a step, between its reads and its writes, keeps them apart.  No order of blocks matters.
-// What bounds it: the rows' bytes, read and written once.
+// it as it is).  Two launches, the second a programmatic dependent of the first:
+//   plan   one block: what each sequence keeps, the free pages that take the place of shared ones, tables, counts, lengths;
+//   evict  a block a sequence, layer and head: the weight of the last row that stays, the list of rows that stay, in order, and their
+//          weights; then K and V by that list.  A row never moves up, so the rows that a step writes were all read in it or before, and
+//          one barrier a step, between its reads and its writes, keeps them apart.  No order of blocks matters.
+// What bounds it: the rows' bytes, read and written once; one block's search runs beside the others' moves.
 #include "cache_dev.cuh"
 
 namespace fibattn {
@@ -30,15 +29,18 @@ struct EvictArgs {
   int32_t* dropped;  // [B] or null
   const float2* rope_lo;
   const float2* rope_hi;
+  float2 turn[kFreq];  // theta / 2 pi as a sum of two
   bool turns;
   EvictJob* jobs;
   int32_t* list;   // free pages taken
   int32_t* old;    // [S, max_pages]: the pages that a sequence held; ~page where a new one takes its place
+  int32_t* taken;  // [S, max_pages / 32 up]: how many of 32 pages are replaced
   int32_t* stays;  // [L, S, H, rows]: the row that comes to place j
 };
 
 // ------------------------------------------------------------------------------------- plan --
-// A thread a sequence for lengths and sums, a warp a sequence for its pages.
+// A thread a sequence for lengths and sums; 32 pages of one a warp at a time, from another warp on for each sequence, so that all
+// warps share a long one and as many short ones go side by side.
 constexpr int kShortList = 4096;
 
 __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const __grid_constant__ EvictArgs a) {
@@ -68,24 +70,25 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const __grid_c
   if (b == 0) s_low = c.n_pages;
   bool any_bad = __syncthreads_or(bad);
   bad = false;
+  const int chunks = (c.max_pages + 31) / 32;
   if (!any_bad) {
-    for (int s = warp; s < a.B; s += kPlanThreads / 32) {
+    for (int s = 0; s < a.B; ++s) {
       if (s_keep[s] < 0) continue;
       const int had = pages_of(c, s_len[s]), has = pages_of(c, s_keep[s]), same = min(a.sink >> c.shift, has);
       const int32_t* row = c.table + static_cast<size_t>(s) * c.max_pages;
       int32_t* old = a.old + static_cast<size_t>(s) * c.max_pages;
-      int shared = 0;
-#pragma unroll 4
-      for (int j = lane; j < had; j += 32) {
-        const int page = row[j];
+      for (int at = (warp - s) & 31; at * 32 < had; at += kPlanThreads / 32) {
+        const int j = at * 32 + lane, page = j < had ? row[j] : 0;
         const bool in = page >= 0 && page < c.n_pages;
         bad |= !in;
         const bool taken = in && j >= same && j < has && c.refs[page] > 1;
-        shared += taken;
-        old[j] = taken ? ~page : page;
+        if (j < had) old[j] = taken ? ~page : page;
+        const int n = __popc(__ballot_sync(0xffffffffu, taken));
+        if (lane == 0) {
+          a.taken[static_cast<size_t>(s) * chunks + at] = n;
+          if (n > 0) atomicAdd(&s_off[s], n);
+        }
       }
-      shared = __reduce_add_sync(0xffffffffu, shared);
-      if (lane == 0) s_off[s] = shared;
     }
   }
   any_bad = __syncthreads_or(bad) || any_bad;
@@ -101,27 +104,30 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const __grid_c
   }
   __syncthreads();  // every offset is there
   int lowest = c.n_pages;
-  for (int s = warp; s < a.B; s += kPlanThreads / 32) {
+  for (int s = 0; s < a.B; ++s) {
     if (s_keep[s] < 0) continue;
     const int had = pages_of(c, s_len[s]), has = pages_of(c, s_keep[s]);
     int32_t* row = c.table + static_cast<size_t>(s) * c.max_pages;
     const int32_t* old = a.old + static_cast<size_t>(s) * c.max_pages;
-    int at = s_off[s];
-    for (int j0 = 0; j0 < had; j0 += 32) {
-      const int j = j0 + lane, page = j < had ? old[j] : 0;  // (this lane wrote it)
+    for (int at = (warp - s) & 31; at * 32 < had; at += kPlanThreads / 32) {
+      const int j = at * 32 + lane, page = j < had ? old[j] : 0;  // (this lane wrote it)
       const bool taken = page < 0, gone = j < had && j >= has;
       const unsigned mask = __ballot_sync(0xffffffffu, taken);
-      if (taken) {
-        const int id = list[at + __popc(mask & ((1u << lane) - 1u))];
-        row[j] = id;
-        c.refs[id] = 1;
+      if (mask != 0) {  // its place in the list: behind what the chunks in front take
+        int before = 0;
+        for (int i = lane; i < at; i += 32) before += __ldcg(a.taken + static_cast<size_t>(s) * chunks + i);
+        before = s_off[s] + __reduce_add_sync(0xffffffffu, before);
+        if (taken) {
+          const int id = list[before + __popc(mask & ((1u << lane) - 1u))];
+          row[j] = id;
+          c.refs[id] = 1;
+        }
       }
       if (gone) row[j] = -1;
       if (taken || gone) {
         const int left = taken ? ~page : page;
         if (atomicSub(&c.refs[left], 1) == 1) lowest = min(lowest, left);
       }
-      at += __popc(mask);
     }
   }
   lowest = __reduce_min_sync(0xffffffffu, lowest);
@@ -136,189 +142,265 @@ __global__ void __launch_bounds__(kPlanThreads) evict_plan_kernel(const __grid_c
 }
 
 // ----------------------------------------------------------------------------------- select --
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kSelRows = 4;  // rows a thread and step
+// A block a sequence, layer and head: rows [sink, end) compete for `need` places.  The last weight that stays is found by passes over the
+// weights, each of which counts keys in up to 2048 bins of the range that is left, at first that from the least key to the largest: weights
+// have few exponents, and threads that meet in a bin go one after the other.  (Bins of the words' upper 11 bits: 157 us for 128 blocks
+// of 65536 rows; two bits a pass by comparing and adding up: 88 us for 1920 blocks of 2048 to 4096 rows, which took 55 by the upper bits.)
 constexpr int kBins = 2048;
 
-// Weights in ascending order as unsigned words: the two zeros alike, NaN below all.
+// Weights in ascending order as unsigned words: the two zeros alike (their sum with 0 is +0), a NaN (the sum's, all ones but the sign) 0.  The
+// largest is infinity's, 0xff800001.
 __device__ __forceinline__ uint32_t order_of(float w) {
-  if (w != w) return 0u;
-  const uint32_t u = __float_as_uint(w == 0.f ? 0.f : w);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  const uint32_t u = __float_as_uint(w + 0.f);
+  return (u ^ (static_cast<uint32_t>(static_cast<int>(u) >> 31) | 0x80000000u)) + 1u;
 }
 
-// Counts of `n` bins in `hist`: the highest bin with at least `need` keys in it and above; *above gets those above it.  The whole
-// block; ends synchronised.
-__device__ __forceinline__ int find_bin(const int* hist, int n, int need, int* sums, int* s_out, int* above) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = n / kSelThreads;  // 4 or 2 bins a thread, from the highest down
-  const int top = n - 1 - each * static_cast<int>(threadIdx.x);
-  int own = 0;
-  for (int i = 0; i < each; ++i) own += hist[top - i];
-  int inc = own;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, inc, d);
-    if (lane >= d) inc += y;
-  }
-  if (lane == 31) sums[warp] = inc;
-  __syncthreads();
-  int before = inc - own;
-  for (int w = 0; w < warp; ++w) before += sums[w];
-  if (before < need && before + own >= need) {  // one thread
-    for (int i = 0; i < each; ++i) {
-      const int x = hist[top - i];
-      if (before + x >= need) {
-        s_out[0] = top - i;
-        s_out[1] = before;
-        break;
-      }
-      before += x;
-    }
-  }
-  __syncthreads();
-  *above = s_out[1];
-  return s_out[0];
-}
+// The key of the last row that stays, and how many of the rows with that key do (the first ones).
+struct Least {
+  uint32_t key;
+  int quota;
+};
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const __grid_constant__ EvictArgs a) {
-  __shared__ int s_hist[kBins];
-  __shared__ int s_sums[kSelWarps * kSelRows + 1], s_out[2];
-  let_second_start();
-  wait_for_first();
-  const CacheDev& c = a.c;
-  const int per = c.L * c.H, b = blockIdx.x / per, lh = blockIdx.x % per, l = lh / c.H, h = lh % c.H;
-  const EvictJob job = a.jobs[b];
-  if (job.keep < 0) return;
-  const size_t task = (static_cast<size_t>(l) * c.S + b) * c.H + h;
-  float* w = a.weights + task * a.rows;
-  int32_t* stays = a.stays + task * a.rows;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int end = job.len - a.recent, need = job.keep - a.sink - a.recent;  // rows [sink, end) compete for `need` places
-  // the last row that stays among them: its key, and how many of the rows with that key stay (the first ones)
-  uint32_t least = 0xffffffffu;  // (no row has it)
-  int quota = 0;
-  if (need > 0) {
-    int left = need;
-    uint32_t prefix = 0;
-#pragma unroll 1
-    for (int pass = 0; pass < 3; ++pass) {
-      const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
-      for (int i = threadIdx.x; i < bins; i += kSelThreads) s_hist[i] = 0;
-      __syncthreads();
-#pragma unroll 8
-      for (int r = a.sink + static_cast<int>(threadIdx.x); r < end; r += kSelThreads) {
-        const uint32_t key = order_of(w[r]);
-        if (pass == 0 || key >> (pass == 1 ? 21 : 10) == prefix) atomicAdd(&s_hist[(key >> shift) & (bins - 1)], 1);
-      }
-      __syncthreads();
-      int above;
-      const int bin = find_bin(s_hist, bins, left, s_sums, s_out, &above);
-      prefix = pass == 0 ? bin : prefix << (pass == 1 ? 11 : 10) | bin;
-      left -= above;
-      __syncthreads();
-    }
-    least = prefix;
-    quota = left;
-  }
-  // The list.  What stays before a row: the rows that stay for certain, and of those with the least key the first ones.  Both counts
-  // in one word: 2048 rows a step.
-  int sure = 0, ties = 0;  // of the steps before
-  for (int r0 = 0; r0 < job.len; r0 += kSelThreads * kSelRows) {
-    float x[kSelRows];
-    unsigned sure_mask[kSelRows], tie_mask[kSelRows];
-#pragma unroll
-    for (int i = 0; i < kSelRows; ++i) {
-      const int r = r0 + i * kSelThreads + threadIdx.x;
-      x[i] = r < job.len ? w[r] : 0.f;
-      const uint32_t key = order_of(x[i]);
-      const bool edge = r < a.sink || (r >= end && r < job.len), mid = r >= a.sink && r < end && need > 0;
-      sure_mask[i] = __ballot_sync(0xffffffffu, edge || (mid && key > least));
-      tie_mask[i] = __ballot_sync(0xffffffffu, mid && key == least);
-      if (lane == 0) s_sums[i * kSelWarps + warp] = __popc(sure_mask[i]) | __popc(tie_mask[i]) << 16;
-    }
-    __syncthreads();  // (and every weight of the step has been read)
-    if (warp == 0) {  // exclusive sums of the 64 words
-      const int x0 = s_sums[2 * lane], x1 = s_sums[2 * lane + 1];
-      int inc = x0 + x1;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int y = __shfl_up_sync(0xffffffffu, inc, d);
-        if (lane >= d) inc += y;
-      }
-      s_sums[2 * lane] = inc - x0 - x1;
-      s_sums[2 * lane + 1] = inc - x1;
-      if (lane == 31) s_sums[64] = inc;
+// What the block's threads share of it.
+template <int THREADS>
+struct Finder {
+  int hist[kBins];
+  int sums[32];
+  uint32_t lows[32], highs[32];
+  int bin, above;
+
+  // The least and the largest of the block's keys.
+  __device__ __forceinline__ void range(uint32_t& low, uint32_t& high) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    if (lane == 0) {
+      lows[warp] = low;
+      highs[warp] = high;
     }
     __syncthreads();
+    low = __reduce_min_sync(0xffffffffu, lane < THREADS / 32 ? lows[lane] : 0xffffffffu);
+    high = __reduce_max_sync(0xffffffffu, lane < THREADS / 32 ? highs[lane] : 0u);
+  }
+
+  // The highest bin with at least `need` keys in it and above; above: those above it.  Ends synchronised.
+  __device__ __forceinline__ void find(int need) {
+    constexpr int EACH = kBins / THREADS;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, top = kBins - 1 - EACH * static_cast<int>(threadIdx.x);
+    int own = 0;
 #pragma unroll
-    for (int i = 0; i < kSelRows; ++i) {
-      const int r = r0 + i * kSelThreads + threadIdx.x, word = s_sums[i * kSelWarps + warp];
-      const unsigned below = (1u << lane) - 1u;
-      const int sures = sure + (word & 0xffff) + __popc(sure_mask[i] & below), tied = ties + (word >> 16) + __popc(tie_mask[i] & below);
-      const bool tie = tie_mask[i] >> lane & 1;
-      if ((sure_mask[i] >> lane & 1) || (tie && tied < quota)) {
-        const int at = sures + min(tied, quota);
-        stays[at] = r;
-        if (at != r) w[at] = x[i];
-      }
+    for (int i = 0; i < EACH; ++i) own += hist[top - i];  // from the highest bin down
+    int inc = own;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, inc, d);
+      if (lane >= d) inc += y;
     }
-    const int all = s_sums[64];
-    sure += all & 0xffff;
-    ties += all >> 16;
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    int before = __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0) + inc - own;
+    if (before < need && before + own >= need) {  // one thread
+      int i = 0;
+      for (int x = hist[top]; before + x < need; x = hist[top - ++i]) before += x;
+      bin = top - i;
+      above = before;
+    }
     __syncthreads();
   }
-}
+
+  // each(f): f(key) for every key of the thread that competes, the same ones at every call.
+  template <typename Each>
+  __device__ __forceinline__ Least least(int need, Each&& each) {
+    uint32_t low = 0xffffffffu, high = 0;
+    each([&](uint32_t key) {
+      low = min(low, key);
+      high = max(high, key);
+    });
+    range(low, high);
+    uint32_t span = high - low;  // what is left: keys low .. low + span
+    for (bool all = true;; all = false) {
+      const int bits = 32 - __clz(span), shift = max(0, bits - 11);
+      for (int i = threadIdx.x; i < kBins; i += THREADS) hist[i] = 0;
+      __syncthreads();
+      each([&](uint32_t key) {
+        if (all || key - low <= span) atomicAdd(&hist[(key - low) >> shift], 1);
+      });
+      __syncthreads();
+      find(need);
+      low += static_cast<uint32_t>(bin) << shift;
+      need -= above;
+      if (shift == 0) return Least{low, need};
+      span = (1u << shift) - 1;
+      __syncthreads();  // (the bin has been read)
+    }
+  }
+};
+
+// The rows of a sequence, layer and head that stay, in order, into `stays`; their weights move.
+template <int THREADS, int KEYS>
+struct Select {
+  static constexpr int WARPS = THREADS / 32, ROWS = THREADS * KEYS;
+  static_assert(ROWS < 1 << 15, "two counts a word");
+  Finder<THREADS> finder;
+  int words[KEYS][WARPS], rows[KEYS];
+
+  __device__ __forceinline__ void run(const EvictArgs& a, const EvictJob& job, float* w, int32_t* stays) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int end = job.len - a.recent, need = job.keep - a.sink - a.recent;
+    float x[KEYS];  // the weights of a step's rows: r0 + i THREADS + thread
+    Least least{0xfffffffeu, 0};  // (above every weight's)
+    auto load = [&](int r0, int most) {
+      if (r0 + ROWS <= most) {
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) x[i] = w[r0 + i * THREADS + threadIdx.x];
+      } else {
+#pragma unroll
+        for (int i = 0; i < KEYS; ++i) x[i] = r0 + i * THREADS + static_cast<int>(threadIdx.x) < most ? w[r0 + i * THREADS + threadIdx.x] : 0.f;
+      }
+    };
+    if (job.len <= ROWS) {
+      load(0, job.len);
+      if (need > 0)
+        least = finder.least(need, [&](auto&& f) {
+#pragma unroll
+          for (int i = 0; i < KEYS; ++i) {
+            if (i * THREADS >= end) break;
+            const int r = i * THREADS + threadIdx.x;
+            if (r >= a.sink && r < end) f(order_of(x[i]));
+          }
+        });
+    } else if (need > 0) {
+      least = finder.least(need, [&](auto&& f) {
+        for (int r0 = a.sink; r0 < end; r0 += ROWS) {
+          load(r0, end);
+          if (r0 + ROWS <= end) {
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i) f(order_of(x[i]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < KEYS; ++i)
+              if (r0 + i * THREADS + static_cast<int>(threadIdx.x) < end) f(order_of(x[i]));
+          }
+        }
+      });
+    }
+    // The list.  What stays before a row: the rows that stay for certain, and of those with the least key the first ones.  Both counts
+    // in one word.
+    int sure = 0, ties = 0;  // of the steps before
+    for (int r0 = 0; r0 < job.len; r0 += ROWS) {
+      if (job.len > ROWS) load(r0, job.len);
+      auto key_of = [&](int i) {  // of a row that stays for certain above all; 1 + that of none
+        const int r = r0 + i * THREADS + threadIdx.x;
+        return r < a.sink || r >= end ? 0xffffffffu : order_of(x[i]);
+      };
+      auto in = [&](int i) { return r0 + i * THREADS + static_cast<int>(threadIdx.x) < job.len; };
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) {
+        if (r0 + i * THREADS >= job.len) break;
+        const uint32_t key = key_of(i);
+        const int n = __popc(__ballot_sync(0xffffffffu, in(i) && key > least.key)) | __popc(__ballot_sync(0xffffffffu, key == least.key)) << 16;
+        if (lane == 0) words[i][warp] = n;
+      }
+      __syncthreads();  // (and every weight of the step has been read)
+      for (int i = warp; i < KEYS; i += WARPS) {  // exclusive sums over the warps
+        if (r0 + i * THREADS >= job.len) break;
+        const int own = lane < WARPS ? words[i][lane] : 0;
+        int inc = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, inc, d);
+          if (lane >= d) inc += y;
+        }
+        if (lane < WARPS) words[i][lane] = inc - own;
+        if (lane == 31) rows[i] = inc;
+      }
+      __syncthreads();
+      int all = 0;  // before the run of THREADS rows
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) {
+        if (r0 + i * THREADS >= job.len) break;
+        const int r = r0 + i * THREADS + threadIdx.x;
+        const uint32_t key = key_of(i);
+        const bool stay = in(i) && key > least.key, tie = key == least.key;
+        const unsigned below = (1u << lane) - 1u, stay_mask = __ballot_sync(0xffffffffu, stay), tie_mask = __ballot_sync(0xffffffffu, tie);
+        const int word = all + words[i][warp], tied = ties + (word >> 16) + __popc(tie_mask & below);
+        if (stay || (tie && tied < least.quota)) {
+          const int at = sure + (word & 0xffff) + __popc(stay_mask & below) + min(tied, least.quota);
+          stays[at] = r;
+          if (at != r) w[at] = x[i];
+        }
+        all += rows[i];
+      }
+      sure += all & 0xffff;
+      ties += all >> 16;
+      __syncthreads();
+    }
+  }
+};
 
 // ------------------------------------------------------------------------------------- move --
-constexpr int kMoveThreads = 512;
+// e^{i d theta} of the pairs 8t .. 8t+7.  bf16: d theta in turns, its fraction exact to 2^-24, and the approximate sine and cosine, 1.2e-6 in
+// all, far below a step of the type; float32: the tables', whose 256 bytes a row are as much to read as K and V (bf16 with them: 128 blocks of
+// 16384 rows moved took 140 us more).
+template <typename DT>
+__device__ __forceinline__ void factors(const EvictArgs& a, int d, int t, float2 (&e)[8]) {
+  if constexpr (sizeof(DT) == 2) {
+    const float x = static_cast<float>(d);  // exact
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      const float2 turn = a.turn[8 * t + u];
+      const float p = x * turn.x;
+      const float f = ((p - rintf(p)) + fmaf(x, turn.x, -p)) + x * turn.y;
+      __sincosf(6.283185307179586f * f, &e[u].y, &e[u].x);
+    }
+  } else {
+    rope_row(a.rope_lo, a.rope_hi, d, t, e);
+  }
+}
 
-// A quad a row, each thread dims 8t .. and 32+8t .. of it: two 16-byte words of bf16, four of float32.
-template <typename DT, int ROWS>
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictArgs a) {
+// The rows of K or V that `stays` lists come to places job.same * P ..: a quad a row, each thread dims 8t .. and 32+8t .. of it: two 16-byte
+// words of bf16, four of float32.  By THREADS threads of the block's, with a barrier of
+// their own.
+template <typename DT, int THREADS, int ROWS>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictJob& job, int v, int l, int b, int h, const int32_t* stays) {
+  const int thread = threadIdx.x % THREADS;
   constexpr int kWords = static_cast<int>(sizeof(DT)), kHalf = kWords / 2;  // 16-byte words a thread and row
-  constexpr int kStep = kMoveThreads / 4 * ROWS;
-  wait_for_first();
+  constexpr int kStep = THREADS / 4 * ROWS;
   const CacheDev& c = a.c;
-  const int v = blockIdx.x & 1, per = c.L * c.H, task = blockIdx.x >> 1, b = task / per, lh = task % per, l = lh / c.H, h = lh % c.H;
-  const EvictJob job = a.jobs[b];
-  if (job.keep < 0) return;
-  const int32_t* stays = a.stays + ((static_cast<size_t>(l) * c.S + b) * c.H + h) * a.rows;
   const int32_t* old = a.old + static_cast<size_t>(b) * c.max_pages;
   const int32_t* now = c.table + static_cast<size_t>(b) * c.max_pages;
   DT* pool = static_cast<DT*>(v ? c.v : c.k) + ((static_cast<size_t>(l) * c.n_pages * c.H + h) << c.shift) * kD;
   const size_t page_elems = (static_cast<size_t>(c.H) << c.shift) * kD;
-  const int t = threadIdx.x & 3, quad = threadIdx.x >> 2, mask = c.P - 1;
+  const int t = thread & 3, quad = thread >> 2, mask = c.P - 1;
   for (int j0 = job.same << c.shift; j0 < job.keep; j0 += kStep) {
     uint4 x[ROWS][kWords];
-    int src[ROWS];
-    bool moves[ROWS];
+    int src[ROWS];  // -1: none, or it is there already
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int j = j0 + i * (kMoveThreads / 4) + quad;
+      const int j = j0 + i * (THREADS / 4) + quad;
       src[i] = j < job.keep ? stays[j] : -1;
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int j = j0 + i * (kMoveThreads / 4) + quad;
-      moves[i] = false;
-      if (src[i] >= 0) {
-        const int page = old[src[i] >> c.shift];
-        moves[i] = src[i] != j || page < 0;
-        if (moves[i]) {
-          const uint4* p = reinterpret_cast<const uint4*>(pool + (page < 0 ? ~page : page) * page_elems + static_cast<size_t>(src[i] & mask) * kD);
-#pragma unroll
-          for (int k = 0; k < kWords; ++k) x[i][k] = p[(k / kHalf) * 4 * kHalf + t * kHalf + k % kHalf];
-        }
+      if (src[i] < 0) continue;
+      const int page = old[src[i] >> c.shift];
+      const uint4* p = reinterpret_cast<const uint4*>(pool + (page < 0 ? ~page : page) * page_elems + static_cast<size_t>(src[i] & mask) * kD);
+      if (src[i] == j0 + i * (THREADS / 4) + quad && page >= 0) {
+        src[i] = -1;
+        continue;
       }
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) x[i][k] = p[(k / kHalf) * 4 * kHalf + t * kHalf + k % kHalf];
     }
-    __syncthreads();  // every row of the step has been read
+    asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(1 + v), "n"(THREADS) : "memory");  // every row of the step has been read
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int j = j0 + i * (kMoveThreads / 4) + quad;
-      if (!moves[i]) continue;
+      const int j = j0 + i * (THREADS / 4) + quad;
+      if (src[i] < 0) continue;
       if (v == 0 && a.turns && src[i] != j) {
         float2 e[8];
         float y[16];
-        rope_row(a.rope_lo, a.rope_hi, src[i] - j, t, e);
+        factors<DT>(a, src[i] - j, t, e);
         if constexpr (sizeof(DT) == 2) {
           const uint32_t u[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w, x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
 #pragma unroll
@@ -350,22 +432,51 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
   }
 }
 
+template <typename DT, int THREADS, int KEYS>
+__global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 4) evict_kernel(const __grid_constant__ EvictArgs a) {
+  constexpr int ROWS = sizeof(DT) == 2 ? 4 : 2;
+  __shared__ Select<THREADS, KEYS> select;
+  wait_for_first();
+  const CacheDev& c = a.c;
+  const int per = c.L * c.H, b = blockIdx.x / per, lh = blockIdx.x % per, l = lh / c.H, h = lh % c.H;
+  const EvictJob job = a.jobs[b];
+  if (job.keep < 0) return;
+  const size_t task = (static_cast<size_t>(l) * c.S + b) * c.H + h;
+  int32_t* stays = a.stays + task * a.rows;
+  select.run(a, job, a.weights + task * a.rows, stays);
+  // One half of the threads K, the other V: one reads while the other writes.  (One after the other, 128 blocks of 65536 rows cut to 16384:
+  // 264 us.)
+  move_rows<DT, THREADS / 2, ROWS>(a, job, threadIdx.x / (THREADS / 2), l, b, h, stays);
+}
+
+// By what the weights' rows can hold: up to 5120 rows a block of 256 threads, four of which share an SM; longer ones 1024 threads, which beyond
+// 16384 rows read the weights anew in each pass.
+template <typename DT>
+cudaError_t launch(const EvictArgs& a, unsigned tasks, cudaStream_t stream) {
+  return a.rows <= 256 * 20 ? launch_second(evict_kernel<DT, 256, 20>, dim3(tasks), 256, 0, stream, a)
+                            : launch_second(evict_kernel<DT, 1024, 16>, dim3(tasks), 1024, 0, stream, a);
+}
+
 size_t rows_bytes(const fib_attn_cache& c, int rows) {
   return round_up(sizeof(int32_t) * static_cast<size_t>(c.n_layers) * c.max_seqs * c.heads * static_cast<size_t>(rows));
 }
 size_t tables_bytes(const fib_attn_cache& c) {
   return round_up(sizeof(int32_t) * static_cast<size_t>(c.max_seqs) * static_cast<size_t>(c.max_pages));
 }
+size_t taken_bytes(const fib_attn_cache& c) {
+  return round_up(sizeof(int32_t) * static_cast<size_t>(c.max_seqs) * ((static_cast<size_t>(c.max_pages) + 31) / 32));
+}
 
 }  // namespace
 
-// jobs, the free pages taken, the old tables, the rows that stay
+// jobs, the free pages taken, the old tables and what is replaced of them, the rows that stay
 size_t cache_evict_workspace_bytes(const fib_attn_cache& c, int rows) {
-  return round_up(sizeof(EvictJob) * kMaxSeqs) + round_up(sizeof(int32_t) * static_cast<size_t>(c.n_pages)) + tables_bytes(c) + rows_bytes(c, rows);
+  return round_up(sizeof(EvictJob) * kMaxSeqs) + round_up(sizeof(int32_t) * static_cast<size_t>(c.n_pages)) + tables_bytes(c) +
+         taken_bytes(c) + rows_bytes(c, rows);
 }
 
 cudaError_t launch_cache_evict(const fib_attn_cache& cache, int B, int rows, const int32_t* keep, int sink, int recent, int n_max,
-                               float* weights, int32_t* dropped, const float2* lo_tab, const float2* hi_tab, bool turns, void* ws,
+                               float* weights, int32_t* dropped, const float2* lo_tab, const float2* hi_tab, const float2* turn, bool turns, void* ws,
                                cudaStream_t stream) {
   EvictArgs a;
   a.c = device_view(cache);
@@ -379,6 +490,7 @@ cudaError_t launch_cache_evict(const fib_attn_cache& cache, int B, int rows, con
   a.dropped = dropped;
   a.rope_lo = lo_tab;
   a.rope_hi = hi_tab;
+  for (int m = 0; m < kFreq; ++m) a.turn[m] = turn[m];
   a.turns = turns;
   unsigned char* at = static_cast<unsigned char*>(ws);
   a.jobs = reinterpret_cast<EvictJob*>(at);
@@ -387,15 +499,14 @@ cudaError_t launch_cache_evict(const fib_attn_cache& cache, int B, int rows, con
   at += round_up(sizeof(int32_t) * static_cast<size_t>(cache.n_pages));
   a.old = reinterpret_cast<int32_t*>(at);
   at += tables_bytes(cache);
+  a.taken = reinterpret_cast<int32_t*>(at);
+  at += taken_bytes(cache);
   a.stays = reinterpret_cast<int32_t*>(at);
   evict_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const unsigned tasks = static_cast<unsigned>(B) * cache.n_layers * cache.heads;
-  e = launch_second(evict_select_kernel, dim3(tasks), kSelThreads, stream, a);
-  if (e != cudaSuccess) return e;
-  return cache.dtype == FIB_DTYPE_F32 ? launch_second(evict_move_kernel<float, 2>, dim3(2 * tasks), kMoveThreads, stream, a)
-                                      : launch_second(evict_move_kernel<__nv_bfloat16, 4>, dim3(2 * tasks), kMoveThreads, stream, a);
+  return cache.dtype == FIB_DTYPE_F32 ? launch<float>(a, tasks, stream) : launch<__nv_bfloat16>(a, tasks, stream);
 }
 
 }  // namespace fibattn

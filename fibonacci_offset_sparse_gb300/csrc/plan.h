@@ -16,6 +16,7 @@ struct fib_attn_plan_s {
   int W = 0, N_max = 0, D = 0, mode = 0;
   double rope_base = 10000.0;
   bool rotates = true;  // else the tables below hold the identity
+  float2 turn[fibattn::kFreq] = {};  // theta_m / 2 pi as a sum of two
   int device = -1;
   float2* d_lo = nullptr;
   float2* d_hi = nullptr;

@@ -345,11 +345,11 @@ cudaError_t launch(const WeighArgs& a, cudaStream_t stream) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   const dim3 grid(152 * 2);  // 152 SMs
-  if (a.G * a.T <= 8) return launch_second(weigh_kernel<DT, true>, grid, kThreads, stream, a);
+  if (a.G * a.T <= 8) return launch_second(weigh_kernel<DT, true>, grid, kThreads, 0, stream, a);
   if constexpr (sizeof(DT) == 2)
     return launch_weigh_tc(a, stream);
   else
-    return launch_second(weigh_kernel<DT, false>, grid, kThreads, stream, a);
+    return launch_second(weigh_kernel<DT, false>, grid, kThreads, 0, stream, a);
 }
 
 int padded(int rows) { return rows <= 8 ? 8 : (rows + 63) / 64 * 64; }

@@ -495,17 +495,7 @@ cudaError_t launch_weigh_tc(const WeighArgs& a, cudaStream_t stream) {
   CUtensorMap map;
   e = map_layers(&map, a.c, a.c.P < kTile ? a.c.P : kTile);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(152);  // one block an SM
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSchedule + TcSchedule::bytes(a.B);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, weigh_tc_kernel, a, map);
+  return launch_second(weigh_tc_kernel, dim3(152), kThreads, kSchedule + TcSchedule::bytes(a.B), stream, a, map);  // one block an SM
 }
 
 }  // namespace fibattn
