@@ -4,8 +4,9 @@
 // one order of sums.  Two launches: the queries rotated, scaled and split once; then one pass over K.
 //
 // What bounds it: the read of K.  Here, for up to 8 query rows a key head (and float32 of any number): keys as the 16 rows of
-// mma.sync's tile, queries as its 8 columns, a warp 64 (float32: 32) rows at a time, 8 KB of loads on their way a warp straight to its
-// registers, in which a lane's 16-byte words are the tile's fragments (the order of the dims is the same for both).
+// mma.sync's tile, queries as its 8 columns.  A warp has units of 4 KB of K to itself and a ring of three of them in shared memory, filled by
+// bulk copies, so 16 warps have 192 KB an SM on their way and no warp waits for another.  A lane's 16-byte words are the tile's fragments
+// (the order of the dims is the same for both).
 // Precision: scores are float32.  The query is split in three bf16 (24 bits; cached bf16 rows enter as stored), float32 query and
 // rows each in two tf32 to nearest (22 bits); the small parts are added up first, as the pipes round toward zero.
 #include "weigh.cuh"
@@ -96,6 +97,7 @@ __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_c
 
 // ---------------------------------------------------------------------------------------- rows --
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kUnitBytes = 4096, kSlots = 3;  // of a warp's ring
 
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
@@ -113,7 +115,7 @@ template <typename DT>
 struct Frag;
 template <>
 struct Frag<__nv_bfloat16> {
-  static constexpr int kTiles = 4, kWords = 2;  // 16-byte words of a row that a lane holds: dims 8t .., 32+8t ..
+  static constexpr int kTiles = 2, kWords = 2;  // 16-byte words of a row that a lane holds: dims 8t .., 32+8t ..
   static constexpr int kGroup = kGroupBytes;
   uint4 q[3][2];
   __device__ __forceinline__ static int word(int t, int k) { return t + 4 * k; }
@@ -138,7 +140,7 @@ struct Frag<__nv_bfloat16> {
 };
 template <>
 struct Frag<float> {
-  static constexpr int kTiles = 2, kWords = 4;  // dims 16k + 4t .., k = 0 .. 3
+  static constexpr int kTiles = 1, kWords = 4;  // dims 16k + 4t .., k = 0 .. 3
   static constexpr int kGroup = kGroupBytes32;
   uint4 q[2][4];
   __device__ __forceinline__ static int word(int t, int k) { return t + 4 * k; }
@@ -178,19 +180,60 @@ struct Frag<float> {
   }
 };
 
-// The schedule: units before each sequence's (of all layers and heads), one run of them a warp.
+// A warp's units: a run of 4 KB pieces of K (32 rows of bf16, 16 of float32) of tasks (sequence, layer, head) after one another.
+struct Cursor {
+  long long u, end;  // the next task's first unit in the run; the run's end
+  int i, last;       // the present task's next unit, and the one behind its last in the run
+  int b, l, h;
+  WeighSeq s;
+
+  // Moves to the next unit, unit `i` of the task; false at the run's end.
+  template <int UNIT>
+  __device__ __forceinline__ bool next(const WeighArgs& a, const long long* start, bool* fresh) {
+    *fresh = ++i >= last;
+    if (!*fresh) return true;
+    if (u >= end) return false;
+    int lo = 0, hi = a.B;  // start[lo] <= u < start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (start[mid] <= u)
+        lo = mid;
+      else
+        hi = mid;
+    }
+    bool ok;
+    b = lo;
+    s = weigh_seq(a, b, &ok);
+    const int units = (s.len + UNIT - 1) / UNIT;
+    const long long off = u - start[b];
+    const int lh = off < 1LL << 31 ? static_cast<int>(static_cast<uint32_t>(off) / static_cast<uint32_t>(units)) : static_cast<int>(off / units);
+    l = lh / a.c.H;
+    h = lh - l * a.c.H;
+    i = static_cast<int>(off - static_cast<long long>(lh) * units);
+    last = static_cast<int>(min(static_cast<long long>(units), i + (end - u)));
+    u += last - i;
+    return true;
+  }
+};
+
 template <typename DT, bool ONE>  // ONE: 8 query rows at most, whose fragments stay in registers
 __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constant__ WeighArgs a) {
   using F = Frag<DT>;
-  constexpr int TILES = F::kTiles, UNIT = 16 * TILES, VALUES = TILES / 2;  // a lane's rows at the end
-  __shared__ long long s_start[kMaxSeqs + 1];
+  constexpr int TILES = F::kTiles, UNIT = 16 * TILES, ROW = kD * static_cast<int>(sizeof(DT));
+  static_assert(UNIT * ROW == kUnitBytes, "a unit");
+  extern __shared__ __align__(128) unsigned char s_ring[];  // [kWarps][kSlots][kUnitBytes]
+  __shared__ uint64_t s_full[kWarps][kSlots];
+  __shared__ int s_there[kWarps][kSlots];  // bit x: box x of the slot's unit lies in the pool
+  __shared__ long long s_start[kMaxSeqs + 1];  // units before each sequence's (of all layers and heads)
   const CacheDev& c = a.c;
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   for (int b = threadIdx.x; b < a.B; b += kThreads) {
     bool ok;
     const WeighSeq s = weigh_seq(a, b, &ok);
     s_start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + UNIT - 1) / UNIT) * c.L * c.H;
   }
+  if (threadIdx.x < kWarps * kSlots) mbar_init(&s_full[0][0] + threadIdx.x, 1);
+  asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   __syncthreads();
   if (threadIdx.x < 32) {
     long long base = 0;
@@ -209,131 +252,154 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     if (lane == 0) s_start[a.B] = base;
   }
   __syncthreads();
-  wait_for_first();
-  const long long total = s_start[a.B], warps = static_cast<long long>(gridDim.x) * kWarps, w = static_cast<long long>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  const long long each = total / warps, rest = total % warps;
-  long long u = w * each + min(w, rest);
-  const long long u1 = u + each + (w < rest ? 1 : 0);
-  while (u < u1) {
-    // the task of unit u, and its units in this run
-    int lo = 0, hi = a.B;  // s_start[lo] <= u < s_start[hi]
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_start[mid] <= u)
-        lo = mid;
-      else
-        hi = mid;
+  const long long total = s_start[a.B], warps = static_cast<long long>(gridDim.x) * kWarps, w = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const long long each = total / warps, rest = total % warps, first = w * each + min(w, rest);
+  const Cursor begin{first, first + each + (w < rest ? 1 : 0), 0, 0, 0, 0, 0, {}};
+  unsigned char* ring = s_ring + warp * kSlots * kUnitBytes;
+  const int box = min(UNIT, c.P);  // rows a copy
+
+  // Copies: lane x those of box x.  The page of the unit after the one that is copied is on its way.
+  Cursor feed = begin;
+  int page = 0, fed = 0;
+  bool fresh, more = feed.next<UNIT>(a, s_start, &fresh);
+  auto look = [&] {
+    const int r = feed.i * UNIT + lane * box;
+    page = more && lane * box < UNIT && r < feed.s.len ? __ldg(c.table + static_cast<size_t>(feed.b) * c.max_pages + (r >> c.shift)) : 0;
+  };
+  auto copy = [&] {
+    if (!more) return;
+    const int slot = fed % kSlots, r = feed.i * UNIT + lane * box;
+    const bool mine = lane * box < UNIT && r < feed.s.len, ok = page >= 0 && page < c.n_pages;
+    const unsigned there = __ballot_sync(0xffffffffu, mine && ok), boxes = __ballot_sync(0xffffffffu, mine);
+    if (there != boxes && lane == 0) atomicExch(a.status, kStatusDeviceAssert);
+    if (lane == 0) {
+      s_there[warp][slot] = static_cast<int>(there);
+      mbar_arrive_tx(&s_full[warp][slot], __popc(there) * box * ROW);
     }
-    const int b = lo;
-    bool ok;
-    const WeighSeq s = weigh_seq(a, b, &ok);
-    const int units = (s.len + UNIT - 1) / UNIT;
-    const long long off = u - s_start[b];
-    const int lh = static_cast<int>(off / units), l = lh / c.H, h = lh % c.H;
-    const int i0 = static_cast<int>(off - static_cast<long long>(lh) * units), i1 = static_cast<int>(min(static_cast<long long>(units), i0 + (u1 - u)));
-    u += i1 - i0;
-    const size_t task = (static_cast<size_t>(l) * a.B + b) * c.H + h;
-    const unsigned char* parts = a.parts + task * (a.mpad / 8) * F::kGroup;
-    const float* refs = a.refs + task * a.mpad;
-    const int used = s.n * a.G, groups = (used + 7) / 8, before = s.len - s.n;  // query row m sees rows up to before + m / G
-    const DT* pool = static_cast<const DT*>(c.k) + ((static_cast<size_t>(l) * c.n_pages * c.H + h) << c.shift) * kD;
-    const size_t page_elems = (static_cast<size_t>(c.H) << c.shift) * kD;
-    const int32_t* table = c.table + static_cast<size_t>(b) * c.max_pages;
-    float* out = a.weights + ((static_cast<size_t>(l) * c.S + b) * c.H + h) * a.rows;
-    F q;
-    float ref[2];
-    int sees[2];  // the last row that the lane's two queries see
-    auto take = [&](int group) {
-      q.load(parts + static_cast<size_t>(group) * F::kGroup, g, t);
-      const float2 r = *reinterpret_cast<const float2*>(refs + group * 8 + 2 * t);
-      ref[0] = r.x;
-      ref[1] = r.y;
+    __syncwarp();
+    if (mine && ok) {
+      const long long row = (((static_cast<long long>(feed.l) * c.n_pages + page) * c.H + feed.h) << c.shift) + (r & (c.P - 1));
+      bulk_g2s(ring + slot * kUnitBytes + lane * box * ROW, static_cast<const unsigned char*>(c.k) + row * ROW, box * ROW, &s_full[warp][slot]);
+    }
+    __syncwarp();
+    ++fed;
+    more = feed.next<UNIT>(a, s_start, &fresh);
+    look();
+  };
+  look();
+  for (int x = 0; x < kSlots; ++x) copy();
+  wait_for_first();
+
+  Cursor k = begin;
+  F q;
+  float ref[2];
+  int sees[2];  // the last row that the lane's two queries see
+  const unsigned char* parts = nullptr;
+  const float* refs = nullptr;
+  float* out = nullptr;
+  int used = 0, before = 0;  // query row m sees rows up to before + m / G
+  auto take = [&](int group) {
+    q.load(parts + static_cast<size_t>(group) * F::kGroup, g, t);
+    const float2 r = *reinterpret_cast<const float2*>(refs + group * 8 + 2 * t);
+    ref[0] = r.x;
+    ref[1] = r.y;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int m = group * 8 + 2 * t + e;
+      sees[e] = m < used ? before + m / a.G : -1;
+    }
+  };
+  for (int n = 0; k.next<UNIT>(a, s_start, &fresh); ++n) {
+    if (fresh) {
+      const size_t task = (static_cast<size_t>(k.l) * a.B + k.b) * c.H + k.h;
+      parts = a.parts + task * (a.mpad / 8) * F::kGroup;
+      refs = a.refs + task * a.mpad;
+      out = a.weights + ((static_cast<size_t>(k.l) * c.S + k.b) * c.H + k.h) * a.rows;
+      used = k.s.n * a.G;
+      before = k.s.len - k.s.n;
+      if (ONE) take(0);
+    }
+    const int r0 = k.i * UNIT, slot = n % kSlots, row = r0 + 8 * t + g;  // the row that the lane writes (float32: of t < 2)
+    const bool writes = 8 * t < UNIT && row < k.s.len;
+    const float old = writes && row < k.s.first ? out[row] : 0.f;
+    const bool landed = mbar_wait(&s_full[warp][slot], (n / kSlots) & 1, a.wait_ns);
+    if (!__all_sync(0xffffffffu, landed)) {
+      if (lane == 0) atomicExch(a.status, kStatusTimeout);
+      break;
+    }
+    const bool there = s_there[warp][slot] >> ((8 * t & (UNIT - 1)) / box) & 1;
+    uint4 x[TILES][2][F::kWords];
+#pragma unroll
+    for (int i = 0; i < TILES; ++i)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const int m = group * 8 + 2 * t + e;
-        sees[e] = m < used ? before + m / a.G : -1;
-      }
-    };
-    if (ONE) take(0);
-    for (int i = i0; i < i1; ++i) {
-      const int r0 = i * UNIT;
-      uint4 x[TILES][2][F::kWords];
-      bool in[TILES];
+        const unsigned char* at = ring + slot * kUnitBytes + (16 * i + 8 * e + g) * ROW;
+        if constexpr (sizeof(DT) == 2) {
+          lds_row_part(at, t, g & 1, x[i][e][0], x[i][e][1]);
+        } else {
 #pragma unroll
-      for (int k = 0; k < TILES; ++k) {
-        const int r = r0 + 16 * k;
-        in[k] = r < s.len;
-        const int page = in[k] ? table[r >> c.shift] : 0;
-        if (in[k] && (page < 0 || page >= c.n_pages)) {
-          in[k] = false;
-          if (lane == 0) atomicExch(a.status, kStatusDeviceAssert);
+          for (int z = 0; z < F::kWords; ++z) x[i][e][z] = reinterpret_cast<const uint4*>(at)[F::word(t, z)];
         }
-        const uint4* p = reinterpret_cast<const uint4*>(pool + page * page_elems + static_cast<size_t>((r & (c.P - 1)) + g) * kD);
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int z = 0; z < F::kWords; ++z) x[k][e][z] = in[k] ? __ldg(p + e * 8 * (kD * sizeof(DT) / 16) + F::word(t, z)) : make_uint4(0, 0, 0, 0);
       }
-      float old[VALUES];
+    float sum[2 * TILES];
 #pragma unroll
-      for (int v = 0; v < VALUES; ++v) {
-        const int r = r0 + 32 * v + 8 * t + g;
-        old[v] = r < s.first && r < s.len ? out[r] : 0.f;
-      }
-      float sum[2 * TILES];
-#pragma unroll
-      for (int v = 0; v < 2 * TILES; ++v) sum[v] = 0.f;
-      for (int group = ONE ? 0 : max(0, r0 - before) * a.G / 8; group < groups; ++group) {
-        if (!ONE) take(group);
-        // whether some query of the group is none, or does not see every row of the unit
-        const bool all = group * 8 + 8 <= used && before + group * 8 / a.G >= r0 + UNIT - 1;
-        float part[2 * TILES];
-        // A NaN may come of an infinite key, where the parts' products are infinities of opposite signs: the upper
-        // part's alone keep the sign, and a second round takes them.
+    for (int v = 0; v < 2 * TILES; ++v) sum[v] = 0.f;
+    const int groups = (used + 7) / 8;
+    for (int group = ONE ? 0 : max(0, r0 - before) * a.G / 8; group < groups; ++group) {
+      if (!ONE) take(group);
+      // whether some query of the group is none, or does not see every row of the unit
+      const bool all = group * 8 + 8 <= used && before + group * 8 / a.G >= r0 + UNIT - 1;
+      float part[2 * TILES];
+      // A NaN may come of an infinite key, where the parts' products are infinities of opposite signs: the upper
+      // part's alone keep the sign, and a second round takes them.
 #pragma unroll 1
-        for (int round = 0; round < 2; ++round) {
-          bool bad = false;
+      for (int round = 0; round < 2; ++round) {
+        bool bad = false;
 #pragma unroll
-          for (int k = 0; k < TILES; ++k) {
-            float y[4];
-            q.scores(x[k][0], x[k][1], y, false);
-            if (round == 1) {
-              float z[4];
-              q.scores(x[k][0], x[k][1], z, true);
+        for (int i = 0; i < TILES; ++i) {
+          float y[4];
+          q.scores(x[i][0], x[i][1], y, false);
+          if (round == 1) {
+            float z[4];
+            q.scores(x[i][0], x[i][1], z, true);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] = isnan(y[e]) ? z[e] : y[e];
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float y0 = ex2(y[2 * e] + ref[0]), y1 = ex2(y[2 * e + 1] + ref[1]);
-              if (!all) {
-                const int r = r0 + 16 * k + 8 * e + g;
-                y0 = r <= sees[0] ? y0 : 0.f;
-                y1 = r <= sees[1] ? y1 : 0.f;
-              }
-              part[2 * k + e] = y0 + y1;
-              bad |= isnan(y0 + y1);
-            }
+            for (int e = 0; e < 4; ++e) y[e] = isnan(y[e]) ? z[e] : y[e];
           }
-          if (!__any_sync(0xffffffffu, bad)) break;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float y0 = ex2(y[2 * e] + ref[0]), y1 = ex2(y[2 * e + 1] + ref[1]);
+            if (!all) {
+              const int r = r0 + 16 * i + 8 * e + g;
+              y0 = r <= sees[0] ? y0 : 0.f;
+              y1 = r <= sees[1] ? y1 : 0.f;
+            }
+            part[2 * i + e] = y0 + y1;
+            bad |= isnan(y0 + y1);
+          }
         }
-#pragma unroll
-        for (int v = 0; v < 2 * TILES; ++v) sum[v] += part[v];
+        if (!__any_sync(0xffffffffu, bad)) break;
       }
-      // a quad has the sums of 8 rows a value over its lanes' columns; then lane t writes those of value t (and t + 4)
 #pragma unroll
-      for (int v = 0; v < 2 * TILES; ++v) sum[v] = quad_sum(sum[v]);
-#pragma unroll
-      for (int v = 0; v < VALUES; ++v) {
-        const int r = r0 + 32 * v + 8 * t + g;
-        const float y = t == 0 ? sum[4 * v] : t == 1 ? sum[4 * v + 1] : t == 2 ? sum[4 * v + 2] : sum[4 * v + 3];
-        bool there = false;  // of the tile that row r lies in
-#pragma unroll
-        for (int k = 0; k < TILES; ++k) there |= in[k] && k == 2 * v + (t >> 1);
-        if (there && r < s.len) out[r] = old[v] + y;
-      }
+      for (int v = 0; v < 2 * TILES; ++v) sum[v] += part[v];
     }
+    // value v of a quad's four lanes, added up, is row 8v + g's; lane t takes that of value t
+#pragma unroll
+    for (int v = 0; v < 2 * TILES; ++v) sum[v] = quad_sum(sum[v]);
+    float y = t == 0 ? sum[0] : sum[1];
+    if constexpr (TILES == 2) y = t == 2 ? sum[2] : t == 3 ? sum[3] : y;
+    if (writes && there) out[row] = old + y;
+    __threadfence_block();  // the slot has been read
+    __syncwarp();
+    copy();
   }
+  // nothing may be in flight when the block ends
+  for (int x = max(0, fed - kSlots); x < fed; ++x) mbar_wait(&s_full[warp][x % kSlots], (x / kSlots) & 1, kWeighDrainNs);
+}
+
+cudaError_t launch_rows(void (*kernel)(WeighArgs), const WeighArgs& a, cudaStream_t stream) {
+  constexpr size_t kRing = static_cast<size_t>(kWarps) * kSlots * kUnitBytes;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRing));
+  return e == cudaSuccess ? launch_second(kernel, dim3(152 * 2), kThreads, kRing, stream, a) : e;  // 152 SMs
 }
 
 template <typename DT>
@@ -344,12 +410,11 @@ cudaError_t launch(const WeighArgs& a, cudaStream_t stream) {
   weigh_prep_kernel<DT><<<dim3(static_cast<unsigned>(a.c.L) * a.B, y, z), kPrepThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const dim3 grid(152 * 2);  // 152 SMs
-  if (a.G * a.T <= 8) return launch_second(weigh_kernel<DT, true>, grid, kThreads, 0, stream, a);
+  if (a.G * a.T <= 8) return launch_rows(weigh_kernel<DT, true>, a, stream);
   if constexpr (sizeof(DT) == 2)
     return launch_weigh_tc(a, stream);
   else
-    return launch_second(weigh_kernel<DT, false>, grid, kThreads, 0, stream, a);
+    return launch_rows(weigh_kernel<DT, false>, a, stream);
 }
 
 int padded(int rows) { return rows <= 8 ? 8 : (rows + 63) / 64 * 64; }

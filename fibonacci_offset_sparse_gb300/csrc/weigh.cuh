@@ -32,6 +32,9 @@ constexpr int kPartBytes = 8 * kD * 2;        // 8 rows of one bf16 part
 constexpr int kGroupBytes = 3 * kPartBytes;   // 8 query rows, bf16
 constexpr int kGroupBytes32 = 2 * 8 * kD * 4;  // ... float32
 
+// For what is in flight when a warp gives up: its wait is not the caller's, which may be too short for a copy.
+constexpr unsigned long long kWeighDrainNs = 2000000000ull;
+
 // Sequence b of a call: rows, new ones (0: nothing to do), the first row whose weight begins with this call.
 struct WeighSeq {
   int len, n, first;
