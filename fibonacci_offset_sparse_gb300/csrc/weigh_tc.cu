@@ -123,6 +123,13 @@ __device__ __forceinline__ void wait16(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// ... r too had come by then.
+__device__ __forceinline__ void pass16(uint32_t (&r)[16]) {
+  asm volatile(""
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                 "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]));
+}
+
 // Offset of cache row r in K, in elements; -1 where its page lies outside the pool.
 __device__ __forceinline__ long long row_at(const WeighArgs& a, const TcTask& k, int r) {
   const CacheDev& c = a.c;
@@ -233,8 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     *k = bars.task[tc & 1];
     return k->rounds > 0;
   };
-  auto release = [&](int tc) {
-    __threadfence_block();
+  auto release = [&](int tc) {  // (no fence, which would wait for what the warp has under way: the next task is written as this one is read)
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars.t_empty[tc & 1]);
   };
@@ -431,18 +437,18 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           };
           const uint32_t from = tmem + buf * kCols + lanes;
           auto add = [&]<bool ALL>() {
-            uint32_t y[16], z[16];
-            ld16(from, y);
-            wait16(y);
-            for (int col = 0; col < cols; col += 32) {
+#pragma unroll
+            for (int col = 0; col < kCols; col += 32) {
+              if (col >= cols) break;
+              uint32_t y[16], z[16];
               const bool second = col + 16 < cols;
+              ld16(from + col, y);
               if (second) ld16(from + col + 16, z);
+              wait16(y);
               use.template operator()<ALL>(y, col);
               if (!second) break;
-              wait16(z);
-              if (col + 32 < cols) ld16(from + col + 32, y);
+              pass16(z);
               use.template operator()<ALL>(z, col + 16);
-              wait16(y);
             }
           };
           if (all)
