@@ -4,10 +4,9 @@
 // A tile is 128 rows of K, as TMA leaves them (K-major, 128-byte swizzle), times up to 128 query rows of the split query, all three parts
 // added up into one accumulator of tensor memory: S [128 rows x queries].  There a thread has a row, so its sum is a loop over its columns:
 //   one load from tensor memory, one add (a pair at a time), one exp2, one add; no shuffle.
-// A task is up to four tiles of a sequence, layer and head, which stay in shared memory while its queries pass by 64 at a time
-// (of those that see the tile), or, where there are 64 at most, eight tiles that pass by the queries.  Blocks take tasks as they
-// come, so that those of prompts, which cost from 4 products to hundreds, fill all SMs.  A row's sum is one thread's, in the order of the
-// queries, whichever block it is.
+// A task is up to four tiles of a sequence, layer and head, which stay in shared memory while its queries pass by (those that see the
+// tile), or, where there are 64 at most, eight tiles that pass by the queries.  Blocks take tasks as they come, so that those of
+// prompts, which cost from 4 products to hundreds, fill all SMs.  A row's sum is one thread's, in the order of the queries, whichever block it is.
 //
 // What bounds it: few query rows the read of K, many the products (three parts) and exp2.
 //
@@ -26,19 +25,26 @@ namespace fibattn {
 namespace {
 
 constexpr int kTile = 128, kTiles = 4, kGroupRows = kTile * kTiles;  // rows of a round
-constexpr int kRounds = 2;                                            // of a task with no more than kCols query rows; else 1
-constexpr int kCols = 64;                                             // query rows of a product
-constexpr int kTileBytes = kTile * kD * 2, kSlots = 2 * kTiles;       // two a tile of the round
-// Slots of queries: one is free again when its products are done and its references read, some 2.5 us after its copy began.
-constexpr int kQuerySlots = 3;
-constexpr int kQueryBytes = kCols / 8 * kGroupBytes, kQuerySlot = kQueryBytes + 1024;  // and their references; a multiple of 1024
-// Buffers of tensor memory, kCols columns each: two a tile of the round, so that a barrier is waited for by the four warps of one tile
-// alone, one round after the other.  (Its parity cannot tell a warp that is a round ahead from one that is not.)
-constexpr int kBuffers = 2 * kTiles;
+constexpr int kTileBytes = kTile * kD * 2;
+constexpr int kRefSlots = 4, kRefBytes = 512;
 constexpr int kSumWarps = 4 * kTiles, kIssuer = kSumWarps, kFeedK = kIssuer + kTiles, kTasks = kFeedK + kTiles, kFeedQ = kTasks + 1;
 constexpr int kThreads = 32 * (kFeedQ + 1);
-constexpr int kQueries = kSlots * kTileBytes, kSchedule = kQueries + kQuerySlots * kQuerySlot;
-static_assert(kQuerySlot % 1024 == 0 && kBuffers * kCols == 512, "layout");
+
+// COLS query rows a product: 64, where a key head has no more, two buffers of tensor memory a tile, two slots of shared memory a tile, and
+// tasks of two rounds; else 128, one buffer, and two slots for the first two tiles.  A product takes 48.5, 54 and 64.6 cycles with 32, 64 and 128
+// columns, and what a warp does a chunk of queries beside its columns costs as much as 40 of them: prompts of 2048 took 66 us with 64.
+template <int COLS>
+struct Shape {
+  static constexpr int kRounds = COLS == 64 ? 2 : 1;
+  static constexpr int kBuffers = 512 / (kTiles * COLS);  // of tensor memory, a tile
+  static constexpr int kSlots = COLS == 64 ? 2 * kTiles : kTiles + 2, kQuerySlots = COLS == 64 ? 3 : 2;
+  static constexpr int kQuerySlot = COLS / 8 * kGroupBytes;
+  static constexpr int kQueries = kSlots * kTileBytes, kRefs = kQueries + kQuerySlots * kQuerySlot, kSchedule = kRefs + kRefSlots * kRefBytes;
+  static_assert(kQuerySlot % 1024 == 0 && COLS * 4 <= kRefBytes, "layout");
+  // Tile t's slots: this one and, where there is one, the next.
+  __device__ __forceinline__ static int slot(int t) { return COLS == 64 || t < 2 ? 2 * t : t + 2; }
+  __device__ __forceinline__ static int slots(int t) { return COLS == 64 || t < 2 ? 2 : 1; }
+};
 
 struct TcTask {
   int b, l, h;
@@ -47,10 +53,13 @@ struct TcTask {
   int r0, rounds;         // rounds 0: there is none any more
 };
 
+// A barrier of one warp's or of one tile's warps, which wait for each of its rounds, one after the other: its parity cannot tell one that is a
+// round ahead from one that is not.
 struct TcBars {
-  uint64_t k_full[kSlots], k_empty[kSlots];
-  uint64_t q_full[kQuerySlots], q_empty[kQuerySlots];
-  uint64_t s_full[kBuffers], s_empty[kBuffers];
+  uint64_t k_full[2 * kTiles], k_empty[2 * kTiles];
+  uint64_t q_full[3], q_empty[3];
+  uint64_t r_full[kRefSlots], r_empty[kRefSlots];
+  uint64_t s_full[2 * kTiles], s_empty[2 * kTiles];
   uint64_t t_full[2], t_empty[2];
   uint64_t drained;
   TcTask task[2];
@@ -59,12 +68,24 @@ struct TcBars {
 };
 
 // Rows of a task of a sequence with `used` query rows.
-__device__ __forceinline__ int task_rows(int used) { return used <= kCols ? kRounds * kGroupRows : kGroupRows; }
+template <int COLS>
+__device__ __forceinline__ int task_rows(int used) {
+  return used <= COLS ? Shape<COLS>::kRounds * kGroupRows : kGroupRows;
+}
 // The chunk of queries from which on some of them see row r, of a task.
-__device__ __forceinline__ int first_chunk(const WeighArgs& a, const TcTask& k, int r) { return max(0, r - k.before) * a.G / kCols; }
-__device__ __forceinline__ int chunks(const TcTask& k) { return (k.used + kCols - 1) / kCols; }
+template <int COLS>
+__device__ __forceinline__ int first_chunk(const WeighArgs& a, const TcTask& k, int r) {
+  return max(0, r - k.before) * a.G / COLS;
+}
+template <int COLS>
+__device__ __forceinline__ int chunks(const TcTask& k) {
+  return (k.used + COLS - 1) / COLS;
+}
 // Columns of chunk c's product.
-__device__ __forceinline__ int columns(const TcTask& k, int c) { return min(kCols, (k.used - c * kCols + 15) / 16 * 16); }
+template <int COLS>
+__device__ __forceinline__ int columns(const TcTask& k, int c) {
+  return min(COLS, (k.used - c * COLS + 15) / 16 * 16);
+}
 
 // The sequences, in shared memory: the tasks before each, and what it is.
 struct TcSchedule {
@@ -75,6 +96,7 @@ struct TcSchedule {
 };
 
 // Task `id` of the call, if there is one (rounds > 0): sequences in order, of each the first rows of all layers and heads before the next.
+template <int COLS>
 __device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& sch, unsigned long long id) {
   TcTask k = {};
   const long long* start = sch.start;
@@ -100,7 +122,7 @@ __device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& 
   k.before = s.len - s.n;
   k.used = s.n * a.G;
   k.first = s.first;
-  const int rows = task_rows(k.used);
+  const int rows = task_rows<COLS>(k.used);
   k.r0 = j * rows;
   k.rounds = (min(rows, s.len - k.r0) + kGroupRows - 1) / kGroupRows;
   return k;
@@ -168,29 +190,35 @@ __device__ __noinline__ float add_infinite(const WeighArgs& a, const TcTask& k, 
   return sum;
 }
 
+template <int COLS>
 __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_constant__ WeighArgs a, const __grid_constant__ CUtensorMap map_k) {
+  using P = Shape<COLS>;
   extern __shared__ __align__(1024) unsigned char smem[];
   __shared__ __align__(16) TcBars bars;
   volatile int& s_err = bars.err;
-  const TcSchedule sch(smem + kSchedule, a.B);
+  const TcSchedule sch(smem + P::kSchedule, a.B);
   long long* start = sch.start;
   const CacheDev& c = a.c;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     s_err = 0;
-    for (int s = 0; s < kSlots; ++s) {
+    for (int s = 0; s < P::kSlots; ++s) {
       mbar_init(&bars.k_full[s], 1);
       mbar_init(&bars.k_empty[s], 1);
     }
-    for (int s = 0; s < kQuerySlots; ++s) {
+    for (int s = 0; s < P::kQuerySlots; ++s) {
       mbar_init(&bars.q_full[s], 1);
-      mbar_init(&bars.q_empty[s], kTiles + kSumWarps);
+      mbar_init(&bars.q_empty[s], kTiles);
+    }
+    for (int s = 0; s < kRefSlots; ++s) {
+      mbar_init(&bars.r_full[s], 1);
+      mbar_init(&bars.r_empty[s], kSumWarps);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.t_full[s], 1);
       mbar_init(&bars.t_empty[s], 1 + 2 * kTiles + kSumWarps);
     }
-    for (int s = 0; s < kBuffers; ++s) {
+    for (int s = 0; s < kTiles * P::kBuffers; ++s) {
       mbar_init(&bars.s_full[s], 1);
       mbar_init(&bars.s_empty[s], 4);
     }
@@ -200,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   for (int b = tid; b < a.B; b += kThreads) {
     bool ok;
     const WeighSeq s = weigh_seq(a, b, &ok);
-    const int rows = task_rows(s.n * a.G);
+    const int rows = task_rows<COLS>(s.n * a.G);
     sch.seq[b] = s;
     start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + rows - 1) / rows) * c.L * c.H;
   }
@@ -221,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     }
     if (lane == 0) start[a.B] = base;
   }
-  if (warp == kIssuer) tmem_alloc(&bars.tmem, kBuffers * kCols);
+  if (warp == kIssuer) tmem_alloc(&bars.tmem, 512);
   fence_before();
   __syncthreads();
   fence_after();
@@ -249,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     // =================================================================== tasks
     for (int tc = 0; wait(&bars.t_empty[tc & 1], ((tc >> 1) & 1) ^ 1); ++tc) {
       unsigned long long id = lane == 0 ? atomicAdd(a.next, 1ull) : 0;
-      const TcTask k = task_at(a, sch, __shfl_sync(0xffffffffu, id, 0));
+      const TcTask k = task_at<COLS>(a, sch, __shfl_sync(0xffffffffu, id, 0));
       if (lane == 0) {
         bars.task[tc & 1] = k;
         mbar_arrive(&bars.t_full[tc & 1]);
@@ -257,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       __syncwarp();
       if (k.rounds == 0) break;
       // A long task is taken alone, till the last of its queries is under way: one that waits for its block waits for nothing else.
-      if (k.used > kCols && !wait(&bars.t_empty[tc & 1], (tc >> 1) & 1)) break;
+      if (k.used > COLS && !wait(&bars.t_empty[tc & 1], (tc >> 1) & 1)) break;
     }
   } else if (warp == kFeedQ) {
     // =================================================================== copies of queries
@@ -266,29 +294,31 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     TcTask k;
     for (int tc = 0; go && read(tc, &k); ++tc) {
       const size_t m = ((static_cast<size_t>(k.l) * a.B + k.b) * c.H + k.h) * a.mpad;
-      const int c1 = chunks(k);
-      for (int ch = first_chunk(a, k, k.r0); ch < c1; ++ch, ++n) {
-        const int slot = n % kQuerySlots, cols = columns(k, ch);
-        go = wait(&bars.q_empty[slot], ((n / kQuerySlots) & 1) ^ 1);
+      const int c1 = chunks<COLS>(k);
+      for (int ch = first_chunk<COLS>(a, k, k.r0); ch < c1; ++ch, ++n) {
+        const int slot = n % P::kQuerySlots, ref = n % kRefSlots, cols = columns<COLS>(k, ch);
+        go = wait(&bars.q_empty[slot], ((n / P::kQuerySlots) & 1) ^ 1) && wait(&bars.r_empty[ref], ((n / kRefSlots) & 1) ^ 1);
         if (!go) break;
         if (lane == 0) {
-          unsigned char* to = smem + kQueries + slot * kQuerySlot;
-          const size_t at = m + static_cast<size_t>(ch) * kCols;
-          mbar_arrive_tx(&bars.q_full[slot], cols / 8 * kGroupBytes + cols * 4);
-          bulk_g2s(to, a.parts + at / 8 * kGroupBytes, cols / 8 * kGroupBytes, &bars.q_full[slot]);
-          bulk_g2s(to + kQueryBytes, a.refs + at, cols * 4, &bars.q_full[slot]);
+          const size_t at = m + static_cast<size_t>(ch) * COLS;
+          mbar_arrive_tx(&bars.q_full[slot], cols / 8 * kGroupBytes);
+          bulk_g2s(smem + P::kQueries + slot * P::kQuerySlot, a.parts + at / 8 * kGroupBytes, cols / 8 * kGroupBytes, &bars.q_full[slot]);
+          mbar_arrive_tx(&bars.r_full[ref], cols * 4);
+          bulk_g2s(smem + P::kRefs + ref * kRefBytes, a.refs + at, cols * 4, &bars.r_full[ref]);
         }
         __syncwarp();
       }
       release(tc);
     }
     // nothing may be in flight when the block ends
-    if (lane == 0)
-      for (int x = max(0, n - kQuerySlots); x < n; ++x) mbar_wait(&bars.q_full[x % kQuerySlots], (x / kQuerySlots) & 1, kDrainNs);
+    if (lane == 0) {
+      for (int x = max(0, n - P::kQuerySlots); x < n; ++x) mbar_wait(&bars.q_full[x % P::kQuerySlots], (x / P::kQuerySlots) & 1, kDrainNs);
+      for (int x = max(0, n - kRefSlots); x < n; ++x) mbar_wait(&bars.r_full[x % kRefSlots], (x / kRefSlots) & 1, kDrainNs);
+    }
     __syncwarp();
   } else if (warp >= kFeedK && warp < kFeedK + kTiles) {
     // =================================================================== copies of rows: tile t of each round
-    const int t = warp - kFeedK, box = min(kTile, c.P);  // rows a copy
+    const int t = warp - kFeedK, box = min(kTile, c.P), slots = P::slots(t);  // rows a copy
     int n = 0;
     bool go = true, left_out[2] = {false, false};        // slots that the test hook does not fill
     TcTask k;
@@ -297,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       for (int x = 0; x < k.rounds; ++x) {
         const int r0 = k.r0 + x * kGroupRows + t * kTile;
         if (r0 >= k.len) break;
-        const int boxes = (min(kTile, k.len - r0) + box - 1) / box, s = n & 1, slot = 2 * t + s;
+        const int boxes = (min(kTile, k.len - r0) + box - 1) / box, s = n & (slots - 1), slot = P::slot(t) + s;
         // lane i copies box i
         const int r = r0 + lane * box;
         int id = lane < boxes ? __ldg(c.table + static_cast<size_t>(k.b) * c.max_pages + (r >> c.shift)) : 0;
@@ -305,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           atomicExch(a.status, kStatusDeviceAssert);
           id = 0;
         }
-        go = wait(&bars.k_empty[slot], ((n >> 1) & 1) ^ 1);
+        go = wait(&bars.k_empty[slot], ((n / slots) & 1) ^ 1);
         if (!go) break;
         ++n;
         left_out[s] = a.skip_copy && x == 0 && t == 0;
@@ -318,8 +348,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       }
     }
     if (lane == 0)
-      for (int x = max(0, n - 2); x < n; ++x)
-        if (!left_out[x & 1]) mbar_wait(&bars.k_full[2 * t + (x & 1)], (x >> 1) & 1, kDrainNs);
+      for (int x = max(0, n - slots); x < n; ++x)
+        if (!left_out[x & (slots - 1)]) mbar_wait(&bars.k_full[P::slot(t) + (x & (slots - 1))], (x / slots) & 1, kDrainNs);
     __syncwarp();
   } else if (warp >= kIssuer && warp < kIssuer + kTiles) {
     // =================================================================== products of tile t of each round
@@ -329,47 +359,48 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     constexpr uint32_t kLead = 16 / 16 << 16, kRowsHigh = 1024 / 16 | 1u << 14 | 2u << 29, kQueryHigh = kGroupBytes / 16 | 1u << 14 | 2u << 29;
     auto at = [](uint32_t high, uint32_t low) { return static_cast<uint64_t>(high) << 32 | low; };
     const int t = same(warp - kIssuer);
-    const uint32_t rows0 = (base + 2 * t * kTileBytes) >> 4 | kLead, query0 = (base + kQueries) >> 4 | kLead, out0 = tmem + 2 * t * kCols;
+    const int slots = P::slots(t), slot0 = P::slot(t), buf0 = t * P::kBuffers;
+    const uint32_t rows0 = (base + slot0 * kTileBytes) >> 4 | kLead, query0 = (base + P::kQueries) >> 4 | kLead, out0 = tmem + buf0 * COLS;
     int qs = 0, q_round = 0, filled = 0, done = 0;  // tiles copied, products made
     bool go = true;
     TcTask k;
     for (int tc = 0; go && read(tc, &k); ++tc) {
-      const int c0 = same(first_chunk(a, k, k.r0)), c1 = same(chunks(k)), last = same(columns(k, chunks(k) - 1));
-      int from[kRounds];  // the first chunk that sees rows of the tile
+      const int c0 = same(first_chunk<COLS>(a, k, k.r0)), c1 = same(chunks<COLS>(k)), last = same(columns<COLS>(k, chunks<COLS>(k) - 1));
+      int from[P::kRounds];  // the first chunk that sees rows of the tile
 #pragma unroll
-      for (int x = 0; x < kRounds; ++x) {
+      for (int x = 0; x < P::kRounds; ++x) {
         const int r = k.r0 + x * kGroupRows + t * kTile;
-        from[x] = same(x < k.rounds && r < k.len ? first_chunk(a, k, r) : INT_MAX);
+        from[x] = same(x < k.rounds && r < k.len ? first_chunk<COLS>(a, k, r) : INT_MAX);
       }
       release(tc);
       for (int ch = c0; ch < c1 && go; ++ch) {
         go = wait(&bars.q_full[qs], q_round & 1);
         if (!go) break;
-        const uint32_t query = query0 + qs * (kQuerySlot / 16), desc = product_of(kTile, ch == c1 - 1 ? last : kCols, false, false);
+        const uint32_t query = query0 + qs * (P::kQuerySlot / 16), desc = product_of(kTile, ch == c1 - 1 ? last : COLS, false, false);
 #pragma unroll
-        for (int x = 0; x < kRounds; ++x) {
+        for (int x = 0; x < P::kRounds; ++x) {
           if (from[x] > ch) break;
           // the tile is there from the first chunk that sees it to the last
-          const int slot = filled & 1, buf = done & 1;
-          if (ch == max(from[x], c0)) go = wait(&bars.k_full[2 * t + slot], (filled >> 1) & 1);
-          if (go) go = wait(&bars.s_empty[2 * t + buf], ((done >> 1) & 1) ^ 1);
+          const int slot = filled & (slots - 1), buf = done & (P::kBuffers - 1);
+          if (ch == max(from[x], c0)) go = wait(&bars.k_full[slot0 + slot], (filled / slots) & 1);
+          if (go) go = wait(&bars.s_empty[buf0 + buf], ((done / P::kBuffers) & 1) ^ 1);
           if (!go) break;
           fence_after();
-          const uint32_t rows = rows0 + slot * (kTileBytes / 16), d = out0 + buf * kCols;
+          const uint32_t rows = rows0 + slot * (kTileBytes / 16), d = out0 + buf * COLS;
           if (one_lane()) {
 #pragma unroll
             for (int part = 2; part >= 0; --part)
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 mma_tc(d, at(kRowsHigh, rows + 2 * y), at(kQueryHigh, query + part * (kPartBytes / 16) + 2 * y), desc, part < 2 || y > 0);
-            commit_tc(&bars.s_full[2 * t + buf]);
-            if (ch == c1 - 1) commit_tc(&bars.k_empty[2 * t + slot]);
+            commit_tc(&bars.s_full[buf0 + buf]);
+            if (ch == c1 - 1) commit_tc(&bars.k_empty[slot0 + slot]);
           }
           ++done;
           if (ch == c1 - 1) ++filled;
         }
         if (go && one_lane()) commit_tc(&bars.q_empty[qs]);
-        if (++qs == kQuerySlots) {
+        if (++qs == P::kQuerySlots) {
           qs = 0;
           ++q_round;
         }
@@ -391,32 +422,33 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       release(tc);
       float* out = a.weights + ((static_cast<size_t>(k.l) * c.S + k.b) * c.H + k.h) * a.rows;
       const int32_t* table = c.table + static_cast<size_t>(k.b) * c.max_pages;
-      float sum[kRounds], old[kRounds];
-      int page[kRounds];  // (looked at in the end)
+      float sum[P::kRounds], old[P::kRounds];
+      int page[P::kRounds];  // (looked at in the end)
+      const int first0 = k.r0 + mine * kTile, row0 = first0 + wq * 32 + lane;  // the tile's and the thread's row in the first round
 #pragma unroll
-      for (int x = 0; x < kRounds; ++x) {
-        const int r = k.r0 + x * kGroupRows + mine * kTile + wq * 32 + lane;  // the thread's row
+      for (int x = 0; x < P::kRounds; ++x) {
+        const int r = row0 + x * kGroupRows;
         sum[x] = 0.f;
         old[x] = x < k.rounds && r < k.first && r < k.len ? out[r] : 0.f;
         page[x] = x < k.rounds && r < k.len ? __ldg(table + (r >> c.shift)) : -1;
       }
-      const int c1 = chunks(k);
-      for (int ch = first_chunk(a, k, k.r0); ch < c1 && go; ++ch, ++n) {
-        const int cols = columns(k, ch), m0 = ch * kCols, sees = k.before + m0 / a.G;  // the last row that the first column sees
-        const float* ref = reinterpret_cast<const float*>(smem + kQueries + n % kQuerySlots * kQuerySlot + kQueryBytes);
-        go = wait(&bars.q_full[n % kQuerySlots], (n / kQuerySlots) & 1);
+      const int c1 = chunks<COLS>(k);
+      for (int ch = first_chunk<COLS>(a, k, k.r0); ch < c1 && go; ++ch, ++n) {
+        const int cols = columns<COLS>(k, ch), m0 = ch * COLS;
+        const float* ref = reinterpret_cast<const float*>(smem + P::kRefs + n % kRefSlots * kRefBytes);
+        go = wait(&bars.r_full[n % kRefSlots], (n / kRefSlots) & 1);
         if (!go) break;
 #pragma unroll
-        for (int x = 0; x < kRounds; ++x) {
-          const int first = k.r0 + x * kGroupRows + mine * kTile, r = first + wq * 32 + lane;
-          if (x >= k.rounds || first >= k.len || first_chunk(a, k, first) > ch) break;  // none of these queries sees the tile
-          const int buf = 2 * mine + (done & 1);
-          go = wait(&bars.s_full[buf], (done >> 1) & 1);
+        for (int x = 0; x < P::kRounds; ++x) {
+          const int first = first0 + x * kGroupRows, r = row0 + x * kGroupRows;
+          if (x >= k.rounds || first >= k.len || max(0, first - k.before) * a.G >= m0 + COLS) break;  // none of these queries sees the tile
+          const int buf = mine * P::kBuffers + (done & (P::kBuffers - 1));
+          go = wait(&bars.s_full[buf], (done / P::kBuffers) & 1);
           if (!go) break;
           ++done;
           fence_after();
           // whether every column is a query row that sees all rows of the tile
-          const bool all = m0 + cols <= k.used && sees >= first + kTile - 1;
+          const bool all = m0 + cols <= k.used && max(0, first + kTile - 1 - k.before) * a.G <= m0;
           const int lo = max(0, r - k.before) * a.G - m0, hi = k.used - m0;  // the columns that see row r
           float s[4] = {0.f, 0.f, 0.f, 0.f};
           auto use = [&]<bool ALL>(const uint32_t (&z)[16], int col) {
@@ -424,21 +456,25 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             for (int e = 0; e < 16; e += 4) {
               const float4 r4 = *reinterpret_cast<const float4*>(ref + col + e);
               float y[4] = {__uint_as_float(z[e]), __uint_as_float(z[e + 1]), __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3])};
-              add2(y[0], y[1], r4.x, r4.y);
-              add2(y[2], y[3], r4.z, r4.w);
+              y[0] += r4.x;
+              y[1] += r4.y;
+              y[2] += r4.z;
+              y[3] += r4.w;
 #pragma unroll
               for (int f = 0; f < 4; ++f) {
                 y[f] = ex2(y[f]);
                 if (!ALL) y[f] = col + e + f >= lo && col + e + f < hi ? y[f] : 0.f;
               }
-              add2(s[0], s[1], y[0], y[1]);
-              add2(s[2], s[3], y[2], y[3]);
+              s[0] += y[0];
+              s[1] += y[1];
+              s[2] += y[2];
+              s[3] += y[3];
             }
           };
-          const uint32_t from = tmem + buf * kCols + lanes;
+          const uint32_t from = tmem + buf * COLS + lanes;
           auto add = [&]<bool ALL>() {
 #pragma unroll
-            for (int col = 0; col < kCols; col += 32) {
+            for (int col = 0; col < COLS; col += 32) {
               if (col >= cols) break;
               uint32_t y[16], z[16];
               const bool second = col + 16 < cols;
@@ -464,12 +500,12 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         }
         __threadfence_block();  // the references have been read
         __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.q_empty[n % kQuerySlots]);
+        if (lane == 0) mbar_arrive(&bars.r_empty[n % kRefSlots]);
       }
       if (!go) break;
 #pragma unroll
-      for (int x = 0; x < kRounds; ++x) {
-        const int r = k.r0 + x * kGroupRows + mine * kTile + wq * 32 + lane;
+      for (int x = 0; x < P::kRounds; ++x) {
+        const int r = row0 + x * kGroupRows;
         if (page[x] >= 0 && page[x] < c.n_pages) out[r] = old[x] + sum[x];
       }
     }
@@ -477,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == kIssuer) tmem_free(tmem, kBuffers * kCols);
+  if (warp == kIssuer) tmem_free(tmem, 512);
 }
 
 // K of all layers as rows of 64 values, [layers][pages * heads * rows]; a copy takes `box` rows.
@@ -495,13 +531,19 @@ cudaError_t map_layers(CUtensorMap* m, const CacheDev& c, int box) {
 
 }  // namespace
 
-cudaError_t launch_weigh_tc(const WeighArgs& a, cudaStream_t stream) {
-  cudaError_t e = allow_shared(weigh_tc_kernel, kSchedule + TcSchedule::bytes(kMaxSeqs));
+template <int COLS>
+static cudaError_t launch(const WeighArgs& a, cudaStream_t stream) {
+  using P = Shape<COLS>;
+  cudaError_t e = allow_shared(weigh_tc_kernel<COLS>, P::kSchedule + TcSchedule::bytes(kMaxSeqs));
   if (e != cudaSuccess) return e;
   CUtensorMap map;
   e = map_layers(&map, a.c, a.c.P < kTile ? a.c.P : kTile);
   if (e != cudaSuccess) return e;
-  return launch_second(weigh_tc_kernel, dim3(152), kThreads, kSchedule + TcSchedule::bytes(a.B), stream, a, map);  // one block an SM
+  return launch_second(weigh_tc_kernel<COLS>, dim3(152), kThreads, P::kSchedule + TcSchedule::bytes(a.B), stream, a, map);  // one block an SM
+}
+
+cudaError_t launch_weigh_tc(const WeighArgs& a, cudaStream_t stream) {
+  return a.G * a.T <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
 }
 
 }  // namespace fibattn
