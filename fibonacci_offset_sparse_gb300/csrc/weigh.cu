@@ -67,6 +67,12 @@ __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_c
       if (t == 0) a.refs[task * a.mpad + m] = ref;
       const int r = m & 7;
       if constexpr (sizeof(DT) == 2) {
+        if (t < 2) {  // an infinite one has no rest
+          const float hi = __bfloat162float(__float2bfloat16_rn(ref)), left = isfinite(hi) ? ref - hi : 0.f;
+          const float mid = __bfloat162float(__float2bfloat16_rn(left));
+          *reinterpret_cast<uint4*>(a.ref_parts + (task * (a.mpad / 8) + m / 8) * kRefGroupBytes + t * 128 + r * 16) =
+              t == 0 ? make_uint4(pack_bf2_rn(hi, mid), pack_bf2_rn(left - mid, 0.f), 0, 0) : make_uint4(0, 0, 0, 0);
+        }
         unsigned char* at = a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes + r * 128;
 #pragma unroll
         for (int part = 0; part < 3; ++part) {
@@ -423,7 +429,8 @@ int padded(int rows) { return rows <= 8 ? 8 : (rows + 63) / 64 * 64; }
 
 size_t weigh_workspace_bytes(const fib_attn_cache& c, int B, int Hq, int T) {
   const size_t tasks = static_cast<size_t>(c.n_layers) * B * c.heads, mpad = padded(Hq / c.heads * T);
-  return 256 + round_up(tasks * mpad * sizeof(float)) + tasks * (mpad / 8) * (c.dtype == FIB_DTYPE_F32 ? kGroupBytes32 : kGroupBytes);
+  return 256 + round_up(tasks * mpad * sizeof(float)) +
+         tasks * (mpad / 8) * (c.dtype == FIB_DTYPE_F32 ? kGroupBytes32 : kGroupBytes + kRefGroupBytes);
 }
 
 cudaError_t launch_cache_weigh(const fib_attn_cache& cache, int B, int Hq, int T, int rows, int n_max, const int32_t* n_new, const int32_t* path,
@@ -454,6 +461,7 @@ cudaError_t launch_cache_weigh(const fib_attn_cache& cache, int B, int Hq, int T
   a.refs = reinterpret_cast<float*>(at);
   at += round_up(static_cast<size_t>(cache.n_layers) * B * cache.heads * a.mpad * sizeof(float));
   a.parts = at;
+  a.ref_parts = at + static_cast<size_t>(cache.n_layers) * B * cache.heads * (a.mpad / 8) * kGroupBytes;
   a.wait_ns = wait_ns;
   a.skip_copy = skip_copy;
   return cache.dtype == FIB_DTYPE_F32 ? launch<float>(a, stream) : launch<__nv_bfloat16>(a, stream);

@@ -3,7 +3,8 @@
 //
 // A tile is 128 rows of K, as TMA leaves them (K-major, 128-byte swizzle), times up to 128 query rows of the split query, all three parts
 // added up into one accumulator of tensor memory: S [128 rows x queries].  There a thread has a row, so its sum is a loop over its columns:
-//   one load from tensor memory, one add (a pair at a time), one exp2, one add; no shuffle.
+//   one load from tensor memory, one exp2, one add; no shuffle.  (That -lse is added by one more product, ones times its parts: with an add
+//   and a read of lse a column the warps that sum were what bounded it.)
 // A task is up to four tiles of a sequence, layer and head, which stay in shared memory while its queries pass by (those that see the
 // tile), or, where there are 64 at most, eight tiles that pass by the queries.  Blocks take tasks as they come, so that those of
 // prompts, which cost from 4 products to hundreds, fill all SMs.  A row's sum is one thread's, in the order of the queries, whichever block it is.
@@ -26,7 +27,7 @@ namespace {
 
 constexpr int kTile = 128, kTiles = 4, kGroupRows = kTile * kTiles;  // rows of a round
 constexpr int kTileBytes = kTile * kD * 2;
-constexpr int kRefSlots = 4, kRefBytes = 512;
+constexpr int kOnesBytes = kTile * 16 * 2;  // 128 rows of 1 1 1 0 ..., whose product with the references' parts is each of them
 constexpr int kSumWarps = 4 * kTiles, kIssuer = kSumWarps, kFeedK = kIssuer + kTiles, kTasks = kFeedK + kTiles, kFeedQ = kTasks + 1;
 constexpr int kThreads = 32 * (kFeedQ + 1);
 
@@ -37,10 +38,10 @@ template <int COLS>
 struct Shape {
   static constexpr int kRounds = COLS == 64 ? 2 : 1;
   static constexpr int kBuffers = 512 / (kTiles * COLS);  // of tensor memory, a tile
-  static constexpr int kSlots = COLS == 64 ? 2 * kTiles : kTiles + 2, kQuerySlots = COLS == 64 ? 3 : 2;
-  static constexpr int kQuerySlot = COLS / 8 * kGroupBytes;
-  static constexpr int kQueries = kSlots * kTileBytes, kRefs = kQueries + kQuerySlots * kQuerySlot, kSchedule = kRefs + kRefSlots * kRefBytes;
-  static_assert(kQuerySlot % 1024 == 0 && COLS * 4 <= kRefBytes, "layout");
+  static constexpr int kSlots = COLS == 64 ? 2 * kTiles : kTiles + 2, kQuerySlots = 2;
+  static constexpr int kQueryRefs = COLS / 8 * kGroupBytes, kQuerySlot = kQueryRefs + COLS / 8 * kRefGroupBytes;  // a slot: queries, references
+  static constexpr int kQueries = kSlots * kTileBytes, kOnes = kQueries + kQuerySlots * kQuerySlot, kSchedule = kOnes + kOnesBytes;
+  static_assert(kQuerySlot % 1024 == 0, "layout");
   // Tile t's slots: this one and, where there is one, the next.
   __device__ __forceinline__ static int slot(int t) { return COLS == 64 || t < 2 ? 2 * t : t + 2; }
   __device__ __forceinline__ static int slots(int t) { return COLS == 64 || t < 2 ? 2 : 1; }
@@ -57,8 +58,7 @@ struct TcTask {
 // round ahead from one that is not.
 struct TcBars {
   uint64_t k_full[2 * kTiles], k_empty[2 * kTiles];
-  uint64_t q_full[3], q_empty[3];
-  uint64_t r_full[kRefSlots], r_empty[kRefSlots];
+  uint64_t q_full[2], q_empty[2];
   uint64_t s_full[2 * kTiles], s_empty[2 * kTiles];
   uint64_t t_full[2], t_empty[2];
   uint64_t drained;
@@ -210,10 +210,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       mbar_init(&bars.q_full[s], 1);
       mbar_init(&bars.q_empty[s], kTiles);
     }
-    for (int s = 0; s < kRefSlots; ++s) {
-      mbar_init(&bars.r_full[s], 1);
-      mbar_init(&bars.r_empty[s], kSumWarps);
-    }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&bars.t_full[s], 1);
       mbar_init(&bars.t_empty[s], 1 + 2 * kTiles + kSumWarps);
@@ -225,6 +221,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     mbar_init(&bars.drained, kTiles);
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
+  for (int i = tid; i < kOnesBytes / 16; i += kThreads)  // [16][2][8] words of a row's 8 values
+    *reinterpret_cast<uint4*>(smem + P::kOnes + 16 * i) = i & 8 ? make_uint4(0, 0, 0, 0) : make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
+  fence_smem();
   for (int b = tid; b < a.B; b += kThreads) {
     bool ok;
     const WeighSeq s = weigh_seq(a, b, &ok);
@@ -296,25 +295,23 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       const size_t m = ((static_cast<size_t>(k.l) * a.B + k.b) * c.H + k.h) * a.mpad;
       const int c1 = chunks<COLS>(k);
       for (int ch = first_chunk<COLS>(a, k, k.r0); ch < c1; ++ch, ++n) {
-        const int slot = n % P::kQuerySlots, ref = n % kRefSlots, cols = columns<COLS>(k, ch);
-        go = wait(&bars.q_empty[slot], ((n / P::kQuerySlots) & 1) ^ 1) && wait(&bars.r_empty[ref], ((n / kRefSlots) & 1) ^ 1);
+        const int slot = n % P::kQuerySlots, cols = columns<COLS>(k, ch);
+        go = wait(&bars.q_empty[slot], ((n / P::kQuerySlots) & 1) ^ 1);
         if (!go) break;
         if (lane == 0) {
-          const size_t at = m + static_cast<size_t>(ch) * COLS;
-          mbar_arrive_tx(&bars.q_full[slot], cols / 8 * kGroupBytes);
-          bulk_g2s(smem + P::kQueries + slot * P::kQuerySlot, a.parts + at / 8 * kGroupBytes, cols / 8 * kGroupBytes, &bars.q_full[slot]);
-          mbar_arrive_tx(&bars.r_full[ref], cols * 4);
-          bulk_g2s(smem + P::kRefs + ref * kRefBytes, a.refs + at, cols * 4, &bars.r_full[ref]);
+          unsigned char* to = smem + P::kQueries + slot * P::kQuerySlot;
+          const size_t at = (m + static_cast<size_t>(ch) * COLS) / 8;
+          mbar_arrive_tx(&bars.q_full[slot], cols / 8 * (kGroupBytes + kRefGroupBytes));
+          bulk_g2s(to, a.parts + at * kGroupBytes, cols / 8 * kGroupBytes, &bars.q_full[slot]);
+          bulk_g2s(to + P::kQueryRefs, a.ref_parts + at * kRefGroupBytes, cols / 8 * kRefGroupBytes, &bars.q_full[slot]);
         }
         __syncwarp();
       }
       release(tc);
     }
     // nothing may be in flight when the block ends
-    if (lane == 0) {
+    if (lane == 0)
       for (int x = max(0, n - P::kQuerySlots); x < n; ++x) mbar_wait(&bars.q_full[x % P::kQuerySlots], (x / P::kQuerySlots) & 1, kDrainNs);
-      for (int x = max(0, n - kRefSlots); x < n; ++x) mbar_wait(&bars.r_full[x % kRefSlots], (x / kRefSlots) & 1, kDrainNs);
-    }
     __syncwarp();
   } else if (warp >= kFeedK && warp < kFeedK + kTiles) {
     // =================================================================== copies of rows: tile t of each round
@@ -357,10 +354,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
     // Descriptors count 16 bytes: 32 bytes on a k step, a part's 1024 on a part.
     constexpr uint32_t kLead = 16 / 16 << 16, kRowsHigh = 1024 / 16 | 1u << 14 | 2u << 29, kQueryHigh = kGroupBytes / 16 | 1u << 14 | 2u << 29;
+    // Ones and references without swizzle: 8 rows of 16 bytes, their other half of k 128 bytes on, 8 more rows 256.
+    constexpr uint32_t kPlainLead = 128 / 16 << 16, kPlainHigh = kRefGroupBytes / 16 | 1u << 14;
     auto at = [](uint32_t high, uint32_t low) { return static_cast<uint64_t>(high) << 32 | low; };
     const int t = same(warp - kIssuer);
     const int slots = P::slots(t), slot0 = P::slot(t), buf0 = t * P::kBuffers;
-    const uint32_t rows0 = (base + slot0 * kTileBytes) >> 4 | kLead, query0 = (base + P::kQueries) >> 4 | kLead, out0 = tmem + buf0 * COLS;
+    const uint32_t rows0 = (base + slot0 * kTileBytes) >> 4 | kLead, query0 = (base + P::kQueries) >> 4 | kLead, refs0 = (base + P::kQueries + P::kQueryRefs) >> 4 | kPlainLead,
+                   ones = (base + P::kOnes) >> 4 | kPlainLead, out0 = tmem + buf0 * COLS;
     int qs = 0, q_round = 0, filled = 0, done = 0;  // tiles copied, products made
     bool go = true;
     TcTask k;
@@ -376,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       for (int ch = c0; ch < c1 && go; ++ch) {
         go = wait(&bars.q_full[qs], q_round & 1);
         if (!go) break;
-        const uint32_t query = query0 + qs * (P::kQuerySlot / 16), desc = product_of(kTile, ch == c1 - 1 ? last : COLS, false, false);
+        const uint32_t query = query0 + qs * (P::kQuerySlot / 16), refs = refs0 + qs * (P::kQuerySlot / 16), desc = product_of(kTile, ch == c1 - 1 ? last : COLS, false, false);
 #pragma unroll
         for (int x = 0; x < P::kRounds; ++x) {
           if (from[x] > ch) break;
@@ -393,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
 #pragma unroll
               for (int y = 0; y < 4; ++y)
                 mma_tc(d, at(kRowsHigh, rows + 2 * y), at(kQueryHigh, query + part * (kPartBytes / 16) + 2 * y), desc, part < 2 || y > 0);
+            mma_tc(d, at(kPlainHigh, ones), at(kPlainHigh, refs), desc, true);  // (the last: a sum is cut where it is added to)
             commit_tc(&bars.s_full[buf0 + buf]);
             if (ch == c1 - 1) commit_tc(&bars.k_empty[slot0 + slot]);
           }
@@ -415,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     // =================================================================== sums
     const int mine = warp >> 2, wq = warp & 3;  // the warp's tile of a round, and its 32 rows of that
     const uint32_t lanes = static_cast<uint32_t>(wq) << 21;
-    int n = 0, done = 0;
+    int done = 0;
     bool go = true;
     TcTask k;
     for (int tc = 0; go && read(tc, &k); ++tc) {
@@ -433,11 +434,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         page[x] = x < k.rounds && r < k.len ? __ldg(table + (r >> c.shift)) : -1;
       }
       const int c1 = chunks<COLS>(k);
-      for (int ch = first_chunk<COLS>(a, k, k.r0); ch < c1 && go; ++ch, ++n) {
+      for (int ch = first_chunk<COLS>(a, k, k.r0); ch < c1 && go; ++ch) {
         const int cols = columns<COLS>(k, ch), m0 = ch * COLS;
-        const float* ref = reinterpret_cast<const float*>(smem + P::kRefs + n % kRefSlots * kRefBytes);
-        go = wait(&bars.r_full[n % kRefSlots], (n / kRefSlots) & 1);
-        if (!go) break;
 #pragma unroll
         for (int x = 0; x < P::kRounds; ++x) {
           const int first = first0 + x * kGroupRows, r = row0 + x * kGroupRows;
@@ -454,12 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           auto use = [&]<bool ALL>(const uint32_t (&z)[16], int col) {
 #pragma unroll
             for (int e = 0; e < 16; e += 4) {
-              const float4 r4 = *reinterpret_cast<const float4*>(ref + col + e);
               float y[4] = {__uint_as_float(z[e]), __uint_as_float(z[e + 1]), __uint_as_float(z[e + 2]), __uint_as_float(z[e + 3])};
-              y[0] += r4.x;
-              y[1] += r4.y;
-              y[2] += r4.z;
-              y[3] += r4.w;
 #pragma unroll
               for (int f = 0; f < 4; ++f) {
                 y[f] = ex2(y[f]);
@@ -498,9 +491,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           if (isnan(part) && r < k.len) part = add_infinite(a, k, r, max(m0, m0 + lo), min(m0 + cols, k.used));
           sum[x] += part;
         }
-        __threadfence_block();  // the references have been read
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.r_empty[n % kRefSlots]);
       }
       if (!go) break;
 #pragma unroll
