@@ -65,6 +65,7 @@ struct TcBars {
   TcTask task[2];
   uint32_t tmem;
   int err;
+  int issued[kTiles];  // chunks of queries that are past the products of the tile
 };
 
 // Rows of a task of a sequence with `used` query rows.
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     s_err = 0;
+    for (int t = 0; t < kTiles; ++t) bars.issued[t] = 0;
     for (int s = 0; s < P::kSlots; ++s) {
       mbar_init(&bars.k_full[s], 1);
       mbar_init(&bars.k_empty[s], 1);
@@ -361,7 +363,21 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     const int slots = P::slots(t), slot0 = P::slot(t), buf0 = t * P::kBuffers;
     const uint32_t rows0 = (base + slot0 * kTileBytes) >> 4 | kLead, query0 = (base + P::kQueries) >> 4 | kLead, refs0 = (base + P::kQueries + P::kQueryRefs) >> 4 | kPlainLead,
                    ones = (base + P::kOnes) >> 4 | kPlainLead, out0 = tmem + buf0 * COLS;
-    int qs = 0, q_round = 0, filled = 0, done = 0;  // tiles copied, products made
+    // With one buffer a tile the tiles go in order, so that a tile's scores are there while the next one's are made: side by side those of all
+    // four were there together, then all sums were formed, and prompts of 2048 took 59 us.
+    constexpr bool kInTurn = P::kBuffers == 1;
+    volatile int* issued = bars.issued;
+    auto turn = [&](int step) {  // the tile before this one is past chunk `step` of the block
+      const unsigned long long since = global_ns();
+      while (issued[t - 1] <= step && !s_err) {
+        if (global_ns() - since > a.wait_ns) {
+          s_err = 1;
+          if (lane == 0) atomicExch(a.status, kStatusTimeout);
+        }
+      }
+      return __all_sync(0xffffffffu, !s_err);
+    };
+    int qs = 0, q_round = 0, filled = 0, done = 0, step = 0;  // tiles copied, products made, chunks
     bool go = true;
     TcTask k;
     for (int tc = 0; go && read(tc, &k); ++tc) {
@@ -384,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           const int slot = filled & (slots - 1), buf = done & (P::kBuffers - 1);
           if (ch == max(from[x], c0)) go = wait(&bars.k_full[slot0 + slot], (filled / slots) & 1);
           if (go) go = wait(&bars.s_empty[buf0 + buf], ((done / P::kBuffers) & 1) ^ 1);
+          if (kInTurn && go && t > 0) go = turn(step);
           if (!go) break;
           fence_after();
           const uint32_t rows = rows0 + slot * (kTileBytes / 16), d = out0 + buf * COLS;
@@ -400,6 +417,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           ++done;
           if (ch == c1 - 1) ++filled;
         }
+        ++step;
+        if (kInTurn && lane == 0) issued[t] = step;
         if (go && one_lane()) commit_tc(&bars.q_empty[qs]);
         if (++qs == P::kQuerySlots) {
           qs = 0;
