@@ -24,79 +24,79 @@ __device__ __forceinline__ float tf32_of(float x) {
   return __uint_as_float(y);
 }
 
-// A quad a query row (of mpad, those behind the last one as 0): block (layer and sequence, 32 rows, head).
+// A quad a query row (of mpad, those behind the last one as 0): block (layer and sequence, 32 rows of its heads after one another).
 template <typename DT>
 __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_constant__ WeighArgs a) {
   let_second_start();
   const int t = threadIdx.x & 3, l = blockIdx.x / a.B, b = blockIdx.x % a.B;
-  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) *a.next = 0;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *a.next = 0;
   bool ok;
   const WeighSeq s = weigh_seq(a, b, &ok);
   if (!ok && threadIdx.x == 0) atomicExch(a.status, kStatusDeviceAssert);
   if (s.n == 0) return;
-  const int used = s.n * a.G;
-  for (int h = blockIdx.z; h < a.c.H; h += gridDim.z) {
+  const int used = s.n * a.G, most = (used + 63) / 64 * 64;  // (no tile reaches behind these)
+  const long long rows = static_cast<long long>(a.c.H) * a.mpad, step = static_cast<long long>(gridDim.y) * (kPrepThreads / 4);
+  for (long long item = static_cast<long long>(blockIdx.y) * (kPrepThreads / 4) + (threadIdx.x >> 2); item < rows; item += step) {
+    const int h = static_cast<int>(item / a.mpad), m = static_cast<int>(item - static_cast<long long>(h) * a.mpad);
+    if (m >= most) continue;
     const size_t task = (static_cast<size_t>(l) * a.B + b) * a.c.H + h;
-    for (int m = blockIdx.y * (kPrepThreads / 4) + (threadIdx.x >> 2); m < a.mpad; m += gridDim.y * (kPrepThreads / 4)) {
-      if (m >= (used + 63) / 64 * 64) break;  // (no tile reaches behind these)
-      const int i = m / a.G, g = m - i * a.G;
-      int node = i;
-      bool live = m < used;
-      if (live && a.path != nullptr) {
-        node = a.path[static_cast<size_t>(b) * a.T + i];
-        if (node < 0 || node >= a.T) {
-          live = false;
-          atomicExch(a.status, kStatusDeviceAssert);
-        }
+    const int i = m / a.G, g = m - i * a.G;
+    int node = i;
+    bool live = m < used;
+    if (live && a.path != nullptr) {
+      node = a.path[static_cast<size_t>(b) * a.T + i];
+      if (node < 0 || node >= a.T) {
+        live = false;
+        atomicExch(a.status, kStatusDeviceAssert);
       }
-      float x[16];
-      float ref = -INFINITY;
-      if (live) {
-        const size_t row = ((static_cast<size_t>(l) * a.B + b) * a.Hq + h * a.G + g) * a.T + node;
-        float2 e[8];
-        load_part(static_cast<const DT*>(a.q) + row * kD, t, x);
-        rope_row(a.rope_lo, a.rope_hi, s.len - s.n + i, t, e);
-        rotate_part(x, e, false);
-        ref = -a.lse[row] * kLog2e;
+    }
+    float x[16];
+    float ref = -INFINITY;
+    if (live) {
+      const size_t row = ((static_cast<size_t>(l) * a.B + b) * a.Hq + h * a.G + g) * a.T + node;
+      float2 e[8];
+      load_part(static_cast<const DT*>(a.q) + row * kD, t, x);
+      rope_row(a.rope_lo, a.rope_hi, s.len - s.n + i, t, e);
+      rotate_part(x, e, false);
+      ref = -a.lse[row] * kLog2e;
 #pragma unroll
-        for (int u = 0; u < 16; ++u) x[u] *= kLog2e / 8.0f;
-      } else {
+      for (int u = 0; u < 16; ++u) x[u] *= kLog2e / 8.0f;
+    } else {
 #pragma unroll
-        for (int u = 0; u < 16; ++u) x[u] = 0.f;
+      for (int u = 0; u < 16; ++u) x[u] = 0.f;
+    }
+    if (t == 0) a.refs[task * a.mpad + m] = ref;
+    const int r = m & 7;
+    if constexpr (sizeof(DT) == 2) {
+      if (t < 2) {  // an infinite one has no rest
+        const float hi = __bfloat162float(__float2bfloat16_rn(ref)), left = isfinite(hi) ? ref - hi : 0.f;
+        const float mid = __bfloat162float(__float2bfloat16_rn(left));
+        *reinterpret_cast<uint4*>(a.ref_parts + (task * (a.mpad / 8) + m / 8) * kRefGroupBytes + t * 128 + r * 16) =
+            t == 0 ? make_uint4(pack_bf2_rn(hi, mid), pack_bf2_rn(left - mid, 0.f), 0, 0) : make_uint4(0, 0, 0, 0);
       }
-      if (t == 0) a.refs[task * a.mpad + m] = ref;
-      const int r = m & 7;
-      if constexpr (sizeof(DT) == 2) {
-        if (t < 2) {  // an infinite one has no rest
-          const float hi = __bfloat162float(__float2bfloat16_rn(ref)), left = isfinite(hi) ? ref - hi : 0.f;
-          const float mid = __bfloat162float(__float2bfloat16_rn(left));
-          *reinterpret_cast<uint4*>(a.ref_parts + (task * (a.mpad / 8) + m / 8) * kRefGroupBytes + t * 128 + r * 16) =
-              t == 0 ? make_uint4(pack_bf2_rn(hi, mid), pack_bf2_rn(left - mid, 0.f), 0, 0) : make_uint4(0, 0, 0, 0);
-        }
-        unsigned char* at = a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes + r * 128;
+      unsigned char* at = a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes + r * 128;
 #pragma unroll
-        for (int part = 0; part < 3; ++part) {
-          uint32_t w[8];
+      for (int part = 0; part < 3; ++part) {
+        uint32_t w[8];
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            w[u] = pack_bf2_rn(x[2 * u], x[2 * u + 1]);
-            x[2 * u] -= bf_lo(w[u]);
-            x[2 * u + 1] -= bf_hi(w[u]);
-          }
-          *reinterpret_cast<uint4*>(at + part * kPartBytes + ((t ^ r) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          *reinterpret_cast<uint4*>(at + part * kPartBytes + (((t + 4) ^ r) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
+        for (int u = 0; u < 8; ++u) {
+          w[u] = pack_bf2_rn(x[2 * u], x[2 * u + 1]);
+          x[2 * u] -= bf_lo(w[u]);
+          x[2 * u + 1] -= bf_hi(w[u]);
         }
-      } else {
-        float* at = reinterpret_cast<float*>(a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes32) + r * kD;
-        float hi[16], lo[16];
-#pragma unroll
-        for (int u = 0; u < 16; ++u) {
-          hi[u] = tf32_of(x[u]);
-          lo[u] = tf32_of(x[u] - hi[u]);
-        }
-        store_part(at, t, hi);
-        store_part(at + 8 * kD, t, lo);
+        *reinterpret_cast<uint4*>(at + part * kPartBytes + ((t ^ r) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        *reinterpret_cast<uint4*>(at + part * kPartBytes + (((t + 4) ^ r) << 4)) = make_uint4(w[4], w[5], w[6], w[7]);
       }
+    } else {
+      float* at = reinterpret_cast<float*>(a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes32) + r * kD;
+      float hi[16], lo[16];
+#pragma unroll
+      for (int u = 0; u < 16; ++u) {
+        hi[u] = tf32_of(x[u]);
+        lo[u] = tf32_of(x[u] - hi[u]);
+      }
+      store_part(at, t, hi);
+      store_part(at + 8 * kD, t, lo);
     }
   }
 }
@@ -117,12 +117,14 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // A lane's fragments.  Lane (g, t) = (lane / 4, lane % 4).
-template <typename DT>
+// kOne: 8 query rows at most, whose fragments stay in registers; kFew: 2 at most, whose parts are columns of one product; kMany: any number.
+enum Rows { kFew, kOne, kMany };
+template <typename DT, Rows ROWS>
 struct Frag;
-template <>
-struct Frag<__nv_bfloat16> {
+template <Rows ROWS>
+struct Frag<__nv_bfloat16, ROWS> {
   static constexpr int kTiles = 2, kWords = 2;  // 16-byte words of a row that a lane holds: dims 8t .., 32+8t ..
-  static constexpr int kGroup = kGroupBytes;
+  static constexpr int kGroup = kGroupBytes, kPer = 2;  // queries of a lane's scores
   uint4 q[3][2];
   __device__ __forceinline__ static int word(int t, int k) { return t + 4 * k; }
   __device__ __forceinline__ void load(const unsigned char* group, int g, int t) {
@@ -131,9 +133,11 @@ struct Frag<__nv_bfloat16> {
 #pragma unroll
       for (int k = 0; k < 2; ++k) q[p][k] = *reinterpret_cast<const uint4*>(group + p * kPartBytes + g * 128 + ((word(t, k) ^ g) << 4));
   }
-  // Scores of 16 rows (x0: row g, x1: row g + 8) and 8 queries; upper: of the queries' upper part alone.
-  __device__ __forceinline__ void scores(const uint4 (&x0)[2], const uint4 (&x1)[2], float (&c)[4], bool upper) const {
-    c[0] = c[1] = c[2] = c[3] = 0.f;
+  __device__ __forceinline__ static int query(int t, int j) { return 2 * t + j; }
+  __device__ __forceinline__ static float add_up(float x) { return quad_sum(x); }  // over a quad's queries
+  // Scores of 16 rows (x0: row g, x1: row g + 8) and 8 queries, y[row][query]; upper: of the queries' upper part alone.
+  __device__ __forceinline__ void scores(const uint4 (&x0)[2], const uint4 (&x1)[2], float (&y)[2][2], bool upper) const {
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int p = 2; p >= 0; --p) {
       if (upper && p > 0) continue;
@@ -142,12 +146,42 @@ struct Frag<__nv_bfloat16> {
       mma_bf16(c, x0[0].z, x1[0].z, x0[1].z, x1[1].z, q[p][0].z, q[p][1].z);
       mma_bf16(c, x0[0].w, x1[0].w, x0[1].w, x1[1].w, q[p][0].w, q[p][1].w);
     }
+    y[0][0] = c[0]; y[0][1] = c[1]; y[1][0] = c[2]; y[1][1] = c[3];
   }
 };
+// Columns 0, 1, 2 of the product are the first query's hi, mid, lo, 4, 5, 6 the second's: a third of the products, and one score a row and
+// lane (of query t / 2) where there are two.  A token of 32 sequences of up to 2048 rows, 16 layers: 132 us, with the other 141.
 template <>
-struct Frag<float> {
+struct Frag<__nv_bfloat16, kFew> {
+  static constexpr int kTiles = 2, kWords = 2;
+  static constexpr int kGroup = kGroupBytes, kPer = 1;
+  uint4 q[2];
+  __device__ __forceinline__ static int word(int t, int k) { return t + 4 * k; }
+  __device__ __forceinline__ void load(const unsigned char* group, int g, int t) {
+    const int part = g & 3, row = g >> 2;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      q[k] = part < 3 ? *reinterpret_cast<const uint4*>(group + part * kPartBytes + row * 128 + ((word(t, k) ^ row) << 4)) : make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ static int query(int t, int) { return t >> 1; }
+  __device__ __forceinline__ static float add_up(float x) { return x + __shfl_xor_sync(0xffffffffu, x, 2); }
+  __device__ __forceinline__ void scores(const uint4 (&x0)[2], const uint4 (&x1)[2], float (&y)[2][1], bool upper) const {
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
+    mma_bf16(c, x0[0].x, x1[0].x, x0[1].x, x1[1].x, q[0].x, q[1].x);
+    mma_bf16(c, x0[0].y, x1[0].y, x0[1].y, x1[1].y, q[0].y, q[1].y);
+    mma_bf16(c, x0[0].z, x1[0].z, x0[1].z, x1[1].z, q[0].z, q[1].z);
+    mma_bf16(c, x0[0].w, x1[0].w, x0[1].w, x1[1].w, q[0].w, q[1].w);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float part = c[2 * e] + c[2 * e + 1];  // hi + mid, or lo + 0
+      y[e][0] = upper ? __shfl_sync(0xffffffffu, c[2 * e], threadIdx.x & 30) : part + __shfl_xor_sync(0xffffffffu, part, 1);
+    }
+  }
+};
+template <Rows ROWS>
+struct Frag<float, ROWS> {
   static constexpr int kTiles = 1, kWords = 4;  // dims 16k + 4t .., k = 0 .. 3
-  static constexpr int kGroup = kGroupBytes32;
+  static constexpr int kGroup = kGroupBytes32, kPer = 2;
   uint4 q[2][4];
   __device__ __forceinline__ static int word(int t, int k) { return t + 4 * k; }
   __device__ __forceinline__ void load(const unsigned char* group, int g, int t) {
@@ -156,8 +190,10 @@ struct Frag<float> {
 #pragma unroll
       for (int k = 0; k < 4; ++k) q[p][k] = reinterpret_cast<const uint4*>(group)[(p * 8 + g) * 16 + word(t, k)];
   }
-  __device__ __forceinline__ void scores(const uint4 (&x0)[4], const uint4 (&x1)[4], float (&c)[4], bool upper) const {
-    c[0] = c[1] = c[2] = c[3] = 0.f;
+  __device__ __forceinline__ static int query(int t, int j) { return 2 * t + j; }
+  __device__ __forceinline__ static float add_up(float x) { return quad_sum(x); }
+  __device__ __forceinline__ void scores(const uint4 (&x0)[4], const uint4 (&x1)[4], float (&y)[2][2], bool upper) const {
+    float c[4] = {0.f, 0.f, 0.f, 0.f};
     float d[4] = {0.f, 0.f, 0.f, 0.f};  // the large products
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -182,7 +218,7 @@ struct Frag<float> {
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) c[e] += d[e];
+    for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = c[e] + d[e];
   }
 };
 
@@ -222,9 +258,10 @@ struct Cursor {
   }
 };
 
-template <typename DT, bool ONE>  // ONE: 8 query rows at most, whose fragments stay in registers
+template <typename DT, Rows ROWS>
 __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constant__ WeighArgs a) {
-  using F = Frag<DT>;
+  using F = Frag<DT, ROWS>;
+  constexpr bool ONE = ROWS != kMany;
   constexpr int TILES = F::kTiles, UNIT = 16 * TILES, ROW = kD * static_cast<int>(sizeof(DT));
   static_assert(UNIT * ROW == kUnitBytes, "a unit");
   extern __shared__ __align__(128) unsigned char s_ring[];  // [kWarps][kSlots][kUnitBytes]
@@ -298,21 +335,19 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
 
   Cursor k = begin;
   F q;
-  float ref[2];
-  int sees[2];  // the last row that the lane's two queries see
+  float ref[F::kPer];
+  int sees[F::kPer];  // the last row that the lane's queries see
   const unsigned char* parts = nullptr;
   const float* refs = nullptr;
   float* out = nullptr;
   int used = 0, before = 0;  // query row m sees rows up to before + m / G
   auto take = [&](int group) {
     q.load(parts + static_cast<size_t>(group) * F::kGroup, g, t);
-    const float2 r = *reinterpret_cast<const float2*>(refs + group * 8 + 2 * t);
-    ref[0] = r.x;
-    ref[1] = r.y;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int m = group * 8 + 2 * t + e;
-      sees[e] = m < used ? before + m / a.G : -1;
+    for (int j = 0; j < F::kPer; ++j) {
+      const int m = group * 8 + F::query(t, j);
+      ref[j] = refs[m];
+      sees[j] = m < used ? before + m / a.G : -1;
     }
   };
   for (int n = 0; k.next<UNIT>(a, s_start, &fresh); ++n) {
@@ -353,8 +388,8 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     const int groups = (used + 7) / 8;
     for (int group = ONE ? 0 : max(0, r0 - before) * a.G / 8; group < groups; ++group) {
       if (!ONE) take(group);
-      // whether some query of the group is none, or does not see every row of the unit
-      const bool all = group * 8 + 8 <= used && before + group * 8 / a.G >= r0 + UNIT - 1;
+      // whether every query that the product has room for is one, and sees every row of the unit
+      const bool all = group * 8 + (ROWS == kFew ? 2 : 8) <= used && before + group * 8 / a.G >= r0 + UNIT - 1;
       float part[2 * TILES];
       // A NaN may come of an infinite key, where the parts' products are infinities of opposite signs: the upper
       // part's alone keep the sign, and a second round takes them.
@@ -363,24 +398,26 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < TILES; ++i) {
-          float y[4];
+          float y[2][F::kPer];
           q.scores(x[i][0], x[i][1], y, false);
           if (round == 1) {
-            float z[4];
+            float z[2][F::kPer];
             q.scores(x[i][0], x[i][1], z, true);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = isnan(y[e]) ? z[e] : y[e];
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int j = 0; j < F::kPer; ++j) y[e][j] = isnan(y[e][j]) ? z[e][j] : y[e][j];
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float y0 = ex2(y[2 * e] + ref[0]), y1 = ex2(y[2 * e + 1] + ref[1]);
-            if (!all) {
-              const int r = r0 + 16 * i + 8 * e + g;
-              y0 = r <= sees[0] ? y0 : 0.f;
-              y1 = r <= sees[1] ? y1 : 0.f;
+            float given = 0.f;
+#pragma unroll
+            for (int j = 0; j < F::kPer; ++j) {
+              const float p = ex2(y[e][j] + ref[j]);
+              given += all || r0 + 16 * i + 8 * e + g <= sees[j] ? p : 0.f;
             }
-            part[2 * i + e] = y0 + y1;
-            bad |= isnan(y0 + y1);
+            part[2 * i + e] = given;
+            bad |= isnan(given);
           }
         }
         if (!__any_sync(0xffffffffu, bad)) break;
@@ -390,7 +427,7 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     }
     // value v of a quad's four lanes, added up, is row 8v + g's; lane t takes that of value t
 #pragma unroll
-    for (int v = 0; v < 2 * TILES; ++v) sum[v] = quad_sum(sum[v]);
+    for (int v = 0; v < 2 * TILES; ++v) sum[v] = F::add_up(sum[v]);
     float y = t == 0 ? sum[0] : sum[1];
     if constexpr (TILES == 2) y = t == 2 ? sum[2] : t == 3 ? sum[3] : y;
     if (writes && there) out[row] = old + y;
@@ -410,17 +447,17 @@ cudaError_t launch_rows(void (*kernel)(WeighArgs), const WeighArgs& a, cudaStrea
 
 template <typename DT>
 cudaError_t launch(const WeighArgs& a, cudaStream_t stream) {
-  const int z = a.c.H < 64 ? a.c.H : 64;
-  int y = (a.mpad + kPrepThreads / 4 - 1) / (kPrepThreads / 4);
-  if (y > 1024) y = 1024;
-  weigh_prep_kernel<DT><<<dim3(static_cast<unsigned>(a.c.L) * a.B, y, z), kPrepThreads, 0, stream>>>(a);
+  const long long blocks = (static_cast<long long>(a.c.H) * a.mpad + kPrepThreads / 4 - 1) / (kPrepThreads / 4);
+  const dim3 grid(static_cast<unsigned>(a.c.L) * a.B, static_cast<unsigned>(blocks < 32768 ? blocks : 32768));
+  weigh_prep_kernel<DT><<<grid, kPrepThreads, 0, stream>>>(a);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  if (a.G * a.T <= 8) return launch_rows(weigh_kernel<DT, true>, a, stream);
-  if constexpr (sizeof(DT) == 2)
-    return launch_weigh_tc(a, stream);
-  else
-    return launch_rows(weigh_kernel<DT, false>, a, stream);
+  if constexpr (sizeof(DT) == 2) {
+    if (a.G * a.T <= 2) return launch_rows(weigh_kernel<DT, kFew>, a, stream);
+    return a.G * a.T <= 8 ? launch_rows(weigh_kernel<DT, kOne>, a, stream) : launch_weigh_tc(a, stream);
+  } else {
+    return a.G * a.T <= 8 ? launch_rows(weigh_kernel<DT, kOne>, a, stream) : launch_rows(weigh_kernel<DT, kMany>, a, stream);
+  }
 }
 
 int padded(int rows) { return rows <= 8 ? 8 : (rows + 63) / 64 * 64; }
