@@ -3,8 +3,8 @@
 // y = amplitude * R(p) x; R is orthogonal a pair, so the transposed map (the backward pass) is the same kernel with the sine
 // negated.  e^{i p theta} is one complex product of two table entries (p = 64 hi + lo, both built in binary64), 1.2e-7 of error.
 //
-// What bounds it: the rows' bytes.  So a quad of threads takes a row as wide loads (each thread both halves of its pairs), reads
-// its eight factors once and uses them for several heads of the token; what is on its way at a time is kHeads rows a quad.
+// What bounds it: the rows' bytes.  So four threads (float32: eight) take a row as wide loads, each both halves of its pairs, read their
+// factors once and use them for several heads of the token; what is on its way at a time is HEADS rows a thread.
 #include "rotary.cuh"
 #include "tc_common.cuh"
 
@@ -23,13 +23,13 @@ __device__ __forceinline__ bool position(const RotaryArgs& a, int b, int n, int*
   return false;
 }
 
+// 16 bytes of a row, as they lie in memory.
 template <typename DT>
-struct Vec8;  // eight values, as they lie in memory
+struct Word;
 template <>
-struct Vec8<__nv_bfloat16> {
+struct Word<__nv_bfloat16> {
+  static constexpr int kValues = 8;
   uint4 x;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { x = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = x; }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = bf_lo(x.x); v[1] = bf_hi(x.x); v[2] = bf_lo(x.y); v[3] = bf_hi(x.y);
     v[4] = bf_lo(x.z); v[5] = bf_hi(x.z); v[6] = bf_lo(x.w); v[7] = bf_hi(x.w);
@@ -39,25 +39,29 @@ struct Vec8<__nv_bfloat16> {
   }
 };
 template <>
-struct Vec8<float> {
-  float4 x, y;
-  __device__ __forceinline__ void load(const float* p) {
-    x = reinterpret_cast<const float4*>(p)[0];
-    y = reinterpret_cast<const float4*>(p)[1];
+struct Word<float> {
+  static constexpr int kValues = 4;
+  uint4 x;
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+    v[0] = __uint_as_float(x.x); v[1] = __uint_as_float(x.y); v[2] = __uint_as_float(x.z); v[3] = __uint_as_float(x.w);
   }
-  __device__ __forceinline__ void store(float* p) const {
-    reinterpret_cast<float4*>(p)[0] = x;
-    reinterpret_cast<float4*>(p)[1] = y;
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-  }
-  __device__ __forceinline__ void set(const float (&v)[8]) {
-    x = make_float4(v[0], v[1], v[2], v[3]);
-    y = make_float4(v[4], v[5], v[6], v[7]);
+  __device__ __forceinline__ void set(const float (&v)[4]) {
+    x = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
   }
 };
+
+// e^{i p theta_m} of N pairs from m on (a multiple of 2), times the amplitude, the sine with its sign.
+template <int N>
+__device__ __forceinline__ void factors(const RotaryArgs& a, int p, int m, float2* e) {
+  const float4* h4 = reinterpret_cast<const float4*>(a.rope_hi + (p / kSplit) * kFreq + m);
+  const float4* l4 = reinterpret_cast<const float4*>(a.rope_lo + (p % kSplit) * kFreq + m);
+#pragma unroll
+  for (int u = 0; u < N / 2; ++u) {
+    const float4 x = __ldg(h4 + u), y = __ldg(l4 + u);
+    e[2 * u] = make_float2((x.x * y.x - x.y * y.y) * a.amp, (x.x * y.y + x.y * y.x) * (a.amp * a.sign));
+    e[2 * u + 1] = make_float2((x.z * y.z - x.w * y.w) * a.amp, (x.z * y.w + x.w * y.z) * (a.amp * a.sign));
+  }
+}
 
 constexpr int kThreads = 128;
 
@@ -73,58 +77,65 @@ __device__ __forceinline__ DT* row_out(const RotaryArgs& a, int b, int h, int n)
   return static_cast<DT*>(a.y[s]) + (b * a.ys[s][0] + at * a.ys[s][1] + n * a.ys[s][2]);
 }
 
-// A quad a token, HEADS heads; thread t of it holds 16 dims of each row, as two runs of eight: of INTERLEAVED pairs
-// 16t .. 16t+15, of rotate-half ones (rot_dim a multiple of 16) 8t .. and their partners, of what is only copied the
-// next 16 that no thread before it holds.
+// 4 (float32: 8) threads a token, HEADS heads; thread t holds two 16-byte words of each row: of rotate-half pairs (rot_dim a multiple of two
+// words) its t-th word of first dims and that of their partners, of what is only copied the next two that no thread before it holds; of
+// interleaved pairs word t of either half of the row.
 template <typename DT, int HEADS, bool INTERLEAVED>
 __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a) {
-  const int t = threadIdx.x & 3;
-  const long long item = static_cast<long long>(blockIdx.x) * (kThreads / 4) + (threadIdx.x >> 2);
+  constexpr int V = Word<DT>::kValues, LANES = kD / (2 * V);
+  const int t = threadIdx.x % LANES;
+  const long long item = static_cast<long long>(blockIdx.x) * (kThreads / LANES) + threadIdx.x / LANES;
   if (item >= static_cast<long long>(a.B) * a.N) return;
   const int b = static_cast<int>(item / a.N), n = static_cast<int>(item - static_cast<long long>(b) * a.N);
-  const int heads = a.heads[0] + a.heads[1], h0 = blockIdx.y * HEADS, turned = a.rot_dim / 16;
-  int at0, at1;
-  if (INTERLEAVED || t >= turned) {
-    at0 = 16 * t;
-    at1 = at0 + 8;
-  } else {
-    at0 = 8 * t;
-    at1 = a.rot_dim / 2 + 8 * t;
+  const int heads = a.heads[0] + a.heads[1], h0 = blockIdx.y * HEADS, turned = a.rot_dim / (2 * V);  // threads with rotate-half pairs
+  int at[2] = {V * t, kD / 2 + V * t};
+  if (!INTERLEAVED) {
+    at[0] = t < turned ? V * t : a.rot_dim + 2 * V * (t - turned);
+    at[1] = t < turned ? a.rot_dim / 2 + V * t : at[0] + V;
   }
-  Vec8<DT> v[HEADS][2];
+  Word<DT> v[HEADS][2];
 #pragma unroll
   for (int i = 0; i < HEADS; ++i)
     if (h0 + i < heads) {
       const DT* x = row_in<DT>(a, b, h0 + i, n);
-      v[i][0].load(x + at0);
-      v[i][1].load(x + at1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) v[i][k].x = *reinterpret_cast<const uint4*>(x + at[k]);
     }
   int p;
   if (!position(a, b, n, &p)) return;
-  // pairs 8t .. 8t+7, of which the first `pairs` are rotated
-  const int pairs = INTERLEAVED ? max(0, min(8, a.rot_dim / 2 - 8 * t)) : t < turned ? 8 : 0;
-  if (pairs > 0) {
-    float2 e[8];
-    rope_row(a.rope_lo, a.rope_hi, p, t, e);
+  float2 e[V];
+  if (INTERLEAVED) {
 #pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      e[u].x *= a.amp;
-      e[u].y *= a.amp * a.sign;
+    for (int k = 0; k < 2; ++k) {
+      if (at[k] >= a.rot_dim) break;
+      factors<V / 2>(a, p, at[k] / 2, e + k * V / 2);
+#pragma unroll
+      for (int i = 0; i < HEADS; ++i) {
+        float x[V];
+        v[i][k].get(x);
+#pragma unroll
+        for (int u = 0; u < V / 2; ++u) {
+          if (at[k] + 2 * u >= a.rot_dim) break;
+          const float2 f = e[k * V / 2 + u];
+          const float c = x[2 * u], d = x[2 * u + 1];
+          x[2 * u] = c * f.x - d * f.y;
+          x[2 * u + 1] = c * f.y + d * f.x;
+        }
+        v[i][k].set(x);
+      }
     }
+  } else if (t < turned) {
+    factors<V>(a, p, V * t, e);
 #pragma unroll
     for (int i = 0; i < HEADS; ++i) {
-      float x[8], y[8];
+      float x[V], y[V];
       v[i][0].get(x);
       v[i][1].get(y);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        float& c = INTERLEAVED ? (u < 4 ? x[2 * (u & 3)] : y[2 * (u & 3)]) : x[u];
-        float& d = INTERLEAVED ? (u < 4 ? x[2 * (u & 3) + 1] : y[2 * (u & 3) + 1]) : y[u];
-        const float c0 = c, d0 = d;
-        if (!INTERLEAVED || u < pairs) {
-          c = c0 * e[u].x - d0 * e[u].y;
-          d = c0 * e[u].y + d0 * e[u].x;
-        }
+      for (int u = 0; u < V; ++u) {
+        const float c = x[u], d = y[u];
+        x[u] = c * e[u].x - d * e[u].y;
+        y[u] = c * e[u].y + d * e[u].x;
       }
       v[i][0].set(x);
       v[i][1].set(y);
@@ -134,8 +145,8 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant_
   for (int i = 0; i < HEADS; ++i)
     if (h0 + i < heads) {
       DT* y = row_out<DT>(a, b, h0 + i, n);
-      v[i][0].store(y + at0);
-      v[i][1].store(y + at1);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) *reinterpret_cast<uint4*>(y + at[k]) = v[i][k].x;
     }
 }
 
@@ -164,9 +175,9 @@ __global__ void __launch_bounds__(kThreads) rotary_any_kernel(const __grid_const
   }
 }
 
-// Whether every row is made of aligned runs of eight.
+// Whether every row is made of aligned words that a thread has both halves of pairs of.
 bool wide(const RotaryArgs& a, int es) {
-  if (a.layout == FIB_ROPE_HALF && a.rot_dim % 16 != 0) return false;
+  if (a.layout == FIB_ROPE_HALF && a.rot_dim % (32 / es) != 0) return false;
   for (int s = 0; s < 2; ++s) {
     if (a.heads[s] == 0) continue;
     if (reinterpret_cast<uintptr_t>(a.x[s]) % 16 != 0 || reinterpret_cast<uintptr_t>(a.y[s]) % 16 != 0) return false;
@@ -181,7 +192,8 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t stream) {
   const long long items = static_cast<long long>(a.B) * a.N;
   const int heads = a.heads[0] + a.heads[1];
   if (wide(a, sizeof(DT))) {
-    const dim3 grid(static_cast<unsigned>((items + kThreads / 4 - 1) / (kThreads / 4)), (heads + HEADS - 1) / HEADS);
+    constexpr int kTokens = kThreads / (kD / (2 * Word<DT>::kValues));
+    const dim3 grid(static_cast<unsigned>((items + kTokens - 1) / kTokens), (heads + HEADS - 1) / HEADS);
     if (a.layout == FIB_ROPE_HALF)
       rotary_kernel<DT, HEADS, false><<<grid, kThreads, 0, stream>>>(a);
     else
@@ -196,7 +208,7 @@ cudaError_t launch(const RotaryArgs& a, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, int dtype, cudaStream_t stream) {
-  return dtype == FIB_DTYPE_F32 ? launch<float, 2>(a, stream) : launch<__nv_bfloat16, 4>(a, stream);
+  return dtype == FIB_DTYPE_F32 ? launch<float, 4>(a, stream) : launch<__nv_bfloat16, 4>(a, stream);
 }
 
 }  // namespace fibattn

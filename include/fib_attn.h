@@ -283,7 +283,7 @@ int fib_attn_rope_destroy(fib_attn_rope_t r);
  * call reads.  Values are rotated in float32 and rounded once.  A position outside [0, N_max)
  * records FIB_ERR_DEVICE_ASSERT in the handle's status word and leaves its rows unwritten.
  * 1 <= B, N; B * N < 2^31; 1 <= Hq <= FIB_MAX_HEADS; 0 <= Hk <= FIB_MAX_HEADS.  Pointers and
- * strides aligned to 16 bytes, and HALF with rot_dim a multiple of 16, take the wide path;
+ * strides aligned to 16 bytes, and HALF with rot_dim a multiple of 16 (float32: 8), take the wide path;
  * else elements are moved one by one (pointers aligned to the type).  Errors: FIB_ERR_INVALID_ARG,
  * FIB_ERR_CUDA.                                                                         */
 int fib_attn_rotary(fib_attn_rope_t r, int dtype, int B, int N, int Hq, int Hk, const void* q,
