@@ -138,10 +138,15 @@ int fib_attn_cache_compact(const fib_attn_cache* c, int32_t* remap, void* worksp
   return cuda_status(launch_cache_compact(*c, remap, workspace, static_cast<cudaStream_t>(stream)));
 }
 
-size_t fib_attn_cache_weigh_workspace_size(const fib_attn_cache* c, int B, int Hq, int T) {
-  if (check_cache(c) != FIB_OK || B < 1 || B > c->max_seqs || T < 1 || T > (1 << 20) || Hq < 1 || Hq > FIB_MAX_HEADS || Hq % c->heads != 0)
-    return 0;
+// What a call of these sizes needs; 0 where they break the rules.  (Query rows are held to 2^40 values, so that no size here leaves 64 bits.)
+static size_t weigh_bytes(const fib_attn_cache* c, int B, int Hq, int T) {
+  if (B < 1 || B > c->max_seqs || T < 1 || T > (1 << 20) || Hq < 1 || Hq > FIB_MAX_HEADS || Hq % c->heads != 0) return 0;
+  if (static_cast<long long>(c->n_layers) * B * Hq > (1LL << 40) / kD / T) return 0;
   return weigh_workspace_bytes(*c, B, Hq, T);
+}
+
+size_t fib_attn_cache_weigh_workspace_size(const fib_attn_cache* c, int B, int Hq, int T) {
+  return check_cache(c) == FIB_OK ? weigh_bytes(c, B, Hq, T) : 0;
 }
 
 int fib_attn_cache_weigh(fib_attn_plan_t p, const fib_attn_cache* c, int B, int Hq, int T, int rows, const int32_t* n_new,
@@ -149,11 +154,11 @@ int fib_attn_cache_weigh(fib_attn_plan_t p, const fib_attn_cache* c, int B, int 
                          size_t ws_bytes, void* stream) {
   int st = check_cache(c);
   if (st != FIB_OK) return st;
-  if (p == nullptr || B < 1 || B > c->max_seqs || T < 1 || T > (1 << 20) || rows < 1 || rows > (1 << 30)) return FIB_ERR_INVALID_ARG;
-  if (Hq < 1 || Hq > FIB_MAX_HEADS || Hq % c->heads != 0) return FIB_ERR_INVALID_ARG;
+  const size_t need = weigh_bytes(c, B, Hq, T);
+  if (p == nullptr || need == 0 || rows < 1 || rows > (1 << 30)) return FIB_ERR_INVALID_ARG;
   if (check_ints(n_new) || !aligned(path, 4) || !aligned(first, 4) || check_tensor(q)) return FIB_ERR_INVALID_ARG;
   if (lse == nullptr || !aligned(lse, 4) || weights == nullptr || !aligned(weights, 4) || weights == lse) return FIB_ERR_INVALID_ARG;
-  if (check_workspace(workspace, ws_bytes, weigh_workspace_bytes(*c, B, Hq, T))) return FIB_ERR_INVALID_ARG;
+  if (check_workspace(workspace, ws_bytes, need)) return FIB_ERR_INVALID_ARG;
   if (workspace == q || workspace == lse || workspace == weights) return FIB_ERR_INVALID_ARG;
   st = check_device(p);
   if (st == FIB_OK) st = check_cache_device(c);

@@ -59,6 +59,9 @@ def test_weigh_arguments(lib):  # noqa: F811
         x = {**good, **kw}
         assert lib.fib_attn_cache_weigh(1 << 12, p, x["B"], x["Hq"], x["T"], x["rows"], x["n"], x["path"], x["first"], x["q"], x["lse"], x["w"],
                                         x["ws"], x["size"], None) == fa.FIB_ERR_INVALID_ARG, kw
+    huge = ctypes.byref(struct(n_layers=256, max_seqs=1024, heads=1024, page_rows=16, n_pages=1))
+    assert lib.fib_attn_cache_weigh_workspace_size(huge, 1024, 1024, 65) == 0  # 2^40 values of queries at most
+    assert lib.fib_attn_cache_weigh_workspace_size(huge, 1024, 1024, 64) > 1 << 40
     with_bad = ctypes.byref(struct(heads=0))
     assert lib.fib_attn_cache_weigh_workspace_size(with_bad, 2, 8, 3) == 0
     assert lib.fib_attn_cache_weigh(1 << 12, with_bad, 2, 8, 3, 100, 16, None, None, 512, 16, 32, 256, need, None) == fa.FIB_ERR_INVALID_ARG

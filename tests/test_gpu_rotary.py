@@ -279,3 +279,38 @@ def test_a_training_step_through_both():
     # two float32 paths, each within 1e-5 (norm) of the same gradient
     assert float((x.grad - y.grad).norm()) <= 2e-5 * float(y.grad.norm())
     assert abs(float(alpha.grad - a2.grad)) <= 2e-4 * abs(float(a2.grad))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,Hq", [(1, 2), (5, 4), (12, 4)])
+def test_decodes_of_a_plan_that_does_not_rotate(dtype, T, Hq):
+    """Rows rotated by fib_attn_rotary at positions of their own (a cache that lost rows: 1000 behind), committed and decoded as they are, against
+    the oracle, which is given rows and queries turned back to the positions that it turns them to."""
+    from oracle import cache_oracle as co
+    from tests.test_gpu_cache import TOL_LSE, TOL_O, HALF, draw as cache_draw, i32, rng
+    r = rng(300, T, Hq)
+    B, H, P, lens = 2, 2, 16, [45, 20]
+    plan = fa.fib_attn_plan_create(fa.FIB_BASE_FIBONACCI, [1.0], 6, 100, fa.FIB_MODE_MASK)
+    fa.fib_attn_plan_set_rotation(plan, False)
+    rope = fa.fib_attn_rope_create(2000, rot_dim=32, layout=fa.FIB_ROPE_INTERLEAVED, scaling=fa.FIB_ROPE_NTK, factor=2.0)
+    cache = fa.fib_attn_cache_create(1, H, P, 12, B, 6, DT[dtype])
+    k, _ = cache_draw(r, (B, H, 45, 64), dtype)
+    v, _ = cache_draw(r, (B, H, 45, 64), dtype)
+    k = fa.fib_attn_rotary(rope, k, start=i32([1000, 1000]))[0]
+    fa.fib_attn_cache_commit(plan, cache, k[None], v[None], i32(lens))
+    assert torch.equal(cache.k[0, cache.table[0, 0].long()], k[0, :, :P])  # as they came
+    q, _ = cache_draw(r, (B, Hq, T, 64), dtype)
+    kn, _ = cache_draw(r, (B, H, T, 64), dtype)
+    vn, vf = cache_draw(r, (B, H, T, 64), dtype)
+    q, kn = fa.fib_attn_rotary(rope, q, kn, start=cache.lens + 1000)
+    ref = co.PagedCache(cache.k.double().cpu().numpy(), cache.v.double().cpu().numpy(), cache.table.cpu().tolist(), cache.lens.cpu().tolist(),
+                        cache.refs.cpu().tolist())
+    pos = np.array(lens)[:, None] + np.arange(T)
+    back = lambda x: turn(x.double().cpu().numpy(), -pos[:, None])  # noqa: E731
+    parent = [[i - 1 for i in range(T)]] * B
+    keys = [(x, 0.0) for x in range(6)] + [(x, 0.0) for x in fa.fib_attn_plan_distances(plan, 0, 100)]
+    for kk, (o, lse) in ((None, fa.fib_attn_dense_tree_decode(plan, 0, cache, q, kn, vn)), (keys, fa.fib_attn_tree_decode(plan, 0, cache, q, kn, vn, N=100))):
+        want, lse_want = co.tree_attend(ref, 0, back(q), back(kn), vf, parent, [T] * B, kk)
+        assert np.abs(lse.double().cpu().numpy() - lse_want).max() <= TOL_LSE
+        assert (np.abs(o.double().cpu().numpy() - want) - HALF[dtype] * np.abs(want)).max() <= TOL_O
+    assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK and fa.fib_attn_rope_status(rope) == fa.FIB_OK

@@ -277,3 +277,55 @@ def test_a_wait_that_runs_out():
     assert fa.fib_attn_last_device_status(plan) == fa.FIB_ERR_TIMEOUT
     fa.fib_attn_plan_set_debug(plan, False, 1_000_000_000)
     run(c, ref, plan, q, qf, lse, w, [20, 20])
+
+
+@pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 3), ("bf16", 20), ("bf16", 100), ("f32", 20)])
+def test_pages_beyond_32_bits(dtype, T):
+    """Pages at the end of a pool whose K and V have more than 2^31 values a layer: weights and eviction as in a small pool of the same rows."""
+    r = rng(210, T)
+    P, H, n = 64, 8, 150
+    small = fa.fib_attn_cache_create(2, H, P, 8, 1, 4, torch.float32 if dtype == "f32" else torch.bfloat16)
+    pages = (1 << 32) // (H * P * 64) // (2 if dtype == "f32" else 1) + 8
+    big = fa.fib_attn_cache_create(2, H, P, pages, 1, 4, small.dtype, k=torch.empty((2, pages, H, P, 64), dtype=small.dtype, device="cuda"),
+                                   v=torch.empty((2, pages, H, P, 64), dtype=small.dtype, device="cuda"))
+    big.refs[:pages - 8] = 1  # the free ones are the last
+    plan = plan_for(400)
+    kn, vn, q = (draw(r, s, dtype)[0] for s in ((2, 1, H, n, 64), (2, 1, H, n, 64), (2, 1, H, T, 64)))
+    lse = torch.full((2, 1, H, T), 4.0, device="cuda")
+    ws = []
+    for c in (small, big):
+        w = torch.zeros((2, 1, H, n), device="cuda")
+        fa.fib_attn_cache_commit(plan, c, kn, vn, i32([n]))
+        fa.fib_attn_cache_weigh(plan, c, q, lse, i32([T]), w, first=i32([0]))
+        ws.append(w.clone())
+        fa.fib_attn_cache_evict(plan, c, w, i32([90]), 3, 20)
+        ws.append(w)
+    assert fa.fib_attn_cache_status(big) == fa.FIB_OK and fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    assert torch.equal(ws[0], ws[2]) and torch.equal(ws[1], ws[3])
+    rows = [[x[:, c.table[0, :2].long()] for x in (c.k, c.v)] for c in (small, big)]
+    assert int(big.table[0, 0]) == pages - 8
+    for a, b in zip(*rows):
+        live = torch.arange(2 * P, device="cuda").view(2, P) < 90
+        assert torch.equal(a.transpose(2, 3)[:, live], b.transpose(2, 3)[:, live])
+
+
+def test_one_plan_on_two_streams():
+    """Calls with workspaces of their own side by side."""
+    r = rng(211)
+    x = [setup(r, "bf16", 2, 4, 1, T, 16, [900, 300], [T, T]) for T in (1, 40, 150)]
+    plan = plan_for(1000)
+    streams = [torch.cuda.Stream() for _ in x]
+    done = []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, (c, ref, q, qf, lse, w, _p) in zip(streams, x):
+            with torch.cuda.stream(s):
+                wd = torch.from_numpy(w).cuda()
+                fa.fib_attn_cache_weigh(plan, c, q, torch.from_numpy(lse).cuda(), i32([q.shape[3]] * 2), wd)
+                done.append(wd)
+    torch.cuda.synchronize()
+    for (c, ref, q, qf, lse, w, _p), *got in zip(x, done[:3], done[3:6], done[6:]):
+        assert all(torch.equal(got[0], g) for g in got)
+        want = w.astype(np.float64)
+        ref.weigh(want, qf, lse.astype(np.float64), [q.shape[3]] * 2)
+        assert np.allclose(got[0].double().cpu().numpy(), want, rtol=1e-4, atol=1e-5)
