@@ -4,7 +4,10 @@
 // negated.  e^{i p theta} is one complex product of two table entries (p = 64 hi + lo, both built in binary64), 1.2e-7 of error.
 //
 // What bounds it: the rows' bytes.  So four threads (float32: eight) take a row as wide loads, each both halves of its pairs, read their
-// factors once and use them for several heads of the token; what is on its way at a time is HEADS rows a thread.
+// factors once and use them for several heads of the token; what is on its way at a time is HEADS rows a thread.  131072 tokens of 8 + 8
+// bf16 heads: 85 us (6.3 TB/s, 94% of a measured copy); 8 x 4096 out of a fused projection: 22 us (91%); 2 x 74198 tokens of 4 + 2 float32
+// heads, interleaved, back into one: 68 us (the copy's rate; with four threads a row 98).  One head alone: 131072 tokens 12 us, 2.8 TB/s, as its
+// factors' reads are four times the row's.  Element by element 2 x 60000 tokens of 16 heads take 223 us, by words 79.
 #include "rotary.cuh"
 #include "tc_common.cuh"
 

@@ -9,12 +9,15 @@
 // tile), or, where there are 64 at most, eight tiles that pass by the queries.  Blocks take tasks as they come, so that those of
 // prompts, which cost from 4 products to hundreds, fill all SMs.  A row's sum is one thread's, in the order of the queries, whichever block it is.
 //
-// What bounds it: few query rows the read of K, many the products (three parts) and exp2.
+// What bounds it: few query rows the read of K, many the products (13 a tile and chunk of queries).  32 tokens over 4 sequences of up to 8192
+// rows, 16 layers, 8 heads (242 MB): 50 us with the queries' 6 (4.8 TB/s); the products alone are 30.  Prompts of 2048 and 1523, 4 layers
+// (134 million scores): 53 us, 15 of them the queries' launch; the products alone are 23 where all SMs have the same, 25 on the one that has
+// the longest task.
 //
 // Block: 16 warps that sum (four a tile), and one warp each for the tasks, the queries, the copies of each of the four tiles and the
-// products of each.  A warp's step (a wait, a few addresses, a copy) takes 500 to 1000 cycles and the twelve products of a tile 900,
-// whatever their columns, as much as a tile may take: with one warp for tasks, queries and copies and one for products a window of 32
-// tokens took 85 us, whatever else was changed, with warps of their own for the copies 73.
+// products of each.  A warp's step (a wait, a few addresses, a copy) takes 500 to 1000 cycles, as much as a tile may take: with one
+// warp for tasks, queries and copies a window of 32 tokens took 85 us, whatever else was changed, with warps of their own for
+// the copies 73, with four for the products 67.
 #include <climits>
 
 #include "tcgen05.cuh"
