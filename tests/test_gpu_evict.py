@@ -52,6 +52,21 @@ def test_rows_that_stay(dtype, P, H, lens, keep, sink, recent, turns):
     run(c, ref, plan, weights_of(r, c, max(lens) + 3), keep, sink, recent, dtype, turns)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("lens,keep,sink,recent", [
+    ([5200, 300, 0], [2600, 299, 0], 4, 100),         # room for more than a block of 256 threads holds
+    ([16384, 6000, 20], [16383, 10, 19], 0, 3),       # all that a block of 1024 holds
+    ([16385, 20001], [8000, 20000], 5, 0),            # more: the weights are read anew in each pass
+    ([33000, 16500], [1, 16000], 1, 0),
+])
+def test_long_sequences(dtype, lens, keep, sink, recent):
+    r = rng(111, *lens)
+    c, ref = make_cache(r, dtype, 1, 2, 64, lens, -(-max(lens) // 64) + 1)
+    w = weights_of(r, c, max(lens) + 1)
+    w[:, 0, 0, 5:max(lens):7], w[:, 0, 0, 3::1000], w[:, 0, 0, 4::2000], w[:, 0, 0, 11::900] = 0.0, np.nan, np.inf, -1.5
+    run(c, ref, plan_for(1 << 16), w, keep, sink, recent, dtype)
+
+
 def test_weights_of_every_kind():
     """Equal ones, zeros of both signs, negative, infinite and NaN ones."""
     r = rng(101)

@@ -65,6 +65,8 @@ def run(c, ref, plan, q, qf, lse, w, n_new, path=None, first=None, turns=True):
     (256, 1, 1, 200, [1025, 200, 512], [200, 200, 150], False),        # several groups of 64 queries, prompts of their own
     (16, 1, 2, 520, [520, 1100], [520, 300], False),
     (64, 1, 16, 8, [260], [8], False),                                 # 16 query heads to a key head
+    (64, 1, 1, 2, [1900, 1], [2, 1], False),                           # two columns of parts, runs over many blocks
+    (16, 2, 2, 1, [1030, 15, 16], [1, 1, 1], False),
 ])
 @pytest.mark.parametrize("kind", ["add", "set", "some"])
 def test_weights(dtype, P, H, G, T, lens, n_new, use_path, kind):
@@ -329,3 +331,12 @@ def test_one_plan_on_two_streams():
         want = w.astype(np.float64)
         ref.weigh(want, qf, lse.astype(np.float64), [q.shape[3]] * 2)
         assert np.allclose(got[0].double().cpu().numpy(), want, rtol=1e-4, atol=1e-5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("G,T", [(1, 1), (2, 4), (1, 40), (3, 90)])
+def test_long_sequences(dtype, G, T):
+    r = rng(212, G, T)
+    lens, n = [9001, 4000], [T, max(1, T // 2)]
+    x = setup(r, dtype, 1, 2, G, T, 32, lens, n)
+    run(x[0], x[1], plan_for(1 << 14), *x[2:6], n, first=[0, 5])
