@@ -281,6 +281,23 @@ def test_a_wait_that_runs_out():
     run(c, ref, plan, q, qf, lse, w, [20, 20])
 
 
+def test_a_long_call_is_no_wait_that_runs_out():
+    """A limit that every step keeps to, and that a block's whole work, 1024 chunks of queries, does not."""
+    r = rng(213)
+    c = fa.fib_attn_cache_create(1, 1, 64, 150, 1, 150, torch.bfloat16)
+    plan = plan_for(1 << 14)
+    kn, q = (draw(r, s, "bf16")[0] for s in ((1, 1, 1, 9000, 64), (1, 1, 16, 8192, 64)))
+    fa.fib_attn_cache_commit(plan, c, kn, kn, i32([9000]))
+    lse = torch.full((1, 1, 16, 8192), 5.0, device="cuda")
+    ws = []
+    for ns in (1_000_000_000, 400_000):
+        fa.fib_attn_plan_set_debug(plan, False, ns)
+        ws.append(torch.zeros((1, 1, 1, 9000), device="cuda"))
+        fa.fib_attn_cache_weigh(plan, c, q, lse, i32([8192]), ws[-1], first=i32([0]))
+        assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    assert torch.equal(*ws) and (ws[0] > 0).all()
+
+
 @pytest.mark.parametrize("dtype,T", [("bf16", 1), ("bf16", 3), ("bf16", 20), ("bf16", 100), ("f32", 20)])
 def test_pages_beyond_32_bits(dtype, T):
     """Pages at the end of a pool whose K and V have more than 2^31 values a layer: weights and eviction as in a small pool of the same rows."""
