@@ -11,6 +11,7 @@
 #include <algorithm>
 #include <cfenv>
 #include <cmath>
+#include <limits>
 #include <numeric>
 #include <set>
 
@@ -125,7 +126,8 @@ void rope_tables(int n_max, const double* theta, std::vector<float>* lo, std::ve
 bool rope_frequencies(const fib_attn_rope_spec& r, double* theta) {
   if (r.layout != FIB_ROPE_HALF && r.layout != FIB_ROPE_INTERLEAVED) return false;
   if (r.rot_dim < 2 || r.rot_dim > kHeadDim || r.rot_dim % 2 != 0) return false;
-  if (!std::isfinite(r.base) || r.base <= 1.0 || !std::isfinite(r.amplitude) || r.amplitude <= 0.0) return false;
+  if (!std::isfinite(r.base) || r.base <= 1.0) return false;
+  if (!(r.amplitude >= std::numeric_limits<float>::min() && r.amplitude <= std::numeric_limits<float>::max())) return false;  // the kernel's type
   if (r.scaling < FIB_ROPE_PLAIN || r.scaling > FIB_ROPE_YARN) return false;
   if (r.scaling != FIB_ROPE_PLAIN && (!std::isfinite(r.factor) || r.factor < 1.0)) return false;
   if (r.scaling == FIB_ROPE_YARN &&

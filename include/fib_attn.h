@@ -246,7 +246,7 @@ int fib_attn_decode(fib_attn_plan_t p, int layer, int B, int H, int N, int pos, 
  *           0, 1) of PLAIN's theta_m: pairs of few turns in n_train positions are stretched,
  *           those of many kept.  (An amplitude of 0.1 ln(factor) + 1 goes with it.)
  * Rules: rot_dim even, 2 .. 64; base > 1; amplitude > 0; factor >= 1 (but PLAIN); n_train >= 1,
- * 0 <= slow < fast (YARN); all finite.                                                  */
+ * 0 <= slow < fast (YARN); all finite, the amplitude a normal float32's.                */
 typedef struct fib_attn_rope_spec_s {
   int layout;
   int rot_dim;

@@ -79,3 +79,10 @@ def test_create_and_null_arguments(lib):
     assert lib.fib_attn_rope_status(None) == fa.FIB_ERR_INVALID_ARG
     assert lib.fib_attn_rope_destroy(None) == fa.FIB_OK
     assert lib.fib_attn_plan_set_rotation(None, 0) == fa.FIB_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("amplitude", [1e39, 1e-60, math.inf, math.nan])
+def test_an_amplitude_is_a_float32(amplitude):
+    spec = fa.RopeSpec(fa.FIB_ROPE_HALF, 64, fa.FIB_ROPE_PLAIN, 1024, 10000.0, 1.0, 1.0, 32.0, amplitude)
+    out = (ctypes.c_double * 32)()
+    assert fa.lib().fib_attn_rope_frequencies(ctypes.byref(spec), out) == fa.FIB_ERR_INVALID_ARG
