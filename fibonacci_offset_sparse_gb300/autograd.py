@@ -10,6 +10,7 @@ prepares K'/V' rows (bf16, W <= 16), the Function keeps that workspace for the b
 place of k and v (the same bytes) and the backward starts from it.
 """
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import fib_attn as fa
 
@@ -60,6 +61,7 @@ class _Rotary(torch.autograd.Function):
         return fa.fib_attn_rotary(rope, q, k, pos=pos, start=start)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         pos, start = ctx.saved_tensors
         # the map is linear, and its transpose the same kernel; gradients come in any strides
@@ -71,6 +73,7 @@ class _Rotary(torch.autograd.Function):
 def rotary(rope, q, k=None, pos=None, start=None):
     """(q, k) rotated by their positions (fib_attn_rotary): q [B, Hq, N, 64], k [B, Hk, N, 64] or None, in any strides, as views
     of a projection are; pos int32 [B, N], or start int32 [B] + n, or n.  For plans that do not rotate
-    (fib_attn_plan_set_rotation).  A backward that is captured into a graph needs leaves of which no eager graph lives, as
+    (fib_attn_plan_set_rotation).  The backward reads pos or start again (so not a cache's lens that a commit changes before it) and
+    is not differentiable itself.  A backward that is captured into a graph needs leaves of which no eager graph lives, as
     any of torch does: x.detach().requires_grad_() is one."""
     return _Rotary.apply(q, k, pos, start, rope)

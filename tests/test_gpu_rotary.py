@@ -210,6 +210,14 @@ def test_gradients(layout, R):
     assert np.abs(k1.grad.double().cpu().numpy() - want).max() <= 2 * 12 * 2.0 ** -24 * 2.5 + 2.0 ** -22  # two terms of |a| + |b| = 2.5, and their sum
 
 
+def test_no_second_derivatives():
+    rope = fa.fib_attn_rope_create(64)
+    q = rand((1, 2, 16, 64), "f32", 18).requires_grad_()
+    g, = torch.autograd.grad(rotary(rope, q)[0].square().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError):
+        g.square().sum().backward()
+
+
 def test_backward_under_capture_with_an_eager_graph_alive():
     """Of the same memory; the leaf is one of the capture's own, as torch ties a leaf to the stream of its living graphs."""
     rope = fa.fib_attn_rope_create(64)
