@@ -501,6 +501,7 @@ cudaError_t launch_cache_weigh(const fib_attn_cache& cache, int B, int Hq, int T
   a.parts = at;
   a.ref_parts = at + static_cast<size_t>(cache.n_layers) * B * cache.heads * (a.mpad / 8) * kGroupBytes;
   a.wait_ns = wait_ns;
+  a.task_ns = wait_ns + static_cast<unsigned long long>((a.G * a.T + 127) / 128) * 20000;  // (128 queries take a task 2 us)
   a.skip_copy = skip_copy;
   return cache.dtype == FIB_DTYPE_F32 ? launch<float>(a, stream) : launch<__nv_bfloat16>(a, stream);
 }

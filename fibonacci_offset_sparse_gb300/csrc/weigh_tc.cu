@@ -260,19 +260,16 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), base = smem_addr(smem);
   wait_for_first();
 
-  // Gives up after `times` the limit, and after one where another warp has.
-  auto wait = [&](uint64_t* bar, uint32_t parity, int times = 1) {
-    for (int x = 0; x < times; ++x) {
-      if (warp_wait(bar, parity, a.wait_ns, &s_err)) return true;
-      if (__any_sync(0xffffffffu, s_err)) break;
-    }
+  auto wait_for = [&](uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
+    if (warp_wait(bar, parity, limit_ns, &s_err)) return true;
     s_err = 1;
     if (lane == 0) atomicExch(a.status, kStatusTimeout);
     return false;
   };
-  // Task number tc of the block, after k, the one before it: what that has to do takes as long as its queries are many.
+  auto wait = [&](uint64_t* bar, uint32_t parity) { return wait_for(bar, parity, a.wait_ns); };
+  // Task number tc of the block, and that this warp has read it (a warp that is done with it only later says so itself).
   auto read = [&](int tc, TcTask* k) {
-    if (!wait(&bars.t_full[tc & 1], (tc >> 1) & 1, 1 + chunks<COLS>(*k))) return false;
+    if (!wait_for(&bars.t_full[tc & 1], (tc >> 1) & 1, a.task_ns)) return false;
     *k = bars.task[tc & 1];
     return k->rounds > 0;
   };
@@ -293,13 +290,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       __syncwarp();
       if (k.rounds == 0) break;
       // A long task is taken alone, till the last of its queries is under way: one that waits for its block waits for nothing else.
-      if (k.used > COLS && !wait(&bars.t_empty[tc & 1], (tc >> 1) & 1, chunks<COLS>(k))) break;
+      if (k.used > COLS && !wait_for(&bars.t_empty[tc & 1], (tc >> 1) & 1, a.task_ns)) break;
     }
   } else if (warp == kFeedQ) {
     // =================================================================== copies of queries
     int n = 0;
     bool go = true;
-    TcTask k = {};
+    TcTask k;
     for (int tc = 0; go && read(tc, &k); ++tc) {
       const size_t m = ((static_cast<size_t>(k.l) * a.B + k.b) * c.H + k.h) * a.mpad;
       const int c1 = chunks<COLS>(k);
@@ -327,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     const int t = warp - kFeedK, box = min(kTile, c.P), slots = P::slots(t);  // rows a copy
     int n = 0;
     bool go = true, left_out[2] = {false, false};        // slots that the test hook does not fill
-    TcTask k = {};
+    TcTask k;
     for (int tc = 0; go && read(tc, &k); ++tc) {
       release(tc);
       for (int x = 0; x < k.rounds; ++x) {
@@ -386,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     };
     int qs = 0, q_round = 0, filled = 0, done = 0, step = 0;  // tiles copied, products made, chunks
     bool go = true;
-    TcTask k = {};
+    TcTask k;
     for (int tc = 0; go && read(tc, &k); ++tc) {
       const int c0 = same(first_chunk<COLS>(a, k, k.r0)), c1 = same(chunks<COLS>(k)), last = same(columns<COLS>(k, chunks<COLS>(k) - 1));
       int from[P::kRounds];  // the first chunk that sees rows of the tile
@@ -444,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     const uint32_t lanes = static_cast<uint32_t>(wq) << 21;
     int done = 0;
     bool go = true;
-    TcTask k = {};
+    TcTask k;
     for (int tc = 0; go && read(tc, &k); ++tc) {
       release(tc);
       float* out = a.weights + ((static_cast<size_t>(k.l) * c.S + k.b) * c.H + k.h) * a.rows;
