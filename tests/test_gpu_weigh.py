@@ -357,3 +357,12 @@ def test_long_sequences(dtype, G, T):
     lens, n = [9001, 4000], [T, max(1, T // 2)]
     x = setup(r, dtype, 1, 2, G, T, 32, lens, n)
     run(x[0], x[1], plan_for(1 << 14), *x[2:6], n, first=[0, 5])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_query_rows_of_an_odd_number_of_heads(dtype):
+    """More rows to rotate than the device holds at once, whose threads take several heads each."""
+    r = rng(214)
+    lens, n = [700, 600], [600, 333]
+    x = setup(r, dtype, 16, 5, 1, 600, 64, lens, n)
+    run(x[0], x[1], plan_for(1000), *x[2:6], n, first=[0, 267])
