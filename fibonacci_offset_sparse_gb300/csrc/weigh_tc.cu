@@ -258,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   __syncthreads();
   fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem, 0), base = smem_addr(smem);
-  wait_for_first();
+  // The rows of a block's first task need nothing of the queries' launch: their copies do not wait for it.
+  if (warp != kTasks && (warp < kFeedK || warp >= kFeedK + kTiles)) wait_for_first();
 
   auto wait_for = [&](uint64_t* bar, uint32_t parity, unsigned long long limit_ns) {
     if (warp_wait(bar, parity, limit_ns, &s_err)) return true;
@@ -281,7 +282,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   if (warp == kTasks) {
     // =================================================================== tasks
     for (int tc = 0; wait(&bars.t_empty[tc & 1], ((tc >> 1) & 1) ^ 1); ++tc) {
-      unsigned long long id = lane == 0 ? atomicAdd(a.next, 1ull) : 0;
+      if (tc == 1) wait_for_first();
+      unsigned long long id = tc == 0 ? blockIdx.x : lane == 0 ? gridDim.x + atomicAdd(a.next, 1ull) : 0;
       const TcTask k = task_at<COLS>(a, sch, __shfl_sync(0xffffffffu, id, 0));
       if (lane == 0) {
         bars.task[tc & 1] = k;
@@ -349,6 +351,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           tma_3d(base + slot * kTileBytes + lane * box * 128, &map_k, 0, ((id * c.H + k.h) << c.shift) + (r & (c.P - 1)), k.l, &bars.k_full[slot]);
         __syncwarp();
       }
+      if (tc == 0) wait_for_first();
     }
     if (lane == 0)
       for (int x = max(0, n - slots); x < n; ++x)
