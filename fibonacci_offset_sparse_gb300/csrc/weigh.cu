@@ -84,8 +84,17 @@ __global__ void __launch_bounds__(kPrepThreads) weigh_prep_kernel(const __grid_c
         if (t < 2) {  // an infinite one has no rest
           const float hi = __bfloat162float(__float2bfloat16_rn(ref)), left = isfinite(hi) ? ref - hi : 0.f;
           const float mid = __bfloat162float(__float2bfloat16_rn(left));
-          *reinterpret_cast<uint4*>(a.ref_parts + (task * (a.mpad / 8) + m / 8) * kRefGroupBytes + t * 128 + r * 16) =
-              t == 0 ? make_uint4(pack_bf2_rn(hi, mid), pack_bf2_rn(left - mid, 0.f), 0, 0) : make_uint4(0, 0, 0, 0);
+          const size_t group = task * (a.mpad / 8) + m / 8;
+          if (a.G * a.T > kSpreadRows) {
+            *reinterpret_cast<uint4*>(a.ref_parts + group * kRefGroupBytes + t * 128 + r * 16) =
+                t == 0 ? make_uint4(pack_bf2_rn(hi, mid), pack_bf2_rn(left - mid, 0.f), 0, 0) : make_uint4(0, 0, 0, 0);
+          } else {
+            const float parts[3] = {hi, mid, left - mid};
+#pragma unroll
+            for (int part = 0; part < 3; ++part)
+              *reinterpret_cast<uint4*>(a.ref_parts + (group * 3 + part) * kRefGroupBytes + t * 128 + r * 16) =
+                  make_uint4(t == 0 ? pack_bf2_rn(parts[part], 0.f) : 0, 0, 0, 0);
+          }
         }
         unsigned char* at = a.parts + (task * (a.mpad / 8) + m / 8) * kGroupBytes + r * 128;
 #pragma unroll
@@ -486,9 +495,10 @@ int padded(int rows) { return rows <= 8 ? 8 : (rows + 63) / 64 * 64; }
 }  // namespace
 
 size_t weigh_workspace_bytes(const fib_attn_cache& c, int B, int Hq, int T) {
-  const size_t tasks = static_cast<size_t>(c.n_layers) * B * c.heads, mpad = padded(Hq / c.heads * T);
+  const int query_rows = Hq / c.heads * T;
+  const size_t tasks = static_cast<size_t>(c.n_layers) * B * c.heads, mpad = padded(query_rows);
   return 256 + round_up(tasks * mpad * sizeof(float)) +
-         tasks * (mpad / 8) * (c.dtype == FIB_DTYPE_F32 ? kGroupBytes32 : kGroupBytes + kRefGroupBytes);
+         tasks * (mpad / 8) * (c.dtype == FIB_DTYPE_F32 ? kGroupBytes32 : kGroupBytes + (query_rows <= kSpreadRows ? 3 : 1) * kRefGroupBytes);
 }
 
 cudaError_t launch_cache_weigh(const fib_attn_cache& cache, int B, int Hq, int T, int rows, int n_max, const int32_t* n_new, const int32_t* path,

@@ -21,7 +21,8 @@ struct WeighArgs {
   // Workspace.  parts: for each layer, sequence and key head, and 8 query rows after one another, the rotated rows times
   // log2(e)/8, split: bf16 hi, mid, lo, each [8][64] with its 16-byte words swizzled as the tensor pipes' 128-byte pattern, word w of
   // row r at w ^ r; float32 hi, lo (tf32), each [8][64].  refs: -lse * log2(e), -inf where there is no row.
-  // ref_parts (weigh_tc.cu alone): the same split in bf16 hi, mid, lo, as rows of 16 of which the others are 0, for 8 query rows [2][8][8].
+  // ref_parts (weigh_tc.cu alone): the same split in bf16 hi, mid, lo, as rows of 16 of which the others are 0, for 8 query rows [2][8][8]; for
+  // kSpreadRows or less a key head three of these, of the first hi alone, of the second mid, of the third lo.
   unsigned char* parts;
   float* refs;
   unsigned char* ref_parts;
@@ -35,6 +36,7 @@ constexpr int kPartBytes = 8 * kD * 2;        // 8 rows of one bf16 part
 constexpr int kGroupBytes = 3 * kPartBytes;   // 8 query rows, bf16
 constexpr int kGroupBytes32 = 2 * 8 * kD * 4;  // ... float32
 constexpr int kRefGroupBytes = 8 * 16 * 2;     // the references of 8 query rows
+constexpr int kSpreadRows = 32;                // query rows a key head up to which weigh_tc.cu has the parts as columns
 
 // For what is in flight when a warp gives up: its wait is not the caller's, which may be too short for a copy.
 constexpr unsigned long long kWeighDrainNs = 2000000000ull;

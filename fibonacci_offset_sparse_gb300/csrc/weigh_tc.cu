@@ -34,20 +34,23 @@ constexpr int kOnesBytes = kTile * 16 * 2;  // 128 rows of 1 1 1 0 ..., whose pr
 constexpr int kSumWarps = 4 * kTiles, kIssuer = kSumWarps, kFeedK = kIssuer + kTiles, kTasks = kFeedK + kTiles, kFeedQ = kTasks + 1;
 constexpr int kThreads = 32 * (kFeedQ + 1);
 
-// COLS query rows a product: 64, where a key head has no more, two buffers of tensor memory a tile, two slots of shared memory a tile, and
-// tasks of two rounds; else 128, one buffer, and two slots for the first two tiles.  A product takes 48.5, 54 and 64.6 cycles with 32, 64 and 128
+// COLS query rows a product.  32, where a key head has no more: the three parts are columns of one product (96, which takes hardly longer than 32 do)
+// and a score is the sum of three; one buffer of tensor memory a tile.  64, where it has no more: the parts add up in 64 columns, two buffers.
+// Both have two slots of shared memory a tile, and tasks of two rounds; else 128, one buffer, and two slots for the first two tiles.  A product takes 48.5, 54 and 64.6 cycles with 32, 64 and 128
 // columns, and what a warp does a chunk of queries beside its columns costs as much as 40 of them: prompts of 2048 took 66 us with 64.
 template <int COLS>
 struct Shape {
-  static constexpr int kRounds = COLS == 64 ? 2 : 1;
-  static constexpr int kBuffers = 512 / (kTiles * COLS);  // of tensor memory, a tile
-  static constexpr int kSlots = COLS == 64 ? 2 * kTiles : kTiles + 2, kQuerySlots = 2;
-  static constexpr int kQueryRefs = COLS / 8 * kGroupBytes, kQuerySlot = kQueryRefs + COLS / 8 * kRefGroupBytes;  // a slot: queries, references
+  static constexpr bool kSpread = COLS == kSpreadRows;  // parts are columns: of 8 queries 24, part by part
+  static constexpr int kRounds = COLS < 128 ? 2 : 1;
+  static constexpr int kBufferCols = kSpread ? 128 : COLS, kBuffers = 512 / (kTiles * kBufferCols);  // of tensor memory, a tile
+  static constexpr int kSlots = COLS < 128 ? 2 * kTiles : kTiles + 2, kQuerySlots = 2;
+  static constexpr int kRefBytes = (kSpread ? 3 : 1) * kRefGroupBytes;  // of 8 queries
+  static constexpr int kQueryRefs = COLS / 8 * kGroupBytes, kQuerySlot = kQueryRefs + COLS / 8 * kRefBytes;  // a slot: queries, references
   static constexpr int kQueries = kSlots * kTileBytes, kOnes = kQueries + kQuerySlots * kQuerySlot, kSchedule = kOnes + kOnesBytes;
   static_assert(kQuerySlot % 1024 == 0, "layout");
   // Tile t's slots: this one and, where there is one, the next.
-  __device__ __forceinline__ static int slot(int t) { return COLS == 64 || t < 2 ? 2 * t : t + 2; }
-  __device__ __forceinline__ static int slots(int t) { return COLS == 64 || t < 2 ? 2 : 1; }
+  __device__ __forceinline__ static int slot(int t) { return COLS < 128 || t < 2 ? 2 * t : t + 2; }
+  __device__ __forceinline__ static int slots(int t) { return COLS < 128 || t < 2 ? 2 : 1; }
 };
 
 struct TcTask {
@@ -309,9 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         if (lane == 0) {
           unsigned char* to = smem + P::kQueries + slot * P::kQuerySlot;
           const size_t at = (m + static_cast<size_t>(ch) * COLS) / 8;
-          mbar_arrive_tx(&bars.q_full[slot], cols / 8 * (kGroupBytes + kRefGroupBytes));
+          mbar_arrive_tx(&bars.q_full[slot], cols / 8 * (kGroupBytes + P::kRefBytes));
           bulk_g2s(to, a.parts + at * kGroupBytes, cols / 8 * kGroupBytes, &bars.q_full[slot]);
-          bulk_g2s(to + P::kQueryRefs, a.ref_parts + at * kRefGroupBytes, cols / 8 * kRefGroupBytes, &bars.q_full[slot]);
+          bulk_g2s(to + P::kQueryRefs, a.ref_parts + at * P::kRefBytes, cols / 8 * P::kRefBytes, &bars.q_full[slot]);
         }
         __syncwarp();
       }
@@ -361,18 +364,19 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     // =================================================================== products of tile t of each round
     // The warp goes as one and its values are the same in all lanes (shuffled, so that the compiler can tell); one lane issues.
     auto same = [](int x) { return __shfl_sync(0xffffffffu, x, 0); };
-    // Descriptors count 16 bytes: 32 bytes on a k step, a part's 1024 on a part.
-    constexpr uint32_t kLead = 16 / 16 << 16, kRowsHigh = 1024 / 16 | 1u << 14 | 2u << 29, kQueryHigh = kGroupBytes / 16 | 1u << 14 | 2u << 29;
+    // Descriptors count 16 bytes: 32 bytes on a k step, a part's 1024 on a part (as columns: eight more rows of the operand).
+    constexpr uint32_t kLead = 16 / 16 << 16, kRowsHigh = 1024 / 16 | 1u << 14 | 2u << 29;
+    constexpr uint32_t kQueryHigh = (P::kSpread ? kPartBytes : kGroupBytes) / 16 | 1u << 14 | 2u << 29;
     // Ones and references without swizzle: 8 rows of 16 bytes, their other half of k 128 bytes on, 8 more rows 256.
     constexpr uint32_t kPlainLead = 128 / 16 << 16, kPlainHigh = kRefGroupBytes / 16 | 1u << 14;
     auto at = [](uint32_t high, uint32_t low) { return static_cast<uint64_t>(high) << 32 | low; };
     const int t = same(warp - kIssuer);
     const int slots = P::slots(t), slot0 = P::slot(t), buf0 = t * P::kBuffers;
     const uint32_t rows0 = (base + slot0 * kTileBytes) >> 4 | kLead, query0 = (base + P::kQueries) >> 4 | kLead, refs0 = (base + P::kQueries + P::kQueryRefs) >> 4 | kPlainLead,
-                   ones = (base + P::kOnes) >> 4 | kPlainLead, out0 = tmem + buf0 * COLS;
+                   ones = (base + P::kOnes) >> 4 | kPlainLead, out0 = tmem + buf0 * P::kBufferCols;
     // With one buffer a tile the tiles go in order, so that a tile's scores are there while the next one's are made: side by side those of all
     // four were there together, then all sums were formed, and prompts of 2048 took 59 us.
-    constexpr bool kInTurn = P::kBuffers == 1;
+    constexpr bool kInTurn = COLS == 128;
     volatile int* issued = bars.issued;
     auto turn = [&](int step) {  // the tile before this one is past chunk `step` of the block
       const unsigned long long since = global_ns();
@@ -399,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       for (int ch = c0; ch < c1 && go; ++ch) {
         go = wait(&bars.q_full[qs], q_round & 1);
         if (!go) break;
-        const uint32_t query = query0 + qs * (P::kQuerySlot / 16), refs = refs0 + qs * (P::kQuerySlot / 16), desc = product_of(kTile, ch == c1 - 1 ? last : COLS, false, false);
+        const uint32_t query = query0 + qs * (P::kQuerySlot / 16), refs = refs0 + qs * (P::kQuerySlot / 16), desc = product_of(kTile, (P::kSpread ? 3 : 1) * (ch == c1 - 1 ? last : COLS), false, false);
 #pragma unroll
         for (int x = 0; x < P::kRounds; ++x) {
           if (from[x] > ch) break;
@@ -410,13 +414,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           if (kInTurn && go && t > 0) go = turn(step);
           if (!go) break;
           fence_after();
-          const uint32_t rows = rows0 + slot * (kTileBytes / 16), d = out0 + buf * COLS;
+          const uint32_t rows = rows0 + slot * (kTileBytes / 16), d = out0 + buf * P::kBufferCols;
           if (one_lane()) {
 #pragma unroll
-            for (int part = 2; part >= 0; --part)
+            for (int part = P::kSpread ? 0 : 2; part >= 0; --part)
 #pragma unroll
               for (int y = 0; y < 4; ++y)
-                mma_tc(d, at(kRowsHigh, rows + 2 * y), at(kQueryHigh, query + part * (kPartBytes / 16) + 2 * y), desc, part < 2 || y > 0);
+                mma_tc(d, at(kRowsHigh, rows + 2 * y), at(kQueryHigh, query + part * (kPartBytes / 16) + 2 * y), desc, (!P::kSpread && part < 2) || y > 0);
             mma_tc(d, at(kPlainHigh, ones), at(kPlainHigh, refs), desc, true);  // (the last: a sum is cut where it is added to)
             commit_tc(&bars.s_full[buf0 + buf]);
             if (ch == c1 - 1) commit_tc(&bars.k_empty[slot0 + slot]);
@@ -490,8 +494,28 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
               s[3] += y[3];
             }
           };
-          const uint32_t from = tmem + buf * COLS + lanes;
+          const uint32_t from = tmem + buf * P::kBufferCols + lanes;
           auto add = [&]<bool ALL>() {
+            if constexpr (P::kSpread) {
+#pragma unroll
+              for (int col = 0; col < COLS; col += 16) {  // 16 queries: twice the columns of 8 queries' upper, middle and lower parts
+                if (col >= cols) break;
+                uint32_t x[16], y[16], z[16];
+                ld16(from + 3 * col, x);
+                ld16(from + 3 * col + 16, y);
+                ld16(from + 3 * col + 32, z);
+                wait16(x);
+                pass16(y);
+                pass16(z);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                  x[e] = __float_as_uint(__uint_as_float(x[e]) + (__uint_as_float(x[8 + e]) + __uint_as_float(y[e])));
+                  x[8 + e] = __float_as_uint(__uint_as_float(y[8 + e]) + (__uint_as_float(z[e]) + __uint_as_float(z[8 + e])));
+                }
+                use.template operator()<ALL>(x, col);
+              }
+              return;
+            }
 #pragma unroll
             for (int col = 0; col < COLS; col += 32) {
               if (col >= cols) break;
@@ -559,6 +583,7 @@ static cudaError_t launch(const WeighArgs& a, cudaStream_t stream) {
 }
 
 cudaError_t launch_weigh_tc(const WeighArgs& a, cudaStream_t stream) {
+  if (a.G * a.T <= kSpreadRows) return launch<kSpreadRows>(a, stream);
   return a.G * a.T <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
 }
 
