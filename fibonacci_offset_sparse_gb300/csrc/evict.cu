@@ -8,7 +8,7 @@
 //          weights; then K and V by that list.  A row never moves up, so the rows that a step writes were all read in it or before, and
 //          one barrier a step, between its reads and its writes, keeps them apart.  No order of blocks matters.
 // What bounds it: the rows' bytes, read and written once; one block's search runs beside the others' moves (in launches of their own search
-// and move took 449 us where now it is 365).  16 sequences of 2048 to 4096 rows cut to 2048, 16 layers, 8 heads, bf16 (2.05 GB): plan 9 us,
+// and move took 449 us, together 365).  16 sequences of 2048 to 4096 rows cut to 2048, 16 layers, 8 heads, bf16 (2.05 GB): plan 9 us,
 // evict 344 (6.0 TB/s); 65536 rows cut to 16384 (1.12 GB, 128 blocks): 220 (5.1 TB/s, after a search of some 45 us in which nothing moves);
 // 16 beams that share prompts of 2048, cut to 1024 (0.82 GB, shared pages from L2): 120.
 #include "cache_dev.cuh"

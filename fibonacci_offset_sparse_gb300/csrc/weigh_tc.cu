@@ -2,7 +2,8 @@
 // tensor cores, the rest as in weigh.cu.
 //
 // A tile is 128 rows of K, as TMA leaves them (K-major, 128-byte swizzle), times up to 128 query rows of the split query, all three parts
-// added up into one accumulator of tensor memory: S [128 rows x queries].  There a thread has a row, so its sum is a loop over its columns:
+// added up into one accumulator of tensor memory: S [128 rows x queries] (32 queries at most: side by side in one of three times as many columns, of
+// which the threads add up three).  There a thread has a row, so its sum is a loop over its columns:
 //   one load from tensor memory, one exp2, one add; no shuffle.  (That -lse is added by one more product, ones times its parts: with an add
 //   and a read of lse a column the warps that sum were what bounded it.)
 // A task is up to four tiles of a sequence, layer and head, which stay in shared memory while its queries pass by (those that see the
@@ -10,9 +11,10 @@
 // prompts, which cost from 4 products to hundreds, fill all SMs.  A row's sum is one thread's, in the order of the queries, whichever block it is.
 //
 // What bounds it: few query rows the read of K, many the products (13 a tile and chunk of queries).  32 tokens over 4 sequences of up to 8192
-// rows, 16 layers, 8 heads (242 MB): 50 us with the queries' 6 (4.8 TB/s); the products alone are 30.  Prompts of 2048 and 1523, 4 layers
-// (134 million scores): 53 us, 15 of them the queries' launch; the products alone are 23 where all SMs have the same, 25 on the one that has
-// the longest task.
+// rows, 16 layers, 8 heads (242 MB): 47 us with the queries' launch; once under way a block's tasks follow one another in 2.95 us, which is HBM's rate,
+// the rest is the start, the queries' 6 and the last tasks.  (13 products of 32 columns a tile, 30 us of tensor pipe, took 49.)  Prompts of
+// 2048 and 1523, 4 layers (134 million scores): 50 us, 14 of them the queries' launch; the products alone are 23 where all SMs have the same, 25 on
+// the one that has the longest task.
 //
 // Block: 16 warps that sum (four a tile), and one warp each for the tasks, the queries, the copies of each of the four tiles and the
 // products of each.  A warp's step (a wait, a few addresses, a copy) takes 500 to 1000 cycles, as much as a tile may take: with one
