@@ -140,8 +140,12 @@ __device__ __forceinline__ void mma_tf32(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // A lane's fragments.  Lane (g, t) = (lane / 4, lane % 4).
-// kOne: 8 query rows at most, whose fragments stay in registers; kFew: 2 at most, whose parts are columns of one product; kMany: any number.
-enum Rows { kFew, kOne, kMany };
+// kOne: 8 query rows at most, whose fragments stay in registers; kFew: 2 at most, whose parts are columns of one product; kMany, kTeam: any
+// number, which pass by the unit's rows, split once, the next eight on their way while eight are used (one block of 8 warps an SM for the
+// registers; float32, 32 tokens over 2 sequences of 3149 rows, 16 layers, 8 heads: 57 us; rows split for each eight, 16 warps an SM, 71); with kTeam
+// several warps share a unit where there are few (a prompt of 328, 5 layers, 3 heads, 6 of queries: 24 us, one warp a unit 39; its barrier
+// costs the 32 tokens 3 us).
+enum Rows { kFew, kOne, kMany, kTeam };
 template <typename DT, Rows ROWS>
 struct Frag;
 template <Rows ROWS>
@@ -215,14 +219,11 @@ struct Frag<float, ROWS> {
   }
   __device__ __forceinline__ static int query(int t, int j) { return 2 * t + j; }
   __device__ __forceinline__ static float add_up(float x) { return quad_sum(x); }
-  __device__ __forceinline__ void scores(const uint4 (&x0)[4], const uint4 (&x1)[4], float (&y)[2][2], bool upper) const {
-    float c[4] = {0.f, 0.f, 0.f, 0.f};
-    float d[4] = {0.f, 0.f, 0.f, 0.f};  // the large products
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint32_t u0[4] = {x0[k].x, x0[k].y, x0[k].z, x0[k].w}, u1[4] = {x1[k].x, x1[k].y, x1[k].z, x1[k].w};
-      const uint32_t qh[4] = {q[0][k].x, q[0][k].y, q[0][k].z, q[0][k].w}, ql[4] = {q[1][k].x, q[1][k].y, q[1][k].z, q[1][k].w};
-      uint32_t h0[4], h1[4], l0[4], l1[4];
+  // Rows split: word k of both.
+  struct Split {
+    uint32_t h0[4], h1[4], l0[4], l1[4];
+    __device__ __forceinline__ void set(const uint4& x0, const uint4& x1) {
+      const uint32_t u0[4] = {x0.x, x0.y, x0.z, x0.w}, u1[4] = {x1.x, x1.y, x1.z, x1.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float f0 = __uint_as_float(u0[e]), f1 = __uint_as_float(u1[e]), g0 = tf32_of(f0), g1 = tf32_of(f1);
@@ -231,17 +232,33 @@ struct Frag<float, ROWS> {
         l0[e] = __float_as_uint(tf32_of(f0 - g0));
         l1[e] = __float_as_uint(tf32_of(f1 - g1));
       }
+    }
+  };
+  static constexpr bool kOnce = ROWS >= kMany;
+  Split rows[kOnce ? 4 : 1];  // of many queries: all of them, once a unit
+  __device__ __forceinline__ void take_rows(const uint4 (&x0)[4], const uint4 (&x1)[4]) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) rows[k].set(x0[k], x1[k]);
+  }
+  __device__ __forceinline__ void scores(const uint4 (&x0)[4], const uint4 (&x1)[4], float (&y)[2][2], bool upper) {
+    float c[4] = {0.f, 0.f, 0.f, 0.f}, b[4] = {0.f, 0.f, 0.f, 0.f};
+    float d[4] = {0.f, 0.f, 0.f, 0.f};  // the large products
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if constexpr (!kOnce) rows[0].set(x0[k], x1[k]);
+      const Split& r = rows[kOnce ? k : 0];
+      const uint32_t qh[4] = {q[0][k].x, q[0][k].y, q[0][k].z, q[0][k].w}, ql[4] = {q[1][k].x, q[1][k].y, q[1][k].z, q[1][k].w};
 #pragma unroll
       for (int e = 0; e < 4; e += 2) {
         if (!upper) {
-          mma_tf32(c, l0[e], l1[e], l0[e + 1], l1[e + 1], qh[e], qh[e + 1]);
-          mma_tf32(c, h0[e], h1[e], h0[e + 1], h1[e + 1], ql[e], ql[e + 1]);
+          mma_tf32(c, r.l0[e], r.l1[e], r.l0[e + 1], r.l1[e + 1], qh[e], qh[e + 1]);
+          mma_tf32(b, r.h0[e], r.h1[e], r.h0[e + 1], r.h1[e + 1], ql[e], ql[e + 1]);
         }
-        mma_tf32(d, h0[e], h1[e], h0[e + 1], h1[e + 1], qh[e], qh[e + 1]);
+        mma_tf32(d, r.h0[e], r.h1[e], r.h0[e + 1], r.h1[e + 1], qh[e], qh[e + 1]);
       }
     }
 #pragma unroll
-    for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = c[e] + d[e];
+    for (int e = 0; e < 4; ++e) y[e >> 1][e & 1] = (c[e] + b[e]) + d[e];
   }
 };
 
@@ -282,13 +299,14 @@ struct Cursor {
 };
 
 template <typename DT, Rows ROWS>
-__global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constant__ WeighArgs a) {
+__global__ void __launch_bounds__(kThreads, ROWS >= kMany ? 1 : 2) weigh_kernel(const __grid_constant__ WeighArgs a) {
   using F = Frag<DT, ROWS>;
-  constexpr bool ONE = ROWS != kMany;
+  constexpr bool ONE = ROWS < kMany;
   constexpr int TILES = F::kTiles, UNIT = 16 * TILES, ROW = kD * static_cast<int>(sizeof(DT));
   static_assert(UNIT * ROW == kUnitBytes, "a unit");
   extern __shared__ __align__(128) unsigned char s_ring[];  // [kWarps][kSlots][kUnitBytes]
   __shared__ uint64_t s_full[kWarps][kSlots];
+  __shared__ float s_part[ROWS == kTeam ? 2 : 1][kWarps][16];  // what a team's warps have of a unit's rows
   __shared__ int s_there[kWarps][kSlots];  // bit x: box x of the slot's unit lies in the pool
   __shared__ long long s_start[kMaxSeqs + 1];  // units before each sequence's (of all layers and heads)
   const CacheDev& c = a.c;
@@ -318,7 +336,13 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     if (lane == 0) s_start[a.B] = base;
   }
   __syncthreads();
-  const long long total = s_start[a.B], warps = static_cast<long long>(gridDim.x) * kWarps, w = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  // kTeam: where there are warps without a unit, 2, 4 or 8 of a block have each, and of its queries every second, fourth or eighth group.
+  const long long total = s_start[a.B];
+  int team = 1;
+  if constexpr (ROWS == kTeam)
+    while (team < kWarps && total * (2 * team) <= static_cast<long long>(gridDim.x) * kWarps) team *= 2;
+  const int slice = warp % team;
+  const long long warps = static_cast<long long>(gridDim.x) * (kWarps / team), w = (static_cast<long long>(blockIdx.x) * kWarps + warp) / team;
   const long long each = total / warps, rest = total % warps, first = w * each + min(w, rest);
   const Cursor begin{first, first + each + (w < rest ? 1 : 0), 0, 0, 0, 0, 0, {}};
   unsigned char* ring = s_ring + warp * kSlots * kUnitBytes;
@@ -364,15 +388,12 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
   const float* refs = nullptr;
   float* out = nullptr;
   int used = 0, before = 0;  // query row m sees rows up to before + m / G
-  auto take = [&](int group) {
-    q.load(parts + static_cast<size_t>(group) * F::kGroup, g, t);
+  auto take = [&](F& to, float (&to_ref)[F::kPer], int group) {
+    to.load(parts + static_cast<size_t>(group) * F::kGroup, g, t);
 #pragma unroll
-    for (int j = 0; j < F::kPer; ++j) {
-      const int m = group * 8 + F::query(t, j);
-      ref[j] = refs[m];
-      sees[j] = m < used ? before + m / a.G : -1;
-    }
+    for (int j = 0; j < F::kPer; ++j) to_ref[j] = refs[group * 8 + F::query(t, j)];
   };
+  bool lost = false;
   for (int n = 0; k.next<UNIT>(a, s_start, &fresh); ++n) {
     if (fresh) {
       const size_t task = (static_cast<size_t>(k.l) * a.B + k.b) * c.H + k.h;
@@ -381,15 +402,20 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
       out = a.weights + ((static_cast<size_t>(k.l) * c.S + k.b) * c.H + k.h) * a.rows;
       used = k.s.n * a.G;
       before = k.s.len - k.s.n;
-      if (ONE) take(0);
+      if constexpr (ONE) {
+        take(q, ref, 0);
+#pragma unroll
+        for (int j = 0; j < F::kPer; ++j) sees[j] = F::query(t, j) < used ? before + F::query(t, j) / a.G : -1;
+      }
     }
     const int r0 = k.i * UNIT, slot = n % kSlots, row = r0 + 8 * t + g;  // the row that the lane writes (float32: of t < 2)
-    const bool writes = 8 * t < UNIT && row < k.s.len;
+    const bool writes = 8 * t < UNIT && row < k.s.len && slice == 0;
     const float old = writes && row < k.s.first ? out[row] : 0.f;
-    const bool landed = mbar_wait(&s_full[warp][slot], (n / kSlots) & 1, a.wait_ns);
+    const bool landed = !lost && mbar_wait(&s_full[warp][slot], (n / kSlots) & 1, a.wait_ns);
     if (!__all_sync(0xffffffffu, landed)) {
       if (lane == 0) atomicExch(a.status, kStatusTimeout);
-      break;
+      if (team == 1) break;
+      lost = true;  // the others wait for this warp's part all the same
     }
     const bool there = s_there[warp][slot] >> ((8 * t & (UNIT - 1)) / box) & 1;
     uint4 x[TILES][2][F::kWords];
@@ -409,10 +435,29 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
 #pragma unroll
     for (int v = 0; v < 2 * TILES; ++v) sum[v] = 0.f;
     const int groups = (used + 7) / 8;
-    for (int group = ONE ? 0 : max(0, r0 - before) * a.G / 8; group < groups; ++group) {
-      if (!ONE) take(group);
+    int from[2 * TILES];  // the first query that sees row 8v + g
+    if constexpr (!ONE) {
+      q.take_rows(x[0][0], x[0][1]);
+#pragma unroll
+      for (int v = 0; v < 2 * TILES; ++v) from[v] = max(0, r0 + 8 * v + g - before) * a.G;
+    }
+    const int edge = max(0, r0 + UNIT - 1 - before) * a.G;  // the first that sees every row of the unit
+    const int group0 = ONE ? 0 : max(0, r0 - before) * a.G / 8;
+    F next;
+    float next_ref[F::kPer];
+    if constexpr (!ONE) take(next, next_ref, min(group0 + slice, groups - 1));
+    for (int group = group0 + slice; group < groups; group += team) {
+      if constexpr (!ONE) {  // the next queries are on their way while these are used
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) q.q[p][k] = next.q[p][k];
+#pragma unroll
+        for (int j = 0; j < F::kPer; ++j) ref[j] = next_ref[j];
+        take(next, next_ref, min(group + team, groups - 1));
+      }
       // whether every query that the product has room for is one, and sees every row of the unit
-      const bool all = group * 8 + (ROWS == kFew ? 2 : 8) <= used && before + group * 8 / a.G >= r0 + UNIT - 1;
+      const bool all = group * 8 + (ROWS == kFew ? 2 : 8) <= used && group * 8 >= edge;
       float part[2 * TILES];
       // A NaN may come of an infinite key, where the parts' products are infinities of opposite signs: the upper
       // part's alone keep the sign, and a second round takes them.
@@ -437,7 +482,10 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
 #pragma unroll
             for (int j = 0; j < F::kPer; ++j) {
               const float p = ex2(y[e][j] + ref[j]);
-              given += all || r0 + 16 * i + 8 * e + g <= sees[j] ? p : 0.f;
+              if constexpr (ONE)
+                given += all || r0 + 16 * i + 8 * e + g <= sees[j] ? p : 0.f;
+              else
+                given += all || (group * 8 + F::query(t, j) < used && group * 8 + F::query(t, j) >= from[2 * i + e]) ? p : 0.f;
             }
             part[2 * i + e] = given;
             bad |= isnan(given);
@@ -453,19 +501,27 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     for (int v = 0; v < 2 * TILES; ++v) sum[v] = F::add_up(sum[v]);
     float y = t == 0 ? sum[0] : sum[1];
     if constexpr (TILES == 2) y = t == 2 ? sum[2] : t == 3 ? sum[3] : y;
+    if constexpr (ROWS == kTeam) {
+      if (team > 1) {
+        static_assert(TILES == 1, "a part: 16 rows");
+        if (t < 2) s_part[n & 1][warp][8 * t + g] = y;
+        asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(1 + warp / team), "r"(32 * team) : "memory");
+        for (int i = 1; i < team && writes; ++i) y += s_part[n & 1][warp + i][8 * t + g];
+      }
+    }
     if (writes && there) out[row] = old + y;
     __threadfence_block();  // the slot has been read
     __syncwarp();
-    copy();
+    if (!lost) copy();  // (a slot whose rows have not come is not filled again)
   }
   // nothing may be in flight when the block ends
   for (int x = max(0, fed - kSlots); x < fed; ++x) mbar_wait(&s_full[warp][x % kSlots], (x / kSlots) & 1, kWeighDrainNs);
 }
 
-cudaError_t launch_rows(void (*kernel)(WeighArgs), const WeighArgs& a, cudaStream_t stream) {
+cudaError_t launch_rows(void (*kernel)(WeighArgs), const WeighArgs& a, int blocks, cudaStream_t stream) {
   constexpr size_t kRing = static_cast<size_t>(kWarps) * kSlots * kUnitBytes;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kRing));
-  return e == cudaSuccess ? launch_second(kernel, dim3(152 * 2), kThreads, kRing, stream, a) : e;  // 152 SMs
+  return e == cudaSuccess ? launch_second(kernel, dim3(152 * blocks), kThreads, kRing, stream, a) : e;  // 152 SMs
 }
 
 template <typename DT>
@@ -483,10 +539,11 @@ cudaError_t launch(const WeighArgs& a, cudaStream_t stream) {
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if constexpr (sizeof(DT) == 2) {
-    if (a.G * a.T <= 2) return launch_rows(weigh_kernel<DT, kFew>, a, stream);
-    return a.G * a.T <= 8 ? launch_rows(weigh_kernel<DT, kOne>, a, stream) : launch_weigh_tc(a, stream);
+    if (a.G * a.T <= 2) return launch_rows(weigh_kernel<DT, kFew>, a, 2, stream);
+    return a.G * a.T <= 8 ? launch_rows(weigh_kernel<DT, kOne>, a, 2, stream) : launch_weigh_tc(a, stream);
   } else {
-    return a.G * a.T <= 8 ? launch_rows(weigh_kernel<DT, kOne>, a, stream) : launch_rows(weigh_kernel<DT, kMany>, a, stream);
+    if (a.G * a.T <= 8) return launch_rows(weigh_kernel<DT, kOne>, a, 2, stream);
+    return a.G * a.T <= 64 ? launch_rows(weigh_kernel<DT, kMany>, a, 1, stream) : launch_rows(weigh_kernel<DT, kTeam>, a, 1, stream);
   }
 }
 

@@ -281,6 +281,36 @@ def test_a_wait_that_runs_out():
     run(c, ref, plan, q, qf, lse, w, [20, 20])
 
 
+@pytest.mark.parametrize("dtype,G,T", [("f32", 1, 1), ("f32", 2, 10), ("f32", 2, 200), ("bf16", 1, 2), ("bf16", 1, 30), ("bf16", 2, 30), ("bf16", 1, 200)])
+def test_a_limit_too_short_for_a_copy(dtype, G, T):
+    """The call ends and says so, or was quick enough; the next one is right."""
+    r = rng(215, G, T)
+    lens, n = [900, 300], [T, T]
+    c, ref, q, qf, lse, w, _ = setup(r, dtype, 1, 2, G, T, 16, lens, n)
+    plan = plan_for(1000)
+    fa.fib_attn_plan_set_debug(plan, False, 1000)
+    for _ in range(3):
+        fa.fib_attn_cache_weigh(plan, c, q, torch.from_numpy(lse).cuda(), i32(n), torch.from_numpy(w).cuda())
+        assert fa.fib_attn_last_device_status(plan) in (fa.FIB_OK, fa.FIB_ERR_TIMEOUT)
+    fa.fib_attn_plan_set_debug(plan, False, 1_000_000_000)
+    run(c, ref, plan, q, qf, lse, w, n)
+
+
+@pytest.mark.parametrize("P,H,G,T,lens,n_new", [
+    (16, 1, 1, 65, [65], [65]),                     # 5 units, eight warps each
+    (32, 1, 2, 40, [500, 70], [40, 33]),            # 37: eight
+    (16, 2, 1, 130, [1500, 300], [130, 1]),         # 226: four
+    (64, 3, 1, 90, [1500, 1200], [90, 0]),          # 282: four
+    (16, 2, 3, 30, [3000, 1700], [30, 30]),         # 588: two
+    (128, 4, 1, 70, [2500, 2300], [70, 70]),        # 1204: one
+])
+@pytest.mark.parametrize("first", [False, True])
+def test_warps_that_share_rows(P, H, G, T, lens, n_new, first):
+    r = rng(216, H, G, T)
+    x = setup(r, "f32", 1, H, G, T, P, lens, n_new)
+    run(x[0], x[1], plan_for(4000), *x[2:6], n_new, first=[0, 3] if first and len(lens) == 2 else None)
+
+
 def test_a_long_call_is_no_wait_that_runs_out():
     """A limit that every step keeps to, and that a block's whole work, 1024 chunks of queries, does not."""
     r = rng(213)
