@@ -39,20 +39,29 @@ inline CacheDev device_view(const fib_attn_cache& c) {
 __device__ __forceinline__ void wait_for_first() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void let_second_start() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
 
-// A kernel, with `shared` bytes of dynamic shared memory, as a programmatic dependent of the one before it on the stream.
+// A kernel, in clusters of `cluster` blocks and with `shared` bytes of dynamic shared memory, as a programmatic dependent of the one before it on
+// the stream.
 template <typename... Params, typename... Args>
-inline cudaError_t launch_second(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t stream, Args... args) {
+inline cudaError_t launch_second_in_clusters(void (*kernel)(Params...), dim3 grid, unsigned cluster, int threads, size_t shared, cudaStream_t stream,
+                                             Args... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = shared;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+template <typename... Params, typename... Args>
+inline cudaError_t launch_second(void (*kernel)(Params...), dim3 grid, int threads, size_t shared, cudaStream_t stream, Args... args) {
+  return launch_second_in_clusters(kernel, grid, 1, threads, shared, stream, args...);
 }
 
 // The counts of four pages from `id` (a multiple of 4) on; 0 behind the last page.

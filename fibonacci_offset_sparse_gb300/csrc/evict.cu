@@ -4,7 +4,7 @@
 // down in order, K turned from its old place to the new one (e^{-i (old - new) theta} a pair; a plan that does not rotate moves
 // it as it is).  Two launches, the second a programmatic dependent of the first:
 //   plan   one block: what each sequence keeps, the free pages that take the place of shared ones, tables, counts, lengths;
-//   evict  a block a sequence, layer and head: the weight of the last row that stays, the list of rows that stay, in order, and their
+//   evict  a block (of few of them, a cluster) a sequence, layer and head: the weight of the last row that stays, the list of rows that stay, in order, and their
 //          weights; then K and V by that list.  A row never moves up, so the rows that a step writes were all read in it or before, and
 //          one barrier a step, between its reads and its writes, keeps them apart.  No order of blocks matters.
 // What bounds it: the rows' bytes, read and written once; one block's search runs beside the others' moves (in launches of their own search
@@ -383,11 +383,15 @@ __device__ __forceinline__ void factors(const EvictArgs& a, int d, int t, float2
   }
 }
 
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;\n" ::: "memory");
+}
+
 // The rows of K or V that `stays` lists come to places job.same * P ..: a quad a row, each thread dims 8t .. and 32+8t .. of it: two 16-byte
-// words of bf16, four of float32.  By THREADS threads of the block's, with a barrier of
-// their own.
-template <typename DT, int THREADS, int ROWS>
-__device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictJob& job, int v, int l, int b, int h, const int32_t* stays) {
+// words of bf16, four of float32.  By THREADS threads of each of `blocks` blocks, `rank` among them, with a barrier of their own (of several blocks: the
+// cluster's).
+template <typename DT, int THREADS, int ROWS, bool SHARED>
+__device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictJob& job, int v, int l, int b, int h, const int32_t* stays, int rank, int blocks) {
   const int thread = threadIdx.x % THREADS;
   constexpr int kWords = static_cast<int>(sizeof(DT)), kHalf = kWords / 2;  // 16-byte words a thread and row
   constexpr int kStep = THREADS / 4 * ROWS;
@@ -397,7 +401,8 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictJob& jo
   DT* pool = static_cast<DT*>(v ? c.v : c.k) + ((static_cast<size_t>(l) * c.n_pages * c.H + h) << c.shift) * kD;
   const size_t page_elems = (static_cast<size_t>(c.H) << c.shift) * kD;
   const int t = thread & 3, quad = thread >> 2, mask = c.P - 1;
-  for (int j0 = job.same << c.shift; j0 < job.keep; j0 += kStep) {
+  for (int start = job.same << c.shift; start < job.keep; start += kStep * blocks) {
+    const int j0 = start + kStep * rank;
     uint4 x[ROWS][kWords];
     int src[ROWS];  // -1: none, or it is there already
 #pragma unroll
@@ -417,7 +422,11 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictJob& jo
 #pragma unroll
       for (int k = 0; k < kWords; ++k) x[i][k] = p[(k / kHalf) * 4 * kHalf + t * kHalf + k % kHalf];
     }
-    asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(1 + v), "n"(THREADS) : "memory");  // every row of the step has been read
+    // every row of the step has been read
+    if (SHARED)
+      cluster_sync();
+    else
+      asm volatile("barrier.cta.sync %0, %1;\n" ::"r"(1 + v), "n"(THREADS) : "memory");
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
       const int j = j0 + i * (THREADS / 4) + quad;
@@ -457,27 +466,49 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictJob& jo
   }
 }
 
-template <typename DT, int THREADS, int KEYS>
+// SHARED: a cluster a sequence, layer and head, whose first block makes the list that all move by.
+template <typename DT, int THREADS, int KEYS, bool SHARED>
 __global__ void __launch_bounds__(THREADS, THREADS >= 1024 ? 1 : 4) evict_kernel(const __grid_constant__ EvictArgs a) {
   constexpr int ROWS = sizeof(DT) == 2 ? 4 : 2;
   __shared__ Select<THREADS, KEYS> select;
   const CacheDev& c = a.c;
-  const int per = c.L * c.H, b = blockIdx.x / per, lh = blockIdx.x % per, l = lh / c.H, h = lh % c.H;
+  int rank = 0, blocks = 1;
+  if constexpr (SHARED) {
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctarank;\n" : "=r"(blocks));
+  }
+  const int per = c.L * c.H, at = blockIdx.x / blocks, b = at / per, lh = at % per, l = lh / c.H, h = lh % c.H;
   const size_t task = (static_cast<size_t>(l) * c.S + b) * c.H + h;
   int32_t* stays = a.stays + task * a.rows;
   EvictJob job;
-  if (!select.run(a, b, a.weights + task * a.rows, stays, &job)) return;
+  if (rank == 0) {
+    if (!select.run(a, b, a.weights + task * a.rows, stays, &job)) return;
+  } else {
+    wait_for_first();
+    job = a.jobs[b];
+    if (job.keep < 0) return;  // (and so in every block of the cluster)
+  }
+  if (SHARED) cluster_sync();
   // One half of the threads K, the other V: one reads while the other writes.  (One after the other, 128 blocks of 65536 rows cut to 16384:
   // 264 us.)
-  move_rows<DT, THREADS / 2, ROWS>(a, job, threadIdx.x / (THREADS / 2), l, b, h, stays);
+  move_rows<DT, THREADS / 2, ROWS, SHARED>(a, job, threadIdx.x / (THREADS / 2), l, b, h, stays, rank, blocks);
+}
+
+template <typename DT, int THREADS, int KEYS>
+cudaError_t launch_in(const EvictArgs& a, unsigned tasks, unsigned blocks, cudaStream_t stream) {
+  return blocks == 1 ? launch_second(evict_kernel<DT, THREADS, KEYS, false>, dim3(tasks), THREADS, 0, stream, a)
+                     : launch_second_in_clusters(evict_kernel<DT, THREADS, KEYS, true>, dim3(tasks * blocks), blocks, THREADS, 0, stream, a);
 }
 
 // By what the weights' rows can hold: up to 5120 rows a block of 256 threads, four of which share an SM; longer ones 1024 threads, which beyond
-// 16384 rows read the weights anew in each pass.
+// 16384 rows read the weights anew in each pass.  Where these leave SMs without one, 2, 4 or 8 blocks of 256 rows or more to each (15 of 30300 rows
+// cut to 10211, bf16: 46 us, one block each 116; 32 of 2077 cut to 1782, float32: 22, 54).
 template <typename DT>
 cudaError_t launch(const EvictArgs& a, unsigned tasks, cudaStream_t stream) {
-  return a.rows <= 256 * 20 ? launch_second(evict_kernel<DT, 256, 20>, dim3(tasks), 256, 0, stream, a)
-                            : launch_second(evict_kernel<DT, 1024, 16>, dim3(tasks), 1024, 0, stream, a);
+  const bool few = a.rows <= 256 * 20;
+  unsigned blocks = 1;
+  while (blocks < 8 && tasks * blocks * 2 <= (few ? 152 * 4 : 152) && a.rows > 256 * static_cast<int>(blocks)) blocks *= 2;
+  return few ? launch_in<DT, 256, 20>(a, tasks, blocks, stream) : launch_in<DT, 1024, 16>(a, tasks, blocks, stream);
 }
 
 size_t rows_bytes(const fib_attn_cache& c, int rows) {

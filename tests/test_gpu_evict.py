@@ -227,3 +227,25 @@ def test_decode_after_eviction_sees_what_is_left():
     assert np.abs(lse.double().cpu().numpy() - lse_ref).max() <= 1e-4
     assert np.abs(o.double().cpu().numpy() - O_ref).max() <= 1e-3
     assert math.isfinite(float(o.sum()))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("L,H,P,lens,keep,sink,recent", [
+    (16, 5, 64, [5500], [2200], 70, 300),                           # 80 long ones: a block each
+    (7, 7, 32, [6000, 17], [5990, 12], 3, 9),                       # 98, with one that is short
+    (2, 3, 16, [700, 2100, 64, 5000], [699, 1000, 64, 33], 5, 20),  # 24: clusters, some with nothing to do
+    (1, 2, 128, [300, 513], [257, 300], 130, 1),                    # 4 of few rows
+    (5, 8, 16, [900, 800, 700, 640, 100], [400, 400, 699, 1, 0], 0, 0),  # 200
+])
+def test_blocks_that_share_rows(dtype, L, H, P, lens, keep, sink, recent):
+    r = rng(112, L, H)
+    c, ref = make_cache(r, dtype, L, H, P, lens, -(-max(lens) // P) + 1)
+    run(c, ref, plan_for(1 << 13), weights_of(r, c, max(lens) + 1), keep, sink, recent, dtype)
+
+
+def test_blocks_that_share_rows_of_shared_pages():
+    """Replaced pages, a sink that stays shared, and one sequence that is left whole."""
+    r = rng(113)
+    lens = [2000, 1900, 1800, 1500]
+    c, ref = make_cache(r, "bf16", 2, 2, 32, lens, 64, spare=200, share=[(1, 0, 50), (2, 0, 50)])
+    run(c, ref, plan_for(1 << 12), weights_of(r, c, 2000), [1000, 1899, 300, 1500], 70, 100, "bf16")
