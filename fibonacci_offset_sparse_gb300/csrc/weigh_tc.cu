@@ -6,7 +6,7 @@
 // which the threads add up three).  There a thread has a row, so its sum is a loop over its columns:
 //   one load from tensor memory, one exp2, one add; no shuffle.  (That -lse is added by one more product, ones times its parts: with an add
 //   and a read of lse a column the warps that sum were what bounded it.)
-// A task is up to four tiles of a sequence, layer and head, which stay in shared memory while its queries pass by (those that see the
+// A task is up to four tiles (of few: two, or one) of a sequence, layer and head, which stay in shared memory while its queries pass by (those that see the
 // tile), or, where there are 64 at most, eight tiles that pass by the queries.  Blocks take tasks as they come, so that those of
 // prompts, which cost from 4 products to hundreds, fill all SMs.  A row's sum is one thread's, in the order of the queries, whichever block it is.
 //
@@ -57,9 +57,9 @@ struct Shape {
 
 struct TcTask {
   int b, l, h;
-  int len, before, used;  // rows; query row m sees rows up to before + m / G; query rows
+  int before, used;  // query row m sees rows up to before + m / G; query rows
   int first;
-  int r0, rounds;         // rounds 0: there is none any more
+  int r0, end, rounds;  // rows r0 .. end - 1; rounds 0: there is none any more
 };
 
 // A barrier of one warp's or of one tile's warps, which wait for each of its rounds, one after the other: its parity cannot tell one that is a
@@ -76,10 +76,10 @@ struct TcBars {
   int issued[kTiles];  // chunks of queries that are past the products of the tile
 };
 
-// Rows of a task of a sequence with `used` query rows.
+// Rows of a task of a sequence with `used` query rows; parts: of a round's four tiles 4, 2 or 1 are a task.
 template <int COLS>
-__device__ __forceinline__ int task_rows(int used) {
-  return used <= COLS ? Shape<COLS>::kRounds * kGroupRows : kGroupRows;
+__device__ __forceinline__ int task_rows(int used, int parts) {
+  return used <= COLS ? Shape<COLS>::kRounds * kGroupRows / parts : kGroupRows / parts;
 }
 // The chunk of queries from which on some of them see row r, of a task.
 template <int COLS>
@@ -106,7 +106,7 @@ struct TcSchedule {
 
 // Task `id` of the call, if there is one (rounds > 0): sequences in order, of each the first rows of all layers and heads before the next.
 template <int COLS>
-__device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& sch, unsigned long long id) {
+__device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& sch, unsigned long long id, int parts) {
   TcTask k = {};
   const long long* start = sch.start;
   if (id >= static_cast<unsigned long long>(start[a.B])) return k;
@@ -127,13 +127,13 @@ __device__ __forceinline__ TcTask task_at(const WeighArgs& a, const TcSchedule& 
   k.b = lo;
   k.l = lh / a.c.H;
   k.h = lh - k.l * a.c.H;
-  k.len = s.len;
   k.before = s.len - s.n;
   k.used = s.n * a.G;
   k.first = s.first;
-  const int rows = task_rows<COLS>(k.used);
+  const int rows = task_rows<COLS>(k.used, parts);
   k.r0 = j * rows;
-  k.rounds = (min(rows, s.len - k.r0) + kGroupRows - 1) / kGroupRows;
+  k.end = min(s.len, k.r0 + rows);
+  k.rounds = (k.end - k.r0 + kGroupRows - 1) / kGroupRows;
   return k;
 }
 
@@ -234,29 +234,44 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   for (int i = tid; i < kOnesBytes / 16; i += kThreads)  // [16][2][8] words of a row's 8 values
     *reinterpret_cast<uint4*>(smem + P::kOnes + 16 * i) = i & 8 ? make_uint4(0, 0, 0, 0) : make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
   fence_smem();
-  for (int b = tid; b < a.B; b += kThreads) {
-    bool ok;
-    const WeighSeq s = weigh_seq(a, b, &ok);
-    const int rows = task_rows<COLS>(s.n * a.G);
-    sch.seq[b] = s;
-    start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + rows - 1) / rows) * c.L * c.H;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    long long base = 0;
-    for (int b0 = 0; b0 < a.B; b0 += 32) {
-      const int b = b0 + lane;
-      const long long own = b < a.B ? start[b] : 0;
-      long long x = own;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const long long y = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += y;
-      }
-      if (b < a.B) start[b] = base + x - own;
-      base += __shfl_sync(0xffffffffu, x, 31);
+  auto count = [&](int parts) {  // the tasks before each sequence's
+    for (int b = tid; b < a.B; b += kThreads) {
+      const WeighSeq s = sch.seq[b];
+      const int rows = task_rows<COLS>(s.n * a.G, parts);
+      start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + rows - 1) / rows) * c.L * c.H;
     }
-    if (lane == 0) start[a.B] = base;
+    __syncthreads();
+    if (warp == 0) {
+      long long base = 0;
+      for (int b0 = 0; b0 < a.B; b0 += 32) {
+        const int b = b0 + lane;
+        const long long own = b < a.B ? start[b] : 0;
+        long long x = own;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long y = __shfl_up_sync(0xffffffffu, x, d);
+          if (lane >= d) x += y;
+        }
+        if (b < a.B) start[b] = base + x - own;
+        base += __shfl_sync(0xffffffffu, x, 31);
+      }
+      if (lane == 0) start[a.B] = base;
+    }
+  };
+  for (int b = tid; b < a.B; b += kThreads) {  // (the thread that counts it)
+    bool ok;
+    sch.seq[b] = weigh_seq(a, b, &ok);
+  }
+  count(1);
+  // Where that leaves blocks without a task, tasks are of two tiles or of one: 32 of 1000 rows and 8000 query rows 104 us, of four tiles 141; 8 of
+  // 1672 rows and as many query rows 26, 34.
+  int parts = 1;
+  if constexpr (COLS == 128) {
+    __syncthreads();
+    const long long total = start[a.B];
+    while (parts < kTiles && total * parts * 2 <= gridDim.x) parts *= 2;
+    __syncthreads();
+    if (parts > 1) count(parts);
   }
   if (warp == kIssuer) tmem_alloc(&bars.tmem, 512);
   fence_before();
@@ -289,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     for (int tc = 0; wait(&bars.t_empty[tc & 1], ((tc >> 1) & 1) ^ 1); ++tc) {
       if (tc == 1) wait_for_first();
       unsigned long long id = tc == 0 ? blockIdx.x : lane == 0 ? gridDim.x + atomicAdd(a.next, 1ull) : 0;
-      const TcTask k = task_at<COLS>(a, sch, __shfl_sync(0xffffffffu, id, 0));
+      const TcTask k = task_at<COLS>(a, sch, __shfl_sync(0xffffffffu, id, 0), parts);
       if (lane == 0) {
         bars.task[tc & 1] = k;
         mbar_arrive(&bars.t_full[tc & 1]);
@@ -336,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       release(tc);
       for (int x = 0; x < k.rounds; ++x) {
         const int r0 = k.r0 + x * kGroupRows + t * kTile;
-        if (r0 >= k.len) break;
-        const int boxes = (min(kTile, k.len - r0) + box - 1) / box, s = n & (slots - 1), slot = P::slot(t) + s;
+        if (r0 >= k.end) break;
+        const int boxes = (min(kTile, k.end - r0) + box - 1) / box, s = n & (slots - 1), slot = P::slot(t) + s;
         // lane i copies box i
         const int r = r0 + lane * box;
         int id = lane < boxes ? __ldg(c.table + static_cast<size_t>(k.b) * c.max_pages + (r >> c.shift)) : 0;
@@ -399,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
 #pragma unroll
       for (int x = 0; x < P::kRounds; ++x) {
         const int r = k.r0 + x * kGroupRows + t * kTile;
-        from[x] = same(x < k.rounds && r < k.len ? first_chunk<COLS>(a, k, r) : INT_MAX);
+        from[x] = same(x < k.rounds && r < k.end ? first_chunk<COLS>(a, k, r) : INT_MAX);
       }
       release(tc);
       for (int ch = c0; ch < c1 && go; ++ch) {
@@ -462,8 +477,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       for (int x = 0; x < P::kRounds; ++x) {
         const int r = row0 + x * kGroupRows;
         sum[x] = 0.f;
-        old[x] = x < k.rounds && r < k.first && r < k.len ? out[r] : 0.f;
-        page[x] = x < k.rounds && r < k.len ? __ldg(table + (r >> c.shift)) : -1;
+        old[x] = x < k.rounds && r < k.first && r < k.end ? out[r] : 0.f;
+        page[x] = x < k.rounds && r < k.end ? __ldg(table + (r >> c.shift)) : -1;
       }
       const int c1 = chunks<COLS>(k);
       for (int ch = first_chunk<COLS>(a, k, k.r0); ch < c1 && go; ++ch) {
@@ -471,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
 #pragma unroll
         for (int x = 0; x < P::kRounds; ++x) {
           const int first = first0 + x * kGroupRows, r = row0 + x * kGroupRows;
-          if (x >= k.rounds || first >= k.len || max(0, first - k.before) * a.G >= m0 + COLS) break;  // none of these queries sees the tile
+          if (x >= k.rounds || first >= k.end || max(0, first - k.before) * a.G >= m0 + COLS) break;  // none of these queries sees the tile
           const int buf = mine * P::kBuffers + (done & (P::kBuffers - 1));
           go = wait(&bars.s_full[buf], (done / P::kBuffers) & 1);
           if (!go) break;
@@ -540,7 +555,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.s_empty[buf]);
           float part = (s[0] + s[1]) + (s[2] + s[3]);
-          if (isnan(part) && r < k.len) part = add_infinite(a, k, r, max(m0, m0 + lo), min(m0 + cols, k.used));
+          if (isnan(part) && r < k.end) part = add_infinite(a, k, r, max(m0, m0 + lo), min(m0 + cols, k.used));
           sum[x] += part;
         }
       }
