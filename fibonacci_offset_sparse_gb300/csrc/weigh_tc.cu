@@ -73,10 +73,11 @@ struct TcBars {
   TcTask task[2];
   uint32_t tmem;
   int err;
+  int parts;  // of a round's four tiles 4, 2 or 1 are a task (1, 2, 4)
   int issued[kTiles];  // chunks of queries that are past the products of the tile
 };
 
-// Rows of a task of a sequence with `used` query rows; parts: of a round's four tiles 4, 2 or 1 are a task.
+// Rows of a task of a sequence with `used` query rows; parts: of a round's four tiles.
 template <int COLS>
 __device__ __forceinline__ int task_rows(int used, int parts) {
   return used <= COLS ? Shape<COLS>::kRounds * kGroupRows / parts : kGroupRows / parts;
@@ -234,18 +235,21 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   for (int i = tid; i < kOnesBytes / 16; i += kThreads)  // [16][2][8] words of a row's 8 values
     *reinterpret_cast<uint4*>(smem + P::kOnes + 16 * i) = i & 8 ? make_uint4(0, 0, 0, 0) : make_uint4(0x3f803f80u, 0x3f80u, 0, 0);
   fence_smem();
-  auto count = [&](int parts) {  // the tasks before each sequence's
-    for (int b = tid; b < a.B; b += kThreads) {
-      const WeighSeq s = sch.seq[b];
-      const int rows = task_rows<COLS>(s.n * a.G, parts);
-      start[b] = s.n == 0 ? 0 : static_cast<long long>((s.len + rows - 1) / rows) * c.L * c.H;
-    }
-    __syncthreads();
-    if (warp == 0) {
+  for (int b = tid; b < a.B; b += kThreads) {
+    bool ok;
+    sch.seq[b] = weigh_seq(a, b, &ok);
+  }
+  __syncthreads();
+  if (warp == 0) {
+    auto count = [&](int parts) {  // the tasks before each sequence's; all of them
       long long base = 0;
       for (int b0 = 0; b0 < a.B; b0 += 32) {
         const int b = b0 + lane;
-        const long long own = b < a.B ? start[b] : 0;
+        long long own = 0;
+        if (b < a.B && sch.seq[b].n > 0) {
+          const int rows = task_rows<COLS>(sch.seq[b].n * a.G, parts);
+          own = static_cast<long long>((sch.seq[b].len + rows - 1) / rows) * c.L * c.H;
+        }
         long long x = own;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -256,22 +260,16 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         base += __shfl_sync(0xffffffffu, x, 31);
       }
       if (lane == 0) start[a.B] = base;
-    }
-  };
-  for (int b = tid; b < a.B; b += kThreads) {  // (the thread that counts it)
-    bool ok;
-    sch.seq[b] = weigh_seq(a, b, &ok);
-  }
-  count(1);
-  // Where that leaves blocks without a task, tasks are of two tiles or of one: 32 of 1000 rows and 8000 query rows 104 us, of four tiles 141; 8 of
-  // 1672 rows and as many query rows 26, 34.
-  int parts = 1;
-  if constexpr (COLS == 128) {
-    __syncthreads();
-    const long long total = start[a.B];
-    while (parts < kTiles && total * parts * 2 <= gridDim.x) parts *= 2;
-    __syncthreads();
+      return base;
+    };
+    // Where few tasks leave blocks without one, they are of two tiles or of one: 32 of 1000 rows and 8000 query rows 102 us, of four tiles 141; 8 of
+    // 1672 rows and as many query rows 25, 34.
+    const long long total = count(1);
+    int parts = 1;
+    if constexpr (COLS == 128)
+      while (parts < kTiles && total * parts * 2 <= gridDim.x) parts *= 2;
     if (parts > 1) count(parts);
+    if (lane == 0) bars.parts = parts;
   }
   if (warp == kIssuer) tmem_alloc(&bars.tmem, 512);
   fence_before();
@@ -304,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     for (int tc = 0; wait(&bars.t_empty[tc & 1], ((tc >> 1) & 1) ^ 1); ++tc) {
       if (tc == 1) wait_for_first();
       unsigned long long id = tc == 0 ? blockIdx.x : lane == 0 ? gridDim.x + atomicAdd(a.next, 1ull) : 0;
-      const TcTask k = task_at<COLS>(a, sch, __shfl_sync(0xffffffffu, id, 0), parts);
+      const TcTask k = task_at<COLS>(a, sch, __shfl_sync(0xffffffffu, id, 0), bars.parts);
       if (lane == 0) {
         bars.task[tc & 1] = k;
         mbar_arrive(&bars.t_full[tc & 1]);
