@@ -38,8 +38,9 @@ constexpr int kThreads = 32 * (kFeedQ + 1);
 
 // COLS query rows a product.  32, where a key head has no more: the three parts are columns of one product (96, which takes hardly longer than 32 do)
 // and a score is the sum of three; one buffer of tensor memory a tile.  64, where it has no more: the parts add up in 64 columns, two buffers.
-// Both have two slots of shared memory a tile, and tasks of two rounds; else 128, one buffer, and two slots for the first two tiles.  A product takes 48.5, 54 and 64.6 cycles with 32, 64 and 128
-// columns, and what a warp does a chunk of queries beside its columns costs as much as 40 of them: prompts of 2048 took 66 us with 64.
+// Both have two slots of shared memory a tile, and tasks of two rounds; else 128, one buffer, and two slots for the first two tiles.  A product takes
+// 48.5, 54 and 64.6 cycles with 32, 64 and 128 columns, and what a warp does a chunk of queries beside its columns costs as much as 40 of them:
+// prompts of 2048 took 66 us with 64.
 template <int COLS>
 struct Shape {
   static constexpr bool kSpread = COLS == kSpreadRows;  // parts are columns: of 8 queries 24, part by part
@@ -418,7 +419,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       for (int ch = c0; ch < c1 && go; ++ch) {
         go = wait(&bars.q_full[qs], q_round & 1);
         if (!go) break;
-        const uint32_t query = query0 + qs * (P::kQuerySlot / 16), refs = refs0 + qs * (P::kQuerySlot / 16), desc = product_of(kTile, (P::kSpread ? 3 : 1) * (ch == c1 - 1 ? last : COLS), false, false);
+        const uint32_t query = query0 + qs * (P::kQuerySlot / 16), refs = refs0 + qs * (P::kQuerySlot / 16);
+        const uint32_t desc = product_of(kTile, (P::kSpread ? 3 : 1) * (ch == c1 - 1 ? last : COLS), false, false);
 #pragma unroll
         for (int x = 0; x < P::kRounds; ++x) {
           if (from[x] > ch) break;
