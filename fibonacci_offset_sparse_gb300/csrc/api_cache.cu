@@ -185,7 +185,7 @@ int fib_attn_cache_evict(fib_attn_plan_t p, const fib_attn_cache* c, int B, int 
   if (st == FIB_OK) st = check_cache_device(c);
   if (st != FIB_OK) return st;
   return cuda_status(launch_cache_evict(*c, B, rows, keep, sink, recent, p->N_max, weights, dropped, p->d_lo, p->d_hi, p->turn,
-                                        p->rotates, workspace, static_cast<cudaStream_t>(stream)));
+                                        workspace, static_cast<cudaStream_t>(stream)));
 }
 
 int fib_attn_tree_decode(fib_attn_plan_t p, int layer, const fib_attn_cache* c, int B, int Hq, int T, int N,

@@ -28,7 +28,7 @@ cudaError_t launch_cache_weigh(const fib_attn_cache& c, int B, int Hq, int T, in
 size_t cache_evict_workspace_bytes(const fib_attn_cache& c, int rows);
 cudaError_t launch_cache_evict(const fib_attn_cache& c, int B, int rows, const int32_t* keep, int sink, int recent, int n_max,
                                float* weights, int32_t* dropped, const float2* lo_tab, const float2* hi_tab, const float2* turn,
-                               bool turns, void* ws, cudaStream_t stream);
+                               void* ws, cudaStream_t stream);
 
 // What the decodes share.  kc, vc: the layer's pools.
 struct TreeArgs {

@@ -32,8 +32,7 @@ struct EvictArgs {
   int32_t* dropped;  // [B] or null
   const float2* rope_lo;
   const float2* rope_hi;
-  float2 turn[kFreq];  // theta / 2 pi as a sum of two
-  bool turns;
+  float2 turn[kFreq];  // theta / 2 pi as a sum of two, whether the plan rotates or not
   EvictJob* jobs;
   int32_t* list;   // free pages taken
   int32_t* old;    // [S, max_pages]: the pages that a sequence held; ~page where a new one takes its place
@@ -383,6 +382,12 @@ __device__ __forceinline__ void factors(const EvictArgs& a, int d, int t, float2
   }
 }
 
+// Whether the plan rotates, as its tables say now (a captured call follows them, not what was set at the capture): pair 0 turns by an angle of 1 a
+// position, whatever the base, and by none in the tables of a plan that does not rotate.
+__device__ __forceinline__ bool rotates(const EvictArgs& a) {
+  return __ldg(&a.rope_lo[kFreq].y) != 0.f;
+}
+
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;\n" ::: "memory");
 }
@@ -401,6 +406,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictJob& jo
   DT* pool = static_cast<DT*>(v ? c.v : c.k) + ((static_cast<size_t>(l) * c.n_pages * c.H + h) << c.shift) * kD;
   const size_t page_elems = (static_cast<size_t>(c.H) << c.shift) * kD;
   const int t = thread & 3, quad = thread >> 2, mask = c.P - 1;
+  const bool turns = v == 0 && rotates(a);
   for (int start = job.same << c.shift; start < job.keep; start += kStep * blocks) {
     const int j0 = start + kStep * rank;
     uint4 x[ROWS][kWords];
@@ -431,7 +437,7 @@ __device__ __forceinline__ void move_rows(const EvictArgs& a, const EvictJob& jo
     for (int i = 0; i < ROWS; ++i) {
       const int j = j0 + i * (THREADS / 4) + quad;
       if (src[i] < 0) continue;
-      if (v == 0 && a.turns && src[i] != j) {
+      if (turns && src[i] != j) {
         float2 e[8];
         float y[16];
         factors<DT>(a, src[i] - j, t, e);
@@ -530,7 +536,7 @@ size_t cache_evict_workspace_bytes(const fib_attn_cache& c, int rows) {
 }
 
 cudaError_t launch_cache_evict(const fib_attn_cache& cache, int B, int rows, const int32_t* keep, int sink, int recent, int n_max,
-                               float* weights, int32_t* dropped, const float2* lo_tab, const float2* hi_tab, const float2* turn, bool turns, void* ws,
+                               float* weights, int32_t* dropped, const float2* lo_tab, const float2* hi_tab, const float2* turn, void* ws,
                                cudaStream_t stream) {
   EvictArgs a;
   a.c = device_view(cache);
@@ -545,7 +551,6 @@ cudaError_t launch_cache_evict(const fib_attn_cache& cache, int B, int rows, con
   a.rope_lo = lo_tab;
   a.rope_hi = hi_tab;
   for (int m = 0; m < kFreq; ++m) a.turn[m] = turn[m];
-  a.turns = turns;
   unsigned char* at = static_cast<unsigned char*>(ws);
   a.jobs = reinterpret_cast<EvictJob*>(at);
   at += round_up(sizeof(EvictJob) * kMaxSeqs);

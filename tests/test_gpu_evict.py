@@ -249,3 +249,33 @@ def test_blocks_that_share_rows_of_shared_pages():
     lens = [2000, 1900, 1800, 1500]
     c, ref = make_cache(r, "bf16", 2, 2, 32, lens, 64, spare=200, share=[(1, 0, 50), (2, 0, 50)])
     run(c, ref, plan_for(1 << 12), weights_of(r, c, 2000), [1000, 1899, 300, 1500], 70, 100, "bf16")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("captured", [True, False])
+@pytest.mark.parametrize("lens,keeps", [([120, 64], ([100, 64], [40, 31])), ([6000], ([2500], [1999]))])
+def test_a_replay_turns_as_the_plan_does_then(dtype, captured, lens, keeps):
+    """The setting of the plan when the graph is replayed, not when the call was captured, says whether K is turned."""
+    r = rng(114, *lens)
+    c, ref = make_cache(r, dtype, 2, 2, 16, lens, -(-max(lens) // 16) + 1)
+    plan, w = plan_for(8192), weights_of(r, c, max(lens))
+    wd, keep = torch.from_numpy(w.copy()).cuda(), i32(lens)
+    ws = torch.empty(fa.fib_attn_cache_evict_workspace_size(c, max(lens)), dtype=torch.uint8, device="cuda")
+    fa.fib_attn_plan_set_rotation(plan, captured)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        fa.fib_attn_cache_evict(plan, c, wd, keep, 3, 5, workspace=ws)
+    for turns, now in zip((not captured, captured), keeps):
+        fa.fib_attn_plan_set_rotation(plan, turns)
+        keep.copy_(i32(now))
+        graph.replay()
+        before = ref.k.copy()
+        assert ref.evict(w, now, 3, 5, [0] * len(lens), turns)
+        assert fa.fib_attn_cache_status(c) == fa.FIB_OK
+        same_tables(c, ref)
+        assert not np.array_equal(before, ref.k)
+        if turns:
+            close_rows(c, ref, dtype)
+        else:
+            assert np.array_equal(c.k.double().cpu().numpy(), ref.k) and np.array_equal(c.v.double().cpu().numpy(), ref.v)
+        ref.k = c.k.double().cpu().numpy()
