@@ -41,7 +41,9 @@ bool rows_apart(const int64_t* s, const int* n) {
   return true;
 }
 
-// One tensor pair of a call.  Strides are below 2^40 elements, so that no sum of them leaves 63 bits.
+constexpr int64_t kFar = 1LL << 58;  // elements: no tensor reaches as far, and neither a sum of three such extents nor the bytes of one leaves 63 bits
+
+// One tensor pair of a call.
 int check_rows(int B, int H, int N, int es, const void* x, const int64_t* xs, const void* y, const int64_t* ys) {
   if (x == nullptr || y == nullptr || xs == nullptr || ys == nullptr || !aligned(x, es) || !aligned(y, es)) return FIB_ERR_INVALID_ARG;
   const int n[3] = {B, H, N};
@@ -50,12 +52,13 @@ int check_rows(int B, int H, int N, int es, const void* x, const int64_t* xs, co
   for (int d = 0; d < 3; ++d) {
     if (xs[d] < 0 || ys[d] < 0 || xs[d] >= 1LL << 40 || ys[d] >= 1LL << 40) return FIB_ERR_INVALID_ARG;
     if (n[d] > 1) {
+      if (std::max(xs[d], ys[d]) > (kFar - 1) / (n[d] - 1)) return FIB_ERR_INVALID_ARG;  // (before the product is made)
       x_end += static_cast<uint64_t>(xs[d]) * (n[d] - 1);
       y_end += static_cast<uint64_t>(ys[d]) * (n[d] - 1);
       same = same && xs[d] == ys[d];
     }
   }
-  if (x_end >= 1ULL << 58 || y_end >= 1ULL << 58 || !rows_apart(ys, n)) return FIB_ERR_INVALID_ARG;
+  if (x_end >= kFar || y_end >= kFar || !rows_apart(ys, n)) return FIB_ERR_INVALID_ARG;
   const uintptr_t x0 = reinterpret_cast<uintptr_t>(x), y0 = reinterpret_cast<uintptr_t>(y);
   if (!same && x0 < y0 + y_end * es && y0 < x0 + x_end * es) return FIB_ERR_INVALID_ARG;
   return FIB_OK;

@@ -86,3 +86,24 @@ def test_an_amplitude_is_a_float32(amplitude):
     spec = fa.RopeSpec(fa.FIB_ROPE_HALF, 64, fa.FIB_ROPE_PLAIN, 1024, 10000.0, 1.0, 1.0, 32.0, amplitude)
     out = (ctypes.c_double * 32)()
     assert fa.lib().fib_attn_rope_frequencies(ctypes.byref(spec), out) == fa.FIB_ERR_INVALID_ARG
+
+
+FAR = 1 << 39  # elements; times 2^25 it is 2^64
+
+
+@pytest.mark.parametrize("dtype", [fa.FIB_DTYPE_F32, fa.FIB_DTYPE_BF16])
+@pytest.mark.parametrize("shape,strides", [
+    ((1, 1, (1 << 25) + 1), (64, 64, FAR)),              # the product alone leaves 64 bits, and the extent comes out as one row
+    (((1 << 25) + 1, 1, 1), (FAR, 64, 64)),
+    ((1, 1, (1 << 24) + 1), (64, 64, FAR)),              # 2^63
+    ((1 << 15, 1 << 10, 1 << 10), (FAR, FAR, FAR)),      # a sum of three
+    ((1, 1, (1 << 19) + 1), (64, 64, FAR)),              # 2^58: the first that is too far
+])
+@pytest.mark.parametrize("far", ["in", "out", "k in", "k out"])
+def test_strides_that_leave_64_bits(lib, dtype, shape, strides, far):
+    B, H, N = shape
+    near, wide = (ctypes.c_int64 * 3)(64 * H * N, 64 * N, 64), (ctypes.c_int64 * 3)(*strides)
+    rows = [1 << 20, near, 1 << 44, near, 1 << 45, near, 1 << 46, near]  # memory that no call here reaches: q, q_out, k, k_out
+    rows[1 + 2 * ["in", "out", "k in", "k out"].index(far)] = wide
+    rope = 1 << 12  # never looked into: the call is refused for its strides
+    assert lib.fib_attn_rotary(rope, dtype, B, N, H, H, *rows, None, None, 0, None) == fa.FIB_ERR_INVALID_ARG
