@@ -64,6 +64,56 @@ int check_rows(int B, int H, int N, int es, const void* x, const int64_t* xs, co
   return FIB_OK;
 }
 
+// Rows of 64 of a tensor that check_rows has passed: where the first lies, strides, extents.
+struct Rows {
+  uintptr_t at;
+  const int64_t* s;
+  int n[3];
+  int64_t end() const {
+    int64_t e = kD;
+    for (int d = 0; d < 3; ++d) e += s[d] * (n[d] - 1);
+    return e;
+  }
+  bool packed() const { return rows_apart(s, n) && end() == static_cast<int64_t>(kD) * n[0] * n[1] * n[2]; }
+};
+
+// Whether some index differences d_i in [low_i, high_i] take `behind` + sum of s_i d_i into (-kD, kD); strides descend, in `more` of them.
+struct Steps {
+  int64_t s, low, high;
+};
+bool meets(const Steps* step, int more, int64_t behind) {
+  if (more == 0) return behind > -kD && behind < kD;
+  int64_t below = kD - 1, above = kD - 1;  // what the smaller strides can still take off and add
+  for (int i = 1; i < more; ++i) {
+    below -= step[i].s * step[i].low;
+    above += step[i].s * step[i].high;
+  }
+  const int64_t s = step->s;
+  // the differences that leave the rest in reach; more than a few only where an input's rows overlap one another, which is not looked into
+  const int64_t first = std::max(step->low, -((behind + above) / s) - 1), last = std::min(step->high, (below - behind) / s + 1);
+  if (last - first > 16) return false;
+  for (int64_t d = first; d <= last; ++d)
+    if (meets(step + 1, more - 1, behind + s * d)) return true;
+  return false;
+}
+
+// Whether an output shares memory with another tensor of the call.  Found for tensors of the same strides, as parts of one projection are
+// (a stride of one row only counts for nothing), and for two without gaps; of others, which may lie in one another's gaps, only by their first rows.
+bool overlap(const Rows& x, const Rows& y, int es) {
+  if (x.at == y.at) return true;
+  if (x.at >= y.at + y.end() * es || y.at >= x.at + x.end() * es) return false;
+  if (x.packed() && y.packed()) return true;
+  Steps step[3];
+  int steps = 0;
+  for (int d = 0; d < 3; ++d) {
+    if (x.n[d] > 1 && y.n[d] > 1 && x.s[d] != y.s[d]) return false;
+    const int64_t s = x.n[d] > 1 ? x.s[d] : y.s[d];
+    if ((x.n[d] > 1 || y.n[d] > 1) && s > 0) step[steps++] = {s, 1 - x.n[d], y.n[d] - 1};
+  }
+  std::sort(step, step + steps, [](const Steps& a, const Steps& b) { return a.s > b.s; });
+  return meets(step, steps, (static_cast<int64_t>(y.at) - static_cast<int64_t>(x.at)) / es);
+}
+
 }  // namespace
 
 extern "C" {
@@ -127,7 +177,11 @@ int fib_attn_rotary(fib_attn_rope_t r, int dtype, int B, int N, int Hq, int Hk, 
   const int es = dtype == FIB_DTYPE_F32 ? 4 : 2;
   if (check_rows(B, Hq, N, es, q, q_strides, q_out, q_out_strides)) return FIB_ERR_INVALID_ARG;
   if (Hk > 0 && check_rows(B, Hk, N, es, k, k_strides, k_out, k_out_strides)) return FIB_ERR_INVALID_ARG;
-  if (Hk > 0 && (k_out == q_out || k_out == q || q_out == k)) return FIB_ERR_INVALID_ARG;
+  if (Hk > 0) {
+    const auto rows = [&](const void* at, const int64_t* s, int H) { return Rows{reinterpret_cast<uintptr_t>(at), s, {B, H, N}}; };
+    const Rows to = rows(q_out, q_out_strides, Hq), k_to = rows(k_out, k_out_strides, Hk);
+    if (overlap(rows(k, k_strides, Hk), to, es) || overlap(rows(q, q_strides, Hq), k_to, es) || overlap(to, k_to, es)) return FIB_ERR_INVALID_ARG;
+  }
   if ((pos != nullptr && start != nullptr) || !aligned(pos, 4) || !aligned(start, 4)) return FIB_ERR_INVALID_ARG;
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return FIB_ERR_CUDA;

@@ -280,7 +280,8 @@ int fib_attn_rope_destroy(fib_attn_rope_t r);
  * say), else n; at most one of them is given.  transpose != 0: the transposed map (angles
  * negated, the same amplitude), which takes the outputs' gradient to the inputs'.
  * q_out may be q itself with the same strides (k_out k), and else must not overlap what the
- * call reads.  Values are rotated in float32 and rounded once.  A position outside [0, N_max)
+ * call reads or writes (refused where it can be told: queries with queries, keys with keys, tensors of the same strides and
+ * tensors without gaps).  Values are rotated in float32 and rounded once.  A position outside [0, N_max)
  * records FIB_ERR_DEVICE_ASSERT in the handle's status word and leaves its rows unwritten.
  * 1 <= B, N; B * N < 2^31; 1 <= Hq <= FIB_MAX_HEADS; 0 <= Hk <= FIB_MAX_HEADS.  Pointers and
  * strides aligned to 16 bytes, and HALF with rot_dim a multiple of 16 (float32: 8), take the wide path;

@@ -322,3 +322,26 @@ def test_decodes_of_a_plan_that_does_not_rotate(dtype, T, Hq):
         assert np.abs(lse.double().cpu().numpy() - lse_want).max() <= TOL_LSE
         assert (np.abs(o.double().cpu().numpy() - want) - HALF[dtype] * np.abs(want)).max() <= TOL_O
     assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK and fa.fib_attn_rope_status(rope) == fa.FIB_OK
+
+
+@pytest.mark.parametrize("B,Hq,Hk,N", [(1, 1, 1, 1), (2, 1, 3, 5), (3, 4, 1, 9), (2, 2, 2, 130), (1, 5, 2, 33)])
+@pytest.mark.parametrize("order", ["qkv", "vqk", "kvq"])
+@pytest.mark.parametrize("tokens_first", [True, False])
+def test_parts_of_one_projection(B, Hq, Hk, N, order, tokens_first):
+    """Queries and keys between one another's rows, in place and into another projection: they overlap in extent and not in memory."""
+    rope = fa.fib_attn_rope_create(N)
+    heads, at = {"q": Hq, "k": Hk, "v": Hk}, {}
+    for x in order:
+        at[x] = sum(heads[y] for y in order[:order.index(x)])
+    shape = (B, N, Hq + 2 * Hk, 64) if tokens_first else (B, Hq + 2 * Hk, N, 64)
+    part = lambda x, t: t.transpose(1, 2)[:, at[x]:at[x] + heads[x]] if tokens_first else t[:, at[x]:at[x] + heads[x]]  # noqa: E731
+    base = rand(shape, "f32", 40)
+    q, k = part("q", base), part("k", base)
+    want = fa.fib_attn_rotary(rope, q, k)
+    into = torch.full_like(base, 3.0)
+    fa.fib_attn_rotary(rope, q, k, q_out=part("q", into), k_out=part("k", into))
+    assert torch.equal(part("q", into), want[0]) and torch.equal(part("k", into), want[1]) and (part("v", into) == 3.0).all()
+    values = part("v", base).clone()
+    fa.fib_attn_rotary(rope, q, k, q_out=q, k_out=k)
+    assert torch.equal(q, want[0]) and torch.equal(k, want[1]) and torch.equal(part("v", base), values)
+    assert fa.fib_attn_rope_status(rope) == fa.FIB_OK

@@ -107,3 +107,29 @@ def test_strides_that_leave_64_bits(lib, dtype, shape, strides, far):
     rows[1 + 2 * ["in", "out", "k in", "k out"].index(far)] = wide
     rope = 1 << 12  # never looked into: the call is refused for its strides
     assert lib.fib_attn_rotary(rope, dtype, B, N, H, H, *rows, None, None, 0, None) == fa.FIB_ERR_INVALID_ARG
+
+
+def _rows(B, H, N, layout):
+    """Strides (b, h, n) of [B, H, N, 64], of [B, N, H, 64], or of H heads of a projection of 8."""
+    return {"rows": (H * N * 64, N * 64, 64), "tokens": (N * H * 64, 64, H * 64), "part": (N * 8 * 64, 64, 8 * 64)}[layout]
+
+
+MEET = [  # the second tensor begins so many elements behind the first; queries and keys with their heads
+    ("rows", 3, 3, 64), ("rows", 3, 3, 1), ("rows", 3, 2, 5 * 64), ("rows", 3, 1, -63), ("rows", 2, 4, 2 * 2 * 5 * 64 - 64),
+    ("tokens", 3, 3, 3 * 64), ("tokens", 4, 2, 128), ("tokens", 1, 1, 64 * 9),
+    ("part", 5, 2, 4 * 64), ("part", 2, 5, -4 * 64), ("part", 3, 3, 8 * 64), ("part", 3, 3, 8 * 64 * 4 + 2 * 64), ("part", 1, 1, 63), ("part", 1, 1, 8 * 64 * 5),
+]
+
+
+@pytest.mark.parametrize("dtype", [fa.FIB_DTYPE_F32, fa.FIB_DTYPE_BF16])
+@pytest.mark.parametrize("layout,Hq,Hk,behind", MEET)
+@pytest.mark.parametrize("which", ["q_out on k", "k_out on q", "both outputs"])
+def test_outputs_that_overlap_the_other_tensors(lib, dtype, layout, Hq, Hk, behind, which):
+    B, N, es = 2, 5, 4 if dtype == fa.FIB_DTYPE_F32 else 2
+    first, strides = 1 << 30, [(ctypes.c_int64 * 3)(*_rows(B, H, N, layout)) for H in (Hq, Hk)]
+    at = {"q": 1 << 40, "q_out": 1 << 41, "k": 1 << 42, "k_out": 1 << 43}  # memory that no call here reaches
+    for name, place in zip({"q_out on k": ("q_out", "k"), "k_out on q": ("q", "k_out"), "both outputs": ("q_out", "k_out")}[which], (first, first + behind * es)):
+        at[name] = place
+    rope = 1 << 12  # never looked into
+    assert lib.fib_attn_rotary(rope, dtype, B, N, Hq, Hk, at["q"], strides[0], at["q_out"], strides[0], at["k"], strides[1], at["k_out"], strides[1],
+                               None, None, 0, None) == fa.FIB_ERR_INVALID_ARG
