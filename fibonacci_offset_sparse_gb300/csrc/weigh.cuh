@@ -28,7 +28,7 @@ struct WeighArgs {
   unsigned char* ref_parts;
   unsigned long long* next;  // weigh_tc.cu: the next task to be taken
   unsigned long long wait_ns;
-  unsigned long long task_ns;  // weigh_tc.cu: ... of a wait for the end of a task
+  unsigned long long task_ns;  // weigh_tc.cu: ... of a wait that may take as long as a task
   int skip_copy;  // test hook: the first rows of every task of weigh_tc.cu are never copied
 };
 

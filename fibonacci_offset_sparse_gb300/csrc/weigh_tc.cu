@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
           const int first = first0 + x * kGroupRows, r = row0 + x * kGroupRows;
           if (x >= k.rounds || first >= k.end || max(0, first - k.before) * a.G >= m0 + COLS) break;  // none of these queries sees the tile
           const int buf = mine * P::kBuffers + (done & (P::kBuffers - 1));
-          go = wait(&bars.s_full[buf], (done / P::kBuffers) & 1);
+          // (the chunks that see the tile may be the last of the task's)
+          go = wait_for(&bars.s_full[buf], (done / P::kBuffers) & 1, a.task_ns);
           if (!go) break;
           ++done;
           fence_after();

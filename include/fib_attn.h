@@ -561,8 +561,8 @@ int fib_attn_debug_indices(fib_attn_plan_t p, int layer, int N, int i_begin, int
 /* Wait bound and test hooks of the plan's kernels (no counterpart in the paper: they
  * exist so that the error paths can be driven without any device fault).  Kernels that
  * stage rows with the bulk-copy engine wait on mbarriers; every such wait gives up after
- * wait_ns nanoseconds (default 1e9; accepted range [1e3, 6e10]; in fib_attn_cache_weigh a wait for the end of a
- * block's work 20 us later for each 128 query rows a key head), records FIB_ERR_TIMEOUT in
+ * wait_ns nanoseconds (default 1e9; accepted range [1e3, 6e10]; in fib_attn_cache_weigh a wait for a tile's
+ * scores or the end of a block's work 20 us later for each 128 query rows a key head), records FIB_ERR_TIMEOUT in
  * the status word, lets the copies already in flight land and returns without writing
  * output (of fib_attn_dense_tree_decode o and lse, of fib_attn_cache_weigh the weights are unspecified then).  debug_flags:
  * FIB_DEBUG_SKIP_COPY makes the bf16 tensor-core forward never complete one of its staged

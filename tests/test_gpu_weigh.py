@@ -396,3 +396,23 @@ def test_many_query_rows_of_an_odd_number_of_heads(dtype):
     lens, n = [700, 600], [600, 333]
     x = setup(r, dtype, 16, 5, 1, 600, 64, lens, n)
     run(x[0], x[1], plan_for(1000), *x[2:6], n, first=[0, 267])
+
+
+def test_a_tile_that_few_queries_see_is_no_wait_that_runs_out():
+    """Rows from 384 on are seen by the last of 1600 chunks of queries alone: their sums begin after a time that no single step takes."""
+    L, G, T = 77, 512, 400  # (as many layers as leave every block a task of four tiles)
+    c = fa.fib_attn_cache_create(L, 1, 16, 25, 1, 25, torch.bfloat16)
+    plan = plan_for(512, alpha=[1.0] * L)
+    g = torch.Generator(device="cuda").manual_seed(217)
+    kn = torch.empty((L, 1, 1, T, 64), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    q = torch.empty((L, 1, G, T, 64), dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    fa.fib_attn_cache_commit(plan, c, kn, kn, i32([T]))
+    lse = torch.full((L, 1, G, T), 5.0, device="cuda")
+    workspace = torch.empty(fa.fib_attn_cache_weigh_workspace_size(c, 1, G, T), dtype=torch.uint8, device="cuda")
+    ws = []
+    for ns in (1_000_000_000, 200_000):
+        fa.fib_attn_plan_set_debug(plan, False, ns)
+        ws.append(torch.zeros((L, 1, 1, T), device="cuda"))
+        fa.fib_attn_cache_weigh(plan, c, q, lse, i32([T]), ws[-1], first=i32([0]), workspace=workspace)
+        assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    assert torch.equal(*ws) and (ws[0] > 0).all()
