@@ -301,7 +301,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
   if (warp == kTasks) {
     // =================================================================== tasks
     for (int tc = 0; wait(&bars.t_empty[tc & 1], ((tc >> 1) & 1) ^ 1); ++tc) {
-      if (tc == 1) wait_for_first();
       unsigned long long id = tc == 0 ? blockIdx.x : lane == 0 ? gridDim.x + atomicAdd(a.next, 1ull) : 0;
       const TcTask k = task_at<COLS>(a, sch, __shfl_sync(0xffffffffu, id, 0), bars.parts);
       if (lane == 0) {
@@ -310,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
       }
       __syncwarp();
       if (k.rounds == 0) break;
+      if (tc == 0) wait_for_first();  // (before the limits below begin: they are of this launch's work; and before `next` is read)
       // A long task is taken alone, till the last of its queries is under way: one that waits for its block waits for nothing else.
       if (k.used > COLS && !wait_for(&bars.t_empty[tc & 1], (tc >> 1) & 1, a.task_ns)) break;
     }
