@@ -416,3 +416,58 @@ def test_a_tile_that_few_queries_see_is_no_wait_that_runs_out():
         fa.fib_attn_cache_weigh(plan, c, q, lse, i32([T]), ws[-1], first=i32([0]), workspace=workspace)
         assert fa.fib_attn_last_device_status(plan) == fa.FIB_OK
     assert torch.equal(*ws) and (ws[0] > 0).all()
+
+
+@pytest.mark.parametrize("dtype,G,T", [("f32", 1, 1), ("f32", 2, 10), ("f32", 2, 200), ("bf16", 1, 2), ("bf16", 1, 30), ("bf16", 2, 30), ("bf16", 1, 200)])
+def test_a_short_limit_is_kept_or_reported(dtype, G, T):
+    """Limits from too short for any copy to long enough: a call that reports nothing has given every weight."""
+    r = rng(218, G, T)
+    lens, n = [900, 300], [T, T]
+    c, ref, q, qf, lse, w, _ = setup(r, dtype, 1, 2, G, T, 16, lens, n)
+    plan, want, new = plan_for(1000), w.astype(np.float64), np.zeros(w.shape)
+    ref.weigh(want, qf, lse.astype(np.float64), n)
+    ref.weigh(new, qf, lse.astype(np.float64), n, None, [0, 0])
+    ld, nd, kept = torch.from_numpy(lse).cuda(), i32(n), []
+    for ns in (1000, 1500, 2500, 5000, 10_000, 100_000, 1_000_000_000):
+        fa.fib_attn_plan_set_debug(plan, False, ns)
+        for _ in range(8):
+            wd = torch.from_numpy(w).cuda()
+            fa.fib_attn_cache_weigh(plan, c, q, ld, nd, wd)
+            status = fa.fib_attn_last_device_status(plan)
+            assert status in (fa.FIB_OK, fa.FIB_ERR_TIMEOUT)
+            if status == fa.FIB_OK:
+                got = wd.double().cpu().numpy()
+                assert (np.abs(got - want) <= tolerance(new, want - new, T * G)).all(), ns
+                kept.append(ns)
+    assert kept.count(1_000_000_000) == 8
+
+
+@pytest.mark.parametrize("dtypes,Ts", [(("bf16", "bf16", "bf16"), (1, 40, 150)), (("f32", "f32", "bf16"), (3, 20, 60)), (("bf16", "bf16", "bf16"), (200, 200, 200))])
+def test_calls_that_are_released_together(dtypes, Ts):
+    """One plan; streams whose calls all stand in line behind one event, with workspaces of their own: bit for bit what the calls give alone."""
+    r = rng(219, *Ts)
+    lens = [1500, 300, 700]
+    plan, calls = plan_for(2000), []
+    for dtype, T in zip(dtypes, Ts):
+        c, _, q, _, lse, w, _ = setup(r, dtype, 8, 4, 1, T, 16, lens, [T] * 3)
+        n, lse, w = i32([T] * 3), torch.from_numpy(lse).cuda(), torch.from_numpy(w).cuda()
+        size = fa.fib_attn_cache_weigh_workspace_size(c, 3, 4, T)
+        alone = w.clone()
+        fa.fib_attn_cache_weigh(plan, c, q, lse, n, alone)
+        assert not torch.equal(alone, w)
+        outs = [w.clone() for _ in range(6)]
+        calls.append((torch.cuda.Stream(), c, q, lse, n, torch.empty(size, dtype=torch.uint8, device="cuda"), outs, alone))
+    torch.cuda.synchronize()
+    gate = torch.cuda.Event()
+    torch.cuda._sleep(60_000_000)  # some 30 ms, in which all calls are put in line
+    gate.record()
+    for s, *_ in calls:
+        s.wait_event(gate)
+    for i in range(6):
+        for s, c, q, lse, n, workspace, outs, _ in calls:
+            fa.fib_attn_cache_weigh(plan, c, q, lse, n, outs[i], workspace=workspace, stream=s)
+    in_line = not gate.query()
+    torch.cuda.synchronize()
+    assert in_line and fa.fib_attn_last_device_status(plan) == fa.FIB_OK
+    for *_, outs, alone in calls:
+        assert all(torch.equal(x, alone) for x in outs)
