@@ -279,3 +279,42 @@ def test_a_replay_turns_as_the_plan_does_then(dtype, captured, lens, keeps):
         else:
             assert np.array_equal(c.k.double().cpu().numpy(), ref.k) and np.array_equal(c.v.double().cpu().numpy(), ref.v)
         ref.k = c.k.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("turns", [True, False])
+def test_a_row_at_a_time(dtype, turns):
+    """64 calls, each of which lets go of the first row, so that all others move by one place and, where the plan rotates, are turned and rounded
+    64 times.  A rounding moves a pair by half a step of its size at most, and the factors (12 * 2^-24 for each of its two values) by less than
+    2^-19: that, added up, is the bound of one pair.  Of all together it is what rounding 64 times gives, computed here in 64 bits between the roundings: a value
+    that the kernel rounds to the other side, of its factors' error of a thousandth of a step, is one in a thousand."""
+    from oracle.cache_oracle import turn
+    from tests.test_gpu_cache import DT, HALF
+    r = rng(115)
+    n, length = 64, 200
+    c, ref = make_cache(r, dtype, 1, 2, 16, [length], 13)
+    plan = plan_for()
+    fa.fib_attn_plan_set_rotation(plan, turns)
+    rows = lambda pool: torch.as_tensor(pool)[0, ref.table[0]].transpose(0, 1).reshape(2, -1, 64)  # noqa: E731
+    first, values = (rows(x)[:, n:length].clone() for x in (ref.k, ref.v))
+    w = torch.arange(1.0, length + 1, device="cuda").expand(1, 1, 2, length).contiguous()
+    for i in range(1, n + 1):
+        fa.fib_attn_cache_evict(plan, c, w, i32([length - i]), 0, 0)
+    assert fa.fib_attn_cache_status(c) == fa.FIB_OK and c.lens.tolist() == [length - n]
+    got, got_v = (rows(x.double().cpu())[:, :length - n] for x in (c.k, c.v))
+    assert torch.equal(got_v, values) and w[0, 0, 0, :length - n].tolist() == [float(x) for x in range(n + 1, length + 1)]
+    if not turns:
+        assert torch.equal(got, first)  # moved, whatever the number of calls
+        return
+    steps = first.numpy()
+    for _ in range(n):
+        steps = torch.from_numpy(turn(steps, -1)).to(DT[dtype]).double().numpy()
+    want = turn(first.numpy(), -n)
+    size = np.hypot(want[..., :32], want[..., 32:])
+    error = got.numpy() - want
+    assert (np.hypot(error[..., :32], error[..., 32:]) <= ((1 + HALF[dtype] + 2.0 ** -19) ** n - 1) * size).all()
+    drift = np.linalg.norm(steps - want)
+    if dtype == "bf16":
+        assert 0.9 * drift <= np.linalg.norm(error) <= 1.1 * drift and 0.03 <= drift / np.linalg.norm(want) <= 0.05
+    else:
+        assert np.linalg.norm(error) <= n * 2.0 ** -22 * np.linalg.norm(want)
