@@ -380,7 +380,7 @@ def _rope_spec(rot_dim, layout, base, scaling, factor, n_train, slow, fast, ampl
 
 def fib_attn_rope_frequencies(rot_dim: int = 64, layout: int = FIB_ROPE_HALF, base: float = 10000.0, scaling: int = FIB_ROPE_PLAIN,
                               factor: float = 1.0, n_train: int = 1024, slow: float = 1.0, fast: float = 32.0) -> list[float]:
-    """The frequencies of the rot_dim / 2 pairs (host only)."""
+    """The frequencies of the rot_dim / 2 pairs (host only).  FIB_ROPE_YARN's ramp is linear in a pair's turns, not in its index."""
     spec = _rope_spec(rot_dim, layout, base, scaling, factor, n_train, slow, fast, 1.0)
     out = (ctypes.c_double * 32)()
     _check("fib_attn_rope_frequencies", lib().fib_attn_rope_frequencies(ctypes.byref(spec), out))

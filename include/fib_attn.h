@@ -244,7 +244,9 @@ int fib_attn_decode(fib_attn_plan_t p, int layer, int B, int H, int N, int pos, 
  *   NTK     (base * factor^(rot_dim/(rot_dim-2)))^(-2m/rot_dim) (rot_dim 2: as PLAIN);
  *   YARN    theta_m (g + (1-g)/factor), g = clamp((n_train theta_m / 2pi - slow) / (fast - slow),
  *           0, 1) of PLAIN's theta_m: pairs of few turns in n_train positions are stretched,
- *           those of many kept.  (An amplitude of 0.1 ln(factor) + 1 goes with it.)
+ *           those of many kept.  (An amplitude of 0.1 ln(factor) + 1 goes with it.)  The ramp g is linear
+ *           in the turns; one that is linear in the pair's index m, between the pairs of `fast` and `slow` turns,
+ *           is another scaling, with other frequencies for the same numbers, and not built.
  * Rules: rot_dim even, 2 .. 64; base > 1; amplitude > 0; factor >= 1 (but PLAIN); n_train >= 1,
  * 0 <= slow < fast (YARN); all finite, the amplitude a normal float32's.                */
 typedef struct fib_attn_rope_spec_s {
