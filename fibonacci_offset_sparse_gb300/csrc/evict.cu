@@ -508,8 +508,9 @@ cudaError_t launch_in(const EvictArgs& a, unsigned tasks, unsigned blocks, cudaS
 }
 
 // By what the weights' rows can hold: up to 5120 rows a block of 256 threads, four of which share an SM; longer ones 1024 threads, which beyond
-// 16384 rows read the weights anew in each pass.  Where these leave SMs without one, 2, 4 or 8 blocks of 256 rows or more to each (15 of 30300 rows
-// cut to 10211, bf16: 46 us, one block each 116; 32 of 2077 cut to 1782, float32: 22, 54).
+// 16384 rows read the weights anew in each pass.  (Lengths are on the device, so that room for more rows than there are takes the larger block: 2048 blocks
+// of 4096 rows cut to 2048 take 387 us with room for 5121 or 131072, 363 with room for 5120; of 2048 to 1024 227, 189; of 600 to 500 61, 43.)  Where these leave SMs without one, 2, 4 or 8 blocks of 256 rows or more to each (15 of 30300 rows
+// cut to 10211, bf16: 47 us, one block each 116; 32 of 2077 cut to 1782, float32: 22, 54).
 template <typename DT>
 cudaError_t launch(const EvictArgs& a, unsigned tasks, cudaStream_t stream) {
   const bool few = a.rows <= 256 * 20;

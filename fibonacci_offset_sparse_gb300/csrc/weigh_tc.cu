@@ -13,7 +13,7 @@
 // What bounds it: few query rows the read of K, many the products (13 a tile and chunk of queries).  32 tokens over 4 sequences of up to 8192
 // rows, 16 layers, 8 heads (242 MB): 47 us with the queries' launch; once under way a block's tasks follow one another in 2.95 us, which is HBM's rate,
 // the rest is the start, the queries' 6 and the last tasks.  (13 products of 32 columns a tile, 30 us of tensor pipe, took 49.)  Prompts of
-// 2048 and 1523, 4 layers (134 million scores): 50 us, 14 of them the queries' launch; the products alone are 23 where all SMs have the same, 25 on
+// 2048 and 1523, 4 layers (104 million scores, in whole tiles 112): 50 us, 14 of them the queries' launch; the products alone are 23 where all SMs have the same, 25 on
 // the one that has the longest task.
 //
 // Block: 16 warps that sum (four a tile), and one warp each for the tasks, the queries, the copies of each of the four tiles and the
@@ -40,7 +40,7 @@ constexpr int kThreads = 32 * (kFeedQ + 1);
 // and a score is the sum of three; one buffer of tensor memory a tile.  64, where it has no more: the parts add up in 64 columns, two buffers.
 // Both have two slots of shared memory a tile, and tasks of two rounds; else 128, one buffer, and two slots for the first two tiles.  A product takes
 // 48.5, 54 and 64.6 cycles with 32, 64 and 128 columns, and what a warp does a chunk of queries beside its columns costs as much as 40 of them:
-// prompts of 2048 took 66 us with 64.
+// prompts of 2048 took 66 us with 64.  The window above takes 47 us with 32 columns; with 64 tokens, or twice the query heads, 64 columns: 54 (floor 36).
 template <int COLS>
 struct Shape {
   static constexpr bool kSpread = COLS == kSpreadRows;  // parts are columns: of 8 queries 24, part by part
